@@ -339,6 +339,119 @@ spear_status_t spear_sched_pick_chunk(spear_sched_t s, int32_t n_decode, double 
 /* Frees the scheduler; NULL is accepted. */
 spear_status_t spear_sched_destroy(spear_sched_t s);
 
+/* ------------------------------------------------------------------------
+ * Key/value cache in 4 bits and the attention that reads it: what stands
+ * between the q/k/v linears and the o linear of a decoder block (the paper's
+ * serving engine has them as given; the formats and kernels are this
+ * library's).
+ *
+ * Pool: device uint8 [n_pages][n_kv_heads][page_size / 16][16 * (D + 8)],
+ * 16-byte aligned, owned by the caller. A block of 16 tokens of one head holds
+ * K codes [16][D / 2], V codes [16][D / 2], K parameters [16][2] and V
+ * parameters [16][2]; byte j of a row of codes holds element 2j in its low
+ * nibble and 2j + 1 in its high one, a parameter pair is bf16 (scale, offset),
+ * and an element stands for code * scale + offset. Slot number
+ * page * page_size + i names token i of a page.
+ *
+ * A row x of D fp32 values is quantised with one scale and offset:
+ *   scale = bf16_RNE((max x - min x) * fl32(1/15)), 0 if that is below 2^-126,
+ *   offset = bf16_RNE(min x),  inv = scale > 0 ? fl32(1 / scale) : 0,
+ *   code = clamp(rint((x - offset) * inv), 0, 15),
+ * each operation in fp32, round to nearest even. A row with an element that
+ * is not finite, or whose range is not, is held with scale = offset = NaN.
+ *
+ * Rotation (rope_dim R > 0): element pairs (i, i + R / 2), or (2i, 2i + 1) if
+ * rope_interleaved, i < R / 2, of the row at position p become
+ *   x1 * c - x2 * s  and  x2 * c + x1 * s,  c = table[p][i], s = table[p][R / 2 + i],
+ * products and sums each rounded to fp32; elements from R on stay as they are.
+ *
+ * Slots, positions, page numbers and lengths are device data that the host
+ * cannot check. The kernels check them: what is out of range is neither read
+ * nor written, and latches INVALID_ARG for spear_kv_check (an append skips the
+ * token; an attention call leaves that sequence's results unspecified).
+ * A handle's calls share its workspace: order them on one stream, or by
+ * events; distinct handles are independent and may share a pool.
+ * ---------------------------------------------------------------------- */
+typedef struct spear_kv_s* spear_kv_t;
+
+typedef struct {
+  int32_t n_heads;             /* query heads, a multiple of n_kv_heads; head h reads
+                                  key/value head h / (n_heads / n_kv_heads) */
+  int32_t n_kv_heads;          /* n_heads / n_kv_heads <= 32 */
+  int32_t head_dim;            /* D: 64 or 128 */
+  int32_t page_size;           /* tokens per page, a multiple of 16, <= 65536 */
+  int32_t n_pages;             /* pages in the pool (>= 1) */
+  void* pool;
+  int32_t rope_dim;            /* R: 0 (no rotation) or a multiple of 16, <= D */
+  int32_t rope_interleaved;
+  int32_t n_positions;         /* rows of rope_table (ignored when rope_dim == 0) */
+  const float* rope_table;     /* device, fp32 [n_positions][R], 16-byte aligned, kept by the
+                                  caller while the handle lives: R / 2 cosines, R / 2 sines */
+} spear_kv_desc_t;
+
+/* Build a handle over the caller's pool. Allocates the attention's workspace
+ * (partial results of work split over a long cache; its size depends on the
+ * device and the head counts only, not on lengths) and clears it on `stream`;
+ * the pool is not touched. Errors: INVALID_ARG (null or misaligned pointers,
+ * values outside the ranges above), OOM, CUDA; *out is NULL then. */
+spear_status_t spear_kv_create(const spear_kv_desc_t* desc, cudaStream_t stream, spear_kv_t* out);
+
+/* Rotate the queries and keys of T tokens and put their keys and values into
+ * the cache, in one launch.
+ *   q: device bf16 [T][n_heads][D], or NULL (no queries to rotate);
+ *   k, v: device bf16 [T][n_kv_heads][D];
+ *   ld_q, ld_k, ld_v, ld_q_out: elements from one token to the next, so that
+ *     slices of a fused projection's output can be passed as they are; heads
+ *     are contiguous. Multiples of 8, at least the row's length;
+ *   positions: device int64 [T] (ignored when rope_dim == 0);
+ *   slots: device int64 [T]; -1 leaves the token's key and value uncached;
+ *   q_out: device bf16 [T][n_heads][D], rotated queries; may be q itself.
+ * Two tokens of one call must not have the same slot. T == 0 is a no-op.
+ * Errors: INVALID_ARG, CUDA. */
+spear_status_t spear_kv_append(spear_kv_t h, const void* q, int64_t ld_q, const void* k, int64_t ld_k, const void* v,
+                               int64_t ld_v, const int64_t* positions, const int64_t* slots, int32_t T, void* q_out,
+                               int64_t ld_q_out, cudaStream_t stream);
+
+/* The values that T slots hold, bf16_RNE(code * scale + offset), into k_out
+ * and v_out: device bf16 [T][n_kv_heads][D], contiguous. Slot -1 gives zeros.
+ * Errors: INVALID_ARG, CUDA. */
+spear_status_t spear_kv_read(spear_kv_t h, const int64_t* slots, int32_t T, void* k_out, void* v_out,
+                             cudaStream_t stream);
+
+/* Causal attention of n_seqs sequences over the cache. Sequence b has the
+ * query rows q_starts[b] <= t < q_starts[b + 1] and L = kv_lens[b] cached
+ * tokens, its new ones included (append them first): key j is token
+ * j % page_size of page page_table[b][j / page_size]. Row i of its n rows
+ * stands at P = L - n + i and sees the keys j <= P, j >= 0, with window > 0
+ * only j > P - window:
+ *   out = bf16_RNE(sum_j softmax_j(scale * q . k_j) v_j),
+ * zeros for a row that sees no key. Softmax statistics and sums are fp32.
+ *   q, out: device bf16 [T][n_heads][D], ld_q, ld_out as for spear_kv_append;
+ *     out may be q itself;
+ *   page_table: device int32 [n_seqs][ld_pt];  kv_lens: device int32 [n_seqs];
+ *   q_starts: device int32 [n_seqs + 1], ascending, within 0..T;
+ *   max_q: the largest number of query rows of a sequence (>= 1).
+ * Sequences whose rows of one key/value head, (n_heads / n_kv_heads) x query
+ * rows, fit a few warp-MMA tiles run in a kernel that streams the cache once
+ * (single tokens, drafts to verify), longer ones in a tensor-core kernel; a
+ * mixed batch runs both. The call only enqueues, so it can be captured in a
+ * graph; lengths are read on the device when it runs.
+ * Errors: INVALID_ARG, CUDA. */
+spear_status_t spear_kv_attention(spear_kv_t h, const void* q, int64_t ld_q, void* out, int64_t ld_out,
+                                  const int32_t* page_table, int32_t ld_pt, const int32_t* kv_lens,
+                                  const int32_t* q_starts, int32_t n_seqs, int32_t T, int32_t max_q, float scale,
+                                  int32_t window, cudaStream_t stream);
+
+/* Synchronise `stream` and report the handle's device status: OK, or
+ * INVALID_ARG if a call since the last check met an index out of range, or
+ * TIMEOUT if a bounded device-side wait gave up. A status other than OK is
+ * cleared and the workspace reset. */
+spear_status_t spear_kv_check(spear_kv_t h, cudaStream_t stream);
+
+/* Free the handle's device memory (waits for queued work, as
+ * spear_linear_destroy does); the pool stays the caller's. NULL is accepted. */
+spear_status_t spear_kv_destroy(spear_kv_t h);
+
 /* Human-readable name of a status code (static storage). */
 const char* spear_status_string(spear_status_t s);
 

@@ -14,6 +14,7 @@ namespace spear {
 enum : unsigned {
   kStatusTimeoutZ = 1u,      // grid-wide "compensator projection done" wait gave up
   kStatusTimeoutPipe = 2u,   // an mbarrier wait in a pipeline gave up
+  kStatusBadIndex = 4u,      // key/value cache: a slot, position, page or length out of range
 };
 
 // Workspace of one handle (device memory, zero-initialised at create).

@@ -1,0 +1,44 @@
+// The key/value cache handle and the device-side view of its pool, shared by
+// the append/read kernels and the attention kernels.
+#pragma once
+#include "internal.h"
+
+struct KvView {
+  uint8_t* pool;
+  int n_heads, n_kv_heads, group;  // group = n_heads / n_kv_heads
+  int D;
+  int page_size, bpp;              // bpp = 16-token blocks per page
+  int n_pages;
+  int block_bytes;                 // 16 * (D + 8)
+  unsigned* status;
+};
+
+struct spear_kv_s {
+  KvView view;
+  int rope_dim, rope_interleaved, n_positions;
+  const float* rope_table;
+  int device, sm_count;
+  void* ws;
+  size_t ws_bytes;
+};
+
+// Arguments of one attention call.
+struct KvAttnArgs {
+  const __nv_bfloat16* q;
+  int64_t ld_q;
+  __nv_bfloat16* out;
+  int64_t ld_out;
+  const int32_t* page_table;
+  int ld_pt;
+  const int32_t* kv_lens;
+  const int32_t* q_starts;
+  int n_seqs, T, max_q;
+  float scale_log2;  // scale * log2(e): scores are kept in units of log2
+  int window;
+};
+
+// The workspace starts with the status word and one arrival counter per CTA of
+// the kernels that split a sequence (cleared at create), then partial results.
+constexpr size_t kKvControlBytes = 16384;
+size_t kv_attention_workspace(const spear_kv_s* h);
+spear_status_t kv_launch_attention(spear_kv_s* h, const KvAttnArgs& a, cudaStream_t stream);

@@ -1,0 +1,375 @@
+// The paged 4-bit key/value cache: handle lifetime, argument checks, the
+// append kernel (rotation, quantisation and the write into the pages, one
+// launch) and the read-back kernel.
+#include <math.h>
+
+#include <new>
+
+#include "kv.h"
+
+namespace spear {
+namespace {
+
+constexpr int kAppendThreads = 256;
+
+SPEAR_DEVINL uint4 ldg_stream(const void* p) {  // read once: keep it out of L1
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
+SPEAR_DEVINL void unpack8(const uint4& w, float (&x)[8]) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(u[i] << 16);
+    x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+  }
+}
+
+struct AppendParams {
+  KvView v;
+  const __nv_bfloat16 *q, *k, *val;
+  int64_t ld_q, ld_k, ld_v, ld_q_out;
+  const int64_t *positions, *slots;
+  int T;
+  __nv_bfloat16* q_out;
+  int rope_dim, interleaved, n_positions;
+  const float* table;
+  int q_rows;  // rotated query rows a token (0: none)
+  int rows;    // q_rows + 2 n_kv_heads
+  int chunk;   // rows of one token that a group of lanes takes
+  int chunks;  // ceil(rows / chunk)
+};
+
+// One row of D values is 8 elements a lane, LPR = D / 8 lanes. A group of LPR
+// lanes takes `chunk` rows of one token, so that the token's cosines and sines
+// (8 of each a lane, as many bytes as four rows) are read once for them.
+// Products and sums are rounded one by one (no contraction), so that the
+// codes are defined bit for bit. Bound by memory: a token reads and writes
+// (2 n_heads + 2 n_kv_heads) D bf16 and 2 n_kv_heads (D / 2 + 4) bytes.
+template <int D>
+__global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_constant__ AppendParams p) {
+  constexpr int LPR = D / 8;
+  const int sub = threadIdx.x % LPR;
+  const int64_t unit = (int64_t)blockIdx.x * (kAppendThreads / LPR) + threadIdx.x / LPR;
+  if (unit >= (int64_t)p.T * p.chunks) return;  // whole groups leave: the shuffles below are within a group
+  const int t = (int)(unit / p.chunks);
+  const int r0 = (int)(unit % p.chunks) * p.chunk;
+  const int r1 = min(r0 + p.chunk, p.rows);
+  const int e0 = sub * 8;
+
+  const int64_t slot = p.slots[t];
+  const int64_t n_slots = (int64_t)p.v.n_pages * p.v.page_size;
+  const bool held = slot >= 0 && slot < n_slots;
+  bool bad = slot < -1 || slot >= n_slots;
+  uint8_t* block = nullptr;
+  int row_in_block = 0;
+  if (held) {
+    const int page = (int)(slot / p.v.page_size), at = (int)(slot % p.v.page_size);
+    block = p.v.pool + ((int64_t)page * p.v.n_kv_heads * p.v.bpp + at / 16) * p.v.block_bytes;
+    row_in_block = at % 16;
+  }
+
+  // this lane's cosines and sines: of its 8 elements (halves) or its 4 pairs
+  const int half = p.rope_dim / 2;
+  const bool rotated = e0 < p.rope_dim;
+  float c[8], s[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) c[i] = 1.f, s[i] = 0.f;
+  if (p.rope_dim > 0) {
+    const int64_t pos = p.positions[t];
+    const bool ok = pos >= 0 && pos < p.n_positions;
+    bad |= !ok;
+    if (ok && rotated) {
+      const float* row = p.table + pos * p.rope_dim;
+      if (p.interleaved) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c[i] = row[e0 / 2 + i], s[i] = row[half + e0 / 2 + i];
+      } else {
+        const int at = e0 < half ? e0 : e0 - half;
+#pragma unroll
+        for (int i = 0; i < 8; i += 4) {
+          *reinterpret_cast<float4*>(c + i) = *reinterpret_cast<const float4*>(row + at + i);
+          *reinterpret_cast<float4*>(s + i) = *reinterpret_cast<const float4*>(row + half + at + i);
+        }
+      }
+    }
+  }
+  if (bad && sub == 0) atomicOr(p.v.status, kStatusBadIndex);
+
+  // the row's partner elements sit half / 8 lanes up or down
+  const int lane = threadIdx.x & 31;
+  const uint32_t mask = (uint32_t)((1ull << LPR) - 1) << (lane / LPR * LPR);
+  const int partner = rotated ? (e0 < half ? lane + half / 8 : lane - half / 8) : lane;
+
+  for (int r = r0; r < r1; ++r) {
+    const int kind = r < p.q_rows ? 0 : (r < p.q_rows + p.v.n_kv_heads ? 1 : 2);
+    const int head = kind == 0 ? r : (kind == 1 ? r - p.q_rows : r - p.q_rows - p.v.n_kv_heads);
+    const __nv_bfloat16* src = (kind == 0 ? p.q + t * p.ld_q : kind == 1 ? p.k + t * p.ld_k : p.val + t * p.ld_v) +
+                               (int64_t)head * D + e0;
+    float x[8];
+    unpack8(ldg_stream(src), x);
+    if (kind < 2 && p.rope_dim > 0) {
+      if (p.interleaved) {
+        if (rotated) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float a = x[2 * i], b = x[2 * i + 1];
+            x[2 * i] = __fsub_rn(__fmul_rn(a, c[i]), __fmul_rn(b, s[i]));
+            x[2 * i + 1] = __fadd_rn(__fmul_rn(b, c[i]), __fmul_rn(a, s[i]));
+          }
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float o = __shfl_sync(mask, x[i], partner);
+          if (rotated)
+            x[i] = e0 < half ? __fsub_rn(__fmul_rn(x[i], c[i]), __fmul_rn(o, s[i]))
+                             : __fadd_rn(__fmul_rn(x[i], c[i]), __fmul_rn(o, s[i]));
+        }
+      }
+    }
+    if (kind == 0) {
+      if (!bad) {
+        uint4 w;
+        w.x = pack_bf16x2(x[0], x[1]);
+        w.y = pack_bf16x2(x[2], x[3]);
+        w.z = pack_bf16x2(x[4], x[5]);
+        w.w = pack_bf16x2(x[6], x[7]);
+        *reinterpret_cast<uint4*>(p.q_out + t * p.ld_q_out + (int64_t)head * D + e0) = w;
+      }
+      continue;
+    }
+    float lo = x[0], hi = x[0], sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      lo = fminf(lo, x[i]);
+      hi = fmaxf(hi, x[i]);
+      sum += x[i] - x[i];  // 0, or NaN where an element is not finite
+    }
+#pragma unroll
+    for (int o = LPR / 2; o > 0; o >>= 1) {
+      lo = fminf(lo, __shfl_xor_sync(mask, lo, o));
+      hi = fmaxf(hi, __shfl_xor_sync(mask, hi, o));
+      sum += __shfl_xor_sync(mask, sum, o);
+    }
+    const float range = __fsub_rn(hi, lo);
+    __nv_bfloat16 sb = __float2bfloat16_rn(__fmul_rn(range, 1.0f / 15.0f));
+    __nv_bfloat16 ob = __float2bfloat16_rn(lo);
+    if (__bfloat162float(sb) < 1.17549435e-38f) sb = __float2bfloat16_rn(0.f);
+    const float sf = __bfloat162float(sb), of = __bfloat162float(ob);
+    const float inv = sf > 0.f ? __fdiv_rn(1.f, sf) : 0.f;
+    uint32_t codes = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float f = fminf(fmaxf(rintf(__fmul_rn(__fsub_rn(x[i], of), inv)), 0.f), 15.f);
+      codes |= (uint32_t)f << (4 * i);
+    }
+    uint32_t par = (uint32_t)__bfloat16_as_ushort(sb) | ((uint32_t)__bfloat16_as_ushort(ob) << 16);
+    if (!(sum == 0.f) || !(range <= 3.402823466e38f)) par = 0x7FC07FC0u;
+    if (block && !bad) {
+      uint8_t* b = block + (int64_t)head * p.v.bpp * p.v.block_bytes;
+      *reinterpret_cast<uint32_t*>(b + (kind - 1) * 8 * D + row_in_block * (D / 2) + sub * 4) = codes;
+      if (sub == 0) *reinterpret_cast<uint32_t*>(b + 16 * D + (kind - 1) * 64 + row_in_block * 4) = par;
+    }
+  }
+}
+
+// A group of D / 8 lanes hands back one row (8 elements a lane).
+template <int D>
+__global__ void __launch_bounds__(kAppendThreads)
+    read_kernel(KvView v, const int64_t* __restrict__ slots, int T, __nv_bfloat16* k_out, __nv_bfloat16* v_out) {
+  constexpr int LPR = D / 8;
+  const int sub = threadIdx.x % LPR;
+  const int64_t unit = (int64_t)blockIdx.x * (kAppendThreads / LPR) + threadIdx.x / LPR;
+  if (unit >= (int64_t)T * v.n_kv_heads * 2) return;
+  const int is_v = (int)(unit % 2);
+  const int64_t row = unit / 2;  // token * n_kv_heads + head
+  const int t = (int)(row / v.n_kv_heads), head = (int)(row % v.n_kv_heads);
+  const int64_t slot = slots[t];
+  uint4 w = make_uint4(0, 0, 0, 0);
+  if (slot >= 0 && slot < (int64_t)v.n_pages * v.page_size) {
+    const int page = (int)(slot / v.page_size), at = (int)(slot % v.page_size);
+    const uint8_t* b = v.pool + (((int64_t)page * v.n_kv_heads + head) * v.bpp + at / 16) * v.block_bytes;
+    const uint32_t codes = *reinterpret_cast<const uint32_t*>(b + is_v * 8 * D + (at % 16) * (D / 2) + sub * 4);
+    const uint32_t par = *reinterpret_cast<const uint32_t*>(b + 16 * D + is_v * 64 + (at % 16) * 4);
+    const float s = __uint_as_float(par << 16), o = __uint_as_float(par & 0xFFFF0000u);
+    uint32_t r[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      r[i] = pack_bf16x2(fmaf((float)((codes >> (8 * i)) & 15u), s, o), fmaf((float)((codes >> (8 * i + 4)) & 15u), s, o));
+    w = make_uint4(r[0], r[1], r[2], r[3]);
+  } else if (slot != -1 && sub == 0) {
+    atomicOr(v.status, kStatusBadIndex);
+  }
+  *reinterpret_cast<uint4*>((is_v ? v_out : k_out) + row * D + sub * 8) = w;
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool row_ok(const void* p, int64_t ld, int64_t len) { return p && aligned16(p) && ld % 8 == 0 && ld >= len; }
+
+}  // namespace
+}  // namespace spear
+
+using namespace spear;
+
+extern "C" {
+
+spear_status_t spear_kv_create(const spear_kv_desc_t* d, cudaStream_t stream, spear_kv_t* out) {
+  if (!out) return SPEAR_ERR_INVALID_ARG;
+  *out = nullptr;
+  if (!d || !d->pool || !aligned16(d->pool)) return SPEAR_ERR_INVALID_ARG;
+  if (d->n_kv_heads < 1 || d->n_heads < d->n_kv_heads || d->n_heads % d->n_kv_heads != 0 ||
+      d->n_heads / d->n_kv_heads > 32 || d->n_heads > 65535)
+    return SPEAR_ERR_INVALID_ARG;
+  if (d->head_dim != 64 && d->head_dim != 128) return SPEAR_ERR_INVALID_ARG;
+  if (d->page_size < 16 || d->page_size % 16 != 0 || d->page_size > 65536 || d->n_pages < 1)
+    return SPEAR_ERR_INVALID_ARG;
+  if (d->rope_dim < 0 || d->rope_dim % 16 != 0 || d->rope_dim > d->head_dim) return SPEAR_ERR_INVALID_ARG;
+  if (d->rope_dim > 0 && (d->n_positions < 1 || !d->rope_table || !aligned16(d->rope_table)))
+    return SPEAR_ERR_INVALID_ARG;
+  spear_kv_s* h = new (std::nothrow) spear_kv_s();
+  if (!h) return SPEAR_ERR_OOM;
+  h->view.pool = static_cast<uint8_t*>(d->pool);
+  h->view.n_heads = d->n_heads;
+  h->view.n_kv_heads = d->n_kv_heads;
+  h->view.group = d->n_heads / d->n_kv_heads;
+  h->view.D = d->head_dim;
+  h->view.page_size = d->page_size;
+  h->view.bpp = d->page_size / 16;
+  h->view.n_pages = d->n_pages;
+  h->view.block_bytes = 16 * (d->head_dim + 8);
+  h->rope_dim = d->rope_dim;
+  h->rope_interleaved = d->rope_interleaved != 0;
+  h->n_positions = d->n_positions;
+  h->rope_table = d->rope_table;
+  cudaError_t e = cudaGetDevice(&h->device);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&h->sm_count, cudaDevAttrMultiProcessorCount, h->device);
+  if (e == cudaSuccess) {
+    h->ws_bytes = kv_attention_workspace(h);
+    e = cudaMalloc(&h->ws, h->ws_bytes);
+  }
+  if (e == cudaSuccess) e = cudaMemsetAsync(h->ws, 0, kKvControlBytes, stream);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    if (h->ws) cudaFree(h->ws);
+    delete h;
+    return e == cudaErrorMemoryAllocation ? SPEAR_ERR_OOM : SPEAR_ERR_CUDA;
+  }
+  h->view.status = static_cast<unsigned*>(h->ws);
+  *out = h;
+  return SPEAR_OK;
+}
+
+spear_status_t spear_kv_append(spear_kv_t h, const void* q, int64_t ld_q, const void* k, int64_t ld_k, const void* v,
+                               int64_t ld_v, const int64_t* positions, const int64_t* slots, int32_t T, void* q_out,
+                               int64_t ld_q_out, cudaStream_t stream) {
+  if (!h || T < 0) return SPEAR_ERR_INVALID_ARG;
+  if (T == 0) return SPEAR_OK;
+  const int64_t D = h->view.D, qn = h->view.n_heads * D, kn = h->view.n_kv_heads * D;
+  if (!row_ok(k, ld_k, kn) || !row_ok(v, ld_v, kn) || !slots || (h->rope_dim > 0 && !positions))
+    return SPEAR_ERR_INVALID_ARG;
+  if (q && (!row_ok(q, ld_q, qn) || !row_ok(q_out, ld_q_out, qn))) return SPEAR_ERR_INVALID_ARG;
+  AppendParams p;
+  p.v = h->view;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.k = static_cast<const __nv_bfloat16*>(k);
+  p.val = static_cast<const __nv_bfloat16*>(v);
+  p.ld_q = ld_q;
+  p.ld_k = ld_k;
+  p.ld_v = ld_v;
+  p.ld_q_out = ld_q_out;
+  p.positions = positions;
+  p.slots = slots;
+  p.T = T;
+  p.q_out = static_cast<__nv_bfloat16*>(q_out);
+  p.rope_dim = h->rope_dim;
+  p.interleaved = h->rope_interleaved;
+  p.n_positions = h->n_positions;
+  p.table = h->rope_table;
+  p.q_rows = q ? h->view.n_heads : 0;
+  p.rows = p.q_rows + 2 * h->view.n_kv_heads;
+  p.chunk = 1;
+  p.chunks = p.rows;
+  const int64_t per_block = kAppendThreads / (D / 8);
+  const int64_t blocks = ((int64_t)T * p.chunks + per_block - 1) / per_block;
+  if (blocks > 0x7FFFFFFF) return SPEAR_ERR_INVALID_ARG;
+  if (D == 128)
+    append_kernel<128><<<(unsigned)blocks, kAppendThreads, 0, stream>>>(p);
+  else
+    append_kernel<64><<<(unsigned)blocks, kAppendThreads, 0, stream>>>(p);
+  return cudaGetLastError() == cudaSuccess ? SPEAR_OK : SPEAR_ERR_CUDA;
+}
+
+spear_status_t spear_kv_read(spear_kv_t h, const int64_t* slots, int32_t T, void* k_out, void* v_out,
+                             cudaStream_t stream) {
+  if (!h || T < 0) return SPEAR_ERR_INVALID_ARG;
+  if (T == 0) return SPEAR_OK;
+  if (!slots || !k_out || !v_out || !aligned16(k_out) || !aligned16(v_out)) return SPEAR_ERR_INVALID_ARG;
+  const int D = h->view.D;
+  const int64_t per_block = kAppendThreads / (D / 8);
+  const int64_t blocks = ((int64_t)T * h->view.n_kv_heads * 2 + per_block - 1) / per_block;
+  if (blocks > 0x7FFFFFFF) return SPEAR_ERR_INVALID_ARG;
+  auto* ko = static_cast<__nv_bfloat16*>(k_out);
+  auto* vo = static_cast<__nv_bfloat16*>(v_out);
+  if (D == 128)
+    read_kernel<128><<<(unsigned)blocks, kAppendThreads, 0, stream>>>(h->view, slots, T, ko, vo);
+  else
+    read_kernel<64><<<(unsigned)blocks, kAppendThreads, 0, stream>>>(h->view, slots, T, ko, vo);
+  return cudaGetLastError() == cudaSuccess ? SPEAR_OK : SPEAR_ERR_CUDA;
+}
+
+spear_status_t spear_kv_attention(spear_kv_t h, const void* q, int64_t ld_q, void* out, int64_t ld_out,
+                                  const int32_t* page_table, int32_t ld_pt, const int32_t* kv_lens,
+                                  const int32_t* q_starts, int32_t n_seqs, int32_t T, int32_t max_q, float scale,
+                                  int32_t window, cudaStream_t stream) {
+  if (!h || n_seqs < 0 || T < 0) return SPEAR_ERR_INVALID_ARG;
+  if (n_seqs == 0 || T == 0) return SPEAR_OK;
+  const int64_t qn = (int64_t)h->view.n_heads * h->view.D;
+  if (!row_ok(q, ld_q, qn) || !row_ok(out, ld_out, qn) || !page_table || ld_pt < 1 || !kv_lens || !q_starts ||
+      max_q < 1 || window < 0 || !isfinite(scale))
+    return SPEAR_ERR_INVALID_ARG;
+  // out is q itself or lies apart from it
+  const char *qb = static_cast<const char*>(q), *ob = static_cast<const char*>(out);
+  const int64_t qs = ((T - 1) * ld_q + qn) * 2, os = ((T - 1) * ld_out + qn) * 2;
+  if ((qb != ob || ld_q != ld_out) && qb < ob + os && ob < qb + qs) return SPEAR_ERR_INVALID_ARG;
+  KvAttnArgs a;
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.ld_q = ld_q;
+  a.out = static_cast<__nv_bfloat16*>(out);
+  a.ld_out = ld_out;
+  a.page_table = page_table;
+  a.ld_pt = ld_pt;
+  a.kv_lens = kv_lens;
+  a.q_starts = q_starts;
+  a.n_seqs = n_seqs;
+  a.T = T;
+  a.max_q = max_q;
+  a.scale_log2 = scale * 1.44269504088896340736f;
+  a.window = window;
+  return kv_launch_attention(h, a, stream);
+}
+
+spear_status_t spear_kv_check(spear_kv_t h, cudaStream_t stream) {
+  if (!h) return SPEAR_ERR_INVALID_ARG;
+  if (cudaStreamSynchronize(stream) != cudaSuccess) return SPEAR_ERR_CUDA;
+  unsigned status = 0;
+  if (cudaMemcpy(&status, h->view.status, sizeof status, cudaMemcpyDeviceToHost) != cudaSuccess)
+    return SPEAR_ERR_CUDA;
+  if (status == 0) return SPEAR_OK;
+  if (cudaMemset(h->ws, 0, kKvControlBytes) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess)
+    return SPEAR_ERR_CUDA;
+  return (status & kStatusTimeoutPipe) ? SPEAR_ERR_TIMEOUT : SPEAR_ERR_INVALID_ARG;
+}
+
+spear_status_t spear_kv_destroy(spear_kv_t h) {
+  if (!h) return SPEAR_OK;
+  if (h->ws) cudaFree(h->ws);
+  delete h;
+  return SPEAR_OK;
+}
+
+}  // extern "C"

@@ -30,6 +30,12 @@ class spear_linear_desc_t(ctypes.Structure):
                 ("gate_hidden", c_int32), ("gate_w1", c_void_p), ("gate_w2", c_void_p)]
 
 
+class spear_kv_desc_t(ctypes.Structure):
+    _fields_ = [("n_heads", c_int32), ("n_kv_heads", c_int32), ("head_dim", c_int32), ("page_size", c_int32),
+                ("n_pages", c_int32), ("pool", c_void_p), ("rope_dim", c_int32), ("rope_interleaved", c_int32),
+                ("n_positions", c_int32), ("rope_table", c_void_p)]
+
+
 class SpearError(RuntimeError):
     def __init__(self, status: int, what: str):
         self.status = status
@@ -88,11 +94,21 @@ def load(path: Path | None = None):
     L.spear_decode_schedule.restype = c_int
     L.spear_prefill_schedule.argtypes = [c_int32] * 7 + [c_void_p, c_void_p, c_int32]
     L.spear_prefill_schedule.restype = c_int
+    L.spear_kv_create.argtypes = [POINTER(spear_kv_desc_t), H, POINTER(c_void_p)]
+    L.spear_kv_append.argtypes = [H, c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_void_p,
+                                  c_int32, c_void_p, c_int64, H]
+    L.spear_kv_read.argtypes = [H, c_void_p, c_int32, c_void_p, c_void_p, H]
+    L.spear_kv_attention.argtypes = [H, c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int32, c_void_p, c_void_p,
+                                     c_int32, c_int32, c_int32, c_float, c_int32, H]
+    L.spear_kv_check.argtypes = [H, H]
+    L.spear_kv_destroy.argtypes = [H]
     L.spear_status_string.argtypes = [c_int]
     L.spear_status_string.restype = c_char_p
     for name in ("spear_linear_create", "spear_linear_forward_decode", "spear_linear_forward_prefill",
                  "spear_linear_forward", "spear_linear_forward_host", "spear_linear_destroy",
-                 "spear_linear_dequantize", "spear_linear_check", "spear_linear_debug_set"):
+                 "spear_linear_dequantize", "spear_linear_check", "spear_linear_debug_set",
+                 "spear_kv_create", "spear_kv_append", "spear_kv_read", "spear_kv_attention", "spear_kv_check",
+                 "spear_kv_destroy"):
         getattr(L, name).restype = c_int
     _lib = L
     return L
@@ -290,6 +306,133 @@ def quantize_rtn(w, group_size=128, stream=None):
     _check(load().spear_quantize_rtn(_ptr(w), int(N), int(K), int(group_size), _ptr(q), _ptr(s), _ptr(z),
                                      _stream(stream)), "spear_quantize_rtn")
     return q, s, z
+
+
+def kv_page_bytes(n_kv_heads: int, head_dim: int, page_size: int) -> int:
+    """Bytes of one page of the 4-bit key/value cache."""
+    return n_kv_heads * (page_size // 16) * 16 * (head_dim + 8)
+
+
+def kv_pool(n_pages: int, n_kv_heads: int, head_dim: int, page_size: int, device="cuda"):
+    """A zeroed pool for :class:`SpearKVCache`: uint8 [n_pages][n_kv_heads][page bytes of a head]."""
+    import torch
+    return torch.zeros((n_pages, n_kv_heads, kv_page_bytes(1, head_dim, page_size)), dtype=torch.uint8, device=device)
+
+
+def rope_table(n_positions: int, rope_dim: int, base: float = 10000.0, device="cuda"):
+    """fp32 [n_positions][rope_dim]: the cosines, then the sines, of p * base^(-2 i / rope_dim)."""
+    import torch
+    inv = base ** (-torch.arange(0, rope_dim, 2, device=device, dtype=torch.float64) / rope_dim)
+    a = torch.arange(n_positions, device=device, dtype=torch.float64)[:, None] * inv
+    return torch.cat([a.cos(), a.sin()], 1).float().contiguous()
+
+
+class SpearKVCache:
+    """Owner of one ``spear_kv_t``: a paged 4-bit key/value cache with the
+    append that fills it and the attention that reads it.
+
+    ``pool`` uint8 [n_pages][n_kv_heads][page_size * (head_dim + 8)] (see
+    :func:`kv_pool`) and ``rope_table`` fp32 [n_positions][rope_dim] or None are
+    CUDA tensors that the object keeps; layers may share a table, and handles
+    over different pools are independent.
+    """
+
+    def __init__(self, n_heads, n_kv_heads, head_dim, page_size, pool, rope_table=None, rope_interleaved=False,
+                 stream=None):
+        import torch
+        page = kv_page_bytes(n_kv_heads, head_dim, page_size)
+        if pool.dtype != torch.uint8 or not pool.is_cuda or not pool.is_contiguous() or \
+                pool.numel() != pool.shape[0] * page:
+            raise ValueError(f"pool must be contiguous CUDA uint8 [n_pages][{page} bytes a page]")
+        if rope_table is not None and (rope_table.dtype != torch.float32 or rope_table.dim() != 2 or
+                                       not rope_table.is_cuda or not rope_table.is_contiguous()):
+            raise ValueError("rope_table must be contiguous CUDA fp32 [n_positions][rope_dim]")
+        positions, rope_dim = (0, 0) if rope_table is None else rope_table.shape
+        d = spear_kv_desc_t(int(n_heads), int(n_kv_heads), int(head_dim), int(page_size), int(pool.shape[0]),
+                            _ptr(pool), int(rope_dim), int(bool(rope_interleaved)), int(positions), _ptr(rope_table))
+        h = c_void_p()
+        L = load()
+        _check(L.spear_kv_create(byref(d), _stream(stream), byref(h)), "spear_kv_create")
+        self.h, self.pool, self.rope_table = h, pool, rope_table
+        self.n_heads, self.n_kv_heads, self.head_dim, self.page_size = n_heads, n_kv_heads, head_dim, page_size
+        self._q_row, self._kv_row = (n_heads, head_dim), (n_kv_heads, head_dim)
+        self._bf16, self._i64, self._i32 = torch.bfloat16, torch.int64, torch.int32
+        self._fns = L.spear_kv_append, L.spear_kv_read, L.spear_kv_attention
+
+    def _rows(self, x, row, what):
+        """The token stride of bf16 [T][heads][D] with contiguous heads."""
+        if x.dtype is not self._bf16 or x.dim() != 3 or x.shape[1:] != row or not x.is_cuda:
+            raise ValueError(f"{what} must be CUDA bf16 [T][{row[0]}][{row[1]}]")
+        s = x.stride()
+        if s[2] != 1 or (s[1] != row[1] and row[0] > 1):
+            raise ValueError(f"{what}: the heads of a token must be contiguous")
+        return s[0] if x.shape[0] > 1 else max(s[0], row[0] * row[1])
+
+    def _index(self, x, dtype, n, what):
+        if x.dtype is not dtype or not x.is_cuda or not x.is_contiguous() or x.numel() < n:
+            raise ValueError(f"{what} must be a contiguous CUDA {dtype} tensor of at least {n} elements")
+        return x.data_ptr()
+
+    def append(self, q, k, v, positions, slots, q_out=None, stream=None):
+        """Rotate q [T][n_heads][D] (or None) and k [T][n_kv_heads][D] to the
+        int64 ``positions`` and put k and v into the int64 ``slots`` (-1: not
+        cached). The rotated queries go to ``q_out`` (default: q in place)."""
+        T = k.shape[0]
+        if v.shape[0] != T or (q is not None and q.shape[0] != T):
+            raise ValueError("q, k and v must have the same number of tokens")
+        ldq = ldo = 0
+        if q is not None:
+            if q_out is None:
+                q_out = q
+            elif q_out.shape[0] != T:
+                raise ValueError("q_out must have as many tokens as q")
+            ldq, ldo = self._rows(q, self._q_row, "q"), self._rows(q_out, self._q_row, "q_out")
+        pos = None if self.rope_table is None else self._index(positions, self._i64, T, "positions")
+        _check(self._fns[0](self.h, _ptr(q), ldq, k.data_ptr(), self._rows(k, self._kv_row, "k"), v.data_ptr(),
+                            self._rows(v, self._kv_row, "v"), pos, self._index(slots, self._i64, T, "slots"), T,
+                            _ptr(q_out), ldo, _stream(stream)), "spear_kv_append")
+        return q_out
+
+    def read(self, slots, k_out, v_out, stream=None):
+        """The cached keys and values of ``slots`` as bf16 [T][n_kv_heads][D]."""
+        T = slots.shape[0]
+        for x, what in ((k_out, "k_out"), (v_out, "v_out")):
+            if x.dtype is not self._bf16 or x.shape != (T, *self._kv_row) or not x.is_cuda or not x.is_contiguous():
+                raise ValueError(f"{what} must be contiguous CUDA bf16 [{T}][n_kv_heads][head_dim]")
+        _check(self._fns[1](self.h, self._index(slots, self._i64, T, "slots"), T, k_out.data_ptr(), v_out.data_ptr(),
+                            _stream(stream)), "spear_kv_read")
+        return k_out, v_out
+
+    def attention(self, q, out, page_table, kv_lens, q_starts, max_q, scale=None, window=0, stream=None):
+        """Causal attention of the query rows q [T][n_heads][D] over the cache
+        into ``out`` (see spear_kv_attention): int32 ``page_table``
+        [n_seqs][max pages], ``kv_lens`` [n_seqs], ``q_starts`` [n_seqs + 1];
+        ``scale`` defaults to head_dim ** -0.5, ``window`` 0 means all earlier keys."""
+        T, n = q.shape[0], page_table.shape[0]
+        if out.shape[0] != T or page_table.dim() != 2:
+            raise ValueError("out must have as many tokens as q, page_table two dimensions")
+        _check(self._fns[2](self.h, q.data_ptr(), self._rows(q, self._q_row, "q"), out.data_ptr(),
+                            self._rows(out, self._q_row, "out"),
+                            self._index(page_table, self._i32, n, "page_table"), page_table.shape[1],
+                            self._index(kv_lens, self._i32, n, "kv_lens"),
+                            self._index(q_starts, self._i32, n + 1, "q_starts"), n, T, max_q,
+                            self.head_dim ** -0.5 if scale is None else scale, window, _stream(stream)),
+               "spear_kv_attention")
+        return out
+
+    def check(self, stream=None) -> int:
+        return load().spear_kv_check(self.h, _stream(stream))
+
+    def close(self) -> None:
+        if getattr(self, "h", None) and self.h.value:
+            load().spear_kv_destroy(self.h)
+            self.h = c_void_p()
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
 
 
 DECODE_SCHEDULE_FIELDS = ("grid", "P", "NW", "T", "MT", "KW", "KC", "NS", "stage_bytes", "smem", "n_stages",
