@@ -40,5 +40,12 @@ struct KvAttnArgs {
 // The workspace starts with the status word and one arrival counter per CTA of
 // the kernels that split a sequence (cleared at create), then partial results.
 constexpr size_t kKvControlBytes = 16384;
+constexpr int kKvMaxTokens = 1 << 30;  // longest sequence: key numbers and their sums with a tile fit 32 bits
+constexpr int kKvDecodeRows = 32;      // most rows of a key/value head that the cache-streaming kernel takes
+// The kernel that streams the cache for sequences of at most 8 nt rows a
+// key/value head (nt 1, 2 or 4); others are left out.
+spear_status_t kv_launch_decode(const spear_kv_s* h, const KvAttnArgs& a, int nt, float* part, unsigned* counters,
+                                cudaStream_t stream);
+size_t kv_decode_workspace(const spear_kv_s* h);
 size_t kv_attention_workspace(const spear_kv_s* h);
 spear_status_t kv_launch_attention(spear_kv_s* h, const KvAttnArgs& a, cudaStream_t stream);

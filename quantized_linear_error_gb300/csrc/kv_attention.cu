@@ -9,7 +9,7 @@ constexpr int kThreads = 128;
 // One warp per (query row, head): every visible key in turn, softmax with a
 // running maximum and sum, D / 32 elements a lane.
 template <int D>
-__global__ void __launch_bounds__(kThreads) simple_kernel(KvView v, KvAttnArgs a) {
+__global__ void __launch_bounds__(kThreads) simple_kernel(KvView v, KvAttnArgs a, int max_rows) {
   constexpr int E = D / 32;
   const int lane = threadIdx.x & 31;
   const int64_t unit = (int64_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
@@ -21,6 +21,7 @@ __global__ void __launch_bounds__(kThreads) simple_kernel(KvView v, KvAttnArgs a
   b = __reduce_max_sync(0xffffffffu, b);
   if (b < 0) return;
   const int n = a.q_starts[b + 1] - a.q_starts[b];
+  if (n * v.group <= max_rows) return;
   const int64_t room = (int64_t)a.ld_pt * v.page_size;
   int64_t L = a.kv_lens[b];
   if (L < 0 || L > room) {
@@ -73,14 +74,27 @@ __global__ void __launch_bounds__(kThreads) simple_kernel(KvView v, KvAttnArgs a
 
 using namespace spear;
 
-size_t kv_attention_workspace(const spear_kv_s*) { return kKvControlBytes; }
+size_t kv_attention_workspace(const spear_kv_s* h) { return kKvControlBytes + kv_decode_workspace(h); }
 
 spear_status_t kv_launch_attention(spear_kv_s* h, const KvAttnArgs& a, cudaStream_t stream) {
+  char* ws = static_cast<char*>(h->ws);
+  auto* counters = reinterpret_cast<unsigned*>(ws + 128);
+  auto* part = reinterpret_cast<float*>(ws + kKvControlBytes);
+  const int64_t most = (int64_t)a.max_q * h->view.group;
+  const bool chunks = most > kKvDecodeRows;
+  const int64_t few = chunks ? h->view.group : most;
+  const int nt = few <= 8 ? 1 : (few <= 16 ? 2 : 4);
+  int max_rows = 0;
+  if (!chunks || a.n_seqs > 1) {
+    max_rows = 8 * nt;
+    const spear_status_t st = kv_launch_decode(h, a, nt, part, counters, stream);
+    if (st != SPEAR_OK || !chunks) return st;
+  }
   const int64_t blocks = ((int64_t)a.T * h->view.n_heads + kThreads / 32 - 1) / (kThreads / 32);
   if (blocks > 0x7FFFFFFF) return SPEAR_ERR_INVALID_ARG;
   if (h->view.D == 128)
-    simple_kernel<128><<<(unsigned)blocks, kThreads, 0, stream>>>(h->view, a);
+    simple_kernel<128><<<(unsigned)blocks, kThreads, 0, stream>>>(h->view, a, max_rows);
   else
-    simple_kernel<64><<<(unsigned)blocks, kThreads, 0, stream>>>(h->view, a);
+    simple_kernel<64><<<(unsigned)blocks, kThreads, 0, stream>>>(h->view, a, max_rows);
   return cudaGetLastError() == cudaSuccess ? SPEAR_OK : SPEAR_ERR_CUDA;
 }

@@ -1,0 +1,568 @@
+// Attention of a few query rows over the paged 4-bit cache: one new token a
+// sequence, or a few drafted ones.
+//
+// For each (sequence, key/value head) the R = 8 NT rows (query tokens x the
+// heads that share the key/value head) meet every visible key once:
+//   s = scale (q . k),  out = sum 2^(s - m) v / sum 2^(s - m)   (s in log2),
+// so the cache is read once, (D + 8) bytes a key for 4 D R flops: bound by
+// memory as long as the instructions that unpack the codes keep up.
+//
+//  - Products run on warp MMAs (m16n8k16) with the cache as the A operand and
+//    the rows as the 8 columns of B, so that no tensor work is spent on padding
+//    a single token's few heads to 16 rows. (tcgen05 would want 128 rows of
+//    dequantised keys written to tensor or shared memory for 8 columns.)
+//  - K: four lanes hold a key's codes, D / 4 channels each, in the order of its
+//    bytes; a code pair becomes the bf16 pair (128 + c) with a mask and an
+//    exponent, the rows of q are permuted alike, and the accumulator starts at
+//    -128 sum(q), so that it ends as q . c. Then s = S (q . c) + O sum(q) with
+//    the key's scale S and offset O.
+//  - V: two keys' words are interleaved by two byte permutes, so that a register
+//    holds one channel of two keys, as the A operand of out^T = V^T p^T wants
+//    it. Codes enter centred, c - 8, exact in bf16 (small magnitudes: neither
+//    the fp32 sums nor the rounding of p S to bf16 lose to a large common
+//    term); sum p (O + 8 S) is kept beside it in fp32. The scores' accumulator
+//    layout becomes p^T's operand layout by one 8 x 8 transpose (movmatrix).
+//  - The running maximum is lazy: p = 2^(s - m) with any m that is at most 8
+//    below the maximum; sums are only rescaled when some score passes m + 8.
+//
+// Work: (sequence, head, tile of 128 keys) units, in this order, are split
+// evenly over the CTAs, whatever the lengths, which only the device knows. A
+// CTA's run is a list of segments, one an item (sequence, head). Partial
+// results of items that several CTAs share go to the workspace; the last CTA
+// of an item to arrive joins them in CTA order (the same bits every time) and
+// resets the counter. No CTA waits for another.
+//
+// A CTA: four warps, 32 keys of a tile each with a state of their own, joined
+// at the end of a segment; a fifth warp copies the tiles' 16-token blocks (one
+// bulk copy each, whatever the page size) into a ring of stages.
+#include <atomic>
+
+#include "kv_device.cuh"
+
+namespace spear {
+namespace {
+
+constexpr int kWarps = 4;                      // consumer warps
+constexpr int kThreads = 32 * (kWarps + 1);
+constexpr int kTile = 32 * kWarps;             // keys of a unit
+constexpr int kBlocksPerTile = kTile / 16;
+constexpr int kMaxStages = 16;
+constexpr float kLazy = 8.f;
+
+struct DecodeParams {
+  KvView v;
+  KvAttnArgs a;
+  int max_rows;        // sequences with more rows of a key/value head are left to the other kernel
+  int NS;              // stages
+  uint32_t stage_bytes;
+  float* part;         // [grid][2][R D + 2 R]
+  unsigned* counters;  // [grid]
+  uint64_t wait_ns;
+};
+
+// Row r of 16 keys of an MMA tile is key kpi(r) of its block: lanes that read
+// K rows (2 i, 2 i + 1 of a quarter warp) then meet rows of both parities, and
+// those that read V rows (2 t, 2 t + 1) rows t and (t + 4) ^ 1: fewer bank conflicts.
+SPEAR_DEVINL int kpi(int r) { return (r & 1) ? ((r >> 1) + 4) ^ 1 : r >> 1; }
+
+template <int N>
+SPEAR_DEVINL void lds_words(uint32_t addr, uint32_t (&w)[N]) {
+  static_assert(N == 1 || N == 2 || N == 4, "");
+  if constexpr (N == 4)
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(addr));
+  else if constexpr (N == 2)
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
+  else
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(addr));
+}
+
+SPEAR_DEVINL uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
+  uint32_t r;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
+  return r;
+}
+
+SPEAR_DEVINL uint32_t movmatrix(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+
+SPEAR_DEVINL void consumer_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory"); }
+
+// A position in the list of units.
+struct Cursor {
+  int b, h, tile;  // tile counts from s.lo
+  KvSeq s;
+};
+
+SPEAR_DEVINL int64_t seq_units(const DecodeParams& p, const KvSeq& s) {
+  return s.n > 0 && s.n * p.v.group <= p.max_rows ? (int64_t)s.tiles * p.v.n_kv_heads : 0;
+}
+
+// The next item's first unit (the caller knows that there is one).
+SPEAR_DEVINL void next_item(const DecodeParams& p, Cursor& c) {
+  c.tile = 0;
+  if (++c.h < p.v.n_kv_heads) return;
+  c.h = 0;
+  do {
+    ++c.b;
+    c.s = kv_seq(p.v, p.a, c.b, kTile);
+  } while (seq_units(p, c.s) == 0);
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads, 4 / NT > 3 ? 3 : 4 / NT)
+    decode_kernel(const __grid_constant__ DecodeParams p) {
+  constexpr int R = 8 * NT;
+  constexpr int BB = 16 * (D + 8);
+  constexpr int KW = D / 32;       // code words of a K row a lane
+  constexpr int VW = D / 64;       // code words of a V row a lane
+  constexpr int E = D / 32;        // elements of a result row a lane
+  constexpr int OS = D + 4;        // row stride of the joined results
+  constexpr int kPart = R * D + 2 * R;
+  extern __shared__ __align__(128) uint8_t smem[];
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem);
+  uint64_t* empty = full + kMaxStages;
+  int64_t* scan = reinterpret_cast<int64_t*>(empty + kMaxStages);  // [kWarps + 1] warp sums, total, unit of the start
+  int* found = reinterpret_cast<int*>(scan + 8);
+  float* ml = reinterpret_cast<float*>(smem + 512);                // [kWarps][R][2]
+  float* om = ml + kWarps * R * 2;                                 // [kWarps][R][OS]
+  const uint32_t om_bytes = (kWarps * R * (2 + OS)) * 4;
+  const uint32_t stages_at = smem_u32(smem) + 512 + (om_bytes + 127) / 128 * 128;
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid & 31;
+
+  if (tid == 0) {
+    for (int i = 0; i < p.NS; ++i) {
+      mbar_init(full + i, 1);
+      mbar_init(empty + i, kWarps);
+    }
+    fence_mbar_init();
+  }
+
+  // ---- this CTA's units [u0, u1)
+  int64_t sum = 0;
+  for (int b = tid; b < p.a.n_seqs; b += kThreads) sum += seq_units(p, kv_seq(p.v, p.a, b, kTile));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (lane == 0) scan[warp] = sum;
+  __syncthreads();
+  int64_t U = 0;
+#pragma unroll
+  for (int w = 0; w <= kWarps; ++w) U += scan[w];
+  const int64_t G = min((int64_t)gridDim.x, U);
+  const int64_t cta = blockIdx.x;
+  if (cta >= G) return;
+  const int64_t u0 = cta * U / G, u1 = (cta + 1) * U / G;
+  // the sequence that u0 falls into
+  if (warp == 0) {
+    int64_t before = 0;
+    for (int b0 = 0; b0 < p.a.n_seqs; b0 += 32) {
+      const int b = b0 + lane;
+      const int64_t own = b < p.a.n_seqs ? seq_units(p, kv_seq(p.v, p.a, b, kTile)) : 0;
+      int64_t incl = own;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += x;
+      }
+      if (own > 0 && u0 >= before + incl - own && u0 < before + incl) {
+        found[0] = b;
+        scan[5] = u0 - (before + incl - own);
+      }
+      before += __shfl_sync(0xffffffffu, incl, 31);
+      if (before > u0) break;
+    }
+  }
+  __syncthreads();
+  Cursor c;
+  c.b = found[0];
+  c.s = kv_seq(p.v, p.a, c.b, kTile);
+  c.h = (int)(scan[5] / c.s.tiles);
+  c.tile = (int)(scan[5] % c.s.tiles);
+
+  if (warp == kWarps) {
+    // ---------------------------------------------------------------- producer
+    int st = 0;
+    unsigned phase = 0;
+    bool bad = false;
+    int64_t issued = 0;
+    for (int64_t u = u0; u < u1; ++u) {
+      const int blk = (c.s.lo + c.tile) * kBlocksPerTile + lane;
+      const bool wanted = lane < kBlocksPerTile && blk < (c.s.L + 15) / 16;
+      const uint8_t* src = nullptr;
+      if (wanted) {
+        const int pg = p.a.page_table[(int64_t)c.b * p.a.ld_pt + blk / p.v.bpp];
+        if (pg >= 0 && pg < p.v.n_pages)
+          src = p.v.pool + (((int64_t)pg * p.v.n_kv_heads + c.h) * p.v.bpp + blk % p.v.bpp) * BB;
+        else
+          atomicOr(p.v.status, kStatusBadIndex);
+      }
+      const unsigned copies = __popc(__ballot_sync(0xffffffffu, src != nullptr));
+      if (issued >= p.NS && !mbar_wait_bounded(empty + st, phase ^ 1u, p.wait_ns)) bad = true;
+      if (__any_sync(0xffffffffu, bad)) {
+        if (lane == 0) atomicOr(p.v.status, kStatusTimeoutPipe);
+        break;
+      }
+      if (lane == 0) mbar_arrive_expect_tx(full + st, copies * BB);
+      __syncwarp();
+      if (src) bulk_g2s_shared_u32(stages_at + st * p.stage_bytes + lane * BB, src, BB, full + st);
+      ++issued;
+      if (++st == p.NS) st = 0, phase ^= 1u;
+      if (++c.tile == c.s.tiles && u + 1 < u1) next_item(p, c);
+    }
+    // the copies in flight land before the CTA's shared memory is given back
+    const int last = (int)min(issued, (int64_t)p.NS);
+    for (int i = 0; i < last; ++i) {
+      if (st == 0) st = p.NS, phase ^= 1u;
+      --st;
+      mbar_wait_bounded(full + st, phase, p.wait_ns);
+    }
+    return;
+  }
+
+  // ---------------------------------------------------------------- consumers
+  const int g = lane >> 2, t = lane & 3;
+  const int kA = kpi(g), vA = kpi(2 * t), vB = kpi(2 * t + 1);
+  const uint32_t c_lo = 0xBD80BD80u;  // -8 * 2^-7
+  const uint32_t c_hi = 0xBF80BF80u;  // -8 * 2^-3
+  int st = 0;
+  unsigned phase = 0;
+  bool bad = false;
+
+  for (int64_t u = u0; u < u1;) {
+    const int64_t len = min((int64_t)(c.s.tiles - c.tile), u1 - u);
+    const KvSeq s = c.s;
+    const int rows = s.n * p.v.group;
+
+    // the rows as B fragments, and their sums
+    uint32_t qf[NT][D / 16][2];
+    float qs[NT][2];
+    int hi[NT][2];  // last visible key of this lane's columns 2 t, 2 t + 1
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = nt * 8 + g;
+      uint4 w[KW];
+#pragma unroll
+      for (int i = 0; i < KW; ++i) w[i] = make_uint4(0, 0, 0, 0);
+      if (r < rows) {
+        const __nv_bfloat16* src = p.a.q + (int64_t)(s.row + r / p.v.group) * p.a.ld_q +
+                                   (int64_t)(c.h * p.v.group + r % p.v.group) * D + t * (D / 4);
+#pragma unroll
+        for (int i = 0; i < KW; ++i) w[i] = reinterpret_cast<const uint4*>(src)[i];
+      }
+      float x = 0.f;
+#pragma unroll
+      for (int i = 0; i < KW; ++i) {
+        const uint32_t e[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x += __uint_as_float(e[k] << 16) + __uint_as_float(e[k] & 0xFFFF0000u);
+        qf[nt][2 * i][0] = prmt(e[0], e[2], 0x5410);
+        qf[nt][2 * i][1] = prmt(e[0], e[2], 0x7632);
+        qf[nt][2 * i + 1][0] = prmt(e[1], e[3], 0x5410);
+        qf[nt][2 * i + 1][1] = prmt(e[1], e[3], 0x7632);
+      }
+      x += __shfl_xor_sync(0xffffffffu, x, 1);
+      x += __shfl_xor_sync(0xffffffffu, x, 2);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        qs[nt][k] = __shfl_sync(0xffffffffu, x, (2 * t + k) * 4);
+        hi[nt][k] = s.L - s.n + min((nt * 8 + 2 * t + k) / p.v.group, s.n - 1);
+      }
+    }
+    float acc[D / 16][NT][4];
+    float m[NT][2], l[NT][2], off[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[j][nt][e] = 0.f;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) m[nt][k] = -INFINITY, l[nt][k] = 0.f, off[nt][k] = 0.f;
+    }
+
+    for (int64_t i = 0; i < len; ++i) {
+      const int key0 = (s.lo + c.tile + (int)i) * kTile + warp * 32;
+      if (!bad && !mbar_wait_bounded(full + st, phase, p.wait_ns)) {
+        bad = true;
+        if (lane == 0) atomicOr(p.v.status, kStatusTimeoutPipe);
+      }
+      bad = __any_sync(0xffffffffu, bad);
+      const uint32_t base = stages_at + st * p.stage_bytes + warp * 2 * BB;
+      if (!bad && key0 < s.L) {
+        float sc[2][NT][4];
+        // ---- scores
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) {
+          const uint32_t blk = base + mt * BB;
+          uint32_t wa[KW], wb[KW];
+          lds_words(blk + kA * (D / 2) + t * (D / 8), wa);
+          lds_words(blk + (8 + kA) * (D / 2) + t * (D / 8), wb);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sc[mt][nt][e] = -128.f * qs[nt][e & 1];
+#pragma unroll
+          for (int j = 0; j < D / 16; ++j) {
+            const int sh = (j & 1) * 8;
+            const uint32_t a[4] = {int4_pair_to_bf16x2_biased(wa[j / 2] >> sh), int4_pair_to_bf16x2_biased(wb[j / 2] >> sh),
+                                   int4_pair_to_bf16x2_biased(wa[j / 2] >> (sh + 4)),
+                                   int4_pair_to_bf16x2_biased(wb[j / 2] >> (sh + 4))};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma_bf16_16816(sc[mt][nt], a, qf[nt][j][0], qf[nt][j][1]);
+          }
+          const uint32_t pa = lds32(blk + 16 * D + 4 * kA), pb = lds32(blk + 16 * D + 4 * (8 + kA));
+          const float s0 = __uint_as_float(pa << 16) * p.a.scale_log2, o0 = __uint_as_float(pa & 0xFFFF0000u) * p.a.scale_log2;
+          const float s1 = __uint_as_float(pb << 16) * p.a.scale_log2, o1 = __uint_as_float(pb & 0xFFFF0000u) * p.a.scale_log2;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            sc[mt][nt][0] = fmaf(s0, sc[mt][nt][0], o0 * qs[nt][0]);
+            sc[mt][nt][1] = fmaf(s0, sc[mt][nt][1], o0 * qs[nt][1]);
+            sc[mt][nt][2] = fmaf(s1, sc[mt][nt][2], o1 * qs[nt][0]);
+            sc[mt][nt][3] = fmaf(s1, sc[mt][nt][3], o1 * qs[nt][1]);
+          }
+        }
+        // ---- mask, where some row does not see all 32 keys
+        const bool masked = key0 + 31 > s.L - s.n || (p.a.window > 0 && key0 <= s.L - 1 - p.a.window);
+        bool see[2][NT][4];
+        if (masked) {
+#pragma unroll
+          for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int key = key0 + mt * 16 + kA + 8 * (e >> 1), last = hi[nt][e & 1];
+                see[mt][nt][e] = key <= last && (p.a.window == 0 || key > last - p.a.window);
+                if (!see[mt][nt][e]) sc[mt][nt][e] = -INFINITY;
+              }
+        }
+        // ---- running maximum
+        bool over = false;
+        float top[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            top[nt][k] = fmaxf(fmaxf(sc[0][nt][k], sc[0][nt][k + 2]), fmaxf(sc[1][nt][k], sc[1][nt][k + 2]));
+            over |= top[nt][k] > m[nt][k] + kLazy;
+          }
+        if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              float x = top[nt][k];
+#pragma unroll
+              for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+              const float mn = fmaxf(m[nt][k], x);
+              const float f = m[nt][k] == -INFINITY ? 0.f : ex2(m[nt][k] - mn);
+              m[nt][k] = mn;
+              l[nt][k] *= f;
+              off[nt][k] *= f;
+#pragma unroll
+              for (int j = 0; j < D / 16; ++j) acc[j][nt][k] *= f, acc[j][nt][k + 2] *= f;
+            }
+        }
+        // ---- weights, and the values
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) {
+          const uint32_t blk = base + mt * BB;
+          const uint32_t pa = lds32(blk + 16 * D + 64 + 4 * kA), pb = lds32(blk + 16 * D + 64 + 4 * (8 + kA));
+          const float vs[2] = {__uint_as_float(pa << 16), __uint_as_float(pb << 16)};
+          const float vo[2] = {fmaf(8.f, vs[0], __uint_as_float(pa & 0xFFFF0000u)),
+                               fmaf(8.f, vs[1], __uint_as_float(pb & 0xFFFF0000u))};
+          uint32_t bf[NT][2];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int k = e & 1, y = e >> 1;
+              const float pe = ex2(sc[mt][nt][e] - (m[nt][k] == -INFINITY ? 0.f : m[nt][k]));
+              l[nt][k] += pe;
+              w[e] = pe * vs[y];
+              float o = pe * vo[y];
+              if (masked && !see[mt][nt][e]) w[e] = 0.f, o = 0.f;  // 0 x NaN of a key that the row does not see
+              off[nt][k] += o;
+            }
+            bf[nt][0] = movmatrix(pack_bf16x2(w[0], w[1]));
+            bf[nt][1] = movmatrix(pack_bf16x2(w[2], w[3]));
+          }
+          uint32_t va[VW], vb[VW], vc[VW], vd[VW];
+          const uint32_t vrow = blk + 8 * D + g * (D / 16);
+          lds_words(vrow + vA * (D / 2), va);
+          lds_words(vrow + vB * (D / 2), vb);
+          lds_words(vrow + (8 + vA) * (D / 2), vc);
+          lds_words(vrow + (8 + vB) * (D / 2), vd);
+#pragma unroll
+          for (int i2 = 0; i2 < VW; ++i2) {
+            uint32_t f0[4], f1[4], f2[4], f3[4];
+            decode_frag_unpack(prmt(va[i2], vb[i2], 0x5410), c_lo, c_hi, f0);
+            decode_frag_unpack(prmt(va[i2], vb[i2], 0x7632), c_lo, c_hi, f1);
+            decode_frag_unpack(prmt(vc[i2], vd[i2], 0x5410), c_lo, c_hi, f2);
+            decode_frag_unpack(prmt(vc[i2], vd[i2], 0x7632), c_lo, c_hi, f3);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t a[4] = {f0[j], f1[j], f2[j], f3[j]};
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) mma_bf16_16816(acc[i2 * 4 + j][nt], a, bf[nt][0], bf[nt][1]);
+            }
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty + st);
+      if (++st == p.NS) st = 0, phase ^= 1u;
+    }
+
+    // ---- join the four warps' states
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) {
+          l[nt][k] += __shfl_xor_sync(0xffffffffu, l[nt][k], o);
+          off[nt][k] += __shfl_xor_sync(0xffffffffu, off[nt][k], o);
+        }
+        const int r = nt * 8 + 2 * t + k;
+        if (g == 0) {
+          ml[(warp * R + r) * 2] = m[nt][k];
+          ml[(warp * R + r) * 2 + 1] = l[nt][k];
+        }
+        float* dst = om + (warp * R + r) * OS + g * (D / 8);
+#pragma unroll
+        for (int i2 = 0; i2 < VW; ++i2)
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            float4 o4;
+            o4.x = fmaf(acc[i2 * 4][nt][k + 2 * y], kFragScaleLo, off[nt][k]);
+            o4.y = fmaf(acc[i2 * 4 + 1][nt][k + 2 * y], kFragScaleHi, off[nt][k]);
+            o4.z = fmaf(acc[i2 * 4 + 2][nt][k + 2 * y], kFragScaleLo, off[nt][k]);
+            o4.w = fmaf(acc[i2 * 4 + 3][nt][k + 2 * y], kFragScaleHi, off[nt][k]);
+            *reinterpret_cast<float4*>(dst + i2 * 8 + y * 4) = o4;
+          }
+      }
+    consumer_sync();
+    const bool whole = c.tile == 0 && len == s.tiles;
+    const int64_t first_unit = u - c.tile;
+    // a segment that starts its item in this CTA and one that goes on with an earlier CTA's have a slot each
+    float* slot = p.part + (cta * 2 + (c.tile == 0 ? 1 : 0)) * kPart;
+    auto write_row = [&](int r, const float (&o)[E], float inv) {
+      if (r >= rows) return;
+      __nv_bfloat16* dst = p.a.out + (int64_t)(s.row + r / p.v.group) * p.a.ld_out +
+                           (int64_t)(c.h * p.v.group + r % p.v.group) * D + lane * E;
+      uint32_t w[E / 2];
+#pragma unroll
+      for (int e = 0; e < E; e += 2) w[e / 2] = pack_bf16x2(o[e] * inv, o[e + 1] * inv);
+      if constexpr (E == 4)
+        *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+      else
+        *reinterpret_cast<uint32_t*>(dst) = w[0];
+    };
+    for (int r = warp; r < R; r += kWarps) {
+      float M = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, ml[(w * R + r) * 2]);
+      float L = 0.f, o[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float mw = ml[(w * R + r) * 2];
+        const float f = mw == -INFINITY ? (ml[(w * R + r) * 2 + 1] == 0.f ? 0.f : 1.f) : ex2(mw - M);
+        L = fmaf(f, ml[(w * R + r) * 2 + 1], L);
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = fmaf(f, om[(w * R + r) * OS + lane * E + e], o[e]);
+      }
+      if (whole) {
+        write_row(r, o, L == 0.f ? 0.f : 1.f / L);
+      } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e) slot[r * D + lane * E + e] = o[e];
+        if (lane == 0) slot[R * D + 2 * r] = M, slot[R * D + 2 * r + 1] = L;
+      }
+    }
+    if (!whole) {
+      // CTAs ca .. cb hold the item's units
+      const int64_t ca = ((first_unit + 1) * G - 1) / U, cb = ((first_unit + s.tiles) * G - 1) / U;
+      __threadfence();
+      consumer_sync();
+      if (tid == 0) found[1] = atomicAdd(p.counters + ca, 1u) == (unsigned)(cb - ca);
+      consumer_sync();
+      if (found[1]) {
+        __threadfence();
+        if (tid == 0) p.counters[ca] = 0;
+        for (int r = warp; r < R; r += kWarps) {
+          float M = -INFINITY;
+          for (int64_t x = ca + lane; x <= cb; x += 32)
+            M = fmaxf(M, __ldcg(p.part + (x * 2 + (x == ca)) * kPart + R * D + 2 * r));
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+          float L = 0.f, o[E];
+#pragma unroll
+          for (int e = 0; e < E; ++e) o[e] = 0.f;
+#pragma unroll 4
+          for (int64_t x = ca; x <= cb; ++x) {
+            const float* q = p.part + (x * 2 + (x == ca)) * kPart;
+            const float mx = __ldcg(q + R * D + 2 * r), lx = __ldcg(q + R * D + 2 * r + 1);
+            const float f = mx == -INFINITY ? (lx == 0.f ? 0.f : 1.f) : ex2(mx - M);
+            L = fmaf(f, lx, L);
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[e] = fmaf(f, __ldcg(q + r * D + lane * E + e), o[e]);
+          }
+          write_row(r, o, L == 0.f ? 0.f : 1.f / L);
+        }
+      }
+    }
+    consumer_sync();  // the joined results have been read
+    u += len;
+    c.tile += (int)len;
+    if (u < u1) next_item(p, c);
+  }
+}
+
+template <int D, int NT>
+spear_status_t launch(const spear_kv_s* h, DecodeParams& p, cudaStream_t stream) {
+  static std::atomic<uint64_t> done{0};
+  if (smem_limit_once(reinterpret_cast<const void*>(decode_kernel<D, NT>), done) != cudaSuccess) return SPEAR_ERR_CUDA;
+  constexpr int kPerSm = 4 / NT > 3 ? 3 : 4 / NT;
+  constexpr uint32_t om = ((kWarps * 8 * NT * (2 + D + 4)) * 4 + 127) / 128 * 128;
+  constexpr uint32_t stage = kBlocksPerTile * 16 * (D + 8);
+  constexpr int kRoom = (227 * 1024 / kPerSm - 1024 - 512 - (int)om) / (int)stage;
+  p.stage_bytes = stage;
+  p.NS = kRoom < kMaxStages ? kRoom : kMaxStages;
+  static_assert(kRoom >= 2, "two stages at least");
+  const size_t smem = 512 + om + (size_t)p.NS * stage;
+  decode_kernel<D, NT><<<h->sm_count * kPerSm, kThreads, smem, stream>>>(p);
+  return cudaGetLastError() == cudaSuccess ? SPEAR_OK : SPEAR_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace spear
+
+using namespace spear;
+
+// CTAs x rows is at most sm_count x 32 for every variant
+size_t kv_decode_workspace(const spear_kv_s* h) {
+  return (size_t)h->sm_count * 2 * 32 * (h->view.D + 2) * sizeof(float);
+}
+
+spear_status_t kv_launch_decode(const spear_kv_s* h, const KvAttnArgs& a, int nt, float* part, unsigned* counters,
+                                cudaStream_t stream) {
+  DecodeParams p;
+  p.v = h->view;
+  p.a = a;
+  p.max_rows = 8 * nt;
+  p.part = part;
+  p.counters = counters;
+  p.wait_ns = 100000000ull;
+  const bool wide = h->view.D == 128;
+  switch (nt) {
+    case 1: return wide ? launch<128, 1>(h, p, stream) : launch<64, 1>(h, p, stream);
+    case 2: return wide ? launch<128, 2>(h, p, stream) : launch<64, 2>(h, p, stream);
+    default: return wide ? launch<128, 4>(h, p, stream) : launch<64, 4>(h, p, stream);
+  }
+}
