@@ -47,5 +47,9 @@ constexpr int kKvDecodeRows = 32;      // most rows of a key/value head that the
 spear_status_t kv_launch_decode(const spear_kv_s* h, const KvAttnArgs& a, int nt, float* part, unsigned* counters,
                                 cudaStream_t stream);
 size_t kv_decode_workspace(const spear_kv_s* h);
+// The tensor-core kernel for the sequences with more than max_rows rows a key/value head.
+spear_status_t kv_launch_prefill(const spear_kv_s* h, const KvAttnArgs& a, int max_rows, float* part,
+                                 unsigned* counters, cudaStream_t stream);
+size_t kv_prefill_workspace(const spear_kv_s* h);
 size_t kv_attention_workspace(const spear_kv_s* h);
 spear_status_t kv_launch_attention(spear_kv_s* h, const KvAttnArgs& a, cudaStream_t stream);

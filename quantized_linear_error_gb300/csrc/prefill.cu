@@ -182,15 +182,6 @@ SPEAR_DEVINL void bulk_commit_wait_all() {
   asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
-// 32 lanes x 32-bit, 16 consecutive columns per thread, registers -> TMEM.
-SPEAR_DEVINL void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
-}
-
 // One half of a K block's A operand for row r: channels 32 h .. 32 h + 31
 // of the block as 16 bf16 pairs (TMEM columns 16 h .. 16 h + 15 of the
 // stage's A slot), from the stage's raw input (words 4 h .. 4 h + 3 of the
@@ -222,31 +213,11 @@ SPEAR_DEVINL void tail_half(const __nv_bfloat16* bt, int rank, int row, int t, i
   }
 }
 
-// 32 lanes x 32-bit, 32 consecutive columns per thread.
-SPEAR_DEVINL void tmem_ld_x32(uint32_t taddr, uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr));
-}
-
 // Named barrier of the 4 epilogue warps; bar.sync counts whole warps, so a
 // warp split by a single-thread branch reconverges first.
 SPEAR_DEVINL void epilogue_bar() {
   __syncwarp();
   asm volatile("bar.sync 1, 128;" ::: "memory");
-}
-
-// A bounded wait whose outcome is the same for the whole warp (the tensor
-// memory loads and stores that follow are warp-collective).
-SPEAR_DEVINL bool warp_wait(uint64_t* bar, unsigned parity, uint64_t limit_ns, uint32_t hint_ns) {
-  const bool ok =
-      hint_ns ? mbar_wait_bounded_hint(bar, parity, limit_ns, hint_ns) : mbar_wait_bounded(bar, parity, limit_ns);
-  return __all_sync(0xffffffffu, ok);
 }
 
 // Non-blocking test of an mbarrier phase (the producer's stage is usually
