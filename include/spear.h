@@ -358,7 +358,8 @@ spear_status_t spear_sched_destroy(spear_sched_t s);
  *   offset = bf16_RNE(min x),  inv = scale > 0 ? fl32(1 / scale) : 0,
  *   code = clamp(rint((x - offset) * inv), 0, 15),
  * each operation in fp32, round to nearest even. A row with an element that
- * is not finite, or whose range is not, is held with scale = offset = NaN.
+ * is not finite, or whose range is above 2^120, is held with scale = offset =
+ * NaN.
  *
  * Rotation (rope_dim R > 0): element pairs (i, i + R / 2), or (2i, 2i + 1) if
  * rope_interleaved, i < R / 2, of the row at position p become

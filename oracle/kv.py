@@ -50,7 +50,7 @@ def quantise(x: np.ndarray):
         inv = np.where(s > 0, F32(1) / np.where(s > 0, s, F32(1)), F32(0)).astype(F32)
         code = np.rint((x - o) * inv)
         code = np.where(np.isnan(code), 0, np.clip(code, 0, 15)).astype(np.uint8)
-        bad = ~np.isfinite(x).all(-1, keepdims=True) | ~np.isfinite(rng)
+        bad = ~np.isfinite(x).all(-1, keepdims=True) | ~(rng <= F32(2.0 ** 120))
     par = np.concatenate([sb, ob], -1)
     return code, np.where(bad, np.uint16(0x7FC0), par)
 

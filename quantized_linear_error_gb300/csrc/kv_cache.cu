@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
       codes |= (uint32_t)f << (4 * i);
     }
     uint32_t par = (uint32_t)__bfloat16_as_ushort(sb) | ((uint32_t)__bfloat16_as_ushort(ob) << 16);
-    if (!(sum == 0.f) || !(range <= 3.402823466e38f)) par = 0x7FC07FC0u;
+    if (!(sum == 0.f) || !(range <= 0x1p120f)) par = 0x7FC07FC0u;
     if (block && !bad) {
       uint8_t* b = block + (int64_t)head * p.v.bpp * p.v.block_bytes;
       *reinterpret_cast<uint32_t*>(b + (kind - 1) * 8 * D + row_in_block * (D / 2) + sub * 4) = codes;
@@ -330,7 +330,8 @@ spear_status_t spear_kv_attention(spear_kv_t h, const void* q, int64_t ld_q, voi
   if (n_seqs == 0 || T == 0) return SPEAR_OK;
   const int64_t qn = (int64_t)h->view.n_heads * h->view.D;
   if (!row_ok(q, ld_q, qn) || !row_ok(out, ld_out, qn) || !page_table || ld_pt < 1 || !kv_lens || !q_starts ||
-      max_q < 1 || window < 0 || !isfinite(scale))
+      max_q < 1 || window < 0 || !isfinite(scale) ||
+      (int64_t)T * h->view.group > 0x7FFF0000)
     return SPEAR_ERR_INVALID_ARG;
   // out is q itself or lies apart from it
   const char *qb = static_cast<const char*>(q), *ob = static_cast<const char*>(out);
@@ -349,7 +350,7 @@ spear_status_t spear_kv_attention(spear_kv_t h, const void* q, int64_t ld_q, voi
   a.T = T;
   a.max_q = max_q;
   a.scale_log2 = scale * 1.44269504088896340736f;
-  a.window = window;
+  a.window = window > kKvMaxTokens ? 0 : window;  // no sequence is longer
   return kv_launch_attention(h, a, stream);
 }
 

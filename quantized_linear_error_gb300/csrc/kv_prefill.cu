@@ -44,6 +44,7 @@ constexpr int kThreads = 512;
 constexpr int kTile = 128;            // keys of a unit
 constexpr int kRows = 256;            // rows of an item
 constexpr int kBlocksPerTile = kTile / 16;
+constexpr int kItemCost = 4;          // units
 constexpr int kHeader = 1024;         // barriers and the start position
 constexpr float kLazy = 8.f;
 constexpr uint32_t kHintNs = 100;
@@ -59,63 +60,92 @@ struct PrefillParams {
 
 struct Header {
   uint64_t raw_full[2], raw_empty[2], k_full[2], k_empty[2], v_full[2], v_empty[2];
-  uint64_t q_full[2], s_full[2], p_full[2], o_full[2], done;
+  uint64_t q_full[2], s_full[2], p_full[2][2], o_full[2], turn[2], done[2];  // p_full: [64 keys][half]
   uint32_t tmem;
-  int start_b, start_h, start_qt, start_tile;
+  int start_b, start_h, start_qt, start_off;
   int last[2];
   int64_t units;
 };
 static_assert(sizeof(Header) <= kHeader, "");
 
-// Row tile qt of a sequence: its key tiles.
+// Row tile qt of a sequence: its key tiles. (Rows of a key/value head, query
+// rows x group, fit 32 bits: the launch checks T x group.)
 struct Item {
   int lo, tiles;
   int rows;  // rows of this tile, <= 256
 };
 
 SPEAR_DEVINL int row_tiles(const PrefillParams& p, const KvSeq& s) {
-  const int64_t rows = (int64_t)s.n * p.v.group;
-  return rows > p.max_rows ? (int)((rows + kRows - 1) / kRows) : 0;
+  const int rows = s.n * p.v.group;
+  return rows > p.max_rows ? (rows + kRows - 1) / kRows : 0;
 }
 
 SPEAR_DEVINL Item item_of(const PrefillParams& p, const KvSeq& s, int qt) {
   Item it;
-  const int64_t rows = (int64_t)s.n * p.v.group, r0 = (int64_t)qt * kRows;
-  it.rows = (int)min((int64_t)kRows, rows - r0);
-  const int t0 = (int)(r0 / p.v.group), t1 = (int)((r0 + it.rows - 1) / p.v.group);
+  const int r0 = qt * kRows;
+  it.rows = min(kRows, s.n * p.v.group - r0);
+  const int t0 = r0 / p.v.group, t1 = (r0 + it.rows - 1) / p.v.group;
   const int last = s.L - s.n + t1;
-  const int64_t first = p.a.window > 0 ? (int64_t)s.L - s.n + t0 - p.a.window + 1 : 0;
-  it.lo = first > 0 ? (int)(first / kTile) : 0;
+  const int first = p.a.window > 0 ? s.L - s.n + t0 - p.a.window + 1 : 0;
+  it.lo = first > 0 ? first / kTile : 0;
   it.tiles = max(1, (last >= 0 ? last / kTile + 1 : 0) - it.lo);
   return it;
 }
 
+// A position in the list of units: unit `off` of an item, of which the first
+// kItemCost stand for the work that an item costs beside its tiles.
 struct Cursor {
-  int b, h, qt, nqt, tile;
+  int b, h, qt, nqt, off;
   KvSeq s;
   Item it;
+  int64_t u;
 };
 
-SPEAR_DEVINL void next_item(const PrefillParams& p, Cursor& c) {
-  c.tile = 0;
-  if (++c.qt == c.nqt) {
-    c.qt = 0;
-    if (++c.h == p.v.n_kv_heads) {
-      c.h = 0;
-      do {
-        ++c.b;
-        c.s = kv_seq(p.v, p.a, c.b, kTile);
-        c.nqt = row_tiles(p, c.s);
-      } while (c.nqt == 0);
+// A CTA's share of an item: key tiles [t0, t1) of its it.tiles.
+struct Segment {
+  KvSeq s;
+  Item it;
+  int b, h, qt;
+  int t0, t1;
+  int64_t unit0;  // the unit of tile 0
+};
+
+SPEAR_DEVINL bool next_segment(const PrefillParams& p, Cursor& c, int64_t u1, Segment& g) {
+  while (c.u < u1) {
+    const int end = (int)min((int64_t)kItemCost + c.it.tiles, c.off + (u1 - c.u));
+    g.s = c.s;
+    g.it = c.it;
+    g.b = c.b;
+    g.h = c.h;
+    g.qt = c.qt;
+    g.t0 = max(0, c.off - kItemCost);
+    g.t1 = max(0, end - kItemCost);
+    g.unit0 = c.u - c.off + kItemCost;
+    c.u += end - c.off;
+    c.off = 0;
+    if (c.u < u1) {
+      if (++c.qt == c.nqt) {
+        c.qt = 0;
+        if (++c.h == p.v.n_kv_heads) {
+          c.h = 0;
+          do {
+            ++c.b;
+            c.s = kv_seq(p.v, p.a, c.b, kTile);
+            c.nqt = row_tiles(p, c.s);
+          } while (c.nqt == 0);
+        }
+      }
+      c.it = item_of(p, c.s, c.qt);
     }
+    if (g.t1 > g.t0) return true;
   }
-  c.it = item_of(p, c.s, c.qt);
+  return false;
 }
 
 // Units of one head of a sequence, the whole warp at it.
 SPEAR_DEVINL int64_t head_units(const PrefillParams& p, const KvSeq& s, int nqt, int lane) {
   int64_t x = 0;
-  for (int qt = lane; qt < nqt; qt += 32) x += item_of(p, s, qt).tiles;
+  for (int qt = lane; qt < nqt; qt += 32) x += kItemCost + item_of(p, s, qt).tiles;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
   return x;
@@ -138,13 +168,16 @@ SPEAR_DEVINL void each_sequence(const PrefillParams& p, int lane, F f) {
 
 SPEAR_DEVINL void wg_sync(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
 
-// Eight codes of a word as four bf16 pairs, elements (0, 4), (1, 5), (2, 6), (3, 7).
-SPEAR_DEVINL uint4 dequant8(uint32_t w, uint32_t ss, uint32_t oo) {
-  uint32_t r[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    r[i] = bf16x2_fma(bf16x2_sub(int4_pair_to_bf16x2_biased(w >> (4 * i)), 0x43004300u), ss, oo);
-  return make_uint4(r[0], r[1], r[2], r[3]);
+// Eight codes of a word as four bf16 pairs, elements (0, 4), (1, 5), (2, 6), (3, 7): code * scale + offset, rounded
+// once. A masked nibble pair reads as tiny bf16 values (see decode_frag_unpack), which one exact multiplication
+// brings to c 2^-7 or c 2^-3; s_lo = scale 2^7, s_hi = scale 2^3.
+SPEAR_DEVINL uint4 dequant8(uint32_t w, uint32_t s_lo, uint32_t s_hi, uint32_t oo) {
+  const uint32_t u = w >> 8;
+  constexpr uint32_t k2p126 = 0x7E807E80u, k0 = 0x80008000u;  // x 2^126 - 0: c 2^-7 and (high nibbles) c 2^-3, exact
+  return make_uint4(bf16x2_fma(bf16x2_fma(w & 0x000F000Fu, k2p126, k0), s_lo, oo),
+                    bf16x2_fma(bf16x2_fma(w & 0x00F000F0u, k2p126, k0), s_hi, oo),
+                    bf16x2_fma(bf16x2_fma(u & 0x000F000Fu, k2p126, k0), s_lo, oo),
+                    bf16x2_fma(bf16x2_fma(u & 0x00F000F0u, k2p126, k0), s_hi, oo));
 }
 
 SPEAR_DEVINL void sts128(uint32_t addr, const uint4& v) {
@@ -155,23 +188,20 @@ SPEAR_DEVINL void sts128(uint32_t addr, const uint4& v) {
 // One key's row: codes (D / 2 bytes at `src`) to row `key` of a swizzled tile.
 template <int D>
 SPEAR_DEVINL void dequant_row(uint32_t src, uint32_t tile, int key, uint32_t par) {
-  const uint32_t ss = __byte_perm(par, par, 0x1010), oo = __byte_perm(par, par, 0x3232);
+  const float sc = __uint_as_float(par << 16);
+  const uint32_t s_lo = pack_bf16x2(sc * 128.f, sc * 128.f), s_hi = pack_bf16x2(sc * 8.f, sc * 8.f);
+  const uint32_t oo = __byte_perm(par, par, 0x3232);
   constexpr int Q = D / 32;  // 16-byte quarters of the packed row
-  uint4 w[Q];
-  int q[Q];
-#pragma unroll
+#pragma unroll 1
   for (int i = 0; i < Q; ++i) {
     // quarters in an order of the key's own: a quarter warp then meets every bank once
-    q[i] = Q == 4 ? (i + (key >> 1)) & 3 : i;
-    w[i] = lds128(src + q[i] * 16);
-  }
-#pragma unroll
-  for (int i = 0; i < Q; ++i) {
-    const uint32_t words[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-    const uint32_t row = tile + (q[i] >> 1) * (kTile * 128) + key * 128;
+    const int q = Q == 4 ? (i + (key >> 1)) & 3 : i;
+    const uint4 w = lds128(src + q * 16);
+    const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+    const uint32_t row = tile + (q >> 1) * (kTile * 128) + key * 128;
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      sts128(row + ((((q[i] & 1) * 4 + j) ^ (key & 7)) * 16), dequant8(words[j], ss, oo));
+      sts128(row + ((((q & 1) * 4 + j) ^ (key & 7)) * 16), dequant8(words[j], s_lo, s_hi, oo));
   }
 }
 
@@ -191,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   Header& hd = *reinterpret_cast<Header*>(smem);
   const uint32_t q_at = smem_u32(smem) + kHeader;
   const uint32_t k_at = q_at + 2 * kTileBytes, v_at = k_at + 2 * kTileBytes, raw_at = v_at + 2 * kTileBytes;
-  const int tid = threadIdx.x, warp = tid / 32, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid / 32, 0), lane = tid & 31;
 
   if (tid == 0) {
 #pragma unroll
@@ -199,15 +229,17 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       mbar_init(&hd.raw_full[i], 1);
       mbar_init(&hd.raw_empty[i], 4);
       mbar_init(&hd.k_full[i], 4);
-      mbar_init(&hd.k_empty[i], 1);
+      mbar_init(&hd.k_empty[i], 2);
       mbar_init(&hd.v_full[i], 4);
-      mbar_init(&hd.v_empty[i], 1);
+      mbar_init(&hd.v_empty[i], 2);
       mbar_init(&hd.q_full[i], 4);
       mbar_init(&hd.s_full[i], 1);
-      mbar_init(&hd.p_full[i], 4);
+      mbar_init(&hd.p_full[0][i], 4);
+      mbar_init(&hd.p_full[1][i], 4);
+      mbar_init(&hd.turn[i], 1);
+      mbar_init(&hd.done[i], 1);
       mbar_init(&hd.o_full[i], 1);
     }
-    mbar_init(&hd.done, 1);
     fence_mbar_init();
   }
   if (warp == 12) {
@@ -234,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         int64_t rest = u0 - before - h * hu;
         for (int q0 = 0; q0 < nqt; q0 += 32) {
           const int qt = q0 + lane;
-          const int own = qt < nqt ? item_of(p, s, qt).tiles : 0;
+          const int own = qt < nqt ? kItemCost + item_of(p, s, qt).tiles : 0;
           int incl = own;
 #pragma unroll
           for (int o = 1; o < 32; o <<= 1) {
@@ -245,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
             hd.start_b = b;
             hd.start_h = h;
             hd.start_qt = qt;
-            hd.start_tile = (int)(rest - (incl - own));
+            hd.start_off = (int)(rest - (incl - own));
           }
           const int sum = __shfl_sync(0xffffffffu, incl, 31);
           if (rest < sum) break;
@@ -260,117 +292,140 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   __syncthreads();
   tc_fence_after_sync();
   const int64_t U = hd.units, G = min((int64_t)gridDim.x, U), cta = blockIdx.x;
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&hd.tmem);
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(&hd.tmem), 0);
   const int64_t u0 = cta < G ? cta * U / G : 0, u1 = cta < G ? (cta + 1) * U / G : 0;
   Cursor c{};
+  c.u = u0;
   if (u0 < u1) {
     c.b = hd.start_b;
     c.h = hd.start_h;
     c.qt = hd.start_qt;
-    c.tile = hd.start_tile;
+    c.off = hd.start_off;
     c.s = kv_seq(p.v, p.a, c.b, kTile);
     c.nqt = row_tiles(p, c.s);
     c.it = item_of(p, c.s, c.qt);
   }
 
+  Segment g;
   if (warp >= 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == 13) {
       // -------------------------------------------------------------- copies of the packed tiles
       int st = 0;
       unsigned ph = 0;
-      int64_t issued = 0;
-      for (int64_t u = u0; u < u1; ++u) {
-        const int blk = (c.it.lo + c.tile) * kBlocksPerTile + lane;
-        const uint8_t* src = nullptr;
-        if (lane < kBlocksPerTile && blk < (c.s.L + 15) / 16) {
-          const int pg = p.a.page_table[(int64_t)c.b * p.a.ld_pt + blk / p.v.bpp];
-          if (pg >= 0 && pg < p.v.n_pages)
-            src = p.v.pool + (((int64_t)pg * p.v.n_kv_heads + c.h) * p.v.bpp + blk % p.v.bpp) * BB;
-          else
-            atomicOr(p.v.status, kStatusBadIndex);
+      unsigned issued = 0;
+      bool ok = true;
+      while (ok && next_segment(p, c, u1, g)) {
+        for (int t = g.t0; t < g.t1; ++t) {
+          const int blk = (g.it.lo + t) * kBlocksPerTile + lane;
+          const uint8_t* src = nullptr;
+          if (lane < kBlocksPerTile && blk < (g.s.L + 15) / 16) {
+            const int pg = p.a.page_table[(int64_t)g.b * p.a.ld_pt + blk / p.v.bpp];
+            if (pg >= 0 && pg < p.v.n_pages)
+              src = p.v.pool + (((int64_t)pg * p.v.n_kv_heads + g.h) * p.v.bpp + blk % p.v.bpp) * BB;
+            else
+              atomicOr(p.v.status, kStatusBadIndex);
+          }
+          const unsigned copies = __popc(__ballot_sync(0xffffffffu, src != nullptr));
+          if (issued >= 2 && !warp_wait(&hd.raw_empty[st], ph ^ 1u, p.wait_ns, kHintNs)) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) mbar_arrive_expect_tx(&hd.raw_full[st], copies * BB);
+          __syncwarp();
+          if (src) bulk_g2s_shared_u32(raw_at + st * kRawBytes + lane * BB, src, BB, &hd.raw_full[st]);
+          ++issued;
+          if (++st == 2) st = 0, ph ^= 1u;
         }
-        const unsigned copies = __popc(__ballot_sync(0xffffffffu, src != nullptr));
-        if (issued >= 2 && !warp_wait(&hd.raw_empty[st], ph ^ 1u, p.wait_ns, kHintNs)) {
-          if (lane == 0) fail(p);
-          break;
-        }
-        if (lane == 0) mbar_arrive_expect_tx(&hd.raw_full[st], copies * BB);
-        __syncwarp();
-        if (src) bulk_g2s_shared_u32(raw_at + st * kRawBytes + lane * BB, src, BB, &hd.raw_full[st]);
-        ++issued;
-        if (++st == 2) st = 0, ph ^= 1u;
-        if (++c.tile == c.it.tiles && u + 1 < u1) next_item(p, c);
       }
-      for (int i = 0; i < (int)min(issued, (int64_t)2); ++i) {  // copies in flight land before the CTA ends
+      if (!ok && lane == 0) fail(p);
+      for (unsigned i = 0; i < min(issued, 2u); ++i) {  // copies in flight land before the CTA ends
         if (st == 0) st = 2, ph ^= 1u;
         --st;
         warp_wait(&hd.raw_full[st], ph, p.wait_ns, kHintNs);
       }
-    } else if (warp == 12 && lane == 0) {
-      // -------------------------------------------------------------- MMA issue
+    } else if (warp != 15) {
+      // -------------------------------------------------------------- MMA issue, one warp a half, uniform
+      const int i = warp == 14;
+      const uint32_t leader = elect_leader();
       const uint32_t idesc_s = idesc_bf16_f32(128, kTile);
       const uint32_t idesc_o = idesc_bf16_f32(128, D) | kIdescBMnMajor;
-      unsigned n_q[2] = {0, 0}, n_p[2] = {0, 0};
+      // a descriptor's address field counts 16 bytes and holds any shared-memory address: steps are added to it
+      const uint64_t q_desc = sw128_kmajor_desc(q_at + i * kTileBytes), k_desc = sw128_kmajor_desc(k_at);
+      const uint64_t v_desc = sw128_mnmajor_desc(v_at, kTile * 128);
+      const uint32_t s_d = tmem + 128 * i, o_d = tmem + 256 + 128 * i;
+      unsigned kc = 0, q_ph = 0, p_ph = 0;
       bool ok = true;
       auto wait = [&](uint64_t* bar, unsigned parity) {
-        if (ok && !mbar_wait_bounded_hint(bar, parity, p.wait_ns, kHintNs)) {
+        if (ok && !warp_wait(bar, parity, p.wait_ns, kHintNs)) {
           ok = false;
-          fail(p);
+          if (leader) fail(p);
         }
         return ok;
       };
-      auto scores = [&](int i, int64_t k, bool first) {  // S_i = Q_i K^T of the CTA's k-th tile
-        const int st = (int)(k & 1);
-        if (!wait(&hd.k_full[st], (unsigned)(k >> 1) & 1u)) return;
-        if (first && !wait(&hd.q_full[i], n_q[i]++ & 1u)) return;
-        tc_fence_after_sync();
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t at = (kk / 4) * (128 * 128) + (kk % 4) * 32;
-          umma_bf16(tmem + 128 * i, sw128_kmajor_desc(q_at + i * kTileBytes + at),
-                    sw128_kmajor_desc(k_at + st * kTileBytes + at), idesc_s, kk != 0);
-        }
-        umma_commit(&hd.s_full[i]);
+      // The halves take turns, "product of the last tile, scores of the next" each, so that one half's softmax
+      // runs beside the other's products; left alone they fall into step and wait for the tensor cores together.
+      unsigned turn_ph = i == 0 ? 1u : 0u;  // half 0's first turn needs no one's leave
+      auto take_turn = [&] {
+        const bool got = wait(&hd.turn[i], turn_ph);
+        turn_ph ^= 1u;
+        return got;
       };
-      int64_t k = 0;
-      int halves = c.it.rows > 128 ? 2 : 1;
-      for (int i = 0; i < halves && u0 < u1; ++i) scores(i, 0, true);
-      if (u0 < u1 && ok) umma_commit(&hd.k_empty[0]);
-      for (int64_t u = u0; u < u1 && ok; ++u, ++k) {
-        const bool first = u == u0 || c.tile == 0;
-        const bool last = c.tile + 1 == c.it.tiles || u + 1 == u1;
-        const int st = (int)(k & 1);
-        int next_halves = halves;
-        bool next_first = false;
-        if (u + 1 < u1 && ++c.tile == c.it.tiles) {
-          next_item(p, c);
-          next_halves = c.it.rows > 128 ? 2 : 1;
-          next_first = true;
-        }
-        for (int i = 0; i < 2 && ok; ++i) {
-          if (i < halves) {
-            if (!wait(&hd.p_full[i], n_p[i]++ & 1u)) break;
-            if (i == 0 && !wait(&hd.v_full[st], (unsigned)(k >> 1) & 1u)) break;
+      bool more = next_segment(p, c, u1, g);
+      if (more) take_turn();
+      while (more && ok) {
+        const int len = __shfl_sync(0xffffffffu, g.t1 - g.t0, 0);
+        const bool mine = __shfl_sync(0xffffffffu, g.it.rows, 0) > 128 * i;
+        more = next_segment(p, c, u1, g);
+        for (int k = 0; k < len; ++k, ++kc) {
+          const unsigned st = kc & 1u, ph = (kc >> 1) & 1u;
+          if (kc == 0 && !wait(&hd.k_full[0], 0)) break;
+          if (mine) {
+            if (k == 0) {
+              if (!wait(&hd.q_full[i], q_ph)) break;
+              q_ph ^= 1u;
+            }
             tc_fence_after_sync();
+            const uint64_t kd = k_desc + st * (kTileBytes >> 4);
 #pragma unroll
-            for (int kk = 0; kk < kTile / 16; ++kk)
-              umma_ts_bf16(tmem + 256 + 128 * i, tmem + 128 * i + 8 * kk,
-                           sw128_mnmajor_desc(v_at + st * kTileBytes + kk * 2048, kTile * 128), idesc_o,
-                           !(first && kk == 0));
-            if (last) umma_commit(&hd.o_full[i]);
-            if (i == halves - 1) umma_commit(&hd.v_empty[st]);
+            for (int kk = 0; kk < D / 16; ++kk) {
+              constexpr uint32_t kBlock = (128 * 128) >> 4;
+              umma_bf16(leader, s_d, q_desc + (kk / 4) * kBlock + (kk % 4) * 2, kd + (kk / 4) * kBlock + (kk % 4) * 2, idesc_s,
+                        kk != 0);
+            }
+            umma_commit(leader, &hd.s_full[i]);
+            umma_commit(leader, &hd.k_empty[st]);
+          } else {
+            if (leader) mbar_arrive(&hd.k_empty[st]);
           }
-          if (u + 1 < u1 && i < next_halves) {
-            scores(i, k + 1, next_first);
-            if (ok && i == next_halves - 1) umma_commit(&hd.k_empty[st ^ 1]);
+          if (leader) mbar_arrive(&hd.turn[i ^ 1]);
+          if (!wait(&hd.v_full[st], ph)) break;
+          if ((more || k + 1 < len) && !wait(&hd.k_full[st ^ 1u], ((kc + 1) >> 1) & 1u)) break;  // before the turn, not in it
+          if (mine && !wait(&hd.p_full[0][i], p_ph)) break;
+          if (!take_turn()) break;
+          if (mine) {
+            const uint64_t vd = v_desc + st * (kTileBytes >> 4);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {  // the first 64 keys' product runs while the others' weights are computed
+              if (x && !wait(&hd.p_full[1][i], p_ph)) break;
+              tc_fence_after_sync();
+#pragma unroll
+              for (int kk = 4 * x; kk < 4 * x + 4; ++kk)
+                umma_ts_bf16(leader, o_d, s_d + 8 * kk, vd + kk * (2048 >> 4), idesc_o, kk == 0 ? (k != 0) : 1u);
+            }
+            if (!ok) break;
+            p_ph ^= 1u;
+            if (k + 1 == len) umma_commit(leader, &hd.o_full[i]);
+            umma_commit(leader, &hd.v_empty[st]);
+          } else {
+            if (leader) mbar_arrive(&hd.v_empty[st]);
           }
         }
-        halves = next_halves;
       }
+      if (leader) mbar_arrive(&hd.turn[i ^ 1]);
       // nothing of this CTA's is still running on the tensor cores when the others go on to the end
-      umma_commit(&hd.done);
-      if (!mbar_wait_bounded(&hd.done, 0, p.wait_ns)) fail(p);
+      umma_commit(leader, &hd.done[i]);
+      if (!warp_wait(&hd.done[i], 0, p.wait_ns, 0) && leader) fail(p);
     }
   } else if (warp >= 8) {
     // ---------------------------------------------------------------- dequantisers
@@ -379,13 +434,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     const uint32_t blk_at = raw_at + (key / 16) * BB;
     const int r = key & 15;
     bool ok = true;
-    int64_t k = 0;
-    for (int64_t u = u0; u < u1; ++u, ++k) {
-      const int st = (int)(k & 1);
-      const unsigned ph = (unsigned)(k >> 1) & 1u;
+    unsigned k = 0;
+    while (next_segment(p, c, u1, g))
+     for (int t = g.t0; t < g.t1; ++t, ++k) {
+      const unsigned st = k & 1u, ph = (k >> 1) & 1u;
       const uint32_t blk = blk_at + st * kRawBytes;
       ok = ok && warp_wait(&hd.raw_full[st], ph, p.wait_ns, kHintNs);
-      const bool live = (c.it.lo + c.tile) * kTile + key < c.s.L;
+      const bool live = (g.it.lo + t) * kTile + key < g.s.L;
       uint32_t kp = 0, vp = 0;
       if (live) {
         kp = lds32(blk + 16 * D + 4 * r);
@@ -405,7 +460,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         mbar_arrive(&hd.v_full[st]);
         mbar_arrive(&hd.raw_empty[st]);
       }
-      if (++c.tile == c.it.tiles && u + 1 < u1) next_item(p, c);
     }
     if (!ok && lane == 0) fail(p);
   } else {
@@ -415,13 +469,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     const int row = 32 * quarter + lane;  // of the half
     const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
     const uint32_t s_t = tmem + lanes + 128 * i, o_t = tmem + lanes + 256 + 128 * i;
-    const float sl = fabsf(p.a.scale_log2);
+    const float sl = fmaxf(fabsf(p.a.scale_log2), 1e-30f);  // 0 x infinity of a masked score is a NaN
     const uint32_t flip = p.a.scale_log2 < 0.f ? 0x80008000u : 0u;
     unsigned n_s = 0, n_o = 0;
     bool ok = true;
 
     // this warp's 32 rows of an item into the Q tile: D / 8 lanes a row, 16 bytes each
-    auto load_q = [&](const Cursor& x) {
+    auto load_q = [&](const Segment& x) {
       constexpr int C = D / 8, RPI = 32 / C;
 #pragma unroll 4
       for (int r0 = 0; r0 < 32; r0 += RPI) {
@@ -429,9 +483,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         const int in_item = 128 * i + rr;
         uint4 w = make_uint4(0, 0, 0, 0);
         if (in_item < x.it.rows) {
-          const int64_t R = (int64_t)x.qt * kRows + in_item;
-          w = *reinterpret_cast<const uint4*>(p.a.q + (x.s.row + R / p.v.group) * p.a.ld_q +
-                                              (int64_t)(x.h * p.v.group + (int)(R % p.v.group)) * D + ch * 8);
+          const int R = x.qt * kRows + in_item, tok = R / p.v.group;
+          w = *reinterpret_cast<const uint4*>(p.a.q + (int64_t)(x.s.row + tok) * p.a.ld_q +
+                                              (int64_t)(x.h * p.v.group + R - tok * p.v.group) * D + ch * 8);
         }
         uint4 o;
         o.x = __byte_perm(w.x, w.z, 0x5410) ^ flip;
@@ -446,91 +500,111 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     };
 
     bool loaded = false;  // the item's Q rows are already in place
-    for (int64_t u = u0; u < u1;) {
-      const int64_t len = min((int64_t)(c.it.tiles - c.tile), u1 - u);
-      const bool mine = c.it.rows > 128 * i;  // a short item has no second half
-      Cursor nx;
+    bool more = next_segment(p, c, u1, g);
+    while (more) {
+      const bool mine = g.it.rows > 128 * i;  // a short item has no second half
+      const int len = g.t1 - g.t0;
+      Segment nx;
       if (mine) {
-        if (!loaded && ok) load_q(c);
+        if (!loaded && ok) load_q(g);
         loaded = false;
-        const int64_t R = (int64_t)c.qt * kRows + min(128 * i + row, c.it.rows - 1);
-        const int hi = c.s.L - c.s.n + (int)(R / p.v.group);  // last key that this row sees
+        const int r0 = g.qt * kRows + 128 * i, R = min(r0 + row, g.qt * kRows + g.it.rows - 1), tok = R / p.v.group;
+        const int hi = g.s.L - g.s.n + tok;  // last key that this row sees
         // keys that every row of the half sees
-        const int64_t ra = (int64_t)c.qt * kRows + 128 * i, rb = (int64_t)c.qt * kRows + min(128 * i + 127, c.it.rows - 1);
-        const int all_hi = c.s.L - c.s.n + (int)(ra / p.v.group);
-        const int all_lo = p.a.window > 0 ? c.s.L - c.s.n + (int)(rb / p.v.group) - p.a.window + 1 : 0;
+        const int all_hi = g.s.L - g.s.n + r0 / p.v.group;
+        const int all_lo = p.a.window > 0 ? g.s.L - g.s.n + min(r0 + 127, g.qt * kRows + g.it.rows - 1) / p.v.group -
+                                                p.a.window + 1 : 0;
         float m = -INFINITY, l = 0.f;
-        for (int64_t k = 0; k < len; ++k) {
-          const int key0 = (c.it.lo + c.tile + (int)k) * kTile;
+        for (int k = 0; k < len; ++k) {
+          const int key0 = (g.it.lo + g.t0 + k) * kTile;
           ok = ok && warp_wait(&hd.s_full[i], n_s & 1u, p.wait_ns, kHintNs);
           ++n_s;
           if (!ok) continue;
           tc_fence_after_sync();
-          uint32_t s[4][32];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) tmem_ld_x32(s_t + 32 * j, s[j]);
-          tmem_ld_wait();
-          const bool masked = key0 + kTile - 1 > all_hi || key0 < all_lo;
-          if (masked) {
+          if (key0 + kTile - 1 > all_hi || key0 < all_lo) {  // some row does not see every key: minus infinity there
             const int d = hi - key0, e = p.a.window > 0 ? d - p.a.window : -1;
+#pragma unroll 1
+            for (int j = 0; j < kTile; j += 32) {
+              uint32_t v[32];
+              tmem_ld_x32(s_t + j, v);
+              tmem_ld_wait();
 #pragma unroll
-            for (int j = 0; j < 128; ++j)
-              if (j > d || j <= e) s[j / 32][j % 32] = 0xFF800000u;
+              for (int x = 0; x < 32; ++x)
+                if (j + x > d || j + x <= e) v[x] = 0xFF800000u;
+              tmem_st_x32(s_t + j, v);
+            }
+            tmem_st_wait();
           }
+          uint32_t v[4][32];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) tmem_ld_x32(s_t + 32 * j, v[j]);
+          tmem_ld_wait();
+          // Weights of the first 64 keys by the present m, beside the maximum over all 128: m is nearly always kept
+          uint32_t w[32];
+          uint64_t sum2[2];
+          auto weights = [&](int y) {
+            const float ms = m == -INFINITY ? 0.f : -m * sl;
+            const uint64_t sl2 = pack_f32x2(sl, sl), ms2 = pack_f32x2(ms, ms);
+#pragma unroll
+            for (int x = 0; x < 64; x += 2) {
+              const uint32_t* q = &v[2 * y + x / 32][x % 32];
+              float pa, pb;
+              unpack_f32x2(fma_f32x2(pack_b32x2(q[0], q[1]), sl2, ms2), pa, pb);
+              pa = ex2(pa);
+              pb = ex2(pb);
+              sum2[(x >> 1) & 1] = x < 4 && y == 0 ? pack_f32x2(pa, pb) : add_f32x2(sum2[(x >> 1) & 1], pack_f32x2(pa, pb));
+              w[x / 2] = pack_bf16x2(pa, pb);
+            }
+          };
+          auto hand_over = [&](int y) {
+            tmem_st_x32(s_t + 32 * y, w);
+            tmem_st_wait();
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&hd.p_full[y][i]);
+          };
+          weights(0);
           float top[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            top[j] = __uint_as_float(s[j][0]);
+            top[j] = fmaxf(__uint_as_float(v[j][0]), __uint_as_float(v[j][1]));
 #pragma unroll
-            for (int x = 1; x < 32; ++x) top[j] = fmaxf(top[j], __uint_as_float(s[j][x]));
+            for (int x = 2; x < 32; x += 2)
+              top[j] = fmaxf(top[j], fmaxf(__uint_as_float(v[j][x]), __uint_as_float(v[j][x + 1])));
           }
           const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-          if (k == 0) {
-            m = mx;
-          } else if (__any_sync(0xffffffffu, m == -INFINITY ? mx > m : (mx - m) * sl > kLazy)) {
-            // the previous product has finished (s_full covers it), the next waits for this thread
+          if (k == 0 || __any_sync(0xffffffffu, m == -INFINITY ? mx > m : (mx - m) * sl > kLazy)) {
             const float mn = fmaxf(m, mx);
-            const float f = m == -INFINITY ? 0.f : ex2((m - mn) * sl);
-            m = mn;
-            l *= f;
-            for (int j = 0; j < D; j += 16) {
-              uint32_t o[16];
-              tmem_ld_x16(o_t + j, o);
-              tmem_ld_wait();
+            if (k > 0) {
+              // the previous product has finished (s_full covers it), the next waits for this thread
+              const float f = m == -INFINITY ? 0.f : ex2((m - mn) * sl);
+              l *= f;
+#pragma unroll 1
+              for (int j = 0; j < D; j += 16) {
+                uint32_t o[16];
+                tmem_ld_x16(o_t + j, o);
+                tmem_ld_wait();
 #pragma unroll
-              for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
-              tmem_st_x16(o_t + j, o);
-            }
-          }
-          const float ms = m == -INFINITY ? 0.f : -m * sl;
-          float sum[2] = {0.f, 0.f};
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            uint32_t w[32];
-#pragma unroll
-            for (int x = 0; x < 64; x += 2) {
-              const float a = __uint_as_float(s[2 * j + x / 32][x % 32]), b = __uint_as_float(s[2 * j + x / 32][x % 32 + 1]);
-              float pa = ex2(fmaf(a, sl, ms)), pb = ex2(fmaf(b, sl, ms));
-              if (masked) {  // scale 0 makes 0 x infinity of a masked score
-                pa = a == -INFINITY ? 0.f : pa;
-                pb = b == -INFINITY ? 0.f : pb;
+                for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
+                tmem_st_x16(o_t + j, o);
               }
-              sum[0] += pa;
-              sum[1] += pb;
-              w[x / 2] = pack_bf16x2(pa, pb);
             }
-            tmem_st_x32(s_t + 32 * j, w);
+            m = mn;
+            tmem_ld_x32(s_t, v[0]);
+            tmem_ld_x32(s_t + 32, v[1]);
+            tmem_ld_wait();
+            weights(0);
           }
-          l += sum[0] + sum[1];
-          tmem_st_wait();
-          tc_fence_before_sync();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&hd.p_full[i]);
+          hand_over(0);
+          weights(1);
+          hand_over(1);
+          float sa, sb;
+          unpack_f32x2(add_f32x2(sum2[0], sum2[1]), sa, sb);
+          l += sa + sb;
         }
-        nx = c;
-        if (u + len < u1) next_item(p, nx);
+        more = next_segment(p, c, u1, nx);
         // the half's scores are done with its Q tile: the next item's rows go in while the last product runs
-        if (u + len < u1 && nx.it.rows > 128 * i && ok) {
+        if (more && nx.it.rows > 128 * i && ok) {
           load_q(nx);
           loaded = true;
         }
@@ -538,10 +612,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         ok = ok && warp_wait(&hd.o_full[i], n_o & 1u, p.wait_ns, kHintNs);
         ++n_o;
         tc_fence_after_sync();
-        const bool whole = c.tile == 0 && len == c.it.tiles;
-        const bool real = 128 * i + row < c.it.rows;
-        __nv_bfloat16* dst = p.a.out + (c.s.row + R / p.v.group) * p.a.ld_out +
-                             (int64_t)(c.h * p.v.group + (int)(R % p.v.group)) * D;
+        const bool whole = len == g.it.tiles;
+        const bool real = 128 * i + row < g.it.rows;
+        __nv_bfloat16* dst = p.a.out + (int64_t)(g.s.row + tok) * p.a.ld_out +
+                             (int64_t)(g.h * p.v.group + R - tok * p.v.group) * D;
         auto write32 = [&](int col, const float (&v)[32], float inv) {
 #pragma unroll
           for (int g8 = 0; g8 < 4; ++g8) {
@@ -567,9 +641,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
             if (real && ok) write32(j, v, inv);
           }
         } else {
-          const int64_t first_unit = u - c.tile;
-          const int64_t ca = ((first_unit + 1) * G - 1) / U, cb = ((first_unit + c.it.tiles) * G - 1) / U;
-          float* slot = p.part + ((cta * 2 + (c.tile == 0 ? 1 : 0)) * 2 + i) * kPart + row;
+          const int64_t ca = ((g.unit0 + 1) * G - 1) / U, cb = ((g.unit0 + g.it.tiles) * G - 1) / U;
+          float* slot = p.part + ((cta * 2 + (g.t0 == 0 ? 1 : 0)) * 2 + i) * kPart + row;
 #pragma unroll
           for (int j = 0; j < D; j += 32) {
             uint32_t o[32];
@@ -616,11 +689,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         }
         tc_fence_before_sync();
       } else {
-        nx = c;
-        if (u + len < u1) next_item(p, nx);
+        more = next_segment(p, c, u1, nx);
       }
-      u += len;
-      c = nx;
+      g = nx;
     }
     if (!ok && lane == 0) fail(p);
   }
