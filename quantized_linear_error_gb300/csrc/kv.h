@@ -48,8 +48,8 @@ spear_status_t kv_launch_decode(const spear_kv_s* h, const KvAttnArgs& a, int nt
                                 cudaStream_t stream);
 size_t kv_decode_workspace(const spear_kv_s* h);
 // The tensor-core kernel for the sequences with more than max_rows rows a key/value head.
-spear_status_t kv_launch_prefill(const spear_kv_s* h, const KvAttnArgs& a, int max_rows, float* part,
-                                 unsigned* counters, cudaStream_t stream);
+spear_status_t kv_launch_prefill(const spear_kv_s* h, const KvAttnArgs& a, int max_rows, void* ws,
+                                 cudaStream_t stream);
 size_t kv_prefill_workspace(const spear_kv_s* h);
 size_t kv_attention_workspace(const spear_kv_s* h);
 spear_status_t kv_launch_attention(spear_kv_s* h, const KvAttnArgs& a, cudaStream_t stream);

@@ -18,7 +18,7 @@ spear_status_t kv_launch_attention(spear_kv_s* h, const KvAttnArgs& a, cudaStrea
   const int64_t few = chunks ? h->view.group : most;
   const int nt = few <= 8 ? 1 : (few <= 16 ? 2 : 4);
   if (!chunks) return kv_launch_decode(h, a, nt, part, counters, stream);
-  if (a.n_seqs == 1) return kv_launch_prefill(h, a, 0, part, counters, stream);
+  if (a.n_seqs == 1) return kv_launch_prefill(h, a, 0, part, stream);
   const spear_status_t st = kv_launch_decode(h, a, nt, part, counters, stream);
-  return st != SPEAR_OK ? st : kv_launch_prefill(h, a, 8 * nt, part, counters, stream);
+  return st != SPEAR_OK ? st : kv_launch_prefill(h, a, 8 * nt, part, stream);
 }

@@ -30,8 +30,9 @@
 //  - One warp copies the packed tiles, a bulk copy a 16-token block.
 //
 // Work: (sequence, head, row tile, key tile) units in this order are split
-// evenly over the CTAs (one an SM); items that several CTAs share are joined
-// by the last of them to arrive, in CTA order, one 128-row half at a time.
+// evenly over the CTAs (one an SM). Items that several CTAs share leave
+// partial results, which a second small kernel joins in CTA order on all SMs
+// (the last CTA of an item to finish, on its own, took 12 us for it).
 #include <atomic>
 
 #include "kv_device.cuh"
@@ -40,31 +41,52 @@
 namespace spear {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 640;         // 8 softmax, 8 dequantising, 2 MMA warps, copies, schedule
+constexpr int kDeqWarps = 8;
 constexpr int kTile = 128;            // keys of a unit
 constexpr int kRows = 256;            // rows of an item
 constexpr int kBlocksPerTile = kTile / 16;
-constexpr int kItemCost = 4;          // units
-constexpr int kHeader = 1024;         // barriers and the start position
+constexpr int kItemCost = 2;          // units
+constexpr int kHeader = 1024;         // barriers, segments
+constexpr int kSegs = 4;              // segments in flight
+constexpr int kSegReaders = 8 + kDeqWarps + 2 + 1;  // warps that read each segment
 constexpr float kLazy = 8.f;
 constexpr uint32_t kHintNs = 100;
+// setmaxnreg: 256 x 168 + 384 x 48 registers are the 640 x 96 of the launch
+constexpr int kJoinRows = 32;
+
+// An item that several CTAs share, written by the CTA that starts it.
+struct Join {
+  int parts;  // 0: none
+  int rows, r0, h, row;
+};
 
 struct PrefillParams {
   KvView v;
   KvAttnArgs a;
-  int max_rows;        // sequences with at most this many rows of a key/value head belong to the other kernel
-  float* part;         // [grid][2][2 halves][D + 2][128]
-  unsigned* counters;  // [grid][2 halves]
+  int max_rows;   // sequences with at most this many rows of a key/value head belong to the other kernel
+  float* part;    // [grid][2][2 halves][D + 2][128]
+  Join* joins;    // [grid]
   uint64_t wait_ns;
+};
+
+// A CTA's share of an item: `len` key tiles from tile `tile0` on.
+struct Segment {
+  int len;          // 0: the end
+  int b, h, L, tile0;
+  int row;          // first query row of the sequence
+  int pos0;         // position of the sequence's first query row
+  int r0, rows;     // the item's rows of the key/value head: [r0, r0 + rows)
+  int whole;        // all of the item's tiles
+  int slot;         // else, this share's partial result
 };
 
 struct Header {
   uint64_t raw_full[2], raw_empty[2], k_full[2], k_empty[2], v_full[2], v_empty[2];
   uint64_t q_full[2], s_full[2], p_full[2][2], o_full[2], turn[2], done[2];  // p_full: [64 keys][half]
+  uint64_t seg_full[kSegs], seg_empty[kSegs];
+  Segment seg[kSegs];
   uint32_t tmem;
-  int start_b, start_h, start_qt, start_off;
-  int last[2];
-  int64_t units;
 };
 static_assert(sizeof(Header) <= kHeader, "");
 
@@ -92,56 +114,6 @@ SPEAR_DEVINL Item item_of(const PrefillParams& p, const KvSeq& s, int qt) {
   return it;
 }
 
-// A position in the list of units: unit `off` of an item, of which the first
-// kItemCost stand for the work that an item costs beside its tiles.
-struct Cursor {
-  int b, h, qt, nqt, off;
-  KvSeq s;
-  Item it;
-  int64_t u;
-};
-
-// A CTA's share of an item: key tiles [t0, t1) of its it.tiles.
-struct Segment {
-  KvSeq s;
-  Item it;
-  int b, h, qt;
-  int t0, t1;
-  int64_t unit0;  // the unit of tile 0
-};
-
-SPEAR_DEVINL bool next_segment(const PrefillParams& p, Cursor& c, int64_t u1, Segment& g) {
-  while (c.u < u1) {
-    const int end = (int)min((int64_t)kItemCost + c.it.tiles, c.off + (u1 - c.u));
-    g.s = c.s;
-    g.it = c.it;
-    g.b = c.b;
-    g.h = c.h;
-    g.qt = c.qt;
-    g.t0 = max(0, c.off - kItemCost);
-    g.t1 = max(0, end - kItemCost);
-    g.unit0 = c.u - c.off + kItemCost;
-    c.u += end - c.off;
-    c.off = 0;
-    if (c.u < u1) {
-      if (++c.qt == c.nqt) {
-        c.qt = 0;
-        if (++c.h == p.v.n_kv_heads) {
-          c.h = 0;
-          do {
-            ++c.b;
-            c.s = kv_seq(p.v, p.a, c.b, kTile);
-            c.nqt = row_tiles(p, c.s);
-          } while (c.nqt == 0);
-        }
-      }
-      c.it = item_of(p, c.s, c.qt);
-    }
-    if (g.t1 > g.t0) return true;
-  }
-  return false;
-}
-
 // Units of one head of a sequence, the whole warp at it.
 SPEAR_DEVINL int64_t head_units(const PrefillParams& p, const KvSeq& s, int nqt, int lane) {
   int64_t x = 0;
@@ -166,7 +138,123 @@ SPEAR_DEVINL void each_sequence(const PrefillParams& p, int lane, F f) {
   }
 }
 
-SPEAR_DEVINL void wg_sync(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
+SPEAR_DEVINL void fail(const PrefillParams& p) { atomicOr(p.v.status, kStatusTimeoutPipe); }
+
+// The warp that lays out a CTA's work. Every CTA counts all units, finds where
+// its equal share begins and hands its segments to the other warps; it also
+// fetches the coming items' query rows into L2.
+template <int D>
+SPEAR_DEVINL void schedule(const PrefillParams& p, Header& hd, int lane) {
+  int64_t U = 0;
+  each_sequence(p, lane, [&](int, const KvSeq& s, int nqt) {
+    U += head_units(p, s, nqt, lane) * p.v.n_kv_heads;
+    return false;
+  });
+  const int64_t G = min((int64_t)gridDim.x, U), cta = blockIdx.x;
+  int64_t u = 0, u1 = 0;
+  if (cta < G) {
+    const int64_t x = (cta + (lane & 1)) * U / G;
+    u = __shfl_sync(0xffffffffu, x, 0);
+    u1 = __shfl_sync(0xffffffffu, x, 1);
+  }
+  int b = 0, h = 0, qt = 0, off = 0, nqt = 0;
+  KvSeq s;
+  if (u < u1) {
+    int64_t before = 0;
+    each_sequence(p, lane, [&](int bb, const KvSeq& ss, int nq) {
+      const int64_t hu = head_units(p, ss, nq, lane);
+      if (u >= before + hu * p.v.n_kv_heads) {
+        before += hu * p.v.n_kv_heads;
+        return false;
+      }
+      b = bb;
+      s = ss;
+      nqt = nq;
+      h = (int)((u - before) / hu);
+      int64_t rest = u - before - h * hu;
+      for (int q0 = 0; q0 < nqt; q0 += 32) {
+        const int own = q0 + lane < nqt ? kItemCost + item_of(p, s, q0 + lane).tiles : 0;
+        int incl = own;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int x = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += x;
+        }
+        const int sum = __shfl_sync(0xffffffffu, incl, 31);
+        if (rest < sum) {
+          const int at = __ffs(__ballot_sync(0xffffffffu, rest < incl)) - 1;
+          qt = q0 + at;
+          off = (int)rest - (__shfl_sync(0xffffffffu, incl, at) - __shfl_sync(0xffffffffu, own, at));
+          break;
+        }
+        rest -= sum;
+      }
+      return true;
+    });
+  }
+  Join join = {};
+  unsigned n = 0;
+  for (bool end = false; !end;) {
+    Segment g = {};
+    while (u < u1 && g.len == 0) {
+      const Item it = item_of(p, s, qt);
+      const int stop = (int)min((int64_t)kItemCost + it.tiles, off + (u1 - u));
+      const int t0 = max(0, off - kItemCost), t1 = max(0, stop - kItemCost);
+      if (t1 > t0) {
+        g.len = t1 - t0;
+        g.b = b;
+        g.h = h;
+        g.L = s.L;
+        g.tile0 = it.lo + t0;
+        g.row = s.row;
+        g.pos0 = s.L - s.n;
+        g.r0 = qt * kRows;
+        g.rows = it.rows;
+        g.whole = g.len == it.tiles;
+        g.slot = (int)cta * 2 + (t0 == 0);  // one slot for the share that starts an item, one for a later share
+        if (t0 == 0 && !g.whole) {
+          const int64_t last = u - off + kItemCost + it.tiles - 1;  // the item's last unit
+          join = {(int)(((last + 1) * G - 1) / U - cta) + 1, it.rows, g.r0, h, s.row};
+        }
+      }
+      u += stop - off;
+      off = 0;
+      if (u < u1 && ++qt == nqt) {
+        qt = 0;
+        if (++h == p.v.n_kv_heads) {
+          h = 0;
+          do {
+            ++b;
+            s = kv_seq(p.v, p.a, b, kTile);
+            nqt = row_tiles(p, s);
+          } while (nqt == 0);
+        }
+      }
+    }
+    end = g.len == 0;
+    for (int r = lane; r < g.rows; r += 32) {
+      const unsigned R = g.r0 + r, tok = R / (unsigned)p.v.group;
+      const __nv_bfloat16* q = p.a.q + (int64_t)(g.row + tok) * p.a.ld_q + (int64_t)(g.h * p.v.group + R - tok * p.v.group) * D;
+#pragma unroll
+      for (int x = 0; x < D; x += 64) prefetch_l2_line(q + x);
+    }
+    const unsigned i = n % kSegs;
+    if (n >= kSegs && !warp_wait(&hd.seg_empty[i], ((n / kSegs) & 1u) ^ 1u, p.wait_ns, 1000)) {
+      if (lane == 0) {
+        fail(p);
+        p.joins[cta] = {};
+      }
+      return;
+    }
+    if (lane == 0) {
+      hd.seg[i] = g;
+      mbar_arrive(&hd.seg_full[i]);
+    }
+    __syncwarp();
+    ++n;
+  }
+  if (lane == 0) p.joins[cta] = join;
+}
 
 // Eight codes of a word as four bf16 pairs, elements (0, 4), (1, 5), (2, 6), (3, 7): code * scale + offset, rounded
 // once. A masked nibble pair reads as tiny bf16 values (see decode_frag_unpack), which one exact multiplication
@@ -185,17 +273,17 @@ SPEAR_DEVINL void sts128(uint32_t addr, const uint4& v) {
                : "memory");
 }
 
-// One key's row: codes (D / 2 bytes at `src`) to row `key` of a swizzled tile.
+// Half `half` of one key's row: codes (D / 2 bytes at `src`) to row `key` of a swizzled tile.
 template <int D>
-SPEAR_DEVINL void dequant_row(uint32_t src, uint32_t tile, int key, uint32_t par) {
+SPEAR_DEVINL void dequant_row(uint32_t src, uint32_t tile, int key, int half, uint32_t par) {
   const float sc = __uint_as_float(par << 16);
   const uint32_t s_lo = pack_bf16x2(sc * 128.f, sc * 128.f), s_hi = pack_bf16x2(sc * 8.f, sc * 8.f);
   const uint32_t oo = __byte_perm(par, par, 0x3232);
-  constexpr int Q = D / 32;  // 16-byte quarters of the packed row
-#pragma unroll 1
+  constexpr int Q = D / 64;  // 16-byte quarters of the packed row a thread
+#pragma unroll
   for (int i = 0; i < Q; ++i) {
-    // quarters in an order of the key's own: a quarter warp then meets every bank once
-    const int q = Q == 4 ? (i + (key >> 1)) & 3 : i;
+    // D = 128: quarters in an order of the key's own, so that a quarter warp meets every bank once
+    const int q = Q == 2 ? (i + 2 * half + (key >> 1)) & 3 : half;
     const uint4 w = lds128(src + q * 16);
     const uint32_t words[4] = {w.x, w.y, w.z, w.w};
     const uint32_t row = tile + (q >> 1) * (kTile * 128) + key * 128;
@@ -209,7 +297,10 @@ SPEAR_DEVINL bool finite_par(uint32_t par) {
   return (par & 0x7F80u) != 0x7F80u && (par & 0x7F800000u) != 0x7F800000u;
 }
 
-SPEAR_DEVINL void fail(const PrefillParams& p) { atomicOr(p.v.status, kStatusTimeoutPipe); }
+// Eight results in the order of Q's permuted elements, 0, 4, 1, 5, 2, 6, 3, 7, back in their places, as bf16.
+SPEAR_DEVINL uint4 unpermute8(const float (&x)[8]) {
+  return make_uint4(pack_bf16x2(x[0], x[2]), pack_bf16x2(x[4], x[6]), pack_bf16x2(x[1], x[3]), pack_bf16x2(x[5], x[7]));
+}
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_constant__ PrefillParams p) {
@@ -227,99 +318,76 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       mbar_init(&hd.raw_full[i], 1);
-      mbar_init(&hd.raw_empty[i], 4);
-      mbar_init(&hd.k_full[i], 4);
+      mbar_init(&hd.raw_empty[i], kDeqWarps);
+      mbar_init(&hd.k_full[i], kDeqWarps);
       mbar_init(&hd.k_empty[i], 2);
-      mbar_init(&hd.v_full[i], 4);
+      mbar_init(&hd.v_full[i], kDeqWarps);
       mbar_init(&hd.v_empty[i], 2);
       mbar_init(&hd.q_full[i], 4);
       mbar_init(&hd.s_full[i], 1);
       mbar_init(&hd.p_full[0][i], 4);
       mbar_init(&hd.p_full[1][i], 4);
+      mbar_init(&hd.o_full[i], 1);
       mbar_init(&hd.turn[i], 1);
       mbar_init(&hd.done[i], 1);
-      mbar_init(&hd.o_full[i], 1);
+    }
+    for (int i = 0; i < kSegs; ++i) {
+      mbar_init(&hd.seg_full[i], 1);
+      mbar_init(&hd.seg_empty[i], kSegReaders);
     }
     fence_mbar_init();
   }
-  if (warp == 12) {
+  if (warp == 16) {
     tmem_alloc(&hd.tmem, 512);
     tmem_relinquish();
-  }
-  // ---- this CTA's units [u0, u1) and the position of u0
-  if (warp == 0) {
-    int64_t U = 0;
-    each_sequence(p, lane, [&](int, const KvSeq& s, int nqt) {
-      U += head_units(p, s, nqt, lane) * p.v.n_kv_heads;
-      return false;
-    });
-    const int64_t G = min((int64_t)gridDim.x, U), u0 = blockIdx.x * U / max(G, (int64_t)1);
-    int64_t before = 0;
-    if ((int64_t)blockIdx.x < G)
-      each_sequence(p, lane, [&](int b, const KvSeq& s, int nqt) {
-        const int64_t hu = head_units(p, s, nqt, lane);
-        if (u0 >= before + hu * p.v.n_kv_heads) {
-          before += hu * p.v.n_kv_heads;
-          return false;
-        }
-        const int h = (int)((u0 - before) / hu);
-        int64_t rest = u0 - before - h * hu;
-        for (int q0 = 0; q0 < nqt; q0 += 32) {
-          const int qt = q0 + lane;
-          const int own = qt < nqt ? kItemCost + item_of(p, s, qt).tiles : 0;
-          int incl = own;
-#pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const int x = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += x;
-          }
-          if (own > 0 && rest >= incl - own && rest < incl) {
-            hd.start_b = b;
-            hd.start_h = h;
-            hd.start_qt = qt;
-            hd.start_off = (int)(rest - (incl - own));
-          }
-          const int sum = __shfl_sync(0xffffffffu, incl, 31);
-          if (rest < sum) break;
-          rest -= sum;
-        }
-        return true;
-      });
-    if (lane == 0) hd.units = U;
   }
   __syncwarp();
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
-  const int64_t U = hd.units, G = min((int64_t)gridDim.x, U), cta = blockIdx.x;
   const uint32_t tmem = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(&hd.tmem), 0);
-  const int64_t u0 = cta < G ? cta * U / G : 0, u1 = cta < G ? (cta + 1) * U / G : 0;
-  Cursor c{};
-  c.u = u0;
-  if (u0 < u1) {
-    c.b = hd.start_b;
-    c.h = hd.start_h;
-    c.qt = hd.start_qt;
-    c.off = hd.start_off;
-    c.s = kv_seq(p.v, p.a, c.b, kTile);
-    c.nqt = row_tiles(p, c.s);
-    c.it = item_of(p, c.s, c.qt);
-  }
 
-  Segment g;
-  if (warp >= 12) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if (warp == 13) {
+  // The n-th segment, read by a whole warp; false at the end (or if the wait gave up).
+  auto read_segment = [&](unsigned n, Segment& g) {
+    const unsigned i = n % kSegs;
+    if (!warp_wait(&hd.seg_full[i], (n / kSegs) & 1u, p.wait_ns, kHintNs)) {
+      if (lane == 0) fail(p);
+      return false;
+    }
+    const volatile Segment& x = hd.seg[i];
+    g.len = __shfl_sync(0xffffffffu, x.len, 0);
+    g.b = x.b;
+    g.h = x.h;
+    g.L = x.L;
+    g.tile0 = x.tile0;
+    g.row = x.row;
+    g.pos0 = x.pos0;
+    g.r0 = x.r0;
+    g.rows = __shfl_sync(0xffffffffu, x.rows, 0);
+    g.whole = x.whole;
+    g.slot = x.slot;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&hd.seg_empty[i]);
+    return g.len > 0;
+  };
+
+  if (warp >= 16) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+    if (warp == 19) {
+      // -------------------------------------------------------------- the CTA's segments, in order
+      schedule<D>(p, hd, lane);
+    } else if (warp == 18) {
       // -------------------------------------------------------------- copies of the packed tiles
       int st = 0;
-      unsigned ph = 0;
-      unsigned issued = 0;
+      unsigned ph = 0, issued = 0;
       bool ok = true;
-      while (ok && next_segment(p, c, u1, g)) {
-        for (int t = g.t0; t < g.t1; ++t) {
-          const int blk = (g.it.lo + t) * kBlocksPerTile + lane;
+      Segment g;
+      for (unsigned n = 0; ok && read_segment(n, g); ++n) {
+        const int blocks = (g.L + 15) / 16;
+        for (int t = 0; t < g.len; ++t) {
+          const int blk = (g.tile0 + t) * kBlocksPerTile + lane;
           const uint8_t* src = nullptr;
-          if (lane < kBlocksPerTile && blk < (g.s.L + 15) / 16) {
+          if (lane < kBlocksPerTile && blk < blocks) {
             const int pg = p.a.page_table[(int64_t)g.b * p.a.ld_pt + blk / p.v.bpp];
             if (pg >= 0 && pg < p.v.n_pages)
               src = p.v.pool + (((int64_t)pg * p.v.n_kv_heads + g.h) * p.v.bpp + blk % p.v.bpp) * BB;
@@ -344,9 +412,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         --st;
         warp_wait(&hd.raw_full[st], ph, p.wait_ns, kHintNs);
       }
-    } else if (warp != 15) {
+    } else {
       // -------------------------------------------------------------- MMA issue, one warp a half, uniform
-      const int i = warp == 14;
+      const int i = warp - 16;
       const uint32_t leader = elect_leader();
       const uint32_t idesc_s = idesc_bf16_f32(128, kTile);
       const uint32_t idesc_o = idesc_bf16_f32(128, D) | kIdescBMnMajor;
@@ -357,10 +425,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       unsigned kc = 0, q_ph = 0, p_ph = 0;
       bool ok = true;
       auto wait = [&](uint64_t* bar, unsigned parity) {
-        if (ok && !warp_wait(bar, parity, p.wait_ns, kHintNs)) {
-          ok = false;
-          if (leader) fail(p);
-        }
+        ok = warp_wait(bar, parity, p.wait_ns, kHintNs);
         return ok;
       };
       // The halves take turns, "product of the last tile, scores of the next" each, so that one half's softmax
@@ -371,15 +436,16 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         turn_ph ^= 1u;
         return got;
       };
-      bool more = next_segment(p, c, u1, g);
-      if (more) take_turn();
+      Segment g;
+      unsigned n = 0;
+      bool more = read_segment(n++, g);
+      if (more) take_turn() && wait(&hd.k_full[0], 0);
       while (more && ok) {
-        const int len = __shfl_sync(0xffffffffu, g.t1 - g.t0, 0);
-        const bool mine = __shfl_sync(0xffffffffu, g.it.rows, 0) > 128 * i;
-        more = next_segment(p, c, u1, g);
+        const int len = g.len;
+        const bool mine = g.rows > 128 * i;
+        more = read_segment(n++, g);
         for (int k = 0; k < len; ++k, ++kc) {
           const unsigned st = kc & 1u, ph = (kc >> 1) & 1u;
-          if (kc == 0 && !wait(&hd.k_full[0], 0)) break;
           if (mine) {
             if (k == 0) {
               if (!wait(&hd.q_full[i], q_ph)) break;
@@ -390,17 +456,17 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
               constexpr uint32_t kBlock = (128 * 128) >> 4;
-              umma_bf16(leader, s_d, q_desc + (kk / 4) * kBlock + (kk % 4) * 2, kd + (kk / 4) * kBlock + (kk % 4) * 2, idesc_s,
-                        kk != 0);
+              umma_bf16(leader, s_d, q_desc + (kk / 4) * kBlock + (kk % 4) * 2,
+                        kd + (kk / 4) * kBlock + (kk % 4) * 2, idesc_s, kk != 0);
             }
             umma_commit(leader, &hd.s_full[i]);
             umma_commit(leader, &hd.k_empty[st]);
-          } else {
-            if (leader) mbar_arrive(&hd.k_empty[st]);
+          } else if (leader) {
+            mbar_arrive(&hd.k_empty[st]);
           }
           if (leader) mbar_arrive(&hd.turn[i ^ 1]);
-          if (!wait(&hd.v_full[st], ph)) break;
-          if ((more || k + 1 < len) && !wait(&hd.k_full[st ^ 1u], ((kc + 1) >> 1) & 1u)) break;  // before the turn, not in it
+          // what the turn needs, before taking it: the next K tile (dequantised after this V tile) or this V tile
+          if (more || k + 1 < len ? !wait(&hd.k_full[st ^ 1u], ((kc + 1) >> 1) & 1u) : !wait(&hd.v_full[st], ph)) break;
           if (mine && !wait(&hd.p_full[0][i], p_ph)) break;
           if (!take_turn()) break;
           if (mine) {
@@ -417,54 +483,59 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
             p_ph ^= 1u;
             if (k + 1 == len) umma_commit(leader, &hd.o_full[i]);
             umma_commit(leader, &hd.v_empty[st]);
-          } else {
-            if (leader) mbar_arrive(&hd.v_empty[st]);
+          } else if (leader) {
+            mbar_arrive(&hd.v_empty[st]);
           }
         }
       }
+      if (!ok && leader) fail(p);
       if (leader) mbar_arrive(&hd.turn[i ^ 1]);
       // nothing of this CTA's is still running on the tensor cores when the others go on to the end
       umma_commit(leader, &hd.done[i]);
       if (!warp_wait(&hd.done[i], 0, p.wait_ns, 0) && leader) fail(p);
     }
   } else if (warp >= 8) {
-    // ---------------------------------------------------------------- dequantisers
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    const int key = tid - 256;
+    // ---------------------------------------------------------------- dequantisers, two threads a key
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+    const int key = (tid - 256) & 127, half = (tid - 256) >> 7;
     const uint32_t blk_at = raw_at + (key / 16) * BB;
     const int r = key & 15;
     bool ok = true;
     unsigned k = 0;
-    while (next_segment(p, c, u1, g))
-     for (int t = g.t0; t < g.t1; ++t, ++k) {
-      const unsigned st = k & 1u, ph = (k >> 1) & 1u;
-      const uint32_t blk = blk_at + st * kRawBytes;
-      ok = ok && warp_wait(&hd.raw_full[st], ph, p.wait_ns, kHintNs);
-      const bool live = (g.it.lo + t) * kTile + key < g.s.L;
-      uint32_t kp = 0, vp = 0;
-      if (live) {
-        kp = lds32(blk + 16 * D + 4 * r);
-        vp = lds32(blk + 16 * D + 64 + 4 * r);
-        if (!finite_par(vp)) vp = 0, kp = 0x7FC07FC0u;
-      }
-      ok = ok && (k < 2 || warp_wait(&hd.k_empty[st], ph ^ 1u, p.wait_ns, kHintNs));
-      if (ok) dequant_row<D>(blk + r * (D / 2), k_at + st * kTileBytes, key, kp);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (ok && lane == 0) mbar_arrive(&hd.k_full[st]);
-      ok = ok && (k < 2 || warp_wait(&hd.v_empty[st], ph ^ 1u, p.wait_ns, kHintNs));
-      if (ok) dequant_row<D>(blk + 8 * D + r * (D / 2), v_at + st * kTileBytes, key, vp);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (ok && lane == 0) {
-        mbar_arrive(&hd.v_full[st]);
-        mbar_arrive(&hd.raw_empty[st]);
+    Segment g;
+    for (unsigned n = 0; ok && read_segment(n, g); ++n) {
+      for (int t = 0; t < g.len; ++t, ++k) {
+        const unsigned st = k & 1u, ph = (k >> 1) & 1u;
+        const uint32_t blk = blk_at + st * kRawBytes;
+        ok = warp_wait(&hd.raw_full[st], ph, p.wait_ns, kHintNs);
+        if (!ok) break;
+        uint32_t kp = 0, vp = 0;
+        if ((g.tile0 + t) * kTile + key < g.L) {
+          kp = lds32(blk + 16 * D + 4 * r);
+          vp = lds32(blk + 16 * D + 64 + 4 * r);
+          if (!finite_par(vp)) vp = 0, kp = 0x7FC07FC0u;
+        }
+        ok = k < 2 || warp_wait(&hd.k_empty[st], ph ^ 1u, p.wait_ns, kHintNs);
+        if (!ok) break;
+        dequant_row<D>(blk + r * (D / 2), k_at + st * kTileBytes, key, half, kp);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&hd.k_full[st]);
+        ok = k < 2 || warp_wait(&hd.v_empty[st], ph ^ 1u, p.wait_ns, kHintNs);
+        if (!ok) break;
+        dequant_row<D>(blk + 8 * D + r * (D / 2), v_at + st * kTileBytes, key, half, vp);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&hd.v_full[st]);
+          mbar_arrive(&hd.raw_empty[st]);
+        }
       }
     }
     if (!ok && lane == 0) fail(p);
   } else {
     // ---------------------------------------------------------------- softmax, one row a thread
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
     const int i = warp / 4, quarter = warp & 3;
     const int row = 32 * quarter + lane;  // of the half
     const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
@@ -474,223 +545,188 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     unsigned n_s = 0, n_o = 0;
     bool ok = true;
 
-    // this warp's 32 rows of an item into the Q tile: D / 8 lanes a row, 16 bytes each
+    // this warp's 32 rows of an item into the Q tile: D / 8 lanes a row, 16 bytes each, eight loads in flight
     auto load_q = [&](const Segment& x) {
-      constexpr int C = D / 8, RPI = 32 / C;
-#pragma unroll 4
-      for (int r0 = 0; r0 < 32; r0 += RPI) {
-        const int rr = 32 * quarter + r0 + lane / C, ch = lane % C;
-        const int in_item = 128 * i + rr;
-        uint4 w = make_uint4(0, 0, 0, 0);
-        if (in_item < x.it.rows) {
-          const int R = x.qt * kRows + in_item, tok = R / p.v.group;
-          w = *reinterpret_cast<const uint4*>(p.a.q + (int64_t)(x.s.row + tok) * p.a.ld_q +
-                                              (int64_t)(x.h * p.v.group + R - tok * p.v.group) * D + ch * 8);
+      constexpr int C = D / 8, RPI = 32 / C, N = C;  // N = 32 / RPI loads a lane
+#pragma unroll
+      for (int b0 = 0; b0 < N; b0 += 8) {
+        uint4 w[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int in_item = 128 * i + 32 * quarter + (b0 + j) * RPI + lane / C;
+          w[j] = make_uint4(0, 0, 0, 0);
+          if (in_item < x.rows) {
+            const unsigned R = x.r0 + in_item, tok = R / (unsigned)p.v.group;
+            w[j] = *reinterpret_cast<const uint4*>(p.a.q + (int64_t)(x.row + tok) * p.a.ld_q +
+                                                   (int64_t)(x.h * p.v.group + R - tok * p.v.group) * D + (lane % C) * 8);
+          }
         }
-        uint4 o;
-        o.x = __byte_perm(w.x, w.z, 0x5410) ^ flip;
-        o.y = __byte_perm(w.x, w.z, 0x7632) ^ flip;
-        o.z = __byte_perm(w.y, w.w, 0x5410) ^ flip;
-        o.w = __byte_perm(w.y, w.w, 0x7632) ^ flip;
-        sts128(q_at + i * kTileBytes + (ch / 8) * (128 * 128) + rr * 128 + (((ch % 8) ^ (rr & 7)) * 16), o);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int rr = 32 * quarter + (b0 + j) * RPI + lane / C, ch = lane % C;
+          uint4 o;
+          o.x = __byte_perm(w[j].x, w[j].z, 0x5410) ^ flip;
+          o.y = __byte_perm(w[j].x, w[j].z, 0x7632) ^ flip;
+          o.z = __byte_perm(w[j].y, w[j].w, 0x5410) ^ flip;
+          o.w = __byte_perm(w[j].y, w[j].w, 0x7632) ^ flip;
+          sts128(q_at + i * kTileBytes + (ch / 8) * (128 * 128) + rr * 128 + (((ch % 8) ^ (rr & 7)) * 16), o);
+        }
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&hd.q_full[i]);
     };
 
-    bool loaded = false;  // the item's Q rows are already in place
-    bool more = next_segment(p, c, u1, g);
-    while (more) {
-      const bool mine = g.it.rows > 128 * i;  // a short item has no second half
-      const int len = g.t1 - g.t0;
+    Segment g;
+    unsigned n = 0;
+    bool more = read_segment(n++, g);
+    if (more && g.rows > 128 * i) load_q(g);
+    while (more && ok) {
       Segment nx;
-      if (mine) {
-        if (!loaded && ok) load_q(g);
-        loaded = false;
-        const int r0 = g.qt * kRows + 128 * i, R = min(r0 + row, g.qt * kRows + g.it.rows - 1), tok = R / p.v.group;
-        const int hi = g.s.L - g.s.n + tok;  // last key that this row sees
-        // keys that every row of the half sees
-        const int all_hi = g.s.L - g.s.n + r0 / p.v.group;
-        const int all_lo = p.a.window > 0 ? g.s.L - g.s.n + min(r0 + 127, g.qt * kRows + g.it.rows - 1) / p.v.group -
-                                                p.a.window + 1 : 0;
-        float m = -INFINITY, l = 0.f;
-        for (int k = 0; k < len; ++k) {
-          const int key0 = (g.it.lo + g.t0 + k) * kTile;
-          ok = ok && warp_wait(&hd.s_full[i], n_s & 1u, p.wait_ns, kHintNs);
-          ++n_s;
-          if (!ok) continue;
-          tc_fence_after_sync();
-          if (key0 + kTile - 1 > all_hi || key0 < all_lo) {  // some row does not see every key: minus infinity there
-            const int d = hi - key0, e = p.a.window > 0 ? d - p.a.window : -1;
-#pragma unroll 1
-            for (int j = 0; j < kTile; j += 32) {
-              uint32_t v[32];
-              tmem_ld_x32(s_t + j, v);
-              tmem_ld_wait();
-#pragma unroll
-              for (int x = 0; x < 32; ++x)
-                if (j + x > d || j + x <= e) v[x] = 0xFF800000u;
-              tmem_st_x32(s_t + j, v);
-            }
-            tmem_st_wait();
-          }
-          uint32_t v[4][32];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) tmem_ld_x32(s_t + 32 * j, v[j]);
-          tmem_ld_wait();
-          // Weights of the first 64 keys by the present m, beside the maximum over all 128: m is nearly always kept
-          uint32_t w[32];
-          uint64_t sum2[2];
-          auto weights = [&](int y) {
-            const float ms = m == -INFINITY ? 0.f : -m * sl;
-            const uint64_t sl2 = pack_f32x2(sl, sl), ms2 = pack_f32x2(ms, ms);
-#pragma unroll
-            for (int x = 0; x < 64; x += 2) {
-              const uint32_t* q = &v[2 * y + x / 32][x % 32];
-              float pa, pb;
-              unpack_f32x2(fma_f32x2(pack_b32x2(q[0], q[1]), sl2, ms2), pa, pb);
-              pa = ex2(pa);
-              pb = ex2(pb);
-              sum2[(x >> 1) & 1] = x < 4 && y == 0 ? pack_f32x2(pa, pb) : add_f32x2(sum2[(x >> 1) & 1], pack_f32x2(pa, pb));
-              w[x / 2] = pack_bf16x2(pa, pb);
-            }
-          };
-          auto hand_over = [&](int y) {
-            tmem_st_x32(s_t + 32 * y, w);
-            tmem_st_wait();
-            tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&hd.p_full[y][i]);
-          };
-          weights(0);
-          float top[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            top[j] = fmaxf(__uint_as_float(v[j][0]), __uint_as_float(v[j][1]));
-#pragma unroll
-            for (int x = 2; x < 32; x += 2)
-              top[j] = fmaxf(top[j], fmaxf(__uint_as_float(v[j][x]), __uint_as_float(v[j][x + 1])));
-          }
-          const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-          if (k == 0 || __any_sync(0xffffffffu, m == -INFINITY ? mx > m : (mx - m) * sl > kLazy)) {
-            const float mn = fmaxf(m, mx);
-            if (k > 0) {
-              // the previous product has finished (s_full covers it), the next waits for this thread
-              const float f = m == -INFINITY ? 0.f : ex2((m - mn) * sl);
-              l *= f;
-#pragma unroll 1
-              for (int j = 0; j < D; j += 16) {
-                uint32_t o[16];
-                tmem_ld_x16(o_t + j, o);
-                tmem_ld_wait();
-#pragma unroll
-                for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
-                tmem_st_x16(o_t + j, o);
-              }
-            }
-            m = mn;
-            tmem_ld_x32(s_t, v[0]);
-            tmem_ld_x32(s_t + 32, v[1]);
-            tmem_ld_wait();
-            weights(0);
-          }
-          hand_over(0);
-          weights(1);
-          hand_over(1);
-          float sa, sb;
-          unpack_f32x2(add_f32x2(sum2[0], sum2[1]), sa, sb);
-          l += sa + sb;
-        }
-        more = next_segment(p, c, u1, nx);
-        // the half's scores are done with its Q tile: the next item's rows go in while the last product runs
-        if (more && nx.it.rows > 128 * i && ok) {
-          load_q(nx);
-          loaded = true;
-        }
-        // ---- the segment's result
-        ok = ok && warp_wait(&hd.o_full[i], n_o & 1u, p.wait_ns, kHintNs);
-        ++n_o;
+      if (g.rows <= 128 * i) {  // a short item has no second half
+        more = read_segment(n++, nx);
+        if (more && nx.rows > 128 * i) load_q(nx);
+        g = nx;
+        continue;
+      }
+      const int in_item = min(128 * i + row, g.rows - 1);
+      const unsigned R = g.r0 + in_item, tok = R / (unsigned)p.v.group;
+      const int hi = g.pos0 + (int)tok;  // last key that this row sees
+      // keys that every row of the half sees
+      const int all_hi = g.pos0 + (g.r0 + 128 * i) / p.v.group;
+      const int all_lo = p.a.window > 0 ? g.pos0 + (g.r0 + min(128 * i + 127, g.rows - 1)) / p.v.group - p.a.window + 1 : 0;
+      float m = -INFINITY, l = 0.f;
+      for (int k = 0; k < g.len; ++k) {
+        const int key0 = (g.tile0 + k) * kTile;
+        ok = warp_wait(&hd.s_full[i], n_s & 1u, p.wait_ns, kHintNs);
+        if (!ok) break;
+        ++n_s;
         tc_fence_after_sync();
-        const bool whole = len == g.it.tiles;
-        const bool real = 128 * i + row < g.it.rows;
-        __nv_bfloat16* dst = p.a.out + (int64_t)(g.s.row + tok) * p.a.ld_out +
-                             (int64_t)(g.h * p.v.group + R - tok * p.v.group) * D;
-        auto write32 = [&](int col, const float (&v)[32], float inv) {
+        uint32_t v[4][32];
 #pragma unroll
-          for (int g8 = 0; g8 < 4; ++g8) {
-            const float* x = v + 8 * g8;  // elements 0, 4, 1, 5, 2, 6, 3, 7
-            uint4 w;
-            w.x = pack_bf16x2(x[0] * inv, x[2] * inv);
-            w.y = pack_bf16x2(x[4] * inv, x[6] * inv);
-            w.z = pack_bf16x2(x[1] * inv, x[3] * inv);
-            w.w = pack_bf16x2(x[5] * inv, x[7] * inv);
-            *reinterpret_cast<uint4*>(dst + col + 8 * g8) = w;
+        for (int j = 0; j < 4; ++j) tmem_ld_x32(s_t + 32 * j, v[j]);
+        tmem_ld_wait();
+        const bool masked = key0 + kTile - 1 > all_hi || key0 < all_lo;
+        const int d = hi - key0, e = p.a.window > 0 ? d - p.a.window : -1;  // visible: e < column <= d
+        auto mask = [&](int j) {
+          const int a = d - 32 * j, b = e - 32 * j;
+          const uint32_t see = (a >= 31 ? 0xffffffffu : a < 0 ? 0u : (2u << a) - 1u) &
+                               ~(b >= 31 ? 0xffffffffu : b < 0 ? 0u : (2u << b) - 1u);
+#pragma unroll
+          for (int x = 0; x < 32; ++x)
+            if (!(see & (1u << x))) v[j][x] = 0xFF800000u;
+        };
+        if (masked) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) mask(j);
+        }
+        // Weights of the first 64 keys by the present m, beside the maximum over all 128: m is nearly always kept
+        uint32_t w[32];
+        uint64_t sum2[2];
+        auto weights = [&](int y) {
+          const float ms = m == -INFINITY ? 0.f : -m * sl;
+          const uint64_t sl2 = pack_f32x2(sl, sl), ms2 = pack_f32x2(ms, ms);
+#pragma unroll
+          for (int x = 0; x < 64; x += 2) {
+            const uint32_t* q = &v[2 * y + x / 32][x % 32];
+            float pa, pb;
+            unpack_f32x2(fma_f32x2(pack_b32x2(q[0], q[1]), sl2, ms2), pa, pb);
+            pa = ex2(pa);
+            pb = ex2(pb);
+            sum2[(x >> 1) & 1] = x < 4 && y == 0 ? pack_f32x2(pa, pb) : add_f32x2(sum2[(x >> 1) & 1], pack_f32x2(pa, pb));
+            w[x / 2] = pack_bf16x2(pa, pb);
           }
         };
-        if (whole) {
-          const float inv = l == 0.f ? 0.f : 1.f / l;
+        auto hand_over = [&](int y) {
+          tmem_st_x32(s_t + 32 * y, w);
+          tmem_st_wait();
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&hd.p_full[y][i]);
+        };
+        weights(0);
+        float top[4];
 #pragma unroll
-          for (int j = 0; j < D; j += 32) {
-            uint32_t o[32];
-            tmem_ld_x32(o_t + j, o);
-            tmem_ld_wait();
-            float v[32];
+        for (int j = 0; j < 4; ++j) {
+          top[j] = fmaxf(__uint_as_float(v[j][0]), __uint_as_float(v[j][1]));
 #pragma unroll
-            for (int x = 0; x < 32; ++x) v[x] = l == 0.f ? 0.f : __uint_as_float(o[x]);
-            if (real && ok) write32(j, v, inv);
-          }
-        } else {
-          const int64_t ca = ((g.unit0 + 1) * G - 1) / U, cb = ((g.unit0 + g.it.tiles) * G - 1) / U;
-          float* slot = p.part + ((cta * 2 + (g.t0 == 0 ? 1 : 0)) * 2 + i) * kPart + row;
-#pragma unroll
-          for (int j = 0; j < D; j += 32) {
-            uint32_t o[32];
-            tmem_ld_x32(o_t + j, o);
-            tmem_ld_wait();
-#pragma unroll
-            for (int x = 0; x < 32; ++x) __stcg(slot + (j + x) * 128, __uint_as_float(o[x]));
-          }
-          __stcg(slot + D * 128, m);
-          __stcg(slot + (D + 1) * 128, l);
-          __threadfence();
-          wg_sync(1 + i);
-          if (row == 0) hd.last[i] = atomicAdd(p.counters + ca * 2 + i, 1u) == (unsigned)(cb - ca);
-          wg_sync(1 + i);
-          if (*reinterpret_cast<volatile int*>(&hd.last[i])) {
-            __threadfence();
-            if (row == 0) p.counters[ca * 2 + i] = 0;
-            float M = -INFINITY, Ls = 0.f;
-            for (int64_t x = ca; x <= cb; ++x)
-              M = fmaxf(M, __ldcg(p.part + ((x * 2 + (x == ca)) * 2 + i) * kPart + D * 128 + row));
-            for (int64_t x = ca; x <= cb; ++x) {
-              const float* q = p.part + ((x * 2 + (x == ca)) * 2 + i) * kPart + D * 128 + row;
-              const float mx = __ldcg(q), lx = __ldcg(q + 128);
-              Ls += mx == -INFINITY ? lx : lx * ex2((mx - M) * sl);
-            }
-            const float inv = Ls == 0.f ? 0.f : 1.f / Ls;
+          for (int x = 2; x < 32; x += 2)
+            top[j] = fmaxf(top[j], fmaxf(__uint_as_float(v[j][x]), __uint_as_float(v[j][x + 1])));
+        }
+        const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+        if (k == 0 || __any_sync(0xffffffffu, m == -INFINITY ? mx > m : (mx - m) * sl > kLazy)) {
+          const float mn = fmaxf(m, mx);
+          if (k > 0) {
+            // the previous product has finished (s_full covers it), the next waits for this thread
+            const float f = m == -INFINITY ? 0.f : ex2((m - mn) * sl);
+            l *= f;
 #pragma unroll 1
-            for (int j = 0; j < D; j += 32) {
-              float v[32];
+            for (int j = 0; j < D; j += 16) {
+              uint32_t o[16];
+              tmem_ld_x16(o_t + j, o);
+              tmem_ld_wait();
 #pragma unroll
-              for (int x = 0; x < 32; ++x) v[x] = 0.f;
-              for (int64_t x = ca; x <= cb; ++x) {
-                const float* q = p.part + ((x * 2 + (x == ca)) * 2 + i) * kPart + row;
-                const float mx = __ldcg(q + D * 128), lx = __ldcg(q + (D + 1) * 128);
-                const float f = mx == -INFINITY ? (lx == 0.f ? 0.f : 1.f) : ex2((mx - M) * sl);
-                if (f != 0.f || lx != 0.f) {
+              for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
+              tmem_st_x16(o_t + j, o);
+            }
+          }
+          m = mn;
+          tmem_ld_x32(s_t, v[0]);
+          tmem_ld_x32(s_t + 32, v[1]);
+          tmem_ld_wait();
+          if (masked) mask(0), mask(1);
+          weights(0);
+        }
+        hand_over(0);
+        weights(1);
+        hand_over(1);
+        float sa, sb;
+        unpack_f32x2(add_f32x2(sum2[0], sum2[1]), sa, sb);
+        l += sa + sb;
+      }
+      if (!ok) break;
+      // the half's scores are done with its Q tile: the next item's rows go in while the last product runs
+      more = read_segment(n++, nx);
+      if (more && nx.rows > 128 * i) load_q(nx);
+      // ---- the segment's result
+      ok = warp_wait(&hd.o_full[i], n_o & 1u, p.wait_ns, kHintNs);
+      if (!ok) break;
+      ++n_o;
+      tc_fence_after_sync();
+      const bool real = 128 * i + row < g.rows;
+      if (g.whole) {
+        __nv_bfloat16* dst = p.a.out + (int64_t)(g.row + tok) * p.a.ld_out +
+                             (int64_t)(g.h * p.v.group + R - tok * p.v.group) * D;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
-                  for (int y = 0; y < 32; ++y) v[y] = fmaf(f, __ldcg(q + (j + y) * 128), v[y]);
-                }
-              }
-              if (real && ok) write32(j, v, inv);
+        for (int j = 0; j < D; j += 32) {
+          uint32_t o[32];
+          tmem_ld_x32(o_t + j, o);
+          tmem_ld_wait();
+          if (real) {
+#pragma unroll
+            for (int x = 0; x < 32; x += 8) {
+              float f[8];
+#pragma unroll
+              for (int y = 0; y < 8; ++y) f[y] = l == 0.f ? 0.f : __uint_as_float(o[x + y]) * inv;
+              *reinterpret_cast<uint4*>(dst + j + x) = unpermute8(f);
             }
           }
         }
-        tc_fence_before_sync();
       } else {
-        more = next_segment(p, c, u1, nx);
+        float* slot = p.part + (int64_t)(g.slot * 2 + i) * kPart + row;
+#pragma unroll
+        for (int j = 0; j < D; j += 32) {
+          uint32_t o[32];
+          tmem_ld_x32(o_t + j, o);
+          tmem_ld_wait();
+#pragma unroll
+          for (int x = 0; x < 32; ++x) __stcg(slot + (j + x) * 128, __uint_as_float(o[x]));
+        }
+        __stcg(slot + D * 128, m);
+        __stcg(slot + (D + 1) * 128, l);
       }
+      tc_fence_before_sync();
       g = nx;
     }
     if (!ok && lane == 0) fail(p);
@@ -699,7 +735,54 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
-  if (warp == 12) tmem_dealloc(tmem, 512);
+  if (warp == 16) tmem_dealloc(tmem, 512);
+}
+
+// Joins the partial results of an item that several CTAs share, in their
+// order: block (CTA that starts the item, 32 rows), a row a lane, D / 8
+// columns a warp. Bound by the partial results' bytes, which come from L2.
+template <int D>
+__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ PrefillParams p) {
+  constexpr int kPart = (D + 2) * 128;
+  constexpr int N = D / 8;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int64_t first = blockIdx.x;
+  const Join j = p.joins[first];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+  const int in_item = blockIdx.y * kJoinRows + lane, half = in_item / 128;
+  if (blockIdx.y * kJoinRows >= (j.parts ? j.rows : 0)) return;
+  const float sl = fmaxf(fabsf(p.a.scale_log2), 1e-30f);
+  auto part = [&](int x) { return p.part + (((first + x) * 2 + (x == 0)) * 2 + half) * kPart + in_item % 128; };
+  float M = -INFINITY;
+  for (int x = 0; x < j.parts; ++x) M = fmaxf(M, __ldcg(part(x) + D * 128));
+  float L = 0.f, o[N];
+#pragma unroll
+  for (int y = 0; y < N; ++y) o[y] = 0.f;
+#pragma unroll 2
+  for (int x = 0; x < j.parts; ++x) {
+    const float* q = part(x);
+    const float m = __ldcg(q + D * 128), l = __ldcg(q + (D + 1) * 128);
+    float v[N];
+#pragma unroll
+    for (int y = 0; y < N; ++y) v[y] = __ldcg(q + (warp * N + y) * 128);
+    // a share in which the row saw nothing but NaN keeps l and its sums as they are
+    const float f = m == -INFINITY ? (l == 0.f ? 0.f : 1.f) : ex2((m - M) * sl);
+    L = fmaf(f, l, L);
+#pragma unroll
+    for (int y = 0; y < N; ++y) o[y] = l == 0.f ? o[y] : fmaf(f, v[y], o[y]);
+  }
+  if (in_item >= j.rows) return;
+  const float inv = L == 0.f ? 0.f : 1.f / L;
+  const unsigned R = j.r0 + in_item, tok = R / (unsigned)p.v.group;
+  __nv_bfloat16* dst = p.a.out + (int64_t)(j.row + tok) * p.a.ld_out +
+                       (int64_t)(j.h * p.v.group + R - tok * p.v.group) * D + warp * N;
+#pragma unroll
+  for (int x = 0; x < N; x += 8) {
+    float f[8];
+#pragma unroll
+    for (int y = 0; y < 8; ++y) f[y] = o[x + y] * inv;
+    *reinterpret_cast<uint4*>(dst + x) = unpermute8(f);
+  }
 }
 
 template <int D>
@@ -710,7 +793,18 @@ spear_status_t launch(const spear_kv_s* h, PrefillParams& p, cudaStream_t stream
   const size_t used = kHeader + 6 * (size_t)kTile * D * 2 + 2 * (size_t)kBlocksPerTile * 16 * (D + 8);
   const size_t smem = used > 116 * 1024 ? used : 116 * 1024;
   prefill_kernel<D><<<h->sm_count, kThreads, smem, stream>>>(p);
-  return cudaGetLastError() == cudaSuccess ? SPEAR_OK : SPEAR_ERR_CUDA;
+  if (cudaGetLastError() != cudaSuccess) return SPEAR_ERR_CUDA;
+  // launched ahead, so that it starts as soon as the last CTA ends
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(h->sm_count, kRows / kJoinRows);
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, join_kernel<D>, p) == cudaSuccess ? SPEAR_OK : SPEAR_ERR_CUDA;
 }
 
 }  // namespace
@@ -718,18 +812,17 @@ spear_status_t launch(const spear_kv_s* h, PrefillParams& p, cudaStream_t stream
 
 using namespace spear;
 
-size_t kv_prefill_workspace(const spear_kv_s* h) {
-  return (size_t)h->sm_count * 4 * (h->view.D + 2) * 128 * sizeof(float);
-}
+static size_t part_bytes(const spear_kv_s* h) { return (size_t)h->sm_count * 4 * (h->view.D + 2) * 128 * sizeof(float); }
 
-spear_status_t kv_launch_prefill(const spear_kv_s* h, const KvAttnArgs& a, int max_rows, float* part,
-                                 unsigned* counters, cudaStream_t stream) {
+size_t kv_prefill_workspace(const spear_kv_s* h) { return part_bytes(h) + (size_t)h->sm_count * sizeof(Join); }
+
+spear_status_t kv_launch_prefill(const spear_kv_s* h, const KvAttnArgs& a, int max_rows, void* ws, cudaStream_t stream) {
   PrefillParams p;
   p.v = h->view;
   p.a = a;
   p.max_rows = max_rows;
-  p.part = part;
-  p.counters = counters;
+  p.part = static_cast<float*>(ws);
+  p.joins = reinterpret_cast<Join*>(static_cast<char*>(ws) + part_bytes(h));
   p.wait_ns = 100000000ull;
   return h->view.D == 128 ? launch<128>(h, p, stream) : launch<64>(h, p, stream);
 }
