@@ -46,7 +46,7 @@ constexpr int kDeqWarps = 8;
 constexpr int kTile = 128;            // keys of a unit
 constexpr int kRows = 256;            // rows of an item
 constexpr int kBlocksPerTile = kTile / 16;
-constexpr int kItemCost = 2;          // units
+constexpr int kItemCost = 4;          // units
 constexpr int kHeader = 1024;         // barriers, segments
 constexpr int kSegs = 4;              // segments in flight
 constexpr int kSegReaders = 8 + kDeqWarps + 2 + 1;  // warps that read each segment
