@@ -60,11 +60,6 @@ struct DecodeParams {
   uint64_t wait_ns;
 };
 
-// Row r of 16 keys of an MMA tile is key kpi(r) of its block: lanes that read
-// K rows (2 i, 2 i + 1 of a quarter warp) then meet rows of both parities, and
-// those that read V rows (2 t, 2 t + 1) rows t and (t + 4) ^ 1: fewer bank conflicts.
-SPEAR_DEVINL int kpi(int r) { return (r & 1) ? ((r >> 1) + 4) ^ 1 : r >> 1; }
-
 template <int N>
 SPEAR_DEVINL void lds_words(uint32_t addr, uint32_t (&w)[N]) {
   static_assert(N == 1 || N == 2 || N == 4, "");
@@ -76,9 +71,22 @@ SPEAR_DEVINL void lds_words(uint32_t addr, uint32_t (&w)[N]) {
     asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(addr));
 }
 
-SPEAR_DEVINL uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
+SPEAR_DEVINL void ldmatrix_x4_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+
+// D = A(16x16, row) * B(16x8, col) + C, f16 inputs, fp32 accumulate.
+SPEAR_DEVINL void mma_f16_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+SPEAR_DEVINL uint32_t pack_f16x2(float lo, float up) {
   uint32_t r;
-  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(up), "f"(lo));
   return r;
 }
 
@@ -223,7 +231,6 @@ __global__ void __launch_bounds__(kThreads, 4 / NT > 3 ? 3 : 4 / NT)
 
   // ---------------------------------------------------------------- consumers
   const int g = lane >> 2, t = lane & 3;
-  const int kA = kpi(g), vA = kpi(2 * t), vB = kpi(2 * t + 1);
   const uint32_t c_lo = 0xBD80BD80u;  // -8 * 2^-7
   const uint32_t c_hi = 0xBF80BF80u;  // -8 * 2^-3
   int st = 0;
@@ -231,13 +238,13 @@ __global__ void __launch_bounds__(kThreads, 4 / NT > 3 ? 3 : 4 / NT)
   bool bad = false;
 
   for (int64_t u = u0; u < u1;) {
-    const int64_t len = min((int64_t)(c.s.tiles - c.tile), u1 - u);
+    const int len = (int)min((int64_t)(c.s.tiles - c.tile), u1 - u);
     const KvSeq s = c.s;
     const int rows = s.n * p.v.group;
 
-    // the rows as B fragments, and their sums
+    // the rows as f16 B fragments, their sums and their scales
     uint32_t qf[NT][D / 16][2];
-    float qs[NT][2];
+    float qs[NT][2], qi[NT][2];
     int hi[NT][2];  // last visible key of this lane's columns 2 t, 2 t + 1
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -251,22 +258,45 @@ __global__ void __launch_bounds__(kThreads, 4 / NT > 3 ? 3 : 4 / NT)
 #pragma unroll
         for (int i = 0; i < KW; ++i) w[i] = reinterpret_cast<const uint4*>(src)[i];
       }
-      float x = 0.f;
+      float x = 0.f, top = 0.f;
 #pragma unroll
       for (int i = 0; i < KW; ++i) {
         const uint32_t e[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
 #pragma unroll
-        for (int k = 0; k < 4; ++k) x += __uint_as_float(e[k] << 16) + __uint_as_float(e[k] & 0xFFFF0000u);
-        qf[nt][2 * i][0] = prmt(e[0], e[2], 0x5410);
-        qf[nt][2 * i][1] = prmt(e[0], e[2], 0x7632);
-        qf[nt][2 * i + 1][0] = prmt(e[1], e[3], 0x5410);
-        qf[nt][2 * i + 1][1] = prmt(e[1], e[3], 0x7632);
+        for (int k = 0; k < 4; ++k) {
+          const float lo = __uint_as_float(e[k] << 16), up = __uint_as_float(e[k] & 0xFFFF0000u);
+          x += lo + up;
+          top = fmaxf(top, fmaxf(fabsf(lo), fabsf(up)));
+        }
       }
-      x += __shfl_xor_sync(0xffffffffu, x, 1);
-      x += __shfl_xor_sync(0xffffffffu, x, 2);
+#pragma unroll
+      for (int o = 1; o < 4; o <<= 1) {
+        x += __shfl_xor_sync(0xffffffffu, x, o);
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      }
+      // a power of two that brings the row's largest element to 128 .. 256
+      const uint32_t es = min(261u - (__float_as_uint(top) >> 23), 254u);
+      const float up2 = __uint_as_float(es << 23), down = __uint_as_float((254u - es) << 23);
+#pragma unroll
+      for (int i = 0; i < KW; ++i) {
+        const uint32_t e[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+        // elements (j, j + 4) meet nibbles j and j + 4, the odd ones of which read 16 times as large
+        auto pair = [&](int j) {
+          const float f = (j & 1) ? up2 * 0.0625f : up2;
+          const uint32_t a = e[j / 2], b = e[j / 2 + 2];
+          return pack_f16x2(f * __uint_as_float((j & 1) ? a & 0xFFFF0000u : a << 16),
+                            f * __uint_as_float((j & 1) ? b & 0xFFFF0000u : b << 16));
+        };
+        qf[nt][2 * i][0] = pair(0);
+        qf[nt][2 * i][1] = pair(1);
+        qf[nt][2 * i + 1][0] = pair(2);
+        qf[nt][2 * i + 1][1] = pair(3);
+      }
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        qs[nt][k] = __shfl_sync(0xffffffffu, x, (2 * t + k) * 4);
+        qs[nt][k] = __shfl_sync(0xffffffffu, x, (2 * t + k) * 4) * p.a.scale_log2;
+        // codes read as c 2^-24
+        qi[nt][k] = __shfl_sync(0xffffffffu, down, (2 * t + k) * 4) * (16777216.f * p.a.scale_log2);
         hi[nt][k] = s.L - s.n + min((nt * 8 + 2 * t + k) / p.v.group, s.n - 1);
       }
     }
@@ -282,14 +312,16 @@ __global__ void __launch_bounds__(kThreads, 4 / NT > 3 ? 3 : 4 / NT)
       for (int k = 0; k < 2; ++k) m[nt][k] = -INFINITY, l[nt][k] = 0.f, off[nt][k] = 0.f;
     }
 
-    for (int64_t i = 0; i < len; ++i) {
-      const int key0 = (s.lo + c.tile + (int)i) * kTile + warp * 32;
+    for (int i = 0; i < len; ++i) {
+      const int key0 = (s.lo + c.tile + i) * kTile + warp * 32;
       if (!bad && !mbar_wait_bounded(full + st, phase, p.wait_ns)) {
         bad = true;
         if (lane == 0) atomicOr(p.v.status, kStatusTimeoutPipe);
       }
       bad = __any_sync(0xffffffffu, bad);
       const uint32_t base = stages_at + st * p.stage_bytes + warp * 2 * BB;
+      // this lane's row of the four 8 x 8 matrices of 16-bit words: key lane % 16 (its low 8 first), chunk lane / 8 % 2
+      const uint32_t vrow = base + 8 * D + ((lane & 7) + (lane >> 4) * 8) * (D / 2) + ((lane >> 3) & 1) * 16;
       if (!bad && key0 < s.L) {
         float sc[2][NT][4];
         // ---- scores
@@ -297,30 +329,28 @@ __global__ void __launch_bounds__(kThreads, 4 / NT > 3 ? 3 : 4 / NT)
         for (int mt = 0; mt < 2; ++mt) {
           const uint32_t blk = base + mt * BB;
           uint32_t wa[KW], wb[KW];
-          lds_words(blk + kA * (D / 2) + t * (D / 8), wa);
-          lds_words(blk + (8 + kA) * (D / 2) + t * (D / 8), wb);
+          lds_words(blk + g * (D / 2) + t * (D / 8), wa);
+          lds_words(blk + (8 + g) * (D / 2) + t * (D / 8), wb);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) sc[mt][nt][e] = -128.f * qs[nt][e & 1];
+            for (int e = 0; e < 4; ++e) sc[mt][nt][e] = 0.f;
 #pragma unroll
           for (int j = 0; j < D / 16; ++j) {
-            const int sh = (j & 1) * 8;
-            const uint32_t a[4] = {int4_pair_to_bf16x2_biased(wa[j / 2] >> sh), int4_pair_to_bf16x2_biased(wb[j / 2] >> sh),
-                                   int4_pair_to_bf16x2_biased(wa[j / 2] >> (sh + 4)),
-                                   int4_pair_to_bf16x2_biased(wb[j / 2] >> (sh + 4))};
+            const uint32_t x = (j & 1) ? wa[j / 2] >> 8 : wa[j / 2], y = (j & 1) ? wb[j / 2] >> 8 : wb[j / 2];
+            const uint32_t a[4] = {x & 0x000F000Fu, y & 0x000F000Fu, x & 0x00F000F0u, y & 0x00F000F0u};
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma_bf16_16816(sc[mt][nt], a, qf[nt][j][0], qf[nt][j][1]);
+            for (int nt = 0; nt < NT; ++nt) mma_f16_16816(sc[mt][nt], a, qf[nt][j][0], qf[nt][j][1]);
           }
-          const uint32_t pa = lds32(blk + 16 * D + 4 * kA), pb = lds32(blk + 16 * D + 4 * (8 + kA));
-          const float s0 = __uint_as_float(pa << 16) * p.a.scale_log2, o0 = __uint_as_float(pa & 0xFFFF0000u) * p.a.scale_log2;
-          const float s1 = __uint_as_float(pb << 16) * p.a.scale_log2, o1 = __uint_as_float(pb & 0xFFFF0000u) * p.a.scale_log2;
+          const uint32_t pa = lds32(blk + 16 * D + 4 * g), pb = lds32(blk + 16 * D + 4 * (8 + g));
+          const float s0 = __uint_as_float(pa << 16), o0 = __uint_as_float(pa & 0xFFFF0000u);
+          const float s1 = __uint_as_float(pb << 16), o1 = __uint_as_float(pb & 0xFFFF0000u);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            sc[mt][nt][0] = fmaf(s0, sc[mt][nt][0], o0 * qs[nt][0]);
-            sc[mt][nt][1] = fmaf(s0, sc[mt][nt][1], o0 * qs[nt][1]);
-            sc[mt][nt][2] = fmaf(s1, sc[mt][nt][2], o1 * qs[nt][0]);
-            sc[mt][nt][3] = fmaf(s1, sc[mt][nt][3], o1 * qs[nt][1]);
+            sc[mt][nt][0] = fmaf(s0 * qi[nt][0], sc[mt][nt][0], o0 * qs[nt][0]);
+            sc[mt][nt][1] = fmaf(s0 * qi[nt][1], sc[mt][nt][1], o0 * qs[nt][1]);
+            sc[mt][nt][2] = fmaf(s1 * qi[nt][0], sc[mt][nt][2], o1 * qs[nt][0]);
+            sc[mt][nt][3] = fmaf(s1 * qi[nt][1], sc[mt][nt][3], o1 * qs[nt][1]);
           }
         }
         // ---- mask, where some row does not see all 32 keys
@@ -333,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 4 / NT > 3 ? 3 : 4 / NT)
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                const int key = key0 + mt * 16 + kA + 8 * (e >> 1), last = hi[nt][e & 1];
+                const int key = key0 + mt * 16 + g + 8 * (e >> 1), last = hi[nt][e & 1];
                 see[mt][nt][e] = key <= last && (p.a.window == 0 || key > last - p.a.window);
                 if (!see[mt][nt][e]) sc[mt][nt][e] = -INFINITY;
               }
@@ -365,11 +395,16 @@ __global__ void __launch_bounds__(kThreads, 4 / NT > 3 ? 3 : 4 / NT)
               for (int j = 0; j < D / 16; ++j) acc[j][nt][k] *= f, acc[j][nt][k + 2] *= f;
             }
         }
+        float mu[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) mu[nt][k] = m[nt][k] == -INFINITY ? 0.f : m[nt][k];
         // ---- weights, and the values
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt) {
           const uint32_t blk = base + mt * BB;
-          const uint32_t pa = lds32(blk + 16 * D + 64 + 4 * kA), pb = lds32(blk + 16 * D + 64 + 4 * (8 + kA));
+          const uint32_t pa = lds32(blk + 16 * D + 64 + 4 * g), pb = lds32(blk + 16 * D + 64 + 4 * (8 + g));
           const float vs[2] = {__uint_as_float(pa << 16), __uint_as_float(pb << 16)};
           const float vo[2] = {fmaf(8.f, vs[0], __uint_as_float(pa & 0xFFFF0000u)),
                                fmaf(8.f, vs[1], __uint_as_float(pb & 0xFFFF0000u))};
@@ -380,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, 4 / NT > 3 ? 3 : 4 / NT)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const int k = e & 1, y = e >> 1;
-              const float pe = ex2(sc[mt][nt][e] - (m[nt][k] == -INFINITY ? 0.f : m[nt][k]));
+              const float pe = ex2(sc[mt][nt][e] - mu[nt][k]);
               l[nt][k] += pe;
               w[e] = pe * vs[y];
               float o = pe * vo[y];
@@ -390,19 +425,17 @@ __global__ void __launch_bounds__(kThreads, 4 / NT > 3 ? 3 : 4 / NT)
             bf[nt][0] = movmatrix(pack_bf16x2(w[0], w[1]));
             bf[nt][1] = movmatrix(pack_bf16x2(w[2], w[3]));
           }
-          uint32_t va[VW], vb[VW], vc[VW], vd[VW];
-          const uint32_t vrow = blk + 8 * D + g * (D / 16);
-          lds_words(vrow + vA * (D / 2), va);
-          lds_words(vrow + vB * (D / 2), vb);
-          lds_words(vrow + (8 + vA) * (D / 2), vc);
-          lds_words(vrow + (8 + vB) * (D / 2), vd);
 #pragma unroll
           for (int i2 = 0; i2 < VW; ++i2) {
+            // 8 keys x 32 channels each: keys 0..7 and 8..15 of two neighbouring 16-byte chunks; a register holds
+            // four channels of keys 2 t and 2 t + 1
+            uint32_t y[4];
+            ldmatrix_x4_trans(y, vrow + mt * BB + i2 * 32);
             uint32_t f0[4], f1[4], f2[4], f3[4];
-            decode_frag_unpack(prmt(va[i2], vb[i2], 0x5410), c_lo, c_hi, f0);
-            decode_frag_unpack(prmt(va[i2], vb[i2], 0x7632), c_lo, c_hi, f1);
-            decode_frag_unpack(prmt(vc[i2], vd[i2], 0x5410), c_lo, c_hi, f2);
-            decode_frag_unpack(prmt(vc[i2], vd[i2], 0x7632), c_lo, c_hi, f3);
+            decode_frag_unpack(y[0], c_lo, c_hi, f0);
+            decode_frag_unpack(y[1], c_lo, c_hi, f1);
+            decode_frag_unpack(y[2], c_lo, c_hi, f2);
+            decode_frag_unpack(y[3], c_lo, c_hi, f3);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const uint32_t a[4] = {f0[j], f1[j], f2[j], f3[j]};
@@ -432,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, 4 / NT > 3 ? 3 : 4 / NT)
           ml[(warp * R + r) * 2] = m[nt][k];
           ml[(warp * R + r) * 2 + 1] = l[nt][k];
         }
-        float* dst = om + (warp * R + r) * OS + g * (D / 8);
+        float* dst = om + (warp * R + r) * OS + g * 4;
 #pragma unroll
         for (int i2 = 0; i2 < VW; ++i2)
 #pragma unroll
@@ -442,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, 4 / NT > 3 ? 3 : 4 / NT)
             o4.y = fmaf(acc[i2 * 4 + 1][nt][k + 2 * y], kFragScaleHi, off[nt][k]);
             o4.z = fmaf(acc[i2 * 4 + 2][nt][k + 2 * y], kFragScaleLo, off[nt][k]);
             o4.w = fmaf(acc[i2 * 4 + 3][nt][k + 2 * y], kFragScaleHi, off[nt][k]);
-            *reinterpret_cast<float4*>(dst + i2 * 8 + y * 4) = o4;
+            *reinterpret_cast<float4*>(dst + i2 * 64 + y * 32) = o4;
           }
       }
     consumer_sync();
@@ -519,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 4 / NT > 3 ? 3 : 4 / NT)
     }
     consumer_sync();  // the joined results have been read
     u += len;
-    c.tile += (int)len;
+    c.tile += len;
     if (u < u1) next_item(p, c);
   }
 }
