@@ -127,10 +127,19 @@ def _ptr(t) -> int | None:
     return None if t is None else t.data_ptr()
 
 
+_raw_stream = None  # torch's accessor of the current stream's handle, once torch is loaded
+
+
 def _stream(stream) -> int:
-    import torch
+    global _raw_stream
     if stream is None:
-        stream = torch.cuda.current_stream()
+        if _raw_stream is None:
+            import torch
+            # (device index) -> cudaStream_t; current_stream() builds a Stream object, 3 us a call
+            get, dev = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+            torch.cuda.current_stream()  # initialises CUDA
+            _raw_stream = (lambda: get(dev())) if get and dev else (lambda: torch.cuda.current_stream().cuda_stream)
+        return _raw_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -357,16 +366,18 @@ class SpearKVCache:
         self.n_heads, self.n_kv_heads, self.head_dim, self.page_size = n_heads, n_kv_heads, head_dim, page_size
         self._q_row, self._kv_row = (n_heads, head_dim), (n_kv_heads, head_dim)
         self._bf16, self._i64, self._i32 = torch.bfloat16, torch.int64, torch.int32
-        self._fns = L.spear_kv_append, L.spear_kv_read, L.spear_kv_attention
+        self._append, self._read, self._attention = L.spear_kv_append, L.spear_kv_read, L.spear_kv_attention
+        self._scale = head_dim ** -0.5
 
-    def _rows(self, x, row, what):
+    def _rows(self, x, T, row, what):
         """The token stride of bf16 [T][heads][D] with contiguous heads."""
-        if x.dtype is not self._bf16 or x.dim() != 3 or x.shape[1:] != row or not x.is_cuda:
-            raise ValueError(f"{what} must be CUDA bf16 [T][{row[0]}][{row[1]}]")
-        s = x.stride()
-        if s[2] != 1 or (s[1] != row[1] and row[0] > 1):
+        heads, D = row
+        if x.dtype is not self._bf16 or x.shape != (T, heads, D) or not x.is_cuda:
+            raise ValueError(f"{what} must be CUDA bf16 [{T}][{heads}][{D}]")
+        s0, s1, s2 = x.stride()
+        if s2 != 1 or (s1 != D and heads > 1):
             raise ValueError(f"{what}: the heads of a token must be contiguous")
-        return s[0] if x.shape[0] > 1 else max(s[0], row[0] * row[1])
+        return s0 if T > 1 else max(s0, heads * D)
 
     def _index(self, x, dtype, n, what):
         if x.dtype is not dtype or not x.is_cuda or not x.is_contiguous() or x.numel() < n:
@@ -378,29 +389,30 @@ class SpearKVCache:
         int64 ``positions`` and put k and v into the int64 ``slots`` (-1: not
         cached). The rotated queries go to ``q_out`` (default: q in place)."""
         T = k.shape[0]
-        if v.shape[0] != T or (q is not None and q.shape[0] != T):
-            raise ValueError("q, k and v must have the same number of tokens")
-        ldq = ldo = 0
+        row, kv_row, rows = self._q_row, self._kv_row, self._rows
+        qp = op = ldq = ldo = 0
         if q is not None:
             if q_out is None:
                 q_out = q
-            elif q_out.shape[0] != T:
-                raise ValueError("q_out must have as many tokens as q")
-            ldq, ldo = self._rows(q, self._q_row, "q"), self._rows(q_out, self._q_row, "q_out")
-        pos = None if self.rope_table is None else self._index(positions, self._i64, T, "positions")
-        _check(self._fns[0](self.h, _ptr(q), ldq, k.data_ptr(), self._rows(k, self._kv_row, "k"), v.data_ptr(),
-                            self._rows(v, self._kv_row, "v"), pos, self._index(slots, self._i64, T, "slots"), T,
-                            _ptr(q_out), ldo, _stream(stream)), "spear_kv_append")
+            qp, ldq, op, ldo = q.data_ptr(), rows(q, T, row, "q"), q_out.data_ptr(), rows(q_out, T, row, "q_out")
+        pos = 0 if self.rope_table is None else self._index(positions, self._i64, T, "positions")
+        st = self._append(self.h, qp, ldq, k.data_ptr(), rows(k, T, kv_row, "k"), v.data_ptr(), rows(v, T, kv_row, "v"),
+                          pos, self._index(slots, self._i64, T, "slots"), T, op, ldo, _stream(stream))
+        if st:
+            raise SpearError(st, "spear_kv_append")
         return q_out
 
     def read(self, slots, k_out, v_out, stream=None):
         """The cached keys and values of ``slots`` as bf16 [T][n_kv_heads][D]."""
         T = slots.shape[0]
-        for x, what in ((k_out, "k_out"), (v_out, "v_out")):
-            if x.dtype is not self._bf16 or x.shape != (T, *self._kv_row) or not x.is_cuda or not x.is_contiguous():
-                raise ValueError(f"{what} must be contiguous CUDA bf16 [{T}][n_kv_heads][head_dim]")
-        _check(self._fns[1](self.h, self._index(slots, self._i64, T, "slots"), T, k_out.data_ptr(), v_out.data_ptr(),
-                            _stream(stream)), "spear_kv_read")
+        shape = (T, *self._kv_row)
+        for x in (k_out, v_out):
+            if x.dtype is not self._bf16 or x.shape != shape or not x.is_cuda or not x.is_contiguous():
+                raise ValueError(f"k_out and v_out must be contiguous CUDA bf16 {list(shape)}")
+        st = self._read(self.h, self._index(slots, self._i64, T, "slots"), T, k_out.data_ptr(), v_out.data_ptr(),
+                        _stream(stream))
+        if st:
+            raise SpearError(st, "spear_kv_read")
         return k_out, v_out
 
     def attention(self, q, out, page_table, kv_lens, q_starts, max_q, scale=None, window=0, stream=None):
@@ -408,16 +420,17 @@ class SpearKVCache:
         into ``out`` (see spear_kv_attention): int32 ``page_table``
         [n_seqs][max pages], ``kv_lens`` [n_seqs], ``q_starts`` [n_seqs + 1];
         ``scale`` defaults to head_dim ** -0.5, ``window`` 0 means all earlier keys."""
-        T, n = q.shape[0], page_table.shape[0]
-        if out.shape[0] != T or page_table.dim() != 2:
-            raise ValueError("out must have as many tokens as q, page_table two dimensions")
-        _check(self._fns[2](self.h, q.data_ptr(), self._rows(q, self._q_row, "q"), out.data_ptr(),
-                            self._rows(out, self._q_row, "out"),
-                            self._index(page_table, self._i32, n, "page_table"), page_table.shape[1],
-                            self._index(kv_lens, self._i32, n, "kv_lens"),
-                            self._index(q_starts, self._i32, n + 1, "q_starts"), n, T, max_q,
-                            self.head_dim ** -0.5 if scale is None else scale, window, _stream(stream)),
-               "spear_kv_attention")
+        T = q.shape[0]
+        if page_table.dim() != 2:
+            raise ValueError("page_table must have two dimensions")
+        n, cols = page_table.shape
+        index, i32, row = self._index, self._i32, self._q_row
+        st = self._attention(self.h, q.data_ptr(), self._rows(q, T, row, "q"), out.data_ptr(),
+                             self._rows(out, T, row, "out"), index(page_table, i32, n, "page_table"), cols,
+                             index(kv_lens, i32, n, "kv_lens"), index(q_starts, i32, n + 1, "q_starts"), n, T, max_q,
+                             self._scale if scale is None else scale, window, _stream(stream))
+        if st:
+            raise SpearError(st, "spear_kv_attention")
         return out
 
     def check(self, stream=None) -> int:
