@@ -12,16 +12,19 @@
 //    a single token's few heads to 16 rows. (tcgen05 would want 128 rows of
 //    dequantised keys written to tensor or shared memory for 8 columns.)
 //  - K: four lanes hold a key's codes, D / 4 channels each, in the order of its
-//    bytes; a code pair becomes the bf16 pair (128 + c) with a mask and an
-//    exponent, the rows of q are permuted alike, and the accumulator starts at
-//    -128 sum(q), so that it ends as q . c. Then s = S (q . c) + O sum(q) with
-//    the key's scale S and offset O.
-//  - V: two keys' words are interleaved by two byte permutes, so that a register
-//    holds one channel of two keys, as the A operand of out^T = V^T p^T wants
-//    it. Codes enter centred, c - 8, exact in bf16 (small magnitudes: neither
-//    the fp32 sums nor the rounding of p S to bf16 lose to a large common
-//    term); sum p (O + 8 S) is kept beside it in fp32. The scores' accumulator
-//    layout becomes p^T's operand layout by one 8 x 8 transpose (movmatrix).
+//    bytes. A masked nibble, or byte, reads as an f16 subnormal, c 2^-24, which
+//    the MMA takes as it is: no arithmetic on K at all. A byte is lo + 16 hi, so
+//    q0 lo + q1 hi = (q0 - q1 / 16) lo + (q1 / 16) byte: four masks a word. The
+//    rows of q are scaled by a power of two into f16, once a segment. Then s =
+//    S (q . c) + O sum(q) with the key's scale S and offset O.
+//  - V: transposed matrix loads of 16-bit words put four channels of two keys
+//    in a register, as the A operand of out^T = V^T p^T wants it; again the low
+//    nibbles and whole bytes enter, and the high nibbles are their difference,
+//    taken at the end. Codes are centred, lo - 8 and byte - 136, exact in bf16
+//    (small magnitudes: neither the fp32 sums nor the rounding of p S to bf16
+//    lose to a large common term); sum p (O + 8 S) is kept beside it in fp32.
+//    The scores' accumulator layout becomes p^T's operand layout by one 8 x 8
+//    transpose (movmatrix).
 //  - The running maximum is lazy: p = 2^(s - m) with any m that is at most 8
 //    below the maximum; sums are only rescaled when some score passes m + 8.
 //
@@ -35,7 +38,10 @@
 // A CTA: four warps, 32 keys of a tile each with a state of their own, joined
 // at the end of a segment; a fifth warp copies the tiles' 16-token blocks (one
 // bulk copy each, whatever the page size) into a ring of stages.
+#include <cuda_fp16.h>
+
 #include <atomic>
+#include <type_traits>
 
 #include "kv_device.cuh"
 
@@ -47,6 +53,7 @@ constexpr int kThreads = 32 * (kWarps + 1);
 constexpr int kTile = 32 * kWarps;             // keys of a unit
 constexpr int kBlocksPerTile = kTile / 16;
 constexpr int kMaxStages = 16;
+constexpr int kMinUnits = 3;                   // a CTA's, where there are few: joining costs as much as two more tiles
 constexpr float kLazy = 8.f;
 
 struct DecodeParams {
@@ -84,11 +91,21 @@ SPEAR_DEVINL void mma_f16_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// The same with C = 0.
+SPEAR_DEVINL void mma_f16_16816_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 SPEAR_DEVINL uint32_t pack_f16x2(float lo, float up) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(up), "f"(lo));
   return r;
 }
+
+// Bytes 1 and 3 of x as two 16-bit halves.
+SPEAR_DEVINL uint32_t odd_bytes(uint32_t x) { return __byte_perm(x, 0, 0x4341); }
 
 SPEAR_DEVINL uint32_t movmatrix(uint32_t x) {
   uint32_t r;
@@ -119,6 +136,15 @@ SPEAR_DEVINL void next_item(const DecodeParams& p, Cursor& c) {
   } while (seq_units(p, c.s) == 0);
 }
 
+SPEAR_DEVINL int64_t scan_inclusive(int64_t x, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  return x;
+}
+
 template <int D, int NT>
 __global__ void __launch_bounds__(kThreads, 4 / NT > 3 ? 3 : 4 / NT)
     decode_kernel(const __grid_constant__ DecodeParams p) {
@@ -132,7 +158,7 @@ __global__ void __launch_bounds__(kThreads, 4 / NT > 3 ? 3 : 4 / NT)
   extern __shared__ __align__(128) uint8_t smem[];
   uint64_t* full = reinterpret_cast<uint64_t*>(smem);
   uint64_t* empty = full + kMaxStages;
-  int64_t* scan = reinterpret_cast<int64_t*>(empty + kMaxStages);  // [kWarps + 1] warp sums, total, unit of the start
+  int64_t* scan = reinterpret_cast<int64_t*>(empty + kMaxStages);  // [kWarps + 1] sums
   int* found = reinterpret_cast<int*>(scan + 8);
   float* ml = reinterpret_cast<float*>(smem + 512);                // [kWarps][R][2]
   float* om = ml + kWarps * R * 2;                                 // [kWarps][R][OS]
@@ -148,46 +174,54 @@ __global__ void __launch_bounds__(kThreads, 4 / NT > 3 ? 3 : 4 / NT)
     fence_mbar_init();
   }
 
-  // ---- this CTA's units [u0, u1)
-  int64_t sum = 0;
-  for (int b = tid; b < p.a.n_seqs; b += kThreads) sum += seq_units(p, kv_seq(p.v, p.a, b, kTile));
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (lane == 0) scan[warp] = sum;
-  __syncthreads();
-  int64_t U = 0;
-#pragma unroll
-  for (int w = 0; w <= kWarps; ++w) U += scan[w];
-  const int64_t G = min((int64_t)gridDim.x, U);
+  // ---- this CTA's units [u0, u1) and the item that u0 falls into; every warp on its own for up to 32 sequences,
+  // so that nothing waits
+  Cursor c;
+  int64_t U = 0, G, u0, u1, at;
   const int64_t cta = blockIdx.x;
-  if (cta >= G) return;
-  const int64_t u0 = cta * U / G, u1 = (cta + 1) * U / G;
-  // the sequence that u0 falls into
-  if (warp == 0) {
+  auto share = [&] {
+    G = min((int64_t)gridDim.x, (U + kMinUnits - 1) / kMinUnits);
+    const int64_t x = G > 0 ? (cta + (lane & 1)) * U / G : 0;
+    u0 = __shfl_sync(0xffffffffu, x, 0);
+    u1 = __shfl_sync(0xffffffffu, x, 1);
+  };
+  if (p.a.n_seqs <= 32) {
+    if (lane < p.a.n_seqs) c.s = kv_seq(p.v, p.a, lane, kTile);
+    const int64_t own = lane < p.a.n_seqs ? seq_units(p, c.s) : 0, incl = scan_inclusive(own, lane);
+    U = __shfl_sync(0xffffffffu, incl, 31);
+    share();
+    c.b = __ffs(__ballot_sync(0xffffffffu, u0 < incl)) - 1;
+    at = u0 - __shfl_sync(0xffffffffu, incl - own, c.b & 31);
+    __syncthreads();  // the barriers are in place
+    if (cta >= G) return;
+  } else {
+    for (int b = tid; b < p.a.n_seqs; b += kThreads) U += seq_units(p, kv_seq(p.v, p.a, b, kTile));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) U += __shfl_xor_sync(0xffffffffu, U, o);
+    if (lane == 0) scan[warp] = U;
+    __syncthreads();
+    U = 0;
+#pragma unroll
+    for (int w = 0; w <= kWarps; ++w) U += scan[w];
+    share();
+    if (cta >= G) return;
     int64_t before = 0;
-    for (int b0 = 0; b0 < p.a.n_seqs; b0 += 32) {
+    for (int b0 = 0;; b0 += 32) {
       const int b = b0 + lane;
       const int64_t own = b < p.a.n_seqs ? seq_units(p, kv_seq(p.v, p.a, b, kTile)) : 0;
-      int64_t incl = own;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t x = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += x;
+      const int64_t incl = before + scan_inclusive(own, lane);
+      before = __shfl_sync(0xffffffffu, incl, 31);
+      if (u0 < before) {
+        const int l = __ffs(__ballot_sync(0xffffffffu, u0 < incl)) - 1;
+        c.b = b0 + l;
+        at = u0 - __shfl_sync(0xffffffffu, incl - own, l);
+        break;
       }
-      if (own > 0 && u0 >= before + incl - own && u0 < before + incl) {
-        found[0] = b;
-        scan[5] = u0 - (before + incl - own);
-      }
-      before += __shfl_sync(0xffffffffu, incl, 31);
-      if (before > u0) break;
     }
   }
-  __syncthreads();
-  Cursor c;
-  c.b = found[0];
   c.s = kv_seq(p.v, p.a, c.b, kTile);
-  c.h = (int)(scan[5] / c.s.tiles);
-  c.tile = (int)(scan[5] % c.s.tiles);
+  c.h = (int)((uint64_t)at / (unsigned)c.s.tiles);
+  c.tile = (int)(at - (int64_t)c.h * c.s.tiles);
 
   if (warp == kWarps) {
     // ---------------------------------------------------------------- producer
@@ -231,8 +265,8 @@ __global__ void __launch_bounds__(kThreads, 4 / NT > 3 ? 3 : 4 / NT)
 
   // ---------------------------------------------------------------- consumers
   const int g = lane >> 2, t = lane & 3;
-  const uint32_t c_lo = 0xBD80BD80u;  // -8 * 2^-7
-  const uint32_t c_hi = 0xBF80BF80u;  // -8 * 2^-3
+  const uint32_t c_lo = 0xBD80BD80u;    // -8 * 2^-7
+  const uint32_t c_byte = 0xBF88BF88u;  // -136 * 2^-7
   int st = 0;
   unsigned phase = 0;
   bool bad = false;
@@ -280,12 +314,15 @@ __global__ void __launch_bounds__(kThreads, 4 / NT > 3 ? 3 : 4 / NT)
 #pragma unroll
       for (int i = 0; i < KW; ++i) {
         const uint32_t e[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-        // elements (j, j + 4) meet nibbles j and j + 4, the odd ones of which read 16 times as large
+        // elements (j, j + 4) and (j + 1, j + 5), j even, meet lo and lo + 16 hi: q0 lo + q1 hi = (q0 - q1 / 16) lo +
+        // (q1 / 16) (lo + 16 hi), the difference taken with what f16 holds of q1 / 16
         auto pair = [&](int j) {
-          const float f = (j & 1) ? up2 * 0.0625f : up2;
           const uint32_t a = e[j / 2], b = e[j / 2 + 2];
-          return pack_f16x2(f * __uint_as_float((j & 1) ? a & 0xFFFF0000u : a << 16),
-                            f * __uint_as_float((j & 1) ? b & 0xFFFF0000u : b << 16));
+          const uint32_t odd = pack_f16x2(up2 * 0.0625f * __uint_as_float(a & 0xFFFF0000u),
+                                          up2 * 0.0625f * __uint_as_float(b & 0xFFFF0000u));
+          if (j & 1) return odd;
+          const float2 o = __half22float2(*reinterpret_cast<const __half2*>(&odd));
+          return pack_f16x2(fmaf(up2, __uint_as_float(a << 16), -o.x), fmaf(up2, __uint_as_float(b << 16), -o.y));
         };
         qf[nt][2 * i][0] = pair(0);
         qf[nt][2 * i][1] = pair(1);
@@ -322,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 4 / NT > 3 ? 3 : 4 / NT)
       const uint32_t base = stages_at + st * p.stage_bytes + warp * 2 * BB;
       // this lane's row of the four 8 x 8 matrices of 16-bit words: key lane % 16 (its low 8 first), chunk lane / 8 % 2
       const uint32_t vrow = base + 8 * D + ((lane & 7) + (lane >> 4) * 8) * (D / 2) + ((lane >> 3) & 1) * 16;
-      if (!bad && key0 < s.L) {
+      auto tile = [&](auto masked) {
         float sc[2][NT][4];
         // ---- scores
 #pragma unroll
@@ -332,15 +369,18 @@ __global__ void __launch_bounds__(kThreads, 4 / NT > 3 ? 3 : 4 / NT)
           lds_words(blk + g * (D / 2) + t * (D / 8), wa);
           lds_words(blk + (8 + g) * (D / 2) + t * (D / 8), wb);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) sc[mt][nt][e] = 0.f;
-#pragma unroll
           for (int j = 0; j < D / 16; ++j) {
-            const uint32_t x = (j & 1) ? wa[j / 2] >> 8 : wa[j / 2], y = (j & 1) ? wb[j / 2] >> 8 : wb[j / 2];
-            const uint32_t a[4] = {x & 0x000F000Fu, y & 0x000F000Fu, x & 0x00F000F0u, y & 0x00F000F0u};
+            // bytes 0 and 2, or 1 and 3, of the word as lo + 16 hi, and lo
+            const uint32_t x = j & 1 ? odd_bytes(wa[j / 2]) : wa[j / 2] & 0x00FF00FFu;
+            const uint32_t y = j & 1 ? odd_bytes(wb[j / 2]) : wb[j / 2] & 0x00FF00FFu;
+            const uint32_t a[4] = {x & 0x000F000Fu, y & 0x000F000Fu, x, y};
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma_f16_16816(sc[mt][nt], a, qf[nt][j][0], qf[nt][j][1]);
+            for (int nt = 0; nt < NT; ++nt) {
+              if (j == 0)
+                mma_f16_16816_first(sc[mt][nt], a, qf[nt][j][0], qf[nt][j][1]);
+              else
+                mma_f16_16816(sc[mt][nt], a, qf[nt][j][0], qf[nt][j][1]);
+            }
           }
           const uint32_t pa = lds32(blk + 16 * D + 4 * g), pb = lds32(blk + 16 * D + 4 * (8 + g));
           const float s0 = __uint_as_float(pa << 16), o0 = __uint_as_float(pa & 0xFFFF0000u);
@@ -353,10 +393,8 @@ __global__ void __launch_bounds__(kThreads, 4 / NT > 3 ? 3 : 4 / NT)
             sc[mt][nt][3] = fmaf(s1 * qi[nt][1], sc[mt][nt][3], o1 * qs[nt][1]);
           }
         }
-        // ---- mask, where some row does not see all 32 keys
-        const bool masked = key0 + 31 > s.L - s.n || (p.a.window > 0 && key0 <= s.L - 1 - p.a.window);
         bool see[2][NT][4];
-        if (masked) {
+        if constexpr (masked) {
 #pragma unroll
           for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
@@ -419,7 +457,9 @@ __global__ void __launch_bounds__(kThreads, 4 / NT > 3 ? 3 : 4 / NT)
               l[nt][k] += pe;
               w[e] = pe * vs[y];
               float o = pe * vo[y];
-              if (masked && !see[mt][nt][e]) w[e] = 0.f, o = 0.f;  // 0 x NaN of a key that the row does not see
+              if constexpr (masked) {
+                if (!see[mt][nt][e]) w[e] = 0.f, o = 0.f;  // 0 x NaN of a key that the row does not see
+              }
               off[nt][k] += o;
             }
             bf[nt][0] = movmatrix(pack_bf16x2(w[0], w[1]));
@@ -431,19 +471,27 @@ __global__ void __launch_bounds__(kThreads, 4 / NT > 3 ? 3 : 4 / NT)
             // four channels of keys 2 t and 2 t + 1
             uint32_t y[4];
             ldmatrix_x4_trans(y, vrow + mt * BB + i2 * 32);
-            uint32_t f0[4], f1[4], f2[4], f3[4];
-            decode_frag_unpack(y[0], c_lo, c_hi, f0);
-            decode_frag_unpack(y[1], c_lo, c_hi, f1);
-            decode_frag_unpack(y[2], c_lo, c_hi, f2);
-            decode_frag_unpack(y[3], c_lo, c_hi, f3);
+            // even j: the low nibble of byte j / 2, lo - 8; odd j: all of the byte, lo + 16 hi - 136 (exact in bf16)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              const uint32_t a[4] = {f0[j], f1[j], f2[j], f3[j]};
+              uint32_t a[4];
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                const uint32_t byte = j < 2 ? y[x] & 0x00FF00FFu : odd_bytes(y[x]);
+                a[x] = bf16x2_fma(j & 1 ? byte : byte & 0x000F000Fu, 0x7E807E80u /* 2^126 */, j & 1 ? c_byte : c_lo);
+              }
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) mma_bf16_16816(acc[i2 * 4 + j][nt], a, bf[nt][0], bf[nt][1]);
             }
           }
         }
+      };
+      if (!bad && key0 < s.L) {
+        // does some row not see all 32 keys?
+        if (key0 + 31 > s.L - s.n || (p.a.window > 0 && key0 <= s.L - 1 - p.a.window))
+          tile(std::true_type{});
+        else
+          tile(std::false_type{});
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(empty + st);
@@ -471,10 +519,12 @@ __global__ void __launch_bounds__(kThreads, 4 / NT > 3 ? 3 : 4 / NT)
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
             float4 o4;
-            o4.x = fmaf(acc[i2 * 4][nt][k + 2 * y], kFragScaleLo, off[nt][k]);
-            o4.y = fmaf(acc[i2 * 4 + 1][nt][k + 2 * y], kFragScaleHi, off[nt][k]);
-            o4.z = fmaf(acc[i2 * 4 + 2][nt][k + 2 * y], kFragScaleLo, off[nt][k]);
-            o4.w = fmaf(acc[i2 * 4 + 3][nt][k + 2 * y], kFragScaleHi, off[nt][k]);
+            const int e = k + 2 * y;
+            const float a0 = acc[i2 * 4][nt][e], a2 = acc[i2 * 4 + 2][nt][e];
+            o4.x = fmaf(a0, 128.f, off[nt][k]);
+            o4.y = fmaf(acc[i2 * 4 + 1][nt][e] - a0, 8.f, off[nt][k]);  // (byte - lo) / 16
+            o4.z = fmaf(a2, 128.f, off[nt][k]);
+            o4.w = fmaf(acc[i2 * 4 + 3][nt][e] - a2, 8.f, off[nt][k]);
             *reinterpret_cast<float4*>(dst + i2 * 64 + y * 32) = o4;
           }
       }
@@ -523,9 +573,9 @@ __global__ void __launch_bounds__(kThreads, 4 / NT > 3 ? 3 : 4 / NT)
       const int64_t ca = ((first_unit + 1) * G - 1) / U, cb = ((first_unit + s.tiles) * G - 1) / U;
       __threadfence();
       consumer_sync();
-      if (tid == 0) found[1] = atomicAdd(p.counters + ca, 1u) == (unsigned)(cb - ca);
+      if (tid == 0) found[0] = atomicAdd(p.counters + ca, 1u) == (unsigned)(cb - ca);
       consumer_sync();
-      if (found[1]) {
+      if (found[0]) {
         __threadfence();
         if (tid == 0) p.counters[ca] = 0;
         for (int r = warp; r < R; r += kWarps) {
