@@ -53,7 +53,8 @@ constexpr int kThreads = 32 * (kWarps + 1);
 constexpr int kTile = 32 * kWarps;             // keys of a unit
 constexpr int kBlocksPerTile = kTile / 16;
 constexpr int kMaxStages = 16;
-constexpr int kMinUnits = 3;                   // a CTA's, where there are few: joining costs as much as two more tiles
+constexpr int kItemCost = 3;                   // units: rows of q in, states joined, results out
+constexpr int kMinUnits = 6;                   // a CTA's, where there are few of them: joining costs as much as more tiles
 constexpr float kLazy = 8.f;
 
 struct DecodeParams {
@@ -115,25 +116,52 @@ SPEAR_DEVINL uint32_t movmatrix(uint32_t x) {
 
 SPEAR_DEVINL void consumer_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory"); }
 
-// A position in the list of units.
+// Units of a sequence: per head its tiles and kItemCost for what an item costs beside them.
+SPEAR_DEVINL int64_t seq_units(const DecodeParams& p, const KvSeq& s) {
+  return s.n > 0 && s.n * p.v.group <= p.max_rows ? (int64_t)(kItemCost + s.tiles) * p.v.n_kv_heads : 0;
+}
+
+// A position in the list of units: unit `off` of an item, the first kItemCost of which are no tiles.
 struct Cursor {
-  int b, h, tile;  // tile counts from s.lo
+  int64_t u;
+  int b, h, off;
   KvSeq s;
 };
 
-SPEAR_DEVINL int64_t seq_units(const DecodeParams& p, const KvSeq& s) {
-  return s.n > 0 && s.n * p.v.group <= p.max_rows ? (int64_t)s.tiles * p.v.n_kv_heads : 0;
+// A CTA's share of an item: tiles [t0, t1), counted from s.lo.
+struct Segment {
+  KvSeq s;
+  int b, h, t0, t1;
+  int64_t unit0;  // the unit of tile 0
+};
+
+SPEAR_DEVINL bool next_segment(const DecodeParams& p, Cursor& c, int64_t u1, Segment& g) {
+  while (c.u < u1) {
+    const int end = (int)min((int64_t)kItemCost + c.s.tiles, c.off + (u1 - c.u));
+    g.s = c.s;
+    g.b = c.b;
+    g.h = c.h;
+    g.t0 = max(0, c.off - kItemCost);
+    g.t1 = max(0, end - kItemCost);
+    g.unit0 = c.u - c.off + kItemCost;
+    c.u += end - c.off;
+    c.off = 0;
+    if (c.u < u1 && ++c.h == p.v.n_kv_heads) {
+      c.h = 0;
+      do {
+        ++c.b;
+        c.s = kv_seq(p.v, p.a, c.b, kTile);
+      } while (seq_units(p, c.s) == 0);
+    }
+    if (g.t1 > g.t0) return true;
+  }
+  return false;
 }
 
-// The next item's first unit (the caller knows that there is one).
-SPEAR_DEVINL void next_item(const DecodeParams& p, Cursor& c) {
-  c.tile = 0;
-  if (++c.h < p.v.n_kv_heads) return;
-  c.h = 0;
-  do {
-    ++c.b;
-    c.s = kv_seq(p.v, p.a, c.b, kTile);
-  } while (seq_units(p, c.s) == 0);
+SPEAR_DEVINL unsigned add_acq_rel(unsigned* p, unsigned x) {
+  unsigned old;
+  asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(x) : "memory");
+  return old;
 }
 
 SPEAR_DEVINL int64_t scan_inclusive(int64_t x, int lane) {
@@ -219,43 +247,47 @@ __global__ void __launch_bounds__(kThreads, 4 / NT > 3 ? 3 : 4 / NT)
       }
     }
   }
+  c.u = u0;
   c.s = kv_seq(p.v, p.a, c.b, kTile);
-  c.h = (int)((uint64_t)at / (unsigned)c.s.tiles);
-  c.tile = (int)(at - (int64_t)c.h * c.s.tiles);
+  const unsigned item = kItemCost + c.s.tiles;
+  c.h = (int)((uint64_t)at / item);
+  c.off = (int)(at - (int64_t)c.h * item);
+  Segment sg;
 
   if (warp == kWarps) {
     // ---------------------------------------------------------------- producer
     int st = 0;
     unsigned phase = 0;
     bool bad = false;
-    int64_t issued = 0;
-    for (int64_t u = u0; u < u1; ++u) {
-      const int blk = (c.s.lo + c.tile) * kBlocksPerTile + lane;
-      const bool wanted = lane < kBlocksPerTile && blk < (c.s.L + 15) / 16;
-      const uint8_t* src = nullptr;
-      if (wanted) {
-        const int pg = p.a.page_table[(int64_t)c.b * p.a.ld_pt + blk / p.v.bpp];
-        if (pg >= 0 && pg < p.v.n_pages)
-          src = p.v.pool + (((int64_t)pg * p.v.n_kv_heads + c.h) * p.v.bpp + blk % p.v.bpp) * BB;
-        else
-          atomicOr(p.v.status, kStatusBadIndex);
+    int issued = 0;
+    while (!bad && next_segment(p, c, u1, sg)) {
+      const int blocks = (sg.s.L + 15) / 16;
+      for (int i = sg.t0; i < sg.t1; ++i) {
+        const int blk = (sg.s.lo + i) * kBlocksPerTile + lane;
+        const uint8_t* src = nullptr;
+        if (lane < kBlocksPerTile && blk < blocks) {
+          const int pg = p.a.page_table[(int64_t)sg.b * p.a.ld_pt + blk / p.v.bpp];
+          if (pg >= 0 && pg < p.v.n_pages)
+            src = p.v.pool + (((int64_t)pg * p.v.n_kv_heads + sg.h) * p.v.bpp + blk % p.v.bpp) * BB;
+          else
+            atomicOr(p.v.status, kStatusBadIndex);
+        }
+        const unsigned copies = __popc(__ballot_sync(0xffffffffu, src != nullptr));
+        if (issued >= p.NS && !mbar_wait_bounded(empty + st, phase ^ 1u, p.wait_ns)) bad = true;
+        bad = __any_sync(0xffffffffu, bad);
+        if (bad) {
+          if (lane == 0) atomicOr(p.v.status, kStatusTimeoutPipe);
+          break;
+        }
+        if (lane == 0) mbar_arrive_expect_tx(full + st, copies * BB);
+        __syncwarp();
+        if (src) bulk_g2s_shared_u32(stages_at + st * p.stage_bytes + lane * BB, src, BB, full + st);
+        issued = min(issued + 1, p.NS);
+        if (++st == p.NS) st = 0, phase ^= 1u;
       }
-      const unsigned copies = __popc(__ballot_sync(0xffffffffu, src != nullptr));
-      if (issued >= p.NS && !mbar_wait_bounded(empty + st, phase ^ 1u, p.wait_ns)) bad = true;
-      if (__any_sync(0xffffffffu, bad)) {
-        if (lane == 0) atomicOr(p.v.status, kStatusTimeoutPipe);
-        break;
-      }
-      if (lane == 0) mbar_arrive_expect_tx(full + st, copies * BB);
-      __syncwarp();
-      if (src) bulk_g2s_shared_u32(stages_at + st * p.stage_bytes + lane * BB, src, BB, full + st);
-      ++issued;
-      if (++st == p.NS) st = 0, phase ^= 1u;
-      if (++c.tile == c.s.tiles && u + 1 < u1) next_item(p, c);
     }
     // the copies in flight land before the CTA's shared memory is given back
-    const int last = (int)min(issued, (int64_t)p.NS);
-    for (int i = 0; i < last; ++i) {
+    for (int i = 0; i < issued; ++i) {
       if (st == 0) st = p.NS, phase ^= 1u;
       --st;
       mbar_wait_bounded(full + st, phase, p.wait_ns);
@@ -271,9 +303,9 @@ __global__ void __launch_bounds__(kThreads, 4 / NT > 3 ? 3 : 4 / NT)
   unsigned phase = 0;
   bool bad = false;
 
-  for (int64_t u = u0; u < u1;) {
-    const int len = (int)min((int64_t)(c.s.tiles - c.tile), u1 - u);
-    const KvSeq s = c.s;
+  while (next_segment(p, c, u1, sg)) {
+    const int len = sg.t1 - sg.t0;
+    const KvSeq s = sg.s;
     const int rows = s.n * p.v.group;
 
     // the rows as f16 B fragments, their sums and their scales
@@ -288,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, 4 / NT > 3 ? 3 : 4 / NT)
       for (int i = 0; i < KW; ++i) w[i] = make_uint4(0, 0, 0, 0);
       if (r < rows) {
         const __nv_bfloat16* src = p.a.q + (int64_t)(s.row + r / p.v.group) * p.a.ld_q +
-                                   (int64_t)(c.h * p.v.group + r % p.v.group) * D + t * (D / 4);
+                                   (int64_t)(sg.h * p.v.group + r % p.v.group) * D + t * (D / 4);
 #pragma unroll
         for (int i = 0; i < KW; ++i) w[i] = reinterpret_cast<const uint4*>(src)[i];
       }
@@ -350,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 4 / NT > 3 ? 3 : 4 / NT)
     }
 
     for (int i = 0; i < len; ++i) {
-      const int key0 = (s.lo + c.tile + i) * kTile + warp * 32;
+      const int key0 = (s.lo + sg.t0 + i) * kTile + warp * 32;
       if (!bad && !mbar_wait_bounded(full + st, phase, p.wait_ns)) {
         bad = true;
         if (lane == 0) atomicOr(p.v.status, kStatusTimeoutPipe);
@@ -529,14 +561,13 @@ __global__ void __launch_bounds__(kThreads, 4 / NT > 3 ? 3 : 4 / NT)
           }
       }
     consumer_sync();
-    const bool whole = c.tile == 0 && len == s.tiles;
-    const int64_t first_unit = u - c.tile;
+    const bool whole = len == s.tiles;
     // a segment that starts its item in this CTA and one that goes on with an earlier CTA's have a slot each
-    float* slot = p.part + (cta * 2 + (c.tile == 0 ? 1 : 0)) * kPart;
+    float* slot = p.part + (cta * 2 + (sg.t0 == 0 ? 1 : 0)) * kPart;
     auto write_row = [&](int r, const float (&o)[E], float inv) {
       if (r >= rows) return;
       __nv_bfloat16* dst = p.a.out + (int64_t)(s.row + r / p.v.group) * p.a.ld_out +
-                           (int64_t)(c.h * p.v.group + r % p.v.group) * D + lane * E;
+                           (int64_t)(sg.h * p.v.group + r % p.v.group) * D + lane * E;
       uint32_t w[E / 2];
 #pragma unroll
       for (int e = 0; e < E; e += 2) w[e / 2] = pack_bf16x2(o[e] * inv, o[e + 1] * inv);
@@ -570,40 +601,51 @@ __global__ void __launch_bounds__(kThreads, 4 / NT > 3 ? 3 : 4 / NT)
     }
     if (!whole) {
       // CTAs ca .. cb hold the item's units
-      const int64_t ca = ((first_unit + 1) * G - 1) / U, cb = ((first_unit + s.tiles) * G - 1) / U;
-      __threadfence();
+      const int64_t x0 = (((lane & 1) ? sg.unit0 + s.tiles : sg.unit0 + 1) * G - 1) / U;
+      const int ca = (int)__shfl_sync(0xffffffffu, x0, 0), parts = (int)__shfl_sync(0xffffffffu, x0, 1) - ca + 1;
       consumer_sync();
-      if (tid == 0) found[0] = atomicAdd(p.counters + ca, 1u) == (unsigned)(cb - ca);
+      // release what the barrier above has collected from the four warps, acquire what the others released
+      if (tid == 0) found[0] = add_acq_rel(p.counters + ca, 1u) == (unsigned)(parts - 1);
       consumer_sync();
       if (found[0]) {
-        __threadfence();
         if (tid == 0) p.counters[ca] = 0;
+        auto part = [&](int x) { return p.part + ((int64_t)(ca + x) * 2 + (x == 0)) * kPart; };
         for (int r = warp; r < R; r += kWarps) {
           float M = -INFINITY;
-          for (int64_t x = ca + lane; x <= cb; x += 32)
-            M = fmaxf(M, __ldcg(p.part + (x * 2 + (x == ca)) * kPart + R * D + 2 * r));
+          for (int x = lane; x < parts; x += 32) M = fmaxf(M, __ldcg(part(x) + R * D + 2 * r));
 #pragma unroll
           for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
           float L = 0.f, o[E];
 #pragma unroll
           for (int e = 0; e < E; ++e) o[e] = 0.f;
-#pragma unroll 4
-          for (int64_t x = ca; x <= cb; ++x) {
-            const float* q = p.part + (x * 2 + (x == ca)) * kPart;
-            const float mx = __ldcg(q + R * D + 2 * r), lx = __ldcg(q + R * D + 2 * r + 1);
-            const float f = mx == -INFINITY ? (lx == 0.f ? 0.f : 1.f) : ex2(mx - M);
-            L = fmaf(f, lx, L);
+          for (int x0 = 0; x0 < parts; x0 += 32) {
+            float f = 0.f, l = 0.f;  // of part x0 + lane
+            if (x0 + lane < parts) {
+              const float m = __ldcg(part(x0 + lane) + R * D + 2 * r);
+              l = __ldcg(part(x0 + lane) + R * D + 2 * r + 1);
+              f = m == -INFINITY ? (l == 0.f ? 0.f : 1.f) : ex2(m - M);
+            }
+            const int n = min(32, parts - x0);
+            for (int y0 = 0; y0 < n; y0 += 8) {
+              float v[8][E];
 #pragma unroll
-            for (int e = 0; e < E; ++e) o[e] = fmaf(f, __ldcg(q + r * D + lane * E + e), o[e]);
+              for (int y = 0; y < 8; ++y)
+#pragma unroll
+                for (int e = 0; e < E; ++e) v[y][e] = y0 + y < n ? __ldcg(part(x0 + y0 + y) + r * D + lane * E + e) : 0.f;
+#pragma unroll
+              for (int y = 0; y < 8; ++y) {
+                const float fy = __shfl_sync(0xffffffffu, f, (y0 + y) & 31);
+                L = fmaf(fy, __shfl_sync(0xffffffffu, l, (y0 + y) & 31), L);
+#pragma unroll
+                for (int e = 0; e < E; ++e) o[e] = fmaf(fy, v[y][e], o[e]);
+              }
+            }
           }
           write_row(r, o, L == 0.f ? 0.f : 1.f / L);
         }
       }
     }
     consumer_sync();  // the joined results have been read
-    u += len;
-    c.tile += len;
-    if (u < u1) next_item(p, c);
   }
 }
 
