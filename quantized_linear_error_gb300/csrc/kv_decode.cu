@@ -164,6 +164,15 @@ SPEAR_DEVINL unsigned add_acq_rel(unsigned* p, unsigned x) {
   return old;
 }
 
+SPEAR_DEVINL void ldcg_row(const float* p, float (&v)[4]) {
+  const float4 x = __ldcg(reinterpret_cast<const float4*>(p));
+  v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+}
+SPEAR_DEVINL void ldcg_row(const float* p, float (&v)[2]) {
+  const float2 x = __ldcg(reinterpret_cast<const float2*>(p));
+  v[0] = x.x, v[1] = x.y;
+}
+
 SPEAR_DEVINL int64_t scan_inclusive(int64_t x, int lane) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -610,38 +619,52 @@ __global__ void __launch_bounds__(kThreads, 4 / NT > 3 ? 3 : 4 / NT)
       if (found[0]) {
         if (tid == 0) p.counters[ca] = 0;
         auto part = [&](int x) { return p.part + ((int64_t)(ca + x) * 2 + (x == 0)) * kPart; };
-        for (int r = warp; r < R; r += kWarps) {
-          float M = -INFINITY;
-          for (int x = lane; x < parts; x += 32) M = fmaxf(M, __ldcg(part(x) + R * D + 2 * r));
+        for (int r = warp; r < R; r += 2 * kWarps) {  // two rows at a time, 16 loads in flight
+          float M[2] = {-INFINITY, -INFINITY};
+          for (int x = lane; x < parts; x += 32)
 #pragma unroll
-          for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-          float L = 0.f, o[E];
+            for (int k = 0; k < 2; ++k) M[k] = fmaxf(M[k], __ldcg(part(x) + R * D + 2 * (r + k * kWarps)));
 #pragma unroll
-          for (int e = 0; e < E; ++e) o[e] = 0.f;
+          for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) M[k] = fmaxf(M[k], __shfl_xor_sync(0xffffffffu, M[k], o));
+          float L[2] = {0.f, 0.f}, o[2][E];
+#pragma unroll
+          for (int e = 0; e < E; ++e) o[0][e] = o[1][e] = 0.f;
           for (int x0 = 0; x0 < parts; x0 += 32) {
-            float f = 0.f, l = 0.f;  // of part x0 + lane
+            float f[2] = {0.f, 0.f}, l[2] = {0.f, 0.f};  // of part x0 + lane
             if (x0 + lane < parts) {
-              const float m = __ldcg(part(x0 + lane) + R * D + 2 * r);
-              l = __ldcg(part(x0 + lane) + R * D + 2 * r + 1);
-              f = m == -INFINITY ? (l == 0.f ? 0.f : 1.f) : ex2(m - M);
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const float2 ml2 = __ldcg(reinterpret_cast<const float2*>(part(x0 + lane) + R * D) + r + k * kWarps);
+                l[k] = ml2.y;
+                f[k] = ml2.x == -INFINITY ? (l[k] == 0.f ? 0.f : 1.f) : ex2(ml2.x - M[k]);
+              }
             }
             const int n = min(32, parts - x0);
             for (int y0 = 0; y0 < n; y0 += 8) {
-              float v[8][E];
+              float v[8][2][E];
 #pragma unroll
               for (int y = 0; y < 8; ++y)
 #pragma unroll
-                for (int e = 0; e < E; ++e) v[y][e] = y0 + y < n ? __ldcg(part(x0 + y0 + y) + r * D + lane * E + e) : 0.f;
+                for (int k = 0; k < 2; ++k)
+                  ldcg_row(part(x0 + min(y0 + y, n - 1)) + (r + k * kWarps) * D + lane * E, v[y][k]);
 #pragma unroll
-              for (int y = 0; y < 8; ++y) {
-                const float fy = __shfl_sync(0xffffffffu, f, (y0 + y) & 31);
-                L = fmaf(fy, __shfl_sync(0xffffffffu, l, (y0 + y) & 31), L);
+              for (int y = 0; y < 8; ++y)
 #pragma unroll
-                for (int e = 0; e < E; ++e) o[e] = fmaf(fy, v[y][e], o[e]);
-              }
+                for (int k = 0; k < 2; ++k) {
+                  const float fy = __shfl_sync(0xffffffffu, f[k], (y0 + y) & 31);
+                  const float ly = __shfl_sync(0xffffffffu, l[k], (y0 + y) & 31);
+                  if (y0 + y < n) {
+                    L[k] = fmaf(fy, ly, L[k]);
+#pragma unroll
+                    for (int e = 0; e < E; ++e) o[k][e] = fmaf(fy, v[y][k][e], o[k][e]);
+                  }
+                }
             }
           }
-          write_row(r, o, L == 0.f ? 0.f : 1.f / L);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) write_row(r + k * kWarps, o[k], L[k] == 0.f ? 0.f : 1.f / L[k]);
         }
       }
     }
