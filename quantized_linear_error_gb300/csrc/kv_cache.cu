@@ -11,22 +11,37 @@ namespace spear {
 namespace {
 
 constexpr int kAppendThreads = 256;
+constexpr int kAppendChunk = 8, kAppendBlocks = 8;
 
-SPEAR_DEVINL uint4 ldg_stream(const void* p) {  // read once: keep it out of L1
-  uint4 v;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
+SPEAR_DEVINL uint2 ldg_stream(const void* p) {  // read once: keep it out of L1
+  uint2 v;
+  asm volatile("ld.global.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
   return v;
 }
 
-SPEAR_DEVINL void unpack8(const uint4& w, float (&x)[8]) {
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(u[i] << 16);
-    x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
-  }
+SPEAR_DEVINL void unpack4(const uint2& w, float* x) {
+  x[0] = __uint_as_float(w.x << 16);
+  x[1] = __uint_as_float(w.x & 0xFFFF0000u);
+  x[2] = __uint_as_float(w.y << 16);
+  x[3] = __uint_as_float(w.y & 0xFFFF0000u);
+}
+
+SPEAR_DEVINL float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+SPEAR_DEVINL float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// The 16-token block of head 0 that holds a slot (in range); page_size is a multiple of 16.
+SPEAR_DEVINL uint8_t* slot_block(const KvView& v, int64_t slot) {
+  const int64_t blk = slot / 16;  // a 64-bit division by bpp takes ten times a 32-bit one
+  const int page = blk <= 0xFFFFFFFFll ? (int)((uint32_t)blk / (uint32_t)v.bpp) : (int)(blk / v.bpp);
+  return v.pool + ((int64_t)page * v.n_kv_heads * v.bpp + (blk - (int64_t)page * v.bpp)) * v.block_bytes;
 }
 
 struct AppendParams {
@@ -36,144 +51,149 @@ struct AppendParams {
   const int64_t *positions, *slots;
   int T;
   __nv_bfloat16* q_out;
-  int rope_dim, interleaved, n_positions;
+  int rope_dim, n_positions;
   const float* table;
   int q_rows;  // rotated query rows a token (0: none)
   int rows;    // q_rows + 2 n_kv_heads
   int chunk;   // rows of one token that a group of lanes takes
-  int chunks;  // ceil(rows / chunk)
 };
 
-// One row of D values is 8 elements a lane, LPR = D / 8 lanes. A group of LPR
-// lanes takes `chunk` rows of one token, so that the token's cosines and sines
-// (8 of each a lane, as many bytes as four rows) are read once for them.
-// Products and sums are rounded one by one (no contraction), so that the
-// codes are defined bit for bit. Bound by memory: a token reads and writes
-// (2 n_heads + 2 n_kv_heads) D bf16 and 2 n_kv_heads (D / 2 + 4) bytes.
-template <int D>
+// One row of D values is 8 elements a lane, LPR = D / 8 lanes: four from `a`
+// on and four from `b` on, which for rotated halves are the four partners, so
+// that a lane has both elements of its pairs and needs four cosines and sines.
+// A group of LPR lanes takes `chunk` rows of one token (a token's cosines and
+// sines are as many bytes as two rows), four rows' loads in flight. Products
+// and sums are rounded one by one (no contraction), so that the codes are
+// defined bit for bit. Bound by memory: a token reads and writes (2 n_heads +
+// 2 n_kv_heads) D bf16 and writes 2 n_kv_heads (D / 2 + 4) bytes.
+template <int D, bool kInterleaved>
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_constant__ AppendParams p) {
-  constexpr int LPR = D / 8;
-  const int sub = threadIdx.x % LPR;
-  const int64_t unit = (int64_t)blockIdx.x * (kAppendThreads / LPR) + threadIdx.x / LPR;
-  if (unit >= (int64_t)p.T * p.chunks) return;  // whole groups leave: the shuffles below are within a group
-  const int t = (int)(unit / p.chunks);
-  const int r0 = (int)(unit % p.chunks) * p.chunk;
+  constexpr int LPR = D / 8, U = 4;
+  const int sub = threadIdx.x % LPR, lane = threadIdx.x & 31;
+  const int t = blockIdx.x * (kAppendThreads / LPR) + threadIdx.x / LPR;
+  if (t >= p.T) return;  // whole groups leave: the shuffles below are within a group
+  const uint32_t mask = (uint32_t)((1ull << LPR) - 1) << (lane / LPR * LPR);
+  const int r0 = blockIdx.y * p.chunk;
   const int r1 = min(r0 + p.chunk, p.rows);
-  const int e0 = sub * 8;
+
+  const int half = p.rope_dim / 2;
+  const bool rotated = kInterleaved ? 8 * sub < p.rope_dim : 4 * sub < half;
+  int a = 8 * sub, b = 8 * sub + 4;  // the lane's elements
+  if (!kInterleaved && p.rope_dim > 0) {
+    a = rotated ? 4 * sub : p.rope_dim + 8 * (sub - half / 4);
+    b = rotated ? a + half : a + 4;
+  }
+
+  // row r of the token, as q rows, k rows, v rows
+  const __nv_bfloat16* qs = p.q + t * p.ld_q;
+  const __nv_bfloat16* ks = p.k + t * p.ld_k;
+  const __nv_bfloat16* vs = p.val + t * p.ld_v;
+  const int k_end = p.q_rows + p.v.n_kv_heads;
+  auto source = [&](int r) {
+    return r < p.q_rows ? qs + r * D : r < k_end ? ks + (r - p.q_rows) * D : vs + (r - k_end) * D;
+  };
+  uint2 wa[U], wb[U];
+  auto load = [&](int r) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const __nv_bfloat16* src = source(min(r + u, r1 - 1));
+      wa[u] = ldg_stream(src + a);
+      wb[u] = ldg_stream(src + b);
+    }
+  };
+  load(r0);
 
   const int64_t slot = p.slots[t];
   const int64_t n_slots = (int64_t)p.v.n_pages * p.v.page_size;
-  const bool held = slot >= 0 && slot < n_slots;
   bool bad = slot < -1 || slot >= n_slots;
   uint8_t* block = nullptr;
-  int row_in_block = 0;
-  if (held) {
-    const int page = (int)(slot / p.v.page_size), at = (int)(slot % p.v.page_size);
-    block = p.v.pool + ((int64_t)page * p.v.n_kv_heads * p.v.bpp + at / 16) * p.v.block_bytes;
-    row_in_block = at % 16;
+  if (slot >= 0 && slot < n_slots) {
+    block = slot_block(p.v, slot) + slot % 16 * 4;  // of the parameters
   }
+  const int codes_at = (int)(slot % 16) * (D / 2 - 4);  // page_size is a multiple of 16
 
-  // this lane's cosines and sines: of its 8 elements (halves) or its 4 pairs
-  const int half = p.rope_dim / 2;
-  const bool rotated = e0 < p.rope_dim;
-  float c[8], s[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) c[i] = 1.f, s[i] = 0.f;
+  float c[4] = {1.f, 1.f, 1.f, 1.f}, s[4] = {0.f, 0.f, 0.f, 0.f};
   if (p.rope_dim > 0) {
     const int64_t pos = p.positions[t];
     const bool ok = pos >= 0 && pos < p.n_positions;
     bad |= !ok;
     if (ok && rotated) {
-      const float* row = p.table + pos * p.rope_dim;
-      if (p.interleaved) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) c[i] = row[e0 / 2 + i], s[i] = row[half + e0 / 2 + i];
-      } else {
-        const int at = e0 < half ? e0 : e0 - half;
-#pragma unroll
-        for (int i = 0; i < 8; i += 4) {
-          *reinterpret_cast<float4*>(c + i) = *reinterpret_cast<const float4*>(row + at + i);
-          *reinterpret_cast<float4*>(s + i) = *reinterpret_cast<const float4*>(row + half + at + i);
-        }
-      }
+      const float* row = p.table + pos * p.rope_dim + 4 * sub;
+      *reinterpret_cast<float4*>(c) = *reinterpret_cast<const float4*>(row);
+      *reinterpret_cast<float4*>(s) = *reinterpret_cast<const float4*>(row + half);
     }
   }
-  if (bad && sub == 0) atomicOr(p.v.status, kStatusBadIndex);
+  if (bad) {
+    if (sub == 0) atomicOr(p.v.status, kStatusBadIndex);
+    return;
+  }
 
-  // the row's partner elements sit half / 8 lanes up or down
-  const int lane = threadIdx.x & 31;
-  const uint32_t mask = (uint32_t)((1ull << LPR) - 1) << (lane / LPR * LPR);
-  const int partner = rotated ? (e0 < half ? lane + half / 8 : lane - half / 8) : lane;
-
-  for (int r = r0; r < r1; ++r) {
-    const int kind = r < p.q_rows ? 0 : (r < p.q_rows + p.v.n_kv_heads ? 1 : 2);
-    const int head = kind == 0 ? r : (kind == 1 ? r - p.q_rows : r - p.q_rows - p.v.n_kv_heads);
-    const __nv_bfloat16* src = (kind == 0 ? p.q + t * p.ld_q : kind == 1 ? p.k + t * p.ld_k : p.val + t * p.ld_v) +
-                               (int64_t)head * D + e0;
-    float x[8];
-    unpack8(ldg_stream(src), x);
-    if (kind < 2 && p.rope_dim > 0) {
-      if (p.interleaved) {
-        if (rotated) {
+  for (int r = r0; r < r1; r += U) {
+    uint2 xa[U], xb[U];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float a = x[2 * i], b = x[2 * i + 1];
-            x[2 * i] = __fsub_rn(__fmul_rn(a, c[i]), __fmul_rn(b, s[i]));
-            x[2 * i + 1] = __fadd_rn(__fmul_rn(b, c[i]), __fmul_rn(a, s[i]));
-          }
-        }
-      } else {
+    for (int u = 0; u < U; ++u) xa[u] = wa[u], xb[u] = wb[u];
+    if (r + U < r1) load(r + U);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float o = __shfl_sync(mask, x[i], partner);
-          if (rotated)
-            x[i] = e0 < half ? __fsub_rn(__fmul_rn(x[i], c[i]), __fmul_rn(o, s[i]))
-                             : __fadd_rn(__fmul_rn(x[i], c[i]), __fmul_rn(o, s[i]));
+    for (int u = 0; u < U; ++u) {
+      const int ru = r + u;
+      if (ru >= r1) break;
+      float x[8];
+      unpack4(xa[u], x);
+      unpack4(xb[u], x + 4);
+      if (ru < k_end && rotated) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          constexpr int f = kInterleaved ? 2 : 1, d = kInterleaved ? 1 : 4;
+          const float x1 = x[f * i], x2 = x[f * i + d];
+          x[f * i] = __fsub_rn(__fmul_rn(x1, c[i]), __fmul_rn(x2, s[i]));
+          x[f * i + d] = __fadd_rn(__fmul_rn(x2, c[i]), __fmul_rn(x1, s[i]));
         }
       }
-    }
-    if (kind == 0) {
-      if (!bad) {
-        uint4 w;
-        w.x = pack_bf16x2(x[0], x[1]);
-        w.y = pack_bf16x2(x[2], x[3]);
-        w.z = pack_bf16x2(x[4], x[5]);
-        w.w = pack_bf16x2(x[6], x[7]);
-        *reinterpret_cast<uint4*>(p.q_out + t * p.ld_q_out + (int64_t)head * D + e0) = w;
+      if (ru < p.q_rows) {
+        __nv_bfloat16* dst = p.q_out + t * p.ld_q_out + ru * D;
+        *reinterpret_cast<uint2*>(dst + a) = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+        *reinterpret_cast<uint2*>(dst + b) = make_uint2(pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+        continue;
       }
-      continue;
-    }
-    float lo = x[0], hi = x[0], sum = 0.f;
+      float lo = x[0], hi = x[0];  // a NaN stays one; infinities show in the range
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      lo = fminf(lo, x[i]);
-      hi = fmaxf(hi, x[i]);
-      sum += x[i] - x[i];  // 0, or NaN where an element is not finite
-    }
+      for (int i = 1; i < 8; ++i) {
+        lo = min_nan(lo, x[i]);
+        hi = max_nan(hi, x[i]);
+      }
 #pragma unroll
-    for (int o = LPR / 2; o > 0; o >>= 1) {
-      lo = fminf(lo, __shfl_xor_sync(mask, lo, o));
-      hi = fmaxf(hi, __shfl_xor_sync(mask, hi, o));
-      sum += __shfl_xor_sync(mask, sum, o);
-    }
-    const float range = __fsub_rn(hi, lo);
-    __nv_bfloat16 sb = __float2bfloat16_rn(__fmul_rn(range, 1.0f / 15.0f));
-    __nv_bfloat16 ob = __float2bfloat16_rn(lo);
-    if (__bfloat162float(sb) < 1.17549435e-38f) sb = __float2bfloat16_rn(0.f);
-    const float sf = __bfloat162float(sb), of = __bfloat162float(ob);
-    const float inv = sf > 0.f ? __fdiv_rn(1.f, sf) : 0.f;
-    uint32_t codes = 0;
+      for (int o = LPR / 2; o > 0; o >>= 1) {
+        lo = min_nan(lo, __shfl_xor_sync(mask, lo, o));
+        hi = max_nan(hi, __shfl_xor_sync(mask, hi, o));
+      }
+      const float range = __fsub_rn(hi, lo);
+      __nv_bfloat16 sb = __float2bfloat16_rn(__fmul_rn(range, 1.0f / 15.0f));
+      const __nv_bfloat16 ob = __float2bfloat16_rn(lo);
+      if (__bfloat162float(sb) < 1.17549435e-38f) sb = __float2bfloat16_rn(0.f);
+      const float sf = __bfloat162float(sb), of = __bfloat162float(ob);
+      const float inv = sf > 0.f ? __fdiv_rn(1.f, sf) : 0.f;
+      // Adding and taking away 2^23 rounds to an integer (half to even); four codes are one number below 2^16, whose
+      // bits stand in the sum with 2^23.
+      uint32_t codes[2];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float f = fminf(fmaxf(rintf(__fmul_rn(__fsub_rn(x[i], of), inv)), 0.f), 15.f);
-      codes |= (uint32_t)f << (4 * i);
-    }
-    uint32_t par = (uint32_t)__bfloat16_as_ushort(sb) | ((uint32_t)__bfloat16_as_ushort(ob) << 16);
-    if (!(sum == 0.f) || !(range <= 0x1p120f)) par = 0x7FC07FC0u;
-    if (block && !bad) {
-      uint8_t* b = block + (int64_t)head * p.v.bpp * p.v.block_bytes;
-      *reinterpret_cast<uint32_t*>(b + (kind - 1) * 8 * D + row_in_block * (D / 2) + sub * 4) = codes;
-      if (sub == 0) *reinterpret_cast<uint32_t*>(b + 16 * D + (kind - 1) * 64 + row_in_block * 4) = par;
+      for (int y = 0; y < 2; ++y) {
+        float f[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          f[i] = __fsub_rn(__fadd_rn(fminf(fmaxf(__fmul_rn(__fsub_rn(x[4 * y + i], of), inv), 0.f), 15.f), 8388608.f),
+                           8388608.f);
+        codes[y] = __float_as_uint(fmaf(fmaf(fmaf(f[3], 16.f, f[2]), 16.f, f[1]), 16.f, f[0]) + 8388608.f);
+      }
+      uint32_t par = (uint32_t)__bfloat16_as_ushort(sb) | ((uint32_t)__bfloat16_as_ushort(ob) << 16);
+      if (!(range <= 0x1p120f)) par = 0x7FC07FC0u;
+      if (block) {
+        const int is_v = ru >= k_end;
+        uint8_t* row = block + (int64_t)(is_v ? ru - k_end : ru - p.q_rows) * p.v.bpp * p.v.block_bytes;
+        uint8_t* cd = row + codes_at + is_v * 8 * D;
+        *reinterpret_cast<uint16_t*>(cd + a / 2) = (uint16_t)codes[0];
+        *reinterpret_cast<uint16_t*>(cd + b / 2) = (uint16_t)codes[1];
+        if (sub == 0) *reinterpret_cast<uint32_t*>(row + 16 * D + is_v * 64) = par;
+      }
     }
   }
 }
@@ -192,10 +212,10 @@ __global__ void __launch_bounds__(kAppendThreads)
   const int64_t slot = slots[t];
   uint4 w = make_uint4(0, 0, 0, 0);
   if (slot >= 0 && slot < (int64_t)v.n_pages * v.page_size) {
-    const int page = (int)(slot / v.page_size), at = (int)(slot % v.page_size);
-    const uint8_t* b = v.pool + (((int64_t)page * v.n_kv_heads + head) * v.bpp + at / 16) * v.block_bytes;
-    const uint32_t codes = *reinterpret_cast<const uint32_t*>(b + is_v * 8 * D + (at % 16) * (D / 2) + sub * 4);
-    const uint32_t par = *reinterpret_cast<const uint32_t*>(b + 16 * D + is_v * 64 + (at % 16) * 4);
+    const uint8_t* b = slot_block(v, slot) + (int64_t)head * v.bpp * v.block_bytes;
+    const int at = (int)(slot % 16);
+    const uint32_t codes = *reinterpret_cast<const uint32_t*>(b + is_v * 8 * D + at * (D / 2) + sub * 4);
+    const uint32_t par = *reinterpret_cast<const uint32_t*>(b + 16 * D + is_v * 64 + at * 4);
     const float s = __uint_as_float(par << 16), o = __uint_as_float(par & 0xFFFF0000u);
     uint32_t r[4];
 #pragma unroll
@@ -287,20 +307,17 @@ spear_status_t spear_kv_append(spear_kv_t h, const void* q, int64_t ld_q, const 
   p.T = T;
   p.q_out = static_cast<__nv_bfloat16*>(q_out);
   p.rope_dim = h->rope_dim;
-  p.interleaved = h->rope_interleaved;
   p.n_positions = h->n_positions;
   p.table = h->rope_table;
   p.q_rows = q ? h->view.n_heads : 0;
   p.rows = p.q_rows + 2 * h->view.n_kv_heads;
-  p.chunk = 1;
-  p.chunks = p.rows;
   const int64_t per_block = kAppendThreads / (D / 8);
-  const int64_t blocks = ((int64_t)T * p.chunks + per_block - 1) / per_block;
-  if (blocks > 0x7FFFFFFF) return SPEAR_ERR_INVALID_ARG;
-  if (D == 128)
-    append_kernel<128><<<(unsigned)blocks, kAppendThreads, 0, stream>>>(p);
-  else
-    append_kernel<64><<<(unsigned)blocks, kAppendThreads, 0, stream>>>(p);
+  p.chunk = kAppendChunk;
+  while (p.chunk > 1 && (int64_t)T * p.rows < (int64_t)p.chunk * per_block * kAppendBlocks * h->sm_count) p.chunk /= 2;
+  const dim3 blocks((unsigned)((T + per_block - 1) / per_block), p.rows / p.chunk + (p.rows % p.chunk != 0));
+  auto* kernel = D == 128 ? (h->rope_interleaved ? append_kernel<128, true> : append_kernel<128, false>)
+                          : (h->rope_interleaved ? append_kernel<64, true> : append_kernel<64, false>);
+  kernel<<<blocks, kAppendThreads, 0, stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? SPEAR_OK : SPEAR_ERR_CUDA;
 }
 
