@@ -11,7 +11,7 @@ namespace spear {
 namespace {
 
 constexpr int kAppendThreads = 256;
-constexpr int kAppendChunk = 8, kAppendBlocks = 8;
+constexpr int kAppendChunk = 8, kAppendBlocks = 4;
 
 SPEAR_DEVINL uint2 ldg_stream(const void* p) {  // read once: keep it out of L1
   uint2 v;
@@ -67,7 +67,7 @@ struct AppendParams {
 // defined bit for bit. Bound by memory: a token reads and writes (2 n_heads +
 // 2 n_kv_heads) D bf16 and writes 2 n_kv_heads (D / 2 + 4) bytes.
 template <int D, bool kInterleaved>
-__global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(kAppendThreads, 4) append_kernel(const __grid_constant__ AppendParams p) {
   constexpr int LPR = D / 8, U = 4;
   const int sub = threadIdx.x % LPR, lane = threadIdx.x & 31;
   const int t = blockIdx.x * (kAppendThreads / LPR) + threadIdx.x / LPR;
@@ -129,17 +129,14 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
   }
 
   for (int r = r0; r < r1; r += U) {
-    uint2 xa[U], xb[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) xa[u] = wa[u], xb[u] = wb[u];
-    if (r + U < r1) load(r + U);
+    if (r > r0) load(r);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int ru = r + u;
       if (ru >= r1) break;
       float x[8];
-      unpack4(xa[u], x);
-      unpack4(xb[u], x + 4);
+      unpack4(wa[u], x);
+      unpack4(wb[u], x + 4);
       if (ru < k_end && rotated) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -198,34 +195,52 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
   }
 }
 
-// A group of D / 8 lanes hands back one row (8 elements a lane).
+// A group of D / 8 lanes hands back `chunk` of a token's 2 n_kv_heads rows (8
+// elements a lane), four rows' loads in flight.
 template <int D>
 __global__ void __launch_bounds__(kAppendThreads)
-    read_kernel(KvView v, const int64_t* __restrict__ slots, int T, __nv_bfloat16* k_out, __nv_bfloat16* v_out) {
-  constexpr int LPR = D / 8;
+    read_kernel(const KvView v, const int64_t* __restrict__ slots, int T, int chunk, __nv_bfloat16* k_out,
+                __nv_bfloat16* v_out) {
+  constexpr int LPR = D / 8, U = 4;
   const int sub = threadIdx.x % LPR;
-  const int64_t unit = (int64_t)blockIdx.x * (kAppendThreads / LPR) + threadIdx.x / LPR;
-  if (unit >= (int64_t)T * v.n_kv_heads * 2) return;
-  const int is_v = (int)(unit % 2);
-  const int64_t row = unit / 2;  // token * n_kv_heads + head
-  const int t = (int)(row / v.n_kv_heads), head = (int)(row % v.n_kv_heads);
+  const int t = blockIdx.x * (kAppendThreads / LPR) + threadIdx.x / LPR;
+  if (t >= T) return;
+  const int r0 = blockIdx.y * chunk, r1 = min(r0 + chunk, 2 * v.n_kv_heads);
   const int64_t slot = slots[t];
-  uint4 w = make_uint4(0, 0, 0, 0);
-  if (slot >= 0 && slot < (int64_t)v.n_pages * v.page_size) {
-    const uint8_t* b = slot_block(v, slot) + (int64_t)head * v.bpp * v.block_bytes;
-    const int at = (int)(slot % 16);
-    const uint32_t codes = *reinterpret_cast<const uint32_t*>(b + is_v * 8 * D + at * (D / 2) + sub * 4);
-    const uint32_t par = *reinterpret_cast<const uint32_t*>(b + 16 * D + is_v * 64 + at * 4);
-    const float s = __uint_as_float(par << 16), o = __uint_as_float(par & 0xFFFF0000u);
-    uint32_t r[4];
+  const bool held = slot >= 0 && slot < (int64_t)v.n_pages * v.page_size;
+  if (!held && slot != -1 && sub == 0) atomicOr(v.status, kStatusBadIndex);
+  const uint8_t* b = held ? slot_block(v, slot) : v.pool;
+  const int at = (int)(slot & 15);
+  for (int r = r0; r < r1; r += U) {
+    uint32_t codes[U], par[U];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      r[i] = pack_bf16x2(fmaf((float)((codes >> (8 * i)) & 15u), s, o), fmaf((float)((codes >> (8 * i + 4)) & 15u), s, o));
-    w = make_uint4(r[0], r[1], r[2], r[3]);
-  } else if (slot != -1 && sub == 0) {
-    atomicOr(v.status, kStatusBadIndex);
+    for (int u = 0; u < U; ++u) {
+      const int ru = min(r + u, r1 - 1), is_v = ru >= v.n_kv_heads;
+      const uint8_t* row = b + (int64_t)(is_v ? ru - v.n_kv_heads : ru) * v.bpp * v.block_bytes;
+      codes[u] = held ? *reinterpret_cast<const uint32_t*>(row + is_v * 8 * D + at * (D / 2) + sub * 4) : 0u;
+      par[u] = held ? *reinterpret_cast<const uint32_t*>(row + 16 * D + is_v * 64 + at * 4) : 0u;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int ru = r + u, is_v = ru >= v.n_kv_heads;
+      if (ru >= r1) break;
+      const float s = __uint_as_float(par[u] << 16), o = __uint_as_float(par[u] & 0xFFFF0000u);
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        w[i] = pack_bf16x2(fmaf((float)((codes[u] >> (8 * i)) & 15u), s, o),
+                           fmaf((float)((codes[u] >> (8 * i + 4)) & 15u), s, o));
+      __nv_bfloat16* dst = (is_v ? v_out : k_out) + ((int64_t)t * v.n_kv_heads + (is_v ? ru - v.n_kv_heads : ru)) * D;
+      *reinterpret_cast<uint4*>(dst + sub * 8) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
   }
-  *reinterpret_cast<uint4*>((is_v ? v_out : k_out) + row * D + sub * 8) = w;
+}
+
+// Rows of a token that a group takes: up to kAppendChunk, as long as the device stays filled.
+int rows_per_group(const spear_kv_s* h, int T, int rows, int64_t groups_per_block) {
+  int chunk = kAppendChunk;
+  while (chunk > 1 && (int64_t)T * rows < chunk * groups_per_block * kAppendBlocks * h->sm_count) chunk /= 2;
+  return chunk;
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -312,9 +327,8 @@ spear_status_t spear_kv_append(spear_kv_t h, const void* q, int64_t ld_q, const 
   p.q_rows = q ? h->view.n_heads : 0;
   p.rows = p.q_rows + 2 * h->view.n_kv_heads;
   const int64_t per_block = kAppendThreads / (D / 8);
-  p.chunk = kAppendChunk;
-  while (p.chunk > 1 && (int64_t)T * p.rows < (int64_t)p.chunk * per_block * kAppendBlocks * h->sm_count) p.chunk /= 2;
-  const dim3 blocks((unsigned)((T + per_block - 1) / per_block), p.rows / p.chunk + (p.rows % p.chunk != 0));
+  p.chunk = rows_per_group(h, T, p.rows, per_block);
+  const dim3 blocks((unsigned)((T + per_block - 1) / per_block), (p.rows + p.chunk - 1) / p.chunk);
   auto* kernel = D == 128 ? (h->rope_interleaved ? append_kernel<128, true> : append_kernel<128, false>)
                           : (h->rope_interleaved ? append_kernel<64, true> : append_kernel<64, false>);
   kernel<<<blocks, kAppendThreads, 0, stream>>>(p);
@@ -328,14 +342,11 @@ spear_status_t spear_kv_read(spear_kv_t h, const int64_t* slots, int32_t T, void
   if (!slots || !k_out || !v_out || !aligned16(k_out) || !aligned16(v_out)) return SPEAR_ERR_INVALID_ARG;
   const int D = h->view.D;
   const int64_t per_block = kAppendThreads / (D / 8);
-  const int64_t blocks = ((int64_t)T * h->view.n_kv_heads * 2 + per_block - 1) / per_block;
-  if (blocks > 0x7FFFFFFF) return SPEAR_ERR_INVALID_ARG;
-  auto* ko = static_cast<__nv_bfloat16*>(k_out);
-  auto* vo = static_cast<__nv_bfloat16*>(v_out);
-  if (D == 128)
-    read_kernel<128><<<(unsigned)blocks, kAppendThreads, 0, stream>>>(h->view, slots, T, ko, vo);
-  else
-    read_kernel<64><<<(unsigned)blocks, kAppendThreads, 0, stream>>>(h->view, slots, T, ko, vo);
+  const int rows = 2 * h->view.n_kv_heads, chunk = rows_per_group(h, T, rows, per_block);
+  const dim3 blocks((unsigned)((T + per_block - 1) / per_block), (rows + chunk - 1) / chunk);
+  auto* kernel = D == 128 ? read_kernel<128> : read_kernel<64>;
+  kernel<<<blocks, kAppendThreads, 0, stream>>>(h->view, slots, T, chunk, static_cast<__nv_bfloat16*>(k_out),
+                                                static_cast<__nv_bfloat16*>(v_out));
   return cudaGetLastError() == cudaSuccess ? SPEAR_OK : SPEAR_ERR_CUDA;
 }
 
