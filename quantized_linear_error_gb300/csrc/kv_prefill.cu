@@ -123,33 +123,46 @@ SPEAR_DEVINL int64_t head_units(const PrefillParams& p, const KvSeq& s, int nqt,
   return x;
 }
 
-// Calls f(sequence, row tiles) for every sequence of this kernel, the warp
-// together, until f returns true.
-template <class F>
-SPEAR_DEVINL void each_sequence(const PrefillParams& p, int lane, F f) {
-  for (int b0 = 0; b0 < p.a.n_seqs; b0 += 32) {
-    const int b = b0 + lane;
-    const bool mine = b < p.a.n_seqs && row_tiles(p, kv_seq(p.v, p.a, b, kTile)) > 0;
-    for (unsigned todo = __ballot_sync(0xffffffffu, mine); todo; todo &= todo - 1) {
-      const int bb = b0 + __ffs(todo) - 1;
-      const KvSeq s = kv_seq(p.v, p.a, bb, kTile);
-      if (f(bb, s, row_tiles(p, s))) return;
-    }
-  }
-}
-
 SPEAR_DEVINL void fail(const PrefillParams& p) { atomicOr(p.v.status, kStatusTimeoutPipe); }
+
+SPEAR_DEVINL KvSeq shuffled(const KvSeq& s, int l) {
+  KvSeq r;
+  r.n = __shfl_sync(0xffffffffu, s.n, l);
+  r.row = __shfl_sync(0xffffffffu, s.row, l);
+  r.L = __shfl_sync(0xffffffffu, s.L, l);
+  return r;  // lo and tiles are of no use here
+}
 
 // The warp that lays out a CTA's work. Every CTA counts all units, finds where
 // its equal share begins and hands its segments to the other warps; it also
 // fetches the coming items' query rows into L2.
 template <int D>
 SPEAR_DEVINL void schedule(const PrefillParams& p, Header& hd, int lane) {
-  int64_t U = 0;
-  each_sequence(p, lane, [&](int, const KvSeq& s, int nqt) {
-    U += head_units(p, s, nqt, lane) * p.v.n_kv_heads;
-    return false;
-  });
+  // units of 32 sequences, lane b's in lane b; the lane's sequence is left in `s`
+  KvSeq s;
+  auto units_of = [&](int b0) {
+    const int b = b0 + lane;
+    int nqt = 0;
+    if (b < p.a.n_seqs) {
+      s = kv_seq(p.v, p.a, b, kTile);
+      nqt = row_tiles(p, s);
+    }
+    int64_t own = 0;
+    for (unsigned todo = __ballot_sync(0xffffffffu, nqt > 0); todo; todo &= todo - 1) {
+      const int l = __ffs(todo) - 1;
+      const int64_t x = head_units(p, shuffled(s, l), __shfl_sync(0xffffffffu, nqt, l), lane) * p.v.n_kv_heads;
+      if (lane == l) own = x;
+    }
+    return own;
+  };
+  int64_t U = 0, own = 0;
+  for (int b0 = 0; b0 < p.a.n_seqs; b0 += 32) {
+    own = units_of(b0);
+    int64_t x = own;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    U += x;
+  }
   const int64_t G = min((int64_t)gridDim.x, U), cta = blockIdx.x;
   int64_t u = 0, u1 = 0;
   if (cta < G) {
@@ -158,39 +171,47 @@ SPEAR_DEVINL void schedule(const PrefillParams& p, Header& hd, int lane) {
     u1 = __shfl_sync(0xffffffffu, x, 1);
   }
   int b = 0, h = 0, qt = 0, off = 0, nqt = 0;
-  KvSeq s;
   if (u < u1) {
     int64_t before = 0;
-    each_sequence(p, lane, [&](int bb, const KvSeq& ss, int nq) {
-      const int64_t hu = head_units(p, ss, nq, lane);
-      if (u >= before + hu * p.v.n_kv_heads) {
-        before += hu * p.v.n_kv_heads;
-        return false;
-      }
-      b = bb;
-      s = ss;
-      nqt = nq;
-      h = (int)((u - before) / hu);
-      int64_t rest = u - before - h * hu;
-      for (int q0 = 0; q0 < nqt; q0 += 32) {
-        const int own = q0 + lane < nqt ? kItemCost + item_of(p, s, q0 + lane).tiles : 0;
-        int incl = own;
+    for (int b0 = 0;; b0 += 32) {  // the sequence that u falls into
+      if (p.a.n_seqs > 32) own = units_of(b0);
+      int64_t incl = own;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int x = __shfl_up_sync(0xffffffffu, incl, o);
-          if (lane >= o) incl += x;
-        }
-        const int sum = __shfl_sync(0xffffffffu, incl, 31);
-        if (rest < sum) {
-          const int at = __ffs(__ballot_sync(0xffffffffu, rest < incl)) - 1;
-          qt = q0 + at;
-          off = (int)rest - (__shfl_sync(0xffffffffu, incl, at) - __shfl_sync(0xffffffffu, own, at));
-          break;
-        }
-        rest -= sum;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += x;
       }
-      return true;
-    });
+      const unsigned past = __ballot_sync(0xffffffffu, u < before + incl);
+      if (past) {
+        const int l = __ffs(past) - 1;
+        b = b0 + l;
+        const int64_t hu = __shfl_sync(0xffffffffu, own, l) / p.v.n_kv_heads;
+        int64_t rest = u - before - (__shfl_sync(0xffffffffu, incl, l) - __shfl_sync(0xffffffffu, own, l));
+        s = shuffled(s, l);
+        nqt = row_tiles(p, s);
+        h = (int)(rest / hu);
+        rest -= h * hu;
+        for (int q0 = 0; q0 < nqt; q0 += 32) {
+          const int cost = q0 + lane < nqt ? kItemCost + item_of(p, s, q0 + lane).tiles : 0;
+          int sum = cost;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += x;
+          }
+          const int all = __shfl_sync(0xffffffffu, sum, 31);
+          if (rest < all) {
+            const int at = __ffs(__ballot_sync(0xffffffffu, rest < sum)) - 1;
+            qt = q0 + at;
+            off = (int)rest - (__shfl_sync(0xffffffffu, sum, at) - __shfl_sync(0xffffffffu, cost, at));
+            break;
+          }
+          rest -= all;
+        }
+        break;
+      }
+      before += __shfl_sync(0xffffffffu, incl, 31);
+    }
   }
   Join join = {};
   unsigned n = 0;
@@ -467,8 +488,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           if (leader) mbar_arrive(&hd.turn[i ^ 1]);
           // what the turn needs, before taking it: the next K tile (dequantised after this V tile) or this V tile
           if (more || k + 1 < len ? !wait(&hd.k_full[st ^ 1u], ((kc + 1) >> 1) & 1u) : !wait(&hd.v_full[st], ph)) break;
-          if (mine && !wait(&hd.p_full[0][i], p_ph)) break;
           if (!take_turn()) break;
+          if (mine && !wait(&hd.p_full[0][i], p_ph)) break;
           if (mine) {
             const uint64_t vd = v_desc + st * (kTileBytes >> 4);
 #pragma unroll
