@@ -22,8 +22,10 @@
 //    the others (0 x NaN in O += P V would not).
 //  - Two softmax warpgroups, one an MMA tile, one row a thread; P goes from
 //    registers to tensor memory. While one works on S the other's products run.
-//    The running maximum is lazy as in the other kernel: O is rescaled only
-//    when a score passes m by 8 in log2.
+//    m need not be the maximum: weights and sums keep their relative precision
+//    whatever their size, so that m is taken from a segment's first tile and
+//    again only when the weights of 64 keys sum to more than 2^16; no other
+//    tile takes a maximum.
 //  - One thread issues the MMAs, in the order O0 S0 O1 S1 of successive tiles:
 //    an S overwrites its P only after the product that reads it, which was
 //    issued before it.
@@ -50,7 +52,7 @@ constexpr int kItemCost = 4;          // units
 constexpr int kHeader = 1024;         // barriers, segments
 constexpr int kSegs = 4;              // segments in flight
 constexpr int kSegReaders = 8 + kDeqWarps + 2 + 1;  // warps that read each segment
-constexpr float kLazy = 8.f;
+constexpr float kBig = 0x1p16f;
 constexpr uint32_t kHintNs = 100;
 // setmaxnreg: 256 x 168 + 384 x 48 registers are the 640 x 96 of the launch
 constexpr int kJoinRows = 32;
@@ -83,7 +85,7 @@ struct Segment {
 
 struct Header {
   uint64_t raw_full[2], raw_empty[2], k_full[2], k_empty[2], v_full[2], v_empty[2];
-  uint64_t q_full[2], s_full[2], p_full[2][2], o_full[2], turn[2], done[2];  // p_full: [64 keys][half]
+  uint64_t q_full[2], s_full[2], p_full[2][2], pa_done[2], o_full[2], turn[2], done[2];  // p_full: [64 keys][half]
   uint64_t seg_full[kSegs], seg_empty[kSegs];
   Segment seg[kSegs];
   uint32_t tmem;
@@ -349,6 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       mbar_init(&hd.p_full[0][i], 4);
       mbar_init(&hd.p_full[1][i], 4);
       mbar_init(&hd.o_full[i], 1);
+      mbar_init(&hd.pa_done[i], 1);
       mbar_init(&hd.turn[i], 1);
       mbar_init(&hd.done[i], 1);
     }
@@ -499,6 +502,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
 #pragma unroll
               for (int kk = 4 * x; kk < 4 * x + 4; ++kk)
                 umma_ts_bf16(leader, o_d, s_d + 8 * kk, vd + kk * (2048 >> 4), idesc_o, kk == 0 ? (k != 0) : 1u);
+              if (x == 0) umma_commit(leader, &hd.pa_done[i]);
             }
             if (!ok) break;
             p_ph ^= 1u;
@@ -641,12 +645,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
 #pragma unroll
           for (int j = 0; j < 4; ++j) mask(j);
         }
-        // Weights of the first 64 keys by the present m, beside the maximum over all 128: m is nearly always kept
         uint32_t w[32];
-        uint64_t sum2[2];
+        // weights of 64 keys by the present m, and their sum
         auto weights = [&](int y) {
           const float ms = m == -INFINITY ? 0.f : -m * sl;
           const uint64_t sl2 = pack_f32x2(sl, sl), ms2 = pack_f32x2(ms, ms);
+          uint64_t sum2[2];
 #pragma unroll
           for (int x = 0; x < 64; x += 2) {
             const uint32_t* q = &v[2 * y + x / 32][x % 32];
@@ -654,9 +658,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
             unpack_f32x2(fma_f32x2(pack_b32x2(q[0], q[1]), sl2, ms2), pa, pb);
             pa = ex2(pa);
             pb = ex2(pb);
-            sum2[(x >> 1) & 1] = x < 4 && y == 0 ? pack_f32x2(pa, pb) : add_f32x2(sum2[(x >> 1) & 1], pack_f32x2(pa, pb));
+            sum2[(x >> 1) & 1] = x < 4 ? pack_f32x2(pa, pb) : add_f32x2(sum2[(x >> 1) & 1], pack_f32x2(pa, pb));
             w[x / 2] = pack_bf16x2(pa, pb);
           }
+          float sa, sb;
+          unpack_f32x2(add_f32x2(sum2[0], sum2[1]), sa, sb);
+          return sa + sb;
         };
         auto hand_over = [&](int y) {
           tmem_st_x32(s_t + 32 * y, w);
@@ -665,21 +672,26 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           __syncwarp();
           if (lane == 0) mbar_arrive(&hd.p_full[y][i]);
         };
-        weights(0);
-        float top[4];
+        // m becomes the row's maximum up to this tile, what has been summed is scaled to it, and the scores of the
+        // first or the last 64 keys are read again
+        auto new_maximum = [&](int y) {
+          float mx = m;
+#pragma unroll 1
+          for (int j = 0; j < kTile; j += 32) {  // the first half may hold weights by now: its scores are in `m` then
+            if (y == 1 && j < 64) continue;
+            tmem_ld_x32(s_t + j, v[0]);
+            tmem_ld_wait();
+            if (masked) {
+              const int a = d - j, b = e - j;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          top[j] = fmaxf(__uint_as_float(v[j][0]), __uint_as_float(v[j][1]));
+              for (int x = 0; x < 32; ++x)
+                if (x > a || x <= b) v[0][x] = 0xFF800000u;
+            }
 #pragma unroll
-          for (int x = 2; x < 32; x += 2)
-            top[j] = fmaxf(top[j], fmaxf(__uint_as_float(v[j][x]), __uint_as_float(v[j][x + 1])));
-        }
-        const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-        if (k == 0 || __any_sync(0xffffffffu, m == -INFINITY ? mx > m : (mx - m) * sl > kLazy)) {
-          const float mn = fmaxf(m, mx);
-          if (k > 0) {
-            // the previous product has finished (s_full covers it), the next waits for this thread
-            const float f = m == -INFINITY ? 0.f : ex2((m - mn) * sl);
+            for (int x = 0; x < 32; ++x) mx = fmaxf(mx, __uint_as_float(v[0][x]));
+          }
+          if (k > 0 || y == 1) {
+            const float f = m == -INFINITY ? 0.f : ex2((m - mx) * sl);
             l *= f;
 #pragma unroll 1
             for (int j = 0; j < D; j += 16) {
@@ -691,19 +703,30 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
               tmem_st_x16(o_t + j, o);
             }
           }
-          m = mn;
-          tmem_ld_x32(s_t, v[0]);
-          tmem_ld_x32(s_t + 32, v[1]);
+          m = mx;
+#pragma unroll
+          for (int j = 2 * y; j < 2 * y + 2; ++j) tmem_ld_x32(s_t + 32 * j, v[j]);
           tmem_ld_wait();
-          if (masked) mask(0), mask(1);
-          weights(0);
+          if (masked) mask(2 * y), mask(2 * y + 1);
+        };
+        // The weights' size shows whether m will do: no maximum is taken as long as their sum stays below kBig
+        float sum = weights(0);
+        if (__any_sync(0xffffffffu, m == -INFINITY || sum > kBig)) {  // the first tile always
+          new_maximum(0);  // the previous product has finished (s_full covers it), the next waits for this thread
+          sum = weights(0);
         }
         hand_over(0);
-        weights(1);
+        l += sum;
+        sum = weights(1);
+        if (__any_sync(0xffffffffu, sum > kBig)) {
+          ok = warp_wait(&hd.pa_done[i], (n_s & 1u) ^ 1u, p.wait_ns, kHintNs);  // the product with the first weights
+          if (!ok) break;
+          tc_fence_after_sync();
+          new_maximum(1);
+          sum = weights(1);
+        }
         hand_over(1);
-        float sa, sb;
-        unpack_f32x2(add_f32x2(sum2[0], sum2[1]), sa, sb);
-        l += sa + sb;
+        l += sum;
       }
       if (!ok) break;
       // the half's scores are done with its Q tile: the next item's rows go in while the last product runs

@@ -223,3 +223,25 @@ def test_refusals():
     two = torch.zeros(4, 4, 64, dtype=torch.bfloat16, device="cuda")
     with pytest.raises(spear.SpearError):
         b.c.attention(**{**good, "q": two[:3], "out": two[1:], "q_starts": i(0, 3), "max_q": 3})
+
+
+def test_scores_that_jump_inside_a_tile():
+    """One key far above all before it, at every place in a tile of 128 keys: the reference of the running sums moves
+    at the first or the second 64 keys of a tile, once or several times, for some rows and not for others."""
+    for at in ([5], [60], [64], [100], [127, 200], [130, 193, 260], [70, 140, 210, 280]):
+        def edit(i, k, v):
+            k *= 0.05
+            for x, j in enumerate(at):
+                k[j] *= 400.0 * (x + 1)
+        for n, L in [(40, 300), (100, 330), (2, 300)]:
+            _check([(n, L)], 4, 2, 128, 16, edit=edit, seed=sum(at))
+
+
+def test_scores_far_below_zero():
+    """All scores at some -400 in units of log2, behind a window that hides the first tiles from most rows."""
+    def edit(i, k, v):
+        k[:] = np.abs(k) + 5
+    for n, L, window in [(1, 300, 0), (100, 400, 60), (200, 200, 0)]:
+        b = Batch([(n, L)], 4, 2, 64, 16, edit=edit, seed=n)
+        b.q = -b.q.abs() - 1
+        b.check(b.run(window=window, scale=1.0), window, 1.0)
