@@ -359,7 +359,7 @@ spear_status_t spear_kv_attention(spear_kv_t h, const void* q, int64_t ld_q, voi
   const int64_t qn = (int64_t)h->view.n_heads * h->view.D;
   if (!row_ok(q, ld_q, qn) || !row_ok(out, ld_out, qn) || !page_table || ld_pt < 1 || !kv_lens || !q_starts ||
       max_q < 1 || window < 0 || !isfinite(scale) ||
-      (int64_t)T * h->view.group > 0x7FFF0000)
+      (int64_t)T * h->view.group >= (1 << 27))
     return SPEAR_ERR_INVALID_ARG;
   // out is q itself or lies apart from it
   const char *qb = static_cast<const char*>(q), *ob = static_cast<const char*>(out);

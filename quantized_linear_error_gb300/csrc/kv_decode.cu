@@ -217,8 +217,8 @@ __global__ void __launch_bounds__(kThreads, 4 / NT > 3 ? 3 : 4 / NT)
   int64_t U = 0, G, u0, u1, at;
   const int64_t cta = blockIdx.x;
   auto share = [&] {
-    G = min((int64_t)gridDim.x, (U + kMinUnits - 1) / kMinUnits);
-    const int64_t x = G > 0 ? (cta + (lane & 1)) * U / G : 0;
+    G = min((int64_t)gridDim.x, div_u64(U + kMinUnits - 1, kMinUnits));
+    const int64_t x = G > 0 ? div_u64((cta + (lane & 1)) * U, G) : 0;
     u0 = __shfl_sync(0xffffffffu, x, 0);
     u1 = __shfl_sync(0xffffffffu, x, 1);
   };
@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, 4 / NT > 3 ? 3 : 4 / NT)
   c.u = u0;
   c.s = kv_seq(p.v, p.a, c.b, kTile);
   const unsigned item = kItemCost + c.s.tiles;
-  c.h = (int)((uint64_t)at / item);
+  c.h = (int)div_u64(at, item);
   c.off = (int)(at - (int64_t)c.h * item);
   Segment sg;
 
@@ -610,7 +610,7 @@ __global__ void __launch_bounds__(kThreads, 4 / NT > 3 ? 3 : 4 / NT)
     }
     if (!whole) {
       // CTAs ca .. cb hold the item's units
-      const int64_t x0 = (((lane & 1) ? sg.unit0 + s.tiles : sg.unit0 + 1) * G - 1) / U;
+      const int64_t x0 = div_u64(((lane & 1) ? sg.unit0 + s.tiles : sg.unit0 + 1) * G - 1, U);
       const int ca = (int)__shfl_sync(0xffffffffu, x0, 0), parts = (int)__shfl_sync(0xffffffffu, x0, 1) - ca + 1;
       consumer_sync();
       // release what the barrier above has collected from the four warps, acquire what the others released

@@ -31,6 +31,11 @@ SPEAR_DEVINL uint64_t add_f32x2(uint64_t a, uint64_t b) {
   return r;
 }
 
+// a / b for a, b >= 0: most are small, and a 64-bit division takes several times a 32-bit one.
+SPEAR_DEVINL int64_t div_u64(int64_t a, int64_t b) {
+  return ((uint64_t)(a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : (int64_t)((uint64_t)a / (uint64_t)b);
+}
+
 // Sequence b of a call as a kernel works on it, every index checked.
 struct KvSeq {
   int n;         // query rows (0: nothing to do)

@@ -66,6 +66,7 @@ struct Join {
 struct PrefillParams {
   KvView v;
   KvAttnArgs a;
+  unsigned inv_group;  // floor(2^32 / group) + 1, 0 for a group of one
   int max_rows;   // sequences with at most this many rows of a key/value head belong to the other kernel
   float* part;    // [grid][2][2 halves][D + 2][128]
   Join* joins;    // [grid]
@@ -92,8 +93,13 @@ struct Header {
 };
 static_assert(sizeof(Header) <= kHeader, "");
 
-// Row tile qt of a sequence: its key tiles. (Rows of a key/value head, query
-// rows x group, fit 32 bits: the launch checks T x group.)
+// R / group for R < 2^27 (the launch checks T x group): the reciprocal's error, below 2^-32, times R stays below
+// 1 / group.
+SPEAR_DEVINL unsigned div_group(const PrefillParams& p, unsigned R) {
+  return p.inv_group ? __umulhi(R, p.inv_group) : R;
+}
+
+// Row tile qt of a sequence: its key tiles.
 struct Item {
   int lo, tiles;
   int rows;  // rows of this tile, <= 256
@@ -108,7 +114,7 @@ SPEAR_DEVINL Item item_of(const PrefillParams& p, const KvSeq& s, int qt) {
   Item it;
   const int r0 = qt * kRows;
   it.rows = min(kRows, s.n * p.v.group - r0);
-  const int t0 = r0 / p.v.group, t1 = (r0 + it.rows - 1) / p.v.group;
+  const int t0 = div_group(p, r0), t1 = div_group(p, r0 + it.rows - 1);
   const int last = s.L - s.n + t1;
   const int first = p.a.window > 0 ? s.L - s.n + t0 - p.a.window + 1 : 0;
   it.lo = first > 0 ? first / kTile : 0;
@@ -168,7 +174,7 @@ SPEAR_DEVINL void schedule(const PrefillParams& p, Header& hd, int lane) {
   const int64_t G = min((int64_t)gridDim.x, U), cta = blockIdx.x;
   int64_t u = 0, u1 = 0;
   if (cta < G) {
-    const int64_t x = (cta + (lane & 1)) * U / G;
+    const int64_t x = div_u64((cta + (lane & 1)) * U, G);
     u = __shfl_sync(0xffffffffu, x, 0);
     u1 = __shfl_sync(0xffffffffu, x, 1);
   }
@@ -187,11 +193,11 @@ SPEAR_DEVINL void schedule(const PrefillParams& p, Header& hd, int lane) {
       if (past) {
         const int l = __ffs(past) - 1;
         b = b0 + l;
-        const int64_t hu = __shfl_sync(0xffffffffu, own, l) / p.v.n_kv_heads;
+        const int64_t hu = div_u64(__shfl_sync(0xffffffffu, own, l), p.v.n_kv_heads);
         int64_t rest = u - before - (__shfl_sync(0xffffffffu, incl, l) - __shfl_sync(0xffffffffu, own, l));
         s = shuffled(s, l);
         nqt = row_tiles(p, s);
-        h = (int)(rest / hu);
+        h = (int)div_u64(rest, hu);
         rest -= h * hu;
         for (int q0 = 0; q0 < nqt; q0 += 32) {
           const int cost = q0 + lane < nqt ? kItemCost + item_of(p, s, q0 + lane).tiles : 0;
@@ -237,7 +243,7 @@ SPEAR_DEVINL void schedule(const PrefillParams& p, Header& hd, int lane) {
         g.slot = (int)cta * 2 + (t0 == 0);  // one slot for the share that starts an item, one for a later share
         if (t0 == 0 && !g.whole) {
           const int64_t last = u - off + kItemCost + it.tiles - 1;  // the item's last unit
-          join = {(int)(((last + 1) * G - 1) / U - cta) + 1, it.rows, g.r0, h, s.row};
+          join = {(int)(div_u64((last + 1) * G - 1, U) - cta) + 1, it.rows, g.r0, h, s.row};
         }
       }
       u += stop - off;
@@ -255,12 +261,6 @@ SPEAR_DEVINL void schedule(const PrefillParams& p, Header& hd, int lane) {
       }
     }
     end = g.len == 0;
-    for (int r = lane; r < g.rows; r += 32) {
-      const unsigned R = g.r0 + r, tok = R / (unsigned)p.v.group;
-      const __nv_bfloat16* q = p.a.q + (int64_t)(g.row + tok) * p.a.ld_q + (int64_t)(g.h * p.v.group + R - tok * p.v.group) * D;
-#pragma unroll
-      for (int x = 0; x < D; x += 64) prefetch_l2_line(q + x);
-    }
     const unsigned i = n % kSegs;
     if (n >= kSegs && !warp_wait(&hd.seg_empty[i], ((n / kSegs) & 1u) ^ 1u, p.wait_ns, 1000)) {
       if (lane == 0) {
@@ -274,6 +274,13 @@ SPEAR_DEVINL void schedule(const PrefillParams& p, Header& hd, int lane) {
       mbar_arrive(&hd.seg_full[i]);
     }
     __syncwarp();
+    if (n > 0)
+      for (int r = lane; r < g.rows; r += 32) {
+        const unsigned R = g.r0 + r, tok = div_group(p, R);
+        const __nv_bfloat16* q = p.a.q + (int64_t)(g.row + tok) * p.a.ld_q + (int64_t)(g.h * p.v.group + R - tok * p.v.group) * D;
+#pragma unroll
+        for (int x = 0; x < D; x += 64) prefetch_l2_line(q + x);
+      }
     ++n;
   }
   if (lane == 0) p.joins[cta] = join;
@@ -570,24 +577,24 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     unsigned n_s = 0, n_o = 0;
     bool ok = true;
 
-    // this warp's 32 rows of an item into the Q tile: D / 8 lanes a row, 16 bytes each, eight loads in flight
+    // this warp's 32 rows of an item into the Q tile: D / 8 lanes a row, 16 bytes each, all loads in flight
     auto load_q = [&](const Segment& x) {
       constexpr int C = D / 8, RPI = 32 / C, N = C;  // N = 32 / RPI loads a lane
 #pragma unroll
-      for (int b0 = 0; b0 < N; b0 += 8) {
-        uint4 w[8];
+      for (int b0 = 0; b0 < N; b0 += N) {
+        uint4 w[N];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < N; ++j) {
           const int in_item = 128 * i + 32 * quarter + (b0 + j) * RPI + lane / C;
           w[j] = make_uint4(0, 0, 0, 0);
           if (in_item < x.rows) {
-            const unsigned R = x.r0 + in_item, tok = R / (unsigned)p.v.group;
+            const unsigned R = x.r0 + in_item, tok = div_group(p, R);
             w[j] = *reinterpret_cast<const uint4*>(p.a.q + (int64_t)(x.row + tok) * p.a.ld_q +
                                                    (int64_t)(x.h * p.v.group + R - tok * p.v.group) * D + (lane % C) * 8);
           }
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < N; ++j) {
           const int rr = 32 * quarter + (b0 + j) * RPI + lane / C, ch = lane % C;
           uint4 o;
           o.x = __byte_perm(w[j].x, w[j].z, 0x5410) ^ flip;
@@ -615,11 +622,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         continue;
       }
       const int in_item = min(128 * i + row, g.rows - 1);
-      const unsigned R = g.r0 + in_item, tok = R / (unsigned)p.v.group;
+      const unsigned R = g.r0 + in_item, tok = div_group(p, R);
       const int hi = g.pos0 + (int)tok;  // last key that this row sees
       // keys that every row of the half sees
-      const int all_hi = g.pos0 + (g.r0 + 128 * i) / p.v.group;
-      const int all_lo = p.a.window > 0 ? g.pos0 + (g.r0 + min(128 * i + 127, g.rows - 1)) / p.v.group - p.a.window + 1 : 0;
+      const int all_hi = g.pos0 + (int)div_group(p, g.r0 + 128 * i);
+      const int all_lo = p.a.window > 0 ? g.pos0 + (int)div_group(p, g.r0 + min(128 * i + 127, g.rows - 1)) - p.a.window + 1 : 0;
       float m = -INFINITY, l = 0.f;
       for (int k = 0; k < g.len; ++k) {
         const int key0 = (g.tile0 + k) * kTile;
@@ -783,12 +790,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
 }
 
 // Joins the partial results of an item that several CTAs share, in their
-// order: block (CTA that starts the item, 32 rows), a row a lane, D / 8
-// columns a warp. Bound by the partial results' bytes, which come from L2.
+// order: block (CTA that starts the item, 32 rows), a row a lane, 8 columns a
+// warp, four shares' loads in flight. Bound by the partial results' bytes,
+// which come from L2.
 template <int D>
-__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ PrefillParams p) {
+__global__ void __launch_bounds__(4 * D) join_kernel(const __grid_constant__ PrefillParams p) {
   constexpr int kPart = (D + 2) * 128;
-  constexpr int N = D / 8;
+  constexpr int N = 8, U = 4;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int64_t first = blockIdx.x;
   const Join j = p.joins[first];
@@ -796,37 +804,48 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Prefi
   const int in_item = blockIdx.y * kJoinRows + lane, half = in_item / 128;
   if (blockIdx.y * kJoinRows >= (j.parts ? j.rows : 0)) return;
   const float sl = fmaxf(fabsf(p.a.scale_log2), 1e-30f);
-  auto part = [&](int x) { return p.part + (((first + x) * 2 + (x == 0)) * 2 + half) * kPart + in_item % 128; };
-  float M = -INFINITY;
-  for (int x = 0; x < j.parts; ++x) M = fmaxf(M, __ldcg(part(x) + D * 128));
-  float L = 0.f, o[N];
+  float M = -INFINITY, L = 0.f, o[N];
 #pragma unroll
   for (int y = 0; y < N; ++y) o[y] = 0.f;
-#pragma unroll 2
-  for (int x = 0; x < j.parts; ++x) {
-    const float* q = part(x);
-    const float m = __ldcg(q + D * 128), l = __ldcg(q + (D + 1) * 128);
-    float v[N];
+  for (int x0 = 0; x0 < j.parts; x0 += U) {
+    float m[U], l[U], v[U][N];
 #pragma unroll
-    for (int y = 0; y < N; ++y) v[y] = __ldcg(q + (warp * N + y) * 128);
-    // a share in which the row saw nothing but NaN keeps l and its sums as they are
-    const float f = m == -INFINITY ? (l == 0.f ? 0.f : 1.f) : ex2((m - M) * sl);
-    L = fmaf(f, l, L);
+    for (int x = 0; x < U; ++x) {
+      const int xx = x0 + x;
+      m[x] = -INFINITY, l[x] = 0.f;
+      if (xx < j.parts) {
+        const float* q = p.part + (((first + xx) * 2 + (xx == 0)) * 2 + half) * kPart + in_item % 128;
+        m[x] = __ldcg(q + D * 128);
+        l[x] = __ldcg(q + (D + 1) * 128);
 #pragma unroll
-    for (int y = 0; y < N; ++y) o[y] = l == 0.f ? o[y] : fmaf(f, v[y], o[y]);
+        for (int y = 0; y < N; ++y) v[x][y] = __ldcg(q + (warp * N + y) * 128);
+      } else {
+#pragma unroll
+        for (int y = 0; y < N; ++y) v[x][y] = 0.f;
+      }
+    }
+    const float top = fmaxf(fmaxf(M, fmaxf(m[0], m[1])), fmaxf(m[2], m[3]));
+    const float f0 = M == -INFINITY ? 1.f : ex2((M - top) * sl);  // nothing, or a NaN, so far: as it is
+    M = top;
+    L *= f0;
+#pragma unroll
+    for (int y = 0; y < N; ++y) o[y] *= f0;
+#pragma unroll
+    for (int x = 0; x < U; ++x) {
+      const float f = m[x] == -INFINITY ? (l[x] == 0.f ? 0.f : 1.f) : ex2((m[x] - M) * sl);
+      L = fmaf(f, l[x], L);
+#pragma unroll
+      for (int y = 0; y < N; ++y) o[y] = l[x] == 0.f ? o[y] : fmaf(f, v[x][y], o[y]);
+    }
   }
   if (in_item >= j.rows) return;
   const float inv = L == 0.f ? 0.f : 1.f / L;
-  const unsigned R = j.r0 + in_item, tok = R / (unsigned)p.v.group;
+  const unsigned R = j.r0 + in_item, tok = div_group(p, R);
   __nv_bfloat16* dst = p.a.out + (int64_t)(j.row + tok) * p.a.ld_out +
                        (int64_t)(j.h * p.v.group + R - tok * p.v.group) * D + warp * N;
 #pragma unroll
-  for (int x = 0; x < N; x += 8) {
-    float f[8];
-#pragma unroll
-    for (int y = 0; y < 8; ++y) f[y] = o[x + y] * inv;
-    *reinterpret_cast<uint4*>(dst + x) = unpermute8(f);
-  }
+  for (int y = 0; y < N; ++y) o[y] *= inv;
+  *reinterpret_cast<uint4*>(dst) = unpermute8(o);
 }
 
 template <int D>
@@ -844,7 +863,7 @@ spear_status_t launch(const spear_kv_s* h, PrefillParams& p, cudaStream_t stream
   at.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(h->sm_count, kRows / kJoinRows);
-  cfg.blockDim = dim3(256);
+  cfg.blockDim = dim3(4 * D);
   cfg.stream = stream;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
@@ -865,6 +884,7 @@ spear_status_t kv_launch_prefill(const spear_kv_s* h, const KvAttnArgs& a, int m
   p.v = h->view;
   p.a = a;
   p.max_rows = max_rows;
+  p.inv_group = h->view.group > 1 ? (unsigned)((1ull << 32) / h->view.group) + 1u : 0u;
   p.part = static_cast<float*>(ws);
   p.joins = reinterpret_cast<Join*>(static_cast<char*>(ws) + part_bytes(h));
   p.wait_ns = 100000000ull;
