@@ -22,6 +22,33 @@ struct spear_kv_s {
   size_t ws_bytes;
 };
 
+// Launches a kernel that begins with kv_follow(): it is set up on the SMs while
+// the kernel before it on the stream ends.
+template <class... P, class... A>
+inline spear_status_t kv_launch(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                                const A&... args) {
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? SPEAR_OK : SPEAR_ERR_CUDA;
+}
+
+#ifdef __CUDACC__
+// Lets the next kernel be set up, and waits until the work before this one on
+// the stream has ended and is visible. Nothing outside the SM is touched before.
+SPEAR_DEVINL void kv_follow() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+#endif
+
 // Arguments of one attention call.
 struct KvAttnArgs {
   const __nv_bfloat16* q;

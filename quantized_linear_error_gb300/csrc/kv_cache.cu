@@ -69,6 +69,7 @@ struct AppendParams {
 template <int D, bool kInterleaved>
 __global__ void __launch_bounds__(kAppendThreads, 4) append_kernel(const __grid_constant__ AppendParams p) {
   constexpr int LPR = D / 8, U = 4;
+  kv_follow();
   const int sub = threadIdx.x % LPR, lane = threadIdx.x & 31;
   const int t = blockIdx.x * (kAppendThreads / LPR) + threadIdx.x / LPR;
   if (t >= p.T) return;  // whole groups leave: the shuffles below are within a group
@@ -202,6 +203,7 @@ __global__ void __launch_bounds__(kAppendThreads)
     read_kernel(const KvView v, const int64_t* __restrict__ slots, int T, int chunk, __nv_bfloat16* k_out,
                 __nv_bfloat16* v_out) {
   constexpr int LPR = D / 8, U = 4;
+  kv_follow();
   const int sub = threadIdx.x % LPR;
   const int t = blockIdx.x * (kAppendThreads / LPR) + threadIdx.x / LPR;
   if (t >= T) return;
@@ -331,8 +333,7 @@ spear_status_t spear_kv_append(spear_kv_t h, const void* q, int64_t ld_q, const 
   const dim3 blocks((unsigned)((T + per_block - 1) / per_block), (p.rows + p.chunk - 1) / p.chunk);
   auto* kernel = D == 128 ? (h->rope_interleaved ? append_kernel<128, true> : append_kernel<128, false>)
                           : (h->rope_interleaved ? append_kernel<64, true> : append_kernel<64, false>);
-  kernel<<<blocks, kAppendThreads, 0, stream>>>(p);
-  return cudaGetLastError() == cudaSuccess ? SPEAR_OK : SPEAR_ERR_CUDA;
+  return kv_launch(kernel, blocks, kAppendThreads, 0, stream, p);
 }
 
 spear_status_t spear_kv_read(spear_kv_t h, const int64_t* slots, int32_t T, void* k_out, void* v_out,
@@ -345,9 +346,8 @@ spear_status_t spear_kv_read(spear_kv_t h, const int64_t* slots, int32_t T, void
   const int rows = 2 * h->view.n_kv_heads, chunk = rows_per_group(h, T, rows, per_block);
   const dim3 blocks((unsigned)((T + per_block - 1) / per_block), (rows + chunk - 1) / chunk);
   auto* kernel = D == 128 ? read_kernel<128> : read_kernel<64>;
-  kernel<<<blocks, kAppendThreads, 0, stream>>>(h->view, slots, T, chunk, static_cast<__nv_bfloat16*>(k_out),
-                                                static_cast<__nv_bfloat16*>(v_out));
-  return cudaGetLastError() == cudaSuccess ? SPEAR_OK : SPEAR_ERR_CUDA;
+  return kv_launch(kernel, blocks, kAppendThreads, 0, stream, h->view, slots, T, chunk,
+                   static_cast<__nv_bfloat16*>(k_out), static_cast<__nv_bfloat16*>(v_out));
 }
 
 spear_status_t spear_kv_attention(spear_kv_t h, const void* q, int64_t ld_q, void* out, int64_t ld_out,

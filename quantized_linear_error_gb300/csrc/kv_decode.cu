@@ -211,6 +211,7 @@ __global__ void __launch_bounds__(kThreads, 4 / NT > 3 ? 3 : 4 / NT)
     fence_mbar_init();
   }
 
+  kv_follow();
   // ---- this CTA's units [u0, u1) and the item that u0 falls into; every warp on its own for up to 32 sequences,
   // so that nothing waits
   Cursor c;
@@ -684,8 +685,7 @@ spear_status_t launch(const spear_kv_s* h, DecodeParams& p, cudaStream_t stream)
   p.NS = kRoom < kMaxStages ? kRoom : kMaxStages;
   static_assert(kRoom >= 2, "two stages at least");
   const size_t smem = 512 + om + (size_t)p.NS * stage;
-  decode_kernel<D, NT><<<h->sm_count * kPerSm, kThreads, smem, stream>>>(p);
-  return cudaGetLastError() == cudaSuccess ? SPEAR_OK : SPEAR_ERR_CUDA;
+  return kv_launch(decode_kernel<D, NT>, dim3(h->sm_count * kPerSm), kThreads, smem, stream, p);
 }
 
 }  // namespace

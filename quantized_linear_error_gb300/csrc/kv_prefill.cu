@@ -373,6 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     tmem_relinquish();
   }
   __syncwarp();
+  kv_follow();
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
@@ -797,7 +798,7 @@ template <int D>
 __global__ void __launch_bounds__(4 * D) join_kernel(const __grid_constant__ PrefillParams p) {
   constexpr int kPart = (D + 2) * 128;
   constexpr int N = 8, U = 4;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  kv_follow();
   const int64_t first = blockIdx.x;
   const Join j = p.joins[first];
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
@@ -855,19 +856,9 @@ spear_status_t launch(const spear_kv_s* h, PrefillParams& p, cudaStream_t stream
   // at least half of an SM's shared memory, so that one CTA has its tensor memory for itself
   const size_t used = kHeader + 6 * (size_t)kTile * D * 2 + 2 * (size_t)kBlocksPerTile * 16 * (D + 8);
   const size_t smem = used > 116 * 1024 ? used : 116 * 1024;
-  prefill_kernel<D><<<h->sm_count, kThreads, smem, stream>>>(p);
-  if (cudaGetLastError() != cudaSuccess) return SPEAR_ERR_CUDA;
-  // launched ahead, so that it starts as soon as the last CTA ends
-  cudaLaunchAttribute at;
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(h->sm_count, kRows / kJoinRows);
-  cfg.blockDim = dim3(4 * D);
-  cfg.stream = stream;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, join_kernel<D>, p) == cudaSuccess ? SPEAR_OK : SPEAR_ERR_CUDA;
+  const spear_status_t st = kv_launch(prefill_kernel<D>, dim3(h->sm_count), kThreads, smem, stream, p);
+  if (st != SPEAR_OK) return st;
+  return kv_launch(join_kernel<D>, dim3(h->sm_count, kRows / kJoinRows), 4 * D, 0, stream, p);
 }
 
 }  // namespace
