@@ -40,6 +40,7 @@
 // bulk copy each, whatever the page size) into a ring of stages.
 #include <cuda_fp16.h>
 
+#include <algorithm>
 #include <atomic>
 #include <type_traits>
 
@@ -56,6 +57,8 @@ constexpr int kMaxStages = 16;
 constexpr int kItemCost = 3;                   // units: rows of q in, states joined, results out
 constexpr int kMinUnits = 6;                   // a CTA's, where there are few of them: joining costs as much as more tiles
 constexpr float kLazy = 8.f;
+// CTAs an SM: the accumulators and the rows of q take 3 D NT / 8 registers a thread
+constexpr int per_sm(int D, int NT) { return D * NT <= 128 ? 3 : (D * NT <= 256 ? 2 : 1); }
 
 struct DecodeParams {
   KvView v;
@@ -183,8 +186,7 @@ SPEAR_DEVINL int64_t scan_inclusive(int64_t x, int lane) {
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, 4 / NT > 3 ? 3 : 4 / NT)
-    decode_kernel(const __grid_constant__ DecodeParams p) {
+__global__ void __launch_bounds__(kThreads, per_sm(D, NT)) decode_kernel(const __grid_constant__ DecodeParams p) {
   constexpr int R = 8 * NT;
   constexpr int BB = 16 * (D + 8);
   constexpr int KW = D / 32;       // code words of a K row a lane
@@ -677,7 +679,7 @@ template <int D, int NT>
 spear_status_t launch(const spear_kv_s* h, DecodeParams& p, cudaStream_t stream) {
   static std::atomic<uint64_t> done{0};
   if (smem_limit_once(reinterpret_cast<const void*>(decode_kernel<D, NT>), done) != cudaSuccess) return SPEAR_ERR_CUDA;
-  constexpr int kPerSm = 4 / NT > 3 ? 3 : 4 / NT;
+  constexpr int kPerSm = per_sm(D, NT);
   constexpr uint32_t om = ((kWarps * 8 * NT * (2 + D + 4)) * 4 + 127) / 128 * 128;
   constexpr uint32_t stage = kBlocksPerTile * 16 * (D + 8);
   constexpr int kRoom = (227 * 1024 / kPerSm - 1024 - 512 - (int)om) / (int)stage;
@@ -693,9 +695,11 @@ spear_status_t launch(const spear_kv_s* h, DecodeParams& p, cudaStream_t stream)
 
 using namespace spear;
 
-// CTAs x rows is at most sm_count x 32 for every variant
 size_t kv_decode_workspace(const spear_kv_s* h) {
-  return (size_t)h->sm_count * 2 * 32 * (h->view.D + 2) * sizeof(float);
+  const int D = h->view.D;
+  int rows = 0;  // of all CTAs of an SM
+  for (int nt = 1; nt <= 4; nt *= 2) rows = std::max(rows, 8 * nt * per_sm(D, nt));
+  return (size_t)h->sm_count * 2 * rows * (D + 2) * sizeof(float);
 }
 
 spear_status_t kv_launch_decode(const spear_kv_s* h, const KvAttnArgs& a, int nt, float* part, unsigned* counters,
