@@ -20,9 +20,11 @@
 //  - V: transposed matrix loads of 16-bit words put four channels of two keys
 //    in a register, as the A operand of out^T = V^T p^T wants it; again the low
 //    nibbles and whole bytes enter, and the high nibbles are their difference,
-//    taken at the end. Codes are centred, lo - 8 and byte - 136, exact in bf16
-//    (small magnitudes: neither the fp32 sums nor the rounding of p S to bf16
-//    lose to a large common term); sum p (O + 8 S) is kept beside it in fp32.
+//    taken at the end. Codes are centred, lo - 8 and byte - 136, exact in 16
+//    bits (small magnitudes: neither the fp32 sums nor the rounding of p S lose
+//    to a large common term); sum p (O + 8 S) is kept beside it in fp32. p S is
+//    rounded to f16, 11 bits; 32 keys with a scale that could leave its range
+//    go through bf16, 8 bits, with the same accumulators.
 //    The scores' accumulator layout becomes p^T's operand layout by one 8 x 8
 //    transpose (movmatrix).
 //  - The running maximum is lazy: p = 2^(s - m) with any m that is at most 8
@@ -100,6 +102,12 @@ SPEAR_DEVINL void mma_f16_16816_first(float (&d)[4], const uint32_t (&a)[4], uin
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+SPEAR_DEVINL uint32_t f16x2_fma(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
 }
 
 SPEAR_DEVINL uint32_t pack_f16x2(float lo, float up) {
@@ -309,8 +317,6 @@ __global__ void __launch_bounds__(kThreads, per_sm(D, NT)) decode_kernel(const _
 
   // ---------------------------------------------------------------- consumers
   const int g = lane >> 2, t = lane & 3;
-  const uint32_t c_lo = 0xBD80BD80u;    // -8 * 2^-7
-  const uint32_t c_byte = 0xBF88BF88u;  // -136 * 2^-7
   int st = 0;
   unsigned phase = 0;
   bool bad = false;
@@ -404,6 +410,8 @@ __global__ void __launch_bounds__(kThreads, per_sm(D, NT)) decode_kernel(const _
       // this lane's row of the four 8 x 8 matrices of 16-bit words: key lane % 16 (its low 8 first), chunk lane / 8 % 2
       const uint32_t vrow = base + 8 * D + ((lane & 7) + (lane >> 4) * 8) * (D / 2) + ((lane >> 3) & 1) * 16;
       auto tile = [&](auto masked) {
+        // the value scale of one key a lane (past the end anything), looked at below
+        const uint32_t sv = lds32(base + (lane >> 4) * BB + 16 * D + 64 + 4 * (lane & 15));
         float sc[2][NT][4];
         // ---- scores
 #pragma unroll
@@ -460,7 +468,11 @@ __global__ void __launch_bounds__(kThreads, per_sm(D, NT)) decode_kernel(const _
             top[nt][k] = fmaxf(fmaxf(sc[0][nt][k], sc[0][nt][k + 2]), fmaxf(sc[1][nt][k], sc[1][nt][k + 2]));
             over |= top[nt][k] > m[nt][k] + kLazy;
           }
-        if (__any_sync(0xffffffffu, over)) {
+        // p S, p <= 2^8, is taken in f16 for scales of 2^-13 .. 2^7, in bf16 where one of the 32 keys has another
+        const bool odd = (uint16_t)(sv - 0x3900u) > 0x0A00u;
+        bool wide = false;
+        if (__any_sync(0xffffffffu, over || odd)) {  // one vote in nearly all cases
+          wide = __any_sync(0xffffffffu, odd);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -483,6 +495,7 @@ __global__ void __launch_bounds__(kThreads, per_sm(D, NT)) decode_kernel(const _
 #pragma unroll
           for (int k = 0; k < 2; ++k) mu[nt][k] = m[nt][k] == -INFINITY ? 0.f : m[nt][k];
         // ---- weights, and the values
+        auto values = [&](auto wide) {
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt) {
           const uint32_t blk = base + mt * BB;
@@ -506,8 +519,8 @@ __global__ void __launch_bounds__(kThreads, per_sm(D, NT)) decode_kernel(const _
               }
               off[nt][k] += o;
             }
-            bf[nt][0] = movmatrix(pack_bf16x2(w[0], w[1]));
-            bf[nt][1] = movmatrix(pack_bf16x2(w[2], w[3]));
+            bf[nt][0] = movmatrix(wide ? pack_bf16x2(w[0], w[1]) : pack_f16x2(w[0], w[1]));
+            bf[nt][1] = movmatrix(wide ? pack_bf16x2(w[2], w[3]) : pack_f16x2(w[2], w[3]));
           }
 #pragma unroll
           for (int i2 = 0; i2 < VW; ++i2) {
@@ -515,24 +528,39 @@ __global__ void __launch_bounds__(kThreads, per_sm(D, NT)) decode_kernel(const _
             // four channels of keys 2 t and 2 t + 1
             uint32_t y[4];
             ldmatrix_x4_trans(y, vrow + mt * BB + i2 * 32);
-            // even j: the low nibble of byte j / 2, lo - 8; odd j: all of the byte, lo + 16 hi - 136 (exact in bf16)
+            // even j: the low nibble of byte j / 2, (lo - 8) 2^-9; odd j: all of the byte, (lo + 16 hi - 136) 2^-9
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               uint32_t a[4];
 #pragma unroll
               for (int x = 0; x < 4; ++x) {
                 const uint32_t byte = j < 2 ? y[x] & 0x00FF00FFu : odd_bytes(y[x]);
-                a[x] = bf16x2_fma(j & 1 ? byte : byte & 0x000F000Fu, 0x7E807E80u /* 2^126 */, j & 1 ? c_byte : c_lo);
+                const uint32_t c = j & 1 ? byte : byte & 0x000F000Fu;
+                if constexpr (wide)
+                  a[x] = bf16x2_fma(c, 0x7D807D80u /* 2^124 */, j & 1 ? 0xBE88BE88u : 0xBC80BC80u);
+                else
+                  a[x] = f16x2_fma(c, 0x78007800u /* 2^15 */, j & 1 ? 0xB440B440u : 0xA400A400u);
               }
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) mma_bf16_16816(acc[i2 * 4 + j][nt], a, bf[nt][0], bf[nt][1]);
+              for (int nt = 0; nt < NT; ++nt) {
+                if constexpr (wide)
+                  mma_bf16_16816(acc[i2 * 4 + j][nt], a, bf[nt][0], bf[nt][1]);
+                else
+                  mma_f16_16816(acc[i2 * 4 + j][nt], a, bf[nt][0], bf[nt][1]);
+              }
             }
           }
         }
+        };
+        if (wide)
+          values(std::true_type{});
+        else
+          values(std::false_type{});
       };
       if (!bad && key0 < s.L) {
         // does some row not see all 32 keys?
-        if (key0 + 31 > s.L - s.n || (p.a.window > 0 && key0 <= s.L - 1 - p.a.window))
+        const bool masked = key0 + 31 > s.L - s.n || (p.a.window > 0 && key0 <= s.L - 1 - p.a.window);
+        if (masked)
           tile(std::true_type{});
         else
           tile(std::false_type{});
@@ -565,10 +593,10 @@ __global__ void __launch_bounds__(kThreads, per_sm(D, NT)) decode_kernel(const _
             float4 o4;
             const int e = k + 2 * y;
             const float a0 = acc[i2 * 4][nt][e], a2 = acc[i2 * 4 + 2][nt][e];
-            o4.x = fmaf(a0, 128.f, off[nt][k]);
-            o4.y = fmaf(acc[i2 * 4 + 1][nt][e] - a0, 8.f, off[nt][k]);  // (byte - lo) / 16
-            o4.z = fmaf(a2, 128.f, off[nt][k]);
-            o4.w = fmaf(acc[i2 * 4 + 3][nt][e] - a2, 8.f, off[nt][k]);
+            o4.x = fmaf(a0, 512.f, off[nt][k]);
+            o4.y = fmaf(acc[i2 * 4 + 1][nt][e] - a0, 32.f, off[nt][k]);  // (byte - lo) / 16
+            o4.z = fmaf(a2, 512.f, off[nt][k]);
+            o4.w = fmaf(acc[i2 * 4 + 3][nt][e] - a2, 32.f, off[nt][k]);
             *reinterpret_cast<float4*>(dst + i2 * 64 + y * 32) = o4;
           }
       }

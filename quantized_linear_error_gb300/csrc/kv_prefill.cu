@@ -573,7 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     const int row = 32 * quarter + lane;  // of the half
     const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
     const uint32_t s_t = tmem + lanes + 128 * i, o_t = tmem + lanes + 256 + 128 * i;
-    const float sl = fmaxf(fabsf(p.a.scale_log2), 1e-30f);  // 0 x infinity of a masked score is a NaN
+    const float sl = fmaxf(fabsf(p.a.scale_log2), 1e-37f);  // 0 x infinity of a masked score is a NaN
     const uint32_t flip = p.a.scale_log2 < 0.f ? 0x80008000u : 0u;
     unsigned n_s = 0, n_o = 0;
     bool ok = true;
@@ -804,7 +804,7 @@ __global__ void __launch_bounds__(4 * D) join_kernel(const __grid_constant__ Pre
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
   const int in_item = blockIdx.y * kJoinRows + lane, half = in_item / 128;
   if (blockIdx.y * kJoinRows >= (j.parts ? j.rows : 0)) return;
-  const float sl = fmaxf(fabsf(p.a.scale_log2), 1e-30f);
+  const float sl = fmaxf(fabsf(p.a.scale_log2), 1e-37f);
   float M = -INFINITY, L = 0.f, o[N];
 #pragma unroll
   for (int y = 0; y < N; ++y) o[y] = 0.f;

@@ -245,3 +245,21 @@ def test_scores_far_below_zero():
         b = Batch([(n, L)], 4, 2, 64, 16, edit=edit, seed=n)
         b.q = -b.q.abs() - 1
         b.check(b.run(window=window, scale=1.0), window, 1.0)
+
+
+@pytest.mark.parametrize("size", [1e-30, 1e-6, 1e-3, 1e3, 1e6, 1e30])
+def test_values_of_any_size(size):
+    """Values, keys or both of a size that f16 does not hold, all of them or one token's, beside ordinary ones."""
+    for n, L in [(1, 300), (3, 200), (80, 300)]:
+        for which in ("v", "one v", "k", "one k"):
+            def edit(i, k, v):
+                if which == "v":
+                    v *= size
+                elif which == "one v":
+                    v[L // 2] *= size
+                elif which == "k":
+                    k *= size
+                else:
+                    k[L // 2] *= min(size, 1e3)
+            scale = 128 ** -0.5 / (size if which == "k" else 1)
+            _check([(n, L)], 4, 2, 128, 16, edit=edit, scale=scale, seed=n)
