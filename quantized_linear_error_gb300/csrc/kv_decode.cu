@@ -104,18 +104,6 @@ SPEAR_DEVINL void mma_f16_16816_first(float (&d)[4], const uint32_t (&a)[4], uin
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 
-SPEAR_DEVINL uint32_t f16x2_fma(uint32_t a, uint32_t b, uint32_t c) {
-  uint32_t r;
-  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
-  return r;
-}
-
-SPEAR_DEVINL uint32_t pack_f16x2(float lo, float up) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(up), "f"(lo));
-  return r;
-}
-
 // Bytes 1 and 3 of x as two 16-bit halves.
 SPEAR_DEVINL uint32_t odd_bytes(uint32_t x) { return __byte_perm(x, 0, 0x4341); }
 

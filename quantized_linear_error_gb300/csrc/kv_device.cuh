@@ -12,6 +12,18 @@ SPEAR_DEVINL float ex2(float x) {
   return y;
 }
 
+SPEAR_DEVINL uint32_t f16x2_fma(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+
+SPEAR_DEVINL uint32_t pack_f16x2(float lo, float up) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(up), "f"(lo));
+  return r;
+}
+
 // Two fp32 operations in one instruction, on register pairs.
 SPEAR_DEVINL uint64_t pack_b32x2(uint32_t a, uint32_t b) {
   uint64_t r;

@@ -4,37 +4,46 @@
 // For each (sequence, key/value head) the rows are the query tokens times the
 // heads that share it, in tiles of 256 (two MMA tiles of 128); a row meets its
 // visible keys in tiles of 128:
-//   S = Q K^T (fp32, tensor memory), P = 2^(scale (S - m)) (bf16, written over
-//   S), O += P V (fp32, tensor memory), l += sum P;  out = O / l.
+//   S = Q K^T (fp32, tensor memory), P = 2^(scale (S - m)) (16 bits, written
+//   over S), O += P V (fp32, tensor memory), l += sum P;  out = O / l.
 // Bound by the tensor cores, 4 D flops a (row, key) pair, with the smaller
 // units close behind: per 256 x 128 block of D = 128 the MMAs take 2048 cycles
 // of an SM, their operands in shared memory 1536 at 128 bytes a cycle, the
-// dequantised tiles' stores 512.
+// dequantised tiles' stores 512; a block takes some 2800 here, the chain
+// scores, weights, product of one half being longer than the other half's
+// products that hide it.
 //
-//  - Dequantisers (4 warps, one key a thread) turn a tile's packed rows into
-//    bf16 code * scale + offset, rounded once, in 128-byte-swizzled shared
-//    memory. Both tiles are stored key by key: K is the K-major B operand of
-//    S, V the MN-major B operand of O, so nothing is transposed. A code word's
-//    pairs come out as elements (0, 4), (1, 5), (2, 6), (3, 7); Q's rows are
-//    permuted alike, and O's columns are put back in the epilogue. Keys past
-//    the sequence's end become zeros, and a key whose V is not finite is moved
-//    to its K (V zero, K NaN): rows that see it get NaN, the mask keeps it from
-//    the others (0 x NaN in O += P V would not).
+//  - Operands are f16, whose 11 bits hold queries and codes' values with an
+//    error far below that of the bf16 result (bf16 operands doubled it). Rows
+//    of Q are scaled by a power of two each. 32 keys at a time may leave f16's
+//    range: their K are scaled by a power of two each, which the softmax takes
+//    back from their columns, and their V and P go through bf16.
+//  - Dequantisers (8 warps, two threads a key) turn a tile's packed rows into
+//    code * scale + offset, rounded once, in 128-byte-swizzled shared memory.
+//    Both tiles are stored key by key: K is the K-major B operand of S, V the
+//    MN-major B operand of O, so nothing is transposed. A code word's pairs come
+//    out as elements (0, 4), (1, 5), (2, 6), (3, 7); Q's rows are permuted
+//    alike, and O's columns are put back in the epilogue. Keys past the
+//    sequence's end become zeros, and a key whose V is not finite is moved to
+//    its K (V zero, K NaN): rows that see it get NaN, the mask keeps it from the
+//    others (0 x NaN in O += P V would not).
 //  - Two softmax warpgroups, one an MMA tile, one row a thread; P goes from
-//    registers to tensor memory. While one works on S the other's products run.
-//    m need not be the maximum: weights and sums keep their relative precision
-//    whatever their size, so that m is taken from a segment's first tile and
-//    again only when the weights of 64 keys sum to more than 2^16; no other
-//    tile takes a maximum.
-//  - One thread issues the MMAs, in the order O0 S0 O1 S1 of successive tiles:
-//    an S overwrites its P only after the product that reads it, which was
-//    issued before it.
-//  - One warp copies the packed tiles, a bulk copy a 16-token block.
+//    registers to tensor memory in two parts, so that the product with the
+//    first 64 keys runs while the other weights are computed. m need not be the
+//    maximum: weights and sums keep their relative precision whatever their
+//    size, so that m is taken from a segment's first tile and again only when
+//    the weights of 64 keys sum to more than 2^14; no other tile takes a maximum.
+//  - Two warps issue the MMAs, one a half, in turns "product of the last tile,
+//    scores of the next": an S overwrites its P only after the product that
+//    reads it, which the same warp issued before it.
+//  - One warp copies the packed tiles, a bulk copy a 16-token block; one lays
+//    out the CTA's work and fetches the coming query rows into L2.
 //
 // Work: (sequence, head, row tile, key tile) units in this order are split
-// evenly over the CTAs (one an SM). Items that several CTAs share leave
-// partial results, which a second small kernel joins in CTA order on all SMs
-// (the last CTA of an item to finish, on its own, took 12 us for it).
+// evenly over the CTAs (one an SM), an item (row tile) counting as four units
+// more than its key tiles. Items that several CTAs share leave partial results,
+// which a second small kernel joins in CTA order on all SMs (the last CTA of an
+// item to finish, on its own, took 12 us for it).
 #include <atomic>
 
 #include "kv_device.cuh"
@@ -52,7 +61,7 @@ constexpr int kItemCost = 4;          // units
 constexpr int kHeader = 1024;         // barriers, segments
 constexpr int kSegs = 4;              // segments in flight
 constexpr int kSegReaders = 8 + kDeqWarps + 2 + 1;  // warps that read each segment
-constexpr float kBig = 0x1p16f;
+constexpr float kBig = 0x1p14f;  // weights up to here fit f16
 constexpr uint32_t kHintNs = 100;
 // setmaxnreg: 256 x 168 + 384 x 48 registers are the 640 x 96 of the launch
 constexpr int kJoinRows = 32;
@@ -90,6 +99,9 @@ struct Header {
   uint64_t seg_full[kSegs], seg_empty[kSegs];
   Segment seg[kSegs];
   uint32_t tmem;
+  // of the last four tiles: per 32 keys bit 0, their K is scaled by 2^-exponent each; bit 1, their V is in bf16
+  uint8_t flags[4][4];
+  int8_t exponent[4][kTile];
 };
 static_assert(sizeof(Header) <= kHeader, "");
 
@@ -286,12 +298,22 @@ SPEAR_DEVINL void schedule(const PrefillParams& p, Header& hd, int lane) {
   if (lane == 0) p.joins[cta] = join;
 }
 
-// Eight codes of a word as four bf16 pairs, elements (0, 4), (1, 5), (2, 6), (3, 7): code * scale + offset, rounded
-// once. A masked nibble pair reads as tiny bf16 values (see decode_frag_unpack), which one exact multiplication
-// brings to c 2^-7 or c 2^-3; s_lo = scale 2^7, s_hi = scale 2^3.
-SPEAR_DEVINL uint4 dequant8(uint32_t w, uint32_t s_lo, uint32_t s_hi, uint32_t oo) {
+// Eight codes of a word as four pairs, elements (0, 4), (1, 5), (2, 6), (3, 7): code * scale + offset, rounded once.
+// f16: a nibble beneath the exponent of 1024 reads as 1024 + c, or + 16 c; c is taken out exactly.
+SPEAR_DEVINL uint4 dequant8_f16(uint32_t w, uint32_t ss, uint32_t oo) {
   const uint32_t u = w >> 8;
-  constexpr uint32_t k2p126 = 0x7E807E80u, k0 = 0x80008000u;  // x 2^126 - 0: c 2^-7 and (high nibbles) c 2^-3, exact
+  constexpr uint32_t k1024 = 0x64006400u, kNeg1024 = 0xE400E400u, kOne = 0x3C003C00u;
+  constexpr uint32_t k16th = 0x2C002C00u, kNeg64 = 0xD400D400u;
+  return make_uint4(f16x2_fma(f16x2_fma((w & 0x000F000Fu) | k1024, kOne, kNeg1024), ss, oo),
+                    f16x2_fma(f16x2_fma((w & 0x00F000F0u) | k1024, k16th, kNeg64), ss, oo),
+                    f16x2_fma(f16x2_fma((u & 0x000F000Fu) | k1024, kOne, kNeg1024), ss, oo),
+                    f16x2_fma(f16x2_fma((u & 0x00F000F0u) | k1024, k16th, kNeg64), ss, oo));
+}
+// bf16: a masked nibble pair reads as tiny values (see decode_frag_unpack), which one exact multiplication brings to
+// c 2^-7 or c 2^-3; s_lo = scale 2^7, s_hi = scale 2^3.
+SPEAR_DEVINL uint4 dequant8_bf16(uint32_t w, uint32_t s_lo, uint32_t s_hi, uint32_t oo) {
+  const uint32_t u = w >> 8;
+  constexpr uint32_t k2p126 = 0x7E807E80u, k0 = 0x80008000u;  // x 2^126 - 0
   return make_uint4(bf16x2_fma(bf16x2_fma(w & 0x000F000Fu, k2p126, k0), s_lo, oo),
                     bf16x2_fma(bf16x2_fma(w & 0x00F000F0u, k2p126, k0), s_hi, oo),
                     bf16x2_fma(bf16x2_fma(u & 0x000F000Fu, k2p126, k0), s_lo, oo),
@@ -303,12 +325,10 @@ SPEAR_DEVINL void sts128(uint32_t addr, const uint4& v) {
                : "memory");
 }
 
-// Half `half` of one key's row: codes (D / 2 bytes at `src`) to row `key` of a swizzled tile.
-template <int D>
-SPEAR_DEVINL void dequant_row(uint32_t src, uint32_t tile, int key, int half, uint32_t par) {
-  const float sc = __uint_as_float(par << 16);
-  const uint32_t s_lo = pack_bf16x2(sc * 128.f, sc * 128.f), s_hi = pack_bf16x2(sc * 8.f, sc * 8.f);
-  const uint32_t oo = __byte_perm(par, par, 0x3232);
+// Half `half` of one key's row: codes (D / 2 bytes at `src`) to row `key` of a swizzled tile, `convert` turning a word
+// into 16 bytes.
+template <int D, class F>
+SPEAR_DEVINL void dequant_row(uint32_t src, uint32_t tile, int key, int half, F convert) {
   constexpr int Q = D / 64;  // 16-byte quarters of the packed row a thread
 #pragma unroll
   for (int i = 0; i < Q; ++i) {
@@ -319,8 +339,14 @@ SPEAR_DEVINL void dequant_row(uint32_t src, uint32_t tile, int key, int half, ui
     const uint32_t row = tile + (q >> 1) * (kTile * 128) + key * 128;
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      sts128(row + ((((q & 1) * 4 + j) ^ (key & 7)) * 16), dequant8(words[j], s_lo, s_hi, oo));
+      sts128(row + ((((q & 1) * 4 + j) ^ (key & 7)) * 16), convert(words[j]));
   }
+}
+
+// Whether a row with these parameters is safe in f16, 11 bits for its larger elements: scale in 2^-12 .. 2^10, offset
+// below 2^14 (the bit patterns of bf16 numbers order like the numbers).
+SPEAR_DEVINL bool fits_f16(uint32_t par) {
+  return (uint16_t)(par - 0x3980u) < 0x0B00u && (par & 0x7FFF0000u) < 0x46800000u;
 }
 
 SPEAR_DEVINL bool finite_par(uint32_t par) {
@@ -448,8 +474,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       // -------------------------------------------------------------- MMA issue, one warp a half, uniform
       const int i = warp - 16;
       const uint32_t leader = elect_leader();
-      const uint32_t idesc_s = idesc_bf16_f32(128, kTile);
-      const uint32_t idesc_o = idesc_bf16_f32(128, D) | kIdescBMnMajor;
+      const uint32_t idesc_s = idesc_f16_f32(128, kTile);
+      const uint32_t idesc_o = idesc_f16_f32(128, D) | kIdescBMnMajor;
+      constexpr uint32_t kHalfWide = (idesc_bf16_f32(128, D) - idesc_f16_f32(128, D)) / 2;
       // a descriptor's address field counts 16 bytes and holds any shared-memory address: steps are added to it
       const uint64_t q_desc = sw128_kmajor_desc(q_at + i * kTileBytes), k_desc = sw128_kmajor_desc(k_at);
       const uint64_t v_desc = sw128_mnmajor_desc(v_at, kTile * 128);
@@ -497,6 +524,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
             mbar_arrive(&hd.k_empty[st]);
           }
           if (leader) mbar_arrive(&hd.turn[i ^ 1]);
+          // (a reduction's result is uniform for the compiler, so that the descriptors below stay in uniform registers)
+          const uint32_t flags =
+              __reduce_or_sync(0xffffffffu, *reinterpret_cast<const volatile uint32_t*>(hd.flags[kc & 3]));
           // what the turn needs, before taking it: the next K tile (dequantised after this V tile) or this V tile
           if (more || k + 1 < len ? !wait(&hd.k_full[st ^ 1u], ((kc + 1) >> 1) & 1u) : !wait(&hd.v_full[st], ph)) break;
           if (!take_turn()) break;
@@ -509,7 +539,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
               tc_fence_after_sync();
 #pragma unroll
               for (int kk = 4 * x; kk < 4 * x + 4; ++kk)
-                umma_ts_bf16(leader, o_d, s_d + 8 * kk, vd + kk * (2048 >> 4), idesc_o, kk == 0 ? (k != 0) : 1u);
+                umma_ts_bf16(leader, o_d, s_d + 8 * kk, vd + kk * (2048 >> 4),
+                             idesc_o + (flags >> (8 * (kk / 2)) & 2u) * kHalfWide, kk == 0 ? (k != 0) : 1u);
               if (x == 0) umma_commit(leader, &hd.pa_done[i]);
             }
             if (!ok) break;
@@ -542,21 +573,54 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         const uint32_t blk = blk_at + st * kRawBytes;
         ok = warp_wait(&hd.raw_full[st], ph, p.wait_ns, kHintNs);
         if (!ok) break;
-        uint32_t kp = 0, vp = 0;
+        uint32_t kp = 0, vp = 0;  // of a key past the end: zeros
         if ((g.tile0 + t) * kTile + key < g.L) {
           kp = lds32(blk + 16 * D + 4 * r);
           vp = lds32(blk + 16 * D + 64 + 4 * r);
-          if (!finite_par(vp)) vp = 0, kp = 0x7FC07FC0u;
         }
         ok = k < 2 || warp_wait(&hd.k_empty[st], ph ^ 1u, p.wait_ns, kHintNs);
         if (!ok) break;
-        dequant_row<D>(blk + r * (D / 2), k_at + st * kTileBytes, key, half, kp);
+        auto put_k = [&](float ks, float ko) {
+          const uint32_t ks2 = pack_f16x2(ks, ks), ko2 = pack_f16x2(ko, ko);
+          dequant_row<D>(blk + r * (D / 2), k_at + st * kTileBytes, key, half,
+                         [&](uint32_t w) { return dequant8_f16(w, ks2, ko2); });
+        };
+        put_k(__uint_as_float(kp << 16), __uint_as_float(kp & 0xFFFF0000u));
+        uint32_t odd = 0;
+        if (__any_sync(0xffffffffu, !fits_f16(kp) || !fits_f16(vp))) {  // the end, or parameters out of f16's range
+          if (!finite_par(vp)) vp = 0, kp = 0x7FC07FC0u;
+          if (!finite_par(kp)) kp = 0x7FC07FC0u;
+          const bool k_odd = kp != 0 && kp != 0x7FC07FC0u && !fits_f16(kp);
+          odd = __any_sync(0xffffffffu, vp != 0 && !fits_f16(vp)) ? 2u : 0u;
+          float ks = __uint_as_float(kp << 16), ko = __uint_as_float(kp & 0xFFFF0000u);
+          int e = 0;
+          if (k_odd) {  // the row's largest element goes to 1 .. 2
+            const float top = fmaxf(fabsf(ko), fabsf(fmaf(15.f, ks, ko)));
+            e = max((int)(__float_as_uint(top) >> 23), 1) - 127;
+            const float f = __uint_as_float((uint32_t)(127 - e) << 23);
+            ks *= f, ko *= f;
+          }
+          odd |= __any_sync(0xffffffffu, k_odd) ? 1u : 0u;
+          if (half == 0 && (odd & 1u)) hd.exponent[k & 3][key] = (int8_t)e;
+          put_k(ks, ko);
+        }
+        if (half == 0 && lane == 0) hd.flags[k & 3][key / 32] = (uint8_t)odd;
+        const bool wide_v = odd & 2u;
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&hd.k_full[st]);
         ok = k < 2 || warp_wait(&hd.v_empty[st], ph ^ 1u, p.wait_ns, kHintNs);
         if (!ok) break;
-        dequant_row<D>(blk + 8 * D + r * (D / 2), v_at + st * kTileBytes, key, half, vp);
+        const uint32_t v_src = blk + 8 * D + r * (D / 2), v_dst = v_at + st * kTileBytes;
+        const float vs = __uint_as_float(vp << 16), vo = __uint_as_float(vp & 0xFFFF0000u);
+        if (!wide_v) {
+          const uint32_t vs2 = pack_f16x2(vs, vs), vo2 = pack_f16x2(vo, vo);
+          dequant_row<D>(v_src, v_dst, key, half, [&](uint32_t w) { return dequant8_f16(w, vs2, vo2); });
+        } else {
+          const uint32_t s_lo = pack_bf16x2(vs * 128.f, vs * 128.f), s_hi = pack_bf16x2(vs * 8.f, vs * 8.f);
+          const uint32_t vo2 = pack_bf16x2(vo, vo);
+          dequant_row<D>(v_src, v_dst, key, half, [&](uint32_t w) { return dequant8_bf16(w, s_lo, s_hi, vo2); });
+        }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
@@ -573,37 +637,54 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     const int row = 32 * quarter + lane;  // of the half
     const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
     const uint32_t s_t = tmem + lanes + 128 * i, o_t = tmem + lanes + 256 + 128 * i;
-    const float sl = fmaxf(fabsf(p.a.scale_log2), 1e-37f);  // 0 x infinity of a masked score is a NaN
-    const uint32_t flip = p.a.scale_log2 < 0.f ? 0x80008000u : 0u;
-    unsigned n_s = 0, n_o = 0;
+    const float scale = fabsf(p.a.scale_log2);
+    const float sign = p.a.scale_log2 < 0.f ? -1.f : 1.f;
+    float sl = 0.f, sl_next = 0.f;  // scale over the row's factor in the Q tile, not 0 (x infinity of a masked score)
+    unsigned n_s = 0, n_o = 0, tiles = 0;  // tiles: of the CTA, as the dequantisers count them
     bool ok = true;
 
-    // this warp's 32 rows of an item into the Q tile: D / 8 lanes a row, 16 bytes each, all loads in flight
+    // This warp's 32 rows of an item into the Q tile: D / 8 lanes a row, 16 bytes each, all loads in flight. A row is
+    // scaled by a power of two that brings its largest element to 2^7 .. 2^8, so that f16 holds its bf16 values.
     auto load_q = [&](const Segment& x) {
       constexpr int C = D / 8, RPI = 32 / C, N = C;  // N = 32 / RPI loads a lane
+      uint4 w[N];
 #pragma unroll
-      for (int b0 = 0; b0 < N; b0 += N) {
-        uint4 w[N];
-#pragma unroll
-        for (int j = 0; j < N; ++j) {
-          const int in_item = 128 * i + 32 * quarter + (b0 + j) * RPI + lane / C;
-          w[j] = make_uint4(0, 0, 0, 0);
-          if (in_item < x.rows) {
-            const unsigned R = x.r0 + in_item, tok = div_group(p, R);
-            w[j] = *reinterpret_cast<const uint4*>(p.a.q + (int64_t)(x.row + tok) * p.a.ld_q +
-                                                   (int64_t)(x.h * p.v.group + R - tok * p.v.group) * D + (lane % C) * 8);
-          }
+      for (int j = 0; j < N; ++j) {
+        const int in_item = 128 * i + 32 * quarter + j * RPI + lane / C;
+        w[j] = make_uint4(0, 0, 0, 0);
+        if (in_item < x.rows) {
+          const unsigned R = x.r0 + in_item, tok = div_group(p, R);
+          w[j] = *reinterpret_cast<const uint4*>(p.a.q + (int64_t)(x.row + tok) * p.a.ld_q +
+                                                 (int64_t)(x.h * p.v.group + R - tok * p.v.group) * D + (lane % C) * 8);
         }
+      }
+      uint32_t top[N / 2];  // the rows' largest magnitudes as bf16, of loads j and j + N / 2
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-          const int rr = 32 * quarter + (b0 + j) * RPI + lane / C, ch = lane % C;
-          uint4 o;
-          o.x = __byte_perm(w[j].x, w[j].z, 0x5410) ^ flip;
-          o.y = __byte_perm(w[j].x, w[j].z, 0x7632) ^ flip;
-          o.z = __byte_perm(w[j].y, w[j].w, 0x5410) ^ flip;
-          o.w = __byte_perm(w[j].y, w[j].w, 0x7632) ^ flip;
-          sts128(q_at + i * kTileBytes + (ch / 8) * (128 * 128) + rr * 128 + (((ch % 8) ^ (rr & 7)) * 16), o);
-        }
+      for (int j = 0; j < N / 2; ++j) {
+        auto largest = [](const uint4& x) {
+          constexpr uint32_t kAbs = 0x7FFF7FFFu;
+          const uint32_t t = __vmaxu2(__vmaxu2(x.x & kAbs, x.y & kAbs), __vmaxu2(x.z & kAbs, x.w & kAbs));
+          return max(t & 0xFFFFu, t >> 16);
+        };
+        top[j] = largest(w[j]) | (largest(w[j + N / 2]) << 16);
+#pragma unroll
+        for (int o = 1; o < C; o <<= 1) top[j] = __vmaxu2(top[j], __shfl_xor_sync(0xffffffffu, top[j], o));
+      }
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        const uint32_t eb = (j < N / 2 ? top[j % (N / 2)] & 0xFFFFu : top[j % (N / 2)] >> 16) >> 7;  // exponent
+        const uint32_t es = eb == 255u ? 127u : min(261u - eb, 254u);  // not finite: as it is
+        const float f = sign * __uint_as_float(es << 23);
+        const uint32_t mine = __shfl_sync(0xffffffffu, es, lane % RPI * C);
+        if (lane / RPI == j) sl_next = fmaxf(scale * __uint_as_float((254u - mine) << 23), 1e-37f);
+        const int rr = 32 * quarter + j * RPI + lane / C, ch = lane % C;
+        auto pair = [&](uint32_t a, uint32_t b, bool up) {
+          return up ? pack_f16x2(f * __uint_as_float(a & 0xFFFF0000u), f * __uint_as_float(b & 0xFFFF0000u))
+                    : pack_f16x2(f * __uint_as_float(a << 16), f * __uint_as_float(b << 16));
+        };
+        const uint4 o = make_uint4(pair(w[j].x, w[j].z, false), pair(w[j].x, w[j].z, true), pair(w[j].y, w[j].w, false),
+                                   pair(w[j].y, w[j].w, true));
+        sts128(q_at + i * kTileBytes + (ch / 8) * (128 * 128) + rr * 128 + (((ch % 8) ^ (rr & 7)) * 16), o);
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -617,6 +698,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     while (more && ok) {
       Segment nx;
       if (g.rows <= 128 * i) {  // a short item has no second half
+        tiles += g.len;
         more = read_segment(n++, nx);
         if (more && nx.rows > 128 * i) load_q(nx);
         g = nx;
@@ -629,112 +711,162 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       const int all_hi = g.pos0 + (int)div_group(p, g.r0 + 128 * i);
       const int all_lo = p.a.window > 0 ? g.pos0 + (int)div_group(p, g.r0 + min(128 * i + 127, g.rows - 1)) - p.a.window + 1 : 0;
       float m = -INFINITY, l = 0.f;
+      sl = sl_next;
       for (int k = 0; k < g.len; ++k) {
         const int key0 = (g.tile0 + k) * kTile;
         ok = warp_wait(&hd.s_full[i], n_s & 1u, p.wait_ns, kHintNs);
         if (!ok) break;
         ++n_s;
         tc_fence_after_sync();
-        uint32_t v[4][32];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) tmem_ld_x32(s_t + 32 * j, v[j]);
-        tmem_ld_wait();
+        const uint32_t flags = *reinterpret_cast<const volatile uint32_t*>(hd.flags[tiles & 3]);
+        const int8_t* exps = hd.exponent[tiles & 3];
+        ++tiles;
         const bool masked = key0 + kTile - 1 > all_hi || key0 < all_lo;
         const int d = hi - key0, e = p.a.window > 0 ? d - p.a.window : -1;  // visible: e < column <= d
-        auto mask = [&](int j) {
+        auto mask = [&](int j, uint32_t (&x32)[32]) {
           const int a = d - 32 * j, b = e - 32 * j;
           const uint32_t see = (a >= 31 ? 0xffffffffu : a < 0 ? 0u : (2u << a) - 1u) &
                                ~(b >= 31 ? 0xffffffffu : b < 0 ? 0u : (2u << b) - 1u);
 #pragma unroll
           for (int x = 0; x < 32; ++x)
-            if (!(see & (1u << x))) v[j][x] = 0xFF800000u;
+            if (!(see & (1u << x))) x32[x] = 0xFF800000u;
         };
-        if (masked) {
+        auto rescale = [&](float mx) {  // m becomes mx, what has been summed is scaled to it
+          const float f = m == -INFINITY ? 0.f : ex2((m - mx) * sl);
+          l *= f;
+          m = mx;
+#pragma unroll 1
+          for (int j = 0; j < D; j += 16) {
+            uint32_t o[16];
+            tmem_ld_x16(o_t + j, o);
+            tmem_ld_wait();
 #pragma unroll
-          for (int j = 0; j < 4; ++j) mask(j);
-        }
-        uint32_t w[32];
-        // weights of 64 keys by the present m, and their sum
-        auto weights = [&](int y) {
-          const float ms = m == -INFINITY ? 0.f : -m * sl;
-          const uint64_t sl2 = pack_f32x2(sl, sl), ms2 = pack_f32x2(ms, ms);
-          uint64_t sum2[2];
-#pragma unroll
-          for (int x = 0; x < 64; x += 2) {
-            const uint32_t* q = &v[2 * y + x / 32][x % 32];
-            float pa, pb;
-            unpack_f32x2(fma_f32x2(pack_b32x2(q[0], q[1]), sl2, ms2), pa, pb);
-            pa = ex2(pa);
-            pb = ex2(pb);
-            sum2[(x >> 1) & 1] = x < 4 ? pack_f32x2(pa, pb) : add_f32x2(sum2[(x >> 1) & 1], pack_f32x2(pa, pb));
-            w[x / 2] = pack_bf16x2(pa, pb);
+            for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
+            tmem_st_x16(o_t + j, o);
           }
-          float sa, sb;
-          unpack_f32x2(add_f32x2(sum2[0], sum2[1]), sa, sb);
-          return sa + sb;
         };
         auto hand_over = [&](int y) {
-          tmem_st_x32(s_t + 32 * y, w);
           tmem_st_wait();
           tc_fence_before_sync();
           __syncwarp();
           if (lane == 0) mbar_arrive(&hd.p_full[y][i]);
         };
-        // m becomes the row's maximum up to this tile, what has been summed is scaled to it, and the scores of the
-        // first or the last 64 keys are read again
-        auto new_maximum = [&](int y) {
+        bool done = false;
+        if (flags == 0) {
+          uint32_t v[4][32];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) tmem_ld_x32(s_t + 32 * j, v[j]);
+          tmem_ld_wait();
+          if (masked) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) mask(j, v[j]);
+          }
+          if (k == 0) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+              for (int x = 0; x < 32; x += 2)
+                m = fmaxf(m, fmaxf(__uint_as_float(v[j][x]), __uint_as_float(v[j][x + 1])));
+          }
+          uint32_t w[32];
+          // weights of 64 keys by the present m, and their sum
+          auto weights = [&](int y) {
+            const float ms = -m * sl;
+            const uint64_t sl2 = pack_f32x2(sl, sl), ms2 = pack_f32x2(ms, ms);
+            uint64_t sum2[2];
+#pragma unroll
+            for (int x = 0; x < 64; x += 2) {
+              const uint32_t* q = &v[2 * y + x / 32][x % 32];
+              float pa, pb;
+              unpack_f32x2(fma_f32x2(pack_b32x2(q[0], q[1]), sl2, ms2), pa, pb);
+              pa = ex2(pa);
+              pb = ex2(pb);
+              sum2[(x >> 1) & 1] = x < 4 ? pack_f32x2(pa, pb) : add_f32x2(sum2[(x >> 1) & 1], pack_f32x2(pa, pb));
+              w[x / 2] = pack_f16x2(pa, pb);
+            }
+            float sa, sb;
+            unpack_f32x2(add_f32x2(sum2[0], sum2[1]), sa, sb);
+            return sa + sb;
+          };
+          // The weights' size shows whether m will do: no maximum is taken as long as their sum stays below kBig (and
+          // m scale is small enough for the one rounding of weights())
+          float sum = weights(0);
+          if (!__any_sync(0xffffffffu, !(fabsf(m * sl) < 16777216.f) || sum > kBig)) {
+            tmem_st_x32(s_t, w);
+            hand_over(0);
+            l += sum;
+            sum = weights(1);
+            if (__any_sync(0xffffffffu, sum > kBig)) {
+              ok = warp_wait(&hd.pa_done[i], (n_s & 1u) ^ 1u, p.wait_ns, kHintNs);  // the product with the first weights
+              if (!ok) break;
+              tc_fence_after_sync();
+              float mx = m;
+#pragma unroll
+              for (int j = 2; j < 4; ++j) {
+                tmem_ld_x32(s_t + 32 * j, v[j]);
+                tmem_ld_wait();
+                if (masked) mask(j, v[j]);
+#pragma unroll
+                for (int x = 0; x < 32; ++x) mx = fmaxf(mx, __uint_as_float(v[j][x]));
+              }
+              rescale(mx);
+              sum = 0.f;
+#pragma unroll
+              for (int x = 0; x < 64; x += 2) {
+                const float pa = ex2((__uint_as_float(v[2 + x / 32][x % 32]) - m) * sl);
+                const float pb = ex2((__uint_as_float(v[2 + x / 32][x % 32 + 1]) - m) * sl);
+                sum += pa + pb;
+                w[x / 2] = pack_f16x2(pa, pb);
+              }
+            }
+            tmem_st_x32(s_t + 32, w);
+            hand_over(1);
+            l += sum;
+            done = true;
+          }
+        }
+        if (!done) {
+          // A new maximum, rows that have seen nothing, keys or values out of f16's range: 32 keys at a time, twice. (The product
+          // before has finished, s_full covers it; the next waits for this thread.)
           float mx = m;
 #pragma unroll 1
-          for (int j = 0; j < kTile; j += 32) {  // the first half may hold weights by now: its scores are in `m` then
-            if (y == 1 && j < 64) continue;
-            tmem_ld_x32(s_t + j, v[0]);
+          for (int j = 0; j < 4; ++j) {
+            uint32_t x32[32];
+            tmem_ld_x32(s_t + 32 * j, x32);
             tmem_ld_wait();
-            if (masked) {
-              const int a = d - j, b = e - j;
+            if (flags >> (8 * j) & 1u) {
 #pragma unroll
               for (int x = 0; x < 32; ++x)
-                if (x > a || x <= b) v[0][x] = 0xFF800000u;
+                x32[x] = __float_as_uint(__uint_as_float(x32[x]) * __uint_as_float((uint32_t)(exps[32 * j + x] + 127) << 23));
             }
+            if (masked) mask(j, x32);
 #pragma unroll
-            for (int x = 0; x < 32; ++x) mx = fmaxf(mx, __uint_as_float(v[0][x]));
+            for (int x = 0; x < 32; ++x) mx = fmaxf(mx, __uint_as_float(x32[x]));
+            if (flags || masked) tmem_st_x32(s_t + 32 * j, x32);
           }
-          if (k > 0 || y == 1) {
-            const float f = m == -INFINITY ? 0.f : ex2((m - mx) * sl);
-            l *= f;
+          tmem_st_wait();
+          if (k > 0)
+            rescale(mx);
+          else
+            m = mx;
+          const float mu = m == -INFINITY ? 0.f : m;
 #pragma unroll 1
-            for (int j = 0; j < D; j += 16) {
-              uint32_t o[16];
-              tmem_ld_x16(o_t + j, o);
-              tmem_ld_wait();
+          for (int j = 0; j < 4; ++j) {
+            uint32_t x32[32], w[16];
+            tmem_ld_x32(s_t + 32 * j, x32);
+            tmem_ld_wait();
+            const bool wide = flags >> (8 * j) & 2u;
 #pragma unroll
-              for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
-              tmem_st_x16(o_t + j, o);
+            for (int x = 0; x < 32; x += 2) {
+              const float pa = ex2((__uint_as_float(x32[x]) - mu) * sl);
+              const float pb = ex2((__uint_as_float(x32[x + 1]) - mu) * sl);
+              l += pa + pb;
+              w[x / 2] = wide ? pack_bf16x2(pa, pb) : pack_f16x2(pa, pb);
             }
+            tmem_st_x16(s_t + 16 * j, w);
+            if (j & 1) hand_over(j >> 1);
           }
-          m = mx;
-#pragma unroll
-          for (int j = 2 * y; j < 2 * y + 2; ++j) tmem_ld_x32(s_t + 32 * j, v[j]);
-          tmem_ld_wait();
-          if (masked) mask(2 * y), mask(2 * y + 1);
-        };
-        // The weights' size shows whether m will do: no maximum is taken as long as their sum stays below kBig
-        float sum = weights(0);
-        if (__any_sync(0xffffffffu, m == -INFINITY || sum > kBig)) {  // the first tile always
-          new_maximum(0);  // the previous product has finished (s_full covers it), the next waits for this thread
-          sum = weights(0);
         }
-        hand_over(0);
-        l += sum;
-        sum = weights(1);
-        if (__any_sync(0xffffffffu, sum > kBig)) {
-          ok = warp_wait(&hd.pa_done[i], (n_s & 1u) ^ 1u, p.wait_ns, kHintNs);  // the product with the first weights
-          if (!ok) break;
-          tc_fence_after_sync();
-          new_maximum(1);
-          sum = weights(1);
-        }
-        hand_over(1);
-        l += sum;
       }
       if (!ok) break;
       // the half's scores are done with its Q tile: the next item's rows go in while the last product runs
@@ -775,7 +907,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
 #pragma unroll
           for (int x = 0; x < 32; ++x) __stcg(slot + (j + x) * 128, __uint_as_float(o[x]));
         }
-        __stcg(slot + D * 128, m);
+        __stcg(slot + D * 128, m * sl);  // in units of log2: the row's factor is gone
         __stcg(slot + (D + 1) * 128, l);
       }
       tc_fence_before_sync();
@@ -804,7 +936,6 @@ __global__ void __launch_bounds__(4 * D) join_kernel(const __grid_constant__ Pre
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
   const int in_item = blockIdx.y * kJoinRows + lane, half = in_item / 128;
   if (blockIdx.y * kJoinRows >= (j.parts ? j.rows : 0)) return;
-  const float sl = fmaxf(fabsf(p.a.scale_log2), 1e-37f);
   float M = -INFINITY, L = 0.f, o[N];
 #pragma unroll
   for (int y = 0; y < N; ++y) o[y] = 0.f;
@@ -826,14 +957,14 @@ __global__ void __launch_bounds__(4 * D) join_kernel(const __grid_constant__ Pre
       }
     }
     const float top = fmaxf(fmaxf(M, fmaxf(m[0], m[1])), fmaxf(m[2], m[3]));
-    const float f0 = M == -INFINITY ? 1.f : ex2((M - top) * sl);  // nothing, or a NaN, so far: as it is
+    const float f0 = M == -INFINITY ? 1.f : ex2(M - top);  // nothing, or a NaN, so far: as it is
     M = top;
     L *= f0;
 #pragma unroll
     for (int y = 0; y < N; ++y) o[y] *= f0;
 #pragma unroll
     for (int x = 0; x < U; ++x) {
-      const float f = m[x] == -INFINITY ? (l[x] == 0.f ? 0.f : 1.f) : ex2((m[x] - M) * sl);
+      const float f = m[x] == -INFINITY ? (l[x] == 0.f ? 0.f : 1.f) : ex2(m[x] - M);
       L = fmaf(f, l[x], L);
 #pragma unroll
       for (int y = 0; y < N; ++y) o[y] = l[x] == 0.f ? o[y] : fmaf(f, v[x][y], o[y]);

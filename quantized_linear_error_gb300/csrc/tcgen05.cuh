@@ -61,6 +61,11 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int m_dim, int n_dim) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n_dim >> 3) << 17) | ((uint32_t)(m_dim >> 4) << 24);
 }
 
+// The same with f16 A and B (formats 0).
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int m_dim, int n_dim) {
+  return (1u << 4) | ((uint32_t)(n_dim >> 3) << 17) | ((uint32_t)(m_dim >> 4) << 24);
+}
+
 // ---------------------------------------------------------------- MMA
 // D[tmem] (+)= A[smem] * B[smem]^T, issued by a single thread.
 SPEAR_DEVINL void umma_bf16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {

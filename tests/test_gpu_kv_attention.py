@@ -263,3 +263,17 @@ def test_values_of_any_size(size):
                     k[L // 2] *= min(size, 1e3)
             scale = 128 ** -0.5 / (size if which == "k" else 1)
             _check([(n, L)], 4, 2, 128, 16, edit=edit, scale=scale, seed=n)
+
+
+@pytest.mark.parametrize("n,L", [(1, 200), (4, 200), (90, 200)])
+def test_queries_of_any_size(n, L):
+    """Rows of zeros, of subnormal and of huge values beside ordinary ones; a negative scale; rows with NaN or
+    infinities are NaN, their neighbours are not."""
+    b = Batch([(n, L)], 8, 2, 64, 16, seed=n)
+    for h, size in enumerate([0.0, 1e-39, 1e-20, 1e-3, 1.0, 1e3, 30.0]):
+        b.q[:, h] *= size
+    b.check(b.run(scale=-0.1), scale=-0.1)
+    b.q[:, 2] *= 1e30
+    b.q[0, 3, 5], b.q[0, 4, 7] = float("nan"), float("inf")
+    got = b.run().float()
+    assert torch.isnan(got[0, 3:5]).all() and torch.isfinite(got[0, [0, 1, 2, 5, 6, 7]]).all() and torch.isfinite(got[1:]).all()
