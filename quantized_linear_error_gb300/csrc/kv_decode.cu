@@ -51,16 +51,18 @@
 namespace spear {
 namespace {
 
-constexpr int kWarps = 4;                      // consumer warps
-constexpr int kThreads = 32 * (kWarps + 1);
-constexpr int kTile = 32 * kWarps;             // keys of a unit
+constexpr int kKeyWarps = 4;                   // consumer warps along the keys of a tile
+constexpr int kTile = 32 * kKeyWarps;          // keys of a unit
 constexpr int kBlocksPerTile = kTile / 16;
 constexpr int kMaxStages = 16;
 constexpr int kItemCost = 3;                   // units: rows of q in, states joined, results out
 constexpr int kMinUnits = 6;                   // a CTA's, where there are few of them: joining costs as much as more tiles
+constexpr int kScan = 10;                      // warps at most
 constexpr float kLazy = 8.f;
-// CTAs an SM: the accumulators and the rows of q take 3 D NT / 8 registers a thread
-constexpr int per_sm(int D, int NT) { return D * NT <= 128 ? 3 : (D * NT <= 256 ? 2 : 1); }
+// A variant: NT 8-row MMA tiles a warp, RG groups of warps with rows of their own over the same keys (four tiles in one
+// warp's registers spill and leave four warps an SM). CTAs an SM: the accumulators and the rows of q take 3 D NT / 8
+// registers a thread.
+constexpr int per_sm(int D, int NT, int RG) { return RG > 1 ? 1 : (D * NT <= 128 ? 3 : 2); }
 
 struct DecodeParams {
   KvView v;
@@ -113,7 +115,10 @@ SPEAR_DEVINL uint32_t movmatrix(uint32_t x) {
   return r;
 }
 
-SPEAR_DEVINL void consumer_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory"); }
+template <int kThreads>
+SPEAR_DEVINL void consumer_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
+}
 
 // Units of a sequence: per head its tiles and kItemCost for what an item costs beside them.
 SPEAR_DEVINL int64_t seq_units(const DecodeParams& p, const KvSeq& s) {
@@ -181,9 +186,11 @@ SPEAR_DEVINL int64_t scan_inclusive(int64_t x, int lane) {
   return x;
 }
 
-template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, per_sm(D, NT)) decode_kernel(const __grid_constant__ DecodeParams p) {
-  constexpr int R = 8 * NT;
+template <int D, int NT, int RG>
+__global__ void __launch_bounds__(32 * (kKeyWarps * RG + 1), per_sm(D, NT, RG))
+    decode_kernel(const __grid_constant__ DecodeParams p) {
+  constexpr int kWarps = kKeyWarps * RG, kThreads = 32 * (kWarps + 1);
+  constexpr int R = 8 * NT * RG;
   constexpr int BB = 16 * (D + 8);
   constexpr int KW = D / 32;       // code words of a K row a lane
   constexpr int VW = D / 64;       // code words of a V row a lane
@@ -193,11 +200,12 @@ __global__ void __launch_bounds__(kThreads, per_sm(D, NT)) decode_kernel(const _
   extern __shared__ __align__(128) uint8_t smem[];
   uint64_t* full = reinterpret_cast<uint64_t*>(smem);
   uint64_t* empty = full + kMaxStages;
-  int64_t* scan = reinterpret_cast<int64_t*>(empty + kMaxStages);  // [kWarps + 1] sums
-  int* found = reinterpret_cast<int*>(scan + 8);
-  float* ml = reinterpret_cast<float*>(smem + 512);                // [kWarps][R][2]
-  float* om = ml + kWarps * R * 2;                                 // [kWarps][R][OS]
-  const uint32_t om_bytes = (kWarps * R * (2 + OS)) * 4;
+  int64_t* scan = reinterpret_cast<int64_t*>(empty + kMaxStages);  // [kScan] sums
+  int* found = reinterpret_cast<int*>(scan + kScan);
+  static_assert(kWarps < kScan, "");
+  float* ml = reinterpret_cast<float*>(smem + 512);                // [kKeyWarps][R][2]
+  float* om = ml + kKeyWarps * R * 2;                              // [kKeyWarps][R][OS]
+  const uint32_t om_bytes = (kKeyWarps * R * (2 + OS)) * 4;
   const uint32_t stages_at = smem_u32(smem) + 512 + (om_bytes + 127) / 128 * 128;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid & 31;
 
@@ -305,6 +313,7 @@ __global__ void __launch_bounds__(kThreads, per_sm(D, NT)) decode_kernel(const _
 
   // ---------------------------------------------------------------- consumers
   const int g = lane >> 2, t = lane & 3;
+  const int kw = warp % kKeyWarps, row0 = warp / kKeyWarps * 8 * NT;  // this warp's keys and rows
   int st = 0;
   unsigned phase = 0;
   bool bad = false;
@@ -320,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, per_sm(D, NT)) decode_kernel(const _
     int hi[NT][2];  // last visible key of this lane's columns 2 t, 2 t + 1
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int r = nt * 8 + g;
+      const int r = row0 + nt * 8 + g;
       uint4 w[KW];
 #pragma unroll
       for (int i = 0; i < KW; ++i) w[i] = make_uint4(0, 0, 0, 0);
@@ -372,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, per_sm(D, NT)) decode_kernel(const _
         qs[nt][k] = __shfl_sync(0xffffffffu, x, (2 * t + k) * 4) * p.a.scale_log2;
         // codes read as c 2^-24
         qi[nt][k] = __shfl_sync(0xffffffffu, down, (2 * t + k) * 4) * (16777216.f * p.a.scale_log2);
-        hi[nt][k] = s.L - s.n + min((nt * 8 + 2 * t + k) / p.v.group, s.n - 1);
+        hi[nt][k] = s.L - s.n + min((row0 + nt * 8 + 2 * t + k) / p.v.group, s.n - 1);
       }
     }
     float acc[D / 16][NT][4];
@@ -388,13 +397,13 @@ __global__ void __launch_bounds__(kThreads, per_sm(D, NT)) decode_kernel(const _
     }
 
     for (int i = 0; i < len; ++i) {
-      const int key0 = (s.lo + sg.t0 + i) * kTile + warp * 32;
+      const int key0 = (s.lo + sg.t0 + i) * kTile + kw * 32;
       if (!bad && !mbar_wait_bounded(full + st, phase, p.wait_ns)) {
         bad = true;
         if (lane == 0) atomicOr(p.v.status, kStatusTimeoutPipe);
       }
       bad = __any_sync(0xffffffffu, bad);
-      const uint32_t base = stages_at + st * p.stage_bytes + warp * 2 * BB;
+      const uint32_t base = stages_at + st * p.stage_bytes + kw * 2 * BB;
       // this lane's row of the four 8 x 8 matrices of 16-bit words: key lane % 16 (its low 8 first), chunk lane / 8 % 2
       const uint32_t vrow = base + 8 * D + ((lane & 7) + (lane >> 4) * 8) * (D / 2) + ((lane >> 3) & 1) * 16;
       auto tile = [&](auto masked) {
@@ -568,12 +577,12 @@ __global__ void __launch_bounds__(kThreads, per_sm(D, NT)) decode_kernel(const _
           l[nt][k] += __shfl_xor_sync(0xffffffffu, l[nt][k], o);
           off[nt][k] += __shfl_xor_sync(0xffffffffu, off[nt][k], o);
         }
-        const int r = nt * 8 + 2 * t + k;
+        const int r = row0 + nt * 8 + 2 * t + k;
         if (g == 0) {
-          ml[(warp * R + r) * 2] = m[nt][k];
-          ml[(warp * R + r) * 2 + 1] = l[nt][k];
+          ml[(kw * R + r) * 2] = m[nt][k];
+          ml[(kw * R + r) * 2 + 1] = l[nt][k];
         }
-        float* dst = om + (warp * R + r) * OS + g * 4;
+        float* dst = om + (kw * R + r) * OS + g * 4;
 #pragma unroll
         for (int i2 = 0; i2 < VW; ++i2)
 #pragma unroll
@@ -588,7 +597,7 @@ __global__ void __launch_bounds__(kThreads, per_sm(D, NT)) decode_kernel(const _
             *reinterpret_cast<float4*>(dst + i2 * 64 + y * 32) = o4;
           }
       }
-    consumer_sync();
+    consumer_sync<32 * kWarps>();
     const bool whole = len == s.tiles;
     // a segment that starts its item in this CTA and one that goes on with an earlier CTA's have a slot each
     float* slot = p.part + (cta * 2 + (sg.t0 == 0 ? 1 : 0)) * kPart;
@@ -607,12 +616,12 @@ __global__ void __launch_bounds__(kThreads, per_sm(D, NT)) decode_kernel(const _
     for (int r = warp; r < R; r += kWarps) {
       float M = -INFINITY;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, ml[(w * R + r) * 2]);
+      for (int w = 0; w < kKeyWarps; ++w) M = fmaxf(M, ml[(w * R + r) * 2]);
       float L = 0.f, o[E];
 #pragma unroll
       for (int e = 0; e < E; ++e) o[e] = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
+      for (int w = 0; w < kKeyWarps; ++w) {
         const float mw = ml[(w * R + r) * 2];
         const float f = mw == -INFINITY ? (ml[(w * R + r) * 2 + 1] == 0.f ? 0.f : 1.f) : ex2(mw - M);
         L = fmaf(f, ml[(w * R + r) * 2 + 1], L);
@@ -631,10 +640,10 @@ __global__ void __launch_bounds__(kThreads, per_sm(D, NT)) decode_kernel(const _
       // CTAs ca .. cb hold the item's units
       const int64_t x0 = div_u64(((lane & 1) ? sg.unit0 + s.tiles : sg.unit0 + 1) * G - 1, U);
       const int ca = (int)__shfl_sync(0xffffffffu, x0, 0), parts = (int)__shfl_sync(0xffffffffu, x0, 1) - ca + 1;
-      consumer_sync();
+      consumer_sync<32 * kWarps>();
       // release what the barrier above has collected from the four warps, acquire what the others released
       if (tid == 0) found[0] = add_acq_rel(p.counters + ca, 1u) == (unsigned)(parts - 1);
-      consumer_sync();
+      consumer_sync<32 * kWarps>();
       if (found[0]) {
         if (tid == 0) p.counters[ca] = 0;
         auto part = [&](int x) { return p.part + ((int64_t)(ca + x) * 2 + (x == 0)) * kPart; };
@@ -687,23 +696,23 @@ __global__ void __launch_bounds__(kThreads, per_sm(D, NT)) decode_kernel(const _
         }
       }
     }
-    consumer_sync();  // the joined results have been read
+    consumer_sync<32 * kWarps>();  // the joined results have been read
   }
 }
 
-template <int D, int NT>
+template <int D, int NT, int RG>
 spear_status_t launch(const spear_kv_s* h, DecodeParams& p, cudaStream_t stream) {
   static std::atomic<uint64_t> done{0};
-  if (smem_limit_once(reinterpret_cast<const void*>(decode_kernel<D, NT>), done) != cudaSuccess) return SPEAR_ERR_CUDA;
-  constexpr int kPerSm = per_sm(D, NT);
-  constexpr uint32_t om = ((kWarps * 8 * NT * (2 + D + 4)) * 4 + 127) / 128 * 128;
+  if (smem_limit_once(reinterpret_cast<const void*>(decode_kernel<D, NT, RG>), done) != cudaSuccess) return SPEAR_ERR_CUDA;
+  constexpr int kPerSm = per_sm(D, NT, RG);
+  constexpr uint32_t om = ((kKeyWarps * 8 * NT * RG * (2 + D + 4)) * 4 + 127) / 128 * 128;
   constexpr uint32_t stage = kBlocksPerTile * 16 * (D + 8);
   constexpr int kRoom = (227 * 1024 / kPerSm - 1024 - 512 - (int)om) / (int)stage;
   p.stage_bytes = stage;
   p.NS = kRoom < kMaxStages ? kRoom : kMaxStages;
   static_assert(kRoom >= 2, "two stages at least");
   const size_t smem = 512 + om + (size_t)p.NS * stage;
-  return kv_launch(decode_kernel<D, NT>, dim3(h->sm_count * kPerSm), kThreads, smem, stream, p);
+  return kv_launch(decode_kernel<D, NT, RG>, dim3(h->sm_count * kPerSm), 32 * (kKeyWarps * RG + 1), smem, stream, p);
 }
 
 }  // namespace
@@ -714,7 +723,8 @@ using namespace spear;
 size_t kv_decode_workspace(const spear_kv_s* h) {
   const int D = h->view.D;
   int rows = 0;  // of all CTAs of an SM
-  for (int nt = 1; nt <= 4; nt *= 2) rows = std::max(rows, 8 * nt * per_sm(D, nt));
+  for (int nt = 1; nt <= 2; ++nt) rows = std::max(rows, 8 * nt * per_sm(D, nt, 1));
+  rows = std::max(rows, 32 * per_sm(D, 2, 2));
   return (size_t)h->sm_count * 2 * rows * (D + 2) * sizeof(float);
 }
 
@@ -729,8 +739,8 @@ spear_status_t kv_launch_decode(const spear_kv_s* h, const KvAttnArgs& a, int nt
   p.wait_ns = 100000000ull;
   const bool wide = h->view.D == 128;
   switch (nt) {
-    case 1: return wide ? launch<128, 1>(h, p, stream) : launch<64, 1>(h, p, stream);
-    case 2: return wide ? launch<128, 2>(h, p, stream) : launch<64, 2>(h, p, stream);
-    default: return wide ? launch<128, 4>(h, p, stream) : launch<64, 4>(h, p, stream);
+    case 1: return wide ? launch<128, 1, 1>(h, p, stream) : launch<64, 1, 1>(h, p, stream);
+    case 2: return wide ? launch<128, 2, 1>(h, p, stream) : launch<64, 2, 1>(h, p, stream);
+    default: return wide ? launch<128, 2, 2>(h, p, stream) : launch<64, 2, 2>(h, p, stream);
   }
 }
