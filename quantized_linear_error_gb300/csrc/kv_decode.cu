@@ -56,7 +56,7 @@ constexpr int kTile = 32 * kKeyWarps;          // keys of a unit
 constexpr int kBlocksPerTile = kTile / 16;
 constexpr int kMaxStages = 16;
 constexpr int kItemCost = 3;                   // units: rows of q in, states joined, results out
-constexpr int kMinUnits = 6;                   // a CTA's, where there are few of them: joining costs as much as more tiles
+constexpr int kMinUnits = 4;                   // a CTA's, where there are few of them
 constexpr int kScan = 10;                      // warps at most
 constexpr float kLazy = 8.f;
 // A variant: NT 8-row MMA tiles a warp, RG groups of warps with rows of their own over the same keys (four tiles in one
@@ -223,8 +223,11 @@ __global__ void __launch_bounds__(32 * (kKeyWarps * RG + 1), per_sm(D, NT, RG))
   Cursor c;
   int64_t U = 0, G, u0, u1, at;
   const int64_t cta = blockIdx.x;
-  auto share = [&] {
-    G = min((int64_t)gridDim.x, div_u64(U + kMinUnits - 1, kMinUnits));
+  auto share = [&](int items) {
+    // Where there is little work, a whole number of CTAs an item (if the items are alike, none has shares of two), of
+    // some kMinUnits each: joining costs as much as a few tiles.
+    const int64_t mean = div_u64(U, max(items, 1));
+    G = min((int64_t)gridDim.x, items * max((int64_t)1, div_u64(mean + kMinUnits / 2, kMinUnits)));
     const int64_t x = G > 0 ? div_u64((cta + (lane & 1)) * U, G) : 0;
     u0 = __shfl_sync(0xffffffffu, x, 0);
     u1 = __shfl_sync(0xffffffffu, x, 1);
@@ -233,13 +236,19 @@ __global__ void __launch_bounds__(32 * (kKeyWarps * RG + 1), per_sm(D, NT, RG))
     if (lane < p.a.n_seqs) c.s = kv_seq(p.v, p.a, lane, kTile);
     const int64_t own = lane < p.a.n_seqs ? seq_units(p, c.s) : 0, incl = scan_inclusive(own, lane);
     U = __shfl_sync(0xffffffffu, incl, 31);
-    share();
+    share(__popc(__ballot_sync(0xffffffffu, own > 0)) * p.v.n_kv_heads);
     c.b = __ffs(__ballot_sync(0xffffffffu, u0 < incl)) - 1;
     at = u0 - __shfl_sync(0xffffffffu, incl - own, c.b & 31);
     __syncthreads();  // the barriers are in place
     if (cta >= G) return;
   } else {
-    for (int b = tid; b < p.a.n_seqs; b += kThreads) U += seq_units(p, kv_seq(p.v, p.a, b, kTile));
+    int items = 0;
+    for (int b = tid; b < p.a.n_seqs; b += kThreads) {
+      const int64_t own = seq_units(p, kv_seq(p.v, p.a, b, kTile));
+      U += own;
+      items += own > 0;
+    }
+    items = __syncthreads_count(items) * p.v.n_kv_heads;  // at least, with more sequences than threads
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) U += __shfl_xor_sync(0xffffffffu, U, o);
     if (lane == 0) scan[warp] = U;
@@ -247,7 +256,7 @@ __global__ void __launch_bounds__(32 * (kKeyWarps * RG + 1), per_sm(D, NT, RG))
     U = 0;
 #pragma unroll
     for (int w = 0; w <= kWarps; ++w) U += scan[w];
-    share();
+    share(items);
     if (cta >= G) return;
     int64_t before = 0;
     for (int b0 = 0;; b0 += 32) {
