@@ -376,7 +376,7 @@ spear_status_t spear_sched_destroy(spear_sched_t s);
 typedef struct spear_kv_s* spear_kv_t;
 
 typedef struct {
-  int32_t n_heads;             /* query heads, a multiple of n_kv_heads; head h reads
+  int32_t n_heads;             /* query heads (<= 4096), a multiple of n_kv_heads; head h reads
                                   key/value head h / (n_heads / n_kv_heads) */
   int32_t n_kv_heads;          /* n_heads / n_kv_heads <= 32 */
   int32_t head_dim;            /* D: 64 or 128 */
@@ -432,7 +432,8 @@ spear_status_t spear_kv_read(spear_kv_t h, const int64_t* slots, int32_t T, void
  *   page_table: device int32 [n_seqs][ld_pt];  kv_lens: device int32 [n_seqs],
  *     at most 2^30;
  *   q_starts: device int32 [n_seqs + 1], ascending, within 0..T;
- *   max_q: the largest number of query rows of a sequence (>= 1).
+ *   max_q: the largest number of query rows of a sequence (>= 1);
+ *   T * (n_heads / n_kv_heads) < 2^27; a window above 2^30 hides nothing.
  * Sequences whose rows of one key/value head, (n_heads / n_kv_heads) x query
  * rows, fit a few warp-MMA tiles run in a kernel that streams the cache once
  * (single tokens, drafts to verify), longer ones in a tensor-core kernel; a

@@ -260,7 +260,7 @@ spear_status_t spear_kv_create(const spear_kv_desc_t* d, cudaStream_t stream, sp
   *out = nullptr;
   if (!d || !d->pool || !aligned16(d->pool)) return SPEAR_ERR_INVALID_ARG;
   if (d->n_kv_heads < 1 || d->n_heads < d->n_kv_heads || d->n_heads % d->n_kv_heads != 0 ||
-      d->n_heads / d->n_kv_heads > 32 || d->n_heads > 65535)
+      d->n_heads / d->n_kv_heads > 32 || d->n_heads > 4096)
     return SPEAR_ERR_INVALID_ARG;
   if (d->head_dim != 64 && d->head_dim != 128) return SPEAR_ERR_INVALID_ARG;
   if (d->page_size < 16 || d->page_size % 16 != 0 || d->page_size > 65536 || d->n_pages < 1)

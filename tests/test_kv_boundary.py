@@ -20,7 +20,7 @@ def _desc(**kw):
     return spear.spear_kv_desc_t(*[d[f] for f, _ in spear.spear_kv_desc_t._fields_])
 
 
-@pytest.mark.parametrize("bad", [dict(n_heads=0), dict(n_heads=7), dict(n_kv_heads=0), dict(n_heads=66), dict(head_dim=96),
+@pytest.mark.parametrize("bad", [dict(n_heads=0), dict(n_heads=7), dict(n_kv_heads=0), dict(n_heads=66), dict(n_heads=8192, n_kv_heads=1024), dict(head_dim=96),
                                  dict(n_heads=1, n_kv_heads=2), dict(n_heads=-8, n_kv_heads=-2),
                                  dict(head_dim=256), dict(page_size=0), dict(page_size=24), dict(page_size=65552),
                                  dict(n_pages=0), dict(pool=None), dict(pool=4104), dict(rope_dim=8), dict(rope_dim=144),
