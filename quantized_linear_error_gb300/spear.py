@@ -364,53 +364,67 @@ class SpearKVCache:
         _check(L.spear_kv_create(byref(d), _stream(stream), byref(h)), "spear_kv_create")
         self.h, self.pool, self.rope_table = h, pool, rope_table
         self.n_heads, self.n_kv_heads, self.head_dim, self.page_size = n_heads, n_kv_heads, head_dim, page_size
-        self._q_row, self._kv_row = (n_heads, head_dim), (n_kv_heads, head_dim)
         self._bf16, self._i64, self._i32 = torch.bfloat16, torch.int64, torch.int32
         self._append, self._read, self._attention = L.spear_kv_append, L.spear_kv_read, L.spear_kv_attention
         self._scale = head_dim ** -0.5
 
-    def _rows(self, x, T, row, what):
-        """The token stride of bf16 [T][heads][D] with contiguous heads."""
-        heads, D = row
-        if x.dtype is not self._bf16 or x.shape != (T, heads, D) or not x.is_cuda:
-            raise ValueError(f"{what} must be CUDA bf16 [{T}][{heads}][{D}]")
-        s0, s1, s2 = x.stride()
-        if s2 != 1 or (s1 != D and heads > 1):
-            raise ValueError(f"{what}: the heads of a token must be contiguous")
-        return s0 if T > 1 else max(s0, heads * D)
-
-    def _index(self, x, dtype, n, what):
-        if x.dtype is not dtype or not x.is_cuda or not x.is_contiguous() or x.numel() < n:
-            raise ValueError(f"{what} must be a contiguous CUDA {dtype} tensor of at least {n} elements")
-        return x.data_ptr()
+    def _bad_rows(self, **xs):
+        """Says what is wrong with one of the tensors bf16 [T][heads][D]."""
+        for what, (x, T, heads) in xs.items():
+            shape = (T, heads, self.head_dim)
+            if x.dtype is not self._bf16 or not x.is_cuda or x.shape != shape:
+                raise ValueError(f"{what} must be CUDA bf16 {list(shape)}")
+            s = x.stride()
+            if s[2] != 1 or (s[1] != self.head_dim and heads > 1):
+                raise ValueError(f"{what}: the heads of a token must be contiguous")
+        raise ValueError("indices must be contiguous CUDA tensors: int64 positions and slots, int32 tables and lengths, "
+                         "with an element for every token or sequence")
 
     def append(self, q, k, v, positions, slots, q_out=None, stream=None):
         """Rotate q [T][n_heads][D] (or None) and k [T][n_kv_heads][D] to the
         int64 ``positions`` and put k and v into the int64 ``slots`` (-1: not
         cached). The rotated queries go to ``q_out`` (default: q in place)."""
-        T = k.shape[0]
-        row, kv_row, rows = self._q_row, self._kv_row, self._rows
-        qp = op = ldq = ldo = 0
+        T, H, G, D, bf16, i64 = k.shape[0], self.n_heads, self.n_kv_heads, self.head_dim, self._bf16, self._i64
+        qp = op = ldq = ldo = pos = 0
+        ldk, k1, k2 = k.stride()
+        ldv, v1, v2 = v.stride()
+        # one expression for all of them: it is on every step's way
+        ok = (k.dtype is bf16 and v.dtype is bf16 and k.shape == (T, G, D) == v.shape and k.is_cuda and v.is_cuda and
+              k2 == 1 == v2 and (k1 == D == v1 or G == 1) and
+              slots.dtype is i64 and slots.is_cuda and slots.is_contiguous() and slots.numel() >= T)
         if q is not None:
             if q_out is None:
                 q_out = q
-            qp, ldq, op, ldo = q.data_ptr(), rows(q, T, row, "q"), q_out.data_ptr(), rows(q_out, T, row, "q_out")
-        pos = 0 if self.rope_table is None else self._index(positions, self._i64, T, "positions")
-        st = self._append(self.h, qp, ldq, k.data_ptr(), rows(k, T, kv_row, "k"), v.data_ptr(), rows(v, T, kv_row, "v"),
-                          pos, self._index(slots, self._i64, T, "slots"), T, op, ldo, _stream(stream))
+            ldq, q1, q2 = q.stride()
+            ldo, o1, o2 = q_out.stride()
+            ok = ok and (q.dtype is bf16 and q_out.dtype is bf16 and q.shape == (T, H, D) == q_out.shape and
+                         q.is_cuda and q_out.is_cuda and q2 == 1 == o2 and (q1 == D == o1 or H == 1))
+            qp, op = q.data_ptr(), q_out.data_ptr()
+        if self.rope_table is not None:
+            ok = ok and (positions.dtype is i64 and positions.is_cuda and positions.is_contiguous() and
+                         positions.numel() >= T)
+            pos = positions.data_ptr()
+        if not ok:
+            rows = {"k": (k, T, G), "v": (v, T, G)}
+            self._bad_rows(**rows, **({} if q is None else {"q": (q, T, H), "q_out": (q_out, T, H)}))
+        if T < 2:  # the stride of a single token means nothing
+            ldq, ldo, ldk, ldv = max(ldq, H * D), max(ldo, H * D), max(ldk, G * D), max(ldv, G * D)
+        st = self._append(self.h, qp, ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, pos, slots.data_ptr(), T, op, ldo,
+                          _stream(stream))
         if st:
             raise SpearError(st, "spear_kv_append")
         return q_out
 
     def read(self, slots, k_out, v_out, stream=None):
         """The cached keys and values of ``slots`` as bf16 [T][n_kv_heads][D]."""
-        T = slots.shape[0]
-        shape = (T, *self._kv_row)
-        for x in (k_out, v_out):
-            if x.dtype is not self._bf16 or x.shape != shape or not x.is_cuda or not x.is_contiguous():
-                raise ValueError(f"k_out and v_out must be contiguous CUDA bf16 {list(shape)}")
-        st = self._read(self.h, self._index(slots, self._i64, T, "slots"), T, k_out.data_ptr(), v_out.data_ptr(),
-                        _stream(stream))
+        T, G, D, bf16 = slots.shape[0], self.n_kv_heads, self.head_dim, self._bf16
+        if not (k_out.dtype is bf16 and v_out.dtype is bf16 and k_out.shape == (T, G, D) == v_out.shape and
+                k_out.is_cuda and v_out.is_cuda and k_out.is_contiguous() and v_out.is_contiguous() and
+                slots.dtype is self._i64 and slots.is_cuda and slots.is_contiguous()):
+            if not (k_out.is_contiguous() and v_out.is_contiguous()):
+                raise ValueError("k_out and v_out must be contiguous")
+            self._bad_rows(k_out=(k_out, T, G), v_out=(v_out, T, G))
+        st = self._read(self.h, slots.data_ptr(), T, k_out.data_ptr(), v_out.data_ptr(), _stream(stream))
         if st:
             raise SpearError(st, "spear_kv_read")
         return k_out, v_out
@@ -420,14 +434,22 @@ class SpearKVCache:
         into ``out`` (see spear_kv_attention): int32 ``page_table``
         [n_seqs][max pages], ``kv_lens`` [n_seqs], ``q_starts`` [n_seqs + 1];
         ``scale`` defaults to head_dim ** -0.5, ``window`` 0 means all earlier keys."""
-        T = q.shape[0]
+        T, H, D, bf16, i32 = q.shape[0], self.n_heads, self.head_dim, self._bf16, self._i32
         if page_table.dim() != 2:
             raise ValueError("page_table must have two dimensions")
         n, cols = page_table.shape
-        index, i32, row = self._index, self._i32, self._q_row
-        st = self._attention(self.h, q.data_ptr(), self._rows(q, T, row, "q"), out.data_ptr(),
-                             self._rows(out, T, row, "out"), index(page_table, i32, n, "page_table"), cols,
-                             index(kv_lens, i32, n, "kv_lens"), index(q_starts, i32, n + 1, "q_starts"), n, T, max_q,
+        ldq, q1, q2 = q.stride()
+        ldo, o1, o2 = out.stride()
+        if not (q.dtype is bf16 and out.dtype is bf16 and q.shape == (T, H, D) == out.shape and q.is_cuda and
+                out.is_cuda and q2 == 1 == o2 and (q1 == D == o1 or H == 1) and
+                page_table.dtype is i32 and page_table.is_cuda and page_table.is_contiguous() and
+                kv_lens.dtype is i32 and kv_lens.is_cuda and kv_lens.is_contiguous() and kv_lens.numel() >= n and
+                q_starts.dtype is i32 and q_starts.is_cuda and q_starts.is_contiguous() and q_starts.numel() > n):
+            self._bad_rows(q=(q, T, H), out=(out, T, H))
+        if T < 2:  # the stride of a single token means nothing
+            ldq, ldo = max(ldq, H * D), max(ldo, H * D)
+        st = self._attention(self.h, q.data_ptr(), ldq, out.data_ptr(), ldo, page_table.data_ptr(), cols,
+                             kv_lens.data_ptr(), q_starts.data_ptr(), n, T, max_q,
                              self._scale if scale is None else scale, window, _stream(stream))
         if st:
             raise SpearError(st, "spear_kv_attention")
