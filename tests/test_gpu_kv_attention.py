@@ -107,6 +107,14 @@ def test_many_sequences():
     _check([(1, 1 + 7 * i % 90) for i in range(300)], 4, 2, 64, 16)
 
 
+def test_many_chunks():
+    """Many sequences of a few row tiles, and among them one of so many that they are counted in another way; more
+    sequences than a warp's lanes."""
+    short = [(5 + 7 * i % 60, 70 + 11 * i % 200) for i in range(20)]
+    _check(short + [(1400, 1401)], 8, 1, 64, 32)
+    _check(short + [(0, 5)] + short + [(700, 720)] + short[:3], 8, 1, 64, 32, window=200)
+
+
 def test_work_split_over_a_long_cache():
     _check([(1, 20001)], 4, 1, 128, 64, seed=3)
     _check([(3, 9000), (1, 11), (40, 6000)], 4, 1, 64, 128, seed=4)
