@@ -65,7 +65,12 @@ struct AppendParams {
 // sines are as many bytes as two rows), four rows' loads in flight. Products
 // and sums are rounded one by one (no contraction), so that the codes are
 // defined bit for bit. Bound by memory: a token reads and writes (2 n_heads +
-// 2 n_kv_heads) D bf16 and writes 2 n_kv_heads (D / 2 + 4) bytes.
+// 2 n_kv_heads) D bf16 and writes 2 n_kv_heads (D / 2 + 4) bytes. Measured:
+// 12289 tokens of 64 + 2 x 8 heads of 128 (470 MB) in 88 us, 5.3 TB/s, 79% of
+// a plain copy; 1088 tokens of 32 + 2 x 32 heads (40 MB) in 14.5 us, 2.8 TB/s: there the
+// launch, the slot and the first row's latency are a third of the time. (16
+// bytes a lane of one row, partners exchanged by shuffles: 12289 tokens with
+// the read-back took 265 us, against 102.)
 template <int D, bool kInterleaved>
 __global__ void __launch_bounds__(kAppendThreads, 4) append_kernel(const __grid_constant__ AppendParams p) {
   constexpr int LPR = D / 8, U = 4;
@@ -197,7 +202,8 @@ __global__ void __launch_bounds__(kAppendThreads, 4) append_kernel(const __grid_
 }
 
 // A group of D / 8 lanes hands back `chunk` of a token's 2 n_kv_heads rows (8
-// elements a lane), four rows' loads in flight.
+// elements a lane), four rows' loads in flight. Bound by memory: 12289 tokens
+// of 2 x 8 heads of 128 (64 MB, most of it written) take 13.4 us, 4.8 TB/s.
 template <int D>
 __global__ void __launch_bounds__(kAppendThreads)
     read_kernel(const KvView v, const int64_t* __restrict__ slots, int T, int chunk, __nv_bfloat16* k_out,

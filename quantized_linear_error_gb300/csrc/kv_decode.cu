@@ -1,11 +1,16 @@
 // Attention of a few query rows over the paged 4-bit cache: one new token a
 // sequence, or a few drafted ones.
 //
-// For each (sequence, key/value head) the R = 8 NT rows (query tokens x the
+// For each (sequence, key/value head) the R = 8 NT RG rows (query tokens x the
 // heads that share the key/value head) meet every visible key once:
 //   s = scale (q . k),  out = sum 2^(s - m) v / sum 2^(s - m)   (s in log2),
 // so the cache is read once, (D + 8) bytes a key for 4 D R flops: bound by
-// memory as long as the instructions that unpack the codes keep up.
+// memory as long as the instructions that unpack the codes keep up. Measured,
+// D = 128: 8 heads a key/value head, 128 sequences of 500 to 8192 keys (607 MB)
+// in 114 us, 5.3 TB/s, 79% of a plain copy; one head each, 64 sequences of 100
+// to 4096 keys and 32 heads (601 MB) in 119 us, 75%; one sequence of 262143
+// keys (285 MB) in 62.5 us, 68%; a call of little work takes 6.5 us, most of it
+// launch, look-up of lengths and pages, first copy and join.
 //
 //  - Products run on warp MMAs (m16n8k16) with the cache as the A operand and
 //    the rows as the 8 columns of B, so that no tensor work is spent on padding
@@ -37,8 +42,16 @@
 // of an item to arrive joins them in CTA order (the same bits every time) and
 // resets the counter. No CTA waits for another.
 //
+// Variants: up to 8 rows one MMA tile a warp (NT = 1), up to 16 two, up to 32 two
+// groups of warps (RG = 2) with 16 rows each over the same tiles: 32 sequences x
+// 4000 keys x 8 heads with 8 / 16 / 32 rows take 36 / 60 / 102 us. The rows'
+// instructions, not the bytes, bound the last two. (Four tiles in a warp's
+// registers instead of two groups: 180 us; eight rows a group, so that 16 and 32
+// rows get 16 warps an SM: 67 and 122 us, the registers spill and each group
+// unpacks again.)
+//
 // A CTA: four warps, 32 keys of a tile each with a state of their own, joined
-// at the end of a segment; a fifth warp copies the tiles' 16-token blocks (one
+// at the end of a segment; a warp more copies the tiles' 16-token blocks (one
 // bulk copy each, whatever the page size) into a ring of stages.
 #include <cuda_fp16.h>
 
@@ -55,8 +68,10 @@ constexpr int kKeyWarps = 4;                   // consumer warps along the keys 
 constexpr int kTile = 32 * kKeyWarps;          // keys of a unit
 constexpr int kBlocksPerTile = kTile / 16;
 constexpr int kMaxStages = 16;
-constexpr int kItemCost = 3;                   // units: rows of q in, states joined, results out
-constexpr int kMinUnits = 4;                   // a CTA's, where there are few of them
+constexpr int kItemCost = 3;                   // units: rows of q in, states joined, results out (64 ragged sequences: 158 us
+                                               // with 0, 119 with 3)
+constexpr int kMinUnits = 4;                   // a CTA's, where there are few of them (4 sequences of 1000 tokens: 13.4 us
+                                               // without the rule, 11.8 with it)
 constexpr int kScan = 10;                      // warps at most
 constexpr float kLazy = 8.f;
 // A variant: NT 8-row MMA tiles a warp, RG groups of warps with rows of their own over the same keys (four tiles in one

@@ -11,7 +11,16 @@
 // of an SM, their operands in shared memory 1536 at 128 bytes a cycle, the
 // dequantised tiles' stores 512; a block takes some 2800 here, the chain
 // scores, weights, product of one half being longer than the other half's
-// products that hide it.
+// products that hide it. Measured, D = 128: a prompt of 8192 tokens, 32 heads
+// over 8 (550 GFLOP), 392 us or 1.40 PFLOP/s in bursts, 71% of a library
+// product's rate, and 405 to 415 us once the power limit lowers the clocks; 320
+// tokens behind 7901 (42 GFLOP) 45 us, of which 5 are the start and 8 partial
+// results and their join.
+//
+// A row tile with at most 128 rows leaves the other half idle, and a key tile
+// then takes 2700 cycles, of which the dequantisers need 2200: both halves at
+// every other tile of it were no faster (127 us against 121 for 32 sequences x
+// 12 drafts x 4 heads at 4000 keys).
 //
 //  - Operands are f16, whose 11 bits hold queries and codes' values with an
 //    error far below that of the bf16 result (bf16 operands doubled it). Rows
