@@ -8,7 +8,7 @@
 // memory as long as the instructions that unpack the codes keep up. Measured,
 // D = 128: 8 heads a key/value head, 128 sequences of 500 to 8192 keys (607 MB)
 // in 114 us, 5.3 TB/s, 79% of a plain copy; one head each, 64 sequences of 100
-// to 4096 keys and 32 heads (601 MB) in 119 us, 75%; one sequence of 262143
+// to 4096 keys and 32 heads (601 MB) in 117 us, 76%; one sequence of 262143
 // keys (285 MB) in 62.5 us, 68%; a call of little work takes 6.5 us, most of it
 // launch, look-up of lengths and pages, first copy and join.
 //
@@ -69,7 +69,7 @@ constexpr int kTile = 32 * kKeyWarps;          // keys of a unit
 constexpr int kBlocksPerTile = kTile / 16;
 constexpr int kMaxStages = 16;
 constexpr int kItemCost = 3;                   // units: rows of q in, states joined, results out (64 ragged sequences: 158 us
-                                               // with 0, 119 with 3)
+                                               // with 0, 119 with 3 when it came in)
 constexpr int kMinUnits = 4;                   // a CTA's, where there are few of them (4 sequences of 1000 tokens: 13.4 us
                                                // without the rule, 11.8 with it)
 constexpr int kScan = 10;                      // warps at most
@@ -637,7 +637,7 @@ __global__ void __launch_bounds__(32 * (kKeyWarps * RG + 1), per_sm(D, NT, RG))
       else
         *reinterpret_cast<uint32_t*>(dst) = w[0];
     };
-    for (int r = warp; r < R; r += kWarps) {
+    for (int r = warp; r < min(R, rows); r += kWarps) {
       float M = -INFINITY;
 #pragma unroll
       for (int w = 0; w < kKeyWarps; ++w) M = fmaxf(M, ml[(w * R + r) * 2]);
@@ -671,7 +671,7 @@ __global__ void __launch_bounds__(32 * (kKeyWarps * RG + 1), per_sm(D, NT, RG))
       if (found[0]) {
         if (tid == 0) p.counters[ca] = 0;
         auto part = [&](int x) { return p.part + ((int64_t)(ca + x) * 2 + (x == 0)) * kPart; };
-        for (int r = warp; r < R; r += 2 * kWarps) {  // two rows at a time, 16 loads in flight
+        for (int r = warp; r < min(R, rows); r += 2 * kWarps) {  // two rows at a time, 16 loads in flight
           float M[2] = {-INFINITY, -INFINITY};
           for (int x = lane; x < parts; x += 32)
 #pragma unroll
