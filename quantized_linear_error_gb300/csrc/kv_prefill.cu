@@ -12,7 +12,7 @@
 // dequantised tiles' stores 512; a block takes some 2800 here, the chain
 // scores, weights, product of one half being longer than the other half's
 // products that hide it. Measured, D = 128: a prompt of 8192 tokens, 32 heads
-// over 8 (550 GFLOP), 392 us or 1.40 PFLOP/s in bursts, 71% of a library
+// over 8 (550 GFLOP), 390 us or 1.41 PFLOP/s in bursts, 71% of a library
 // product's rate, and 405 to 415 us once the power limit lowers the clocks; 320
 // tokens behind 7901 (42 GFLOP) 45 us, of which 5 are the start and 8 partial
 // results and their join.
@@ -708,19 +708,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       if (lane == 0) mbar_arrive(&hd.q_full[i]);
     };
 
-    Segment g;
-    unsigned n = 0;
-    bool more = read_segment(n++, g);
-    if (more && g.rows > 128 * i) load_q(g);
-    while (more && ok) {
-      Segment nx;
-      if (g.rows <= 128 * i) {  // a short item has no second half
-        tiles += g.len;
-        more = read_segment(n++, nx);
-        if (more && nx.rows > 128 * i) load_q(nx);
-        g = nx;
-        continue;
-      }
+    // One copy of the code that loads rows, met before every segment: the first time with nothing to compute. (The three
+    // roles' loops share the instruction cache; with three copies the prompt of 8192 tokens took 396 us.)
+    Segment g = {};
+    bool mine = false;  // a short item has no second half
+    for (unsigned n = 0;;) {
       const int in_item = min(128 * i + row, g.rows - 1);
       const unsigned R = g.r0 + in_item, tok = div_group(p, R);
       const int hi = g.pos0 + (int)tok;  // last key that this row sees
@@ -729,7 +721,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       const int all_lo = p.a.window > 0 ? g.pos0 + (int)div_group(p, g.r0 + min(128 * i + 127, g.rows - 1)) - p.a.window + 1 : 0;
       float m = -INFINITY, l = 0.f;
       sl = sl_next;
-      for (int k = 0; k < g.len; ++k) {
+      if (!mine) tiles += g.len;
+      for (int k = 0; mine && k < g.len; ++k) {
         const int key0 = (g.tile0 + k) * kTile;
         ok = warp_wait(&hd.s_full[i], n_s & 1u, p.wait_ns, kHintNs);
         if (!ok) break;
@@ -887,48 +880,53 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       }
       if (!ok) break;
       // the half's scores are done with its Q tile: the next item's rows go in while the last product runs
-      more = read_segment(n++, nx);
-      if (more && nx.rows > 128 * i) load_q(nx);
-      // ---- the segment's result
-      ok = warp_wait(&hd.o_full[i], n_o & 1u, p.wait_ns, kHintNs);
-      if (!ok) break;
-      ++n_o;
-      tc_fence_after_sync();
-      const bool real = 128 * i + row < g.rows;
-      if (g.whole) {
-        __nv_bfloat16* dst = p.a.out + (int64_t)(g.row + tok) * p.a.ld_out +
-                             (int64_t)(g.h * p.v.group + R - tok * p.v.group) * D;
-        const float inv = l == 0.f ? 0.f : 1.f / l;
+      Segment nx;
+      const bool more = read_segment(n++, nx), next = more && nx.rows > 128 * i;
+      if (next) load_q(nx);
+      if (mine) {
+        // ---- the segment's result
+        ok = warp_wait(&hd.o_full[i], n_o & 1u, p.wait_ns, kHintNs);
+        if (!ok) break;
+        ++n_o;
+        tc_fence_after_sync();
+        const bool real = 128 * i + row < g.rows;
+        if (g.whole) {
+          __nv_bfloat16* dst = p.a.out + (int64_t)(g.row + tok) * p.a.ld_out +
+                               (int64_t)(g.h * p.v.group + R - tok * p.v.group) * D;
+          const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
-        for (int j = 0; j < D; j += 32) {
-          uint32_t o[32];
-          tmem_ld_x32(o_t + j, o);
-          tmem_ld_wait();
-          if (real) {
+          for (int j = 0; j < D; j += 32) {
+            uint32_t o[32];
+            tmem_ld_x32(o_t + j, o);
+            tmem_ld_wait();
+            if (real) {
 #pragma unroll
-            for (int x = 0; x < 32; x += 8) {
-              float f[8];
+              for (int x = 0; x < 32; x += 8) {
+                float f[8];
 #pragma unroll
-              for (int y = 0; y < 8; ++y) f[y] = l == 0.f ? 0.f : __uint_as_float(o[x + y]) * inv;
-              *reinterpret_cast<uint4*>(dst + j + x) = unpermute8(f);
+                for (int y = 0; y < 8; ++y) f[y] = l == 0.f ? 0.f : __uint_as_float(o[x + y]) * inv;
+                *reinterpret_cast<uint4*>(dst + j + x) = unpermute8(f);
+              }
             }
           }
-        }
-      } else {
-        float* slot = p.part + (int64_t)(g.slot * 2 + i) * kPart + row;
+        } else {
+          float* slot = p.part + (int64_t)(g.slot * 2 + i) * kPart + row;
 #pragma unroll
-        for (int j = 0; j < D; j += 32) {
-          uint32_t o[32];
-          tmem_ld_x32(o_t + j, o);
-          tmem_ld_wait();
+          for (int j = 0; j < D; j += 32) {
+            uint32_t o[32];
+            tmem_ld_x32(o_t + j, o);
+            tmem_ld_wait();
 #pragma unroll
-          for (int x = 0; x < 32; ++x) __stcg(slot + (j + x) * 128, __uint_as_float(o[x]));
+            for (int x = 0; x < 32; ++x) __stcg(slot + (j + x) * 128, __uint_as_float(o[x]));
+          }
+          __stcg(slot + D * 128, m * sl);  // in units of log2: the row's factor is gone
+          __stcg(slot + (D + 1) * 128, l);
         }
-        __stcg(slot + D * 128, m * sl);  // in units of log2: the row's factor is gone
-        __stcg(slot + (D + 1) * 128, l);
+        tc_fence_before_sync();
       }
-      tc_fence_before_sync();
+      if (!more) break;
       g = nx;
+      mine = next;
     }
     if (!ok && lane == 0) fail(p);
   }
