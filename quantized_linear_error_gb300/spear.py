@@ -385,7 +385,7 @@ class SpearKVCache:
         int64 ``positions`` and put k and v into the int64 ``slots`` (-1: not
         cached). The rotated queries go to ``q_out`` (default: q in place)."""
         T, H, G, D, bf16, i64 = k.shape[0], self.n_heads, self.n_kv_heads, self.head_dim, self._bf16, self._i64
-        qp = op = ldq = ldo = pos = 0
+        qp = op = ldq = ldo = 0
         ldk, k1, k2 = k.stride()
         ldv, v1, v2 = v.stride()
         # one expression for all of them: it is on every step's way
@@ -401,12 +401,12 @@ class SpearKVCache:
                          q.is_cuda and q_out.is_cuda and q2 == 1 == o2 and (q1 == D == o1 or H == 1))
             qp, op = q.data_ptr(), q_out.data_ptr()
         if self.rope_table is not None:
-            ok = ok and (positions.dtype is i64 and positions.is_cuda and positions.is_contiguous() and
-                         positions.numel() >= T)
-            pos = positions.data_ptr()
+            ok = ok and (positions is not None and positions.dtype is i64 and positions.is_cuda and
+                         positions.is_contiguous() and positions.numel() >= T)
         if not ok:
             rows = {"k": (k, T, G), "v": (v, T, G)}
             self._bad_rows(**rows, **({} if q is None else {"q": (q, T, H), "q_out": (q_out, T, H)}))
+        pos = 0 if self.rope_table is None else positions.data_ptr()
         if T < 2:  # the stride of a single token means nothing
             ldq, ldo, ldk, ldv = max(ldq, H * D), max(ldo, H * D), max(ldk, G * D), max(ldv, G * D)
         st = self._append(self.h, qp, ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, pos, slots.data_ptr(), T, op, ldo,

@@ -151,7 +151,7 @@ def test_refusals():
     q, k, v = (torch.zeros(3, h, 64, dtype=torch.bfloat16, device="cuda") for h in (4, 2, 2))
     i = torch.zeros(3, dtype=torch.int64, device="cuda")
     for bad in [dict(q=q.float()), dict(q=q[:2]), dict(k=k[:, :1]), dict(v=v.transpose(0, 1).contiguous().transpose(0, 1)),
-                dict(positions=i.int()), dict(slots=i[:2]), dict(q_out=q[:2]), dict(slots=i.cpu()), dict(k=k.cpu()),
+                dict(positions=None), dict(positions=i.int()), dict(slots=i[:2]), dict(q_out=q[:2]), dict(slots=i.cpu()), dict(k=k.cpu()),
                 dict(positions=torch.zeros(6, dtype=torch.int64, device="cuda")[::2])]:
         a = dict(q=q, k=k, v=v, positions=i, slots=i, q_out=None)
         a.update(bad)
