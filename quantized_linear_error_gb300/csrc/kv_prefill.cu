@@ -12,7 +12,7 @@
 // dequantised tiles' stores 512; a block takes some 2800 here, the chain
 // scores, weights, product of one half being longer than the other half's
 // products that hide it. Measured, D = 128: a prompt of 8192 tokens, 32 heads
-// over 8 (550 GFLOP), 390 us or 1.41 PFLOP/s in bursts, 71% of a library
+// over 8 (550 GFLOP), 393 us or 1.40 PFLOP/s in bursts, 71% of a library
 // product's rate, and 405 to 415 us once the power limit lowers the clocks; 320
 // tokens behind 7901 (42 GFLOP) 45 us, of which 5 are the start and 8 partial
 // results and their join.
@@ -192,63 +192,65 @@ SPEAR_DEVINL void schedule(const PrefillParams& p, Header& hd, int lane) {
     }
     return own;
   };
-  int64_t U = 0, own = 0;
-  for (int b0 = 0; b0 < p.a.n_seqs; b0 += 32) {
-    own = units_of(b0);
-    int64_t x = own;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    U += x;
-  }
-  const int64_t G = min((int64_t)gridDim.x, U), cta = blockIdx.x;
-  int64_t u = 0, u1 = 0;
-  if (cta < G) {
-    const int64_t x = div_u64((cta + (lane & 1)) * U, G);
-    u = __shfl_sync(0xffffffffu, x, 0);
-    u1 = __shfl_sync(0xffffffffu, x, 1);
-  }
+  int64_t U = 0, own = 0, G = 0, u = 0, u1 = 0, before = 0;
+  const int64_t cta = blockIdx.x;
   int b = 0, h = 0, qt = 0, off = 0, nqt = 0;
-  if (u < u1) {
-    int64_t before = 0;
-    for (int b0 = 0;; b0 += 32) {  // the sequence that u falls into
-      if (p.a.n_seqs > 32) own = units_of(b0);
-      int64_t incl = own;
+  bool counted = false;
+  for (int b0 = 0;;) {  // once over all sequences for the sum, then to the one that u falls into (one copy of the code)
+    if (!counted || p.a.n_seqs > 32) own = units_of(b0);
+    if (!counted) {
+      int64_t x = own;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t x = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += x;
-      }
-      const unsigned past = __ballot_sync(0xffffffffu, u < before + incl);
-      if (past) {
-        const int l = __ffs(past) - 1;
-        b = b0 + l;
-        const int64_t hu = div_u64(__shfl_sync(0xffffffffu, own, l), p.v.n_kv_heads);
-        int64_t rest = u - before - (__shfl_sync(0xffffffffu, incl, l) - __shfl_sync(0xffffffffu, own, l));
-        s = shuffled(s, l);
-        nqt = row_tiles(p, s);
-        h = (int)div_u64(rest, hu);
-        rest -= h * hu;
-        for (int q0 = 0; q0 < nqt; q0 += 32) {
-          const int cost = q0 + lane < nqt ? kItemCost + item_of(p, s, q0 + lane).tiles : 0;
-          int sum = cost;
-#pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const int x = __shfl_up_sync(0xffffffffu, sum, o);
-            if (lane >= o) sum += x;
-          }
-          const int all = __shfl_sync(0xffffffffu, sum, 31);
-          if (rest < all) {
-            const int at = __ffs(__ballot_sync(0xffffffffu, rest < sum)) - 1;
-            qt = q0 + at;
-            off = (int)rest - (__shfl_sync(0xffffffffu, sum, at) - __shfl_sync(0xffffffffu, cost, at));
-            break;
-          }
-          rest -= all;
-        }
-        break;
-      }
-      before += __shfl_sync(0xffffffffu, incl, 31);
+      for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+      U += x;
+      b0 += 32;
+      if (b0 < p.a.n_seqs) continue;
+      G = min((int64_t)gridDim.x, U);
+      if (cta >= G) break;
+      x = div_u64((cta + (lane & 1)) * U, G);
+      u = __shfl_sync(0xffffffffu, x, 0);
+      u1 = __shfl_sync(0xffffffffu, x, 1);
+      counted = true;
+      b0 = 0;
+      continue;
     }
+    int64_t incl = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t x = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += x;
+    }
+    const unsigned past = __ballot_sync(0xffffffffu, u < before + incl);
+    if (past) {
+      const int l = __ffs(past) - 1;
+      b = b0 + l;
+      const int64_t hu = div_u64(__shfl_sync(0xffffffffu, own, l), p.v.n_kv_heads);
+      int64_t rest = u - before - (__shfl_sync(0xffffffffu, incl, l) - __shfl_sync(0xffffffffu, own, l));
+      s = shuffled(s, l);
+      nqt = row_tiles(p, s);
+      h = (int)div_u64(rest, hu);
+      rest -= h * hu;
+      for (int q0 = 0; q0 < nqt; q0 += 32) {
+        const int cost = q0 + lane < nqt ? kItemCost + item_of(p, s, q0 + lane).tiles : 0;
+        int sum = cost;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int x = __shfl_up_sync(0xffffffffu, sum, o);
+          if (lane >= o) sum += x;
+        }
+        const int all = __shfl_sync(0xffffffffu, sum, 31);
+        if (rest < all) {
+          const int at = __ffs(__ballot_sync(0xffffffffu, rest < sum)) - 1;
+          qt = q0 + at;
+          off = (int)rest - (__shfl_sync(0xffffffffu, sum, at) - __shfl_sync(0xffffffffu, cost, at));
+          break;
+        }
+        rest -= all;
+      }
+      break;
+    }
+    before += __shfl_sync(0xffffffffu, incl, 31);
+    b0 += 32;
   }
   Join join = {};
   unsigned n = 0;
@@ -660,48 +662,53 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     unsigned n_s = 0, n_o = 0, tiles = 0;  // tiles: of the CTA, as the dequantisers count them
     bool ok = true;
 
-    // This warp's 32 rows of an item into the Q tile: D / 8 lanes a row, 16 bytes each, all loads in flight. A row is
+    // This warp's 32 rows of an item into the Q tile: D / 8 lanes a row, 16 bytes each, the loads of 16 rows in flight
+    // (all 32 at once are twice the code, which comes from memory at a call's start: the mixed step took 128 us against
+    // 124; a quarter at a time waits too often, 415 us for the prompt of 8192 tokens against 393). A row is
     // scaled by a power of two that brings its largest element to 2^7 .. 2^8, so that f16 holds its bf16 values.
     auto load_q = [&](const Segment& x) {
-      constexpr int C = D / 8, RPI = 32 / C, N = C;  // N = 32 / RPI loads a lane
-      uint4 w[N];
+      constexpr int C = D / 8, RPI = 32 / C, N = C / 2;  // 32 / RPI loads a lane, N at a time
+#pragma unroll 1
+      for (int j0 = 0; j0 < C; j0 += N) {
+        uint4 w[N];
 #pragma unroll
-      for (int j = 0; j < N; ++j) {
-        const int in_item = 128 * i + 32 * quarter + j * RPI + lane / C;
-        w[j] = make_uint4(0, 0, 0, 0);
-        if (in_item < x.rows) {
-          const unsigned R = x.r0 + in_item, tok = div_group(p, R);
-          w[j] = *reinterpret_cast<const uint4*>(p.a.q + (int64_t)(x.row + tok) * p.a.ld_q +
-                                                 (int64_t)(x.h * p.v.group + R - tok * p.v.group) * D + (lane % C) * 8);
+        for (int j = 0; j < N; ++j) {
+          const int in_item = 128 * i + 32 * quarter + (j0 + j) * RPI + lane / C;
+          w[j] = make_uint4(0, 0, 0, 0);
+          if (in_item < x.rows) {
+            const unsigned R = x.r0 + in_item, tok = div_group(p, R);
+            w[j] = *reinterpret_cast<const uint4*>(p.a.q + (int64_t)(x.row + tok) * p.a.ld_q +
+                                                   (int64_t)(x.h * p.v.group + R - tok * p.v.group) * D + (lane % C) * 8);
+          }
         }
-      }
-      uint32_t top[N / 2];  // the rows' largest magnitudes as bf16, of loads j and j + N / 2
+        uint32_t top[N / 2];  // the rows' largest magnitudes as bf16, of loads j and j + N / 2
 #pragma unroll
-      for (int j = 0; j < N / 2; ++j) {
-        auto largest = [](const uint4& x) {
-          constexpr uint32_t kAbs = 0x7FFF7FFFu;
-          const uint32_t t = __vmaxu2(__vmaxu2(x.x & kAbs, x.y & kAbs), __vmaxu2(x.z & kAbs, x.w & kAbs));
-          return max(t & 0xFFFFu, t >> 16);
-        };
-        top[j] = largest(w[j]) | (largest(w[j + N / 2]) << 16);
+        for (int j = 0; j < N / 2; ++j) {
+          auto largest = [](const uint4& x) {
+            constexpr uint32_t kAbs = 0x7FFF7FFFu;
+            const uint32_t t = __vmaxu2(__vmaxu2(x.x & kAbs, x.y & kAbs), __vmaxu2(x.z & kAbs, x.w & kAbs));
+            return max(t & 0xFFFFu, t >> 16);
+          };
+          top[j] = largest(w[j]) | (largest(w[j + N / 2]) << 16);
 #pragma unroll
-        for (int o = 1; o < C; o <<= 1) top[j] = __vmaxu2(top[j], __shfl_xor_sync(0xffffffffu, top[j], o));
-      }
+          for (int o = 1; o < C; o <<= 1) top[j] = __vmaxu2(top[j], __shfl_xor_sync(0xffffffffu, top[j], o));
+        }
 #pragma unroll
-      for (int j = 0; j < N; ++j) {
-        const uint32_t eb = (j < N / 2 ? top[j % (N / 2)] & 0xFFFFu : top[j % (N / 2)] >> 16) >> 7;  // exponent
-        const uint32_t es = eb == 255u ? 127u : min(261u - eb, 254u);  // not finite: as it is
-        const float f = sign * __uint_as_float(es << 23);
-        const uint32_t mine = __shfl_sync(0xffffffffu, es, lane % RPI * C);
-        if (lane / RPI == j) sl_next = fmaxf(scale * __uint_as_float((254u - mine) << 23), 1e-37f);
-        const int rr = 32 * quarter + j * RPI + lane / C, ch = lane % C;
-        auto pair = [&](uint32_t a, uint32_t b, bool up) {
-          return up ? pack_f16x2(f * __uint_as_float(a & 0xFFFF0000u), f * __uint_as_float(b & 0xFFFF0000u))
-                    : pack_f16x2(f * __uint_as_float(a << 16), f * __uint_as_float(b << 16));
-        };
-        const uint4 o = make_uint4(pair(w[j].x, w[j].z, false), pair(w[j].x, w[j].z, true), pair(w[j].y, w[j].w, false),
-                                   pair(w[j].y, w[j].w, true));
-        sts128(q_at + i * kTileBytes + (ch / 8) * (128 * 128) + rr * 128 + (((ch % 8) ^ (rr & 7)) * 16), o);
+        for (int j = 0; j < N; ++j) {
+          const uint32_t eb = (j < N / 2 ? top[j % (N / 2)] & 0xFFFFu : top[j % (N / 2)] >> 16) >> 7;  // exponent
+          const uint32_t es = eb == 255u ? 127u : min(261u - eb, 254u);  // not finite: as it is
+          const float f = sign * __uint_as_float(es << 23);
+          const uint32_t mine = __shfl_sync(0xffffffffu, es, lane % RPI * C);
+          if (lane / RPI == j0 + j) sl_next = fmaxf(scale * __uint_as_float((254u - mine) << 23), 1e-37f);
+          const int rr = 32 * quarter + (j0 + j) * RPI + lane / C, ch = lane % C;
+          auto pair = [&](uint32_t a, uint32_t b, bool up) {
+            return up ? pack_f16x2(f * __uint_as_float(a & 0xFFFF0000u), f * __uint_as_float(b & 0xFFFF0000u))
+                      : pack_f16x2(f * __uint_as_float(a << 16), f * __uint_as_float(b << 16));
+          };
+          const uint4 o = make_uint4(pair(w[j].x, w[j].z, false), pair(w[j].x, w[j].z, true), pair(w[j].y, w[j].w, false),
+                                     pair(w[j].y, w[j].w, true));
+          sts128(q_at + i * kTileBytes + (ch / 8) * (128 * 128) + rr * 128 + (((ch % 8) ^ (rr & 7)) * 16), o);
+        }
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -709,7 +716,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     };
 
     // One copy of the code that loads rows, met before every segment: the first time with nothing to compute. (The three
-    // roles' loops share the instruction cache; with three copies the prompt of 8192 tokens took 396 us.)
+    // roles' loops share the instruction cache: three copies cost the prompt of 8192 tokens 5 us, the mixed step 4.)
     Segment g = {};
     bool mine = false;  // a short item has no second half
     for (unsigned n = 0;;) {
@@ -894,7 +901,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           __nv_bfloat16* dst = p.a.out + (int64_t)(g.row + tok) * p.a.ld_out +
                                (int64_t)(g.h * p.v.group + R - tok * p.v.group) * D;
           const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
+#pragma unroll 1
           for (int j = 0; j < D; j += 32) {
             uint32_t o[32];
             tmem_ld_x32(o_t + j, o);
@@ -911,7 +918,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           }
         } else {
           float* slot = p.part + (int64_t)(g.slot * 2 + i) * kPart + row;
-#pragma unroll
+#pragma unroll 1
           for (int j = 0; j < D; j += 32) {
             uint32_t o[32];
             tmem_ld_x32(o_t + j, o);
