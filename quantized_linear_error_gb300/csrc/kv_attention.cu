@@ -11,9 +11,10 @@ spear_status_t kv_launch_attention(spear_kv_s* h, const KvAttnArgs& a, cudaStrea
   char* ws = static_cast<char*>(h->ws);
   auto* counters = reinterpret_cast<unsigned*>(ws + 128);
   auto* part = reinterpret_cast<float*>(ws + kKvControlBytes);
-  // Up to kKvDecodeRows rows a key/value head the few-row kernel is the faster, 32 sequences x 8 key/value heads x 4000
-  // keys with 16 / 24 / 32 rows: 60 / 101 / 102 us against 115 of the chunk kernel, whose time is the same from 9 to 128
-  // rows (D = 64: 39 / 74 / 74 against 80); 64 sequences of 500 keys with 32 rows: 51 against 59.
+  // Up to kKvDecodeRows rows a key/value head the few-row kernel is the faster or as fast, 32 sequences x 8 key/value
+  // heads x 4000 keys with 16 / 24 / 32 rows: 59 / 101 / 103 us against 99 of the chunk kernel, whose time is the same
+  // from 9 to 128 rows (D = 64: 39 / 74 / 74 against 78); 64 sequences of 500 keys with 20 rows: 46 against 49 (D = 64:
+  // 29 against 36); 4 of 4000 keys with 32 rows: 24 against 25 (D = 64: 18 against 21).
   // Both kernels read the lengths on the device and leave the other's sequences
   // out; they follow each other on the stream, so they share the workspace.
   const int64_t most = (int64_t)a.max_q * h->view.group;

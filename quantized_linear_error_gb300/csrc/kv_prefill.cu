@@ -19,8 +19,8 @@
 //
 // A row tile with at most 128 rows leaves the other half idle, and a key tile
 // then takes 2700 cycles, of which the dequantisers need 2200: both halves at
-// every other tile of it were no faster (127 us against 121 for 32 sequences x
-// 12 drafts x 4 heads at 4000 keys).
+// every other tile of it were 5% slower (32 sequences x 12 drafts x 4 heads at
+// 4000 keys).
 //
 //  - Operands are f16, whose 11 bits hold queries and codes' values with an
 //    error far below that of the bf16 result (bf16 operands doubled it). Rows
