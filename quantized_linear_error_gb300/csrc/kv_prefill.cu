@@ -12,7 +12,7 @@
 // dequantised tiles' stores 512; a block takes some 2800 here, the chain
 // scores, weights, product of one half being longer than the other half's
 // products that hide it. Measured, D = 128: a prompt of 8192 tokens, 32 heads
-// over 8 (550 GFLOP), 393 us or 1.40 PFLOP/s in bursts, 71% of a library
+// over 8 (550 GFLOP), 388 us or 1.42 PFLOP/s in bursts, 72% of a library
 // product's rate, and 405 to 415 us once the power limit lowers the clocks; 320
 // tokens behind 7901 (42 GFLOP) 45 us, of which 5 are the start and 8 partial
 // results and their join.
@@ -349,12 +349,15 @@ SPEAR_DEVINL void sts128(uint32_t addr, const uint4& v) {
 template <int D, class F>
 SPEAR_DEVINL void dequant_row(uint32_t src, uint32_t tile, int key, int half, F convert) {
   constexpr int Q = D / 64;  // 16-byte quarters of the packed row a thread
+  // D = 128: quarters in an order of the key's own, so that a quarter warp meets every bank once
+  auto quarter = [&](int i) { return Q == 2 ? (i + 2 * half + (key >> 1)) & 3 : half; };
+  uint4 w[Q];
+#pragma unroll
+  for (int i = 0; i < Q; ++i) w[i] = lds128(src + quarter(i) * 16);
 #pragma unroll
   for (int i = 0; i < Q; ++i) {
-    // D = 128: quarters in an order of the key's own, so that a quarter warp meets every bank once
-    const int q = Q == 2 ? (i + 2 * half + (key >> 1)) & 3 : half;
-    const uint4 w = lds128(src + q * 16);
-    const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+    const int q = quarter(i);
+    const uint32_t words[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
     const uint32_t row = tile + (q >> 1) * (kTile * 128) + key * 128;
 #pragma unroll
     for (int j = 0; j < 4; ++j)
