@@ -431,7 +431,7 @@ __global__ void __launch_bounds__(32 * (kKeyWarps * RG + 1), per_sm(D, NT, RG))
       // this lane's row of the four 8 x 8 matrices of 16-bit words: key lane % 16 (its low 8 first), chunk lane / 8 % 2
       const uint32_t vrow = base + 8 * D + ((lane & 7) + (lane >> 4) * 8) * (D / 2) + ((lane >> 3) & 1) * 16;
       auto tile = [&](auto masked) {
-        // the value scale of one key a lane (past the end anything), looked at below
+        // the value scale of one key a lane, looked at below
         const uint32_t sv = lds32(base + (lane >> 4) * BB + 16 * D + 64 + 4 * (lane & 15));
         float sc[2][NT][4];
         // ---- scores
@@ -490,7 +490,9 @@ __global__ void __launch_bounds__(32 * (kKeyWarps * RG + 1), per_sm(D, NT, RG))
             over |= top[nt][k] > m[nt][k] + kLazy;
           }
         // p S, p <= 2^8, is taken in f16 for scales of 2^-13 .. 2^7, in bf16 where one of the 32 keys has another
-        const bool odd = (uint16_t)(sv - 0x3900u) > 0x0A00u;
+        bool odd = (uint16_t)(sv - 0x3900u) > 0x0A00u;
+        // of keys that some row sees: past the end stands what earlier work has left, and the results' bits must not follow it
+        if constexpr (masked) odd = odd && key0 + lane < s.L && (p.a.window == 0 || key0 + lane > s.L - s.n - p.a.window);
         bool wide = false;
         if (__any_sync(0xffffffffu, over || odd)) {  // one vote in nearly all cases
           wide = __any_sync(0xffffffffu, odd);
