@@ -111,11 +111,12 @@ def attention(q: np.ndarray, K: np.ndarray, V: np.ndarray, scale: float, window:
     return out, mag, ref
 
 
-def tolerance(out: np.ndarray, mag: np.ndarray, ref: np.ndarray) -> np.ndarray:
+def tolerance(out: np.ndarray, mag: np.ndarray, ref: np.ndarray, keys: float = 2.0 ** -9) -> np.ndarray:
     """Largest error of an implementation that rounds the result, the weights and the cached values to bf16 once
-    (2^-9 relative each) and keeps everything else in fp32. Keys off by 2^-9 move a score by d = 2^-9 ref at most
+    (2^-9 relative each) and keeps everything else in fp32. Keys off by `keys` move a score by d = keys ref at most
     and a weight by a factor within exp(+-2 d) (numerator and denominator); the roundings of weights and values add
     2^-9 each, of a value or of its distance from the middle of its row's range, which is at most 16/15 of the row's
-    largest element (mag); the weights' sum takes one such rounding too. fp32 sums stay well within what is left."""
-    d = 2.0 ** -9 * ref[..., None]
-    return 2.0 ** -9 * np.abs(out) + (np.expm1(2 * d) + 3.5 * 2.0 ** -9) * mag[..., None] * 16 / 15 + 1e-30
+    largest element (mag); the weights' sum takes one such rounding too. fp32 sums stay well within what is left. The
+    bound scales with the values and is zero for a row that sees none but zeros: such a row has no error."""
+    d = keys * ref[..., None]
+    return 2.0 ** -9 * np.abs(out) + (np.expm1(2 * d) + 3.5 * 2.0 ** -9) * mag[..., None] * 16 / 15

@@ -6,6 +6,7 @@ import torch
 from oracle import kv
 from quantized_linear_error_gb300 import spear
 
+from . import kv_cases
 from .test_gpu_kv_attention import Batch
 
 pytestmark = pytest.mark.gpu
@@ -13,6 +14,10 @@ pytestmark = pytest.mark.gpu
 
 def _dev(a):
     return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+def _f64(t):
+    return t.float().cpu().numpy().astype(np.float64)
 
 
 def _leftovers(D, word):
@@ -26,6 +31,16 @@ def _leftovers(D, word):
         c.attention(q, torch.empty_like(q), torch.arange(2, **i32).repeat(100, 1), torch.full((100,), 256, **i32),
                     torch.arange(0, 100 * n + 1, n, **i32), n)
         assert c.check() == spear.SPEAR_OK
+
+
+# ---------------------------------------------------------------------------------- exact scores
+@pytest.mark.parametrize("name", kv_cases.CASES)
+def test_scores_held_exactly(name):
+    """The reference of the running sums, where a score's own rounding leaves the bound no room."""
+    b = kv_cases.CASES[name]()
+    got = b.run(window=b.window, scale=b.scale)
+    assert b.c.check() == spear.SPEAR_OK
+    kv_cases.check(b, _f64(got))
 
 
 # ---------------------------------------------------------------------------------- past the end of a sequence
