@@ -28,12 +28,19 @@
 //    taken at the end. Codes are centred, lo - 8 and byte - 136, exact in 16
 //    bits (small magnitudes: neither the fp32 sums nor the rounding of p S lose
 //    to a large common term); sum p (O + 8 S) is kept beside it in fp32. p S is
-//    rounded to f16, 11 bits; 32 keys with a scale that could leave its range
-//    go through bf16, 8 bits, with the same accumulators.
+//    rounded to f16, 11 bits (its range: see the reference, below); 32 keys with
+//    a scale far below the largest so far go through bf16, 8 bits, with the same
+//    accumulators.
 //    The scores' accumulator layout becomes p^T's operand layout by one 8 x 8
 //    transpose (movmatrix).
-//  - The running maximum is lazy: p = 2^(s - m) with any m that is at most 8
-//    below the maximum; sums are only rescaled when some score passes m + 8.
+//  - The reference m of the weights p = 2^(s - m) is free, and does two things.
+//    It follows the maximum lazily: sums are only rescaled when some score passes
+//    it by 8 more than at first. And it lies k below the maximum, k such that the
+//    warp's largest value scale so far times 2^k is in 2^6 .. 2^7: then p S is
+//    below 2^15, and all of f16's range beneath serves small weights, which keep
+//    8 bits down to some 2^-22 of the largest and are lost below 2^-31. (With k =
+//    0 weights of 2^-17 of values of size 0.01 were lost: thousands of keys
+//    behind one that has most of the weight.)
 //
 // Work: (sequence, head, tile of 128 keys) units, in this order, are split
 // evenly over the CTAs, whatever the lengths, which only the device knows. A
@@ -74,6 +81,10 @@ constexpr int kMinUnits = 4;                   // a CTA's, where there are few o
                                                // without the rule, 11.8 with it)
 constexpr int kScan = 10;                      // warps at most
 constexpr float kLazy = 8.f;
+// Value scales, by their exponent fields. Largest ones of 2^-54 .. 2^46 choose k (beyond, 2^k and the sums could leave fp32);
+// f16 takes this many binades from the largest down.
+constexpr uint32_t kScaleMin = 73, kScaleMax = 173, kScaleBinades = 10;
+constexpr uint32_t kNoScale = 255u << 23;
 // A variant: NT 8-row MMA tiles a warp, RG groups of warps with rows of their own over the same keys (four tiles in one
 // warp's registers spill and leave four warps an SM). CTAs an SM: the accumulators and the rows of q take 3 D NT / 8
 // registers a thread.
@@ -147,31 +158,29 @@ struct Cursor {
   KvSeq s;
 };
 
-// A CTA's share of an item: tiles [t0, t1), counted from s.lo.
+// A CTA's share of the item that its cursor stands at (or at the end of): tiles [t0, t1), counted from s.lo.
 struct Segment {
-  KvSeq s;
-  int b, h, t0, t1;
-  int64_t unit0;  // the unit of tile 0
+  int t0, t1;
 };
 
+// (The cursor goes on to the next item only when that is asked for, so that an item's numbers are held once.)
 SPEAR_DEVINL bool next_segment(const DecodeParams& p, Cursor& c, int64_t u1, Segment& g) {
   while (c.u < u1) {
+    if (c.off == kItemCost + c.s.tiles) {
+      c.off = 0;
+      if (++c.h == p.v.n_kv_heads) {
+        c.h = 0;
+        do {
+          ++c.b;
+          c.s = kv_seq(p.v, p.a, c.b, kTile);
+        } while (seq_units(p, c.s) == 0);
+      }
+    }
     const int end = (int)min((int64_t)kItemCost + c.s.tiles, c.off + (u1 - c.u));
-    g.s = c.s;
-    g.b = c.b;
-    g.h = c.h;
     g.t0 = max(0, c.off - kItemCost);
     g.t1 = max(0, end - kItemCost);
-    g.unit0 = c.u - c.off + kItemCost;
     c.u += end - c.off;
-    c.off = 0;
-    if (c.u < u1 && ++c.h == p.v.n_kv_heads) {
-      c.h = 0;
-      do {
-        ++c.b;
-        c.s = kv_seq(p.v, p.a, c.b, kTile);
-      } while (seq_units(p, c.s) == 0);
-    }
+    c.off = end;
     if (g.t1 > g.t0) return true;
   }
   return false;
@@ -301,14 +310,14 @@ __global__ void __launch_bounds__(32 * (kKeyWarps * RG + 1), per_sm(D, NT, RG))
     bool bad = false;
     int issued = 0;
     while (!bad && next_segment(p, c, u1, sg)) {
-      const int blocks = (sg.s.L + 15) / 16;
+      const int blocks = (c.s.L + 15) / 16;
       for (int i = sg.t0; i < sg.t1; ++i) {
-        const int blk = (sg.s.lo + i) * kBlocksPerTile + lane;
+        const int blk = (c.s.lo + i) * kBlocksPerTile + lane;
         const uint8_t* src = nullptr;
         if (lane < kBlocksPerTile && blk < blocks) {
-          const int pg = p.a.page_table[(int64_t)sg.b * p.a.ld_pt + blk / p.v.bpp];
+          const int pg = p.a.page_table[(int64_t)c.b * p.a.ld_pt + blk / p.v.bpp];
           if (pg >= 0 && pg < p.v.n_pages)
-            src = p.v.pool + (((int64_t)pg * p.v.n_kv_heads + sg.h) * p.v.bpp + blk % p.v.bpp) * BB;
+            src = p.v.pool + (((int64_t)pg * p.v.n_kv_heads + c.h) * p.v.bpp + blk % p.v.bpp) * BB;
           else
             atomicOr(p.v.status, kStatusBadIndex);
         }
@@ -344,7 +353,7 @@ __global__ void __launch_bounds__(32 * (kKeyWarps * RG + 1), per_sm(D, NT, RG))
 
   while (next_segment(p, c, u1, sg)) {
     const int len = sg.t1 - sg.t0;
-    const KvSeq s = sg.s;
+    const KvSeq& s = c.s;
     const int rows = s.n * p.v.group;
 
     // the rows as f16 B fragments, their sums and their scales
@@ -359,7 +368,7 @@ __global__ void __launch_bounds__(32 * (kKeyWarps * RG + 1), per_sm(D, NT, RG))
       for (int i = 0; i < KW; ++i) w[i] = make_uint4(0, 0, 0, 0);
       if (r < rows) {
         const __nv_bfloat16* src = p.a.q + (int64_t)(s.row + r / p.v.group) * p.a.ld_q +
-                                   (int64_t)(sg.h * p.v.group + r % p.v.group) * D + t * (D / 4);
+                                   (int64_t)(c.h * p.v.group + r % p.v.group) * D + t * (D / 4);
 #pragma unroll
         for (int i = 0; i < KW; ++i) w[i] = reinterpret_cast<const uint4*>(src)[i];
       }
@@ -410,6 +419,8 @@ __global__ void __launch_bounds__(32 * (kKeyWarps * RG + 1), per_sm(D, NT, RG))
     }
     float acc[D / 16][NT][4];
     float m[NT][2], l[NT][2], off[NT][2];
+    uint32_t low_s = kNoScale;  // bits of the lowest value scale that f16 takes; none has been met yet
+    float lazy = kLazy;         // kLazy + k
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -487,15 +498,25 @@ __global__ void __launch_bounds__(32 * (kKeyWarps * RG + 1), per_sm(D, NT, RG))
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             top[nt][k] = fmaxf(fmaxf(sc[0][nt][k], sc[0][nt][k + 2]), fmaxf(sc[1][nt][k], sc[1][nt][k + 2]));
-            over |= top[nt][k] > m[nt][k] + kLazy;
+            over |= top[nt][k] > m[nt][k] + lazy;
           }
-        // p S, p <= 2^8, is taken in f16 for scales of 2^-13 .. 2^7, in bf16 where one of the 32 keys has another
-        bool odd = (uint16_t)(sv - 0x3900u) > 0x0A00u;
-        // of keys that some row sees: past the end stands what earlier work has left, and the results' bits must not follow it
-        if constexpr (masked) odd = odd && key0 + lane < s.L && (p.a.window == 0 || key0 + lane > s.L - s.n - p.a.window);
+        // Scales that f16 takes? (0, of a row of one value, it does not.) Of keys that some row sees: past the end stands
+        // what earlier work has left, and the results' bits must not follow it.
+        const uint32_t scale = sv << 16;
+        bool counts = true;
+        if constexpr (masked) counts = key0 + lane < s.L && (p.a.window == 0 || key0 + lane > s.L - s.n - p.a.window);
+        auto odd = [&] { return counts && scale - low_s > (kScaleBinades << 23 | 0x7FFFFF); };
         bool wide = false;
-        if (__any_sync(0xffffffffu, over || odd)) {  // one vote in nearly all cases
-          wide = __any_sync(0xffffffffu, odd);
+        if (__any_sync(0xffffffffu, over || odd())) {  // one vote in nearly all cases
+          const float below = lazy - kLazy;  // m is so much below the maximum
+          const uint32_t ex = scale >> 23 & 255u;
+          const uint32_t most = __reduce_max_sync(
+              0xffffffffu, counts && ex - 1u < 254u ? min(max(ex, kScaleMin), kScaleMax) : 0u);
+          if (low_s == kNoScale ? most > 0 : most > (low_s >> 23) + kScaleBinades) {
+            low_s = (most - kScaleBinades) << 23;
+            lazy = kLazy + 133.f - (float)most;
+          }
+          wide = __any_sync(0xffffffffu, odd());
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -503,7 +524,7 @@ __global__ void __launch_bounds__(32 * (kKeyWarps * RG + 1), per_sm(D, NT, RG))
               float x = top[nt][k];
 #pragma unroll
               for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-              const float mn = fmaxf(m[nt][k], x);
+              const float mn = fmaxf(m[nt][k] + below, x) - (lazy - kLazy);
               const float f = m[nt][k] == -INFINITY ? 0.f : ex2(m[nt][k] - mn);
               m[nt][k] = mn;
               l[nt][k] *= f;
@@ -630,7 +651,7 @@ __global__ void __launch_bounds__(32 * (kKeyWarps * RG + 1), per_sm(D, NT, RG))
     auto write_row = [&](int r, const float (&o)[E], float inv) {
       if (r >= rows) return;
       __nv_bfloat16* dst = p.a.out + (int64_t)(s.row + r / p.v.group) * p.a.ld_out +
-                           (int64_t)(sg.h * p.v.group + r % p.v.group) * D + lane * E;
+                           (int64_t)(c.h * p.v.group + r % p.v.group) * D + lane * E;
       uint32_t w[E / 2];
 #pragma unroll
       for (int e = 0; e < E; e += 2) w[e / 2] = pack_bf16x2(o[e] * inv, o[e + 1] * inv);
@@ -664,7 +685,8 @@ __global__ void __launch_bounds__(32 * (kKeyWarps * RG + 1), per_sm(D, NT, RG))
     }
     if (!whole) {
       // CTAs ca .. cb hold the item's units
-      const int64_t x0 = div_u64(((lane & 1) ? sg.unit0 + s.tiles : sg.unit0 + 1) * G - 1, U);
+      const int64_t unit0 = c.u - c.off + kItemCost;  // of tile 0
+      const int64_t x0 = div_u64(((lane & 1) ? unit0 + s.tiles : unit0 + 1) * G - 1, U);
       const int ca = (int)__shfl_sync(0xffffffffu, x0, 0), parts = (int)__shfl_sync(0xffffffffu, x0, 1) - ca + 1;
       consumer_sync<32 * kWarps>();
       // release what the barrier above has collected from the four warps, acquire what the others released

@@ -67,3 +67,51 @@ def test_what_lies_past_the_end_changes_no_bit(D, n):
             first = got if first is None else first
             assert torch.equal(got, first), (window, hex(fill), hex(word), [
                 L for i, (_, L) in enumerate(seqs) if not torch.equal(got[i * n:i * n + n], first[i * n:i * n + n])])
+
+
+# ---------------------------------------------------------------------------------- small weights
+def _shared_cache(b, copies):
+    """The one sequence of b, `copies` times over the same pages with the same queries, so that every CTA has whole items."""
+    n, L = b.seqs[0]
+    c = spear.SpearKVCache(b.Hq, b.Hk, b.D, b.page, _dev(b.pool))
+    q = b.q.cuda().repeat(copies, 1, 1)
+    out = torch.empty_like(q)
+    c.attention(q, out, _dev(b.table).repeat(copies, 1), _dev(np.full(copies, L, np.int32)),
+                _dev(np.arange(copies + 1, dtype=np.int32) * n), n, scale=b.scale)
+    assert c.check() == spear.SPEAR_OK
+    return out.view(copies, n, b.Hq, b.D)
+
+
+def test_small_weights_of_small_values_few_rows():
+    """Keys that hold nearly all of the weight, and whose values are small, before thousands with weights near 2^-17 and
+    values of size 0.01 with a channel of one sign: their sum is a third of the result."""
+    L, D, Hk = 16384, 128, 8
+    def edit(i, k, v, rng):
+        k[:] = kv_cases.key_rows(rng, k.shape, 2.0 ** -5)
+        k[:, :, 2:18] = 0
+        v[:] = rng.normal(size=v.shape)
+        v[:, :, 0] = 3
+        v *= 0.01
+        for j in (0, 33, 70, 100):  # one for each warp's keys of a tile
+            k[j], v[j] = 0, v[j] * 0.02
+            k[j, :, 2:18] = 1.0
+    b = kv_cases.case([(1, L)], Hk, Hk, D, 64, edit, kv_cases.query_rows(5, 1, Hk, D, most=2), scale=0.75)
+    b.q[:, :, 2:18] = 1.0
+    out = _shared_cache(b, 60)
+    for s in (0, 30, 59):
+        kv_cases.check(b, _f64(out[s]))
+
+
+def test_value_scales_of_every_size_in_one_cache():
+    """Blocks of values that grow and shrink by 2^5 to 2^40 from one to the next, and single rows among them."""
+    for step in (5, 20, 40, -5, -20, -40):
+        def edit(i, k, v, rng):
+            k[:] = kv_cases.key_rows(rng, k.shape, 2.0 ** -5)
+            e = (np.arange(len(v)) // 32 % 2 if abs(step) > 20 else np.arange(len(v)) // 96 % 4) * step
+            e[7::50] = rng.integers(-40, 41, len(e[7::50]))
+            v *= 2.0 ** e[:, None, None]
+        for n in (1, 4, 60):
+            b = kv_cases.case([(n, 700), (n, 90)], 4, 2, 64, 16, edit, kv_cases.query_rows(n, 2 * n, 4, 64), seed=step + 40)
+            got = b.run(scale=b.scale)
+            assert b.c.check() == spear.SPEAR_OK
+            kv_cases.check(b, _f64(got))
