@@ -39,9 +39,12 @@
 //  - Two softmax warpgroups, one an MMA tile, one row a thread; P goes from
 //    registers to tensor memory in two parts, so that the product with the
 //    first 64 keys runs while the other weights are computed. m need not be the
-//    maximum: weights and sums keep their relative precision whatever their
-//    size, so that m is taken from a segment's first tile and again only when
-//    the weights of 64 keys sum to more than 2^14; no other tile takes a maximum.
+//    maximum: it is taken from a segment's first tile, 8 binades below its
+//    maximum, and again only when the weights of 64 keys sum to more than 2^15;
+//    no other tile takes a maximum. In between all of f16's range serves: weights
+//    keep 8 bits down to 2^-24 of the largest, and are lost below 2^-33 (with the
+//    maximum itself for m 2^-16 and 2^-25: thousands of keys of weight 2^-22
+//    behind one came out 14% off).
 //  - Two warps issue the MMAs, one a half, in turns "product of the last tile,
 //    scores of the next": an S overwrites its P only after the product that
 //    reads it, which the same warp issued before it.
@@ -70,7 +73,8 @@ constexpr int kItemCost = 4;          // units
 constexpr int kHeader = 1024;         // barriers, segments
 constexpr int kSegs = 4;              // segments in flight
 constexpr int kSegReaders = 8 + kDeqWarps + 2 + 1;  // warps that read each segment
-constexpr float kBig = 0x1p14f;  // weights up to here fit f16
+constexpr float kBig = 0x1p15f;   // weights up to here fit f16
+constexpr float kFresh = 8.f;     // log2 of the largest weight when m is taken
 constexpr uint32_t kHintNs = 100;
 // setmaxnreg: 256 x 168 + 384 x 48 registers are the 640 x 96 of the launch
 constexpr int kJoinRows = 32;
@@ -751,6 +755,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           for (int x = 0; x < 32; ++x)
             if (!(see & (1u << x))) x32[x] = 0xFF800000u;
         };
+        auto below = [&](float mx) { return mx - __fdividef(kFresh, sl); };
         auto rescale = [&](float mx) {  // m becomes mx, what has been summed is scaled to it
           const float f = m == -INFINITY ? 0.f : ex2((m - mx) * sl);
           l *= f;
@@ -787,6 +792,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
 #pragma unroll
               for (int x = 0; x < 32; x += 2)
                 m = fmaxf(m, fmaxf(__uint_as_float(v[j][x]), __uint_as_float(v[j][x + 1])));
+            m = below(m);
           }
           uint32_t w[32];
           // weights of 64 keys by the present m, and their sum
@@ -820,7 +826,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
               ok = warp_wait(&hd.pa_done[i], (n_s & 1u) ^ 1u, p.wait_ns, kHintNs);  // the product with the first weights
               if (!ok) break;
               tc_fence_after_sync();
-              float mx = m;
+              float mx = -INFINITY;
 #pragma unroll
               for (int j = 2; j < 4; ++j) {
                 tmem_ld_x32(s_t + 32 * j, v[j]);
@@ -829,7 +835,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
 #pragma unroll
                 for (int x = 0; x < 32; ++x) mx = fmaxf(mx, __uint_as_float(v[j][x]));
               }
-              rescale(mx);
+              rescale(fmaxf(m, below(mx)));
               sum = 0.f;
 #pragma unroll
               for (int x = 0; x < 64; x += 2) {
@@ -848,7 +854,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         if (!done) {
           // A new maximum, rows that have seen nothing, keys or values out of f16's range: 32 keys at a time, twice. (The product
           // before has finished, s_full covers it; the next waits for this thread.)
-          float mx = m;
+          float mx = -INFINITY;
 #pragma unroll 1
           for (int j = 0; j < 4; ++j) {
             uint32_t x32[32];
@@ -866,9 +872,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           }
           tmem_st_wait();
           if (k > 0)
-            rescale(mx);
+            rescale(fmaxf(m, below(mx)));
           else
-            m = mx;
+            m = below(mx);
           const float mu = m == -INFINITY ? 0.f : m;
 #pragma unroll 1
           for (int j = 0; j < 4; ++j) {

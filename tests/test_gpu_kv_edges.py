@@ -102,6 +102,22 @@ def test_small_weights_of_small_values_few_rows():
         kv_cases.check(b, _f64(out[s]))
 
 
+@pytest.mark.parametrize("D,bits", [(64, 21.4), (128, 22.6)])
+def test_small_weights_in_a_chunk(D, bits):
+    """One key holds nearly all of the weight and its value is 0; thousands behind it have weights of 2^-bits, alike, and
+    are all of the result."""
+    n, L = 80, 6000
+    def edit(i, k, v, rng):
+        k[:] = 0
+        k[0, :, 2:18], v[0] = 1.0, 0
+    q = kv_cases.query_rows(5, n, 2, D, most=2)
+    q[:, :, 2:18] = 1.0
+    b = kv_cases.case([(n, L)], 2, 1, D, 64, edit, q, scale=bits * np.log(2) / 16)
+    out = _shared_cache(b, 200)
+    for s in (0, 100, 199):
+        kv_cases.check(b, _f64(out[s]))
+
+
 def test_value_scales_of_every_size_in_one_cache():
     """Blocks of values that grow and shrink by 2^5 to 2^40 from one to the next, and single rows among them."""
     for step in (5, 20, 40, -5, -20, -40):
