@@ -429,8 +429,9 @@ spear_status_t spear_kv_read(spear_kv_t h, const int64_t* slots, int32_t T, void
  * zeros for a row that sees no key. Softmax statistics and sums are fp32.
  *   q, out: device bf16 [T][n_heads][D], ld_q, ld_out as for spear_kv_append;
  *     out may be q itself;
- *   page_table: device int32 [n_seqs][ld_pt];  kv_lens: device int32 [n_seqs],
- *     at most 2^30;
+ *   page_table: device int32 [n_seqs][ld_pt]; entries of pages that no row sees,
+ *     past a sequence's end or wholly before its window, may be anything;
+ *   kv_lens: device int32 [n_seqs], at most 2^30;
  *   q_starts: device int32 [n_seqs + 1], ascending, within 0..T;
  *   max_q: the largest number of query rows of a sequence (>= 1);
  *   T * (n_heads / n_kv_heads) < 2^27; a window above 2^30 hides nothing.

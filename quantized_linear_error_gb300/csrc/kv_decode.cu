@@ -310,11 +310,11 @@ __global__ void __launch_bounds__(32 * (kKeyWarps * RG + 1), per_sm(D, NT, RG))
     bool bad = false;
     int issued = 0;
     while (!bad && next_segment(p, c, u1, sg)) {
-      const int blocks = (c.s.L + 15) / 16;
+      const int blocks = (c.s.L + 15) / 16, first = first_key(p.a, c.s.L - c.s.n) / 16;  // pages before may be gone
       for (int i = sg.t0; i < sg.t1; ++i) {
         const int blk = (c.s.lo + i) * kBlocksPerTile + lane;
         const uint8_t* src = nullptr;
-        if (lane < kBlocksPerTile && blk < blocks) {
+        if (lane < kBlocksPerTile && blk >= first && blk < blocks) {
           const int pg = p.a.page_table[(int64_t)c.b * p.a.ld_pt + blk / p.v.bpp];
           if (pg >= 0 && pg < p.v.n_pages)
             src = p.v.pool + (((int64_t)pg * p.v.n_kv_heads + c.h) * p.v.bpp + blk % p.v.bpp) * BB;
@@ -500,8 +500,8 @@ __global__ void __launch_bounds__(32 * (kKeyWarps * RG + 1), per_sm(D, NT, RG))
             top[nt][k] = fmaxf(fmaxf(sc[0][nt][k], sc[0][nt][k + 2]), fmaxf(sc[1][nt][k], sc[1][nt][k + 2]));
             over |= top[nt][k] > m[nt][k] + lazy;
           }
-        // Scales that f16 takes? (0, of a row of one value, it does not.) Of keys that some row sees: past the end stands
-        // what earlier work has left, and the results' bits must not follow it.
+        // Scales that f16 takes? (0, of a row of one value, it does not.) Of keys that some row sees: in other places may
+        // stand what earlier work has left, and the results' bits must not follow it.
         const uint32_t scale = sv << 16;
         bool counts = true;
         if constexpr (masked) counts = key0 + lane < s.L && (p.a.window == 0 || key0 + lane > s.L - s.n - p.a.window);

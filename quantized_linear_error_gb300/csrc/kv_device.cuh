@@ -48,6 +48,9 @@ SPEAR_DEVINL int64_t div_u64(int64_t a, int64_t b) {
   return ((uint64_t)(a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : (int64_t)((uint64_t)a / (uint64_t)b);
 }
 
+// The first key that a row at position `pos` sees.
+SPEAR_DEVINL int first_key(const KvAttnArgs& a, int pos) { return a.window > 0 ? max(0, pos - a.window + 1) : 0; }
+
 // Sequence b of a call as a kernel works on it, every index checked.
 struct KvSeq {
   int n;         // query rows (0: nothing to do)
@@ -68,8 +71,7 @@ SPEAR_DEVINL KvSeq kv_seq(const KvView& v, const KvAttnArgs& a, int b, int tile)
   if (!rows_ok || !len_ok) atomicOr(v.status, kStatusBadIndex);
   s.n = rows_ok ? end - s.row : 0;
   s.L = len_ok ? len : (len < 0 ? 0 : (int)room);
-  const int64_t first = a.window > 0 ? (int64_t)s.L - s.n - a.window + 1 : 0;  // first key that row 0 sees
-  s.lo = first > 0 ? (int)(first / tile) : 0;
+  s.lo = first_key(a, s.L - s.n) / tile;
   s.tiles = max(1, (s.L + tile - 1) / tile - s.lo);
   return s;
 }

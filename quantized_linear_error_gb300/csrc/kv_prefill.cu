@@ -33,7 +33,7 @@
 //    MN-major B operand of O, so nothing is transposed. A code word's pairs come
 //    out as elements (0, 4), (1, 5), (2, 6), (3, 7); Q's rows are permuted
 //    alike, and O's columns are put back in the epilogue. Keys past the
-//    sequence's end become zeros, and a key whose V is not finite is moved to
+//    sequence's end or before the window become zeros, and a key whose V is not finite is moved to
 //    its K (V zero, K NaN): rows that see it get NaN, the mask keeps it from the
 //    others (0 x NaN in O += P V would not).
 //  - Two softmax warpgroups, one an MMA tile, one row a thread; P goes from
@@ -99,6 +99,7 @@ struct PrefillParams {
 struct Segment {
   int len;          // 0: the end
   int b, h, L, tile0;
+  int first;        // first key that any of the item's rows sees
   int row;          // first query row of the sequence
   int pos0;         // position of the sequence's first query row
   int r0, rows;     // the item's rows of the key/value head: [r0, r0 + rows)
@@ -126,6 +127,7 @@ SPEAR_DEVINL unsigned div_group(const PrefillParams& p, unsigned R) {
 
 // Row tile qt of a sequence: its key tiles.
 struct Item {
+  int first;  // key that a row sees
   int lo, tiles;
   int rows;  // rows of this tile, <= 256
 };
@@ -141,8 +143,8 @@ SPEAR_DEVINL Item item_of(const PrefillParams& p, const KvSeq& s, int qt) {
   it.rows = min(kRows, s.n * p.v.group - r0);
   const int t0 = div_group(p, r0), t1 = div_group(p, r0 + it.rows - 1);
   const int last = s.L - s.n + t1;
-  const int first = p.a.window > 0 ? s.L - s.n + t0 - p.a.window + 1 : 0;
-  it.lo = first > 0 ? first / kTile : 0;
+  it.first = first_key(p.a, s.L - s.n + t0);
+  it.lo = it.first / kTile;
   it.tiles = max(1, (last >= 0 ? last / kTile + 1 : 0) - it.lo);
   return it;
 }
@@ -270,6 +272,7 @@ SPEAR_DEVINL void schedule(const PrefillParams& p, Header& hd, int lane) {
         g.h = h;
         g.L = s.L;
         g.tile0 = it.lo + t0;
+        g.first = it.first;
         g.row = s.row;
         g.pos0 = s.L - s.n;
         g.r0 = qt * kRows;
@@ -444,6 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     g.h = x.h;
     g.L = x.L;
     g.tile0 = x.tile0;
+    g.first = x.first;
     g.row = x.row;
     g.pos0 = x.pos0;
     g.r0 = x.r0;
@@ -467,11 +471,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       bool ok = true;
       Segment g;
       for (unsigned n = 0; ok && read_segment(n, g); ++n) {
-        const int blocks = (g.L + 15) / 16;
+        const int blocks = (g.L + 15) / 16, first = g.first / 16;  // pages before may be gone
         for (int t = 0; t < g.len; ++t) {
           const int blk = (g.tile0 + t) * kBlocksPerTile + lane;
           const uint8_t* src = nullptr;
-          if (lane < kBlocksPerTile && blk < blocks) {
+          if (lane < kBlocksPerTile && blk >= first && blk < blocks) {
             const int pg = p.a.page_table[(int64_t)g.b * p.a.ld_pt + blk / p.v.bpp];
             if (pg >= 0 && pg < p.v.n_pages)
               src = p.v.pool + (((int64_t)pg * p.v.n_kv_heads + g.h) * p.v.bpp + blk % p.v.bpp) * BB;
@@ -599,8 +603,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         const uint32_t blk = blk_at + st * kRawBytes;
         ok = warp_wait(&hd.raw_full[st], ph, p.wait_ns, kHintNs);
         if (!ok) break;
-        uint32_t kp = 0, vp = 0;  // of a key past the end: zeros
-        if ((g.tile0 + t) * kTile + key < g.L) {
+        uint32_t kp = 0, vp = 0;  // of a key past the end, or before all rows' windows: zeros
+        if (const int at = (g.tile0 + t) * kTile + key; at >= g.first && at < g.L) {
           kp = lds32(blk + 16 * D + 4 * r);
           vp = lds32(blk + 16 * D + 64 + 4 * r);
         }
@@ -613,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         };
         put_k(__uint_as_float(kp << 16), __uint_as_float(kp & 0xFFFF0000u));
         uint32_t odd = 0;
-        if (__any_sync(0xffffffffu, !fits_f16(kp) || !fits_f16(vp))) {  // the end, or parameters out of f16's range
+        if (__any_sync(0xffffffffu, !fits_f16(kp) || !fits_f16(vp))) {  // either end, or parameters out of f16's range
           if (!finite_par(vp)) vp = 0, kp = 0x7FC07FC0u;
           if (!finite_par(kp)) kp = 0x7FC07FC0u;
           const bool k_odd = kp != 0 && kp != 0x7FC07FC0u && !fits_f16(kp);

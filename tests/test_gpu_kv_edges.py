@@ -45,7 +45,7 @@ def test_scores_held_exactly(name):
 
 # ---------------------------------------------------------------------------------- past the end of a sequence
 @pytest.mark.parametrize("D", [64, 128])
-@pytest.mark.parametrize("n", [1, 4])
+@pytest.mark.parametrize("n", [1, 4, 40])
 def test_what_lies_past_the_end_changes_no_bit(D, n):
     """Free slots of a sequence's last block, blocks past it that were never copied, and keys before the window: zeros, NaN,
     scales that 16-bit weights take and scales that they do not."""
@@ -131,3 +131,16 @@ def test_value_scales_of_every_size_in_one_cache():
             got = b.run(scale=b.scale)
             assert b.c.check() == spear.SPEAR_OK
             kv_cases.check(b, _f64(got))
+
+
+# ---------------------------------------------------------------------------------- released pages
+@pytest.mark.parametrize("n,L,window,D,page", [(1, 500, 100, 128, 16), (4, 777, 64, 64, 48), (1, 1000, 1, 128, 32),
+                                               (100, 700, 128, 128, 16), (300, 1500, 200, 64, 32), (90, 900, 17, 128, 64)])
+def test_pages_before_the_window_may_be_released(n, L, window, D, page):
+    """Pages that no query row sees any more stand as -1 in the table, and nothing of them is looked at."""
+    _leftovers(D, 0x7FC07FC0)
+    seqs = [(n, L), (n, L - 130), (n, L - 5)]
+    b = Batch(seqs, 4, 2, D, page, seed=n)
+    for i, (_, length) in enumerate(seqs):
+        b.table[i, :max(0, length - n - window + 1) // page] = -1
+    b.check(b.run(window=window), window)
