@@ -426,7 +426,12 @@ spear_status_t spear_kv_read(spear_kv_t h, const int64_t* slots, int32_t T, void
  * stands at P = L - n + i and sees the keys j <= P, j >= 0, with window > 0
  * only j > P - window:
  *   out = bf16_RNE(sum_j softmax_j(scale * q . k_j) v_j),
- * zeros for a row that sees no key. Softmax statistics and sums are fp32.
+ * zeros for a row that sees no key. Scores, softmax statistics and sums are
+ * fp32; the weights are rounded to f16 (11 bits), or bf16 for 32 keys at a time
+ * whose values' scales lie far apart, and for chunks so are the cached keys and
+ * values, code * scale + offset. Where q . k * scale and the result are ordinary
+ * fp32 numbers, elements of q up to 2^118 / max(1, scale) and cached elements up
+ * to 2^80 in size are served; larger ones may give infinities or NaN.
  *   q, out: device bf16 [T][n_heads][D], ld_q, ld_out as for spear_kv_append;
  *     out may be q itself;
  *   page_table: device int32 [n_seqs][ld_pt]; entries of pages that no row sees,

@@ -388,8 +388,9 @@ __global__ void __launch_bounds__(32 * (kKeyWarps * RG + 1), per_sm(D, NT, RG))
         x += __shfl_xor_sync(0xffffffffu, x, o);
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
       }
-      // a power of two that brings the row's largest element to 128 .. 256
-      const uint32_t es = min(261u - (__float_as_uint(top) >> 23), 254u);
+      // a power of two that brings the row's largest element to 2^14 .. 2^15 (less leaves more to qi, which is to stay finite:
+      // it does for rows below 2^118 / scale)
+      const uint32_t es = min(268u - (__float_as_uint(top) >> 23), 253u);
       const float up2 = __uint_as_float(es << 23), down = __uint_as_float((254u - es) << 23);
 #pragma unroll
       for (int i = 0; i < KW; ++i) {

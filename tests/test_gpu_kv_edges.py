@@ -144,3 +144,15 @@ def test_pages_before_the_window_may_be_released(n, L, window, D, page):
     for i, (_, length) in enumerate(seqs):
         b.table[i, :max(0, length - n - window + 1) // page] = -1
     b.check(b.run(window=window), window)
+
+
+# ---------------------------------------------------------------------------------- queries
+@pytest.mark.parametrize("n", [1, 4, 90])
+def test_huge_queries_and_tiny_keys(n):
+    """Rows of 1e30 to 2e35 whose products with the keys are ordinary numbers, and the other way round."""
+    for size in (1e30, 5e34, 1e-30):
+        def edit(i, k, v):
+            k /= size
+        b = Batch([(n, 200)], 8, 2, 128, 16, seed=n, edit=edit)
+        b.q = (b.q.float() * size).bfloat16()
+        b.check(b.run())
