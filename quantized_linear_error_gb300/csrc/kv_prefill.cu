@@ -707,8 +707,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
 #pragma unroll
         for (int j = 0; j < N; ++j) {
           const uint32_t eb = (j < N / 2 ? top[j % (N / 2)] & 0xFFFFu : top[j % (N / 2)] >> 16) >> 7;  // exponent
-          const uint32_t es = eb == 255u ? 127u : min(261u - eb, 254u);  // not finite: as it is
-          const float f = sign * __uint_as_float(es << 23);
+          const uint32_t es = eb == 255u ? 127u : min(261u - eb, 254u);
+          // not finite: all of the row is NaN, as its result is (minus infinity alone would look like a mask's)
+          const float f = eb == 255u ? NAN : sign * __uint_as_float(es << 23);
           const uint32_t mine = __shfl_sync(0xffffffffu, es, lane % RPI * C);
           if (lane / RPI == j0 + j) sl_next = fmaxf(scale * __uint_as_float((254u - mine) << 23), 1e-37f);
           const int rr = 32 * quarter + (j0 + j) * RPI + lane / C, ch = lane % C;

@@ -156,3 +156,15 @@ def test_huge_queries_and_tiny_keys(n):
         b = Batch([(n, 200)], 8, 2, 128, 16, seed=n, edit=edit)
         b.q = (b.q.float() * size).bfloat16()
         b.check(b.run())
+
+
+@pytest.mark.parametrize("n", [1, 4, 90])
+def test_rows_with_infinities_are_nan(n):
+    """Also where every score is minus infinity; a row that sees no key stays zero."""
+    def edit(i, k, v):
+        np.abs(k, out=k)
+    b = Batch([(n, 200), (n, 0)], 4, 2, 64, 16, seed=n, edit=edit)
+    b.q[0, 1], b.q[0, 2, 9], b.q[n, 0] = -float("inf"), -float("inf"), float("inf")
+    got = b.run().float()
+    assert torch.isnan(got[0, 1:3]).all() and torch.isfinite(got[0, [0, 3]]).all() and torch.isfinite(got[1:n]).all()
+    assert not got[n:].any()
