@@ -56,6 +56,7 @@
 // more than its key tiles. Items that several CTAs share leave partial results,
 // which a second small kernel joins in CTA order on all SMs (the last CTA of an
 // item to finish, on its own, took 12 us for it).
+#include <algorithm>
 #include <atomic>
 
 #include "kv_device.cuh"
@@ -1045,6 +1046,10 @@ spear_status_t kv_launch_prefill(const spear_kv_s* h, const KvAttnArgs& a, int m
   p.inv_group = h->view.group > 1 ? (unsigned)((1ull << 32) / h->view.group) + 1u : 0u;
   p.part = static_cast<float*>(ws);
   p.joins = reinterpret_cast<Join*>(static_cast<char*>(ws) + part_bytes(h));
-  p.wait_ns = 100000000ull;
+  // Most waits are for a tile, some for segments: the schedule's for the softmax to take the next one, and an idle half's
+  // first for scores, while the other half works on as many as are in flight. A segment can be all the key tiles of an
+  // item, 1.4 us each: twice that, so often, beside 100 ms. (100 ms alone ended a correct call beyond 9 million keys.)
+  const int64_t keys = std::min((int64_t)a.ld_pt * h->view.page_size, (int64_t)kKvMaxTokens);
+  p.wait_ns = 100000000ull + (uint64_t)(keys / kTile + 1) * (2 * 1400 * (kSegs + 1));
   return h->view.D == 128 ? launch<128>(h, p, stream) : launch<64>(h, p, stream);
 }

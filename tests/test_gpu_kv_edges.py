@@ -146,6 +146,30 @@ def test_pages_before_the_window_may_be_released(n, L, window, D, page):
     b.check(b.run(window=window), window)
 
 
+# ---------------------------------------------------------------------------------- long segments
+def test_items_that_take_longer_than_a_wait():
+    """Six row tiles a CTA, each over 12 million keys (the same page again and again): a tile takes over 100 ms."""
+    D, page, L, n = 64, 4096, 12 << 20, 256
+    Hk = 6 * torch.cuda.get_device_properties(0).multi_processor_count
+    gen = torch.Generator("cuda").manual_seed(1)
+    pool = spear.kv_pool(1, Hk, D, page)
+    c = spear.SpearKVCache(Hk, Hk, D, page, pool)
+    for at in range(0, page, 256):
+        k, v = (torch.randn(256, Hk, D, device="cuda", generator=gen).bfloat16() for _ in range(2))
+        c.append(None, k, v, None, torch.arange(at, at + 256, device="cuda"))
+    q = torch.randn(n, Hk, D, device="cuda", generator=gen).bfloat16()
+    out = torch.empty_like(q)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    c.attention(q, out, torch.zeros(1, L // page, **i32), torch.tensor([L], **i32), torch.tensor([0, n], **i32), n)
+    assert c.check() == spear.SPEAR_OK
+    host = pool.cpu().numpy()
+    for h in (0, 7, Hk - 1):
+        K, V = kv.unpack_rows(host[:, h:h + 1], page, D, np.arange(page))
+        # the last rows see all but a few of the keys, each page's keys L / page times
+        ref, mag, big = kv.attention(_f64(q[-1:, h:h + 1]), K, V, D ** -0.5)
+        assert np.all(np.abs(_f64(out[-1:, h:h + 1]) - ref) <= kv.tolerance(ref, mag, big) + 1e-5)
+
+
 # ---------------------------------------------------------------------------------- queries
 @pytest.mark.parametrize("n", [1, 4, 90])
 def test_huge_queries_and_tiny_keys(n):
