@@ -433,7 +433,8 @@ spear_status_t spear_kv_read(spear_kv_t h, const int64_t* slots, int32_t T, void
  * fp32 numbers, elements of q up to 2^118 / max(1, scale) and cached elements up
  * to 2^80 in size are served; larger ones may give infinities or NaN.
  *   q, out: device bf16 [T][n_heads][D], ld_q, ld_out as for spear_kv_append;
- *     out may be q itself;
+ *     out is q itself or shares no element with it: memory of its own, or (with
+ *     the same ld) other columns of the same rows;
  *   page_table: device int32 [n_seqs][ld_pt]; entries of pages that no row sees,
  *     past a sequence's end or wholly before its window, may be anything;
  *   kv_lens: device int32 [n_seqs], at most 2^30;

@@ -254,6 +254,22 @@ int rows_per_group(const spear_kv_s* h, int T, int rows, int64_t groups_per_bloc
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool row_ok(const void* p, int64_t ld, int64_t len) { return p && aligned16(p) && ld % 8 == 0 && ld >= len; }
 
+// T rows of `len` elements, `ld` from one to the next.
+struct Rows {
+  const void* p;
+  int64_t ld, len;
+};
+
+// Whether no element of one is the other's: ranges that do not meet, or columns of the same rows that do not.
+bool apart(const Rows& a, const Rows& b, int64_t T) {
+  const auto pa = reinterpret_cast<uintptr_t>(a.p), pb = reinterpret_cast<uintptr_t>(b.p);
+  const Rows &lo = pa <= pb ? a : b, &up = pa <= pb ? b : a;
+  const int64_t off = (int64_t)((pa <= pb ? pb - pa : pa - pb) / 2);  // elements; both are aligned
+  if (off >= (T - 1) * lo.ld + lo.len) return true;
+  return T > 1 && a.ld == b.ld && off % a.ld >= lo.len && off % a.ld + up.len <= a.ld;
+}
+bool same(const Rows& a, const Rows& b, int64_t T) { return a.p == b.p && (a.ld == b.ld || T == 1); }
+
 }  // namespace
 }  // namespace spear
 
@@ -367,10 +383,8 @@ spear_status_t spear_kv_attention(spear_kv_t h, const void* q, int64_t ld_q, voi
       max_q < 1 || window < 0 || !isfinite(scale) ||
       (int64_t)T * h->view.group >= (1 << 27))
     return SPEAR_ERR_INVALID_ARG;
-  // out is q itself or lies apart from it
-  const char *qb = static_cast<const char*>(q), *ob = static_cast<const char*>(out);
-  const int64_t qs = ((T - 1) * ld_q + qn) * 2, os = ((T - 1) * ld_out + qn) * 2;
-  if ((qb != ob || ld_q != ld_out) && qb < ob + os && ob < qb + qs) return SPEAR_ERR_INVALID_ARG;
+  const Rows qr{q, ld_q, qn}, outr{out, ld_out, qn};
+  if (!same(qr, outr, T) && !apart(qr, outr, T)) return SPEAR_ERR_INVALID_ARG;
   KvAttnArgs a;
   a.q = static_cast<const __nv_bfloat16*>(q);
   a.ld_q = ld_q;

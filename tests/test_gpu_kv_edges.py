@@ -192,3 +192,20 @@ def test_rows_with_infinities_are_nan(n):
     got = b.run().float()
     assert torch.isnan(got[0, 1:3]).all() and torch.isfinite(got[0, [0, 3]]).all() and torch.isfinite(got[1:n]).all()
     assert not got[n:].any()
+
+
+# ---------------------------------------------------------------------------------- arguments
+def test_query_and_result_in_one_row_buffer():
+    """Neighbouring columns of the same rows do not overlap; columns that do are refused."""
+    for n in (1, 40):
+        b = Batch([(n, 100), (n, 90)], 4, 2, 64, 16)
+        want = b.run()
+        rows = torch.zeros(2 * n, 13, 64, dtype=torch.bfloat16, device="cuda")
+        for at, to in ((0, 4), (8, 1), (1, 9)):
+            q, out = rows[:, at:at + 4], rows[:, to:to + 4]
+            q.copy_(b.q)
+            args = (_dev(b.table), _dev(np.array([100, 90], np.int32)), _dev(b.starts), n)
+            assert torch.equal(b.c.attention(q, out, *args), want)
+            for clash in (rows[:, at + 1:at + 5], rows[:, at + 3:at + 7] if at + 7 <= 13 else rows[:, at - 1:at + 3]):
+                with pytest.raises(spear.SpearError):
+                    b.c.attention(q, clash, *args)
