@@ -406,7 +406,9 @@ spear_status_t spear_kv_create(const spear_kv_desc_t* desc, cudaStream_t stream,
  *     are contiguous. Multiples of 8, at least the row's length;
  *   positions: device int64 [T] (ignored when rope_dim == 0);
  *   slots: device int64 [T]; -1 leaves the token's key and value uncached;
- *   q_out: device bf16 [T][n_heads][D], rotated queries; may be q itself.
+ *   q_out: device bf16 [T][n_heads][D], rotated queries: q itself, or it shares
+ *     no element with q, k and v (memory of its own, or, with the same ld, other
+ *     columns of the same rows).
  * Two tokens of one call must not have the same slot. T == 0 is a no-op.
  * Errors: INVALID_ARG, CUDA. */
 spear_status_t spear_kv_append(spear_kv_t h, const void* q, int64_t ld_q, const void* k, int64_t ld_k, const void* v,
@@ -414,7 +416,8 @@ spear_status_t spear_kv_append(spear_kv_t h, const void* q, int64_t ld_q, const 
                                int64_t ld_q_out, cudaStream_t stream);
 
 /* The values that T slots hold, bf16_RNE(code * scale + offset), into k_out
- * and v_out: device bf16 [T][n_kv_heads][D], contiguous. Slot -1 gives zeros.
+ * and v_out: device bf16 [T][n_kv_heads][D], contiguous, apart from each other.
+ * Slot -1 gives zeros.
  * Errors: INVALID_ARG, CUDA. */
 spear_status_t spear_kv_read(spear_kv_t h, const int64_t* slots, int32_t T, void* k_out, void* v_out,
                              cudaStream_t stream);

@@ -331,7 +331,12 @@ spear_status_t spear_kv_append(spear_kv_t h, const void* q, int64_t ld_q, const 
   const int64_t D = h->view.D, qn = h->view.n_heads * D, kn = h->view.n_kv_heads * D;
   if (!row_ok(k, ld_k, kn) || !row_ok(v, ld_v, kn) || !slots || (h->rope_dim > 0 && !positions))
     return SPEAR_ERR_INVALID_ARG;
-  if (q && (!row_ok(q, ld_q, qn) || !row_ok(q_out, ld_q_out, qn))) return SPEAR_ERR_INVALID_ARG;
+  if (q) {
+    if (!row_ok(q, ld_q, qn) || !row_ok(q_out, ld_q_out, qn)) return SPEAR_ERR_INVALID_ARG;
+    const Rows qr{q, ld_q, qn}, outr{q_out, ld_q_out, qn};
+    if ((!same(qr, outr, T) && !apart(qr, outr, T)) || !apart({k, ld_k, kn}, outr, T) || !apart({v, ld_v, kn}, outr, T))
+      return SPEAR_ERR_INVALID_ARG;
+  }
   AppendParams p;
   p.v = h->view;
   p.q = static_cast<const __nv_bfloat16*>(q);
@@ -363,7 +368,8 @@ spear_status_t spear_kv_read(spear_kv_t h, const int64_t* slots, int32_t T, void
   if (!h || T < 0) return SPEAR_ERR_INVALID_ARG;
   if (T == 0) return SPEAR_OK;
   if (!slots || !k_out || !v_out || !aligned16(k_out) || !aligned16(v_out)) return SPEAR_ERR_INVALID_ARG;
-  const int D = h->view.D;
+  const int D = h->view.D, kn = h->view.n_kv_heads * D;
+  if (!apart({k_out, kn, kn}, {v_out, kn, kn}, T)) return SPEAR_ERR_INVALID_ARG;
   const int64_t per_block = kAppendThreads / (D / 8);
   const int rows = 2 * h->view.n_kv_heads, chunk = rows_per_group(h, T, rows, per_block);
   const dim3 blocks((unsigned)((T + per_block - 1) / per_block), (rows + chunk - 1) / chunk);

@@ -1,4 +1,4 @@
-"""Attention over the 4-bit cache at the edges of its numbers and of its caller's tables."""
+"""The 4-bit cache and its attention at the edges of their numbers and of their caller's tables and buffers."""
 import numpy as np
 import pytest
 import torch
@@ -209,3 +209,28 @@ def test_query_and_result_in_one_row_buffer():
             for clash in (rows[:, at + 1:at + 5], rows[:, at + 3:at + 7] if at + 7 <= 13 else rows[:, at - 1:at + 3]):
                 with pytest.raises(spear.SpearError):
                     b.c.attention(q, clash, *args)
+
+
+def test_rotated_queries_that_overlap_what_is_read_are_refused():
+    """A result that shares elements with q (but is not q), k or v would be a race; neighbouring columns are none."""
+    c = spear.SpearKVCache(4, 2, 64, 16, spear.kv_pool(1, 2, 64, 16), spear.rope_table(8, 64))
+    for T in (1, 3):
+        rows = torch.randn(T, 16, 64, device="cuda", generator=torch.Generator("cuda").manual_seed(T)).bfloat16()
+        pos, slots = torch.arange(T, device="cuda"), torch.full((T,), -1, device="cuda")
+        q, k, v = rows[:, :4].clone(), rows[:, 4:6].clone(), rows[:, 6:8].clone()
+        want = c.append(q, k, v, pos, slots, torch.empty_like(q))
+        q, k, v = rows[:, :4], rows[:, 4:6], rows[:, 6:8]
+        assert torch.equal(c.append(q, k, v, pos, slots, rows[:, 8:12]), want)
+        for at in (1, 2, 3, 4, 5, 7):
+            with pytest.raises(spear.SpearError):
+                c.append(q, k, v, pos, slots, rows[:, at:at + 4])
+        flat = rows.view(-1)
+        with pytest.raises(spear.SpearError):  # another stride from the same place
+            c.append(q, k, v, pos, slots, flat[64:64 + T * 4 * 64].view(T, 4, 64))
+        assert torch.equal(c.append(q, k, v, pos, slots), want)
+        with pytest.raises(spear.SpearError):
+            c.read(slots, flat[:T * 128].view(T, 2, 64), flat[64:64 + T * 128].view(T, 2, 64))
+        with pytest.raises(spear.SpearError):
+            c.read(slots, flat[:T * 128].view(T, 2, 64), flat[:T * 128].view(T, 2, 64))
+        c.read(slots, flat[:T * 128].view(T, 2, 64), flat[T * 128:T * 256].view(T, 2, 64))
+    assert c.check() == spear.SPEAR_OK
