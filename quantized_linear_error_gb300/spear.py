@@ -408,7 +408,7 @@ class SpearKVCache:
             self._bad_rows(**rows, **({} if q is None else {"q": (q, T, H), "q_out": (q_out, T, H)}))
         pos = 0 if self.rope_table is None else positions.data_ptr()
         if T < 2:  # the stride of a single token means nothing
-            ldq, ldo, ldk, ldv = max(ldq, H * D), max(ldo, H * D), max(ldk, G * D), max(ldv, G * D)
+            ldq, ldo, ldk, ldv = H * D, H * D, G * D, G * D
         st = self._append(self.h, qp, ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, pos, slots.data_ptr(), T, op, ldo,
                           _stream(stream))
         if st:
@@ -447,7 +447,7 @@ class SpearKVCache:
                 q_starts.dtype is i32 and q_starts.is_cuda and q_starts.is_contiguous() and q_starts.numel() > n):
             self._bad_rows(q=(q, T, H), out=(out, T, H))
         if T < 2:  # the stride of a single token means nothing
-            ldq, ldo = max(ldq, H * D), max(ldo, H * D)
+            ldq = ldo = H * D
         st = self._attention(self.h, q.data_ptr(), ldq, out.data_ptr(), ldo, page_table.data_ptr(), cols,
                              kv_lens.data_ptr(), q_starts.data_ptr(), n, T, max_q,
                              self._scale if scale is None else scale, window, _stream(stream))

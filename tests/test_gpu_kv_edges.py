@@ -234,3 +234,20 @@ def test_rotated_queries_that_overlap_what_is_read_are_refused():
             c.read(slots, flat[:T * 128].view(T, 2, 64), flat[:T * 128].view(T, 2, 64))
         c.read(slots, flat[:T * 128].view(T, 2, 64), flat[T * 128:T * 256].view(T, 2, 64))
     assert c.check() == spear.SPEAR_OK
+
+
+def test_strides_of_a_single_token():
+    """The stride of one token is of no account, in whatever tensor it stands."""
+    b = Batch([(1, 100)], 4, 2, 64, 16)
+    want = b.run()
+    q = b.q.cuda()
+    for stride in (0, 1, 64, 300, 4 * 64 + 3):
+        odd = lambda x: torch.as_strided(x, x.shape, (stride, 64, 1), x.storage_offset())
+        out = torch.empty_like(q)
+        args = (_dev(b.table), _dev(np.array([100], np.int32)), _dev(b.starts), 1)
+        b.c.attention(odd(q), odd(out), *args)
+        assert torch.equal(out, want)
+        k = torch.randn(1, 2, 64, device="cuda").bfloat16()
+        b.c.append(odd(q), odd(k), odd(k), None, torch.tensor([-1], device="cuda"), odd(out))
+        assert torch.equal(out, q)
+    assert b.c.check() == spear.SPEAR_OK
