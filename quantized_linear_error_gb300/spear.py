@@ -448,6 +448,8 @@ class SpearKVCache:
             self._bad_rows(q=(q, T, H), out=(out, T, H))
         if T < 2:  # the stride of a single token means nothing
             ldq = ldo = H * D
+        if max_q >> 31 or window >> 31:  # ctypes would cut them to 32 bits; below zero stays refused
+            max_q, window = (min(max(x, -1), (1 << 31) - 1) for x in (max_q, window))
         st = self._attention(self.h, q.data_ptr(), ldq, out.data_ptr(), ldo, page_table.data_ptr(), cols,
                              kv_lens.data_ptr(), q_starts.data_ptr(), n, T, max_q,
                              self._scale if scale is None else scale, window, _stream(stream))

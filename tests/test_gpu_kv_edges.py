@@ -251,3 +251,16 @@ def test_strides_of_a_single_token():
         b.c.append(odd(q), odd(k), odd(k), None, torch.tensor([-1], device="cuda"), odd(out))
         assert torch.equal(out, q)
     assert b.c.check() == spear.SPEAR_OK
+
+
+def test_numbers_past_32_bits():
+    """A window or a row count that no 32-bit number holds means what it says."""
+    b = Batch([(1, 100), (2, 90)], 4, 2, 64, 16)
+    want = b.run()
+    for big in (1 << 31, (1 << 32) + 5, 1 << 40):
+        assert torch.equal(b.run(window=big), want)
+        assert torch.equal(b.run(max_q=big), want)
+    for low in (-1, -(1 << 31), -(1 << 32) + 7):
+        for kw in (dict(window=low), dict(max_q=low)):
+            with pytest.raises(spear.SpearError):
+                b.run(**kw)
