@@ -392,9 +392,10 @@ typedef struct {
 
 /* Build a handle over the caller's pool. Allocates the attention's workspace
  * (partial results of work split over a long cache; its size depends on the
- * device and the head counts only, not on lengths) and clears it on `stream`;
- * the pool is not touched. Errors: INVALID_ARG (null or misaligned pointers,
- * values outside the ranges above), OOM, CUDA; *out is NULL then. */
+ * device and the head counts only, not on lengths), clears it on `stream` and
+ * synchronises `stream`, so that calls may follow on any; the pool is not
+ * touched. Errors: INVALID_ARG (null or misaligned pointers, values outside the
+ * ranges above), OOM, CUDA; *out is NULL then. */
 spear_status_t spear_kv_create(const spear_kv_desc_t* desc, cudaStream_t stream, spear_kv_t* out);
 
 /* Rotate the queries and keys of T tokens and put their keys and values into
@@ -431,8 +432,9 @@ spear_status_t spear_kv_read(spear_kv_t h, const int64_t* slots, int32_t T, void
  *   out = bf16_RNE(sum_j softmax_j(scale * q . k_j) v_j),
  * zeros for a row that sees no key. Scores, softmax statistics and sums are
  * fp32; the weights are rounded to f16 (11 bits), or bf16 for 32 keys at a time
- * whose values' scales lie far apart, and for chunks so are the cached keys and
- * values, code * scale + offset. Where q . k * scale and the result are ordinary
+ * whose values' scales lie far apart. For chunks so are the cached keys and
+ * values, code * scale + offset; for few rows differences of neighbours in q are
+ * rounded to f16. Where q . k * scale and the result are ordinary
  * fp32 numbers, elements of q up to 2^118 / max(1, scale) and cached elements up
  * to 2^80 in size are served; larger ones may give infinities or NaN.
  *   q, out: device bf16 [T][n_heads][D], ld_q, ld_out as for spear_kv_append;

@@ -312,6 +312,7 @@ spear_status_t spear_kv_create(const spear_kv_desc_t* d, cudaStream_t stream, sp
     e = cudaMalloc(&h->ws, h->ws_bytes);
   }
   if (e == cudaSuccess) e = cudaMemsetAsync(h->ws, 0, kKvControlBytes, stream);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(stream);  // the first call may be on another stream
   if (e != cudaSuccess) {
     cudaGetLastError();
     if (h->ws) cudaFree(h->ws);

@@ -264,3 +264,15 @@ def test_numbers_past_32_bits():
         for kw in (dict(window=low), dict(max_q=low)):
             with pytest.raises(spear.SpearError):
                 b.run(**kw)
+
+
+def test_a_new_handle_is_ready_for_any_stream():
+    """Its workspace has been cleared when the constructor returns, whatever the stream had to do before."""
+    pool, side = spear.kv_pool(1, 2, 64, 16), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        a = torch.randn(8192, 8192, device="cuda")
+        for _ in range(20):
+            a @ a
+        c = spear.SpearKVCache(4, 2, 64, 16, pool)
+    assert side.query() and c.check() == spear.SPEAR_OK
