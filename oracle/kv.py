@@ -112,11 +112,13 @@ def attention(q: np.ndarray, K: np.ndarray, V: np.ndarray, scale: float, window:
 
 
 def tolerance(out: np.ndarray, mag: np.ndarray, ref: np.ndarray, keys: float = 2.0 ** -9) -> np.ndarray:
-    """Largest error of an implementation that rounds the result, the weights and the cached values to bf16 once
-    (2^-9 relative each) and keeps everything else in fp32. Keys off by `keys` move a score by d = keys ref at most
-    and a weight by a factor within exp(+-2 d) (numerator and denominator); the roundings of weights and values add
-    2^-9 each, of a value or of its distance from the middle of its row's range, which is at most 16/15 of the row's
-    largest element (mag); the weights' sum takes one such rounding too. fp32 sums stay well within what is left. The
-    bound scales with the values and is zero for a row that sees none but zeros: such a row has no error."""
+    """Largest error of an implementation that rounds the result to bf16 once, weights and cached values to f16 once, and
+    keeps everything else in fp32. Keys off by `keys` move a score by d = keys ref at most and a weight by a factor
+    within exp(+-2 d) (numerator and denominator). The result's rounding is 2^-8 of it at most, which is no larger than
+    mag; those of weights and values are 2^-11 each, of a value or of its distance from the middle of its row's range,
+    which is at most 16/15 of the row's largest element (mag). That leaves 2^-8 of mag for fp32 sums and for keys whose
+    weights and values go through bf16, 2^-8 each: where such a key alone makes the result and all three roundings are
+    at their worst together, they pass the bound by a quarter. The bound scales with the values and is zero for a row
+    that sees none but zeros: such a row has no error."""
     d = keys * ref[..., None]
     return 2.0 ** -9 * np.abs(out) + (np.expm1(2 * d) + 3.5 * 2.0 ** -9) * mag[..., None] * 16 / 15

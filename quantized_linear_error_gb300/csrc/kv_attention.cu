@@ -11,10 +11,14 @@ spear_status_t kv_launch_attention(spear_kv_s* h, const KvAttnArgs& a, cudaStrea
   char* ws = static_cast<char*>(h->ws);
   auto* counters = reinterpret_cast<unsigned*>(ws + 128);
   auto* part = reinterpret_cast<float*>(ws + kKvControlBytes);
-  // Up to kKvDecodeRows rows a key/value head the few-row kernel is the faster or as fast, 32 sequences x 8 key/value
-  // heads x 4000 keys with 16 / 24 / 32 rows: 59 / 101 / 103 us against 99 of the chunk kernel, whose time is the same
-  // from 9 to 128 rows (D = 64: 39 / 74 / 74 against 78); 64 sequences of 500 keys with 20 rows: 46 against 49 (D = 64:
-  // 29 against 36); 4 of 4000 keys with 32 rows: 24 against 25 (D = 64: 18 against 21).
+  // Up to kKvDecodeRows rows a key/value head the few-row kernel is the faster, or within 2%: 32 sequences x 8 key/value
+  // heads x 4000 keys with 16 / 24 / 32 rows take 60 / 100 / 102 us against 99 / 100 / 100 of the chunk kernel, whose time
+  // is the same from 9 to 128 rows (D = 64: 40 / 76 / 76 against 78 / 78 / 79); 64 sequences of 500 keys with 20 rows 48
+  // against 50 (D = 64: 30 against 37); 4 of 4000 keys with 32 rows 24 against 26 (D = 64: 18 against 21).
+  // Beside a chunk the few-row kernel takes the variant of single tokens: a larger one costs them more than drafts gain.
+  // 32 sequences of 2000 to 4000 keys and a chunk of 512, 4 heads a key/value head, with the variant of 8 / 16 / 32 rows:
+  // single tokens 70 / 87 / 116 us, 2 drafts 72 / 89 / 119, 8 drafts 104 / 104 / 126 (8 sequences: 49 / 54 / 61, 49 / 54
+  // / 63, 50 / 49 / 67). 4 drafts, which are 16 rows, lose with 32 sequences, 104 / 92 / 119, not with 8, 50 / 57 / 62.
   // Both kernels read the lengths on the device and leave the other's sequences
   // out; they follow each other on the stream, so they share the workspace.
   const int64_t most = (int64_t)a.max_q * h->view.group;

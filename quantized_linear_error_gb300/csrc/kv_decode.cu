@@ -7,8 +7,8 @@
 // so the cache is read once, (D + 8) bytes a key for 4 D R flops: bound by
 // memory as long as the instructions that unpack the codes keep up. Measured,
 // D = 128: 8 heads a key/value head, 128 sequences of 500 to 8192 keys (607 MB)
-// in 114 us, 5.3 TB/s, 79% of a plain copy; one head each, 64 sequences of 100
-// to 4096 keys and 32 heads (601 MB) in 117 us, 76%; one sequence of 262143
+// in 115 us, 5.3 TB/s, 78% of a plain copy; one head each, 64 sequences of 100
+// to 4096 keys and 32 heads (601 MB) in 118 us, 76%; one sequence of 262143
 // keys (285 MB) in 62.5 us, 68%; a call of little work takes 6.5 us, most of it
 // launch, look-up of lengths and pages, first copy and join.
 //

@@ -12,9 +12,9 @@
 // dequantised tiles' stores 512; a block takes some 2800 here, the chain
 // scores, weights, product of one half being longer than the other half's
 // products that hide it. Measured, D = 128: a prompt of 8192 tokens, 32 heads
-// over 8 (550 GFLOP), 388 us or 1.42 PFLOP/s in bursts, 72% of a library
-// product's rate, and 405 to 415 us once the power limit lowers the clocks; 320
-// tokens behind 7901 (42 GFLOP) 45 us, of which 5 are the start and 8 partial
+// over 8 (550 GFLOP), 387 us or 1.42 PFLOP/s in bursts, 72% of a library
+// product's rate, and 403 to 411 us once the power limit lowers the clocks; 320
+// tokens behind 7901 (42 GFLOP) 44.5 us, of which 5 are the start and 8 partial
 // results and their join.
 //
 // A row tile with at most 128 rows leaves the other half idle, and a key tile
