@@ -435,9 +435,10 @@ spear_status_t spear_kv_read(spear_kv_t h, const int64_t* slots, int32_t T, void
  * (11 bits, 8 at 2^-22 of the largest; below 2^-31 they count in the sum alone),
  * or bf16 for 32 keys at a time whose values' scales lie far apart. For chunks
  * so are the cached keys and values, code * scale + offset; for few rows
- * differences of neighbours in q are rounded to f16. Where q . k * scale and the result are ordinary
- * fp32 numbers, elements of q up to 2^118 / max(1, scale) and cached elements up
- * to 2^80 in size are served; larger ones may give infinities or NaN.
+ * differences of neighbours in q are rounded to f16. Where q . k * scale and the
+ * result are ordinary fp32 numbers, elements of q up to 2^118 / max(1, scale) and
+ * cached elements up to 2^80 in size are served; larger ones may give infinities
+ * or NaN.
  *   q, out: device bf16 [T][n_heads][D], ld_q, ld_out as for spear_kv_append;
  *     out is q itself or shares no element with it: memory of its own, or (with
  *     the same ld) other columns of the same rows;
@@ -451,8 +452,8 @@ spear_status_t spear_kv_read(spear_kv_t h, const int64_t* slots, int32_t T, void
  * rows, fit a few warp-MMA tiles run in a kernel that streams the cache once
  * (single tokens, drafts to verify), longer ones in a tensor-core kernel. A call
  * with longer ones runs both, and drafts then count as long unless they fit the
- * tiles of single tokens (8, 16 or 32 rows). The call only enqueues, so it can be captured in a
- * graph; lengths are read on the device when it runs.
+ * tiles of single tokens (8, 16 or 32 rows). The call only enqueues, so it can be
+ * captured in a graph; lengths are read on the device when it runs.
  * Errors: INVALID_ARG, CUDA. */
 spear_status_t spear_kv_attention(spear_kv_t h, const void* q, int64_t ld_q, void* out, int64_t ld_out,
                                   const int32_t* page_table, int32_t ld_pt, const int32_t* kv_lens,

@@ -410,6 +410,8 @@ __global__ void __launch_bounds__(32 * (kKeyWarps * RG + 1), per_sm(D, NT, RG))
         qf[nt][2 * i + 1][0] = pair(2);
         qf[nt][2 * i + 1][1] = pair(3);
       }
+      // a row with an infinity is NaN, as its result is (minus infinity alone would look like a mask's)
+      if (top == INFINITY) x = NAN;
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         qs[nt][k] = __shfl_sync(0xffffffffu, x, (2 * t + k) * 4) * p.a.scale_log2;

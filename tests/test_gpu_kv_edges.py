@@ -194,6 +194,22 @@ def test_rows_with_infinities_are_nan(n):
     assert not got[n:].any()
 
 
+def test_a_row_of_one_infinity_is_nan_wherever_it_stands():
+    """In every element and of either sign, also where no key's code is 0 there, so that all scores are the same infinity."""
+    for n in (1, 3, 40):
+        def edit(i, k, v):
+            k[:] = 1.0 + 15 * (np.arange(64) != i)  # codes 0 in one channel alone, 15 in the others
+        seqs = [(n, n + 2)] * 64
+        b = Batch(seqs, 2, 1, 64, 16, seed=n, edit=edit)
+        for sign in (1, -1):
+            for i in range(64):
+                b.q[b.starts[i]:b.starts[i + 1], 1] = 0.5
+                b.q[b.starts[i]:b.starts[i + 1], 1, (i + 1) % 64] = sign * float("inf")
+            got = b.run().float()
+            assert torch.isnan(got[:, 1]).all(), (n, sign, (~torch.isnan(got[:, 1])).any(-1).nonzero().flatten().tolist())
+            assert torch.isfinite(got[:, 0]).all()
+
+
 # ---------------------------------------------------------------------------------- arguments
 def test_query_and_result_in_one_row_buffer():
     """Neighbouring columns of the same rows do not overlap; columns that do are refused."""
