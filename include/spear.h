@@ -437,7 +437,7 @@ spear_status_t spear_kv_read(spear_kv_t h, const int64_t* slots, int32_t T, void
  * so are the cached keys and values, code * scale + offset; for few rows
  * differences of neighbours in q are rounded to f16. Where q . k * scale and the
  * result are ordinary fp32 numbers, elements of q up to 2^118 / max(1, scale) and
- * cached elements up to 2^80 in size are served; larger ones may give infinities
+ * cached elements up to 2^60 in size are served; larger ones may give infinities
  * or NaN.
  *   q, out: device bf16 [T][n_heads][D], ld_q, ld_out as for spear_kv_append;
  *     out is q itself or shares no element with it: memory of its own, or (with

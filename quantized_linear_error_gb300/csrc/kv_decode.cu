@@ -81,9 +81,9 @@ constexpr int kMinUnits = 4;                   // a CTA's, where there are few o
                                                // without the rule, 11.8 with it)
 constexpr int kScan = 10;                      // warps at most
 constexpr float kLazy = 8.f;
-// Value scales, by their exponent fields. Largest ones of 2^-54 .. 2^46 choose k (beyond, 2^k and the sums could leave fp32);
+// Value scales, by their exponent fields. Largest ones of 2^-34 .. 2^46 choose k (beyond, 2^k and the sums could leave fp32);
 // f16 takes this many binades from the largest down.
-constexpr uint32_t kScaleMin = 73, kScaleMax = 173, kScaleBinades = 10;
+constexpr uint32_t kScaleMin = 93, kScaleMax = 173, kScaleBinades = 10;
 constexpr uint32_t kNoScale = 255u << 23;
 // A variant: NT 8-row MMA tiles a warp, RG groups of warps with rows of their own over the same keys (four tiles in one
 // warp's registers spill and leave four warps an SM). CTAs an SM: the accumulators and the rows of q take 3 D NT / 8

@@ -133,6 +133,19 @@ def test_value_scales_of_every_size_in_one_cache():
             kv_cases.check(b, _f64(got))
 
 
+@pytest.mark.parametrize("n", [1, 4, 60])
+def test_large_constant_values_among_tiny_ones(n):
+    """Every second row is one value of 2^60 (scale 0) in a cache whose other values are of size 2^-56: sums stay finite."""
+    def edit(i, k, v, rng):
+        k[:] = kv_cases.key_rows(rng, k.shape, 2.0 ** -5)
+        v *= 2.0 ** -56
+        v[1::2] = 2.0 ** 60
+    b = kv_cases.case([(n, 9000)], 4, 2, 64, 16, edit, kv_cases.query_rows(n, n, 4, 64))
+    got = b.run(scale=b.scale)
+    assert b.c.check() == spear.SPEAR_OK
+    kv_cases.check(b, _f64(got))
+
+
 # ---------------------------------------------------------------------------------- released pages
 @pytest.mark.parametrize("n,L,window,D,page", [(1, 500, 100, 128, 16), (4, 777, 64, 64, 48), (1, 1000, 1, 128, 32),
                                                (100, 700, 128, 128, 16), (300, 1500, 200, 64, 32), (90, 900, 17, 128, 64)])
