@@ -33,9 +33,9 @@
 //    MN-major B operand of O, so nothing is transposed. A code word's pairs come
 //    out as elements (0, 4), (1, 5), (2, 6), (3, 7); Q's rows are permuted
 //    alike, and O's columns are put back in the epilogue. Keys past the
-//    sequence's end or before the window become zeros, and a key whose V is not finite is moved to
-//    its K (V zero, K NaN): rows that see it get NaN, the mask keeps it from the
-//    others (0 x NaN in O += P V would not).
+//    sequence's end or before the window become zeros, and a key whose V is not
+//    finite is moved to its K (V zero, K NaN): rows that see it get NaN, the mask
+//    keeps it from the others (0 x NaN in O += P V would not).
 //  - Two softmax warpgroups, one an MMA tile, one row a thread; P goes from
 //    registers to tensor memory in two parts, so that the product with the
 //    first 64 keys runs while the other weights are computed. m need not be the
