@@ -470,6 +470,112 @@ spear_status_t spear_kv_check(spear_kv_t h, cudaStream_t stream);
  * spear_linear_destroy does); the pool stays the caller's. NULL is accepted. */
 spear_status_t spear_kv_destroy(spear_kv_t h);
 
+/* ------------------------------------------------------------------------
+ * 8-bit integers: rows in 8 bits, the norm that writes them, and linears of
+ * 8-bit weights and activations, beside the 4-bit ones (the paper compares
+ * with such layers; the forms and kernels here are this library's).
+ *
+ * A row v of fp32 values in 8 bits is K codes (int8) and one scale (fp32):
+ *   a = max |v|,  scale = fl32(a / 127),
+ *   code = clamp(rint(v * fl32(127 / a)), -127, 127),
+ * each operation in fp32, round to nearest even; an element stands for
+ * code * scale. A row with a below 2^-100 is held as zeros (scale 0); one with
+ * an element that is not finite has scale NaN and codes 0, so that it reads as
+ * NaN.
+ *
+ * Matrices are rows of K (or N) contiguous elements, ld elements from one row
+ * to the next (ld >= K; of no account for a single row), aligned to their
+ * elements. Rows whose base and ld are multiples of 16 bytes (8 for codes) are
+ * moved in wide accesses. M == 0 is a no-op. Calls only enqueue on `stream`.
+ * ---------------------------------------------------------------------- */
+typedef enum { SPEAR_BF16 = 0, SPEAR_F16 = 1, SPEAR_F32 = 2 } spear_dtype_t;
+
+/* Root-mean-square norm of M rows, with the residual's addition before it and
+ * 8-bit rows as its result, in one launch:
+ *   h = x + residual (fp32; x alone if residual is NULL), residual_out = round(h),
+ *   v = h / sqrt(mean(h^2) + eps) * weight,
+ *   y = round(v) (x's type), and / or q, scales = v in 8 bits.
+ * Statistics and sums are fp32, of the unrounded h. The codes are taken from
+ * h * weight, whose row v is up to a positive factor, which goes into the scale
+ * alone; where max |h * weight| is below 2^-110 the row counts as zeros.
+ *   x: device, `type`, [M][ld_x]; weight: device [K], `type` or fp32;
+ *   residual, residual_out: device, `type` or fp32 (residual_type), both or
+ *     neither; the same rows (residual_out == residual) or apart;
+ *   y: or NULL; q: int8 [M][ld_q], with scales fp32 [M], or NULL; one of both.
+ * y and residual_out may be x's own rows if the element types are the same;
+ * else results share no element with each other or with what is read. K up to
+ * 32768. eps >= 0, finite; with eps 0 a row of zeros gives NaN.
+ * Rows with an element that is not finite give NaN (in residual_out only there).
+ * Errors: INVALID_ARG, UNSUPPORTED (K), CUDA. */
+spear_status_t spear_rms_norm(const void* x, int64_t ld_x, spear_dtype_t type, const void* residual,
+                              int64_t ld_residual, void* residual_out, int64_t ld_residual_out,
+                              spear_dtype_t residual_type, const void* weight, spear_dtype_t weight_type, float eps,
+                              int32_t M, int32_t K, void* y, int64_t ld_y, int8_t* q, int64_t ld_q, float* scales,
+                              cudaStream_t stream);
+
+/* M rows in 8 bits, bit for bit as defined above: activations each step (a scale
+ * a token), weights once (a scale an output channel). K up to 32768.
+ *   x: device, `type`; q: int8 [M][ld_q]; scales: fp32 [M]; all apart.
+ * Errors: INVALID_ARG, UNSUPPORTED (K), CUDA. */
+spear_status_t spear_quantize_rows(const void* x, int64_t ld_x, spear_dtype_t type, int32_t M, int32_t K, int8_t* q,
+                                   int64_t ld_q, float* scales, cudaStream_t stream);
+
+/* What rows in 8 bits stand for: out = round(code * scale) as `type`.
+ * Errors: INVALID_ARG, UNSUPPORTED (more than 2^39 elements), CUDA. */
+spear_status_t spear_dequantize_rows(const int8_t* q, int64_t ld_q, const float* scales, int32_t M, int32_t K, void* out,
+                                     int64_t ld_out, spear_dtype_t type, cudaStream_t stream);
+
+typedef struct spear_w8_s* spear_w8_t;
+
+typedef enum {
+  SPEAR_ACT_SILU = 0,          /* act(g) = g / (1 + exp(-g)) */
+  SPEAR_ACT_GELU = 1           /* act(g) = g / (1 + exp(-2 z)), z = sqrt(2 / pi) (g + 0.044715 g^3): the tanh form */
+} spear_act_t;
+
+typedef struct {
+  int32_t K;                   /* input features, a multiple of 16 */
+  int32_t N;                   /* output features, >= 1 */
+  const int8_t* qweight;       /* device, int8 [N][K], 16-byte aligned */
+  const float* scales;         /* device, fp32 [N]: one scale an output channel */
+  const int8_t* qweight_up;    /* second projection of a gated pair, or NULL; as qweight */
+  const float* scales_up;      /* its scales, or NULL */
+  spear_act_t activation;      /* of a gated pair (ignored otherwise) */
+  int32_t max_tokens;          /* largest M a forward on this handle will use (>= 1) */
+} spear_w8_desc_t;
+
+/* Build a handle from 8-bit weights: the weights are copied and laid out once,
+ * in one layout that serves every number of tokens, and `stream` is
+ * synchronised, so that the caller may free its buffers.
+ * Errors: INVALID_ARG (null or misaligned pointers, values outside the ranges
+ * above), UNSUPPORTED (K > 2^20, N > 2^22, max_tokens > 2^20), OOM, CUDA; *out
+ * is NULL then. */
+spear_status_t spear_w8_create(const spear_w8_desc_t* desc, cudaStream_t stream, spear_w8_t* out);
+
+/* Product of 8-bit integers with scales for each token and channel:
+ *   p[m][n] = x_scales[m] * scales[n] * sum_k x[m][k] qweight[n][k],
+ *   y[m][n] = round(p[m][n]), or round(act(p[m][n]) * p_up[m][n]) of a gated handle
+ * (both projections, the activation and the product in one kernel).
+ * The integers are exact, and so are sums below 2^24 in size (in fp32); larger
+ * ones are rounded to fp32, in an order that depends on the shape and M. The
+ * codes may be -128 .. 127.
+ *   x: device int8 [M][ld_x], 16-byte aligned, ld_x a multiple of 16 (M > 1);
+ *   x_scales: device fp32 [M]; y: device, `type`, [M][ld_y], apart from x.
+ * Up to 32 tokens run in a kernel that streams the weights once, more on the
+ * tensor cores. A handle's calls share its workspace: order them on one stream,
+ * or by events; distinct handles are independent. The handle belongs to the
+ * device that was current at create, which has to be current here.
+ * Errors: INVALID_ARG, CUDA. */
+spear_status_t spear_w8_forward(spear_w8_t h, const int8_t* x, int64_t ld_x, const float* x_scales, void* y, int64_t ld_y,
+                                spear_dtype_t type, int32_t M, cudaStream_t stream);
+
+/* Synchronise `stream` and report the handle's device status: OK, or TIMEOUT if
+ * a bounded device-side wait gave up since the last check; the status is then
+ * cleared and the workspace reset. */
+spear_status_t spear_w8_check(spear_w8_t h, cudaStream_t stream);
+
+/* Free the handle's device memory (waits for queued work). NULL is accepted. */
+spear_status_t spear_w8_destroy(spear_w8_t h);
+
 /* Human-readable name of a status code (static storage). */
 const char* spear_status_string(spear_status_t s);
 

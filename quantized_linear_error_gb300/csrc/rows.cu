@@ -1,0 +1,446 @@
+// Rows of a decoder layer between its linears: the root-mean-square norm with
+// the residual's addition and an output in 8 bits, the 8-bit quantisation of
+// rows, and the read-back.
+//
+// A row v in 8 bits is codes and one fp32 scale:
+//   a = max |v|, scale = a / 127, code = clamp(rint(v * (127 / a)), -127, 127).
+// The norm v = h * rstd * w, rstd = 1 / sqrt(mean h^2 + eps), needs the sum of
+// squares before anything can be written; the codes need max |v| as well. Since
+// rstd > 0 is one factor of the whole row, max |v| = rstd max |h w| and
+// v / max |v| = h w / max |h w|: both reductions run over the same registers at
+// once, and a row is read once and written once.
+//
+// Bound by memory: a row stays in registers (8 to 32 elements a thread) between
+// the loads and the stores.
+#include <cuda_fp16.h>
+
+#include <type_traits>
+
+#include "kv_device.cuh"
+#include "w8.h"
+
+namespace spear {
+namespace {
+
+SPEAR_DEVINL float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// Eight elements from p (of which `n` exist) as fp32; `vec`: p is 16-byte aligned and all eight exist.
+// kOnce: rows that nobody reads again, out of the caches' way.
+template <bool kOnce, class T>
+SPEAR_DEVINL void load8(const T* p, int n, bool vec, float (&x)[8]) {
+  if (vec) {
+    constexpr int words = sizeof(T) / 2;
+    uint4 w[words];
+#pragma unroll
+    for (int i = 0; i < words; ++i) {
+      const uint4* src = reinterpret_cast<const uint4*>(p) + i;
+      w[i] = kOnce ? __ldcs(src) : *src;
+    }
+    T e[8];
+    memcpy(e, w, sizeof(e));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = (float)e[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = i < n ? (float)p[i] : 0.f;
+  }
+}
+
+template <class T>
+SPEAR_DEVINL T rounded(float x) {
+  if constexpr (sizeof(T) == 4) return x;
+  else if constexpr (std::is_same<T, __half>::value) return __float2half_rn(x);
+  else return __float2bfloat16_rn(x);
+}
+
+template <class T>
+SPEAR_DEVINL void store8(T* p, int n, bool vec, const float (&x)[8]) {
+  T e[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) e[i] = rounded<T>(x[i]);
+  if (vec) {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
+      uint4 w;
+      memcpy(&w, reinterpret_cast<const char*>(e) + 16 * i, 16);
+      *(reinterpret_cast<uint4*>(p) + i) = w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) p[i] = e[i];
+  }
+}
+
+struct RowsParams {
+  const void* x;
+  int64_t ld_x;
+  const void* res;  // or null
+  int64_t ld_res;
+  void* res_out;
+  int64_t ld_res_out;
+  const void* weight;
+  void* y;  // or null
+  int64_t ld_y;
+  int8_t* q;  // or null
+  int64_t ld_q;
+  float* scales;
+  int M, K;
+  float eps;
+  int res_f32, weight_f32;
+  int vec_x, vec_res, vec_res_out, vec_w, vec_y, vec_q;
+};
+
+// Sum of a and maximum of b over the row's threads, in every one of them.
+template <bool kWarpRows>
+SPEAR_DEVINL void reduce_row(float& a, float& b, float2* part) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    a += __shfl_xor_sync(0xffffffffu, a, o);
+    b = max_nan(b, __shfl_xor_sync(0xffffffffu, b, o));
+  }
+  if (kWarpRows) return;
+  const int lane = threadIdx.x & 31, warps = blockDim.x / 32;
+  if (lane == 0) part[threadIdx.x / 32] = make_float2(a, b);
+  __syncthreads();
+  const float2 v = lane < warps ? part[lane] : make_float2(0.f, 0.f);
+  a = v.x, b = v.y;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    a += __shfl_xor_sync(0xffffffffu, a, o);
+    b = max_nan(b, __shfl_xor_sync(0xffffffffu, b, o));
+  }
+}
+
+// One row a warp (kWarpRows, K <= 256 NV) or a block: NV groups of eight
+// elements a thread, `stride` groups apart.
+template <class T, int NV, bool kNorm, bool kWarpRows>
+__global__ void __launch_bounds__(kWarpRows ? 256 : 1024) rows_kernel(const __grid_constant__ RowsParams p) {
+  __shared__ float2 part[2][32];
+  kv_follow();
+  const int64_t row = kWarpRows ? (int64_t)blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32 : blockIdx.x;
+  if (row >= p.M) return;  // whole warps, or nobody
+  const int at = kWarpRows ? threadIdx.x & 31 : threadIdx.x, stride = kWarpRows ? 32 : blockDim.x;
+
+  float h[NV][8];
+  const T* x = static_cast<const T*>(p.x) + row * p.ld_x;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int k = (at + i * stride) * 8;
+    load8<true>(x + k, p.K - k, p.vec_x && k + 8 <= p.K, h[i]);
+  }
+  if (kNorm && p.res) {
+    float r[NV][8];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int k = (at + i * stride) * 8;
+      const bool vec = p.vec_res && k + 8 <= p.K;
+      if (p.res_f32) load8<true>(static_cast<const float*>(p.res) + row * p.ld_res + k, p.K - k, vec, r[i]);
+      else load8<true>(static_cast<const T*>(p.res) + row * p.ld_res + k, p.K - k, vec, r[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int k = (at + i * stride) * 8;
+      const bool vec = p.vec_res_out && k + 8 <= p.K;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) h[i][j] += r[i][j];
+      if (p.res_f32) store8(static_cast<float*>(p.res_out) + row * p.ld_res_out + k, p.K - k, vec, h[i]);
+      else store8(static_cast<T*>(p.res_out) + row * p.ld_res_out + k, p.K - k, vec, h[i]);
+    }
+  }
+
+  // The weight stays in registers beside one or two groups; more of it is read again from the caches.
+  constexpr bool kHold = kNorm && NV <= 2;
+  float held_w[kHold ? NV : 1][8];
+  auto load_w = [&](int i, float (&w)[8]) {
+    const int k = (at + i * stride) * 8;
+    const bool vec = p.vec_w && k + 8 <= p.K;
+    if (p.weight_f32) load8<false>(static_cast<const float*>(p.weight) + k, p.K - k, vec, w);
+    else load8<false>(static_cast<const T*>(p.weight) + k, p.K - k, vec, w);
+  };
+  if constexpr (kHold) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) load_w(i, held_w[i]);
+  }
+  // h w of group i
+  auto weighted = [&](int i, float (&v)[8]) {
+    if constexpr (!kNorm) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = h[i][j];
+    } else if constexpr (kHold) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = h[i][j] * held_w[i][j];
+    } else {
+      load_w(i, v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] *= h[i][j];
+    }
+  };
+  auto statistics = [&](float& ss, float& top, float2* scratch) {
+    ss = 0.f, top = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      float v[8];
+      weighted(i, v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (kNorm) ss += h[i][j] * h[i][j];
+        top = max_nan(top, fabsf(v[j]));
+      }
+    }
+    reduce_row<kWarpRows>(ss, top, scratch);
+  };
+  float ss, top, rstd = 1.f;
+  statistics(ss, top, part[0]);
+  if (kNorm) {
+    float eps = p.eps;
+    // squares beyond fp32 (the same for the whole row): h times a power of two, which rstd takes back
+    if (ss > 0x1p120f || (ss < 0x1p-60f && eps < 0x1p-60f)) {
+      const float by = ss > 0x1p120f ? 0x1p-96f : 0x1p80f;
+      eps = eps * by * by;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) h[i][j] *= by;
+      statistics(ss, top, part[1]);
+    }
+    rstd = __frsqrt_rn(__fdiv_rn(ss, (float)p.K) + eps);
+    if (!(ss < INFINITY)) rstd = NAN;  // an element that is not finite: the whole row
+  }
+  const float a = kNorm ? top * rstd : top;
+  const bool finite = a < INFINITY, held = finite && a >= 0x1p-100f && top >= 0x1p-110f;
+  const float inv = held ? __fdiv_rn(127.f, top) : 0.f;
+  if (p.q && at == 0) p.scales[row] = held ? __fdiv_rn(a, 127.f) : finite ? 0.f : NAN;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int k = (at + i * stride) * 8;
+    float v[8];
+    weighted(i, v);
+    if (p.q) {
+      int c[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) c[j] = held ? max(-127, min(127, __float2int_rn(v[j] * inv))) : 0;
+      int8_t* dst = p.q + row * p.ld_q + k;
+      if (p.vec_q && k + 8 <= p.K) {
+        uint2 o;
+        o.x = (uint32_t)(c[0] & 255) | (uint32_t)(c[1] & 255) << 8 | (uint32_t)(c[2] & 255) << 16 | (uint32_t)c[3] << 24;
+        o.y = (uint32_t)(c[4] & 255) | (uint32_t)(c[5] & 255) << 8 | (uint32_t)(c[6] & 255) << 16 | (uint32_t)c[7] << 24;
+        *reinterpret_cast<uint2*>(dst) = o;
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (k + j < p.K) dst[j] = (int8_t)c[j];
+      }
+    }
+    if (kNorm && p.y) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] *= rstd;
+      store8(static_cast<T*>(p.y) + row * p.ld_y + k, p.K - k, p.vec_y && k + 8 <= p.K, v);
+    }
+  }
+}
+
+template <class T, bool kNorm>
+spear_status_t launch_rows(const RowsParams& p, int sms, cudaStream_t stream) {
+  const int groups = (p.K + 7) / 8;
+  if (groups <= 128) {  // a warp a row: no barrier
+    const dim3 grid((unsigned)((p.M + 7) / 8));
+    if (groups <= 32) return kv_launch(rows_kernel<T, 1, kNorm, true>, grid, 256, 0, stream, p);
+    if (groups <= 64) return kv_launch(rows_kernel<T, 2, kNorm, true>, grid, 256, 0, stream, p);
+    return kv_launch(rows_kernel<T, 4, kNorm, true>, grid, 256, 0, stream, p);
+  }
+  // a block a row: as many threads as it takes where there are few rows, several groups a thread otherwise
+  const int nv = max((groups + 1023) / 1024, p.M <= sms ? 1 : 2);
+  const int threads = ((groups + nv - 1) / nv + 31) / 32 * 32;
+  const dim3 grid((unsigned)p.M);
+  switch (nv) {
+    case 1: return kv_launch(rows_kernel<T, 1, kNorm, false>, grid, threads, 0, stream, p);
+    case 2: return kv_launch(rows_kernel<T, 2, kNorm, false>, grid, threads, 0, stream, p);
+    case 3: return kv_launch(rows_kernel<T, 3, kNorm, false>, grid, threads, 0, stream, p);
+    default: return kv_launch(rows_kernel<T, 4, kNorm, false>, grid, threads, 0, stream, p);
+  }
+}
+
+template <bool kNorm>
+spear_status_t launch_rows(const RowsParams& p, spear_dtype_t type, cudaStream_t stream) {
+  int sms = 0;
+  const spear_status_t st = sm_count_of_current(&sms);
+  if (st != SPEAR_OK) return st;
+  switch (type) {
+    case SPEAR_BF16: return launch_rows<__nv_bfloat16, kNorm>(p, sms, stream);
+    case SPEAR_F16: return launch_rows<__half, kNorm>(p, sms, stream);
+    default: return launch_rows<float, kNorm>(p, sms, stream);
+  }
+}
+
+// Values of 16 codes a thread, along the rows.
+template <class T>
+__global__ void __launch_bounds__(256) dequantize_kernel(const int8_t* __restrict__ q, int64_t ld_q,
+                                                         const float* __restrict__ scales, int M, int K,
+                                                         T* __restrict__ out, int64_t ld_out, int vec) {
+  kv_follow();
+  const int groups = (K + 15) / 16;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t row = div_u64(i, groups);
+  if (row >= M) return;
+  const int k = (int)(i - row * groups) * 16;
+  const int8_t* src = q + row * ld_q + k;
+  T* dst = out + row * ld_out + k;
+  const float s = scales[row];
+  int8_t c[16];
+  if (vec && k + 16 <= K) {
+    const uint4 w = *reinterpret_cast<const uint4*>(src);
+    memcpy(c, &w, 16);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) c[j] = k + j < K ? src[j] : (int8_t)0;
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = (float)c[8 * h + j] * s;
+    store8(dst + 8 * h, K - k - 8 * h, vec && k + 16 <= K, v);
+  }
+}
+
+bool aligned(const void* p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+bool type_ok(spear_dtype_t t) { return t == SPEAR_BF16 || t == SPEAR_F16 || t == SPEAR_F32; }
+unsigned size_of(spear_dtype_t t) { return t == SPEAR_F32 ? 4 : 2; }
+// 16-byte accesses of whole groups of eight elements
+int vec_ok(const void* p, int64_t ld, int M, unsigned size) {
+  return aligned(p, 16) && (M == 1 || ld * size % 16 == 0);
+}
+bool rows_ok(const void* p, int64_t ld, int K, unsigned size) { return p && ld >= K && aligned(p, size); }
+
+// Whether rows [M][K] of two arrays (elements of sa and sb bytes) share bytes; the same rows count as apart if `same_ok`.
+bool rows_overlap(const void* a, int64_t ld_a, unsigned sa, const void* b, int64_t ld_b, unsigned sb, int M, int K,
+                  bool same_ok) {
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
+  const uintptr_t la = (uintptr_t)ld_a * sa, lb = (uintptr_t)ld_b * sb;
+  if (same_ok && a0 == b0 && sa == sb && (la == lb || M == 1)) return false;
+  const uintptr_t a1 = a0 + (uintptr_t)(M - 1) * la + (uintptr_t)K * sa, b1 = b0 + (uintptr_t)(M - 1) * lb + (uintptr_t)K * sb;
+  if (a1 <= b0 || b1 <= a0) return false;
+  if (la != lb) return true;
+  // the same distance from row to row: other columns of the same rows are apart
+  const uintptr_t d = a0 <= b0 ? (b0 - a0) % la : (a0 - b0) % la;  // of the later one behind a row of the earlier one
+  const uintptr_t first = a0 <= b0 ? (uintptr_t)K * sa : (uintptr_t)K * sb, second = a0 <= b0 ? (uintptr_t)K * sb : (uintptr_t)K * sa;
+  return d < first || d + second > la;
+}
+
+// Whether the bytes from a's first to its last row meet those of b's.
+bool extents_meet(const void* a, int64_t ld_a, unsigned sa, int Ma, int Ka, const void* b, int64_t ld_b, unsigned sb,
+                  int Mb, int Kb) {
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
+  return a0 < b0 + (uintptr_t)(Mb - 1) * ld_b * sb + (uintptr_t)Kb * sb &&
+         b0 < a0 + (uintptr_t)(Ma - 1) * ld_a * sa + (uintptr_t)Ka * sa;
+}
+
+}  // namespace
+
+spear_status_t sm_count_of_current(int* sms) {
+  static std::atomic<int> known[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return SPEAR_ERR_CUDA;
+  if (dev < 64 && (*sms = known[dev].load(std::memory_order_relaxed)) > 0) return SPEAR_OK;
+  if (cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return SPEAR_ERR_CUDA;
+  if (dev < 64) known[dev].store(*sms, std::memory_order_relaxed);
+  return SPEAR_OK;
+}
+
+}  // namespace spear
+
+using namespace spear;
+
+extern "C" spear_status_t spear_rms_norm(const void* x, int64_t ld_x, spear_dtype_t type, const void* residual,
+                                         int64_t ld_residual, void* residual_out, int64_t ld_residual_out,
+                                         spear_dtype_t residual_type, const void* weight, spear_dtype_t weight_type,
+                                         float eps, int32_t M, int32_t K, void* y, int64_t ld_y, int8_t* q, int64_t ld_q,
+                                         float* scales, cudaStream_t stream) {
+  if (!type_ok(type) || M < 0 || K < 1 || !(eps >= 0.f && eps < INFINITY)) return SPEAR_ERR_INVALID_ARG;
+  if (weight_type != type && weight_type != SPEAR_F32) return SPEAR_ERR_INVALID_ARG;
+  const unsigned sx = size_of(type), sw = size_of(weight_type);
+  if (!rows_ok(weight, K, K, sw)) return SPEAR_ERR_INVALID_ARG;
+  if (M > 0) {
+    if (q && scales && extents_meet(x, ld_x, sx, M, K, scales, 1, 4, M, 1)) return SPEAR_ERR_INVALID_ARG;
+    if (!rows_ok(x, ld_x, K, sx) || (!y && !q) || (q && (!scales || !aligned(scales, 4) || ld_q < K)) ||
+        (y && !rows_ok(y, ld_y, K, sx)))
+      return SPEAR_ERR_INVALID_ARG;
+    const struct { const void* p; int64_t ld; unsigned s; } in[] = {{x, ld_x, sx}, {residual, ld_residual, size_of(residual_type)}},
+        out[] = {{residual ? residual_out : nullptr, ld_residual_out, size_of(residual_type)}, {y, ld_y, sx}, {q, ld_q, 1}};
+    if (residual) {
+      if ((residual_type != type && residual_type != SPEAR_F32) || !rows_ok(residual, ld_residual, K, in[1].s) ||
+          !rows_ok(residual_out, ld_residual_out, K, in[1].s))
+        return SPEAR_ERR_INVALID_ARG;
+    }
+    for (int i = 0; i < 3; ++i) {
+      if (!out[i].p) continue;
+      if (extents_meet(out[i].p, out[i].ld, out[i].s, M, K, weight, K, sw, 1, K) ||
+          (q && extents_meet(out[i].p, out[i].ld, out[i].s, M, K, scales, 1, 4, M, 1)))
+        return SPEAR_ERR_INVALID_ARG;
+      for (const auto& a : in)
+        if (a.p && rows_overlap(out[i].p, out[i].ld, out[i].s, a.p, a.ld, a.s, M, K, true)) return SPEAR_ERR_INVALID_ARG;
+      for (int j = 0; j < i; ++j)
+        if (out[j].p && rows_overlap(out[i].p, out[i].ld, out[i].s, out[j].p, out[j].ld, out[j].s, M, K, false))
+          return SPEAR_ERR_INVALID_ARG;
+    }
+  }
+  if (K > kRowsMaxWidth) return SPEAR_ERR_UNSUPPORTED;
+  if (M == 0) return SPEAR_OK;
+  RowsParams p = {};
+  p.x = x, p.ld_x = ld_x, p.weight = weight, p.y = y, p.ld_y = ld_y, p.q = q, p.ld_q = ld_q, p.scales = scales;
+  p.res = residual, p.ld_res = ld_residual, p.res_out = residual_out, p.ld_res_out = ld_residual_out;
+  p.M = M, p.K = K, p.eps = eps;
+  p.res_f32 = residual_type == SPEAR_F32, p.weight_f32 = weight_type == SPEAR_F32;
+  p.vec_x = vec_ok(x, ld_x, M, sx), p.vec_w = aligned(weight, 16), p.vec_y = y && vec_ok(y, ld_y, M, sx);
+  p.vec_res = residual && vec_ok(residual, ld_residual, M, size_of(residual_type));
+  p.vec_res_out = residual && vec_ok(residual_out, ld_residual_out, M, size_of(residual_type));
+  p.vec_q = aligned(q, 8) && (M == 1 || ld_q % 8 == 0);
+  return launch_rows<true>(p, type, stream);
+}
+
+extern "C" spear_status_t spear_quantize_rows(const void* x, int64_t ld_x, spear_dtype_t type, int32_t M, int32_t K,
+                                              int8_t* q, int64_t ld_q, float* scales, cudaStream_t stream) {
+  if (!type_ok(type) || M < 0 || K < 1) return SPEAR_ERR_INVALID_ARG;
+  if (M > 0 && (!rows_ok(x, ld_x, K, size_of(type)) || !q || ld_q < K || !scales || !aligned(scales, 4) ||
+                rows_overlap(q, ld_q, 1, x, ld_x, size_of(type), M, K, false) ||
+                extents_meet(q, ld_q, 1, M, K, scales, 1, 4, M, 1) ||
+                extents_meet(x, ld_x, size_of(type), M, K, scales, 1, 4, M, 1)))
+    return SPEAR_ERR_INVALID_ARG;
+  if (K > kRowsMaxWidth) return SPEAR_ERR_UNSUPPORTED;
+  if (M == 0) return SPEAR_OK;
+  RowsParams p = {};
+  p.x = x, p.ld_x = ld_x, p.q = q, p.ld_q = ld_q, p.scales = scales, p.M = M, p.K = K;
+  p.vec_x = vec_ok(x, ld_x, M, size_of(type)), p.vec_q = aligned(q, 8) && (M == 1 || ld_q % 8 == 0);
+  return launch_rows<false>(p, type, stream);
+}
+
+extern "C" spear_status_t spear_dequantize_rows(const int8_t* q, int64_t ld_q, const float* scales, int32_t M, int32_t K,
+                                                void* out, int64_t ld_out, spear_dtype_t type, cudaStream_t stream) {
+  if (!type_ok(type) || M < 0 || K < 1) return SPEAR_ERR_INVALID_ARG;
+  const unsigned s = size_of(type);
+  if (M > 0 && (!q || ld_q < K || !scales || !aligned(scales, 4) || !rows_ok(out, ld_out, K, s) ||
+                rows_overlap(out, ld_out, s, q, ld_q, 1, M, K, false) ||
+                extents_meet(out, ld_out, s, M, K, scales, 1, 4, M, 1)))
+    return SPEAR_ERR_INVALID_ARG;
+  if (M == 0) return SPEAR_OK;
+  const int64_t blocks = ((int64_t)M * ((K + 15) / 16) + 255) / 256;
+  if (blocks > 0x7FFFFFFF) return SPEAR_ERR_UNSUPPORTED;
+  const int vec = vec_ok(out, ld_out, M, s) && vec_ok(q, ld_q, M, 1);
+  const dim3 grid((unsigned)blocks);
+  switch (type) {
+    case SPEAR_BF16:
+      return kv_launch(dequantize_kernel<__nv_bfloat16>, grid, 256, 0, stream, q, ld_q, scales, M, K,
+                       static_cast<__nv_bfloat16*>(out), ld_out, vec);
+    case SPEAR_F16:
+      return kv_launch(dequantize_kernel<__half>, grid, 256, 0, stream, q, ld_q, scales, M, K,
+                       static_cast<__half*>(out), ld_out, vec);
+    default:
+      return kv_launch(dequantize_kernel<float>, grid, 256, 0, stream, q, ld_q, scales, M, K, static_cast<float*>(out),
+                       ld_out, vec);
+  }
+}

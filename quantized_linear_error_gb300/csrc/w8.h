@@ -1,0 +1,55 @@
+// Linears of 8-bit integer weights and activations: handle, kernel-side weight
+// layout and launches (not part of the public ABI).
+#pragma once
+#include "internal.h"
+
+// Kernel-side weights, built once by spear_w8_create and read by both kernels.
+// Rows are grouped in strips of 16, zero rows past N. A strip and 64 input
+// channels make a block of 1 KB, blocks ordered [strip][k block]: 64 chunks of
+// 16 channels of one row. The chunk of row r and channels 16 t .. 16 t + 15
+// (t = 0 .. 3), with g = r % 8, stands at 16-byte place
+//   (r / 8) * 32 + t * 8 + (g ^ 2 t),
+// so that 8 lanes in a row hit all banks both when a warp reads as MMA
+// fragments are laid out (lane 4 g + t takes rows g and g + 8) and when lanes
+// are rows. Codes are kept with their top bit turned (code + 128 as a byte).
+// A gated handle's strip holds 8 rows of the first weight, then the same 8 of
+// the second, so that one lane (or lanes 8 apart) has both of an output.
+constexpr int kW8Strip = 16, kW8K = 64, kW8Block = kW8Strip * kW8K;
+
+#ifdef __CUDACC__
+SPEAR_DEVINL int w8_place(int r, int t) { return (r >> 3) * 32 + t * 8 + ((r & 7) ^ (2 * t)); }
+#endif
+
+struct spear_w8_s {
+  int device, sm_count;
+  int K, N;            // N outputs
+  int gated, act;      // act: spear_act_t
+  int strips, kb;      // strips of 16 weight rows (an even number), blocks of 64 channels
+  int max_tokens;
+  uint8_t* w;          // [strips][kb][1 KB]
+  float* w_scales;     // [strips * 16], in the strips' row order
+  void* ws;            // status word, arrival counters, partial sums
+  unsigned* status;
+  unsigned* counters;  // [strips], zero between calls
+  float* part;         // sums of work that several CTAs share
+  size_t ws_bytes, control_bytes;  // control: status and counters, cleared at create
+};
+
+struct W8Call {
+  const int8_t* x;
+  int64_t ld_x;
+  const float* x_scales;
+  void* y;
+  int64_t ld_y;
+  int type;  // spear_dtype_t of y
+  int M;
+};
+
+constexpr int kW8DecodeTokens = 32;        // up to here weights are streamed past few tokens
+constexpr int kRowsMaxWidth = 32768;       // 1024 threads x 32 elements in registers
+
+namespace spear {
+spear_status_t sm_count_of_current(int* sms);
+size_t w8_decode_workspace(const spear_w8_s* h);
+spear_status_t w8_launch_decode(const spear_w8_s* h, const W8Call& c, cudaStream_t stream);
+}

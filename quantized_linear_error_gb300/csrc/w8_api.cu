@@ -1,0 +1,154 @@
+// Linears of 8-bit integers: handle lifetime, argument checks, the weight
+// layout kernel and the dispatch by token count.
+#include <algorithm>
+#include <new>
+
+#include "w8_device.cuh"
+
+namespace spear {
+namespace {
+
+// One thread a 16-byte chunk of the layout (see w8.h).
+__global__ void __launch_bounds__(256) layout_kernel(const int8_t* __restrict__ q0, const int8_t* __restrict__ q1, int N,
+                                                     int K, int kb, int64_t chunks, uint8_t* __restrict__ w) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= chunks) return;
+  const int64_t block = i >> 6;
+  const int r = (int)(i >> 2) & 15, t = (int)i & 3;
+  const int64_t strip = block / kb;
+  const int k = (int)(block - strip * kb) * kW8K + t * 16;
+  const int8_t* src = q0;
+  int64_t n = strip * 16 + r;
+  if (q1) {
+    src = r < 8 ? q0 : q1;
+    n = strip * 8 + (r & 7);
+  }
+  uint4 v = make_uint4(0, 0, 0, 0);
+  if (n < N && k < K) v = *reinterpret_cast<const uint4*>(src + n * K + k);
+  v.x ^= kW8Bias, v.y ^= kW8Bias, v.z ^= kW8Bias, v.w ^= kW8Bias;
+  *reinterpret_cast<uint4*>(w + block * kW8Block + w8_place(r, t) * 16) = v;
+}
+
+__global__ void __launch_bounds__(256) scales_kernel(const float* __restrict__ s0, const float* __restrict__ s1, int N,
+                                                     int rows, float* __restrict__ out) {
+  const int i = blockIdx.x * 256 + threadIdx.x;
+  if (i >= rows) return;
+  const float* src = s1 && (i & 8) ? s1 : s0;
+  const int n = s1 ? (i >> 4) * 8 + (i & 7) : i;
+  out[i] = n < N ? src[n] : 0.f;
+}
+
+bool aligned(const void* p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+}  // namespace
+}  // namespace spear
+
+using namespace spear;
+
+extern "C" spear_status_t spear_w8_create(const spear_w8_desc_t* d, cudaStream_t stream, spear_w8_t* out) {
+  if (!out) return SPEAR_ERR_INVALID_ARG;
+  *out = nullptr;
+  if (!d || !d->qweight || !d->scales || !aligned(d->qweight, 16) || !aligned(d->scales, 4)) return SPEAR_ERR_INVALID_ARG;
+  if (d->K < 16 || d->K % 16 != 0 || d->N < 1 || d->max_tokens < 1) return SPEAR_ERR_INVALID_ARG;
+  const bool gated = d->qweight_up != nullptr;
+  if (gated) {
+    if (!aligned(d->qweight_up, 16) || !d->scales_up || !aligned(d->scales_up, 4)) return SPEAR_ERR_INVALID_ARG;
+    if (d->activation != SPEAR_ACT_SILU && d->activation != SPEAR_ACT_GELU) return SPEAR_ERR_INVALID_ARG;
+  } else if (d->scales_up) {
+    return SPEAR_ERR_INVALID_ARG;
+  }
+  if (d->K > (1 << 20) || d->N > (1 << 22) || d->max_tokens > (1 << 20)) return SPEAR_ERR_UNSUPPORTED;
+  spear_w8_s* h = new (std::nothrow) spear_w8_s();
+  if (!h) return SPEAR_ERR_OOM;
+  h->K = d->K, h->N = d->N, h->gated = gated, h->act = d->activation, h->max_tokens = d->max_tokens;
+  h->kb = (d->K + kW8K - 1) / kW8K;
+  h->strips = (gated ? (d->N + 7) / 8 : (d->N + 15) / 16);
+  h->strips = (h->strips + 1) / 2 * 2;
+  if ((int64_t)h->strips * h->kb > 1 << 30) {  // block numbers are 32-bit
+    delete h;
+    return SPEAR_ERR_UNSUPPORTED;
+  }
+  cudaError_t e = cudaGetDevice(&h->device);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&h->sm_count, cudaDevAttrMultiProcessorCount, h->device);
+  const int64_t blocks = (int64_t)h->strips * h->kb;
+  const size_t w_bytes = (size_t)blocks * kW8Block, s_bytes = (size_t)h->strips * 16 * 4;
+  const size_t control = 128 + ((size_t)h->strips * 4 + 127) / 128 * 128;
+  if (e == cudaSuccess) {
+    h->ws_bytes = control + w8_decode_workspace(h);
+    e = cudaMalloc(&h->w, w_bytes);
+  }
+  if (e == cudaSuccess) e = cudaMalloc(&h->w_scales, s_bytes);
+  if (e == cudaSuccess) e = cudaMalloc(&h->ws, h->ws_bytes);
+  if (e == cudaSuccess) {
+    h->status = static_cast<unsigned*>(h->ws);
+    h->counters = h->status + 32;
+    h->control_bytes = control;
+    h->part = reinterpret_cast<float*>(static_cast<char*>(h->ws) + control);
+    e = cudaMemsetAsync(h->ws, 0, control, stream);
+  }
+  if (e == cudaSuccess) {
+    const int64_t chunks = blocks * 64;
+    layout_kernel<<<(unsigned)((chunks + 255) / 256), 256, 0, stream>>>(d->qweight, d->qweight_up, d->N, d->K, h->kb, chunks,
+                                                                        h->w);
+    scales_kernel<<<(h->strips * 16 + 255) / 256, 256, 0, stream>>>(d->scales, d->scales_up, d->N, h->strips * 16,
+                                                                    h->w_scales);
+    e = cudaGetLastError();
+  }
+  if (e == cudaSuccess) e = cudaStreamSynchronize(stream);  // the caller may reuse its buffers
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    spear_w8_destroy(h);
+    return e == cudaErrorMemoryAllocation ? SPEAR_ERR_OOM : SPEAR_ERR_CUDA;
+  }
+  *out = h;
+  return SPEAR_OK;
+}
+
+extern "C" spear_status_t spear_w8_destroy(spear_w8_t h) {
+  if (!h) return SPEAR_OK;
+  cudaError_t e = cudaSuccess;
+  for (void* p : {static_cast<void*>(h->w), static_cast<void*>(h->w_scales), h->ws}) {
+    const cudaError_t f = p ? cudaFree(p) : cudaSuccess;
+    if (f != cudaSuccess) e = f;
+  }
+  delete h;
+  return e == cudaSuccess ? SPEAR_OK : SPEAR_ERR_CUDA;
+}
+
+extern "C" spear_status_t spear_w8_forward(spear_w8_t h, const int8_t* x, int64_t ld_x, const float* x_scales, void* y,
+                                           int64_t ld_y, spear_dtype_t type, int32_t M, cudaStream_t stream) {
+  if (!h || M < 0 || M > h->max_tokens) return SPEAR_ERR_INVALID_ARG;
+  if (type != SPEAR_BF16 && type != SPEAR_F16 && type != SPEAR_F32) return SPEAR_ERR_INVALID_ARG;
+  if (M == 0) return SPEAR_OK;
+  const unsigned size = type == SPEAR_F32 ? 4 : 2;
+  if (!x || !x_scales || !y || !aligned(x, 16) || !aligned(x_scales, 4) || !aligned(y, size)) return SPEAR_ERR_INVALID_ARG;
+  if (ld_x < h->K || (M > 1 && ld_x % 16 != 0) || ld_y < h->N) return SPEAR_ERR_INVALID_ARG;
+  const uintptr_t x0 = reinterpret_cast<uintptr_t>(x), y0 = reinterpret_cast<uintptr_t>(y), s0 = reinterpret_cast<uintptr_t>(x_scales);
+  const uintptr_t x1 = x0 + (uintptr_t)(M - 1) * ld_x + h->K, y1 = y0 + ((uintptr_t)(M - 1) * ld_y + h->N) * size;
+  if ((x0 < y1 && y0 < x1) || (s0 < y1 && y0 < s0 + (uintptr_t)M * 4)) return SPEAR_ERR_INVALID_ARG;
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return SPEAR_ERR_CUDA;
+  if (dev != h->device) return SPEAR_ERR_INVALID_ARG;
+  W8Call c = {x, ld_x, x_scales, y, ld_y, (int)type, M};
+  for (int m = 0; m < M; m += kW8DecodeTokens) {
+    c.M = std::min(kW8DecodeTokens, M - m);
+    c.x = x + m * ld_x;
+    c.x_scales = x_scales + m;
+    c.y = static_cast<char*>(y) + m * ld_y * size;
+    const spear_status_t st = w8_launch_decode(h, c, stream);
+    if (st != SPEAR_OK) return st;
+  }
+  return SPEAR_OK;
+}
+
+extern "C" spear_status_t spear_w8_check(spear_w8_t h, cudaStream_t stream) {
+  if (!h) return SPEAR_ERR_INVALID_ARG;
+  unsigned status = 0;
+  if (cudaMemcpyAsync(&status, h->status, sizeof(status), cudaMemcpyDeviceToHost, stream) != cudaSuccess ||
+      cudaStreamSynchronize(stream) != cudaSuccess)
+    return SPEAR_ERR_CUDA;
+  if (status == 0) return SPEAR_OK;
+  if (cudaMemsetAsync(h->ws, 0, h->control_bytes, stream) != cudaSuccess || cudaStreamSynchronize(stream) != cudaSuccess)
+    return SPEAR_ERR_CUDA;
+  return SPEAR_ERR_TIMEOUT;
+}

@@ -19,6 +19,8 @@ HEADER = PKG.parent / "include" / "spear.h"
 
 SPEAR_OK, SPEAR_ERR_INVALID_ARG, SPEAR_ERR_UNSUPPORTED, SPEAR_ERR_OOM, SPEAR_ERR_CUDA, SPEAR_ERR_TIMEOUT = range(6)
 SPEAR_GATE_SIGMOID, SPEAR_GATE_ONE, SPEAR_GATE_MLP = 0, 1, 2
+SPEAR_BF16, SPEAR_F16, SPEAR_F32 = 0, 1, 2
+SPEAR_ACT_SILU, SPEAR_ACT_GELU = 0, 1
 DECODE_MAX_TOKENS = 32
 
 
@@ -34,6 +36,11 @@ class spear_kv_desc_t(ctypes.Structure):
     _fields_ = [("n_heads", c_int32), ("n_kv_heads", c_int32), ("head_dim", c_int32), ("page_size", c_int32),
                 ("n_pages", c_int32), ("pool", c_void_p), ("rope_dim", c_int32), ("rope_interleaved", c_int32),
                 ("n_positions", c_int32), ("rope_table", c_void_p)]
+
+
+class spear_w8_desc_t(ctypes.Structure):
+    _fields_ = [("K", c_int32), ("N", c_int32), ("qweight", c_void_p), ("scales", c_void_p), ("qweight_up", c_void_p),
+                ("scales_up", c_void_p), ("activation", c_int), ("max_tokens", c_int32)]
 
 
 class SpearError(RuntimeError):
@@ -102,13 +109,22 @@ def load(path: Path | None = None):
                                      c_int32, c_int32, c_int32, c_float, c_int32, H]
     L.spear_kv_check.argtypes = [H, H]
     L.spear_kv_destroy.argtypes = [H]
+    L.spear_rms_norm.argtypes = [H, c_int64, c_int, H, c_int64, H, c_int64, c_int, H, c_int, c_float, c_int32, c_int32,
+                                 H, c_int64, H, c_int64, H, H]
+    L.spear_quantize_rows.argtypes = [H, c_int64, c_int, c_int32, c_int32, H, c_int64, H, H]
+    L.spear_dequantize_rows.argtypes = [H, c_int64, H, c_int32, c_int32, H, c_int64, c_int, H]
+    L.spear_w8_create.argtypes = [POINTER(spear_w8_desc_t), H, POINTER(c_void_p)]
+    L.spear_w8_forward.argtypes = [H, H, c_int64, H, H, c_int64, c_int, c_int32, H]
+    L.spear_w8_check.argtypes = [H, H]
+    L.spear_w8_destroy.argtypes = [H]
     L.spear_status_string.argtypes = [c_int]
     L.spear_status_string.restype = c_char_p
     for name in ("spear_linear_create", "spear_linear_forward_decode", "spear_linear_forward_prefill",
                  "spear_linear_forward", "spear_linear_forward_host", "spear_linear_destroy",
                  "spear_linear_dequantize", "spear_linear_check", "spear_linear_debug_set",
                  "spear_kv_create", "spear_kv_append", "spear_kv_read", "spear_kv_attention", "spear_kv_check",
-                 "spear_kv_destroy"):
+                 "spear_kv_destroy", "spear_rms_norm", "spear_quantize_rows", "spear_dequantize_rows", "spear_w8_create",
+                 "spear_w8_forward", "spear_w8_check", "spear_w8_destroy"):
         getattr(L, name).restype = c_int
     _lib = L
     return L
@@ -463,6 +479,163 @@ class SpearKVCache:
     def close(self) -> None:
         if getattr(self, "h", None) and self.h.value:
             load().spear_kv_destroy(self.h)
+            self.h = c_void_p()
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class _Rows:
+    """What the calls on rows look up: torch's types, once torch is loaded."""
+
+    def __init__(self):
+        import torch
+        self.types = {torch.bfloat16: SPEAR_BF16, torch.float16: SPEAR_F16, torch.float32: SPEAR_F32}
+        self.i8, self.f32, self.empty = torch.int8, torch.float32, torch.empty
+        L = load()
+        self.norm, self.quantize, self.dequantize = L.spear_rms_norm, L.spear_quantize_rows, L.spear_dequantize_rows
+
+
+_rows_ = None
+
+
+def _rows() -> _Rows:
+    global _rows_
+    if _rows_ is None:
+        _rows_ = _Rows()
+    return _rows_
+
+
+def _ld(what, name, x, M, K, *dtypes) -> int:
+    """Elements from one row of x to the next, of a CUDA tensor [M][K] with contiguous rows of one of the dtypes."""
+    if x.dtype not in dtypes or not x.is_cuda or x.shape != (M, K):
+        kinds = " or ".join(str(d).replace("torch.", "") for d in dtypes)
+        raise ValueError(f"{what}: {name} must be CUDA {kinds} [{M}][{K}]")
+    ld, one = x.stride()
+    if one != 1 and K > 1:
+        raise ValueError(f"{what}: {name}: the elements of a row must be contiguous")
+    return ld if M > 1 else K  # the stride of a single row means nothing
+
+
+def _vector(what, name, x, n, *dtypes) -> int:
+    """Address of a contiguous CUDA tensor [n] of one of the dtypes."""
+    if x.dtype not in dtypes or not x.is_cuda or x.shape != (n,) or not x.is_contiguous():
+        kinds = " or ".join(str(d).replace("torch.", "") for d in dtypes)
+        raise ValueError(f"{what}: {name} must be contiguous CUDA {kinds} [{n}]")
+    return x.data_ptr()
+
+
+def rms_norm(x, weight, eps=1e-5, residual=None, residual_out=None, y=None, q=None, scales=None, stream=None):
+    """Root-mean-square norm of the rows of x [M][K] (bf16, f16 or fp32) times ``weight`` [K] (x's type or fp32), in one
+    launch. ``residual`` [M][K] (x's type or fp32) is added to x first and the sum goes to ``residual_out`` (default: in
+    place). The result goes to ``y`` (x's type), to ``q`` int8 [M][K] with ``scales`` fp32 [M] (8-bit rows, as
+    :class:`SpearW8Linear` takes them), or to both. See spear_rms_norm."""
+    r = _rows()
+    f32, (M, K), xt = r.f32, x.shape, x.dtype
+    t = r.types.get(xt, -1)
+    ld_x = _ld("rms_norm", "x", x, M, K, *r.types)
+    w = _vector("rms_norm", "weight", weight, K, xt, f32)
+    rt = rp = ro = ld_r = ld_ro = yp = ld_y = qp = ld_q = sp = 0
+    if residual is not None:
+        if residual_out is None:
+            residual_out = residual
+        rt = r.types.get(residual.dtype, -1)
+        ld_r = _ld("rms_norm", "residual", residual, M, K, xt, f32)
+        ld_ro = _ld("rms_norm", "residual_out", residual_out, M, K, residual.dtype)
+        rp, ro = residual.data_ptr(), residual_out.data_ptr()
+    elif residual_out is not None:
+        raise ValueError("rms_norm: residual_out without residual")
+    if y is not None:
+        yp, ld_y = y.data_ptr(), _ld("rms_norm", "y", y, M, K, xt)
+    if q is not None and scales is not None:
+        qp, ld_q = q.data_ptr(), _ld("rms_norm", "q", q, M, K, r.i8)
+        sp = _vector("rms_norm", "scales", scales, M, f32)
+    elif q is not None or scales is not None or y is None:
+        raise ValueError("rms_norm: give y, or q and scales, or all three")
+    st = r.norm(x.data_ptr(), ld_x, t, rp, ld_r, ro, ld_ro, rt, w, r.types[weight.dtype], eps, M, K, yp, ld_y, qp, ld_q, sp,
+                _stream(stream))
+    if st:
+        raise SpearError(st, "spear_rms_norm")
+    return y if q is None else (q, scales)
+
+
+def quantize_rows(x, q=None, scales=None, stream=None):
+    """Rows of x [M][K] (bf16, f16 or fp32) in 8 bits: (q int8 [M][K], scales fp32 [M]), made if not given; activations
+    with a scale a token, or weights with a scale an output channel. See spear_quantize_rows."""
+    r = _rows()
+    M, K = x.shape
+    ld_x = _ld("quantize_rows", "x", x, M, K, *r.types)
+    if q is None:
+        q = r.empty((M, K), dtype=r.i8, device=x.device)
+    if scales is None:
+        scales = r.empty((M,), dtype=r.f32, device=x.device)
+    st = r.quantize(x.data_ptr(), ld_x, r.types[x.dtype], M, K, q.data_ptr(), _ld("quantize_rows", "q", q, M, K, r.i8),
+                    _vector("quantize_rows", "scales", scales, M, r.f32), _stream(stream))
+    if st:
+        raise SpearError(st, "spear_quantize_rows")
+    return q, scales
+
+
+def dequantize_rows(q, scales, out, stream=None):
+    """What 8-bit rows stand for, q * scales, into ``out`` [M][K] (bf16, f16 or fp32). See spear_dequantize_rows."""
+    r = _rows()
+    M, K = q.shape
+    st = r.dequantize(q.data_ptr(), _ld("dequantize_rows", "q", q, M, K, r.i8),
+                      _vector("dequantize_rows", "scales", scales, M, r.f32), M, K, out.data_ptr(),
+                      _ld("dequantize_rows", "out", out, M, K, *r.types), r.types[out.dtype], _stream(stream))
+    if st:
+        raise SpearError(st, "spear_dequantize_rows")
+    return out
+
+
+class SpearW8Linear:
+    """Owner of one ``spear_w8_t``: a linear of 8-bit integer weights and activations.
+
+    ``qweight`` int8 [N][K] and ``scales`` fp32 [N] (see :func:`quantize_rows`) are contiguous CUDA tensors; with ``up`` and
+    ``up_scales`` of the same shapes the layer is a gated pair, act(x W^T) * (x U^T), ``activation`` "silu" or "gelu" (the
+    tanh form). The library copies them; the tensors may be freed after construction. Linears that read the same x (q, k
+    and v) are one layer of their weights stacked along N.
+    """
+
+    def __init__(self, qweight, scales, max_tokens=32, up=None, up_scales=None, activation="silu", stream=None):
+        r = _rows()
+        N, K = qweight.shape
+        acts = {"silu": SPEAR_ACT_SILU, "gelu": SPEAR_ACT_GELU}
+        if activation not in acts:
+            raise ValueError(f"activation must be one of {sorted(acts)}")
+        if (up is None) != (up_scales is None):
+            raise ValueError("up and up_scales come together")
+        for name, w, s in (("qweight", qweight, scales), ("up", up, up_scales)):
+            if w is not None:
+                if _ld("SpearW8Linear", name, w, N, K, r.i8) != K or not w.is_contiguous():
+                    raise ValueError(f"SpearW8Linear: {name} must be contiguous")
+                _vector("SpearW8Linear", "the scales of " + name, s, N, r.f32)
+        d = spear_w8_desc_t(K, N, _ptr(qweight), _ptr(scales), _ptr(up), _ptr(up_scales), acts[activation], int(max_tokens))
+        h = c_void_p()
+        L = load()
+        _check(L.spear_w8_create(byref(d), _stream(stream), byref(h)), "spear_w8_create")
+        self.h, self.K, self.N, self.gated, self.max_tokens = h, K, N, up is not None, int(max_tokens)
+        self._forward, self._types, self._i8, self._f32 = L.spear_w8_forward, r.types, r.i8, r.f32
+
+    def forward(self, q, scales, y, stream=None):
+        """y [M][N] (bf16, f16 or fp32) of the 8-bit rows ``q`` int8 [M][K] with ``scales`` fp32 [M]."""
+        M = q.shape[0]
+        st = self._forward(self.h, q.data_ptr(), _ld("SpearW8Linear", "q", q, M, self.K, self._i8),
+                           _vector("SpearW8Linear", "scales", scales, M, self._f32), y.data_ptr(),
+                           _ld("SpearW8Linear", "y", y, M, self.N, *self._types), self._types[y.dtype], M, _stream(stream))
+        if st:
+            raise SpearError(st, "spear_w8_forward")
+        return y
+
+    def check(self, stream=None) -> int:
+        return load().spear_w8_check(self.h, _stream(stream))
+
+    def close(self) -> None:
+        if getattr(self, "h", None) and self.h.value:
+            load().spear_w8_destroy(self.h)
             self.h = c_void_p()
 
     def __del__(self):

@@ -1,0 +1,103 @@
+"""Refusals of the 8-bit calls that need no GPU: every bad descriptor and argument is turned down before the device is
+touched."""
+import ctypes
+
+import pytest
+
+from quantized_linear_error_gb300 import build, spear
+
+BAD, UNSUPPORTED = spear.SPEAR_ERR_INVALID_ARG, spear.SPEAR_ERR_UNSUPPORTED
+
+
+@pytest.fixture(scope="module")
+def L():
+    build.build()
+    return spear.load()
+
+
+def _desc(**kw):
+    d = dict(K=64, N=8, qweight=4096, scales=4096, qweight_up=None, scales_up=None, activation=0, max_tokens=4)
+    d.update(kw)
+    return spear.spear_w8_desc_t(*[d[f] for f, _ in spear.spear_w8_desc_t._fields_])
+
+
+@pytest.mark.parametrize("bad", [dict(K=0), dict(K=8), dict(K=72), dict(K=-64), dict(N=0), dict(N=-8), dict(qweight=None),
+                                 dict(qweight=4104), dict(scales=None), dict(scales=4098), dict(max_tokens=0),
+                                 dict(qweight_up=4096), dict(scales_up=4096), dict(qweight_up=4100, scales_up=4096),
+                                 dict(qweight_up=4096, scales_up=4098),
+                                 dict(qweight_up=4096, scales_up=4096, activation=2),
+                                 dict(qweight_up=4096, scales_up=4096, activation=-1)])
+def test_create_rejects_bad_descriptor(L, bad):
+    h = ctypes.c_void_p(1234)
+    assert L.spear_w8_create(ctypes.byref(_desc(**bad)), None, ctypes.byref(h)) == BAD
+    assert h.value is None
+
+
+@pytest.mark.parametrize("big", [dict(K=(1 << 20) + 16), dict(N=(1 << 22) + 1), dict(max_tokens=(1 << 20) + 1),
+                                 dict(K=1 << 20, N=1 << 22)])
+def test_create_rejects_sizes_past_the_kernels(L, big):
+    h = ctypes.c_void_p(1234)
+    assert L.spear_w8_create(ctypes.byref(_desc(**big)), None, ctypes.byref(h)) == UNSUPPORTED
+    assert h.value is None
+
+
+def test_null_arguments(L):
+    h = ctypes.c_void_p()
+    assert L.spear_w8_create(None, None, ctypes.byref(h)) == BAD
+    assert L.spear_w8_create(ctypes.byref(_desc()), None, None) == BAD
+    assert L.spear_w8_forward(None, 16, 64, 16, 16, 8, 0, 1, None) == BAD
+    assert L.spear_w8_check(None, None) == BAD
+    assert L.spear_w8_destroy(None) == spear.SPEAR_OK
+
+
+M, K = 4, 64
+NORM = dict(x=1 << 20, ld_x=K, type=0, res=None, ld_res=0, res_out=None, ld_res_out=0, res_type=0, weight=2 << 20,
+            weight_type=0, eps=1e-5, M=M, K=K, y=3 << 20, ld_y=K, q=4 << 20, ld_q=K, scales=5 << 20)
+RES = dict(res=6 << 20, ld_res=K, res_out=7 << 20, ld_res_out=K)
+
+
+def _norm(L, **kw):
+    return L.spear_rms_norm(*{**NORM, **kw}.values(), None)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(x=None), dict(x=(1 << 20) + 1), dict(ld_x=K - 1), dict(type=3), dict(type=-1), dict(weight=None),
+    dict(weight=(2 << 20) + 1), dict(weight_type=1), dict(weight_type=3), dict(eps=-1.0), dict(eps=float("nan")),
+    dict(eps=float("inf")), dict(M=-1), dict(K=0), dict(y=None, q=None), dict(y=(3 << 20) + 1), dict(ld_y=K - 1),
+    dict(ld_q=K - 1), dict(scales=None), dict(scales=(5 << 20) + 2),
+    {**RES, "res_out": None}, {**RES, "ld_res": K - 1}, {**RES, "ld_res_out": 0}, {**RES, "res_type": 1},
+    {**RES, "res": (6 << 20) + 1},
+    # results that overlap what is read, each other, the weight or the scales
+    dict(y=(1 << 20) + 2 * K), dict(q=1 << 20), dict(q=(3 << 20) + 8), dict(y=2 << 20), dict(scales=(4 << 20) + 16),
+    dict(scales=1 << 20), {**RES, "res_out": (6 << 20) + 2 * K}, {**RES, "res_out": 3 << 20}, {**RES, "y": 6 << 20, "ld_y": K + 8},
+    {**RES, "res_type": 2, "res_out": 1 << 20}, {**RES, "q": 6 << 20}])
+def test_norm_rejects_bad_arguments(L, bad):
+    assert _norm(L, **bad) == BAD
+
+
+def test_norm_rejects_rows_past_the_registers(L):
+    assert _norm(L, K=32769, ld_x=32769, ld_y=32769, ld_q=32769) == UNSUPPORTED
+
+
+def test_no_rows_is_a_no_op(L):
+    assert _norm(L, M=0, x=None, y=None, q=None, scales=None) == spear.SPEAR_OK
+    assert L.spear_quantize_rows(None, K, 0, 0, K, None, K, None, None) == spear.SPEAR_OK
+    assert L.spear_dequantize_rows(None, K, None, 0, K, None, K, 0, None) == spear.SPEAR_OK
+
+
+@pytest.mark.parametrize("bad", [dict(x=None), dict(ld_x=K - 1), dict(x=(1 << 20) + 1), dict(type=3), dict(M=-1), dict(K=0),
+                                 dict(q=None), dict(ld_q=K - 1), dict(scales=None), dict(scales=(5 << 20) + 1),
+                                 dict(q=(1 << 20) + 64), dict(scales=1 << 20), dict(scales=4 << 20)])
+def test_quantize_rejects_bad_arguments(L, bad):
+    a = dict(x=1 << 20, ld_x=K, type=0, M=M, K=K, q=4 << 20, ld_q=K, scales=5 << 20)
+    a.update(bad)
+    assert L.spear_quantize_rows(*a.values(), None) == BAD
+
+
+@pytest.mark.parametrize("bad", [dict(q=None), dict(ld_q=K - 1), dict(scales=None), dict(scales=(5 << 20) + 1), dict(M=-1),
+                                 dict(K=0), dict(out=None), dict(out=(1 << 20) + 1), dict(ld_out=K - 1), dict(type=3),
+                                 dict(out=4 << 20), dict(out=5 << 20)])
+def test_dequantize_rejects_bad_arguments(L, bad):
+    a = dict(q=4 << 20, ld_q=K, scales=5 << 20, M=M, K=K, out=1 << 20, ld_out=K, type=0)
+    a.update(bad)
+    assert L.spear_dequantize_rows(*a.values(), None) == BAD
