@@ -4,29 +4,32 @@
 #include "internal.h"
 
 // Kernel-side weights, built once by spear_w8_create and read by both kernels.
-// Rows are grouped in strips of 16, zero rows past N. A strip and 64 input
-// channels make a block of 1 KB, blocks ordered [strip][k block]: 64 chunks of
-// 16 channels of one row. The chunk of row r and channels 16 t .. 16 t + 15
-// (t = 0 .. 3), with g = r % 8, stands at 16-byte place
+// Rows are grouped in strips of 16 and tiles of 8 strips, zero rows past N. A
+// strip and 64 input channels make a block of 1 KB; blocks are ordered
+// [tile][k block][strip of the tile], so that 128 rows and 64 channels are 8 KB
+// in a row. A block is 64 chunks of 16 channels of one row: the chunk of row r
+// and channels 16 t .. 16 t + 15 (t = 0 .. 3), with g = r % 8, stands at
+// 16-byte place
 //   (r / 8) * 32 + t * 8 + (g ^ 2 t),
 // so that 8 lanes in a row hit all banks both when a warp reads as MMA
 // fragments are laid out (lane 4 g + t takes rows g and g + 8) and when lanes
 // are rows. Codes are kept with their top bit turned (code + 128 as a byte).
 // A gated handle's strip holds 8 rows of the first weight, then the same 8 of
 // the second, so that one lane (or lanes 8 apart) has both of an output.
-constexpr int kW8Strip = 16, kW8K = 64, kW8Block = kW8Strip * kW8K;
+constexpr int kW8Strip = 16, kW8K = 64, kW8Block = kW8Strip * kW8K, kW8Tile = 8;
 
-#ifdef __CUDACC__
-SPEAR_DEVINL int w8_place(int r, int t) { return (r >> 3) * 32 + t * 8 + ((r & 7) ^ (2 * t)); }
-#endif
+__host__ __device__ inline int w8_place(int r, int t) { return (r >> 3) * 32 + t * 8 + ((r & 7) ^ (2 * t)); }
+__host__ __device__ inline int64_t w8_block(int strip, int k, int kb) {
+  return (((int64_t)(strip / kW8Tile) * kb + k) * kW8Tile + strip % kW8Tile) * kW8Block;
+}
 
 struct spear_w8_s {
   int device, sm_count;
   int K, N;            // N outputs
   int gated, act;      // act: spear_act_t
-  int strips, kb;      // strips of 16 weight rows (an even number), blocks of 64 channels
+  int strips, kb;      // strips of 16 weight rows (whole tiles), blocks of 64 channels
   int max_tokens;
-  uint8_t* w;          // [strips][kb][1 KB]
+  uint8_t* w;          // strips * kb blocks
   float* w_scales;     // [strips * 16], in the strips' row order
   void* ws;            // status word, arrival counters, partial sums
   unsigned* status;

@@ -15,8 +15,8 @@ __global__ void __launch_bounds__(256) layout_kernel(const int8_t* __restrict__ 
   if (i >= chunks) return;
   const int64_t block = i >> 6;
   const int r = (int)(i >> 2) & 15, t = (int)i & 3;
-  const int64_t strip = block / kb;
-  const int k = (int)(block - strip * kb) * kW8K + t * 16;
+  const int64_t at = block / kW8Tile, tile = at / kb, strip = tile * kW8Tile + block % kW8Tile;
+  const int k = (int)(at - tile * kb) * kW8K + t * 16;
   const int8_t* src = q0;
   int64_t n = strip * 16 + r;
   if (q1) {
@@ -63,7 +63,7 @@ extern "C" spear_status_t spear_w8_create(const spear_w8_desc_t* d, cudaStream_t
   h->K = d->K, h->N = d->N, h->gated = gated, h->act = d->activation, h->max_tokens = d->max_tokens;
   h->kb = (d->K + kW8K - 1) / kW8K;
   h->strips = (gated ? (d->N + 7) / 8 : (d->N + 15) / 16);
-  h->strips = (h->strips + 1) / 2 * 2;
+  h->strips = (h->strips + kW8Tile - 1) / kW8Tile * kW8Tile;
   if ((int64_t)h->strips * h->kb > 1 << 30) {  // block numbers are 32-bit
     delete h;
     return SPEAR_ERR_UNSUPPORTED;

@@ -4,14 +4,15 @@
 //   y[m][n] = round(s_x[m] s_w[n] sum_k q_x[m][k] q_w[n][k])
 //
 // Bound by the weights' bytes. Each warp streams blocks of its own through a
-// private ring in shared memory (asynchronous 16-byte copies; a lane reads back
-// only what it copied, so nothing but its own copies has to be waited for),
+// private ring in shared memory (bulk copies; it waits for nothing but them),
 // turns the codes into f16 in registers and feeds warp MMAs whose A operand is
 // 16 weight rows and whose columns are 8 tokens. Products of codes and their
 // sums below 2^24 are exact in the fp32 accumulators.
 //
-// The warps of a CTA take blocks of the same rows along K in turn; their sums
-// are added in shared memory in a fixed order.
+// A warp takes RS strips of 16 rows at once, so that a token's codes are
+// fetched and converted once for them; the warps of a CTA take blocks of the
+// same rows along K in turn, and their sums are added in shared memory in a
+// fixed order.
 #include <algorithm>
 
 #include "w8_device.cuh"
@@ -28,22 +29,10 @@ struct StreamParams {
   void* y;
   int64_t ld_y;
   float* part;
-  unsigned* counters;
+  unsigned *counters, *status;
   int type, M, K, N, kb, gated, act;
   int units, balanced, per;  // blocks in all; split evenly, or `per` whole row groups a CTA
 };
-
-SPEAR_DEVINL void cp_async16(uint32_t dst, const void* src, unsigned bytes) {  // zeros past `bytes`
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-SPEAR_DEVINL void cp_async16_stream(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-SPEAR_DEVINL void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-SPEAR_DEVINL void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 
 SPEAR_DEVINL void mma_f16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -51,20 +40,23 @@ SPEAR_DEVINL void mma_f16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// First block of CTA c.
+constexpr uint64_t kWaitNs = 100000000ull;
+
+// First unit of CTA c.
 __host__ __device__ inline int range_start(int c, int grid, int units, int balanced, int per, int kb) {
   if (balanced) return (int)((int64_t)c * units / grid);
   const int64_t u = (int64_t)c * per * kb;
   return u < units ? (int)u : units;
 }
 
-// MT tiles of 8 tokens, RS strips of 16 rows a warp, NW warps, D blocks in flight a warp.
+// MT tiles of 8 tokens, RS strips of 16 rows a warp, NW warps, D stages a warp.
 template <int MT, int RS, int NW, int D>
 struct Plan {
-  static constexpr int kStage = RS * kW8Block + MT * 512;     // a warp's
+  static constexpr int kStage = RS * kW8Block;                // a warp's
   static constexpr int kRing = NW * D * kStage;
   static constexpr int kElems = RS * MT * 128;                // sums of a row group
-  static constexpr int kSmem = kRing + 2 * NW * kElems * 4 + 16;
+  static constexpr int kBars = kRing + NW * kElems * 4;
+  static constexpr int kSmem = kBars + NW * D * 8 + 16;
   static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
 };
 
@@ -75,59 +67,54 @@ __global__ void __launch_bounds__(NW * 32, 1) stream_kernel(const __grid_constan
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int u0 = range_start(blockIdx.x, gridDim.x, p.units, p.balanced, p.per, p.kb);
   const int u1 = range_start(blockIdx.x + 1, gridDim.x, p.units, p.balanced, p.per, p.kb);
-  const uint32_t ring = smem_u32(smem) + warp * D * P::kStage + lane * 16;
+  uint8_t* ring = smem + warp * D * P::kStage;
   float* red = reinterpret_cast<float*>(smem + P::kRing);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + P::kBars) + warp * D;
   volatile int& last = *reinterpret_cast<volatile int*>(smem + P::kSmem - 16);
 
   grid_launch_dependents();
-  // a row group's strips follow each other, kb blocks each
-  int fg = u0 / p.kb, fk = u0 - fg * p.kb + warp, fu = u0 + warp;  // the block to be copied next
+  // The block to be copied next: unit fu = row group fg, k block fk.
+  int fg = u0 / p.kb, fk = u0 - fg * p.kb + warp, fu = u0 + warp, copied = u1;
   while (fk >= p.kb) fk -= p.kb, ++fg;
-  auto fetch_w = [&](int stage) {
-    if (fu < u1) {
-      const uint8_t* src = p.w + ((int64_t)fg * RS * p.kb + fk) * kW8Block + w8_place(g, t) * 16;
-#pragma unroll
-      for (int r = 0; r < RS; ++r)
-#pragma unroll
-        for (int half = 0; half < 2; ++half)
-          cp_async16_stream(ring + stage * P::kStage + r * kW8Block + half * 512,
-                            src + (int64_t)r * p.kb * kW8Block + half * 512);
+  auto fetch = [&](int stage) {
+    if (fu < copied) {
+      if (lane == 0) mbar_arrive_expect_tx(bars + stage, P::kStage);
+      __syncwarp();
+      // the group's strips of one k block lie side by side
+      if (lane == 0)
+        bulk_g2s(ring + stage * P::kStage, p.w + w8_block(fg * RS, fk, p.kb), P::kStage, bars + stage);
     }
-  };
-  auto fetch_x = [&](int stage, int u, int kblock) {
-    if (u < u1) {
-      const int k = kblock * kW8K + t * 16;
-#pragma unroll
-      for (int j = 0; j < MT; ++j) {
-        const int m = j * 8 + g;
-        const bool real = m < p.M && k < p.K;  // K is a multiple of 16
-        cp_async16(ring + stage * P::kStage + RS * kW8Block + j * 512, real ? p.x + m * p.ld_x + k : p.x, real ? 16 : 0);
-      }
-    }
-  };
-  auto advance = [&] {
     fu += NW, fk += NW;
     while (fk >= p.kb) fk -= p.kb, ++fg;
   };
-  const int u_first = fu, k_first = fk;
+  uint4 xr[MT];  // of the unit that is worked on next
+  int xk = u0 % p.kb + warp;
+  while (xk >= p.kb) xk -= p.kb;
+  auto fetch_x = [&](int u) {
+    const int k = xk * kW8K + t * 16;
 #pragma unroll
-  for (int d = 0; d < D; ++d) {  // the handle's own weights, while the kernel before this one ends
-    fetch_w(d);
-    advance();
-  }
-  grid_wait();
-  {
-    int u = u_first, k = k_first;
-#pragma unroll
-    for (int d = 0; d < D; ++d) {
-      fetch_x(d, u, k);
-      cp_async_commit();
-      u += NW, k += NW;
-      while (k >= p.kb) k -= p.kb;
+    for (int j = 0; j < MT; ++j) {
+      const int m = j * 8 + g;
+      xr[j] = make_uint4(0, 0, 0, 0);
+      if (u < u1 && m < p.M && k < p.K) xr[j] = *reinterpret_cast<const uint4*>(p.x + m * p.ld_x + k);  // K is a multiple of 16
     }
+    xk += NW;
+    while (xk >= p.kb) xk -= p.kb;
+  };
+  if (lane == 0) {
+#pragma unroll
+    for (int d = 0; d < D; ++d) mbar_init(bars + d, 1);
+    fence_mbar_init();
   }
+  __syncwarp();
+#pragma unroll
+  for (int d = 0; d < D; ++d) fetch(d);  // the handle's own weights, while the kernel before this one ends
+  grid_wait();
+  fetch_x(u0 + warp);
 
-  int u = u0 + warp, stage = 0, buf = 0;
+  int u = u0 + warp, stage = 0;
+  unsigned phase = 0;
+  const uint32_t place = w8_place(g, t) * 16;
   for (int seg = u0; seg < u1;) {
     const int group = seg / p.kb, end = min(u1, (group + 1) * p.kb);
     float acc[RS][MT][4];
@@ -138,21 +125,27 @@ __global__ void __launch_bounds__(NW * 32, 1) stream_kernel(const __grid_constan
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[r][j][i] = 0.f;
     for (; u < end; u += NW) {
-      cp_async_wait<D - 1>();
-      const uint32_t at = ring + stage * P::kStage;
       uint32_t b[MT][8];
 #pragma unroll
       for (int j = 0; j < MT; ++j) {
-        const uint4 v = lds128(at + RS * kW8Block + j * 512);
-        w8_unpack(v.x ^ kW8Bias, b[j][0], b[j][1]);
-        w8_unpack(v.y ^ kW8Bias, b[j][2], b[j][3]);
-        w8_unpack(v.z ^ kW8Bias, b[j][4], b[j][5]);
-        w8_unpack(v.w ^ kW8Bias, b[j][6], b[j][7]);
+        w8_unpack(xr[j].x ^ kW8Bias, b[j][0], b[j][1]);
+        w8_unpack(xr[j].y ^ kW8Bias, b[j][2], b[j][3]);
+        w8_unpack(xr[j].z ^ kW8Bias, b[j][4], b[j][5]);
+        w8_unpack(xr[j].w ^ kW8Bias, b[j][6], b[j][7]);
       }
+      fetch_x(u + NW);
+      if (u < copied && !__all_sync(0xffffffffu, mbar_wait_bounded(bars + stage, phase, kWaitNs))) {
+        copied = min(copied, fu);  // no further copies; those in flight are still waited for
+        if (lane == 0) atomicOr(p.status, kStatusTimeoutPipe);
+      }
+      const uint32_t at = smem_u32(ring + stage * P::kStage) + place;
+      uint4 v[RS][2];
+#pragma unroll
+      for (int r = 0; r < RS; ++r) v[r][0] = lds128(at + r * kW8Block), v[r][1] = lds128(at + r * kW8Block + 512);
 #pragma unroll
       for (int r = 0; r < RS; ++r) {
-        const uint4 v0 = lds128(at + r * kW8Block), v1 = lds128(at + r * kW8Block + 512);
-        const uint32_t lo[4] = {v0.x, v0.y, v0.z, v0.w}, hi[4] = {v1.x, v1.y, v1.z, v1.w};
+        const uint32_t lo[4] = {v[r][0].x, v[r][0].y, v[r][0].z, v[r][0].w};
+        const uint32_t hi[4] = {v[r][1].x, v[r][1].y, v[r][1].z, v[r][1].w};
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
           uint32_t a0, a1, a2, a3;
@@ -162,13 +155,12 @@ __global__ void __launch_bounds__(NW * 32, 1) stream_kernel(const __grid_constan
           for (int j = 0; j < MT; ++j) mma_f16_16816(acc[r][j], a0, a1, a2, a3, b[j][2 * s], b[j][2 * s + 1]);
         }
       }
-      fetch_w(stage);
-      fetch_x(stage, fu, fk);
-      cp_async_commit();
-      advance();
-      stage = stage + 1 == D ? 0 : stage + 1;
+      __syncwarp();  // every lane has read its part
+      fetch(stage);
+      if (++stage == D) stage = 0, phase ^= 1;
     }
-    float* mine = red + (buf * NW + warp) * P::kElems;
+    __syncthreads();  // the sums of the group before have been read
+    float* mine = red + warp * P::kElems;
 #pragma unroll
     for (int r = 0; r < RS; ++r)
 #pragma unroll
@@ -176,11 +168,10 @@ __global__ void __launch_bounds__(NW * 32, 1) stream_kernel(const __grid_constan
 #pragma unroll
         for (int i = 0; i < 4; ++i) mine[((r * MT + j) * 4 + i) * 32 + lane] = acc[r][j][i];
     __syncthreads();
-    const float* sums = red + buf * NW * P::kElems;
     auto own_sum = [&](int e) {
       float a = 0.f;
 #pragma unroll
-      for (int w = 0; w < NW; ++w) a += sums[w * P::kElems + e];
+      for (int w = 0; w < NW; ++w) a += red[w * P::kElems + e];
       return a;
     };
     // element e: [r][j][i][lane] -> row 16 r + lane / 4 + 8 (i / 2), token 8 j + 2 (lane % 4) + i % 2
@@ -227,41 +218,61 @@ __global__ void __launch_bounds__(NW * 32, 1) stream_kernel(const __grid_constan
         });
       }
     }
-    buf ^= 1;
     seg = end;
   }
 }
 
+struct Split {
+  int groups, per, grid, balanced;
+  int64_t cost;  // strips x blocks of the CTA with the most, and what joining takes
+};
+
+// Whole row groups of RS strips need no joining between CTAs; an even split does, about the time of 64 blocks.
+Split split(const spear_w8_s* h, int RS, int NW) {
+  Split s;
+  const int used = h->gated ? (h->N + 7) / 8 : (h->N + 15) / 16;
+  s.groups = (used + RS - 1) / RS;
+  s.per = (s.groups + h->sm_count - 1) / h->sm_count;
+  s.grid = (s.groups + s.per - 1) / s.per;
+  s.balanced = 0;
+  s.cost = (int64_t)s.per * h->kb * RS;
+  const int64_t units = (int64_t)s.groups * h->kb;
+  const int even = (int)std::min<int64_t>(h->sm_count, std::max<int64_t>(1, units / NW));
+  const int64_t cost = (units + even - 1) / even * RS + 64;
+  if (cost < s.cost) s.balanced = 1, s.grid = even, s.cost = cost;
+  return s;
+}
+
 template <int MT, int RS, int NW, int D>
-spear_status_t launch(const spear_w8_s* h, const W8Call& c, cudaStream_t stream) {
+spear_status_t launch(const spear_w8_s* h, const W8Call& c, const Split& sp, cudaStream_t stream) {
   using P = Plan<MT, RS, NW, D>;
   static std::atomic<uint64_t> configured{0};
   if (smem_limit_once(reinterpret_cast<const void*>(&stream_kernel<MT, RS, NW, D>), configured) != cudaSuccess)
     return SPEAR_ERR_CUDA;
-  StreamParams p = {h->w, h->w_scales, c.x, c.ld_x, c.x_scales, c.y, c.ld_y, h->part, h->counters};
+  StreamParams p = {h->w, h->w_scales, c.x, c.ld_x, c.x_scales, c.y, c.ld_y, h->part, h->counters, h->status};
   p.type = c.type, p.M = c.M, p.K = h->K, p.N = h->N, p.kb = h->kb, p.gated = h->gated, p.act = h->act;
-  const int groups = h->strips / RS;
-  p.units = groups * h->kb;
-  p.per = (groups + h->sm_count - 1) / h->sm_count;
-  int grid = (groups + p.per - 1) / p.per;
-  // Whole row groups need no joining between CTAs; an even split does (about the time of 64 KB a CTA).
-  const int even = std::min(h->sm_count, std::max(1, p.units / NW));
-  if ((int64_t)p.per * h->kb - p.units / even > 64 / RS) {
-    p.balanced = 1;
-    grid = even;
-  }
-  return kv_launch(stream_kernel<MT, RS, NW, D>, dim3(grid), NW * 32, P::kSmem, stream, p);
+  p.units = sp.groups * h->kb, p.per = sp.per, p.balanced = sp.balanced;
+  return kv_launch(stream_kernel<MT, RS, NW, D>, dim3(sp.grid), NW * 32, P::kSmem, stream, p);
+}
+
+template <int MT, int NW, int D1, int D2, int D4>
+spear_status_t launch(const spear_w8_s* h, const W8Call& c, cudaStream_t stream) {
+  const Split s1 = split(h, 1, NW), s2 = split(h, 2, NW), s4 = split(h, 4, NW);
+  // several strips a warp need fewer instructions a block
+  if (s4.cost * 16 <= s2.cost * 17 && s4.cost * 8 <= s1.cost * 10) return launch<MT, 4, NW, D4>(h, c, s4, stream);
+  if (s2.cost * 8 <= s1.cost * 9) return launch<MT, 2, NW, D2>(h, c, s2, stream);
+  return launch<MT, 1, NW, D1>(h, c, s1, stream);
 }
 
 }  // namespace
 
 // Two parts a CTA, of the variant with the most sums.
-size_t w8_decode_workspace(const spear_w8_s* h) { return (size_t)2 * h->sm_count * Plan<4, 2, 8, 4>::kElems * sizeof(float); }
+size_t w8_decode_workspace(const spear_w8_s* h) { return (size_t)2 * h->sm_count * Plan<4, 4, 8, 4>::kElems * sizeof(float); }
 
 spear_status_t w8_launch_decode(const spear_w8_s* h, const W8Call& c, cudaStream_t stream) {
-  if (c.M <= 8) return launch<1, 1, 16, 6>(h, c, stream);
-  if (c.M <= 16) return launch<2, 2, 16, 3>(h, c, stream);
-  return launch<4, 2, 8, 4>(h, c, stream);
+  if (c.M <= 8) return launch<1, 16, 10, 5, 3>(h, c, stream);
+  if (c.M <= 16) return launch<2, 16, 10, 4, 2>(h, c, stream);
+  return launch<4, 8, 16, 8, 4>(h, c, stream);
 }
 
 }  // namespace spear
