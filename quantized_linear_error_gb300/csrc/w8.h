@@ -34,6 +34,7 @@ struct spear_w8_s {
   void* ws;            // status word, arrival counters, partial sums
   unsigned* status;
   unsigned* counters;  // [strips], zero between calls
+  unsigned* gemm_counters;  // of the tensor-core kernel's shared tiles, zero between calls
   float* part;         // sums of work that several CTAs share
   size_t ws_bytes, control_bytes;  // control: status and counters, cleared at create
 };
@@ -54,5 +55,8 @@ constexpr int kRowsMaxWidth = 32768;       // 1024 threads x 32 elements in regi
 namespace spear {
 spear_status_t sm_count_of_current(int* sms);
 size_t w8_decode_workspace(const spear_w8_s* h);
+size_t w8_prefill_workspace(const spear_w8_s* h);
+size_t w8_prefill_counters(const spear_w8_s* h);
+spear_status_t w8_launch_prefill(const spear_w8_s* h, const W8Call& c, cudaStream_t stream);
 spear_status_t w8_launch_decode(const spear_w8_s* h, const W8Call& c, cudaStream_t stream);
 }

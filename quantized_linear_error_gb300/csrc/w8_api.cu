@@ -72,9 +72,9 @@ extern "C" spear_status_t spear_w8_create(const spear_w8_desc_t* d, cudaStream_t
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&h->sm_count, cudaDevAttrMultiProcessorCount, h->device);
   const int64_t blocks = (int64_t)h->strips * h->kb;
   const size_t w_bytes = (size_t)blocks * kW8Block, s_bytes = (size_t)h->strips * 16 * 4;
-  const size_t control = 128 + ((size_t)h->strips * 4 + 127) / 128 * 128;
   if (e == cudaSuccess) {
-    h->ws_bytes = control + w8_decode_workspace(h);
+    h->control_bytes = 128 + ((h->strips + w8_prefill_counters(h)) * 4 + 127) / 128 * 128;
+    h->ws_bytes = h->control_bytes + std::max(w8_decode_workspace(h), w8_prefill_workspace(h));
     e = cudaMalloc(&h->w, w_bytes);
   }
   if (e == cudaSuccess) e = cudaMalloc(&h->w_scales, s_bytes);
@@ -82,9 +82,9 @@ extern "C" spear_status_t spear_w8_create(const spear_w8_desc_t* d, cudaStream_t
   if (e == cudaSuccess) {
     h->status = static_cast<unsigned*>(h->ws);
     h->counters = h->status + 32;
-    h->control_bytes = control;
-    h->part = reinterpret_cast<float*>(static_cast<char*>(h->ws) + control);
-    e = cudaMemsetAsync(h->ws, 0, control, stream);
+    h->gemm_counters = h->counters + h->strips;
+    h->part = reinterpret_cast<float*>(static_cast<char*>(h->ws) + h->control_bytes);
+    e = cudaMemsetAsync(h->ws, 0, h->control_bytes, stream);
   }
   if (e == cudaSuccess) {
     const int64_t chunks = blocks * 64;
@@ -129,16 +129,8 @@ extern "C" spear_status_t spear_w8_forward(spear_w8_t h, const int8_t* x, int64_
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess) return SPEAR_ERR_CUDA;
   if (dev != h->device) return SPEAR_ERR_INVALID_ARG;
-  W8Call c = {x, ld_x, x_scales, y, ld_y, (int)type, M};
-  for (int m = 0; m < M; m += kW8DecodeTokens) {
-    c.M = std::min(kW8DecodeTokens, M - m);
-    c.x = x + m * ld_x;
-    c.x_scales = x_scales + m;
-    c.y = static_cast<char*>(y) + m * ld_y * size;
-    const spear_status_t st = w8_launch_decode(h, c, stream);
-    if (st != SPEAR_OK) return st;
-  }
-  return SPEAR_OK;
+  const W8Call c = {x, ld_x, x_scales, y, ld_y, (int)type, M};
+  return M <= kW8DecodeTokens ? w8_launch_decode(h, c, stream) : w8_launch_prefill(h, c, stream);
 }
 
 extern "C" spear_status_t spear_w8_check(spear_w8_t h, cudaStream_t stream) {

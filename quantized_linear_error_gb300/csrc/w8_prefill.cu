@@ -1,0 +1,553 @@
+// Many tokens (more than 32) through 8-bit integer weights on the tcgen05
+// tensor cores.
+//
+//   y[m][n] = round(s_x[m] s_w[n] sum_k q_x[m][k] q_w[n][k])
+//
+// sm_103a has no integer MMA of tcgen05's rate, and codes are exact in f16, their
+// products and sums below 2^24 in fp32: the contraction runs at the f16 rate and
+// is bound by it (2 M N K operations).
+//
+// A small kernel turns the tokens' codes into f16 tiles in the order that the
+// tensor cores read (64 channels x 8 tokens, 1 KB, 128-byte swizzle), so that a
+// stage's tokens are one bulk copy; every row tile reads them again, from L2.
+// The weights stay in 8 bits until they reach the SM.
+//
+// A pair of CTAs (a cluster, cta_group::2) works on 256 weight rows x TN tokens:
+// each CTA holds 128 of the rows and half of the tokens, and the MMAs read both
+// halves of the tokens, which halves the shared memory traffic of a single CTA's
+// tile. Roles of a CTA:
+//   warp 0       copies: 8 KB of codes (128 rows x 64 channels) and TN / 2 tokens a stage
+//   warp 1       issues the MMAs of the pair (in the first CTA): A from tensor
+//                memory, B from both CTAs' shared memory
+//   warps 2-9    codes -> f16 -> tensor memory: two warps 32 rows, half the channels each
+//   warps 10-13  epilogue, from the accumulator that the MMAs have left, while they
+//                fill the other one
+//
+// Work is split in whole tiles as long as they fill all pairs; what does not come
+// out even is split along K. Parts of a tile that several pairs share are added by
+// the last one to finish, in the pairs' order, so that a repeated call gives the
+// same bits and nobody waits for another pair.
+#include <algorithm>
+
+#include "tcgen05.cuh"
+#include "w8_device.cuh"
+
+namespace spear {
+namespace {
+
+constexpr uint64_t kWaitNs = 100000000ull;
+constexpr int kThreads = 14 * 32;
+constexpr int kRawBytes = kW8Tile * kW8Block;  // 128 rows x 64 channels
+constexpr int kMaxTokens = 192;                // of a tile: two accumulators and four A slots in 512 columns
+constexpr int kMaxStages = 16, kMaxSlots = 8;
+constexpr int kSmemBudget = 222 * 1024;
+
+struct GemmParams {
+  const uint8_t *w, *x16;
+  const float *w_scales, *x_scales;
+  void* y;
+  int64_t ld_y;
+  float* part;
+  unsigned *counters, *status;
+  int type, pairs_ok;     // pairs_ok: 16-bit results may be stored two at a time
+  int M, N, kb, act, w_tiles;
+  int TN, n_tok, groups;  // tokens of a tile, token tiles, groups of 8 tokens in x16
+  int tiles, sk_tiles, sk_pairs;  // tiles in all; those split along K, over that many pairs
+  int stages, slots, stage_bytes, acc_stride;
+};
+
+struct Segment {
+  int tile, k0, k1;
+};
+
+// The pair's segments in order: its share of the tiles that are split, then whole ones.
+struct Segments {
+  int u, end, next, step;
+  SPEAR_DEVINL Segments(const GemmParams& p, int pair, int pairs) {
+    const int64_t units = (int64_t)p.sk_tiles * p.kb;
+    u = pair < p.sk_pairs ? (int)(pair * units / p.sk_pairs) : 0;
+    end = pair < p.sk_pairs ? (int)((pair + 1) * units / p.sk_pairs) : 0;
+    next = p.sk_tiles + pair;
+    step = pairs;
+  }
+  SPEAR_DEVINL bool get(const GemmParams& p, Segment& s) {
+    if (u < end) {
+      s.tile = u / p.kb;
+      s.k0 = u - s.tile * p.kb;
+      s.k1 = min(p.kb, s.k0 + end - u);
+      u += s.k1 - s.k0;
+      return true;
+    }
+    if (next >= p.tiles) return false;
+    s.tile = next, s.k0 = 0, s.k1 = p.kb;
+    next += step;
+    return true;
+  }
+};
+
+SPEAR_DEVINL uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+SPEAR_DEVINL void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+// Arrive on the first CTA's barrier at the same place.
+SPEAR_DEVINL void mbar_arrive_leader(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .b32 a;\n\t"
+      "mapa.shared::cluster.u32 a, %0, 0;\n\t"
+      "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n\t}" ::"r"(smem_u32(bar))
+      : "memory");
+}
+SPEAR_DEVINL bool mbar_try_wait_cluster(uint64_t* bar, unsigned parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// Bounded, the same for the whole warp.
+SPEAR_DEVINL bool wait_cluster(uint64_t* bar, unsigned parity) {
+  bool ok = mbar_try_wait_cluster(bar, parity);
+  if (!__all_sync(0xffffffffu, ok)) {
+    const uint64_t t0 = globaltimer();
+    while (!(ok = mbar_try_wait_cluster(bar, parity)) && globaltimer() - t0 <= kWaitNs) {
+    }
+  }
+  return __all_sync(0xffffffffu, ok);
+}
+
+SPEAR_DEVINL void umma2_ts(uint32_t leader, uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                           uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(leader)
+      : "memory");
+}
+// Arrive on both CTAs' barriers when the MMAs issued so far have completed.
+SPEAR_DEVINL void umma2_commit(uint32_t leader, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t.reg .b16 m;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "mov.b16 m, 3;\n\t"
+      "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n\t}" ::"r"(
+          smem_u32(bar)),
+      "r"(leader)
+      : "memory");
+}
+
+struct Shared {
+  uint64_t raw[kMaxStages];    // a stage's copies have landed (this CTA)
+  uint64_t a[kMaxStages];      // its codes stand in tensor memory, in both CTAs (the first CTA's)
+  uint64_t empty[kMaxStages];  // its MMAs have run (both CTAs)
+  uint64_t acc_full[2];        // an accumulator is complete (both CTAs)
+  uint64_t acc_empty[2];       // it has been read, in both CTAs (the first CTA's)
+  uint32_t tmem;
+};
+
+// One warp's 32 rows of an accumulator: scaled, rounded and stored, or left as a part.
+template <bool kGated>
+struct Epilogue {
+  const GemmParams& p;
+  int lane, row0;        // row0: first weight row of the warp
+  float sw;              // scale of this lane's row
+
+  SPEAR_DEVINL void store16(int m, int n, float v0, float v1, bool both_ok) const {  // n even (if pairs_ok)
+    if (m >= p.M) return;
+    const int64_t at = m * p.ld_y + n;
+    if (both_ok && n + 1 < p.N) {
+      uint32_t w;
+      if (p.type == SPEAR_BF16) w = pack_bf16x2(v0, v1);
+      else {
+        const __half2 h = __floats2half2_rn(v0, v1);
+        memcpy(&w, &h, 4);
+      }
+      *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.y) + at) = w;
+    } else {
+      if (n < p.N) w8_store(p.y, at, p.type, v0);
+      if (n + 1 < p.N) w8_store(p.y, at + 1, p.type, v1);
+    }
+  }
+
+  // v: 16 columns (tokens m0 ..) of this lane's row; sx: lane j holds token m0 + j's scale (j < 16).
+  SPEAR_DEVINL void columns(const float (&v)[16], int m0, float sx) const {
+    if constexpr (kGated) {
+      // lanes l and l + 8 hold an output's two projections: the first takes the even tokens, the second the odd ones
+      const bool up = lane & 8;
+      const int n = row0 / 2 + (lane >> 4) * 8 + (lane & 7);
+      float o[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float a = v[2 * j] * __shfl_sync(0xffffffffu, sx, 2 * j) * sw;
+        const float b = v[2 * j + 1] * __shfl_sync(0xffffffffu, sx, 2 * j + 1) * sw;
+        const float other = __shfl_xor_sync(0xffffffffu, up ? a : b, 8);
+        const float g = up ? other : a, u = up ? b : other;
+        o[j] = w8_act(g, p.act) * u;
+      }
+      const int m = m0 + (up ? 1 : 0);
+      if (p.type == SPEAR_F32) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (m + 2 * j < p.M && n < p.N) static_cast<float*>(p.y)[(m + 2 * j) * p.ld_y + n] = o[j];
+        return;
+      }
+#pragma unroll
+      for (int j = 0; j < 8; j += 2) {  // neighbours trade a token each, so that both store pairs of outputs
+        const float got = __shfl_xor_sync(0xffffffffu, lane & 1 ? o[j] : o[j + 1], 1);
+        if (lane & 1) store16(m + 2 * j + 2, n - 1, got, o[j + 1], p.pairs_ok);
+        else store16(m + 2 * j, n, o[j], got, p.pairs_ok);
+      }
+    } else {
+      const int n = row0 + lane;
+      if (p.type == SPEAR_F32) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const float a = v[j] * __shfl_sync(0xffffffffu, sx, j) * sw;
+          if (m0 + j < p.M && n < p.N) static_cast<float*>(p.y)[(m0 + j) * p.ld_y + n] = a;
+        }
+        return;
+      }
+#pragma unroll
+      for (int j = 0; j < 16; j += 2) {
+        const float a = v[j] * __shfl_sync(0xffffffffu, sx, j) * sw;
+        const float b = v[j + 1] * __shfl_sync(0xffffffffu, sx, j + 1) * sw;
+        const float got = __shfl_xor_sync(0xffffffffu, lane & 1 ? a : b, 1);
+        if (lane & 1) store16(m0 + j + 1, n - 1, got, b, p.pairs_ok);
+        else store16(m0 + j, n, a, got, p.pairs_ok);
+      }
+    }
+  }
+};
+
+template <bool kGated>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant__ GemmParams p) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;  // the swizzle goes by the address
+  Shared& sh = *reinterpret_cast<Shared*>(smem + p.stages * p.stage_bytes);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+  const int rank = (int)cluster_rank(), pair = blockIdx.x / 2, pairs = gridDim.x / 2;
+  grid_launch_dependents();
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < p.stages; ++s) {
+      mbar_init(&sh.raw[s], 1);
+      mbar_init(&sh.a[s], 16);
+      mbar_init(&sh.empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&sh.acc_full[b], 1);
+      mbar_init(&sh.acc_empty[b], 8);
+    }
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sh.tmem)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    tc_fence_before_sync();
+  }
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after_sync();
+  const uint32_t tmem = sh.tmem;
+  const uint32_t a_base = tmem + 2 * p.acc_stride;
+  const int b_bytes = p.TN * 64;
+
+  Segments segs(p, pair, pairs);
+  Segment sg;
+  bool ok = true;
+  if (warp == 0) {
+    if (lane == 0) {
+      int s = 0, issued = 0;
+      unsigned phase = 1;  // the first pass through the ring finds every stage empty
+      bool waited = false;
+      // the handle's own weights go out ahead of the tokens, which the kernel before this one writes
+      int held = 0;
+      const uint8_t* held_b[kMaxStages];
+      auto flush = [&] {
+        grid_wait();
+        waited = true;
+        for (int i = 0; i < held; ++i) bulk_g2s(smem + i * p.stage_bytes, held_b[i], b_bytes, &sh.raw[i]);
+      };
+      while (ok && segs.get(p, sg)) {
+        const int row = sg.tile / p.n_tok, tok = sg.tile - row * p.n_tok;
+        const uint8_t* w = p.w + ((int64_t)min(row * 2 + rank, p.w_tiles - 1) * p.kb + sg.k0) * kRawBytes;
+        const uint8_t* b = p.x16 + ((int64_t)sg.k0 * p.groups + (tok * p.TN + rank * (p.TN / 2)) / 8) * 1024;
+        for (int k = sg.k0; k < sg.k1; ++k) {
+          if (issued >= p.stages) {
+            if (!waited) flush();
+            if (!mbar_wait_bounded(&sh.empty[s], phase, kWaitNs)) {
+              ok = false;
+              break;
+            }
+          }
+          mbar_arrive_expect_tx(&sh.raw[s], kRawBytes + b_bytes);
+          uint8_t* at = smem + s * p.stage_bytes;
+          bulk_g2s(at + b_bytes, w, kRawBytes, &sh.raw[s]);
+          if (waited) bulk_g2s(at, b, b_bytes, &sh.raw[s]);
+          else held_b[held++] = b;
+          w += kRawBytes, b += (int64_t)p.groups * 1024;
+          ++issued;
+          if (++s == p.stages) s = 0, phase ^= 1;
+        }
+      }
+      if (!waited) flush();
+      // every stage's MMAs have run before the CTA may leave (or, given up, its copies have landed)
+      const int left = min(issued, p.stages);
+      if (!ok) atomicOr(p.status, kStatusTimeoutPipe);
+      for (int i = 0; i < left; ++i) {
+        if (issued < p.stages) s = i;
+        const unsigned use = issued < p.stages ? 0 : phase;
+        if (ok) ok = mbar_wait_bounded(&sh.empty[s], use, kWaitNs);
+        else mbar_wait_bounded(&sh.raw[s], use, kWaitNs / 10);
+        if (++s == p.stages) s = 0, phase ^= 1;
+      }
+    } else {
+      grid_wait();
+    }
+  } else if (warp == 1) {
+    if (rank == 0) {
+      const uint32_t leader = elect_leader();
+      const uint32_t idesc = idesc_f16_f32(256, p.TN);
+      int s = 0, slot = 0, buf = 0;
+      unsigned phase = 0, acc_phase = 1;
+      while (ok && segs.get(p, sg)) {
+        ok = wait_cluster(&sh.acc_empty[buf], acc_phase);
+        if (!ok) break;
+        tc_fence_after_sync();
+        const uint32_t d = tmem + buf * p.acc_stride;
+        for (int k = sg.k0; k < sg.k1; ++k) {
+          ok = wait_cluster(&sh.a[s], phase);
+          if (!ok) break;
+          tc_fence_after_sync();
+          const uint64_t desc = sw128_kmajor_desc(smem_u32(smem + s * p.stage_bytes));
+          const uint32_t a = a_base + slot * 32;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) umma2_ts(leader, d, a + 8 * i, desc + 2 * i, idesc, k > sg.k0 || i > 0);
+          umma2_commit(leader, &sh.empty[s]);
+          if (++s == p.stages) s = 0, phase ^= 1;
+          if (++slot == p.slots) slot = 0;
+        }
+        if (!ok) break;
+        umma2_commit(leader, &sh.acc_full[buf]);
+        if ((buf ^= 1) == 0) acc_phase ^= 1;
+      }
+      if (!ok && lane == 0) atomicOr(p.status, kStatusTimeoutPipe);
+    }
+    grid_wait();
+  } else if (warp < 10) {
+    const int quarter = warp & 3, half = (warp - 2) >> 2;
+    const int r = 32 * quarter + lane;
+    const uint32_t at0 = (uint32_t)((r >> 4) * kW8Block + w8_place(r & 15, 2 * half) * 16);
+    const uint32_t at1 = (uint32_t)((r >> 4) * kW8Block + w8_place(r & 15, 2 * half + 1) * 16);
+    const uint32_t dst = a_base + ((uint32_t)(32 * quarter) << 16) + 16 * half;
+    const uint32_t base = smem_u32(smem) + b_bytes;
+    int s = 0, slot = 0, done = 0, es = 0;  // es: stage of the block whose MMAs free the slot
+    unsigned phase = 0, e_phase = 0;
+    while (ok && segs.get(p, sg)) {
+      for (int k = sg.k0; k < sg.k1; ++k) {
+        ok = warp_wait(&sh.raw[s], phase, kWaitNs, 0);
+        if (!ok) break;
+        const uint4 v0 = lds128(base + s * p.stage_bytes + at0), v1 = lds128(base + s * p.stage_bytes + at1);
+        uint32_t f[16];
+        w8_unpack(v0.x, f[0], f[1]), w8_unpack(v0.y, f[2], f[3]), w8_unpack(v0.z, f[4], f[5]), w8_unpack(v0.w, f[6], f[7]);
+        w8_unpack(v1.x, f[8], f[9]), w8_unpack(v1.y, f[10], f[11]), w8_unpack(v1.z, f[12], f[13]), w8_unpack(v1.w, f[14], f[15]);
+        if (done >= p.slots) {
+          ok = wait_cluster(&sh.empty[es], e_phase);
+          if (!ok) break;
+          tc_fence_after_sync();
+          if (++es == p.stages) es = 0, e_phase ^= 1;
+        } else {
+          ++done;
+        }
+        tmem_st_x16(dst + slot * 32, f);
+        tmem_st_wait();
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_leader(&sh.a[s]);
+        if (++s == p.stages) s = 0, phase ^= 1;
+        if (++slot == p.slots) slot = 0;
+      }
+    }
+    if (!ok && lane == 0) atomicOr(p.status, kStatusTimeoutPipe);
+    grid_wait();
+  } else {
+    grid_wait();  // the tokens' scales, and what the kernel before this one may still read of y
+    const int quarter = warp & 3;
+    int buf = 0;
+    unsigned phase = 0;
+    while (segs.get(p, sg)) {
+      const int row = sg.tile / p.n_tok, tok = sg.tile - row * p.n_tok;
+      const int row0 = (row * 2 + rank) * 128 + 32 * quarter;
+      const bool whole = sg.k0 == 0 && sg.k1 == p.kb;
+      const bool rows = row0 < p.w_tiles * 128;
+      const Epilogue<kGated> out{p, lane, row0, rows ? p.w_scales[row0 + lane] : 0.f};
+      ok = wait_cluster(&sh.acc_full[buf], phase);
+      if (!ok) break;
+      tc_fence_after_sync();
+      const uint32_t acc = tmem + buf * p.acc_stride + ((uint32_t)(32 * quarter) << 16);
+      const int64_t tile_floats = (int64_t)p.TN * 128;
+      // parts: [pair][0 or 1][rank][token][row]; a pair's part is number 1 if the pair starts inside the tile
+      auto part_of = [&](int c) {
+        const int64_t units = (int64_t)p.sk_tiles * p.kb;
+        const int first = c * units / p.sk_pairs >= (int64_t)sg.tile * p.kb ? 1 : 0;
+        return p.part + ((int64_t)(2 * c + first) * 2 + rank) * tile_floats + 32 * quarter + lane;
+      };
+      float* mine = whole ? nullptr : part_of(pair);
+      for (int c = 0; c < p.TN; c += 16) {
+        uint32_t v[16];
+        tmem_ld_x16(acc + c, v);
+        tmem_ld_wait();
+        if (whole) {
+          const int m0 = tok * p.TN + c, mj = m0 + (lane & 15);
+          const float sx = mj < p.M ? p.x_scales[mj] : 0.f;
+          float f[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) f[j] = __uint_as_float(v[j]);
+          out.columns(f, m0, sx);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) mine[(int64_t)(c + j) * 128] = __uint_as_float(v[j]);
+        }
+      }
+      tc_fence_before_sync();
+      if (!whole) __threadfence();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_leader(&sh.acc_empty[buf]);
+      if ((buf ^= 1) == 0) phase ^= 1;
+      if (whole) continue;
+      // the pairs that share the tile: from the one with its first block to the one with its last
+      const int64_t units = (int64_t)p.sk_tiles * p.kb;
+      const int64_t t0 = (int64_t)sg.tile * p.kb, t1 = t0 + p.kb;
+      int c0 = pair, c1 = pair;
+      while (c0 * units / p.sk_pairs > t0) --c0;
+      while ((c1 + 1) * units / p.sk_pairs < t1) ++c1;
+      unsigned last = 0;
+      if (lane == 0) {
+        unsigned* counter = p.counters + (sg.tile * 2 + rank) * 4 + quarter;
+        last = atomicAdd(counter, 1u) == (unsigned)(c1 - c0);
+        if (last) *counter = 0;
+      }
+      if (!__shfl_sync(0xffffffffu, last, 0)) continue;
+      __threadfence();
+      for (int c = 0; c < p.TN; c += 16) {
+        float f[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) f[j] = 0.f;
+        for (int q = c0; q <= c1; ++q) {
+          const float* from = part_of(q) + (int64_t)c * 128;
+          float g[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) g[j] = __ldcg(from + j * 128);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) f[j] += g[j];
+        }
+        const int m0 = tok * p.TN + c, mj = m0 + (lane & 15);
+        out.columns(f, m0, mj < p.M ? p.x_scales[mj] : 0.f);
+      }
+    }
+    if (!ok && lane == 0) atomicOr(p.status, kStatusTimeoutPipe);
+  }
+  __syncwarp();
+  tc_fence_before_sync();
+  __syncthreads();
+  cluster_sync();
+  if (warp == 1) {
+    tc_fence_after_sync();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  }
+}
+
+// Tokens' codes -> f16 tiles [k block][8 tokens][1 KB]: a warp a tile, lane 4 r + t the 16 channels 16 t .. of token r.
+// The order of channels within 16 is that of w8_unpack, as for the weights. Tokens past M and channels past K are zeros.
+constexpr int kConvertTiles = 4;  // k blocks a warp
+__global__ void __launch_bounds__(256) convert_kernel(const int8_t* __restrict__ x, int64_t ld_x, int M, int K, int kb,
+                                                      int groups, uint8_t* __restrict__ x16) {
+  kv_follow();
+  const int lane = threadIdx.x & 31, r = lane >> 2, t = lane & 3;
+  const int group = blockIdx.x, k0 = (blockIdx.y * 8 + threadIdx.x / 32) * kConvertTiles;
+  const int m = group * 8 + r;
+  uint4 v[kConvertTiles];
+#pragma unroll
+  for (int i = 0; i < kConvertTiles; ++i) {
+    const int k = (k0 + i) * kW8K + t * 16;
+    v[i] = make_uint4(0, 0, 0, 0);
+    if (m < M && k < K) v[i] = *reinterpret_cast<const uint4*>(x + m * ld_x + k);
+  }
+#pragma unroll
+  for (int i = 0; i < kConvertTiles; ++i) {
+    if (k0 + i >= kb) break;
+    uint4 a, b;
+    w8_unpack(v[i].x ^ kW8Bias, a.x, a.y), w8_unpack(v[i].y ^ kW8Bias, a.z, a.w);
+    w8_unpack(v[i].z ^ kW8Bias, b.x, b.y), w8_unpack(v[i].w ^ kW8Bias, b.z, b.w);
+    uint8_t* tile = x16 + ((int64_t)(k0 + i) * groups + group) * 1024 + r * 128;
+    *reinterpret_cast<uint4*>(tile + ((2 * t) ^ r) * 16) = a;
+    *reinterpret_cast<uint4*>(tile + ((2 * t + 1) ^ r) * 16) = b;
+  }
+}
+
+int tile_tokens(int M, int* n_tok) {
+  *n_tok = (M + kMaxTokens - 1) / kMaxTokens;
+  return ((M + *n_tok - 1) / *n_tok + 15) / 16 * 16;
+}
+
+size_t part_bytes(const spear_w8_s* h) { return (size_t)(h->sm_count / 2) * 2 * 2 * kMaxTokens * 128 * sizeof(float); }
+
+}  // namespace
+
+size_t w8_prefill_counters(const spear_w8_s* h) { return (size_t)h->sm_count * 8; }
+
+// Parts of shared tiles, then the tokens in f16 (of whole token tiles).
+size_t w8_prefill_workspace(const spear_w8_s* h) {
+  if (h->max_tokens <= kW8DecodeTokens) return 0;
+  return part_bytes(h) + (size_t)h->kb * 128 * ((size_t)h->max_tokens + kMaxTokens);
+}
+
+spear_status_t w8_launch_prefill(const spear_w8_s* h, const W8Call& c, cudaStream_t stream) {
+  GemmParams p = {};
+  p.w = h->w, p.x16 = reinterpret_cast<uint8_t*>(h->part) + part_bytes(h), p.w_scales = h->w_scales, p.x_scales = c.x_scales;
+  p.y = c.y, p.ld_y = c.ld_y, p.part = h->part, p.counters = h->gemm_counters, p.status = h->status;
+  p.type = c.type, p.M = c.M, p.N = h->N, p.kb = h->kb, p.act = h->act, p.w_tiles = h->strips / kW8Tile;
+  p.pairs_ok = (reinterpret_cast<uintptr_t>(c.y) & 3) == 0 && (c.ld_y % 2 == 0 || c.M == 1);
+  p.TN = tile_tokens(c.M, &p.n_tok);
+  p.groups = p.n_tok * p.TN / 8;
+  p.acc_stride = (p.TN + 31) / 32 * 32;
+  p.slots = std::min(kMaxSlots, (512 - 2 * p.acc_stride) / 32);
+  p.stage_bytes = kRawBytes + p.TN * 64;
+  p.stages = std::min(kMaxStages, kSmemBudget / p.stage_bytes);
+  const size_t smem = std::max((size_t)p.stages * p.stage_bytes + sizeof(Shared) + 1024, (size_t)120 * 1024);  // one CTA an SM
+
+  const int pairs = h->sm_count / 2;
+  p.tiles = (p.w_tiles + 1) / 2 * p.n_tok;
+  // Tiles that do not fill the pairs evenly are split along K, together with one round of whole ones, so that every
+  // pair gets as much; adding the parts takes about as long as a dozen blocks of a tile.
+  const int over = p.tiles % pairs;
+  p.sk_pairs = pairs;
+  if (over && (int64_t)p.kb * (pairs - over) / pairs > 12) {
+    p.sk_tiles = p.tiles < pairs ? p.tiles : over + pairs;
+    const int64_t units = (int64_t)p.sk_tiles * p.kb;
+    if (p.tiles < pairs) p.sk_pairs = (int)std::min<int64_t>(pairs, std::max<int64_t>(p.tiles, units / 8));
+  }
+  const int grid = 2 * std::min(pairs, std::max(p.sk_tiles ? p.sk_pairs : 0, p.tiles - p.sk_tiles));
+
+  const void* kernel = h->gated ? reinterpret_cast<const void*>(&gemm_kernel<true>) : reinterpret_cast<const void*>(&gemm_kernel<false>);
+  static std::atomic<uint64_t> configured[2];
+  if (smem_limit_once(kernel, configured[h->gated]) != cudaSuccess) return SPEAR_ERR_CUDA;
+  const dim3 cgrid(p.groups, (h->kb + 8 * kConvertTiles - 1) / (8 * kConvertTiles));
+  const spear_status_t st = kv_launch(convert_kernel, cgrid, 256, 0, stream, c.x, c.ld_x, c.M, h->K, h->kb, p.groups,
+                                      const_cast<uint8_t*>(p.x16));
+  if (st != SPEAR_OK) return st;
+  return h->gated ? kv_launch(gemm_kernel<true>, dim3(grid), kThreads, smem, stream, p)
+                  : kv_launch(gemm_kernel<false>, dim3(grid), kThreads, smem, stream, p);
+}
+
+}  // namespace spear
