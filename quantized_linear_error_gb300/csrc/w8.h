@@ -27,7 +27,7 @@ struct spear_w8_s {
   int device, sm_count;
   int K, N;            // N outputs
   int gated, act;      // act: spear_act_t
-  int strips, kb;      // strips of 16 weight rows (whole tiles), blocks of 64 channels
+  int strips, kb;      // strips of 16 weight rows (whole tiles), blocks of 64 channels (an even number)
   int max_tokens;
   uint8_t* w;          // strips * kb blocks
   float* w_scales;     // [strips * 16], in the strips' row order

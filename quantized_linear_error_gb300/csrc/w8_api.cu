@@ -61,7 +61,7 @@ extern "C" spear_status_t spear_w8_create(const spear_w8_desc_t* d, cudaStream_t
   spear_w8_s* h = new (std::nothrow) spear_w8_s();
   if (!h) return SPEAR_ERR_OOM;
   h->K = d->K, h->N = d->N, h->gated = gated, h->act = d->activation, h->max_tokens = d->max_tokens;
-  h->kb = (d->K + kW8K - 1) / kW8K;
+  h->kb = (d->K + 2 * kW8K - 1) / (2 * kW8K) * 2;
   h->strips = (gated ? (d->N + 7) / 8 : (d->N + 15) / 16);
   h->strips = (h->strips + kW8Tile - 1) / kW8Tile * kW8Tile;
   if ((int64_t)h->strips * h->kb > 1 << 30) {  // block numbers are 32-bit

@@ -8,25 +8,34 @@
 // is bound by it (2 M N K operations).
 //
 // A small kernel turns the tokens' codes into f16 tiles in the order that the
-// tensor cores read (64 channels x 8 tokens, 1 KB, 128-byte swizzle), so that a
-// stage's tokens are one bulk copy; every row tile reads them again, from L2.
-// The weights stay in 8 bits until they reach the SM.
+// tensor cores read (64 channels x 8 tokens, 1 KB, 128-byte swizzle) and the
+// copies run through, so that a stage's tokens are one bulk copy; every row tile
+// reads them again, from L2. The weights stay in 8 bits until they reach the SM.
 //
 // A pair of CTAs (a cluster, cta_group::2) works on 256 weight rows x TN tokens:
 // each CTA holds 128 of the rows and half of the tokens, and the MMAs read both
 // halves of the tokens, which halves the shared memory traffic of a single CTA's
-// tile. Roles of a CTA:
-//   warp 0       copies: 8 KB of codes (128 rows x 64 channels) and TN / 2 tokens a stage
+// tile. A stage is 128 channels. Roles of a CTA:
+//   warp 0       copies the weights' codes, 16 KB a stage
 //   warp 1       issues the MMAs of the pair (in the first CTA): A from tensor
 //                memory, B from both CTAs' shared memory
-//   warps 2-9    codes -> f16 -> tensor memory: two warps 32 rows, half the channels each
+//   warps 2-9    codes -> f16 -> tensor memory: two warps 32 rows, 64 channels each
 //   warps 10-13  epilogue, from the accumulator that the MMAs have left, while they
 //                fill the other one
+//   warp 14      copies the tokens, TN / 2 of them a stage
+// What each role does a stage is fixed cost next to the MMAs' 4 TN cycles: with 64
+// channels a stage and one thread for both copies, a stage took 530 cycles of
+// that thread, 350 of the dequantising warps and 325 of the issuing one.
 //
 // Work is split in whole tiles as long as they fill all pairs; what does not come
 // out even is split along K. Parts of a tile that several pairs share are added by
 // the last one to finish, in the pairs' order, so that a repeated call gives the
 // same bits and nobody waits for another pair.
+//
+// Barriers between the CTAs of a pair order tensor memory and shared memory that
+// copies have filled, each with the tcgen05 fences or by the copies' own
+// completion; no ordinary memory goes through them, so that the arrivals need no
+// wider scope than they have (cluster scope on both sides: 4 times the time).
 #include <algorithm>
 
 #include "tcgen05.cuh"
@@ -36,10 +45,10 @@ namespace spear {
 namespace {
 
 constexpr uint64_t kWaitNs = 100000000ull;
-constexpr int kThreads = 14 * 32;
-constexpr int kRawBytes = kW8Tile * kW8Block;  // 128 rows x 64 channels
-constexpr int kMaxTokens = 192;                // of a tile: two accumulators and four A slots in 512 columns
-constexpr int kMaxStages = 16, kMaxSlots = 8;
+constexpr int kThreads = 15 * 32;
+constexpr int kRawBytes = 2 * kW8Tile * kW8Block;  // 128 rows x 128 channels
+constexpr int kMaxTokens = 192;                    // of a tile: two accumulators and two A slots in 512 columns
+constexpr int kMaxStages = 8, kMaxSlots = 4;
 constexpr int kSmemBudget = 222 * 1024;
 
 struct GemmParams {
@@ -50,8 +59,8 @@ struct GemmParams {
   float* part;
   unsigned *counters, *status;
   int type, pairs_ok;     // pairs_ok: 16-bit results may be stored two at a time
-  int M, N, kb, act, w_tiles;
-  int TN, n_tok, groups;  // tokens of a tile, token tiles, groups of 8 tokens in x16
+  int M, N, ks, act, w_tiles;  // ks: stages of a tile
+  int TN, n_tok;               // tokens of a tile, token tiles
   int tiles, sk_tiles, sk_pairs;  // tiles in all; those split along K, over that many pairs
   int stages, slots, stage_bytes, acc_stride;
 };
@@ -64,7 +73,7 @@ struct Segment {
 struct Segments {
   int u, end, next, step;
   SPEAR_DEVINL Segments(const GemmParams& p, int pair, int pairs) {
-    const int64_t units = (int64_t)p.sk_tiles * p.kb;
+    const int64_t units = (int64_t)p.sk_tiles * p.ks;
     u = pair < p.sk_pairs ? (int)(pair * units / p.sk_pairs) : 0;
     end = pair < p.sk_pairs ? (int)((pair + 1) * units / p.sk_pairs) : 0;
     next = p.sk_tiles + pair;
@@ -72,14 +81,14 @@ struct Segments {
   }
   SPEAR_DEVINL bool get(const GemmParams& p, Segment& s) {
     if (u < end) {
-      s.tile = u / p.kb;
-      s.k0 = u - s.tile * p.kb;
-      s.k1 = min(p.kb, s.k0 + end - u);
+      s.tile = u / p.ks;
+      s.k0 = u - s.tile * p.ks;
+      s.k1 = min(p.ks, s.k0 + end - u);
       u += s.k1 - s.k0;
       return true;
     }
     if (next >= p.tiles) return false;
-    s.tile = next, s.k0 = 0, s.k1 = p.kb;
+    s.tile = next, s.k0 = 0, s.k1 = p.ks;
     next += step;
     return true;
   }
@@ -94,34 +103,40 @@ SPEAR_DEVINL void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release;" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
-// Arrive on the first CTA's barrier at the same place.
-SPEAR_DEVINL void mbar_arrive_leader(uint64_t* bar) {
-  asm volatile(
-      "{\n\t.reg .b32 a;\n\t"
-      "mapa.shared::cluster.u32 a, %0, 0;\n\t"
-      "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n\t}" ::"r"(smem_u32(bar))
-      : "memory");
+// Address of the first CTA's barrier at the same place, and an arrival on it.
+SPEAR_DEVINL uint32_t leader_bar(uint64_t* bar) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_u32(bar)));
+  return r;
 }
-SPEAR_DEVINL bool mbar_try_wait_cluster(uint64_t* bar, unsigned parity) {
+SPEAR_DEVINL void mbar_arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+SPEAR_DEVINL bool mbar_test(uint32_t bar, unsigned parity) {
   uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
+      : "r"(bar), "r"(parity)
       : "memory");
   return ok != 0;
 }
-// Bounded, the same for the whole warp.
-SPEAR_DEVINL bool wait_cluster(uint64_t* bar, unsigned parity) {
-  bool ok = mbar_try_wait_cluster(bar, parity);
-  if (!__all_sync(0xffffffffu, ok)) {
-    const uint64_t t0 = globaltimer();
-    while (!(ok = mbar_try_wait_cluster(bar, parity)) && globaltimer() - t0 <= kWaitNs) {
-    }
-  }
-  return __all_sync(0xffffffffu, ok);
+// Bounded wait of a whole warp; most phases are over when they are asked for, which a test shows sooner than a try.
+SPEAR_DEVINL bool wait_bar(uint64_t* bar, unsigned parity) {
+  if (__all_sync(0xffffffffu, mbar_test(smem_u32(bar), parity))) return true;
+  return warp_wait(bar, parity, kWaitNs, 0);
+}
+// By the elected lane of a warp whose control flow is uniform.
+SPEAR_DEVINL void expect_and_copy(uint32_t leader, uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %4, 0;\n\t"
+      "@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%3], %2;\n\t"
+      "@q cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n\t}" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(bar), "r"(leader)
+      : "memory");
 }
 
 SPEAR_DEVINL void umma2_ts(uint32_t leader, uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
@@ -240,7 +255,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_ke
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.stages; ++s) {
-      mbar_init(&sh.raw[s], 1);
+      mbar_init(&sh.raw[s], 2);
       mbar_init(&sh.a[s], 16);
       mbar_init(&sh.empty[s], 1);
     }
@@ -260,60 +275,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_ke
   tc_fence_after_sync();
   const uint32_t tmem = sh.tmem;
   const uint32_t a_base = tmem + 2 * p.acc_stride;
-  const int b_bytes = p.TN * 64;
+  const int b_bytes = p.TN * 128;  // half the tokens x 128 channels
 
   Segments segs(p, pair, pairs);
   Segment sg;
   bool ok = true;
-  if (warp == 0) {
-    if (lane == 0) {
-      int s = 0, issued = 0;
-      unsigned phase = 1;  // the first pass through the ring finds every stage empty
-      bool waited = false;
-      // the handle's own weights go out ahead of the tokens, which the kernel before this one writes
-      int held = 0;
-      const uint8_t* held_b[kMaxStages];
-      auto flush = [&] {
-        grid_wait();
-        waited = true;
-        for (int i = 0; i < held; ++i) bulk_g2s(smem + i * p.stage_bytes, held_b[i], b_bytes, &sh.raw[i]);
-      };
-      while (ok && segs.get(p, sg)) {
-        const int row = sg.tile / p.n_tok, tok = sg.tile - row * p.n_tok;
-        const uint8_t* w = p.w + ((int64_t)min(row * 2 + rank, p.w_tiles - 1) * p.kb + sg.k0) * kRawBytes;
-        const uint8_t* b = p.x16 + ((int64_t)sg.k0 * p.groups + (tok * p.TN + rank * (p.TN / 2)) / 8) * 1024;
-        for (int k = sg.k0; k < sg.k1; ++k) {
-          if (issued >= p.stages) {
-            if (!waited) flush();
-            if (!mbar_wait_bounded(&sh.empty[s], phase, kWaitNs)) {
-              ok = false;
-              break;
-            }
-          }
-          mbar_arrive_expect_tx(&sh.raw[s], kRawBytes + b_bytes);
-          uint8_t* at = smem + s * p.stage_bytes;
-          bulk_g2s(at + b_bytes, w, kRawBytes, &sh.raw[s]);
-          if (waited) bulk_g2s(at, b, b_bytes, &sh.raw[s]);
-          else held_b[held++] = b;
-          w += kRawBytes, b += (int64_t)p.groups * 1024;
-          ++issued;
-          if (++s == p.stages) s = 0, phase ^= 1;
-        }
-      }
-      if (!waited) flush();
-      // every stage's MMAs have run before the CTA may leave (or, given up, its copies have landed)
-      const int left = min(issued, p.stages);
-      if (!ok) atomicOr(p.status, kStatusTimeoutPipe);
-      for (int i = 0; i < left; ++i) {
-        if (issued < p.stages) s = i;
-        const unsigned use = issued < p.stages ? 0 : phase;
-        if (ok) ok = mbar_wait_bounded(&sh.empty[s], use, kWaitNs);
-        else mbar_wait_bounded(&sh.raw[s], use, kWaitNs / 10);
+  if (warp == 0 || warp == 14) {
+    // Copies: the handle's own weights ahead of the kernel before this one, the tokens' tiles behind it.
+    const bool tokens = warp == 14;
+    if (tokens) grid_wait();
+    const uint32_t leader = elect_leader();
+    const uint32_t bytes = tokens ? b_bytes : kRawBytes;
+    const uint32_t dst = smem_u32(smem) + (tokens ? 0 : b_bytes);
+    int s = 0, issued = 0;
+    unsigned phase = 1;  // the first pass through the ring finds every stage empty
+    while (ok && segs.get(p, sg)) {
+      const int row = sg.tile / p.n_tok, tok = sg.tile - row * p.n_tok;
+      const uint8_t* src = tokens ? p.x16 + (int64_t)(tok * 2 + rank) * p.ks * b_bytes
+                                  : p.w + (int64_t)min(row * 2 + rank, p.w_tiles - 1) * p.ks * kRawBytes;
+      src += (int64_t)sg.k0 * bytes;
+      for (int k = sg.k0; k < sg.k1; ++k) {
+        ok = wait_bar(&sh.empty[s], phase);
+        if (!ok) break;
+        expect_and_copy(leader, dst + s * p.stage_bytes, src, bytes, smem_u32(&sh.raw[s]));
+        src += bytes;
+        ++issued;
         if (++s == p.stages) s = 0, phase ^= 1;
       }
-    } else {
-      grid_wait();
     }
+    if (!ok && lane == 0) atomicOr(p.status, kStatusTimeoutPipe);
+    // every stage's MMAs have run before the CTA may leave (or, given up, its copies have landed)
+    const int left = min(issued, p.stages);
+    if (issued < p.stages) s = 0, phase = 0;
+    for (int i = 0; i < left; ++i) {
+      if (ok) ok = wait_bar(&sh.empty[s], phase);
+      else warp_wait(&sh.raw[s], phase, kWaitNs / 10, 0);
+      if (++s == p.stages) s = 0, phase ^= 1;
+    }
+    if (!tokens) grid_wait();
   } else if (warp == 1) {
     if (rank == 0) {
       const uint32_t leader = elect_leader();
@@ -321,18 +320,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_ke
       int s = 0, slot = 0, buf = 0;
       unsigned phase = 0, acc_phase = 1;
       while (ok && segs.get(p, sg)) {
-        ok = wait_cluster(&sh.acc_empty[buf], acc_phase);
+        ok = wait_bar(&sh.acc_empty[buf], acc_phase);
         if (!ok) break;
         tc_fence_after_sync();
         const uint32_t d = tmem + buf * p.acc_stride;
         for (int k = sg.k0; k < sg.k1; ++k) {
-          ok = wait_cluster(&sh.a[s], phase);
+          ok = wait_bar(&sh.a[s], phase);
           if (!ok) break;
           tc_fence_after_sync();
           const uint64_t desc = sw128_kmajor_desc(smem_u32(smem + s * p.stage_bytes));
-          const uint32_t a = a_base + slot * 32;
+          const uint64_t desc2 = desc + (p.TN * 64 >> 4);  // the second 64 channels
+          const uint32_t a = a_base + slot * 64;
 #pragma unroll
           for (int i = 0; i < 4; ++i) umma2_ts(leader, d, a + 8 * i, desc + 2 * i, idesc, k > sg.k0 || i > 0);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) umma2_ts(leader, d, a + 32 + 8 * i, desc2 + 2 * i, idesc, 1);
           umma2_commit(leader, &sh.empty[s]);
           if (++s == p.stages) s = 0, phase ^= 1;
           if (++slot == p.slots) slot = 0;
@@ -347,33 +349,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_ke
   } else if (warp < 10) {
     const int quarter = warp & 3, half = (warp - 2) >> 2;
     const int r = 32 * quarter + lane;
-    const uint32_t at0 = (uint32_t)((r >> 4) * kW8Block + w8_place(r & 15, 2 * half) * 16);
-    const uint32_t at1 = (uint32_t)((r >> 4) * kW8Block + w8_place(r & 15, 2 * half + 1) * 16);
-    const uint32_t dst = a_base + ((uint32_t)(32 * quarter) << 16) + 16 * half;
-    const uint32_t base = smem_u32(smem) + b_bytes;
-    int s = 0, slot = 0, done = 0, es = 0;  // es: stage of the block whose MMAs free the slot
+    const uint32_t base = smem_u32(smem) + b_bytes + half * (kRawBytes / 2) + (r >> 4) * kW8Block;
+    uint32_t at[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) at[t] = base + w8_place(r & 15, t) * 16;
+    const uint32_t dst = a_base + ((uint32_t)(32 * quarter) << 16) + 32 * half;
+    const uint32_t full = leader_bar(&sh.a[0]);
+    int s = 0, slot = 0, done = 0, es = 0;  // es: the stage whose MMAs free the slot
     unsigned phase = 0, e_phase = 0;
     while (ok && segs.get(p, sg)) {
       for (int k = sg.k0; k < sg.k1; ++k) {
-        ok = warp_wait(&sh.raw[s], phase, kWaitNs, 0);
+        ok = wait_bar(&sh.raw[s], phase);
         if (!ok) break;
-        const uint4 v0 = lds128(base + s * p.stage_bytes + at0), v1 = lds128(base + s * p.stage_bytes + at1);
-        uint32_t f[16];
-        w8_unpack(v0.x, f[0], f[1]), w8_unpack(v0.y, f[2], f[3]), w8_unpack(v0.z, f[4], f[5]), w8_unpack(v0.w, f[6], f[7]);
-        w8_unpack(v1.x, f[8], f[9]), w8_unpack(v1.y, f[10], f[11]), w8_unpack(v1.z, f[12], f[13]), w8_unpack(v1.w, f[14], f[15]);
+        uint32_t f[32];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const uint4 v = lds128(at[t] + s * p.stage_bytes);
+          w8_unpack(v.x, f[8 * t], f[8 * t + 1]), w8_unpack(v.y, f[8 * t + 2], f[8 * t + 3]);
+          w8_unpack(v.z, f[8 * t + 4], f[8 * t + 5]), w8_unpack(v.w, f[8 * t + 6], f[8 * t + 7]);
+        }
         if (done >= p.slots) {
-          ok = wait_cluster(&sh.empty[es], e_phase);
+          ok = wait_bar(&sh.empty[es], e_phase);
           if (!ok) break;
           tc_fence_after_sync();
           if (++es == p.stages) es = 0, e_phase ^= 1;
         } else {
           ++done;
         }
-        tmem_st_x16(dst + slot * 32, f);
+        tmem_st_x32(dst + slot * 64, f);
         tmem_st_wait();
         tc_fence_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive_leader(&sh.a[s]);
+        if (lane == 0) mbar_arrive_cluster(full + 8 * s);
         if (++s == p.stages) s = 0, phase ^= 1;
         if (++slot == p.slots) slot = 0;
       }
@@ -383,76 +390,101 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_ke
   } else {
     grid_wait();  // the tokens' scales, and what the kernel before this one may still read of y
     const int quarter = warp & 3;
+    const uint32_t emptied = leader_bar(&sh.acc_empty[0]);
+    const int64_t units = (int64_t)p.sk_tiles * p.ks, part_floats = (int64_t)p.TN * 128;
     int buf = 0;
     unsigned phase = 0;
     while (segs.get(p, sg)) {
       const int row = sg.tile / p.n_tok, tok = sg.tile - row * p.n_tok;
       const int row0 = (row * 2 + rank) * 128 + 32 * quarter;
-      const bool whole = sg.k0 == 0 && sg.k1 == p.kb;
       const bool rows = row0 < p.w_tiles * 128;
       const Epilogue<kGated> out{p, lane, row0, rows ? p.w_scales[row0 + lane] : 0.f};
-      ok = wait_cluster(&sh.acc_full[buf], phase);
+      auto scale_of = [&](int c) {
+        const int m = tok * p.TN + c + (lane & 15);
+        return m < p.M ? p.x_scales[m] : 0.f;
+      };
+      ok = wait_bar(&sh.acc_full[buf], phase);
       if (!ok) break;
       tc_fence_after_sync();
       const uint32_t acc = tmem + buf * p.acc_stride + ((uint32_t)(32 * quarter) << 16);
-      const int64_t tile_floats = (int64_t)p.TN * 128;
-      // parts: [pair][0 or 1][rank][token][row]; a pair's part is number 1 if the pair starts inside the tile
-      auto part_of = [&](int c) {
-        const int64_t units = (int64_t)p.sk_tiles * p.kb;
-        const int first = c * units / p.sk_pairs >= (int64_t)sg.tile * p.kb ? 1 : 0;
-        return p.part + ((int64_t)(2 * c + first) * 2 + rank) * tile_floats + 32 * quarter + lane;
+      auto release = [&] {
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(emptied + 8 * buf);
+        if ((buf ^= 1) == 0) phase ^= 1;
       };
-      float* mine = whole ? nullptr : part_of(pair);
-      for (int c = 0; c < p.TN; c += 16) {
-        uint32_t v[16];
-        tmem_ld_x16(acc + c, v);
-        tmem_ld_wait();
-        if (whole) {
-          const int m0 = tok * p.TN + c, mj = m0 + (lane & 15);
-          const float sx = mj < p.M ? p.x_scales[mj] : 0.f;
-          float f[16];
-#pragma unroll
-          for (int j = 0; j < 16; ++j) f[j] = __uint_as_float(v[j]);
-          out.columns(f, m0, sx);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 16; ++j) mine[(int64_t)(c + j) * 128] = __uint_as_float(v[j]);
+      if (sg.k0 == 0 && sg.k1 == p.ks) {
+        for (int c = 0; c < p.TN; c += 16) {
+          float v[16];
+          tmem_ld_x16(acc + c, reinterpret_cast<uint32_t(&)[16]>(v));
+          const float sx = scale_of(c);
+          tmem_ld_wait();
+          out.columns(v, tok * p.TN + c, sx);
         }
+        release();
+        continue;
       }
-      tc_fence_before_sync();
-      if (!whole) __threadfence();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_leader(&sh.acc_empty[buf]);
-      if ((buf ^= 1) == 0) phase ^= 1;
-      if (whole) continue;
-      // the pairs that share the tile: from the one with its first block to the one with its last
-      const int64_t units = (int64_t)p.sk_tiles * p.kb;
-      const int64_t t0 = (int64_t)sg.tile * p.kb, t1 = t0 + p.kb;
+      // The pairs that share the tile: from the one with its first stage to the one with its last. A pair's part
+      // [token][row] is its number 1 if the pair starts inside the tile, else 0.
+      const int64_t t0 = (int64_t)sg.tile * p.ks, t1 = t0 + p.ks;
       int c0 = pair, c1 = pair;
       while (c0 * units / p.sk_pairs > t0) --c0;
       while ((c1 + 1) * units / p.sk_pairs < t1) ++c1;
-      unsigned last = 0;
-      if (lane == 0) {
-        unsigned* counter = p.counters + (sg.tile * 2 + rank) * 4 + quarter;
-        last = atomicAdd(counter, 1u) == (unsigned)(c1 - c0);
-        if (last) *counter = 0;
-      }
-      if (!__shfl_sync(0xffffffffu, last, 0)) continue;
-      __threadfence();
-      for (int c = 0; c < p.TN; c += 16) {
-        float f[16];
+      auto part_of = [&](int q) {
+        const int first = q * units / p.sk_pairs >= t0 ? 1 : 0;
+        return p.part + ((int64_t)(2 * q + first) * 2 + rank) * part_floats + 32 * quarter + lane;
+      };
+      unsigned* counter = p.counters + (sg.tile * 2 + rank) * 4 + quarter;
+      const unsigned others = c1 - c0;
+      // All others have left their parts: this one need not go through memory.
+      bool held = __shfl_sync(0xffffffffu, ld_acquire_gpu(counter), 0) == others, last = held;
+      if (!held) {
+        float* mine = part_of(pair);
+        for (int c = 0; c < p.TN; c += 32) {
+          uint32_t v[32];
+          tmem_ld_x32(acc + c, v);  // of the next accumulator, or the A slots, past TN: not stored
+          tmem_ld_wait();
 #pragma unroll
-        for (int j = 0; j < 16; ++j) f[j] = 0.f;
-        for (int q = c0; q <= c1; ++q) {
-          const float* from = part_of(q) + (int64_t)c * 128;
-          float g[16];
-#pragma unroll
-          for (int j = 0; j < 16; ++j) g[j] = __ldcg(from + j * 128);
-#pragma unroll
-          for (int j = 0; j < 16; ++j) f[j] += g[j];
+          for (int j = 0; j < 32; ++j)
+            if (c + j < p.TN) mine[(c + j) * 128] = __uint_as_float(v[j]);
         }
-        const int m0 = tok * p.TN + c, mj = m0 + (lane & 15);
-        out.columns(f, m0, mj < p.M ? p.x_scales[mj] : 0.f);
+        __threadfence();
+        release();
+        unsigned n = 0;
+        if (lane == 0) n = atomicAdd(counter, 1u);
+        last = __shfl_sync(0xffffffffu, n, 0) == others;
+      }
+      if (last) {
+        __threadfence();
+        if (lane == 0) *counter = 0;
+        constexpr int kAtOnce = 3;
+        for (int c = 0; c < p.TN; c += 16) {
+          float v[16], f[16];
+          if (held) tmem_ld_x16(acc + c, reinterpret_cast<uint32_t(&)[16]>(v));
+          const float sx = scale_of(c);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) f[j] = 0.f;
+          for (int q = c0; q <= c1; q += kAtOnce) {
+            float g[kAtOnce][16];
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i) {
+              if (q + i > c1 || (held && q + i == pair)) continue;
+              const float* from = part_of(q + i) + c * 128;
+#pragma unroll
+              for (int j = 0; j < 16; ++j) g[i][j] = __ldcg(from + j * 128);
+            }
+            if (held) tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i) {
+              if (q + i > c1) continue;
+              const bool own = held && q + i == pair;
+#pragma unroll
+              for (int j = 0; j < 16; ++j) f[j] += own ? v[j] : g[i][j];
+            }
+          }
+          out.columns(f, tok * p.TN + c, sx);
+        }
+        if (held) release();
       }
     }
     if (!ok && lane == 0) atomicOr(p.status, kStatusTimeoutPipe);
@@ -467,15 +499,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_ke
   }
 }
 
-// Tokens' codes -> f16 tiles [k block][8 tokens][1 KB]: a warp a tile, lane 4 r + t the 16 channels 16 t .. of token r.
-// The order of channels within 16 is that of w8_unpack, as for the weights. Tokens past M and channels past K are zeros.
+// Tokens' codes -> f16 tiles of 8 tokens x 64 channels (1 KB), ordered [half of a token tile][k block][tile of the
+// half]: a warp a tile, lane 4 r + t the 16 channels 16 t .. of token r. The order of channels within 16 is that of
+// w8_unpack, as for the weights. Tokens past M and channels past K are zeros.
 constexpr int kConvertTiles = 4;  // k blocks a warp
 __global__ void __launch_bounds__(256) convert_kernel(const int8_t* __restrict__ x, int64_t ld_x, int M, int K, int kb,
-                                                      int groups, uint8_t* __restrict__ x16) {
+                                                      int half_groups, uint8_t* __restrict__ x16) {
   kv_follow();
   const int lane = threadIdx.x & 31, r = lane >> 2, t = lane & 3;
   const int group = blockIdx.x, k0 = (blockIdx.y * 8 + threadIdx.x / 32) * kConvertTiles;
-  const int m = group * 8 + r;
+  const int half = group / half_groups, m = group * 8 + r;
   uint4 v[kConvertTiles];
 #pragma unroll
   for (int i = 0; i < kConvertTiles; ++i) {
@@ -489,7 +522,7 @@ __global__ void __launch_bounds__(256) convert_kernel(const int8_t* __restrict__
     uint4 a, b;
     w8_unpack(v[i].x ^ kW8Bias, a.x, a.y), w8_unpack(v[i].y ^ kW8Bias, a.z, a.w);
     w8_unpack(v[i].z ^ kW8Bias, b.x, b.y), w8_unpack(v[i].w ^ kW8Bias, b.z, b.w);
-    uint8_t* tile = x16 + ((int64_t)(k0 + i) * groups + group) * 1024 + r * 128;
+    uint8_t* tile = x16 + (((int64_t)half * kb + k0 + i) * half_groups + (group - half * half_groups)) * 1024 + r * 128;
     *reinterpret_cast<uint4*>(tile + ((2 * t) ^ r) * 16) = a;
     *reinterpret_cast<uint4*>(tile + ((2 * t + 1) ^ r) * 16) = b;
   }
@@ -502,6 +535,9 @@ int tile_tokens(int M, int* n_tok) {
 
 size_t part_bytes(const spear_w8_s* h) { return (size_t)(h->sm_count / 2) * 2 * 2 * kMaxTokens * 128 * sizeof(float); }
 
+// Room for whole token tiles: 16 n_tok tokens more than M at most.
+size_t x16_tokens(const spear_w8_s* h) { return (size_t)h->max_tokens + h->max_tokens / 8 + 256; }
+
 }  // namespace
 
 size_t w8_prefill_counters(const spear_w8_s* h) { return (size_t)h->sm_count * 8; }
@@ -509,20 +545,19 @@ size_t w8_prefill_counters(const spear_w8_s* h) { return (size_t)h->sm_count * 8
 // Parts of shared tiles, then the tokens in f16 (of whole token tiles).
 size_t w8_prefill_workspace(const spear_w8_s* h) {
   if (h->max_tokens <= kW8DecodeTokens) return 0;
-  return part_bytes(h) + (size_t)h->kb * 128 * ((size_t)h->max_tokens + kMaxTokens);
+  return part_bytes(h) + (size_t)h->kb * 128 * x16_tokens(h);
 }
 
 spear_status_t w8_launch_prefill(const spear_w8_s* h, const W8Call& c, cudaStream_t stream) {
   GemmParams p = {};
   p.w = h->w, p.x16 = reinterpret_cast<uint8_t*>(h->part) + part_bytes(h), p.w_scales = h->w_scales, p.x_scales = c.x_scales;
   p.y = c.y, p.ld_y = c.ld_y, p.part = h->part, p.counters = h->gemm_counters, p.status = h->status;
-  p.type = c.type, p.M = c.M, p.N = h->N, p.kb = h->kb, p.act = h->act, p.w_tiles = h->strips / kW8Tile;
+  p.type = c.type, p.M = c.M, p.N = h->N, p.ks = h->kb / 2, p.act = h->act, p.w_tiles = h->strips / kW8Tile;
   p.pairs_ok = (reinterpret_cast<uintptr_t>(c.y) & 3) == 0 && (c.ld_y % 2 == 0 || c.M == 1);
   p.TN = tile_tokens(c.M, &p.n_tok);
-  p.groups = p.n_tok * p.TN / 8;
   p.acc_stride = (p.TN + 31) / 32 * 32;
-  p.slots = std::min(kMaxSlots, (512 - 2 * p.acc_stride) / 32);
-  p.stage_bytes = kRawBytes + p.TN * 64;
+  p.slots = std::min(kMaxSlots, (512 - 2 * p.acc_stride) / 64);
+  p.stage_bytes = kRawBytes + p.TN * 128;
   p.stages = std::min(kMaxStages, kSmemBudget / p.stage_bytes);
   const size_t smem = std::max((size_t)p.stages * p.stage_bytes + sizeof(Shared) + 1024, (size_t)120 * 1024);  // one CTA an SM
 
@@ -532,18 +567,19 @@ spear_status_t w8_launch_prefill(const spear_w8_s* h, const W8Call& c, cudaStrea
   // pair gets as much; adding the parts takes about as long as a dozen blocks of a tile.
   const int over = p.tiles % pairs;
   p.sk_pairs = pairs;
-  if (over && (int64_t)p.kb * (pairs - over) / pairs > 12) {
+  if (over && (int64_t)p.ks * (pairs - over) / pairs > 6) {
     p.sk_tiles = p.tiles < pairs ? p.tiles : over + pairs;
-    const int64_t units = (int64_t)p.sk_tiles * p.kb;
-    if (p.tiles < pairs) p.sk_pairs = (int)std::min<int64_t>(pairs, std::max<int64_t>(p.tiles, units / 8));
+    const int64_t units = (int64_t)p.sk_tiles * p.ks;
+    if (p.tiles < pairs) p.sk_pairs = (int)std::min<int64_t>(pairs, std::max<int64_t>(p.tiles, units / 4));
   }
   const int grid = 2 * std::min(pairs, std::max(p.sk_tiles ? p.sk_pairs : 0, p.tiles - p.sk_tiles));
 
   const void* kernel = h->gated ? reinterpret_cast<const void*>(&gemm_kernel<true>) : reinterpret_cast<const void*>(&gemm_kernel<false>);
   static std::atomic<uint64_t> configured[2];
   if (smem_limit_once(kernel, configured[h->gated]) != cudaSuccess) return SPEAR_ERR_CUDA;
-  const dim3 cgrid(p.groups, (h->kb + 8 * kConvertTiles - 1) / (8 * kConvertTiles));
-  const spear_status_t st = kv_launch(convert_kernel, cgrid, 256, 0, stream, c.x, c.ld_x, c.M, h->K, h->kb, p.groups,
+  const int groups = p.n_tok * p.TN / 8;
+  const dim3 cgrid(groups, (h->kb + 8 * kConvertTiles - 1) / (8 * kConvertTiles));
+  const spear_status_t st = kv_launch(convert_kernel, cgrid, 256, 0, stream, c.x, c.ld_x, c.M, h->K, h->kb, p.TN / 16,
                                       const_cast<uint8_t*>(p.x16));
   if (st != SPEAR_OK) return st;
   return h->gated ? kv_launch(gemm_kernel<true>, dim3(grid), kThreads, smem, stream, p)
