@@ -31,12 +31,14 @@ struct spear_w8_s {
   int max_tokens;
   uint8_t* w;          // strips * kb blocks
   float* w_scales;     // [strips * 16], in the strips' row order
-  void* ws;            // status word, arrival counters, partial sums
+  void* ws;                 // all of the following
   unsigned* status;
-  unsigned* counters;  // [strips], zero between calls
-  unsigned* gemm_counters;  // of the tensor-core kernel's shared tiles, zero between calls
-  float* part;         // sums of work that several CTAs share
-  size_t ws_bytes, control_bytes;  // control: status and counters, cleared at create
+  unsigned* counters;       // [strips], of the few-token kernel's shared rows; zero between calls
+  unsigned* gemm_counters;  // of the tensor-core kernel's shared tiles; zero between calls
+  int* sums;                // their sums; zero between calls
+  float* part;              // sums of the few-token kernel's shared rows
+  uint8_t* x16;             // tokens in f16
+  size_t ws_bytes, zero_bytes;  // the first zero_bytes are cleared at create
 };
 
 struct W8Call {
@@ -57,6 +59,7 @@ spear_status_t sm_count_of_current(int* sms);
 size_t w8_decode_workspace(const spear_w8_s* h);
 size_t w8_prefill_workspace(const spear_w8_s* h);
 size_t w8_prefill_counters(const spear_w8_s* h);
+size_t w8_prefill_sums(const spear_w8_s* h);
 spear_status_t w8_launch_prefill(const spear_w8_s* h, const W8Call& c, cudaStream_t stream);
 spear_status_t w8_launch_decode(const spear_w8_s* h, const W8Call& c, cudaStream_t stream);
 }

@@ -72,19 +72,25 @@ extern "C" spear_status_t spear_w8_create(const spear_w8_desc_t* d, cudaStream_t
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&h->sm_count, cudaDevAttrMultiProcessorCount, h->device);
   const int64_t blocks = (int64_t)h->strips * h->kb;
   const size_t w_bytes = (size_t)blocks * kW8Block, s_bytes = (size_t)h->strips * 16 * 4;
+  size_t sums_at = 0;
   if (e == cudaSuccess) {
-    h->control_bytes = 128 + ((h->strips + w8_prefill_counters(h)) * 4 + 127) / 128 * 128;
-    h->ws_bytes = h->control_bytes + std::max(w8_decode_workspace(h), w8_prefill_workspace(h));
+    const size_t words = 32 + h->strips + w8_prefill_counters(h), sums = (words * 4 + 127) / 128 * 128;
+    h->zero_bytes = sums + w8_prefill_sums(h);
+    h->ws_bytes = h->zero_bytes + w8_decode_workspace(h) + w8_prefill_workspace(h);
+    sums_at = sums;
     e = cudaMalloc(&h->w, w_bytes);
   }
   if (e == cudaSuccess) e = cudaMalloc(&h->w_scales, s_bytes);
   if (e == cudaSuccess) e = cudaMalloc(&h->ws, h->ws_bytes);
   if (e == cudaSuccess) {
+    char* ws = static_cast<char*>(h->ws);
     h->status = static_cast<unsigned*>(h->ws);
     h->counters = h->status + 32;
     h->gemm_counters = h->counters + h->strips;
-    h->part = reinterpret_cast<float*>(static_cast<char*>(h->ws) + h->control_bytes);
-    e = cudaMemsetAsync(h->ws, 0, h->control_bytes, stream);
+    h->sums = reinterpret_cast<int*>(ws + sums_at);
+    h->part = reinterpret_cast<float*>(ws + h->zero_bytes);
+    h->x16 = reinterpret_cast<uint8_t*>(ws + h->zero_bytes + w8_decode_workspace(h));
+    e = cudaMemsetAsync(h->ws, 0, h->zero_bytes, stream);
   }
   if (e == cudaSuccess) {
     const int64_t chunks = blocks * 64;
@@ -140,7 +146,7 @@ extern "C" spear_status_t spear_w8_check(spear_w8_t h, cudaStream_t stream) {
       cudaStreamSynchronize(stream) != cudaSuccess)
     return SPEAR_ERR_CUDA;
   if (status == 0) return SPEAR_OK;
-  if (cudaMemsetAsync(h->ws, 0, h->control_bytes, stream) != cudaSuccess || cudaStreamSynchronize(stream) != cudaSuccess)
+  if (cudaMemsetAsync(h->ws, 0, h->zero_bytes, stream) != cudaSuccess || cudaStreamSynchronize(stream) != cudaSuccess)
     return SPEAR_ERR_CUDA;
   return SPEAR_ERR_TIMEOUT;
 }

@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(NW * 32, 1) stream_kernel(const __grid_constan
         if (m >= p.M || n >= p.N) continue;
         const float sx = p.x_scales[m];
         float v = sum(e) * sx * p.w_scales[row];
-        if (p.gated) v = w8_act(v, p.act) * (sum(e + 64) * sx * p.w_scales[row + 8]);
+        if (p.gated) v = (p.type == SPEAR_F32 ? w8_act<true>(v, p.act) : w8_act<false>(v, p.act)) * (sum(e + 64) * sx * p.w_scales[row + 8]);
         w8_store(p.y, m * p.ld_y + n, p.type, v);
       }
     };

@@ -28,9 +28,11 @@
 // that thread, 350 of the dequantising warps and 325 of the issuing one.
 //
 // Work is split in whole tiles as long as they fill all pairs; what does not come
-// out even is split along K. Parts of a tile that several pairs share are added by
-// the last one to finish, in the pairs' order, so that a repeated call gives the
-// same bits and nobody waits for another pair.
+// out even is split along K. The pairs that share a tile add their parts, as 32-bit
+// integers, in memory: no order of the additions changes the sum, so that a
+// repeated call gives the same bits. The last one to finish takes the sum, adds its
+// own part from tensor memory and leaves zeros; nobody waits for another pair.
+// (fp32 parts, read one after the other by the last pair: 20 us for 128 tokens.)
 //
 // Barriers between the CTAs of a pair order tensor memory and shared memory that
 // copies have filled, each with the tcgen05 fences or by the copies' own
@@ -48,22 +50,36 @@ constexpr uint64_t kWaitNs = 100000000ull;
 constexpr int kThreads = 15 * 32;
 constexpr int kRawBytes = 2 * kW8Tile * kW8Block;  // 128 rows x 128 channels
 constexpr int kMaxTokens = 192;                    // of a tile: two accumulators and two A slots in 512 columns
+constexpr int kSmem = 227 * 1024;
 constexpr int kMaxStages = 8, kMaxSlots = 4;
-constexpr int kSmemBudget = 222 * 1024;
+
 
 struct GemmParams {
   const uint8_t *w, *x16;
   const float *w_scales, *x_scales;
   void* y;
   int64_t ld_y;
-  float* part;
+  int* sums;              // [tile][rank][token][row] of shared tiles, zero between calls
   unsigned *counters, *status;
-  int type, pairs_ok;     // pairs_ok: 16-bit results may be stored two at a time
+  int type, vec;          // vec: 16-bit results may be stored eight at a time
   int M, N, ks, act, w_tiles;  // ks: stages of a tile
   int TN, n_tok;               // tokens of a tile, token tiles
   int tiles, sk_tiles, sk_pairs;  // tiles in all; those split along K, over that many pairs
   int stages, slots, stage_bytes, acc_stride;
 };
+
+// Add `bytes` of 32-bit integers in shared memory to those at dst; waits for such copies by the thread that issued them.
+SPEAR_DEVINL void bulk_add_s32(int* dst, const int* src, uint32_t bytes) {
+  asm volatile("cp.reduce.async.bulk.global.shared::cta.bulk_group.add.s32 [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)),
+               "r"(bytes)
+               : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+template <int N>
+SPEAR_DEVINL void bulk_wait_read() {  // all but N have read their source
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+SPEAR_DEVINL void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 struct Segment {
   int tile, k0, k1;
@@ -161,90 +177,130 @@ SPEAR_DEVINL void umma2_commit(uint32_t leader, uint64_t* bar) {
       : "memory");
 }
 
+// 32 rows x 16 columns of an accumulator: v[8 h + 4 i + e] is row 16 h + lane / 4 + 8 (e / 2), column 8 i + 2 (lane % 4)
+// + e % 2, the fragment of 8 x 8 matrices, so that a store of transposed matrices gives rows of tokens, and both
+// projections of a gated output stand in one lane.
+SPEAR_DEVINL void acc_load(uint32_t taddr, uint32_t (&v)[16]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(v[8 * h]), "=r"(v[8 * h + 1]), "=r"(v[8 * h + 2]), "=r"(v[8 * h + 3]), "=r"(v[8 * h + 4]),
+                   "=r"(v[8 * h + 5]), "=r"(v[8 * h + 6]), "=r"(v[8 * h + 7])
+                 : "r"(taddr + ((uint32_t)(16 * h) << 16)));
+}
+SPEAR_DEVINL void store_transposed(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
+               "r"(d)
+               : "memory");
+}
+
+// What an epilogue warp keeps in shared memory.
+struct EpilogueShared {
+  int sums[2][512];           // two parts of 16 columns on their way, or 16 tokens' results
+  float scales[kMaxTokens];   // of the tile's tokens
+};
+
+// One warp's 32 rows of an accumulator, 16 tokens at a time: scaled, rounded and stored.
+template <bool kGated, bool kF32>
+struct Epilogue {
+  const GemmParams& p;
+  EpilogueShared& sh;
+  int lane, n0;      // n0: first output of the warp's
+  float sw[4];       // scales of the rows lane / 4 + 8 i
+
+  SPEAR_DEVINL Epilogue(const GemmParams& p, EpilogueShared& sh, int lane, int row0, int tok) : p(p), sh(sh), lane(lane) {
+    n0 = kGated ? row0 / 2 : row0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sw[i] = row0 < p.w_tiles * 128 ? p.w_scales[row0 + 8 * i + (lane >> 2)] : 0.f;
+    __syncwarp();
+    for (int c = lane; c < p.TN; c += 32) {
+      const int m = tok * p.TN + c;
+      sh.scales[c] = m < p.M ? p.x_scales[m] : 0.f;
+    }
+    __syncwarp();
+  }
+
+  SPEAR_DEVINL uint32_t pack(float a, float b) const {
+    if (p.type == SPEAR_BF16) return pack_bf16x2(a, b);
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  // Eight neighbouring outputs of token m.
+  SPEAR_DEVINL void store8(uint32_t from, int m, int n) const {
+    if (m >= p.M) return;
+    const uint4 w = lds128(from);
+    uint16_t* y = static_cast<uint16_t*>(p.y) + m * p.ld_y + n;
+    if (p.vec && n + 8 <= p.N) {
+      *reinterpret_cast<uint4*>(y) = w;
+    } else {
+      const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (n + i < p.N) y[i] = (uint16_t)(words[i / 2] >> (16 * (i & 1)));
+    }
+  }
+
+  // Columns c .. c + 15 of the tile, tokens m0 ..
+  SPEAR_DEVINL void columns(float (&v)[16], int c, int m0) const {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float2 sx = *reinterpret_cast<const float2*>(&sh.scales[c + 8 * i + 2 * (lane & 3)]);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float& x = v[8 * h + 4 * i + e];
+          x = x * (e & 1 ? sx.y : sx.x) * sw[2 * h + (e >> 1)];
+        }
+    }
+    if constexpr (kGated) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) v[4 * q + e] = w8_act<kF32>(v[4 * q + e], p.act) * v[4 * q + e + 2];
+    }
+    if constexpr (kF32) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        if (kGated && (j & 2)) continue;
+        const int m = m0 + 4 * (j & 4 ? 2 : 0) + 2 * (lane & 3) + (j & 1);
+        const int n = n0 + (kGated ? 8 * (j >> 3) : 16 * (j >> 3) + 8 * ((j >> 1) & 1)) + (lane >> 2);
+        if (m < p.M && n < p.N) static_cast<float*>(p.y)[m * p.ld_y + n] = v[j];
+      }
+    } else {
+      const uint32_t at = smem_u32(sh.sums);
+      __syncwarp();
+      if constexpr (kGated) {  // 32 bytes a token, 48 apart: no bank conflicts
+        store_transposed(at + (8 * (lane >> 4) + (lane & 7)) * 48 + ((lane >> 3) & 1) * 16, pack(v[0], v[1]), pack(v[8], v[9]),
+                         pack(v[4], v[5]), pack(v[12], v[13]));
+        __syncwarp();
+        store8(at + (lane >> 1) * 48 + (lane & 1) * 16, m0 + (lane >> 1), n0 + (lane & 1) * 8);
+      } else {                 // 64 bytes a token, 80 apart
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          store_transposed(at + (8 * i + (lane & 7)) * 80 + (lane >> 3) * 16, pack(v[4 * i], v[4 * i + 1]),
+                           pack(v[4 * i + 2], v[4 * i + 3]), pack(v[8 + 4 * i], v[8 + 4 * i + 1]),
+                           pack(v[8 + 4 * i + 2], v[8 + 4 * i + 3]));
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          store8(at + (8 * i + (lane >> 2)) * 80 + (lane & 3) * 16, m0 + 8 * i + (lane >> 2), n0 + (lane & 3) * 8);
+      }
+    }
+  }
+};
+
 struct Shared {
   uint64_t raw[kMaxStages];    // a stage's copies have landed (this CTA)
   uint64_t a[kMaxStages];      // its codes stand in tensor memory, in both CTAs (the first CTA's)
   uint64_t empty[kMaxStages];  // its MMAs have run (both CTAs)
   uint64_t acc_full[2];        // an accumulator is complete (both CTAs)
   uint64_t acc_empty[2];       // it has been read, in both CTAs (the first CTA's)
+  alignas(16) EpilogueShared epilogue[4];
   uint32_t tmem;
 };
 
-// One warp's 32 rows of an accumulator: scaled, rounded and stored, or left as a part.
-template <bool kGated>
-struct Epilogue {
-  const GemmParams& p;
-  int lane, row0;        // row0: first weight row of the warp
-  float sw;              // scale of this lane's row
-
-  SPEAR_DEVINL void store16(int m, int n, float v0, float v1, bool both_ok) const {  // n even (if pairs_ok)
-    if (m >= p.M) return;
-    const int64_t at = m * p.ld_y + n;
-    if (both_ok && n + 1 < p.N) {
-      uint32_t w;
-      if (p.type == SPEAR_BF16) w = pack_bf16x2(v0, v1);
-      else {
-        const __half2 h = __floats2half2_rn(v0, v1);
-        memcpy(&w, &h, 4);
-      }
-      *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.y) + at) = w;
-    } else {
-      if (n < p.N) w8_store(p.y, at, p.type, v0);
-      if (n + 1 < p.N) w8_store(p.y, at + 1, p.type, v1);
-    }
-  }
-
-  // v: 16 columns (tokens m0 ..) of this lane's row; sx: lane j holds token m0 + j's scale (j < 16).
-  SPEAR_DEVINL void columns(const float (&v)[16], int m0, float sx) const {
-    if constexpr (kGated) {
-      // lanes l and l + 8 hold an output's two projections: the first takes the even tokens, the second the odd ones
-      const bool up = lane & 8;
-      const int n = row0 / 2 + (lane >> 4) * 8 + (lane & 7);
-      float o[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float a = v[2 * j] * __shfl_sync(0xffffffffu, sx, 2 * j) * sw;
-        const float b = v[2 * j + 1] * __shfl_sync(0xffffffffu, sx, 2 * j + 1) * sw;
-        const float other = __shfl_xor_sync(0xffffffffu, up ? a : b, 8);
-        const float g = up ? other : a, u = up ? b : other;
-        o[j] = w8_act(g, p.act) * u;
-      }
-      const int m = m0 + (up ? 1 : 0);
-      if (p.type == SPEAR_F32) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (m + 2 * j < p.M && n < p.N) static_cast<float*>(p.y)[(m + 2 * j) * p.ld_y + n] = o[j];
-        return;
-      }
-#pragma unroll
-      for (int j = 0; j < 8; j += 2) {  // neighbours trade a token each, so that both store pairs of outputs
-        const float got = __shfl_xor_sync(0xffffffffu, lane & 1 ? o[j] : o[j + 1], 1);
-        if (lane & 1) store16(m + 2 * j + 2, n - 1, got, o[j + 1], p.pairs_ok);
-        else store16(m + 2 * j, n, o[j], got, p.pairs_ok);
-      }
-    } else {
-      const int n = row0 + lane;
-      if (p.type == SPEAR_F32) {
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const float a = v[j] * __shfl_sync(0xffffffffu, sx, j) * sw;
-          if (m0 + j < p.M && n < p.N) static_cast<float*>(p.y)[(m0 + j) * p.ld_y + n] = a;
-        }
-        return;
-      }
-#pragma unroll
-      for (int j = 0; j < 16; j += 2) {
-        const float a = v[j] * __shfl_sync(0xffffffffu, sx, j) * sw;
-        const float b = v[j + 1] * __shfl_sync(0xffffffffu, sx, j + 1) * sw;
-        const float got = __shfl_xor_sync(0xffffffffu, lane & 1 ? a : b, 1);
-        if (lane & 1) store16(m0 + j + 1, n - 1, got, b, p.pairs_ok);
-        else store16(m0 + j, n, a, got, p.pairs_ok);
-      }
-    }
-  }
-};
-
-template <bool kGated>
+template <bool kGated, bool kF32>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant__ GemmParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;  // the swizzle goes by the address
@@ -391,18 +447,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_ke
     grid_wait();  // the tokens' scales, and what the kernel before this one may still read of y
     const int quarter = warp & 3;
     const uint32_t emptied = leader_bar(&sh.acc_empty[0]);
-    const int64_t units = (int64_t)p.sk_tiles * p.ks, part_floats = (int64_t)p.TN * 128;
+    EpilogueShared& mine = sh.epilogue[warp - 10];
+    const int64_t units = (int64_t)p.sk_tiles * p.ks;
     int buf = 0;
     unsigned phase = 0;
     while (segs.get(p, sg)) {
       const int row = sg.tile / p.n_tok, tok = sg.tile - row * p.n_tok;
-      const int row0 = (row * 2 + rank) * 128 + 32 * quarter;
-      const bool rows = row0 < p.w_tiles * 128;
-      const Epilogue<kGated> out{p, lane, row0, rows ? p.w_scales[row0 + lane] : 0.f};
-      auto scale_of = [&](int c) {
-        const int m = tok * p.TN + c + (lane & 15);
-        return m < p.M ? p.x_scales[m] : 0.f;
-      };
+      const Epilogue<kGated, kF32> out(p, mine, lane, (row * 2 + rank) * 128 + 32 * quarter, tok);
       ok = wait_bar(&sh.acc_full[buf], phase);
       if (!ok) break;
       tc_fence_after_sync();
@@ -416,38 +467,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_ke
       if (sg.k0 == 0 && sg.k1 == p.ks) {
         for (int c = 0; c < p.TN; c += 16) {
           float v[16];
-          tmem_ld_x16(acc + c, reinterpret_cast<uint32_t(&)[16]>(v));
-          const float sx = scale_of(c);
+          acc_load(acc + c, reinterpret_cast<uint32_t(&)[16]>(v));
           tmem_ld_wait();
-          out.columns(v, tok * p.TN + c, sx);
+          out.columns(v, c, tok * p.TN + c);
         }
         release();
         continue;
       }
-      // The pairs that share the tile: from the one with its first stage to the one with its last. A pair's part
-      // [token][row] is its number 1 if the pair starts inside the tile, else 0.
+      // The pairs that share the tile: from the one with its first stage to the one with its last.
       const int64_t t0 = (int64_t)sg.tile * p.ks, t1 = t0 + p.ks;
       int c0 = pair, c1 = pair;
       while (c0 * units / p.sk_pairs > t0) --c0;
       while ((c1 + 1) * units / p.sk_pairs < t1) ++c1;
-      auto part_of = [&](int q) {
-        const int first = q * units / p.sk_pairs >= t0 ? 1 : 0;
-        return p.part + ((int64_t)(2 * q + first) * 2 + rank) * part_floats + 32 * quarter + lane;
-      };
+      // [16 columns][4][lane][4]: a lane's 16 values of acc_load as four vectors
+      int* sums = p.sums + ((int64_t)(sg.tile * 2 + rank) * 4 + quarter) * p.TN * 32;
       unsigned* counter = p.counters + (sg.tile * 2 + rank) * 4 + quarter;
       const unsigned others = c1 - c0;
-      // All others have left their parts: this one need not go through memory.
-      bool held = __shfl_sync(0xffffffffu, ld_acquire_gpu(counter), 0) == others, last = held;
+      // All others have added theirs: this part need not go through memory.
+      const bool held = __shfl_sync(0xffffffffu, ld_acquire_gpu(counter), 0) == others;
+      bool last = held;
       if (!held) {
-        float* mine = part_of(pair);
-        for (int c = 0; c < p.TN; c += 32) {
-          uint32_t v[32];
-          tmem_ld_x32(acc + c, v);  // of the next accumulator, or the A slots, past TN: not stored
+        for (int c = 0, b = 0; c < p.TN; c += 16, b ^= 1) {
+          float v[16];
+          acc_load(acc + c, reinterpret_cast<uint32_t(&)[16]>(v));
           tmem_ld_wait();
+          if (lane == 0) bulk_wait_read<1>();  // the part before the last one has left shared memory
+          __syncwarp();
 #pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (c + j < p.TN) mine[(c + j) * 128] = __uint_as_float(v[j]);
+          for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<int4*>(&mine.sums[b][(j * 32 + lane) * 4]) =
+                make_int4(__float2int_rn(v[4 * j]), __float2int_rn(v[4 * j + 1]), __float2int_rn(v[4 * j + 2]),
+                          __float2int_rn(v[4 * j + 3]));
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) bulk_add_s32(sums + c * 32, mine.sums[b], 2048);
         }
+        if (lane == 0) bulk_wait_all();
         __threadfence();
         release();
         unsigned n = 0;
@@ -457,32 +512,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_ke
       if (last) {
         __threadfence();
         if (lane == 0) *counter = 0;
-        constexpr int kAtOnce = 3;
-        for (int c = 0; c < p.TN; c += 16) {
-          float v[16], f[16];
-          if (held) tmem_ld_x16(acc + c, reinterpret_cast<uint32_t(&)[16]>(v));
-          const float sx = scale_of(c);
+        constexpr int kAhead = 3;  // groups of 16 columns on their way
+        int4 g[kAhead][4];
+        auto load = [&](int c, int4 (&to)[4]) {
 #pragma unroll
-          for (int j = 0; j < 16; ++j) f[j] = 0.f;
-          for (int q = c0; q <= c1; q += kAtOnce) {
-            float g[kAtOnce][16];
+          for (int j = 0; j < 4; ++j)
+            if (c < p.TN) to[j] = __ldcg(reinterpret_cast<const int4*>(sums + c * 32) + j * 32 + lane);
+        };
 #pragma unroll
-            for (int i = 0; i < kAtOnce; ++i) {
-              if (q + i > c1 || (held && q + i == pair)) continue;
-              const float* from = part_of(q + i) + c * 128;
+        for (int i = 0; i < kAhead; ++i) load(16 * i, g[i]);
+        for (int c0 = 0; c0 < p.TN; c0 += 16 * kAhead) {
 #pragma unroll
-              for (int j = 0; j < 16; ++j) g[i][j] = __ldcg(from + j * 128);
+          for (int i = 0; i < kAhead; ++i) {
+            const int c = c0 + 16 * i;
+            if (c >= p.TN) break;
+            float v[16];
+            if (held) {
+              acc_load(acc + c, reinterpret_cast<uint32_t(&)[16]>(v));
+              tmem_ld_wait();
             }
-            if (held) tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < kAtOnce; ++i) {
-              if (q + i > c1) continue;
-              const bool own = held && q + i == pair;
-#pragma unroll
-              for (int j = 0; j < 16; ++j) f[j] += own ? v[j] : g[i][j];
+            for (int j = 0; j < 16; ++j) {
+              const int* e = reinterpret_cast<const int*>(&g[i][j / 4]);
+              v[j] = (float)(e[j % 4] + (held ? __float2int_rn(v[j]) : 0));
             }
+            load(c + 16 * kAhead, g[i]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              *(reinterpret_cast<int4*>(sums + c * 32) + j * 32 + lane) = make_int4(0, 0, 0, 0);
+            out.columns(v, c, tok * p.TN + c);
           }
-          out.columns(f, tok * p.TN + c, sx);
         }
         if (held) release();
       }
@@ -533,32 +592,32 @@ int tile_tokens(int M, int* n_tok) {
   return ((M + *n_tok - 1) / *n_tok + 15) / 16 * 16;
 }
 
-size_t part_bytes(const spear_w8_s* h) { return (size_t)(h->sm_count / 2) * 2 * 2 * kMaxTokens * 128 * sizeof(float); }
-
 // Room for whole token tiles: 16 n_tok tokens more than M at most.
 size_t x16_tokens(const spear_w8_s* h) { return (size_t)h->max_tokens + h->max_tokens / 8 + 256; }
 
 }  // namespace
 
-size_t w8_prefill_counters(const spear_w8_s* h) { return (size_t)h->sm_count * 8; }
-
-// Parts of shared tiles, then the tokens in f16 (of whole token tiles).
+// Arrival counters (2 CTAs x 4 warps a shared tile, fewer than two tiles a pair) and sums of shared tiles: zero between calls.
+size_t w8_prefill_counters(const spear_w8_s* h) { return h->max_tokens > kW8DecodeTokens ? (size_t)h->sm_count * 8 : 0; }
+size_t w8_prefill_sums(const spear_w8_s* h) {
+  return h->max_tokens > kW8DecodeTokens ? (size_t)h->sm_count * 2 * kMaxTokens * 128 * sizeof(int) : 0;
+}
+// The tokens in f16.
 size_t w8_prefill_workspace(const spear_w8_s* h) {
-  if (h->max_tokens <= kW8DecodeTokens) return 0;
-  return part_bytes(h) + (size_t)h->kb * 128 * x16_tokens(h);
+  return h->max_tokens > kW8DecodeTokens ? (size_t)h->kb * 128 * x16_tokens(h) : 0;
 }
 
 spear_status_t w8_launch_prefill(const spear_w8_s* h, const W8Call& c, cudaStream_t stream) {
   GemmParams p = {};
-  p.w = h->w, p.x16 = reinterpret_cast<uint8_t*>(h->part) + part_bytes(h), p.w_scales = h->w_scales, p.x_scales = c.x_scales;
-  p.y = c.y, p.ld_y = c.ld_y, p.part = h->part, p.counters = h->gemm_counters, p.status = h->status;
+  p.w = h->w, p.x16 = h->x16, p.w_scales = h->w_scales, p.x_scales = c.x_scales;
+  p.y = c.y, p.ld_y = c.ld_y, p.sums = h->sums, p.counters = h->gemm_counters, p.status = h->status;
   p.type = c.type, p.M = c.M, p.N = h->N, p.ks = h->kb / 2, p.act = h->act, p.w_tiles = h->strips / kW8Tile;
-  p.pairs_ok = (reinterpret_cast<uintptr_t>(c.y) & 3) == 0 && (c.ld_y % 2 == 0 || c.M == 1);
+  p.vec = (reinterpret_cast<uintptr_t>(c.y) & 15) == 0 && (c.ld_y % 8 == 0 || c.M == 1);
   p.TN = tile_tokens(c.M, &p.n_tok);
   p.acc_stride = (p.TN + 31) / 32 * 32;
   p.slots = std::min(kMaxSlots, (512 - 2 * p.acc_stride) / 64);
   p.stage_bytes = kRawBytes + p.TN * 128;
-  p.stages = std::min(kMaxStages, kSmemBudget / p.stage_bytes);
+  p.stages = std::min(kMaxStages, (int)(kSmem - sizeof(Shared) - 1024) / p.stage_bytes);
   const size_t smem = std::max((size_t)p.stages * p.stage_bytes + sizeof(Shared) + 1024, (size_t)120 * 1024);  // one CTA an SM
 
   const int pairs = h->sm_count / 2;
@@ -567,23 +626,25 @@ spear_status_t w8_launch_prefill(const spear_w8_s* h, const W8Call& c, cudaStrea
   // pair gets as much; adding the parts takes about as long as a dozen blocks of a tile.
   const int over = p.tiles % pairs;
   p.sk_pairs = pairs;
-  if (over && (int64_t)p.ks * (pairs - over) / pairs > 6) {
+  // A sum of K products of codes has to fit 32 bits.
+  if (over && h->K <= 65536 && (int64_t)p.ks * (pairs - over) / pairs > 6) {
     p.sk_tiles = p.tiles < pairs ? p.tiles : over + pairs;
     const int64_t units = (int64_t)p.sk_tiles * p.ks;
     if (p.tiles < pairs) p.sk_pairs = (int)std::min<int64_t>(pairs, std::max<int64_t>(p.tiles, units / 4));
   }
   const int grid = 2 * std::min(pairs, std::max(p.sk_tiles ? p.sk_pairs : 0, p.tiles - p.sk_tiles));
 
-  const void* kernel = h->gated ? reinterpret_cast<const void*>(&gemm_kernel<true>) : reinterpret_cast<const void*>(&gemm_kernel<false>);
-  static std::atomic<uint64_t> configured[2];
-  if (smem_limit_once(kernel, configured[h->gated]) != cudaSuccess) return SPEAR_ERR_CUDA;
+  static std::atomic<uint64_t> configured[4];
+  constexpr void (*kernels[4])(GemmParams) = {gemm_kernel<false, false>, gemm_kernel<false, true>, gemm_kernel<true, false>,
+                                              gemm_kernel<true, true>};
+  const int which = 2 * h->gated + (c.type == SPEAR_F32);
+  if (smem_limit_once(reinterpret_cast<const void*>(kernels[which]), configured[which]) != cudaSuccess) return SPEAR_ERR_CUDA;
   const int groups = p.n_tok * p.TN / 8;
   const dim3 cgrid(groups, (h->kb + 8 * kConvertTiles - 1) / (8 * kConvertTiles));
   const spear_status_t st = kv_launch(convert_kernel, cgrid, 256, 0, stream, c.x, c.ld_x, c.M, h->K, h->kb, p.TN / 16,
                                       const_cast<uint8_t*>(p.x16));
   if (st != SPEAR_OK) return st;
-  return h->gated ? kv_launch(gemm_kernel<true>, dim3(grid), kThreads, smem, stream, p)
-                  : kv_launch(gemm_kernel<false>, dim3(grid), kThreads, smem, stream, p);
+  return kv_launch(kernels[which], dim3(grid), kThreads, smem, stream, p);
 }
 
 }  // namespace spear
