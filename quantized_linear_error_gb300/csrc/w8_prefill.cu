@@ -50,7 +50,7 @@ constexpr uint64_t kWaitNs = 100000000ull;
 constexpr int kThreads = 15 * 32;
 constexpr int kRawBytes = 2 * kW8Tile * kW8Block;  // 128 rows x 128 channels
 constexpr int kMaxTokens = 192;                    // of a tile: two accumulators and two A slots in 512 columns
-constexpr int kSmem = 227 * 1024;
+constexpr int kSmem = 225 * 1024;
 constexpr int kMaxStages = 8, kMaxSlots = 4;
 
 
@@ -300,8 +300,9 @@ struct Shared {
   uint32_t tmem;
 };
 
+// (Registers for 608 threads: a block of convert_kernel runs beside this one.)
 template <bool kGated, bool kF32>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant__ GemmParams p) {
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads + 128, 1) gemm_kernel(const __grid_constant__ GemmParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;  // the swizzle goes by the address
   Shared& sh = *reinterpret_cast<Shared*>(smem + p.stages * p.stage_bytes);
@@ -512,7 +513,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_ke
       if (last) {
         __threadfence();
         if (lane == 0) *counter = 0;
-        constexpr int kAhead = 3;  // groups of 16 columns on their way
+        constexpr int kAhead = 2;  // groups of 16 columns on their way
         int4 g[kAhead][4];
         auto load = [&](int c, int4 (&to)[4]) {
 #pragma unroll
