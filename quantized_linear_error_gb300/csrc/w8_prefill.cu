@@ -19,7 +19,7 @@
 //   warp 0       copies the weights' codes, 16 KB a stage
 //   warp 1       issues the MMAs of the pair (in the first CTA): A from tensor
 //                memory, B from both CTAs' shared memory
-//   warps 2-9    codes -> f16 -> tensor memory: two warps 32 rows, 64 channels each
+//   warps 2-9    codes -> f16 -> tensor memory: two warps 32 rows, every other stage each
 //   warps 10-13  epilogue, from the accumulator that the MMAs have left, while they
 //                fill the other one
 //   warp 14      copies the tokens, TN / 2 of them a stage
@@ -155,15 +155,21 @@ SPEAR_DEVINL void expect_and_copy(uint32_t leader, uint32_t dst, const void* src
       : "memory");
 }
 
-SPEAR_DEVINL void umma2_ts(uint32_t leader, uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                           uint32_t accumulate) {
+// Eight k steps of 16: A from tensor memory, 8 columns a step; B from two tiles of 64 channels, 32 bytes a step.
+SPEAR_DEVINL void umma2_stage(uint32_t leader, uint32_t d, uint32_t a, uint64_t b0, uint64_t b1, uint32_t idesc, uint32_t accumulate) {
+#define SPEAR_MMA(A, B, P) "@q tcgen05.mma.cta_group::2.kind::f16 [%0], [" A "], " B ", %4, " P ";\n\t"
+#define SPEAR_NEXT "add.u32 a, a, 8;\n\tadd.u64 b, b, 2;\n\t"
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "setp.ne.b32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(leader)
+      "{\n\t.reg .pred p, q, t;\n\t.reg .b32 a;\n\t.reg .b64 b;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\tsetp.ne.b32 q, %6, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+      "mov.b32 a, %1;\n\tmov.b64 b, %2;\n\t"
+      SPEAR_MMA("a", "b", "p") SPEAR_NEXT SPEAR_MMA("a", "b", "t") SPEAR_NEXT SPEAR_MMA("a", "b", "t") SPEAR_NEXT
+      SPEAR_MMA("a", "b", "t") "add.u32 a, a, 8;\n\tmov.b64 b, %3;\n\t"
+      SPEAR_MMA("a", "b", "t") SPEAR_NEXT SPEAR_MMA("a", "b", "t") SPEAR_NEXT SPEAR_MMA("a", "b", "t") SPEAR_NEXT
+      SPEAR_MMA("a", "b", "t") "}" ::"r"(d), "r"(a), "l"(b0), "l"(b1), "r"(idesc), "r"(accumulate), "r"(leader)
       : "memory");
+#undef SPEAR_MMA
+#undef SPEAR_NEXT
 }
 // Arrive on both CTAs' barriers when the MMAs issued so far have completed.
 SPEAR_DEVINL void umma2_commit(uint32_t leader, uint64_t* bar) {
@@ -313,7 +319,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads + 128, 1) g
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.stages; ++s) {
       mbar_init(&sh.raw[s], 2);
-      mbar_init(&sh.a[s], 16);
+      mbar_init(&sh.a[s], 8);
       mbar_init(&sh.empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -387,11 +393,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads + 128, 1) g
           tc_fence_after_sync();
           const uint64_t desc = sw128_kmajor_desc(smem_u32(smem + s * p.stage_bytes));
           const uint64_t desc2 = desc + (p.TN * 64 >> 4);  // the second 64 channels
-          const uint32_t a = a_base + slot * 64;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) umma2_ts(leader, d, a + 8 * i, desc + 2 * i, idesc, k > sg.k0 || i > 0);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) umma2_ts(leader, d, a + 32 + 8 * i, desc2 + 2 * i, idesc, 1);
+          umma2_stage(leader, d, a_base + slot * 64, desc, desc2, idesc, k > sg.k0);
           umma2_commit(leader, &sh.empty[s]);
           if (++s == p.stages) s = 0, phase ^= 1;
           if (++slot == p.slots) slot = 0;
@@ -404,43 +406,59 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads + 128, 1) g
     }
     grid_wait();
   } else if (warp < 10) {
-    const int quarter = warp & 3, half = (warp - 2) >> 2;
+    const int quarter = warp & 3, turn = (warp - 2) >> 2;  // every other stage
     const int r = 32 * quarter + lane;
-    const uint32_t base = smem_u32(smem) + b_bytes + half * (kRawBytes / 2) + (r >> 4) * kW8Block;
+    const uint32_t base = smem_u32(smem) + b_bytes + (r >> 4) * kW8Block;
     uint32_t at[4];
 #pragma unroll
     for (int t = 0; t < 4; ++t) at[t] = base + w8_place(r & 15, t) * 16;
-    const uint32_t dst = a_base + ((uint32_t)(32 * quarter) << 16) + 32 * half;
+    const uint32_t dst = a_base + ((uint32_t)(32 * quarter) << 16);
     const uint32_t full = leader_bar(&sh.a[0]);
-    int s = 0, slot = 0, done = 0, es = 0;  // es: the stage whose MMAs free the slot
+    // s, slot: of stage n; es: the stage whose MMAs free the slot, stage n - slots
+    int n = 0, s = 0, slot = 0, es = 0;
     unsigned phase = 0, e_phase = 0;
+    auto next = [&] {
+      if (++n > p.slots && ++es == p.stages) es = 0, e_phase ^= 1;
+      if (++s == p.stages) s = 0, phase ^= 1;
+      if (++slot == p.slots) slot = 0;
+    };
+    if (turn) next();
+    int skip = turn;  // stages to pass before the next one of this warp's
     while (ok && segs.get(p, sg)) {
-      for (int k = sg.k0; k < sg.k1; ++k) {
+      int k = sg.k0 + skip;
+      for (; k < sg.k1; k += 2) {
         ok = wait_bar(&sh.raw[s], phase);
         if (!ok) break;
-        uint32_t f[32];
+        const uint32_t from = s * p.stage_bytes;
+        uint4 v[8];  // all loads ahead of the first conversion
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const uint4 v = lds128(at[t] + s * p.stage_bytes);
-          w8_unpack(v.x, f[8 * t], f[8 * t + 1]), w8_unpack(v.y, f[8 * t + 2], f[8 * t + 3]);
-          w8_unpack(v.z, f[8 * t + 4], f[8 * t + 5]), w8_unpack(v.w, f[8 * t + 6], f[8 * t + 7]);
-        }
-        if (done >= p.slots) {
+        for (int t = 0; t < 8; ++t) v[t] = lds128(at[t & 3] + from + (t >> 2) * (kRawBytes / 2));
+        uint32_t f[32];
+        auto convert = [&](int half) {
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            const uint4 w = v[4 * half + t];
+            w8_unpack(w.x, f[8 * t], f[8 * t + 1]), w8_unpack(w.y, f[8 * t + 2], f[8 * t + 3]);
+            w8_unpack(w.z, f[8 * t + 4], f[8 * t + 5]), w8_unpack(w.w, f[8 * t + 6], f[8 * t + 7]);
+          }
+        };
+        convert(0);
+        if (n >= p.slots) {
           ok = wait_bar(&sh.empty[es], e_phase);
           if (!ok) break;
           tc_fence_after_sync();
-          if (++es == p.stages) es = 0, e_phase ^= 1;
-        } else {
-          ++done;
         }
         tmem_st_x32(dst + slot * 64, f);
+        convert(1);
+        tmem_st_x32(dst + slot * 64 + 32, f);
         tmem_st_wait();
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(full + 8 * s);
-        if (++s == p.stages) s = 0, phase ^= 1;
-        if (++slot == p.slots) slot = 0;
+        next();
+        next();
       }
+      skip = k - sg.k1;
     }
     if (!ok && lane == 0) atomicOr(p.status, kStatusTimeoutPipe);
     grid_wait();
