@@ -477,60 +477,59 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads + 128, 1) g
       if (!ok) break;
       tc_fence_after_sync();
       const uint32_t acc = tmem + buf * p.acc_stride + ((uint32_t)(32 * quarter) << 16);
-      auto release = [&] {
-        tc_fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(emptied + 8 * buf);
-        if ((buf ^= 1) == 0) phase ^= 1;
-      };
-      if (sg.k0 == 0 && sg.k1 == p.ks) {
+      const bool whole = sg.k0 == 0 && sg.k1 == p.ks;
+      // [16 columns][4][lane][4]: a lane's 16 values of acc_load as four vectors
+      int* sums = p.sums + ((int64_t)(sg.tile * 2 + rank) * 4 + quarter) * p.TN * 32;
+      bool held = true, last = true;  // this pair's part is in tensor memory; the tile is complete with it
+      if (!whole) {
+        // The pairs that share the tile: from the one with its first stage to the one with its last.
+        const int64_t t0 = (int64_t)sg.tile * p.ks, t1 = t0 + p.ks;
+        int c0 = pair, c1 = pair;
+        while (c0 * units / p.sk_pairs > t0) --c0;
+        while ((c1 + 1) * units / p.sk_pairs < t1) ++c1;
+        unsigned* counter = p.counters + (sg.tile * 2 + rank) * 4 + quarter;
+        const unsigned others = c1 - c0;
+        // Where all others have added theirs, this part need not go through memory.
+        held = __shfl_sync(0xffffffffu, ld_acquire_gpu(counter), 0) == others;
+        if (!held) {
+#pragma unroll 1
+          for (int c = 0, b = 0; c < p.TN; c += 16, b ^= 1) {
+            float v[16];
+            acc_load(acc + c, reinterpret_cast<uint32_t(&)[16]>(v));
+            tmem_ld_wait();
+            if (lane == 0) bulk_wait_read<1>();  // the copy before the last one has left shared memory
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              *reinterpret_cast<int4*>(&mine.sums[b][(j * 32 + lane) * 4]) =
+                  make_int4(__float2int_rn(v[4 * j]), __float2int_rn(v[4 * j + 1]), __float2int_rn(v[4 * j + 2]),
+                            __float2int_rn(v[4 * j + 3]));
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) bulk_add_s32(sums + c * 32, mine.sums[b], 2048);
+          }
+          unsigned n = 0;
+          if (lane == 0) {
+            bulk_wait_all();
+            __threadfence();
+            n = atomicAdd(counter, 1u);
+          }
+          last = __shfl_sync(0xffffffffu, n, 0) == others;
+        }
+        if (last) {
+          __threadfence();
+          if (lane == 0) *counter = 0;
+        }
+      }
+      if (whole) {
+#pragma unroll 1  // a call with few tiles runs this from a cold instruction cache
         for (int c = 0; c < p.TN; c += 16) {
           float v[16];
           acc_load(acc + c, reinterpret_cast<uint32_t(&)[16]>(v));
           tmem_ld_wait();
           out.columns(v, c, tok * p.TN + c);
         }
-        release();
-        continue;
-      }
-      // The pairs that share the tile: from the one with its first stage to the one with its last.
-      const int64_t t0 = (int64_t)sg.tile * p.ks, t1 = t0 + p.ks;
-      int c0 = pair, c1 = pair;
-      while (c0 * units / p.sk_pairs > t0) --c0;
-      while ((c1 + 1) * units / p.sk_pairs < t1) ++c1;
-      // [16 columns][4][lane][4]: a lane's 16 values of acc_load as four vectors
-      int* sums = p.sums + ((int64_t)(sg.tile * 2 + rank) * 4 + quarter) * p.TN * 32;
-      unsigned* counter = p.counters + (sg.tile * 2 + rank) * 4 + quarter;
-      const unsigned others = c1 - c0;
-      // All others have added theirs: this part need not go through memory.
-      const bool held = __shfl_sync(0xffffffffu, ld_acquire_gpu(counter), 0) == others;
-      bool last = held;
-      if (!held) {
-        for (int c = 0, b = 0; c < p.TN; c += 16, b ^= 1) {
-          float v[16];
-          acc_load(acc + c, reinterpret_cast<uint32_t(&)[16]>(v));
-          tmem_ld_wait();
-          if (lane == 0) bulk_wait_read<1>();  // the part before the last one has left shared memory
-          __syncwarp();
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            *reinterpret_cast<int4*>(&mine.sums[b][(j * 32 + lane) * 4]) =
-                make_int4(__float2int_rn(v[4 * j]), __float2int_rn(v[4 * j + 1]), __float2int_rn(v[4 * j + 2]),
-                          __float2int_rn(v[4 * j + 3]));
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) bulk_add_s32(sums + c * 32, mine.sums[b], 2048);
-        }
-        if (lane == 0) bulk_wait_all();
-        __threadfence();
-        release();
-        unsigned n = 0;
-        if (lane == 0) n = atomicAdd(counter, 1u);
-        last = __shfl_sync(0xffffffffu, n, 0) == others;
-      }
-      if (last) {
-        __threadfence();
-        if (lane == 0) *counter = 0;
+      } else if (last) {
         constexpr int kAhead = 2;  // groups of 16 columns on their way
         int4 g[kAhead][4];
         auto load = [&](int c, int4 (&to)[4]) {
@@ -540,6 +539,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads + 128, 1) g
         };
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) load(16 * i, g[i]);
+#pragma unroll 1
         for (int c0 = 0; c0 < p.TN; c0 += 16 * kAhead) {
 #pragma unroll
           for (int i = 0; i < kAhead; ++i) {
@@ -562,8 +562,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads + 128, 1) g
             out.columns(v, c, tok * p.TN + c);
           }
         }
-        if (held) release();
       }
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(emptied + 8 * buf);
+      if ((buf ^= 1) == 0) phase ^= 1;
     }
     if (!ok && lane == 0) atomicOr(p.status, kStatusTimeoutPipe);
   }
@@ -606,9 +609,41 @@ __global__ void __launch_bounds__(256) convert_kernel(const int8_t* __restrict__
   }
 }
 
-int tile_tokens(int M, int* n_tok) {
-  *n_tok = (M + kMaxTokens - 1) / kMaxTokens;
-  return ((M + *n_tok - 1) / *n_tok + 15) / 16 * 16;
+// How a call is cut: n_tok tiles of TN tokens; sk_tiles of all the tiles split along K over sk_pairs pairs.
+struct Cut {
+  int TN, n_tok, tiles, sk_tiles, sk_pairs;
+  int64_t cycles;
+};
+
+// The cut with the least estimated time. Measured, in cycles of an SM: a stage takes the MMAs' 4 TN and 40 more, 200 in
+// calls so long that the power limit lowers the clocks (2048 tokens, 4096 x 14336: 511 ns with TN 192, 447 with 160);
+// 580 at least
+// (8 MMAs of 64 cycles, whatever TN, and the hand-over); the last tile's epilogue 25 TN; adding up a
+// split tile 3000 and 110 TN, which whole tiles that follow it hide. Chunk of 320 tokens, 6144 x 4096: 2 x 160 split 26
+// us, 2 x 160 whole 21, 3 x 112 21, 4 x 80 27; 512 tokens, 8192 x 8192: 3 x 176 split 54, whole 62, 4 x 128 59 and 58.
+Cut cut(const spear_w8_s* h, int M, size_t room) {
+  const int pairs = h->sm_count / 2, ks = h->kb / 2, rows = (h->strips / kW8Tile + 1) / 2;
+  const int beside = (int64_t)M * h->strips * h->kb > (100ll << 30) / (kW8Strip * kW8K) ? 200 : 40;  // 2^37 products
+  Cut best = {};
+  for (int n = (M + kMaxTokens - 1) / kMaxTokens, most = n + 4; n <= most; ++n) {
+    Cut c = {((M + n - 1) / n + 15) / 16 * 16, n, rows * n, 0, pairs, 0};
+    if (n < most - 4 + 1 || (size_t)c.TN * n <= room) {
+      const int64_t stage = std::max(4 * c.TN + beside, 580);
+      c.cycles = (c.tiles + pairs - 1) / pairs * ks * stage + 25 * c.TN;
+      if (best.TN == 0 || c.cycles < best.cycles) best = c;
+      const int over = c.tiles % pairs;
+      if (over && h->K <= 65536) {  // a sum of K products of codes has to fit 32 bits
+        // together with one round of whole tiles, so that every pair gets as much
+        c.sk_tiles = c.tiles < pairs ? c.tiles : over + pairs;
+        const int64_t units = (int64_t)c.sk_tiles * ks;
+        if (c.tiles < pairs) c.sk_pairs = (int)std::min<int64_t>(pairs, std::max<int64_t>(c.tiles, units / 4));
+        const int64_t join = 3000 + 110 * c.TN, left = (int64_t)(c.tiles - c.sk_tiles) / pairs * ks * stage;
+        c.cycles = (units + c.sk_pairs - 1) / c.sk_pairs * stage + std::max(join, left + 25 * c.TN);
+        if (c.cycles < best.cycles) best = c;
+      }
+    }
+  }
+  return best;
 }
 
 // Room for whole token tiles: 16 n_tok tokens more than M at most.
@@ -632,25 +667,15 @@ spear_status_t w8_launch_prefill(const spear_w8_s* h, const W8Call& c, cudaStrea
   p.y = c.y, p.ld_y = c.ld_y, p.sums = h->sums, p.counters = h->gemm_counters, p.status = h->status;
   p.type = c.type, p.M = c.M, p.N = h->N, p.ks = h->kb / 2, p.act = h->act, p.w_tiles = h->strips / kW8Tile;
   p.vec = (reinterpret_cast<uintptr_t>(c.y) & 15) == 0 && (c.ld_y % 8 == 0 || c.M == 1);
-  p.TN = tile_tokens(c.M, &p.n_tok);
+  const int pairs = h->sm_count / 2;
+  const Cut k = cut(h, c.M, x16_tokens(h));
+  p.TN = k.TN, p.n_tok = k.n_tok, p.tiles = k.tiles, p.sk_tiles = k.sk_tiles, p.sk_pairs = k.sk_pairs;
   p.acc_stride = (p.TN + 31) / 32 * 32;
   p.slots = std::min(kMaxSlots, (512 - 2 * p.acc_stride) / 64);
   p.stage_bytes = kRawBytes + p.TN * 128;
   p.stages = std::min(kMaxStages, (int)(kSmem - sizeof(Shared) - 1024) / p.stage_bytes);
   const size_t smem = std::max((size_t)p.stages * p.stage_bytes + sizeof(Shared) + 1024, (size_t)120 * 1024);  // one CTA an SM
 
-  const int pairs = h->sm_count / 2;
-  p.tiles = (p.w_tiles + 1) / 2 * p.n_tok;
-  // Tiles that do not fill the pairs evenly are split along K, together with one round of whole ones, so that every
-  // pair gets as much; adding the parts takes about as long as a dozen blocks of a tile.
-  const int over = p.tiles % pairs;
-  p.sk_pairs = pairs;
-  // A sum of K products of codes has to fit 32 bits.
-  if (over && h->K <= 65536 && (int64_t)p.ks * (pairs - over) / pairs > 6) {
-    p.sk_tiles = p.tiles < pairs ? p.tiles : over + pairs;
-    const int64_t units = (int64_t)p.sk_tiles * p.ks;
-    if (p.tiles < pairs) p.sk_pairs = (int)std::min<int64_t>(pairs, std::max<int64_t>(p.tiles, units / 4));
-  }
   const int grid = 2 * std::min(pairs, std::max(p.sk_tiles ? p.sk_pairs : 0, p.tiles - p.sk_tiles));
 
   static std::atomic<uint64_t> configured[4];
