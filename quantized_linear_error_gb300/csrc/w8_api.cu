@@ -15,8 +15,8 @@ __global__ void __launch_bounds__(256) layout_kernel(const int8_t* __restrict__ 
   if (i >= chunks) return;
   const int64_t block = i >> 6;
   const int r = (int)(i >> 2) & 15, t = (int)i & 3;
-  const int64_t at = block / kW8Tile, tile = at / kb, strip = tile * kW8Tile + block % kW8Tile;
-  const int k = (int)(at - tile * kb) * kW8K + t * 16;
+  const int64_t at = block / 2, pair = at / kb, strip = pair * 2 + block % 2;
+  const int k = (int)(at - pair * kb) * kW8K + t * 16;
   const int8_t* src = q0;
   int64_t n = strip * 16 + r;
   if (q1) {

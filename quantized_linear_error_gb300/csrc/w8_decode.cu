@@ -9,8 +9,10 @@
 // 16 weight rows and whose columns are 8 tokens. Products of codes and their
 // sums below 2^24 are exact in the fp32 accumulators.
 //
-// A warp takes RS strips of 16 rows at once, so that a token's codes are
-// fetched and converted once for them; the warps of a CTA take blocks of the
+// A warp takes 4 KB at a time, RS strips of 16 rows by KU blocks of 64 channels,
+// so that what a turn costs beside the arithmetic (a wait, copies to issue, the
+// tokens' codes) is spread over as much (a token through 14336 x 4096 with 1, 2,
+// 4 KB a turn: 19.3, 14.6, 12.5 us); the warps of a CTA take the units of the
 // same rows along K in turn, and their sums are added in shared memory in a
 // fixed order.
 #include <algorithm>
@@ -30,8 +32,8 @@ struct StreamParams {
   int64_t ld_y;
   float* part;
   unsigned *counters, *status;
-  int type, M, K, N, kb, gated, act;
-  int units, balanced, per;  // blocks in all; split evenly, or `per` whole row groups a CTA
+  int type, M, K, N, kq, gated, act;  // kq: units of a row group
+  int units, balanced, per;           // units in all; split evenly, or `per` whole row groups a CTA
 };
 
 SPEAR_DEVINL void mma_f16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -43,16 +45,16 @@ SPEAR_DEVINL void mma_f16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_
 constexpr uint64_t kWaitNs = 100000000ull;
 
 // First unit of CTA c.
-__host__ __device__ inline int range_start(int c, int grid, int units, int balanced, int per, int kb) {
+__host__ __device__ inline int range_start(int c, int grid, int units, int balanced, int per, int kq) {
   if (balanced) return (int)((int64_t)c * units / grid);
-  const int64_t u = (int64_t)c * per * kb;
+  const int64_t u = (int64_t)c * per * kq;
   return u < units ? (int)u : units;
 }
 
-// MT tiles of 8 tokens, RS strips of 16 rows a warp, NW warps, D stages a warp.
-template <int MT, int RS, int NW, int D>
+// MT tiles of 8 tokens, RS strips of 16 rows x KU blocks a unit, NW warps, D units of a warp on their way.
+template <int MT, int RS, int KU, int NW, int D>
 struct Plan {
-  static constexpr int kStage = RS * kW8Block;                // a warp's
+  static constexpr int kStage = RS * KU * kW8Block;           // a unit
   static constexpr int kRing = NW * D * kStage;
   static constexpr int kElems = RS * MT * 128;                // sums of a row group
   static constexpr int kBars = kRing + NW * kElems * 4;
@@ -60,46 +62,51 @@ struct Plan {
   static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
 };
 
-template <int MT, int RS, int NW, int D>
+template <int MT, int RS, int KU, int NW, int D>
 __global__ void __launch_bounds__(NW * 32, 1) stream_kernel(const __grid_constant__ StreamParams p) {
-  using P = Plan<MT, RS, NW, D>;
+  using P = Plan<MT, RS, KU, NW, D>;
+  constexpr int kRuns = RS / 2, kRun = 2 * KU * kW8Block;  // a unit's pairs of strips, and the bytes of one
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int u0 = range_start(blockIdx.x, gridDim.x, p.units, p.balanced, p.per, p.kb);
-  const int u1 = range_start(blockIdx.x + 1, gridDim.x, p.units, p.balanced, p.per, p.kb);
+  const int u0 = range_start(blockIdx.x, gridDim.x, p.units, p.balanced, p.per, p.kq);
+  const int u1 = range_start(blockIdx.x + 1, gridDim.x, p.units, p.balanced, p.per, p.kq);
   uint8_t* ring = smem + warp * D * P::kStage;
   float* red = reinterpret_cast<float*>(smem + P::kRing);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + P::kBars) + warp * D;
   volatile int& last = *reinterpret_cast<volatile int*>(smem + P::kSmem - 16);
 
   grid_launch_dependents();
-  // The block to be copied next: unit fu = row group fg, k block fk.
-  int fg = u0 / p.kb, fk = u0 - fg * p.kb + warp, fu = u0 + warp, copied = u1;
-  while (fk >= p.kb) fk -= p.kb, ++fg;
+  // The unit to be copied next: fu = row group fg, unit fk of it; lane i copies its run i.
+  const int64_t pair_bytes = (int64_t)p.kq * kRun;  // of a pair of strips
+  int fg = u0 / p.kq, fk = u0 - fg * p.kq + warp, fu = u0 + warp, copied = u1;
+  while (fk >= p.kq) fk -= p.kq, ++fg;
   auto fetch = [&](int stage) {
     if (fu < copied) {
       if (lane == 0) mbar_arrive_expect_tx(bars + stage, P::kStage);
-      __syncwarp();
-      // the group's strips of one k block lie side by side
-      if (lane == 0)
-        bulk_g2s(ring + stage * P::kStage, p.w + w8_block(fg * RS, fk, p.kb), P::kStage, bars + stage);
+      if (lane < kRuns)
+        bulk_g2s(ring + stage * P::kStage + lane * kRun, p.w + (fg * kRuns + lane) * pair_bytes + (int64_t)fk * kRun, kRun,
+                 bars + stage);
     }
     fu += NW, fk += NW;
-    while (fk >= p.kb) fk -= p.kb, ++fg;
+    while (fk >= p.kq) fk -= p.kq, ++fg;
   };
-  uint4 xr[MT];  // of the unit that is worked on next
-  int xk = u0 % p.kb + warp;
-  while (xk >= p.kb) xk -= p.kb;
+  uint4 xr[KU][MT];  // of the unit that is worked on next
+  int xk = u0 % p.kq + warp;
+  while (xk >= p.kq) xk -= p.kq;
+  const int8_t* xrow = p.x + g * p.ld_x + t * 16;
   auto fetch_x = [&](int u) {
-    const int k = xk * kW8K + t * 16;
 #pragma unroll
-    for (int j = 0; j < MT; ++j) {
-      const int m = j * 8 + g;
-      xr[j] = make_uint4(0, 0, 0, 0);
-      if (u < u1 && m < p.M && k < p.K) xr[j] = *reinterpret_cast<const uint4*>(p.x + m * p.ld_x + k);  // K is a multiple of 16
+    for (int q = 0; q < KU; ++q) {
+      const int k = (xk * KU + q) * kW8K;
+#pragma unroll
+      for (int j = 0; j < MT; ++j) {
+        xr[q][j] = make_uint4(0, 0, 0, 0);
+        if (u < u1 && j * 8 + g < p.M && k + t * 16 < p.K)  // K is a multiple of 16
+          xr[q][j] = *reinterpret_cast<const uint4*>(xrow + j * 8 * p.ld_x + k);
+      }
     }
     xk += NW;
-    while (xk >= p.kb) xk -= p.kb;
+    while (xk >= p.kq) xk -= p.kq;
   };
   if (lane == 0) {
 #pragma unroll
@@ -116,7 +123,7 @@ __global__ void __launch_bounds__(NW * 32, 1) stream_kernel(const __grid_constan
   unsigned phase = 0;
   const uint32_t place = w8_place(g, t) * 16;
   for (int seg = u0; seg < u1;) {
-    const int group = seg / p.kb, end = min(u1, (group + 1) * p.kb);
+    const int group = seg / p.kq, end = min(u1, (group + 1) * p.kq);
     float acc[RS][MT][4];
 #pragma unroll
     for (int r = 0; r < RS; ++r)
@@ -125,36 +132,46 @@ __global__ void __launch_bounds__(NW * 32, 1) stream_kernel(const __grid_constan
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[r][j][i] = 0.f;
     for (; u < end; u += NW) {
-      uint32_t b[MT][8];
+      uint32_t b[KU][MT][8];
 #pragma unroll
-      for (int j = 0; j < MT; ++j) {
-        w8_unpack(xr[j].x ^ kW8Bias, b[j][0], b[j][1]);
-        w8_unpack(xr[j].y ^ kW8Bias, b[j][2], b[j][3]);
-        w8_unpack(xr[j].z ^ kW8Bias, b[j][4], b[j][5]);
-        w8_unpack(xr[j].w ^ kW8Bias, b[j][6], b[j][7]);
-      }
+      for (int q = 0; q < KU; ++q)
+#pragma unroll
+        for (int j = 0; j < MT; ++j) {
+          w8_unpack(xr[q][j].x ^ kW8Bias, b[q][j][0], b[q][j][1]);
+          w8_unpack(xr[q][j].y ^ kW8Bias, b[q][j][2], b[q][j][3]);
+          w8_unpack(xr[q][j].z ^ kW8Bias, b[q][j][4], b[q][j][5]);
+          w8_unpack(xr[q][j].w ^ kW8Bias, b[q][j][6], b[q][j][7]);
+        }
       fetch_x(u + NW);
       if (u < copied && !__all_sync(0xffffffffu, mbar_wait_bounded(bars + stage, phase, kWaitNs))) {
         copied = min(copied, fu);  // no further copies; those in flight are still waited for
         if (lane == 0) atomicOr(p.status, kStatusTimeoutPipe);
       }
+      // strip r of k block q: run r / 2, [q][r % 2]
       const uint32_t at = smem_u32(ring + stage * P::kStage) + place;
-      uint4 v[RS][2];
+      uint4 v[KU][RS][2];
 #pragma unroll
-      for (int r = 0; r < RS; ++r) v[r][0] = lds128(at + r * kW8Block), v[r][1] = lds128(at + r * kW8Block + 512);
+      for (int q = 0; q < KU; ++q)
 #pragma unroll
-      for (int r = 0; r < RS; ++r) {
-        const uint32_t lo[4] = {v[r][0].x, v[r][0].y, v[r][0].z, v[r][0].w};
-        const uint32_t hi[4] = {v[r][1].x, v[r][1].y, v[r][1].z, v[r][1].w};
+        for (int r = 0; r < RS; ++r)
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          uint32_t a0, a1, a2, a3;
-          w8_unpack(lo[s], a0, a2);
-          w8_unpack(hi[s], a1, a3);
+          for (int half = 0; half < 2; ++half)
+            v[q][r][half] = lds128(at + (r / 2) * kRun + (2 * q + r % 2) * kW8Block + half * 512);
 #pragma unroll
-          for (int j = 0; j < MT; ++j) mma_f16_16816(acc[r][j], a0, a1, a2, a3, b[j][2 * s], b[j][2 * s + 1]);
+      for (int q = 0; q < KU; ++q)
+#pragma unroll
+        for (int r = 0; r < RS; ++r) {
+          const uint32_t lo[4] = {v[q][r][0].x, v[q][r][0].y, v[q][r][0].z, v[q][r][0].w};
+          const uint32_t hi[4] = {v[q][r][1].x, v[q][r][1].y, v[q][r][1].z, v[q][r][1].w};
+#pragma unroll
+          for (int s = 0; s < 4; ++s) {
+            uint32_t a0, a1, a2, a3;
+            w8_unpack(lo[s], a0, a2);
+            w8_unpack(hi[s], a1, a3);
+#pragma unroll
+            for (int j = 0; j < MT; ++j) mma_f16_16816(acc[r][j], a0, a1, a2, a3, b[q][j][2 * s], b[q][j][2 * s + 1]);
+          }
         }
-      }
       __syncwarp();  // every lane has read its part
       fetch(stage);
       if (++stage == D) stage = 0, phase ^= 1;
@@ -190,19 +207,19 @@ __global__ void __launch_bounds__(NW * 32, 1) stream_kernel(const __grid_constan
         w8_store(p.y, m * p.ld_y + n, p.type, v);
       }
     };
-    if (seg == group * p.kb && end == (group + 1) * p.kb) {
+    if (seg == group * p.kq && end == (group + 1) * p.kq) {
       finish(own_sum);
     } else {
       // shared with other CTAs: the last one to arrive adds the parts in the CTAs' order
-      auto slot = [&](int c, int first) { return p.part + ((int64_t)2 * c + (first >= group * p.kb ? 1 : 0)) * P::kElems; };
+      auto slot = [&](int c, int first) { return p.part + ((int64_t)2 * c + (first >= group * p.kq ? 1 : 0)) * P::kElems; };
       float* part = slot(blockIdx.x, u0);
       for (int e = threadIdx.x; e < P::kElems; e += NW * 32) part[e] = own_sum(e);
       __threadfence();
       __syncthreads();
       // CTAs that hold a block of the group: from the one with its first to the one with its last
       int c0 = blockIdx.x, c1 = blockIdx.x;
-      while (range_start(c0, gridDim.x, p.units, 1, 0, 0) > group * p.kb) --c0;
-      while (range_start(c1 + 1, gridDim.x, p.units, 1, 0, 0) < (group + 1) * p.kb) ++c1;
+      while (range_start(c0, gridDim.x, p.units, 1, 0, 0) > group * p.kq) --c0;
+      while (range_start(c1 + 1, gridDim.x, p.units, 1, 0, 0) < (group + 1) * p.kq) ++c1;
       if (threadIdx.x == 0) {
         last = atomicAdd(p.counters + group, 1u) == (unsigned)(c1 - c0);
         if (last) p.counters[group] = 0;
@@ -223,56 +240,56 @@ __global__ void __launch_bounds__(NW * 32, 1) stream_kernel(const __grid_constan
 }
 
 struct Split {
-  int groups, per, grid, balanced;
-  int64_t cost;  // strips x blocks of the CTA with the most, and what joining takes
+  int groups, kq, per, grid, balanced;
+  int64_t cost;  // blocks of the CTA with the most, and what joining takes
 };
 
-// Whole row groups of RS strips need no joining between CTAs; an even split does, about the time of 64 blocks.
-Split split(const spear_w8_s* h, int RS, int NW) {
+// Whole row groups of RS strips need no joining between CTAs; an even split does, about the time of 200 blocks (4.5 us).
+Split split(const spear_w8_s* h, int RS, int KU, int NW) {
   Split s;
   const int used = h->gated ? (h->N + 7) / 8 : (h->N + 15) / 16;
   s.groups = (used + RS - 1) / RS;
+  s.kq = h->kb / KU;
   s.per = (s.groups + h->sm_count - 1) / h->sm_count;
   s.grid = (s.groups + s.per - 1) / s.per;
   s.balanced = 0;
-  s.cost = (int64_t)s.per * h->kb * RS;
-  const int64_t units = (int64_t)s.groups * h->kb;
+  s.cost = (int64_t)s.per * s.kq * RS * KU;
+  const int64_t units = (int64_t)s.groups * s.kq;
   const int even = (int)std::min<int64_t>(h->sm_count, std::max<int64_t>(1, units / NW));
-  const int64_t cost = (units + even - 1) / even * RS + 64;
+  const int64_t cost = (units + even - 1) / even * RS * KU + 200;
   if (cost < s.cost) s.balanced = 1, s.grid = even, s.cost = cost;
   return s;
 }
 
-template <int MT, int RS, int NW, int D>
+template <int MT, int RS, int KU, int NW, int D>
 spear_status_t launch(const spear_w8_s* h, const W8Call& c, const Split& sp, cudaStream_t stream) {
-  using P = Plan<MT, RS, NW, D>;
+  using P = Plan<MT, RS, KU, NW, D>;
   static std::atomic<uint64_t> configured{0};
-  if (smem_limit_once(reinterpret_cast<const void*>(&stream_kernel<MT, RS, NW, D>), configured) != cudaSuccess)
+  if (smem_limit_once(reinterpret_cast<const void*>(&stream_kernel<MT, RS, KU, NW, D>), configured) != cudaSuccess)
     return SPEAR_ERR_CUDA;
   StreamParams p = {h->w, h->w_scales, c.x, c.ld_x, c.x_scales, c.y, c.ld_y, h->part, h->counters, h->status};
-  p.type = c.type, p.M = c.M, p.K = h->K, p.N = h->N, p.kb = h->kb, p.gated = h->gated, p.act = h->act;
-  p.units = sp.groups * h->kb, p.per = sp.per, p.balanced = sp.balanced;
-  return kv_launch(stream_kernel<MT, RS, NW, D>, dim3(sp.grid), NW * 32, P::kSmem, stream, p);
+  p.type = c.type, p.M = c.M, p.K = h->K, p.N = h->N, p.kq = sp.kq, p.gated = h->gated, p.act = h->act;
+  p.units = sp.groups * sp.kq, p.per = sp.per, p.balanced = sp.balanced;
+  return kv_launch(stream_kernel<MT, RS, KU, NW, D>, dim3(sp.grid), NW * 32, P::kSmem, stream, p);
 }
 
-template <int MT, int NW, int D1, int D2, int D4>
+// Two strips by two blocks, or four strips where that costs no balance: half the tokens' codes.
+template <int MT, int NW, int D>
 spear_status_t launch(const spear_w8_s* h, const W8Call& c, cudaStream_t stream) {
-  const Split s1 = split(h, 1, NW), s2 = split(h, 2, NW), s4 = split(h, 4, NW);
-  // several strips a warp need fewer instructions a block
-  if (s4.cost * 16 <= s2.cost * 17 && s4.cost * 8 <= s1.cost * 10) return launch<MT, 4, NW, D4>(h, c, s4, stream);
-  if (s2.cost * 8 <= s1.cost * 9) return launch<MT, 2, NW, D2>(h, c, s2, stream);
-  return launch<MT, 1, NW, D1>(h, c, s1, stream);
+  const Split s2 = split(h, 2, 2, NW), s4 = split(h, 4, 1, NW);
+  if (s4.cost * 16 <= s2.cost * 17) return launch<MT, 4, 1, NW, D>(h, c, s4, stream);
+  return launch<MT, 2, 2, NW, D>(h, c, s2, stream);
 }
 
 }  // namespace
 
 // Two parts a CTA, of the variant with the most sums.
-size_t w8_decode_workspace(const spear_w8_s* h) { return (size_t)2 * h->sm_count * Plan<4, 4, 8, 4>::kElems * sizeof(float); }
+size_t w8_decode_workspace(const spear_w8_s* h) { return (size_t)2 * h->sm_count * Plan<4, 4, 1, 8, 4>::kElems * sizeof(float); }
 
 spear_status_t w8_launch_decode(const spear_w8_s* h, const W8Call& c, cudaStream_t stream) {
-  if (c.M <= 8) return launch<1, 16, 10, 5, 3>(h, c, stream);
-  if (c.M <= 16) return launch<2, 16, 10, 4, 2>(h, c, stream);
-  return launch<4, 8, 16, 8, 4>(h, c, stream);
+  if (c.M <= 8) return launch<1, 16, 3>(h, c, stream);
+  if (c.M <= 16) return launch<2, 16, 2>(h, c, stream);
+  return launch<4, 8, 4>(h, c, stream);
 }
 
 }  // namespace spear

@@ -348,20 +348,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads + 128, 1) g
     const bool tokens = warp == 14;
     if (tokens) grid_wait();
     const uint32_t leader = elect_leader();
-    const uint32_t bytes = tokens ? b_bytes : kRawBytes;
+    const int64_t run = (int64_t)p.ks * 4096;  // of a pair of strips
     const uint32_t dst = smem_u32(smem) + (tokens ? 0 : b_bytes);
     int s = 0, issued = 0;
     unsigned phase = 1;  // the first pass through the ring finds every stage empty
     while (ok && segs.get(p, sg)) {
       const int row = sg.tile / p.n_tok, tok = sg.tile - row * p.n_tok;
-      const uint8_t* src = tokens ? p.x16 + (int64_t)(tok * 2 + rank) * p.ks * b_bytes
-                                  : p.w + (int64_t)min(row * 2 + rank, p.w_tiles - 1) * p.ks * kRawBytes;
-      src += (int64_t)sg.k0 * bytes;
+      const uint8_t* src = tokens ? p.x16 + ((int64_t)(tok * 2 + rank) * p.ks + sg.k0) * b_bytes
+                                  : p.w + min(row * 2 + rank, p.w_tiles - 1) * 4 * run + (int64_t)sg.k0 * 4096;
       for (int k = sg.k0; k < sg.k1; ++k) {
         ok = wait_bar(&sh.empty[s], phase);
         if (!ok) break;
-        expect_and_copy(leader, dst + s * p.stage_bytes, src, bytes, smem_u32(&sh.raw[s]));
-        src += bytes;
+        if (tokens) {
+          expect_and_copy(leader, dst + s * p.stage_bytes, src, b_bytes, smem_u32(&sh.raw[s]));
+          src += b_bytes;
+        } else {
+          if (leader) mbar_arrive_expect_tx(&sh.raw[s], kRawBytes);
+          // lane i < 4: a pair of strips' 4 KB
+          if (lane < 4) bulk_g2s_shared_u32(dst + s * p.stage_bytes + lane * 4096, src + lane * run, 4096, &sh.raw[s]);
+          src += 4096;
+        }
         ++issued;
         if (++s == p.stages) s = 0, phase ^= 1;
       }
@@ -408,7 +414,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads + 128, 1) g
   } else if (warp < 10) {
     const int quarter = warp & 3, turn = (warp - 2) >> 2;  // every other stage
     const int r = 32 * quarter + lane;
-    const uint32_t base = smem_u32(smem) + b_bytes + (r >> 4) * kW8Block;
+    const uint32_t base = smem_u32(smem) + b_bytes + (r >> 5) * 4 * kW8Block + ((r >> 4) & 1) * kW8Block;  // quarter's pair
     uint32_t at[4];
 #pragma unroll
     for (int t = 0; t < 4; ++t) at[t] = base + w8_place(r & 15, t) * 16;
@@ -432,7 +438,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads + 128, 1) g
         const uint32_t from = s * p.stage_bytes;
         uint4 v[8];  // all loads ahead of the first conversion
 #pragma unroll
-        for (int t = 0; t < 8; ++t) v[t] = lds128(at[t & 3] + from + (t >> 2) * (kRawBytes / 2));
+        for (int t = 0; t < 8; ++t) v[t] = lds128(at[t & 3] + from + (t >> 2) * 2 * kW8Block);
         uint32_t f[32];
         auto convert = [&](int half) {
 #pragma unroll
