@@ -53,7 +53,11 @@ struct W8Call {
   int M;
 };
 
-constexpr int kW8DecodeTokens = 32;        // up to here weights are streamed past few tokens
+// Whether M tokens go to the tensor-core kernel: more than 32, or more than 16 through many weights. The streaming
+// kernel's warp MMAs take as long as the weights' bytes from 17 tokens on; the other one's start costs 6 us more. 32
+// tokens through 17 / 34 / 59 / 67 / 235 MB: 9.1 / - / 21.5 / 24.0 / 66 us against 13.8 / - / 15.7 / 20.0 / 43.
+inline bool w8_many(const spear_w8_s* h, int M) { return M > 32 || (M > 16 && (int64_t)h->strips * h->kb > 36 * 1024); }
+
 constexpr int kRowsMaxWidth = 32768;       // 1024 threads x 32 elements in registers
 
 namespace spear {

@@ -136,7 +136,7 @@ extern "C" spear_status_t spear_w8_forward(spear_w8_t h, const int8_t* x, int64_
   if (cudaGetDevice(&dev) != cudaSuccess) return SPEAR_ERR_CUDA;
   if (dev != h->device) return SPEAR_ERR_INVALID_ARG;
   const W8Call c = {x, ld_x, x_scales, y, ld_y, (int)type, M};
-  return M <= kW8DecodeTokens ? w8_launch_decode(h, c, stream) : w8_launch_prefill(h, c, stream);
+  return w8_many(h, M) ? w8_launch_prefill(h, c, stream) : w8_launch_decode(h, c, stream);
 }
 
 extern "C" spear_status_t spear_w8_check(spear_w8_t h, cudaStream_t stream) {

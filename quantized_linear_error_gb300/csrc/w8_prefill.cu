@@ -658,13 +658,13 @@ size_t x16_tokens(const spear_w8_s* h) { return (size_t)h->max_tokens + h->max_t
 }  // namespace
 
 // Arrival counters (2 CTAs x 4 warps a shared tile, fewer than two tiles a pair) and sums of shared tiles: zero between calls.
-size_t w8_prefill_counters(const spear_w8_s* h) { return h->max_tokens > kW8DecodeTokens ? (size_t)h->sm_count * 8 : 0; }
+size_t w8_prefill_counters(const spear_w8_s* h) { return w8_many(h, h->max_tokens) ? (size_t)h->sm_count * 8 : 0; }
 size_t w8_prefill_sums(const spear_w8_s* h) {
-  return h->max_tokens > kW8DecodeTokens ? (size_t)h->sm_count * 2 * kMaxTokens * 128 * sizeof(int) : 0;
+  return w8_many(h, h->max_tokens) ? (size_t)h->sm_count * 2 * kMaxTokens * 128 * sizeof(int) : 0;
 }
 // The tokens in f16.
 size_t w8_prefill_workspace(const spear_w8_s* h) {
-  return h->max_tokens > kW8DecodeTokens ? (size_t)h->kb * 128 * x16_tokens(h) : 0;
+  return w8_many(h, h->max_tokens) ? (size_t)h->kb * 128 * x16_tokens(h) : 0;
 }
 
 spear_status_t w8_launch_prefill(const spear_w8_s* h, const W8Call& c, cudaStream_t stream) {
