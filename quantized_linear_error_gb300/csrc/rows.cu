@@ -14,10 +14,11 @@
 // the loads and the stores.
 #include <cuda_fp16.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "kv_device.cuh"
-#include "w8.h"
+#include "w8_device.cuh"
 
 namespace spear {
 namespace {
@@ -76,6 +77,27 @@ SPEAR_DEVINL void store8(T* p, int n, bool vec, const float (&x)[8]) {
   }
 }
 
+// Eight elements from k on of a row of K, by every lane of a warp, lane i + 1 the next eight behind lane i's. fp32 ones
+// are 32 bytes a lane: neighbours trade halves, so that each instruction writes whole sectors.
+template <class T>
+SPEAR_DEVINL void put8(T* row, int k, int K, bool vec, const float (&x)[8]) {
+  if (sizeof(T) == 4 && vec && K % 8 == 0) {
+    const bool odd = threadIdx.x & 1;
+    float4 own, got;
+    float* g = &got.x;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) g[j] = __shfl_xor_sync(0xffffffffu, odd ? x[j] : x[4 + j], 1);
+    own = odd ? make_float4(x[4], x[5], x[6], x[7]) : make_float4(x[0], x[1], x[2], x[3]);
+    const int k0 = k & ~8;  // the pair's first element
+    // even lanes: the first halves, of their own eight and of the neighbour's; odd lanes: the second halves
+    float4* to = reinterpret_cast<float4*>(row + k0 + (odd ? 4 : 0));
+    if (k0 < K) to[0] = odd ? got : own;
+    if (k0 + 8 < K) to[2] = odd ? own : got;
+  } else if (k < K) {
+    store8(row + k, K - k, vec && k + 8 <= K, x);
+  }
+}
+
 struct RowsParams {
   const void* x;
   int64_t ld_x;
@@ -96,14 +118,14 @@ struct RowsParams {
 };
 
 // Sum of a and maximum of b over the row's threads, in every one of them.
-template <bool kWarpRows>
+template <bool kWarp>
 SPEAR_DEVINL void reduce_row(float& a, float& b, float2* part) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     a += __shfl_xor_sync(0xffffffffu, a, o);
     b = max_nan(b, __shfl_xor_sync(0xffffffffu, b, o));
   }
-  if (kWarpRows) return;
+  if (kWarp) return;
   const int lane = threadIdx.x & 31, warps = blockDim.x / 32;
   if (lane == 0) part[threadIdx.x / 32] = make_float2(a, b);
   __syncthreads();
@@ -116,45 +138,96 @@ SPEAR_DEVINL void reduce_row(float& a, float& b, float2* part) {
   }
 }
 
-// One row a warp (kWarpRows, K <= 256 NV) or a block: NV groups of eight
-// elements a thread, `stride` groups apart.
-template <class T, int NV, bool kNorm, bool kWarpRows>
-__global__ void __launch_bounds__(kWarpRows ? 256 : 1024) rows_kernel(const __grid_constant__ RowsParams p) {
-  __shared__ float2 part[2][32];
+// 16 bytes to a shared address, past the registers.
+SPEAR_DEVINL void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+SPEAR_DEVINL void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+SPEAR_DEVINL void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+template <class T>
+SPEAR_DEVINL void lds8(uint32_t from, float (&x)[8]) {
+  constexpr int words = sizeof(T) / 2;
+  uint4 w[words];
+#pragma unroll
+  for (int i = 0; i < words; ++i) w[i] = lds128(from + 16 * i);
+  T e[8];
+  memcpy(e, w, sizeof(e));
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = (float)e[i];
+}
+
+// How rows are handed out: a warp (K <= 256 NV) or a block a row, or warps or blocks that go through rows of their own
+// with the next kRing rows on their way: a thread copies what it will work on to shared memory, so that it waits for
+// its own copies alone. Measured, one row after the other / with rows on their way, shares of a plain copy's rate:
+// 12289 rows of 8192 with the residual, bf16, 61 / 94%; 8-bit rows of 12289 x 8192 77 / 97%.
+enum RowsBy { kWarpRow, kBlockRow, kWarpRows, kBlockRows };
+constexpr int kRing = 2, kPartBytes = 3 * 32 * 8;
+
+// NV groups of eight elements a thread, `stride` groups apart.
+// R: the residual's type (kWarpRows and kBlockRows; the others ask each time).
+template <class T, int NV, bool kNorm, int kBy, class R>
+__global__ void __launch_bounds__(kBy == kBlockRow || kBy == kBlockRows ? 1024 : 256) rows_kernel(const __grid_constant__ RowsParams p) {
+  constexpr bool kWarp = kBy == kWarpRow || kBy == kWarpRows, kAhead = kBy == kWarpRows || kBy == kBlockRows;
+  extern __shared__ __align__(16) uint8_t smem[];
+  auto part = reinterpret_cast<float2(*)[32]>(smem);  // [3][32], not for kWarpRow
   kv_follow();
-  const int64_t row = kWarpRows ? (int64_t)blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32 : blockIdx.x;
-  if (row >= p.M) return;  // whole warps, or nobody
-  const int at = kWarpRows ? threadIdx.x & 31 : threadIdx.x, stride = kWarpRows ? 32 : blockDim.x;
+  const int64_t first = kWarp ? (int64_t)blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32 : blockIdx.x;
+  if (first >= p.M) return;  // whole warps, or nobody
+  const int at = kWarp ? threadIdx.x & 31 : threadIdx.x, stride = kWarp ? 32 : blockDim.x;
+  const int64_t next = kWarp ? (int64_t)gridDim.x * (blockDim.x / 32) : gridDim.x;
+
+  // [stage][word][thread] of 16 bytes: x's words, group after group, then the residual's. The two words of eight fp32
+  // elements lie as in the row for a warp's 1 KB, and its lanes copy 512 bytes of it side by side.
+  const int words = sizeof(T) / 2 + (kNorm && p.res ? sizeof(R) / 2 : 0);
+  const int lane = threadIdx.x & 31;
+  const uint32_t step = blockDim.x * 16, ring = smem_u32(smem) + kPartBytes;
+  const uint32_t mine = threadIdx.x * 16, mine32 = (threadIdx.x & ~31) * 32 + lane * 32;
+  // eight elements from k on of `row`, `size` bytes each, to the words at `to`
+  auto copy8 = [&](uint32_t to, const void* row, int64_t k, int size) {
+    const char* src = static_cast<const char*>(row) + k * size;
+    if (size == 2) {
+      if (k < p.K) cp_async16(to + mine, src);
+    } else {
+      const int64_t k0 = k - 8 * lane;  // the warp's
+      const char* src0 = static_cast<const char*>(row) + k0 * 4 + lane * 16;
+      const uint32_t to0 = to + (threadIdx.x & ~31) * 32 + lane * 16;
+      if (k0 + 4 * lane < p.K) cp_async16(to0, src0);
+      if (k0 + 128 + 4 * lane < p.K) cp_async16(to0 + 512, src0 + 512);
+    }
+  };
+  auto read8 = [&](uint32_t from, int size, float (&v)[8]) {
+    if (size == 4) lds8<float>(from + mine32, v);
+    else lds8<T>(from + mine, v);
+  };
+  auto copy = [&](int64_t row, int stage) {
+    if (row < p.M) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int64_t k = (int64_t)(at + i * stride) * 8;  // K is a multiple of 8 here
+        const uint32_t to = ring + (stage * NV + i) * words * step;
+        copy8(to, static_cast<const T*>(p.x) + row * p.ld_x, k, sizeof(T));
+        if (kNorm && p.res) copy8(to + sizeof(T) / 2 * step, static_cast<const R*>(p.res) + row * p.ld_res, k, sizeof(R));
+      }
+    }
+    cp_async_commit();
+  };
+  const uint32_t weight_at = ring + kRing * NV * words * step, weight_words = p.weight_f32 ? 2 : sizeof(T) / 2;
+  if constexpr (kAhead) {
+    if (kNorm)  // the weight's groups behind the ring, for all of the rows
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        copy8(weight_at + i * weight_words * step, p.weight, (int64_t)(at + i * stride) * 8, p.weight_f32 ? 4 : sizeof(T));
+#pragma unroll
+    for (int i = 0; i < kRing; ++i) copy(first + i * next, i);
+  }
 
   float h[NV][8];
-  const T* x = static_cast<const T*>(p.x) + row * p.ld_x;
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int k = (at + i * stride) * 8;
-    load8<true>(x + k, p.K - k, p.vec_x && k + 8 <= p.K, h[i]);
-  }
-  if (kNorm && p.res) {
-    float r[NV][8];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int k = (at + i * stride) * 8;
-      const bool vec = p.vec_res && k + 8 <= p.K;
-      if (p.res_f32) load8<true>(static_cast<const float*>(p.res) + row * p.ld_res + k, p.K - k, vec, r[i]);
-      else load8<true>(static_cast<const T*>(p.res) + row * p.ld_res + k, p.K - k, vec, r[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int k = (at + i * stride) * 8;
-      const bool vec = p.vec_res_out && k + 8 <= p.K;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) h[i][j] += r[i][j];
-      if (p.res_f32) store8(static_cast<float*>(p.res_out) + row * p.ld_res_out + k, p.K - k, vec, h[i]);
-      else store8(static_cast<T*>(p.res_out) + row * p.ld_res_out + k, p.K - k, vec, h[i]);
-    }
-  }
-
   // The weight stays in registers beside one or two groups; more of it is read again from the caches.
-  constexpr bool kHold = kNorm && NV <= 2;
+  constexpr bool kHold = kNorm && NV <= 2 && !kAhead;
   float held_w[kHold ? NV : 1][8];
   auto load_w = [&](int i, float (&w)[8]) {
     const int k = (at + i * stride) * 8;
@@ -175,9 +248,14 @@ __global__ void __launch_bounds__(kWarpRows ? 256 : 1024) rows_kernel(const __gr
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] = h[i][j] * held_w[i][j];
     } else {
-      load_w(i, v);
+      if constexpr (kAhead) {
+        read8(weight_at + i * weight_words * step, p.weight_f32 ? 4 : sizeof(T), v);
+      } else {
+        load_w(i, v);
+      }
+      const bool in = !kAhead || (at + i * stride) * 8 < p.K;  // past the row there may be anything
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] *= h[i][j];
+      for (int j = 0; j < 8; ++j) v[j] = in ? v[j] * h[i][j] : 0.f;
     }
   };
   auto statistics = [&](float& ss, float& top, float2* scratch) {
@@ -192,76 +270,144 @@ __global__ void __launch_bounds__(kWarpRows ? 256 : 1024) rows_kernel(const __gr
         top = max_nan(top, fabsf(v[j]));
       }
     }
-    reduce_row<kWarpRows>(ss, top, scratch);
+    reduce_row<kWarp>(ss, top, scratch);
   };
-  float ss, top, rstd = 1.f;
-  statistics(ss, top, part[0]);
-  if (kNorm) {
-    float eps = p.eps;
-    // squares beyond fp32 (the same for the whole row): h times a power of two, which rstd takes back
-    if (ss > 0x1p120f || (ss < 0x1p-60f && eps < 0x1p-60f)) {
-      const float by = ss > 0x1p120f ? 0x1p-96f : 0x1p80f;
-      eps = eps * by * by;
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) h[i][j] *= by;
-      statistics(ss, top, part[1]);
+  int stage = 0, turn = 0;
+  for (int64_t row = first; row < p.M; row += next) {
+    if constexpr (kAhead) {
+      cp_async_wait<kRing - 1>();
+      __syncwarp();  // what the warp's other lanes have copied
     }
-    rstd = __frsqrt_rn(__fdiv_rn(ss, (float)p.K) + eps);
-    if (!(ss < INFINITY)) rstd = NAN;  // an element that is not finite: the whole row
-  }
-  const float a = kNorm ? top * rstd : top;
-  const bool finite = a < INFINITY, held = finite && a >= 0x1p-100f && top >= 0x1p-110f;
-  const float inv = held ? __fdiv_rn(127.f, top) : 0.f;
-  if (p.q && at == 0) p.scales[row] = held ? __fdiv_rn(a, 127.f) : finite ? 0.f : NAN;
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int k = (at + i * stride) * 8;
-    float v[8];
-    weighted(i, v);
-    if (p.q) {
-      int c[8];
+    for (int i = 0; i < NV; ++i) {
+      const int k = (at + i * stride) * 8;
+      if constexpr (kAhead) {
+        if (k < p.K) read8(ring + (stage * NV + i) * words * step, sizeof(T), h[i]);
+        else
 #pragma unroll
-      for (int j = 0; j < 8; ++j) c[j] = held ? max(-127, min(127, __float2int_rn(v[j] * inv))) : 0;
-      int8_t* dst = p.q + row * p.ld_q + k;
-      if (p.vec_q && k + 8 <= p.K) {
-        uint2 o;
-        o.x = (uint32_t)(c[0] & 255) | (uint32_t)(c[1] & 255) << 8 | (uint32_t)(c[2] & 255) << 16 | (uint32_t)c[3] << 24;
-        o.y = (uint32_t)(c[4] & 255) | (uint32_t)(c[5] & 255) << 8 | (uint32_t)(c[6] & 255) << 16 | (uint32_t)c[7] << 24;
-        *reinterpret_cast<uint2*>(dst) = o;
+          for (int j = 0; j < 8; ++j) h[i][j] = 0.f;
       } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (k + j < p.K) dst[j] = (int8_t)c[j];
+        load8<true>(static_cast<const T*>(p.x) + row * p.ld_x + k, p.K - k, p.vec_x && k + 8 <= p.K, h[i]);
       }
     }
-    if (kNorm && p.y) {
+    if (kNorm && p.res) {
+      float r[NV][8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] *= rstd;
-      store8(static_cast<T*>(p.y) + row * p.ld_y + k, p.K - k, p.vec_y && k + 8 <= p.K, v);
+      for (int i = 0; i < NV; ++i) {
+        const int k = (at + i * stride) * 8;
+        if constexpr (kAhead) {
+          if (k < p.K) read8(ring + ((stage * NV + i) * words + sizeof(T) / 2) * step, sizeof(R), r[i]);
+        } else {
+          const bool vec = p.vec_res && k + 8 <= p.K;
+          if (p.res_f32) load8<true>(static_cast<const float*>(p.res) + row * p.ld_res + k, p.K - k, vec, r[i]);
+          else load8<true>(static_cast<const T*>(p.res) + row * p.ld_res + k, p.K - k, vec, r[i]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int k = (at + i * stride) * 8;
+        if (k < p.K)  // beyond, h stays zero
+#pragma unroll
+          for (int j = 0; j < 8; ++j) h[i][j] += r[i][j];
+        if (kAhead ? sizeof(R) == 4 : p.res_f32) put8(static_cast<float*>(p.res_out) + row * p.ld_res_out, k, p.K, p.vec_res_out, h[i]);
+        else put8(static_cast<T*>(p.res_out) + row * p.ld_res_out, k, p.K, p.vec_res_out, h[i]);
+      }
     }
+    if constexpr (kAhead) {
+      __syncwarp();  // all lanes have read the stage
+      copy(row + kRing * next, stage);
+      if (++stage == kRing) stage = 0;
+    }
+    float ss, top, rstd = 1.f;
+    statistics(ss, top, part[turn]);  // a thread may still read what the row before left there: two in turn
+    turn ^= 1;
+    if (kNorm) {
+      float eps = p.eps;
+      // squares beyond fp32 (the same for the whole row): h times a power of two, which rstd takes back
+      if (ss > 0x1p120f || (ss < 0x1p-60f && eps < 0x1p-60f)) {
+        const float by = ss > 0x1p120f ? 0x1p-96f : 0x1p80f;
+        eps = eps * by * by;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) h[i][j] *= by;
+        statistics(ss, top, part[2]);
+        if (!kWarp) __syncthreads();
+      }
+      rstd = __frsqrt_rn(__fdiv_rn(ss, (float)p.K) + eps);
+      if (!(ss < INFINITY)) rstd = NAN;  // an element that is not finite: the whole row
+    }
+    const float a = kNorm ? top * rstd : top;
+    const bool finite = a < INFINITY, held = finite && a >= 0x1p-100f && top >= 0x1p-110f;
+    const float inv = held ? __fdiv_rn(127.f, top) : 0.f;
+    if (p.q && at == 0) p.scales[row] = held ? __fdiv_rn(a, 127.f) : finite ? 0.f : NAN;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int k = (at + i * stride) * 8;
+      float v[8];
+      weighted(i, v);
+      if (p.q) {
+        // rint by adding 1.5 * 2^23, whose last byte is the code (|v inv| < 127.5); conversions take four times as long
+        uint32_t c[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) c[j] = __float_as_uint(__fadd_rn(__fmul_rn(v[j], inv), 12582912.f));
+        uint2 o;
+        o.x = held ? __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410) : 0u;
+        o.y = held ? __byte_perm(__byte_perm(c[4], c[5], 0x0040), __byte_perm(c[6], c[7], 0x0040), 0x5410) : 0u;
+        int8_t* dst = p.q + row * p.ld_q + k;
+        if (p.vec_q && k + 8 <= p.K) {
+          *reinterpret_cast<uint2*>(dst) = o;
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (k + j < p.K) dst[j] = (int8_t)((j < 4 ? o.x : o.y) >> (8 * (j & 3)));
+        }
+      }
+      if (kNorm && p.y) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] *= rstd;
+        put8(static_cast<T*>(p.y) + row * p.ld_y, k, p.K, p.vec_y, v);
+      }
+    }
+    if constexpr (!kAhead) break;
   }
+}
+
+template <class T, int NV, bool kNorm, bool kWarp>
+spear_status_t launch_rows(const RowsParams& p, int sms, int threads, cudaStream_t stream) {
+  constexpr int kOne = kWarp ? kWarpRow : kBlockRow, kMany = kWarp ? kWarpRows : kBlockRows;
+  const int per = kWarp ? threads / 32 : 1;  // rows of a block at a time
+  const int words = sizeof(T) / 2 + (kNorm && p.res ? (p.res_f32 ? 2 : sizeof(T) / 2) : 0);
+  const size_t smem = ((size_t)kRing * words + (kNorm ? (p.weight_f32 ? 2 : sizeof(T) / 2) : 0)) * NV * threads * 16 + kPartBytes;
+  // Rows that take wide copies, and more than one for each of the blocks that the SMs hold.
+  const int blocks = std::min(1024 / threads, (int)(228 * 1024 / (smem + 1024)));  // of an SM
+  if (blocks > 0 && p.M > (int64_t)blocks * sms * per && p.K % 8 == 0 && p.vec_x && (!p.res || p.vec_res) &&
+      (!kNorm || p.vec_w)) {
+    const bool f32 = kNorm && p.res && p.res_f32 && sizeof(T) == 2;
+    constexpr void (*kernels[2])(RowsParams) = {
+        rows_kernel<T, NV, kNorm, kMany, T>, rows_kernel<T, NV, kNorm, kMany, std::conditional_t<kNorm, float, T>>};
+    static std::atomic<uint64_t> configured[2];
+    if (smem_limit_once(reinterpret_cast<const void*>(kernels[f32]), configured[f32]) != cudaSuccess) return SPEAR_ERR_CUDA;
+    return kv_launch(kernels[f32], dim3(blocks * sms), threads, smem, stream, p);
+  }
+  return kv_launch(rows_kernel<T, NV, kNorm, kOne, T>, dim3((unsigned)((p.M + per - 1) / per)), threads, kPartBytes, stream,
+                   p);
 }
 
 template <class T, bool kNorm>
 spear_status_t launch_rows(const RowsParams& p, int sms, cudaStream_t stream) {
   const int groups = (p.K + 7) / 8;
-  if (groups <= 128) {  // a warp a row: no barrier
-    const dim3 grid((unsigned)((p.M + 7) / 8));
-    if (groups <= 32) return kv_launch(rows_kernel<T, 1, kNorm, true>, grid, 256, 0, stream, p);
-    if (groups <= 64) return kv_launch(rows_kernel<T, 2, kNorm, true>, grid, 256, 0, stream, p);
-    return kv_launch(rows_kernel<T, 4, kNorm, true>, grid, 256, 0, stream, p);
-  }
-  // a block a row: as many threads as it takes where there are few rows, several groups a thread otherwise
-  const int nv = max((groups + 1023) / 1024, p.M <= sms ? 1 : 2);
+  if (groups <= 32) return launch_rows<T, 1, kNorm, true>(p, sms, 256, stream);
+  if (groups <= 64) return launch_rows<T, 2, kNorm, true>(p, sms, 256, stream);
+  if (groups <= 128) return launch_rows<T, 4, kNorm, true>(p, sms, 256, stream);
+  // A block a row: as many threads as it takes where there are few rows, else at most 512, so that two blocks fit an SM.
+  const int nv = p.M <= sms ? (groups + 1023) / 1024 : std::min(4, std::max(2, (groups + 511) / 512));
   const int threads = ((groups + nv - 1) / nv + 31) / 32 * 32;
-  const dim3 grid((unsigned)p.M);
   switch (nv) {
-    case 1: return kv_launch(rows_kernel<T, 1, kNorm, false>, grid, threads, 0, stream, p);
-    case 2: return kv_launch(rows_kernel<T, 2, kNorm, false>, grid, threads, 0, stream, p);
-    case 3: return kv_launch(rows_kernel<T, 3, kNorm, false>, grid, threads, 0, stream, p);
-    default: return kv_launch(rows_kernel<T, 4, kNorm, false>, grid, threads, 0, stream, p);
+    case 1: return launch_rows<T, 1, kNorm, false>(p, sms, threads, stream);
+    case 2: return launch_rows<T, 2, kNorm, false>(p, sms, threads, stream);
+    case 3: return launch_rows<T, 3, kNorm, false>(p, sms, threads, stream);
+    default: return launch_rows<T, 4, kNorm, false>(p, sms, threads, stream);
   }
 }
 
@@ -277,34 +423,51 @@ spear_status_t launch_rows(const RowsParams& p, spear_dtype_t type, cudaStream_t
   }
 }
 
-// Values of 16 codes a thread, along the rows.
+// Values of 16 codes a thread and turn, along the rows. A code's byte (code + 128) under the exponent of 2^23 is 2^23 +
+// 128 + code, exactly.
+constexpr int kTurns = 2;
 template <class T>
 __global__ void __launch_bounds__(256) dequantize_kernel(const int8_t* __restrict__ q, int64_t ld_q,
                                                          const float* __restrict__ scales, int M, int K,
                                                          T* __restrict__ out, int64_t ld_out, int vec) {
   kv_follow();
   const int groups = (K + 15) / 16;
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t row = div_u64(i, groups);
-  if (row >= M) return;
-  const int k = (int)(i - row * groups) * 16;
-  const int8_t* src = q + row * ld_q + k;
-  T* dst = out + row * ld_out + k;
-  const float s = scales[row];
-  int8_t c[16];
-  if (vec && k + 16 <= K) {
-    const uint4 w = *reinterpret_cast<const uint4*>(src);
-    memcpy(c, &w, 16);
-  } else {
+  uint4 w[kTurns];
+  float s[kTurns];
+  int64_t row[kTurns];
+  int k[kTurns];
 #pragma unroll
-    for (int j = 0; j < 16; ++j) c[j] = k + j < K ? src[j] : (int8_t)0;
+  for (int i = 0; i < kTurns; ++i) {
+    const int64_t g = ((int64_t)blockIdx.x * kTurns + i) * 256 + threadIdx.x;
+    row[i] = div_u64(g, groups);
+    k[i] = (int)(g - row[i] * groups) * 16;
+    w[i] = make_uint4(0, 0, 0, 0);
+    s[i] = 0.f;
+    if (row[i] >= M) continue;
+    const int8_t* src = q + row[i] * ld_q + k[i];
+    s[i] = scales[row[i]];
+    if (vec && k[i] + 16 <= K) {
+      w[i] = __ldcs(reinterpret_cast<const uint4*>(src));
+    } else {
+      int8_t c[16];
+#pragma unroll
+      for (int j = 0; j < 16; ++j) c[j] = k[i] + j < K ? src[j] : (int8_t)0;
+      memcpy(&w[i], c, 16);
+    }
   }
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    float v[8];
+  for (int i = 0; i < kTurns; ++i) {
+    if (row[i] >= M) continue;
+    T* dst = out + row[i] * ld_out + k[i];
+    const uint32_t c[4] = {w[i].x ^ kW8Bias, w[i].y ^ kW8Bias, w[i].z ^ kW8Bias, w[i].w ^ kW8Bias};
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = (float)c[8 * h + j] * s;
-    store8(dst + 8 * h, K - k - 8 * h, vec && k + 16 <= K, v);
+    for (int h = 0; h < 2; ++h) {
+      float v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        v[j] = (__uint_as_float(__byte_perm(c[2 * h + j / 4], 0x4B000000u, 0x7440 + (j & 3))) - 8388736.f) * s[i];
+      store8(dst + 8 * h, K - k[i] - 8 * h, vec && k[i] + 16 <= K, v);
+    }
   }
 }
 
@@ -428,7 +591,7 @@ extern "C" spear_status_t spear_dequantize_rows(const int8_t* q, int64_t ld_q, c
                 extents_meet(out, ld_out, s, M, K, scales, 1, 4, M, 1)))
     return SPEAR_ERR_INVALID_ARG;
   if (M == 0) return SPEAR_OK;
-  const int64_t blocks = ((int64_t)M * ((K + 15) / 16) + 255) / 256;
+  const int64_t blocks = ((int64_t)M * ((K + 15) / 16) + 256 * kTurns - 1) / (256 * kTurns);
   if (blocks > 0x7FFFFFFF) return SPEAR_ERR_UNSUPPORTED;
   const int vec = vec_ok(out, ld_out, M, s) && vec_ok(q, ld_q, M, 1);
   const dim3 grid((unsigned)blocks);

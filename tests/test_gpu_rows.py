@@ -122,6 +122,64 @@ def test_norm_outputs_one_by_one_are_the_same(only, wdtype):
     _codes_near(q, s, w8.rms_norm(_np(ro * 0), _np(w), 1e-6, (_np(x) + _np(r)))[1])
 
 
+# rows enough that warps and blocks go through several of their own, of each width class and pair of types
+@pytest.mark.parametrize("x,res,weight", [(BF16, BF16, BF16), (BF16, F32, BF16), (F16, F16, F32), (F16, F32, F32),
+                                          (F32, F32, F32), (BF16, None, F32), (F32, None, F32)])
+@pytest.mark.parametrize("M,K", [(11000, 128), (11000, 264), (5300, 520), (5300, 1016), (1500, 1032), (1300, 4096),
+                                 (700, 8200), (650, 12296), (330, 16384), (170, 20488)])
+def test_many_rows(M, K, x, res, weight):
+    X, W = _rand(K, M, K, dtype=x), _rand(K + 1, K, dtype=weight) + 1
+    R = None if res is None else _rand(K + 2, M, K, dtype=res, scale=3.0)
+    if M > 1000:
+        X[7, 3], X[M - 1, K - 1] = float("nan"), float("inf")
+    ro = None if res is None else torch.empty_like(R)
+    y, q, s = torch.empty_like(X), torch.empty(M, K, dtype=torch.int8, device="cuda"), torch.empty(M, device="cuda")
+    spear.rms_norm(X, W, 1e-5, R, ro, y, q, s)
+    # the same rows a few at a time: the kernel that takes a row and ends
+    for i in list(range(0, M, M // 3)) + [M - 5]:
+        part = slice(i, i + 5)
+        n = X[part].shape[0]
+        y1, q1, s1 = torch.empty_like(X[part]), torch.empty(n, K, dtype=torch.int8, device="cuda"), torch.empty(n, device="cuda")
+        ro1 = None if res is None else torch.empty_like(R[part])
+        spear.rms_norm(X[part], W, 1e-5, None if R is None else R[part], ro1, y1, q1, s1)
+        if R is not None:
+            assert torch.equal(ro[part].nan_to_num(9.0), ro1.nan_to_num(9.0))
+    h = X.double() if R is None else (X.float() + R.float()).double()
+    if R is not None:
+        assert torch.equal(ro.nan_to_num(9.0), (X.float() + R.float()).to(res).nan_to_num(9.0))
+    v = h / (h.square().mean(1, keepdim=True) + 1e-5).sqrt() * W.double()
+    bad = ~h.isfinite().all(1)
+    assert torch.equal(y.isnan().all(1), bad) and torch.equal(s.isnan(), bad) and not q[bad].any()
+    ok = ~bad
+    half, floor = torch.finfo(x).eps / 2, 2.0 ** -25 if x is F16 else 2.0 ** -140
+    tol = v[ok].abs() * (NORM_REL + half * (1 + NORM_REL)) + floor
+    assert bool(((y[ok].double() - v[ok]).abs() <= tol).all())
+    a, sd = v[ok].abs().amax(1), s[ok].double()
+    assert bool(((sd - a / 127).abs() <= a / 127 * (NORM_REL + 2.0 ** -23)).all())
+    assert bool(((q[ok].double() * sd[:, None] - v[ok]).abs() <= sd[:, None] * (0.5 + 127 * 4 * NORM_REL)).all())
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("M,K", [(11000, 128), (5300, 520), (2600, 1024), (1500, 1032), (1300, 4096), (700, 11008),
+                                 (330, 16384), (170, 28672)])
+def test_quantize_many_rows(M, K, dtype):
+    x = _rand(M, M, K + 16, dtype=dtype)[:, 8:8 + K]
+    q, s = spear.quantize_rows(x)
+    qr, sr = w8.quantize_rows(_np(x))
+    assert np.array_equal(q.cpu().numpy(), qr) and np.array_equal(s.cpu().numpy(), sr)
+    out = spear.dequantize_rows(q, s, torch.empty(M, K, dtype=dtype, device="cuda"))
+    assert torch.equal(out, (q.float() * s[:, None]).to(dtype))
+
+
+def test_many_rows_in_place():
+    M, K = 2000, 2048
+    x, w, r = _rand(1, M, K, dtype=BF16), _rand(2, K, dtype=BF16), _rand(3, M, K, dtype=F32)
+    y, ro = torch.empty_like(x), torch.empty_like(r)
+    spear.rms_norm(x, w, 1e-5, r, ro, y)
+    spear.rms_norm(x, w, 1e-5, r, r, x)
+    assert torch.equal(x, y) and torch.equal(r, ro)
+
+
 def test_norm_in_place_and_strided():
     M, K = 70, 1000
     wide = _rand(5, M, 3 * 1008, dtype=BF16)

@@ -114,6 +114,21 @@ def test_the_same_bits_whatever_the_batch():
                 assert torch.equal(_forward(layer, (x[0][a:b], x[1][a:b]), dtype), whole[a:b])
 
 
+def test_many_tiles_and_splits():
+    """Token counts around a tile's, weights of which 17 tokens go to the tensor cores, tiles split over pairs."""
+    for N, K in ((11008, 4096), (2304, 8192), (256 * 76, 512), (20000, 2048)):
+        w = _codes(N, N, K)
+        layer = _layer(w, max_tokens=700)
+        wd, sw = _dev(w[0]).double(), _dev(w[1])
+        for M in (17, 32, 63, 150, 192, 193, 385, 500, 577, 700):
+            x = _codes(M, M, K)
+            y = _forward(layer, x, F32)
+            p = _dev(x[0]).double() @ wd.t()  # integers below 2^24: exact
+            assert float(p.abs().max()) < 2 ** 24
+            assert torch.equal(y, p.float() * _dev(x[1])[:, None] * sw)
+        layer.close()
+
+
 def test_strides_and_untouched_elements():
     N, K = 72, 160
     w = _codes(1, N, K)
