@@ -533,47 +533,84 @@ def rms_norm(x, weight, eps=1e-5, residual=None, residual_out=None, y=None, q=No
     launch. ``residual`` [M][K] (x's type or fp32) is added to x first and the sum goes to ``residual_out`` (default: in
     place). The result goes to ``y`` (x's type), to ``q`` int8 [M][K] with ``scales`` fp32 [M] (8-bit rows, as
     :class:`SpearW8Linear` takes them), or to both. See spear_rms_norm."""
-    r = _rows()
-    f32, (M, K), xt = r.f32, x.shape, x.dtype
-    t = r.types.get(xt, -1)
-    ld_x = _ld("rms_norm", "x", x, M, K, *r.types)
-    w = _vector("rms_norm", "weight", weight, K, xt, f32)
-    rt = rp = ro = ld_r = ld_ro = yp = ld_y = qp = ld_q = sp = 0
+    r = _rows_ or _rows()
+    types, f32, shape, xt, wt = r.types, r.f32, x.shape, x.dtype, weight.dtype
+    M, K = shape
+    # one expression for all of a kind: it is on every step's way
+    ld_x, one = x.stride()
+    ok = (xt in types and (wt is xt or wt is f32) and x.is_cuda and weight.is_cuda and weight.shape == (K,) and
+          weight.is_contiguous())
+    t, rp, ro, ld_r, ld_ro, rt, yp, ld_y, qp, ld_q, sp = types.get(xt, 0), 0, 0, 0, 0, 0, 0, 0, 0, 0, 0
     if residual is not None:
         if residual_out is None:
             residual_out = residual
-        rt = r.types.get(residual.dtype, -1)
-        ld_r = _ld("rms_norm", "residual", residual, M, K, xt, f32)
-        ld_ro = _ld("rms_norm", "residual_out", residual_out, M, K, residual.dtype)
-        rp, ro = residual.data_ptr(), residual_out.data_ptr()
-    elif residual_out is not None:
-        raise ValueError("rms_norm: residual_out without residual")
+        rd = residual.dtype
+        (ld_r, one_r), (ld_ro, one_ro) = residual.stride(), residual_out.stride()
+        ok = (ok and (rd is xt or rd is f32) and residual_out.dtype is rd and residual.shape == shape == residual_out.shape and
+              residual.is_cuda and residual_out.is_cuda and (one_r == 1 == one_ro or K == 1))
+        rt, rp, ro = types.get(rd, 0), residual.data_ptr(), residual_out.data_ptr()
+    else:
+        ok = ok and residual_out is None
     if y is not None:
-        yp, ld_y = y.data_ptr(), _ld("rms_norm", "y", y, M, K, xt)
+        ld_y, one_y = y.stride()
+        ok = ok and y.dtype is xt and y.shape == shape and y.is_cuda and (one_y == 1 or K == 1)
+        yp = y.data_ptr()
     if q is not None and scales is not None:
-        qp, ld_q = q.data_ptr(), _ld("rms_norm", "q", q, M, K, r.i8)
-        sp = _vector("rms_norm", "scales", scales, M, f32)
-    elif q is not None or scales is not None or y is None:
-        raise ValueError("rms_norm: give y, or q and scales, or all three")
-    st = r.norm(x.data_ptr(), ld_x, t, rp, ld_r, ro, ld_ro, rt, w, r.types[weight.dtype], eps, M, K, yp, ld_y, qp, ld_q, sp,
+        ld_q, one_q = q.stride()
+        ok = (ok and q.dtype is r.i8 and q.shape == shape and q.is_cuda and (one_q == 1 or K == 1) and
+              scales.dtype is f32 and scales.shape == (M,) and scales.is_cuda and scales.is_contiguous())
+        qp, sp = q.data_ptr(), scales.data_ptr()
+    else:
+        ok = ok and q is None and scales is None and y is not None
+    if not ok or (one != 1 and K > 1):
+        _bad_norm(r, x, weight, residual, residual_out, y, q, scales)
+    if M < 2:  # the stride of a single row means nothing
+        ld_x = ld_r = ld_ro = ld_y = ld_q = K
+    st = r.norm(x.data_ptr(), ld_x, t, rp, ld_r, ro, ld_ro, rt, weight.data_ptr(), types[wt], eps, M, K, yp, ld_y, qp, ld_q, sp,
                 _stream(stream))
     if st:
         raise SpearError(st, "spear_rms_norm")
     return y if q is None else (q, scales)
 
 
+def _bad_norm(r, x, weight, residual, residual_out, y, q, scales):
+    """Says what is wrong with the arguments of rms_norm."""
+    (M, K), xt = x.shape, x.dtype
+    _ld("rms_norm", "x", x, M, K, *r.types)
+    _vector("rms_norm", "weight", weight, K, xt, r.f32)
+    if residual is not None:
+        _ld("rms_norm", "residual", residual, M, K, xt, r.f32)
+        _ld("rms_norm", "residual_out", residual_out, M, K, residual.dtype)
+    elif residual_out is not None:
+        raise ValueError("rms_norm: residual_out without residual")
+    if y is not None:
+        _ld("rms_norm", "y", y, M, K, xt)
+    if q is not None and scales is not None:
+        _ld("rms_norm", "q", q, M, K, r.i8)
+        _vector("rms_norm", "scales", scales, M, r.f32)
+    raise ValueError("rms_norm: give y, or q and scales, or all three")
+
+
 def quantize_rows(x, q=None, scales=None, stream=None):
     """Rows of x [M][K] (bf16, f16 or fp32) in 8 bits: (q int8 [M][K], scales fp32 [M]), made if not given; activations
     with a scale a token, or weights with a scale an output channel. See spear_quantize_rows."""
-    r = _rows()
-    M, K = x.shape
-    ld_x = _ld("quantize_rows", "x", x, M, K, *r.types)
+    r = _rows_ or _rows()
+    shape, xt = x.shape, x.dtype
+    M, K = shape
     if q is None:
         q = r.empty((M, K), dtype=r.i8, device=x.device)
     if scales is None:
         scales = r.empty((M,), dtype=r.f32, device=x.device)
-    st = r.quantize(x.data_ptr(), ld_x, r.types[x.dtype], M, K, q.data_ptr(), _ld("quantize_rows", "q", q, M, K, r.i8),
-                    _vector("quantize_rows", "scales", scales, M, r.f32), _stream(stream))
+    (ld_x, one), (ld_q, one_q) = x.stride(), q.stride()
+    if not (xt in r.types and x.is_cuda and q.dtype is r.i8 and q.shape == shape and q.is_cuda and
+            (one == 1 == one_q or K == 1) and scales.dtype is r.f32 and scales.shape == (M,) and scales.is_cuda and
+            scales.is_contiguous()):
+        _ld("quantize_rows", "x", x, M, K, *r.types)
+        _ld("quantize_rows", "q", q, M, K, r.i8)
+        _vector("quantize_rows", "scales", scales, M, r.f32)
+    if M < 2:
+        ld_x = ld_q = K
+    st = r.quantize(x.data_ptr(), ld_x, r.types[xt], M, K, q.data_ptr(), ld_q, scales.data_ptr(), _stream(stream))
     if st:
         raise SpearError(st, "spear_quantize_rows")
     return q, scales
@@ -581,11 +618,19 @@ def quantize_rows(x, q=None, scales=None, stream=None):
 
 def dequantize_rows(q, scales, out, stream=None):
     """What 8-bit rows stand for, q * scales, into ``out`` [M][K] (bf16, f16 or fp32). See spear_dequantize_rows."""
-    r = _rows()
-    M, K = q.shape
-    st = r.dequantize(q.data_ptr(), _ld("dequantize_rows", "q", q, M, K, r.i8),
-                      _vector("dequantize_rows", "scales", scales, M, r.f32), M, K, out.data_ptr(),
-                      _ld("dequantize_rows", "out", out, M, K, *r.types), r.types[out.dtype], _stream(stream))
+    r = _rows_ or _rows()
+    shape, ot = q.shape, out.dtype
+    M, K = shape
+    (ld_q, one_q), (ld_o, one) = q.stride(), out.stride()
+    if not (ot in r.types and out.is_cuda and q.dtype is r.i8 and out.shape == shape and q.is_cuda and
+            (one == 1 == one_q or K == 1) and scales.dtype is r.f32 and scales.shape == (M,) and scales.is_cuda and
+            scales.is_contiguous()):
+        _ld("dequantize_rows", "q", q, M, K, r.i8)
+        _ld("dequantize_rows", "out", out, M, K, *r.types)
+        _vector("dequantize_rows", "scales", scales, M, r.f32)
+    if M < 2:
+        ld_q = ld_o = K
+    st = r.dequantize(q.data_ptr(), ld_q, scales.data_ptr(), M, K, out.data_ptr(), ld_o, r.types[ot], _stream(stream))
     if st:
         raise SpearError(st, "spear_dequantize_rows")
     return out
@@ -622,10 +667,17 @@ class SpearW8Linear:
 
     def forward(self, q, scales, y, stream=None):
         """y [M][N] (bf16, f16 or fp32) of the 8-bit rows ``q`` int8 [M][K] with ``scales`` fp32 [M]."""
-        M = q.shape[0]
-        st = self._forward(self.h, q.data_ptr(), _ld("SpearW8Linear", "q", q, M, self.K, self._i8),
-                           _vector("SpearW8Linear", "scales", scales, M, self._f32), y.data_ptr(),
-                           _ld("SpearW8Linear", "y", y, M, self.N, *self._types), self._types[y.dtype], M, _stream(stream))
+        M, K, N, yt = q.shape[0], self.K, self.N, y.dtype
+        (ld_q, one_q), (ld_y, one) = q.stride(), y.stride()
+        if not (q.dtype is self._i8 and q.shape == (M, K) and q.is_cuda and one_q == 1 and yt in self._types and
+                y.shape == (M, N) and y.is_cuda and (one == 1 or N == 1) and scales.dtype is self._f32 and
+                scales.shape == (M,) and scales.is_cuda and scales.is_contiguous()):
+            _ld("SpearW8Linear", "q", q, M, K, self._i8)
+            _ld("SpearW8Linear", "y", y, M, N, *self._types)
+            _vector("SpearW8Linear", "scales", scales, M, self._f32)
+        if M < 2:
+            ld_q, ld_y = K, N
+        st = self._forward(self.h, q.data_ptr(), ld_q, scales.data_ptr(), y.data_ptr(), ld_y, self._types[yt], M, _stream(stream))
         if st:
             raise SpearError(st, "spear_w8_forward")
         return y
