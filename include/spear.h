@@ -541,11 +541,21 @@ typedef struct {
   const float* scales_up;      /* its scales, or NULL */
   spear_act_t activation;      /* of a gated pair (ignored otherwise) */
   int32_t max_tokens;          /* largest M a forward on this handle will use (>= 1) */
+  void* workspace;             /* device, 128-byte aligned, or NULL: the handle allocates its own. A workspace serves any
+                                  number of handles whose calls follow one another (a model's layers), is the library's
+                                  alone while they live, and is larger than the weights of small layers: 31 MB and
+                                  2.25 K bytes a token */
+  int64_t workspace_bytes;     /* at least what spear_w8_workspace says (ignored without a workspace) */
 } spear_w8_desc_t;
 
+/* Bytes of the workspace that a handle of this descriptor needs on the current device (its workspace fields are of no
+ * account). Errors: as for spear_w8_create. */
+spear_status_t spear_w8_workspace(const spear_w8_desc_t* desc, int64_t* bytes);
+
 /* Build a handle from 8-bit weights: the weights are copied and laid out once,
- * in one layout that serves every number of tokens, and `stream` is
- * synchronised, so that the caller may free its buffers.
+ * in one layout that serves every number of tokens, part of the workspace is
+ * cleared, and `stream` is synchronised, so that the caller may free its
+ * buffers. No call that uses the same workspace may be running meanwhile.
  * Errors: INVALID_ARG (null or misaligned pointers, values outside the ranges
  * above), UNSUPPORTED (K > 2^20, N > 2^22, max_tokens > 2^20), OOM, CUDA; *out
  * is NULL then. */
@@ -561,9 +571,10 @@ spear_status_t spear_w8_create(const spear_w8_desc_t* desc, cudaStream_t stream,
  *   x: device int8 [M][ld_x], 16-byte aligned, ld_x a multiple of 16 (M > 1);
  *   x_scales: device fp32 [M]; y: device, `type`, [M][ld_y], apart from x.
  * Up to 32 tokens run in a kernel that streams the weights once, more on the
- * tensor cores. A handle's calls share its workspace: order them on one stream,
- * or by events; distinct handles are independent. The handle belongs to the
- * device that was current at create, which has to be current here.
+ * tensor cores, as do 17 on through more than 36 MB of weights. A handle's calls
+ * share its workspace: order them on one stream, or by events, as those of other
+ * handles with the same workspace; else handles are independent. The handle
+ * belongs to the device that was current at create, which has to be current here.
  * Errors: INVALID_ARG, CUDA. */
 spear_status_t spear_w8_forward(spear_w8_t h, const int8_t* x, int64_t ld_x, const float* x_scales, void* y, int64_t ld_y,
                                 spear_dtype_t type, int32_t M, cudaStream_t stream);

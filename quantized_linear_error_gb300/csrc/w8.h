@@ -33,14 +33,18 @@ struct spear_w8_s {
   int max_tokens;
   uint8_t* w;          // strips * kb blocks
   float* w_scales;     // [strips * 16], in the strips' row order
-  void* ws;                 // all of the following
+  void* control;            // status and counters
   unsigned* status;
   unsigned* counters;       // [strips], of the few-token kernel's shared rows; zero between calls
   unsigned* gemm_counters;  // of the tensor-core kernel's shared tiles; zero between calls
-  int* sums;                // their sums; zero between calls
+  size_t control_bytes;
+  // The workspace: the caller's, which several handles may use in turn, or the handle's own.
+  void* ws;
+  int ws_owned;
   float* part;              // sums of the few-token kernel's shared rows
+  int* sums;                // of the tensor-core kernel's shared tiles; zero between calls
+  size_t sums_bytes;
   uint8_t* x16;             // tokens in f16
-  size_t ws_bytes, zero_bytes;  // the first zero_bytes are cleared at create
 };
 
 struct W8Call {

@@ -45,53 +45,87 @@ bool aligned(const void* p, unsigned a) { return (reinterpret_cast<uintptr_t>(p)
 
 using namespace spear;
 
-extern "C" spear_status_t spear_w8_create(const spear_w8_desc_t* d, cudaStream_t stream, spear_w8_t* out) {
-  if (!out) return SPEAR_ERR_INVALID_ARG;
-  *out = nullptr;
+namespace {
+
+// The sizes that a descriptor asks for, or why not.
+spear_status_t set_up(const spear_w8_desc_t* d, spear_w8_s* h) {
   if (!d || !d->qweight || !d->scales || !aligned(d->qweight, 16) || !aligned(d->scales, 4)) return SPEAR_ERR_INVALID_ARG;
   if (d->K < 16 || d->K % 16 != 0 || d->N < 1 || d->max_tokens < 1) return SPEAR_ERR_INVALID_ARG;
-  const bool gated = d->qweight_up != nullptr;
-  if (gated) {
+  h->gated = d->qweight_up != nullptr;
+  if (h->gated) {
     if (!aligned(d->qweight_up, 16) || !d->scales_up || !aligned(d->scales_up, 4)) return SPEAR_ERR_INVALID_ARG;
     if (d->activation != SPEAR_ACT_SILU && d->activation != SPEAR_ACT_GELU) return SPEAR_ERR_INVALID_ARG;
   } else if (d->scales_up) {
     return SPEAR_ERR_INVALID_ARG;
   }
+  if (d->workspace && (!aligned(d->workspace, 128) || d->workspace_bytes < 0)) return SPEAR_ERR_INVALID_ARG;
   if (d->K > (1 << 20) || d->N > (1 << 22) || d->max_tokens > (1 << 20)) return SPEAR_ERR_UNSUPPORTED;
+  h->K = d->K, h->N = d->N, h->act = d->activation, h->max_tokens = d->max_tokens;
+  h->kb = (d->K + 2 * kW8K - 1) / (2 * kW8K) * 2;
+  h->strips = h->gated ? (d->N + 7) / 8 : (d->N + 15) / 16;
+  h->strips = (h->strips + kW8Tile - 1) / kW8Tile * kW8Tile;
+  if ((int64_t)h->strips * h->kb > 1 << 30) return SPEAR_ERR_UNSUPPORTED;  // block numbers are 32-bit
+  return SPEAR_OK;
+}
+
+spear_status_t look_at_device(spear_w8_s* h) {
+  return cudaGetDevice(&h->device) == cudaSuccess &&
+                 cudaDeviceGetAttribute(&h->sm_count, cudaDevAttrMultiProcessorCount, h->device) == cudaSuccess
+             ? SPEAR_OK
+             : SPEAR_ERR_CUDA;
+}
+
+// [part][sums][x16]: the first two at the same place whatever the layer, so that handles that share a workspace leave
+// each other's zeros alone.
+size_t workspace_bytes(const spear_w8_s* h) {
+  return w8_decode_workspace(h) + w8_prefill_sums(h) + w8_prefill_workspace(h);
+}
+
+}  // namespace
+
+extern "C" spear_status_t spear_w8_workspace(const spear_w8_desc_t* d, int64_t* bytes) {
+  if (!bytes) return SPEAR_ERR_INVALID_ARG;
+  spear_w8_s h = {};
+  spear_status_t st = set_up(d, &h);
+  if (st == SPEAR_OK) st = look_at_device(&h);
+  if (st == SPEAR_OK) *bytes = (int64_t)workspace_bytes(&h);
+  return st;
+}
+
+extern "C" spear_status_t spear_w8_create(const spear_w8_desc_t* d, cudaStream_t stream, spear_w8_t* out) {
+  if (!out) return SPEAR_ERR_INVALID_ARG;
+  *out = nullptr;
   spear_w8_s* h = new (std::nothrow) spear_w8_s();
   if (!h) return SPEAR_ERR_OOM;
-  h->K = d->K, h->N = d->N, h->gated = gated, h->act = d->activation, h->max_tokens = d->max_tokens;
-  h->kb = (d->K + 2 * kW8K - 1) / (2 * kW8K) * 2;
-  h->strips = (gated ? (d->N + 7) / 8 : (d->N + 15) / 16);
-  h->strips = (h->strips + kW8Tile - 1) / kW8Tile * kW8Tile;
-  if ((int64_t)h->strips * h->kb > 1 << 30) {  // block numbers are 32-bit
+  spear_status_t st = set_up(d, h);
+  if (st == SPEAR_OK) st = look_at_device(h);
+  if (st == SPEAR_OK && d->workspace && (size_t)d->workspace_bytes < workspace_bytes(h)) st = SPEAR_ERR_INVALID_ARG;
+  if (st != SPEAR_OK) {
     delete h;
-    return SPEAR_ERR_UNSUPPORTED;
+    return st;
   }
-  cudaError_t e = cudaGetDevice(&h->device);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&h->sm_count, cudaDevAttrMultiProcessorCount, h->device);
   const int64_t blocks = (int64_t)h->strips * h->kb;
-  const size_t w_bytes = (size_t)blocks * kW8Block, s_bytes = (size_t)h->strips * 16 * 4;
-  size_t sums_at = 0;
-  if (e == cudaSuccess) {
-    const size_t words = 32 + h->strips + w8_prefill_counters(h), sums = (words * 4 + 127) / 128 * 128;
-    h->zero_bytes = sums + w8_prefill_sums(h);
-    h->ws_bytes = h->zero_bytes + w8_decode_workspace(h) + w8_prefill_workspace(h);
-    sums_at = sums;
-    e = cudaMalloc(&h->w, w_bytes);
+  h->control_bytes = (32 + h->strips + w8_prefill_counters(h)) * 4;
+  h->sums_bytes = w8_prefill_sums(h);
+  cudaError_t e = cudaMalloc(&h->w, (size_t)blocks * kW8Block);
+  if (e == cudaSuccess) e = cudaMalloc(&h->w_scales, (size_t)h->strips * 16 * 4);
+  if (e == cudaSuccess) e = cudaMalloc(&h->control, h->control_bytes);
+  h->ws = d->workspace;
+  if (e == cudaSuccess && !h->ws) {
+    e = cudaMalloc(&h->ws, workspace_bytes(h));
+    h->ws_owned = 1;
   }
-  if (e == cudaSuccess) e = cudaMalloc(&h->w_scales, s_bytes);
-  if (e == cudaSuccess) e = cudaMalloc(&h->ws, h->ws_bytes);
   if (e == cudaSuccess) {
-    char* ws = static_cast<char*>(h->ws);
-    h->status = static_cast<unsigned*>(h->ws);
+    h->status = static_cast<unsigned*>(h->control);
     h->counters = h->status + 32;
     h->gemm_counters = h->counters + h->strips;
-    h->sums = reinterpret_cast<int*>(ws + sums_at);
-    h->part = reinterpret_cast<float*>(ws + h->zero_bytes);
-    h->x16 = reinterpret_cast<uint8_t*>(ws + h->zero_bytes + w8_decode_workspace(h));
-    e = cudaMemsetAsync(h->ws, 0, h->zero_bytes, stream);
+    char* ws = static_cast<char*>(h->ws);
+    h->part = reinterpret_cast<float*>(ws);
+    h->sums = reinterpret_cast<int*>(ws + w8_decode_workspace(h));
+    h->x16 = reinterpret_cast<uint8_t*>(h->sums) + h->sums_bytes;
+    e = cudaMemsetAsync(h->control, 0, h->control_bytes, stream);
   }
+  if (e == cudaSuccess && h->sums_bytes) e = cudaMemsetAsync(h->sums, 0, h->sums_bytes, stream);
   if (e == cudaSuccess) {
     const int64_t chunks = blocks * 64;
     layout_kernel<<<(unsigned)((chunks + 255) / 256), 256, 0, stream>>>(d->qweight, d->qweight_up, d->N, d->K, h->kb, chunks,
@@ -113,7 +147,7 @@ extern "C" spear_status_t spear_w8_create(const spear_w8_desc_t* d, cudaStream_t
 extern "C" spear_status_t spear_w8_destroy(spear_w8_t h) {
   if (!h) return SPEAR_OK;
   cudaError_t e = cudaSuccess;
-  for (void* p : {static_cast<void*>(h->w), static_cast<void*>(h->w_scales), h->ws}) {
+  for (void* p : {static_cast<void*>(h->w), static_cast<void*>(h->w_scales), h->control, h->ws_owned ? h->ws : nullptr}) {
     const cudaError_t f = p ? cudaFree(p) : cudaSuccess;
     if (f != cudaSuccess) e = f;
   }
@@ -146,7 +180,9 @@ extern "C" spear_status_t spear_w8_check(spear_w8_t h, cudaStream_t stream) {
       cudaStreamSynchronize(stream) != cudaSuccess)
     return SPEAR_ERR_CUDA;
   if (status == 0) return SPEAR_OK;
-  if (cudaMemsetAsync(h->ws, 0, h->zero_bytes, stream) != cudaSuccess || cudaStreamSynchronize(stream) != cudaSuccess)
+  if (cudaMemsetAsync(h->control, 0, h->control_bytes, stream) != cudaSuccess ||
+      (h->sums_bytes && cudaMemsetAsync(h->sums, 0, h->sums_bytes, stream) != cudaSuccess) ||
+      cudaStreamSynchronize(stream) != cudaSuccess)
     return SPEAR_ERR_CUDA;
   return SPEAR_ERR_TIMEOUT;
 }

@@ -40,7 +40,8 @@ class spear_kv_desc_t(ctypes.Structure):
 
 class spear_w8_desc_t(ctypes.Structure):
     _fields_ = [("K", c_int32), ("N", c_int32), ("qweight", c_void_p), ("scales", c_void_p), ("qweight_up", c_void_p),
-                ("scales_up", c_void_p), ("activation", c_int), ("max_tokens", c_int32)]
+                ("scales_up", c_void_p), ("activation", c_int), ("max_tokens", c_int32), ("workspace", c_void_p),
+                ("workspace_bytes", c_int64)]
 
 
 class SpearError(RuntimeError):
@@ -113,6 +114,7 @@ def load(path: Path | None = None):
                                  H, c_int64, H, c_int64, H, H]
     L.spear_quantize_rows.argtypes = [H, c_int64, c_int, c_int32, c_int32, H, c_int64, H, H]
     L.spear_dequantize_rows.argtypes = [H, c_int64, H, c_int32, c_int32, H, c_int64, c_int, H]
+    L.spear_w8_workspace.argtypes = [POINTER(spear_w8_desc_t), POINTER(c_int64)]
     L.spear_w8_create.argtypes = [POINTER(spear_w8_desc_t), H, POINTER(c_void_p)]
     L.spear_w8_forward.argtypes = [H, H, c_int64, H, H, c_int64, c_int, c_int32, H]
     L.spear_w8_check.argtypes = [H, H]
@@ -123,7 +125,7 @@ def load(path: Path | None = None):
                  "spear_linear_forward", "spear_linear_forward_host", "spear_linear_destroy",
                  "spear_linear_dequantize", "spear_linear_check", "spear_linear_debug_set",
                  "spear_kv_create", "spear_kv_append", "spear_kv_read", "spear_kv_attention", "spear_kv_check",
-                 "spear_kv_destroy", "spear_rms_norm", "spear_quantize_rows", "spear_dequantize_rows", "spear_w8_create",
+                 "spear_kv_destroy", "spear_rms_norm", "spear_quantize_rows", "spear_dequantize_rows", "spear_w8_workspace", "spear_w8_create",
                  "spear_w8_forward", "spear_w8_check", "spear_w8_destroy"):
         getattr(L, name).restype = c_int
     _lib = L
@@ -636,6 +638,16 @@ def dequantize_rows(q, scales, out, stream=None):
     return out
 
 
+def w8_workspace_bytes(N, K, max_tokens, gated=False) -> int:
+    """Bytes of the workspace of a :class:`SpearW8Linear` with weights [N][K]; the largest of several layers serves all."""
+    some = 4096  # any address: nothing is read
+    up = some if gated else None
+    d = spear_w8_desc_t(int(K), int(N), some, some, up, up, SPEAR_ACT_SILU, int(max_tokens), None, 0)
+    n = c_int64()
+    _check(load().spear_w8_workspace(byref(d), byref(n)), "spear_w8_workspace")
+    return n.value
+
+
 class SpearW8Linear:
     """Owner of one ``spear_w8_t``: a linear of 8-bit integer weights and activations.
 
@@ -643,9 +655,13 @@ class SpearW8Linear:
     ``up_scales`` of the same shapes the layer is a gated pair, act(x W^T) * (x U^T), ``activation`` "silu" or "gelu" (the
     tanh form). The library copies them; the tensors may be freed after construction. Linears that read the same x (q, k
     and v) are one layer of their weights stacked along N.
+
+    ``workspace`` is a CUDA uint8 tensor of at least :func:`w8_workspace_bytes`, which layers whose calls follow one another
+    may share (the object keeps it); without one the layer has its own.
     """
 
-    def __init__(self, qweight, scales, max_tokens=32, up=None, up_scales=None, activation="silu", stream=None):
+    def __init__(self, qweight, scales, max_tokens=32, up=None, up_scales=None, activation="silu", workspace=None,
+                 stream=None):
         r = _rows()
         N, K = qweight.shape
         acts = {"silu": SPEAR_ACT_SILU, "gelu": SPEAR_ACT_GELU}
@@ -658,11 +674,17 @@ class SpearW8Linear:
                 if _ld("SpearW8Linear", name, w, N, K, r.i8) != K or not w.is_contiguous():
                     raise ValueError(f"SpearW8Linear: {name} must be contiguous")
                 _vector("SpearW8Linear", "the scales of " + name, s, N, r.f32)
-        d = spear_w8_desc_t(K, N, _ptr(qweight), _ptr(scales), _ptr(up), _ptr(up_scales), acts[activation], int(max_tokens))
+        d = spear_w8_desc_t(K, N, _ptr(qweight), _ptr(scales), _ptr(up), _ptr(up_scales), acts[activation], int(max_tokens),
+                            None, 0)
+        if workspace is not None:
+            if not workspace.is_cuda or not workspace.is_contiguous():
+                raise ValueError("SpearW8Linear: workspace must be a contiguous CUDA tensor")
+            d.workspace, d.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
         h = c_void_p()
         L = load()
         _check(L.spear_w8_create(byref(d), _stream(stream), byref(h)), "spear_w8_create")
         self.h, self.K, self.N, self.gated, self.max_tokens = h, K, N, up is not None, int(max_tokens)
+        self.workspace = workspace
         self._forward, self._types, self._i8, self._f32 = L.spear_w8_forward, r.types, r.i8, r.f32
 
     def forward(self, q, scales, y, stream=None):

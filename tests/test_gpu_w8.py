@@ -197,6 +197,40 @@ def test_repeated_and_captured_calls_give_the_same_bits():
     assert a.check() == spear.SPEAR_OK and b.check() == spear.SPEAR_OK
 
 
+def test_layers_share_a_workspace():
+    """Layers of several shapes and token counts on one workspace, in one graph, give what they give alone."""
+    shapes = [(700, 1024, False, 200), (256, 4096, False, 16), (2000, 2048, True, 300), (300, 512, False, 40)]
+    ws = torch.full((max(spear.w8_workspace_bytes(n, k, m, g) for n, k, g, m in shapes),), 255, dtype=torch.uint8, device="cuda")
+    layers = []
+    for i, (N, K, gated, most) in enumerate(shapes):
+        w, u = _codes(i, N, K), _codes(10 + i, N, K) if gated else None
+        up = dict(up=_dev(u[0]), up_scales=_dev(u[1])) if gated else {}
+        layers.append((spear.SpearW8Linear(_dev(w[0]), _dev(w[1]), max_tokens=most, workspace=ws, **up), _layer(w, u, most), K, N, most))
+    calls = []
+    for n, (shared, alone, K, N, most) in enumerate(layers * 2):
+        x = _codes(n, most if n < len(layers) else (most + 1) // 2, K)
+        q, s = _dev(x[0]), _dev(x[1])
+        y = [torch.empty(q.shape[0], N, dtype=BF16, device="cuda") for _ in range(2)]
+        alone.forward(q, s, y[1])
+        calls.append((shared, q, s, y))
+    for shared, q, s, y in calls:
+        shared.forward(q, s, y[0])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for shared, q, s, y in calls:
+            shared.forward(q, s, y[0])
+    for _, _, _, y in calls:
+        assert torch.equal(y[0], y[1])
+        y[0].zero_()
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    for shared, _, _, y in calls:
+        assert torch.equal(y[0], y[1]) and shared.check() == spear.SPEAR_OK
+    with pytest.raises(spear.SpearError):  # too small
+        spear.SpearW8Linear(_dev(_codes(0, 64, 64)[0]), _dev(_codes(0, 64, 64)[1]), max_tokens=100, workspace=ws[:1 << 20])
+
+
 def test_refusals():
     w = _codes(1, 24, 64)
     layer = _layer(w, max_tokens=8)

@@ -16,7 +16,7 @@ def L():
 
 
 def _desc(**kw):
-    d = dict(K=64, N=8, qweight=4096, scales=4096, qweight_up=None, scales_up=None, activation=0, max_tokens=4)
+    d = dict(K=64, N=8, qweight=4096, scales=4096, qweight_up=None, scales_up=None, activation=0, max_tokens=4, workspace=None, workspace_bytes=0)
     d.update(kw)
     return spear.spear_w8_desc_t(*[d[f] for f, _ in spear.spear_w8_desc_t._fields_])
 
@@ -26,7 +26,8 @@ def _desc(**kw):
                                  dict(qweight_up=4096), dict(scales_up=4096), dict(qweight_up=4100, scales_up=4096),
                                  dict(qweight_up=4096, scales_up=4098),
                                  dict(qweight_up=4096, scales_up=4096, activation=2),
-                                 dict(qweight_up=4096, scales_up=4096, activation=-1)])
+                                 dict(qweight_up=4096, scales_up=4096, activation=-1),
+                                 dict(workspace=4096 + 64, workspace_bytes=1 << 30), dict(workspace=4096, workspace_bytes=-1)])
 def test_create_rejects_bad_descriptor(L, bad):
     h = ctypes.c_void_p(1234)
     assert L.spear_w8_create(ctypes.byref(_desc(**bad)), None, ctypes.byref(h)) == BAD
@@ -45,6 +46,9 @@ def test_null_arguments(L):
     h = ctypes.c_void_p()
     assert L.spear_w8_create(None, None, ctypes.byref(h)) == BAD
     assert L.spear_w8_create(ctypes.byref(_desc()), None, None) == BAD
+    assert L.spear_w8_workspace(None, ctypes.byref(ctypes.c_int64())) == BAD
+    assert L.spear_w8_workspace(ctypes.byref(_desc()), None) == BAD
+    assert L.spear_w8_workspace(ctypes.byref(_desc(K=8)), ctypes.byref(ctypes.c_int64())) == BAD
     assert L.spear_w8_forward(None, 16, 64, 16, 16, 8, 0, 1, None) == BAD
     assert L.spear_w8_check(None, None) == BAD
     assert L.spear_w8_destroy(None) == spear.SPEAR_OK
