@@ -625,7 +625,8 @@ struct Cut {
 // calls so long that the power limit lowers the clocks (2048 tokens, 4096 x 14336: 511 ns with TN 192, 447 with 160);
 // 580 at least
 // (8 MMAs of 64 cycles, whatever TN, and the hand-over); the last tile's epilogue 25 TN; adding up a
-// split tile 3000 and 110 TN, which whole tiles that follow it hide. Chunk of 320 tokens, 6144 x 4096: 2 x 160 split 26
+// split tile 3000 and 110 TN, which whole tiles that follow it hide (61 tokens through 22016 x 4096, 86 tiles on 76
+// pairs: 21.6 us; with all of them split 25.9). Chunk of 320 tokens, 6144 x 4096: 2 x 160 split 26
 // us, 2 x 160 whole 21, 3 x 112 21, 4 x 80 27; 512 tokens, 8192 x 8192: 3 x 176 split 54, whole 62, 4 x 128 59 and 58.
 Cut cut(const spear_w8_s* h, int M, size_t room) {
   const int pairs = h->sm_count / 2, ks = h->kb / 2, rows = (h->strips / kW8Tile + 1) / 2;
@@ -639,12 +640,11 @@ Cut cut(const spear_w8_s* h, int M, size_t room) {
       if (best.TN == 0 || c.cycles < best.cycles) best = c;
       const int over = c.tiles % pairs;
       if (over && h->K <= 65536) {  // a sum of K products of codes has to fit 32 bits
-        // together with one round of whole tiles, so that every pair gets as much
-        c.sk_tiles = c.tiles < pairs ? c.tiles : over + pairs;
-        const int64_t units = (int64_t)c.sk_tiles * ks;
-        if (c.tiles < pairs) c.sk_pairs = (int)std::min<int64_t>(pairs, std::max<int64_t>(c.tiles, units / 4));
-        const int64_t join = 3000 + 110 * c.TN, left = (int64_t)(c.tiles - c.sk_tiles) / pairs * ks * stage;
-        c.cycles = (units + c.sk_pairs - 1) / c.sk_pairs * stage + std::max(join, left + 25 * c.TN);
+        // what is over goes first, at least four stages a pair; whole tiles hide its adding up
+        c.sk_tiles = over;
+        const int64_t units = (int64_t)over * ks, whole = c.tiles / pairs * ks * stage, join = 3000 + 110 * c.TN;
+        c.sk_pairs = (int)std::min<int64_t>(pairs, std::max<int64_t>(c.tiles < pairs ? over : 1, units / 4));
+        c.cycles = (units + c.sk_pairs - 1) / c.sk_pairs * stage + std::max(join, whole + 25 * c.TN);
         if (c.cycles < best.cycles) best = c;
       }
     }
