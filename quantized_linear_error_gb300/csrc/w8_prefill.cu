@@ -626,11 +626,12 @@ struct Cut {
 // 580 at least
 // (8 MMAs of 64 cycles, whatever TN, and the hand-over); the last tile's epilogue 25 TN; adding up a
 // split tile 3000 and 110 TN, which whole tiles that follow it hide (61 tokens through 22016 x 4096, 86 tiles on 76
-// pairs: 21.6 us; with all of them split 25.9). Chunk of 320 tokens, 6144 x 4096: 2 x 160 split 26
+// pairs: 23.9 us; with all of them split 25.0); 8000 then (2048 tokens through 4096 x 4096, 13 x 160: 52.1 us with
+// a split, 51.1 without, although that is 96 stages against 88). Chunk of 320 tokens, 6144 x 4096: 2 x 160 split 26
 // us, 2 x 160 whole 21, 3 x 112 21, 4 x 80 27; 512 tokens, 8192 x 8192: 3 x 176 split 54, whole 62, 4 x 128 59 and 58.
 Cut cut(const spear_w8_s* h, int M, size_t room) {
   const int pairs = h->sm_count / 2, ks = h->kb / 2, rows = (h->strips / kW8Tile + 1) / 2;
-  const int beside = (int64_t)M * h->strips * h->kb > (100ll << 30) / (kW8Strip * kW8K) ? 200 : 40;  // 2^37 products
+  const int beside = (int64_t)M * h->strips * h->kb > (64ll << 30) / (kW8Strip * kW8K) ? 200 : 40;  // 2^36 products
   Cut best = {};
   for (int n = (M + kMaxTokens - 1) / kMaxTokens, most = n + 4; n <= most; ++n) {
     Cut c = {((M + n - 1) / n + 15) / 16 * 16, n, rows * n, 0, pairs, 0};
@@ -644,7 +645,7 @@ Cut cut(const spear_w8_s* h, int M, size_t room) {
         c.sk_tiles = over;
         const int64_t units = (int64_t)over * ks, whole = c.tiles / pairs * ks * stage, join = 3000 + 110 * c.TN;
         c.sk_pairs = (int)std::min<int64_t>(pairs, std::max<int64_t>(c.tiles < pairs ? over : 1, units / 4));
-        c.cycles = (units + c.sk_pairs - 1) / c.sk_pairs * stage + std::max(join, whole + 25 * c.TN);
+        c.cycles = (units + c.sk_pairs - 1) / c.sk_pairs * stage + (c.tiles < pairs ? join : std::max(join, whole + 25 * c.TN) + 8000);
         if (c.cycles < best.cycles) best = c;
       }
     }
