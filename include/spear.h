@@ -543,7 +543,7 @@ typedef struct {
   int32_t max_tokens;          /* largest M a forward on this handle will use (>= 1) */
   void* workspace;             /* device, 128-byte aligned, or NULL: the handle allocates its own. A workspace serves any
                                   number of handles whose calls follow one another (a model's layers), is the library's
-                                  alone while they live, and is larger than the weights of small layers: 31 MB and
+                                  alone while they live, and is larger than the weights of small layers: 16 MB and
                                   2.25 K bytes a token */
   int64_t workspace_bytes;     /* at least what spear_w8_workspace says (ignored without a workspace) */
 } spear_w8_desc_t;

@@ -390,8 +390,8 @@ spear_status_t launch_rows(const RowsParams& p, int sms, int threads, cudaStream
     if (smem_limit_once(reinterpret_cast<const void*>(kernels[f32]), configured[f32]) != cudaSuccess) return SPEAR_ERR_CUDA;
     return kv_launch(kernels[f32], dim3(blocks * sms), threads, smem, stream, p);
   }
-  return kv_launch(rows_kernel<T, NV, kNorm, kOne, T>, dim3((unsigned)((p.M + per - 1) / per)), threads, kPartBytes, stream,
-                   p);
+  return kv_launch(rows_kernel<T, NV, kNorm, kOne, T>, dim3((unsigned)(((int64_t)p.M + per - 1) / per)), threads, kPartBytes,
+                   stream, p);
 }
 
 template <class T, bool kNorm>
@@ -529,7 +529,10 @@ extern "C" spear_status_t spear_rms_norm(const void* x, int64_t ld_x, spear_dtyp
   const unsigned sx = size_of(type), sw = size_of(weight_type);
   if (!rows_ok(weight, K, K, sw)) return SPEAR_ERR_INVALID_ARG;
   if (M > 0) {
-    if (q && scales && extents_meet(x, ld_x, sx, M, K, scales, 1, 4, M, 1)) return SPEAR_ERR_INVALID_ARG;
+    if (q && scales &&
+        (extents_meet(x, ld_x, sx, M, K, scales, 1, 4, M, 1) || extents_meet(weight, K, sw, 1, K, scales, 1, 4, M, 1) ||
+         (residual && extents_meet(residual, ld_residual, size_of(residual_type), M, K, scales, 1, 4, M, 1))))
+      return SPEAR_ERR_INVALID_ARG;
     if (!rows_ok(x, ld_x, K, sx) || (!y && !q) || (q && (!scales || !aligned(scales, 4) || ld_q < K)) ||
         (y && !rows_ok(y, ld_y, K, sx)))
       return SPEAR_ERR_INVALID_ARG;

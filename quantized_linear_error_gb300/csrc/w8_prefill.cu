@@ -346,6 +346,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads + 128, 1) g
   if (warp == 0 || warp == 14) {
     // Copies: the handle's own weights ahead of the kernel before this one, the tokens' tiles behind it.
     const bool tokens = warp == 14;
+    bool follows = tokens;  // from here on a wait's time is limited, so not while the kernel before this one may run
     if (tokens) grid_wait();
     const uint32_t leader = elect_leader();
     const int64_t run = (int64_t)p.ks * 4096;  // of a pair of strips
@@ -357,6 +358,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads + 128, 1) g
       const uint8_t* src = tokens ? p.x16 + ((int64_t)(tok * 2 + rank) * p.ks + sg.k0) * b_bytes
                                   : p.w + min(row * 2 + rank, p.w_tiles - 1) * 4 * run + (int64_t)sg.k0 * 4096;
       for (int k = sg.k0; k < sg.k1; ++k) {
+        if (!follows && issued == p.stages) {
+          grid_wait();
+          follows = true;
+        }
         ok = wait_bar(&sh.empty[s], phase);
         if (!ok) break;
         if (tokens) {
@@ -372,6 +377,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads + 128, 1) g
         if (++s == p.stages) s = 0, phase ^= 1;
       }
     }
+    if (!follows) grid_wait();
     if (!ok && lane == 0) atomicOr(p.status, kStatusTimeoutPipe);
     // every stage's MMAs have run before the CTA may leave (or, given up, its copies have landed)
     const int left = min(issued, p.stages);
@@ -381,8 +387,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads + 128, 1) g
       else warp_wait(&sh.raw[s], phase, kWaitNs / 10, 0);
       if (++s == p.stages) s = 0, phase ^= 1;
     }
-    if (!tokens) grid_wait();
   } else if (warp == 1) {
+    grid_wait();
     if (rank == 0) {
       const uint32_t leader = elect_leader();
       const uint32_t idesc = idesc_f16_f32(256, p.TN);
@@ -410,8 +416,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads + 128, 1) g
       }
       if (!ok && lane == 0) atomicOr(p.status, kStatusTimeoutPipe);
     }
-    grid_wait();
   } else if (warp < 10) {
+    grid_wait();
     const int quarter = warp & 3, turn = (warp - 2) >> 2;  // every other stage
     const int r = 32 * quarter + lane;
     const uint32_t base = smem_u32(smem) + b_bytes + (r >> 5) * 4 * kW8Block + ((r >> 4) & 1) * kW8Block;  // quarter's pair
@@ -467,7 +473,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads + 128, 1) g
       skip = k - sg.k1;
     }
     if (!ok && lane == 0) atomicOr(p.status, kStatusTimeoutPipe);
-    grid_wait();
   } else {
     grid_wait();  // the tokens' scales, and what the kernel before this one may still read of y
     const int quarter = warp & 3;
@@ -658,10 +663,10 @@ size_t x16_tokens(const spear_w8_s* h) { return (size_t)h->max_tokens + h->max_t
 
 }  // namespace
 
-// Arrival counters (2 CTAs x 4 warps a shared tile, fewer than two tiles a pair) and sums of shared tiles: zero between calls.
-size_t w8_prefill_counters(const spear_w8_s* h) { return w8_many(h, h->max_tokens) ? (size_t)h->sm_count * 8 : 0; }
+// Arrival counters (2 CTAs x 4 warps a shared tile, fewer than one tile a pair) and sums of shared tiles: zero between calls.
+size_t w8_prefill_counters(const spear_w8_s* h) { return w8_many(h, h->max_tokens) ? (size_t)h->sm_count * 4 : 0; }
 size_t w8_prefill_sums(const spear_w8_s* h) {
-  return w8_many(h, h->max_tokens) ? (size_t)h->sm_count * 2 * kMaxTokens * 128 * sizeof(int) : 0;
+  return w8_many(h, h->max_tokens) ? (size_t)h->sm_count * kMaxTokens * 128 * sizeof(int) : 0;
 }
 // The tokens in f16.
 size_t w8_prefill_workspace(const spear_w8_s* h) {

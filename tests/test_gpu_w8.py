@@ -41,7 +41,7 @@ def _equal(y, want):
 
 
 # (N, K): strips and blocks that are not whole, one and many row groups a CTA, work split between CTAs
-SHAPES = [(1, 16), (8, 64), (17, 80), (128, 256), (300, 1040), (1000, 4096), (4096, 512), (136, 11008), (5000, 144)]
+SHAPES = [(1, 16), (8, 64), (17, 80), (128, 256), (300, 1040), (1000, 4096), (4096, 512), (136, 11008), (5000, 144), (72, 70016)]
 TOKENS = [1, 2, 7, 8, 9, 16, 17, 31, 32, 33, 61, 64, 100, 128, 129, 200, 257]
 
 

@@ -73,7 +73,7 @@ def _norm(L, **kw):
     {**RES, "res": (6 << 20) + 1},
     # results that overlap what is read, each other, the weight or the scales
     dict(y=(1 << 20) + 2 * K), dict(q=1 << 20), dict(q=(3 << 20) + 8), dict(y=2 << 20), dict(scales=(4 << 20) + 16),
-    dict(scales=1 << 20), {**RES, "res_out": (6 << 20) + 2 * K}, {**RES, "res_out": 3 << 20}, {**RES, "y": 6 << 20, "ld_y": K + 8},
+    dict(scales=1 << 20), dict(scales=2 << 20), {**RES, "scales": 6 << 20}, {**RES, "res_out": (6 << 20) + 2 * K}, {**RES, "res_out": 3 << 20}, {**RES, "y": 6 << 20, "ld_y": K + 8},
     {**RES, "res_type": 2, "res_out": 1 << 20}, {**RES, "q": 6 << 20}])
 def test_norm_rejects_bad_arguments(L, bad):
     assert _norm(L, **bad) == BAD
