@@ -187,30 +187,32 @@ __global__ void __launch_bounds__(kBy == kBlockRow || kBy == kBlockRows ? 1024 :
   const uint32_t step = blockDim.x * 16, ring = smem_u32(smem) + kPartBytes;
   const uint32_t mine = threadIdx.x * 16, mine32 = (threadIdx.x & ~31) * 32 + lane * 32;
   // eight elements from k on of `row`, `size` bytes each, to the words at `to`
-  auto copy8 = [&](uint32_t to, const void* row, int64_t k, int size) {
-    const char* src = static_cast<const char*>(row) + k * size;
+  auto copy8 = [&](uint32_t to, const char* row, int k, int size) {
     if (size == 2) {
-      if (k < p.K) cp_async16(to + mine, src);
+      if (k < p.K) cp_async16(to + mine, row + (uint32_t)(k * 2));
     } else {
-      const int64_t k0 = k - 8 * lane;  // the warp's
-      const char* src0 = static_cast<const char*>(row) + k0 * 4 + lane * 16;
-      const uint32_t to0 = to + (threadIdx.x & ~31) * 32 + lane * 16;
-      if (k0 + 4 * lane < p.K) cp_async16(to0, src0);
-      if (k0 + 128 + 4 * lane < p.K) cp_async16(to0 + 512, src0 + 512);
+      const int k0 = k - 4 * lane;  // the warp's first element, and this lane's four from there
+      to += mine32 - lane * 16;
+      const char* src = row + (uint32_t)(k0 * 4);
+      if (k0 < p.K) cp_async16(to, src);
+      if (k0 + 128 < p.K) cp_async16(to + 512, src + 512);
     }
   };
   auto read8 = [&](uint32_t from, int size, float (&v)[8]) {
     if (size == 4) lds8<float>(from + mine32, v);
     else lds8<T>(from + mine, v);
   };
+  const char* const x0 = static_cast<const char*>(p.x);
+  const char* const r0 = static_cast<const char*>(p.res);
   auto copy = [&](int64_t row, int stage) {
     if (row < p.M) {
+      const char *x = x0 + row * p.ld_x * (int)sizeof(T), *r = r0 + row * p.ld_res * (int)sizeof(R);
+      uint32_t to = ring + stage * (NV * words) * step;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int64_t k = (int64_t)(at + i * stride) * 8;  // K is a multiple of 8 here
-        const uint32_t to = ring + (stage * NV + i) * words * step;
-        copy8(to, static_cast<const T*>(p.x) + row * p.ld_x, k, sizeof(T));
-        if (kNorm && p.res) copy8(to + sizeof(T) / 2 * step, static_cast<const R*>(p.res) + row * p.ld_res, k, sizeof(R));
+      for (int i = 0; i < NV; ++i, to += words * step) {
+        const int k = (at + i * stride) * 8;  // K is a multiple of 8 here
+        copy8(to, x, k, sizeof(T));
+        if (kNorm && p.res) copy8(to + sizeof(T) / 2 * step, r, k, sizeof(R));
       }
     }
     cp_async_commit();
@@ -220,54 +222,57 @@ __global__ void __launch_bounds__(kBy == kBlockRow || kBy == kBlockRows ? 1024 :
     if (kNorm)  // the weight's groups behind the ring, for all of the rows
 #pragma unroll
       for (int i = 0; i < NV; ++i)
-        copy8(weight_at + i * weight_words * step, p.weight, (int64_t)(at + i * stride) * 8, p.weight_f32 ? 4 : sizeof(T));
+        copy8(weight_at + i * weight_words * step, static_cast<const char*>(p.weight), (at + i * stride) * 8,
+              p.weight_f32 ? 4 : sizeof(T));
 #pragma unroll
     for (int i = 0; i < kRing; ++i) copy(first + i * next, i);
   }
 
   float h[NV][8];
-  // The weight stays in registers beside one or two groups; more of it is read again from the caches.
-  constexpr bool kHold = kNorm && NV <= 2 && !kAhead;
-  float held_w[kHold ? NV : 1][8];
+  // h w stays in registers beside one or two groups; of more it is made again.
+  constexpr bool kHold = kNorm && NV <= 2;
+  float hw[kHold ? NV : 1][8];
   auto load_w = [&](int i, float (&w)[8]) {
     const int k = (at + i * stride) * 8;
-    const bool vec = p.vec_w && k + 8 <= p.K;
-    if (p.weight_f32) load8<false>(static_cast<const float*>(p.weight) + k, p.K - k, vec, w);
-    else load8<false>(static_cast<const T*>(p.weight) + k, p.K - k, vec, w);
-  };
-  if constexpr (kHold) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) load_w(i, held_w[i]);
-  }
-  // h w of group i
-  auto weighted = [&](int i, float (&v)[8]) {
-    if constexpr (!kNorm) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = h[i][j];
-    } else if constexpr (kHold) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = h[i][j] * held_w[i][j];
+    if constexpr (kAhead) {
+      read8(weight_at + i * weight_words * step, p.weight_f32 ? 4 : sizeof(T), w);
     } else {
-      if constexpr (kAhead) {
-        read8(weight_at + i * weight_words * step, p.weight_f32 ? 4 : sizeof(T), v);
+      const bool vec = p.vec_w && k + 8 <= p.K;
+      if (p.weight_f32) load8<false>(static_cast<const float*>(p.weight) + k, p.K - k, vec, w);
+      else load8<false>(static_cast<const T*>(p.weight) + k, p.K - k, vec, w);
+    }
+  };
+  if constexpr (kHold && !kAhead) {  // beside x, not after it
+#pragma unroll
+    for (int i = 0; i < NV; ++i) load_w(i, hw[i]);
+  }
+  // h w of group i; `loaded`: w is in hw
+  auto weighted = [&](int i, float (&v)[8], bool loaded) {
+    if constexpr (kHold && !kAhead) {
+      if (loaded) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = hw[i][j];
       } else {
         load_w(i, v);
       }
-      const bool in = !kAhead || (at + i * stride) * 8 < p.K;  // past the row there may be anything
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = in ? v[j] * h[i][j] : 0.f;
+    } else if constexpr (kNorm) {
+      load_w(i, v);
     }
+    const bool in = !kAhead || (at + i * stride) * 8 < p.K;  // past the row there may be anything
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = !kNorm ? h[i][j] : in ? v[j] * h[i][j] : 0.f;
   };
-  auto statistics = [&](float& ss, float& top, float2* scratch) {
+  auto statistics = [&](float& ss, float& top, float2* scratch, bool loaded) {
     ss = 0.f, top = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       float v[8];
-      weighted(i, v);
+      weighted(i, v, loaded);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         if (kNorm) ss += h[i][j] * h[i][j];
-        top = max_nan(top, fabsf(v[j]));
+        if (p.q) top = max_nan(top, fabsf(v[j]));
+        if constexpr (kHold) hw[i][j] = v[j];
       }
     }
     reduce_row<kWarp>(ss, top, scratch);
@@ -319,7 +324,7 @@ __global__ void __launch_bounds__(kBy == kBlockRow || kBy == kBlockRows ? 1024 :
       if (++stage == kRing) stage = 0;
     }
     float ss, top, rstd = 1.f;
-    statistics(ss, top, part[turn]);  // a thread may still read what the row before left there: two in turn
+    statistics(ss, top, part[turn], true);  // a thread may still read what the row before left there: two in turn
     turn ^= 1;
     if (kNorm) {
       float eps = p.eps;
@@ -331,7 +336,7 @@ __global__ void __launch_bounds__(kBy == kBlockRow || kBy == kBlockRows ? 1024 :
         for (int i = 0; i < NV; ++i)
 #pragma unroll
           for (int j = 0; j < 8; ++j) h[i][j] *= by;
-        statistics(ss, top, part[2]);
+        statistics(ss, top, part[2], false);
         if (!kWarp) __syncthreads();
       }
       rstd = __frsqrt_rn(__fdiv_rn(ss, (float)p.K) + eps);
@@ -345,7 +350,12 @@ __global__ void __launch_bounds__(kBy == kBlockRow || kBy == kBlockRows ? 1024 :
     for (int i = 0; i < NV; ++i) {
       const int k = (at + i * stride) * 8;
       float v[8];
-      weighted(i, v);
+      if constexpr (kHold) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = hw[i][j];
+      } else {
+        weighted(i, v, false);
+      }
       if (p.q) {
         // rint by adding 1.5 * 2^23, whose last byte is the code (|v inv| < 127.5); conversions take four times as long
         uint32_t c[8];
