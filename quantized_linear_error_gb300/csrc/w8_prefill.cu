@@ -594,29 +594,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads + 128, 1) g
 // Tokens' codes -> f16 tiles of 8 tokens x 64 channels (1 KB), ordered [half of a token tile][k block][tile of the
 // half]: a warp a tile, lane 4 r + t the 16 channels 16 t .. of token r. The order of channels within 16 is that of
 // w8_unpack, as for the weights. Tokens past M and channels past K are zeros.
-constexpr int kConvertTiles = 4;  // k blocks a warp
-__global__ void __launch_bounds__(256) convert_kernel(const int8_t* __restrict__ x, int64_t ld_x, int M, int K, int kb,
-                                                      int half_groups, uint8_t* __restrict__ x16) {
+// Blocks go through the work with the next loads on their way: one fits an SM beside the main kernel's.
+constexpr int kConvertThreads = 256, kConvertTiles = 4;  // k blocks a warp and turn
+__global__ void __launch_bounds__(kConvertThreads) convert_kernel(const int8_t* __restrict__ x, int64_t ld_x, int M, int K,
+                                                                  int kb, int half_groups, int groups,
+                                                                  uint8_t* __restrict__ x16) {
   kv_follow();
   const int lane = threadIdx.x & 31, r = lane >> 2, t = lane & 3;
-  const int group = blockIdx.x, k0 = (blockIdx.y * 8 + threadIdx.x / 32) * kConvertTiles;
-  const int half = group / half_groups, m = group * 8 + r;
-  uint4 v[kConvertTiles];
+  const int step = gridDim.x * (kConvertThreads / 32), turns = (kb + kConvertTiles - 1) / kConvertTiles, tasks = turns * groups;
+  auto load = [&](int task, uint4 (&v)[kConvertTiles]) {
+    const int group = task / turns, k0 = (task - group * turns) * kConvertTiles, m = group * 8 + r;
 #pragma unroll
-  for (int i = 0; i < kConvertTiles; ++i) {
-    const int k = (k0 + i) * kW8K + t * 16;
-    v[i] = make_uint4(0, 0, 0, 0);
-    if (m < M && k < K) v[i] = *reinterpret_cast<const uint4*>(x + m * ld_x + k);
-  }
+    for (int i = 0; i < kConvertTiles; ++i) {
+      const int k = (k0 + i) * kW8K + t * 16;
+      v[i] = make_uint4(0, 0, 0, 0);
+      if (m < M && k < K) v[i] = *reinterpret_cast<const uint4*>(x + m * ld_x + k);
+    }
+  };
+  int task = blockIdx.x * (kConvertThreads / 32) + threadIdx.x / 32;
+  uint4 v[kConvertTiles], next[kConvertTiles];
+  if (task < tasks) load(task, v);
+  for (; task < tasks; task += step) {
+    if (task + step < tasks) load(task + step, next);
+    const int group = task / turns, k0 = (task - group * turns) * kConvertTiles, half = group / half_groups;
+    uint8_t* tile = x16 + (((int64_t)half * kb + k0) * half_groups + (group - half * half_groups)) * 1024 + r * 128;
 #pragma unroll
-  for (int i = 0; i < kConvertTiles; ++i) {
-    if (k0 + i >= kb) break;
-    uint4 a, b;
-    w8_unpack(v[i].x ^ kW8Bias, a.x, a.y), w8_unpack(v[i].y ^ kW8Bias, a.z, a.w);
-    w8_unpack(v[i].z ^ kW8Bias, b.x, b.y), w8_unpack(v[i].w ^ kW8Bias, b.z, b.w);
-    uint8_t* tile = x16 + (((int64_t)half * kb + k0 + i) * half_groups + (group - half * half_groups)) * 1024 + r * 128;
-    *reinterpret_cast<uint4*>(tile + ((2 * t) ^ r) * 16) = a;
-    *reinterpret_cast<uint4*>(tile + ((2 * t + 1) ^ r) * 16) = b;
+    for (int i = 0; i < kConvertTiles; ++i) {
+      uint4 a, b;
+      w8_unpack(v[i].x ^ kW8Bias, a.x, a.y), w8_unpack(v[i].y ^ kW8Bias, a.z, a.w);
+      w8_unpack(v[i].z ^ kW8Bias, b.x, b.y), w8_unpack(v[i].w ^ kW8Bias, b.z, b.w);
+      if (k0 + i < kb) {
+        uint8_t* at = tile + (int64_t)i * half_groups * 1024;
+        *reinterpret_cast<uint4*>(at + ((2 * t) ^ r) * 16) = a;
+        *reinterpret_cast<uint4*>(at + ((2 * t + 1) ^ r) * 16) = b;
+      }
+      v[i] = next[i];
+    }
   }
 }
 
@@ -695,10 +708,10 @@ spear_status_t w8_launch_prefill(const spear_w8_s* h, const W8Call& c, cudaStrea
                                               gemm_kernel<true, true>};
   const int which = 2 * h->gated + (c.type == SPEAR_F32);
   if (smem_limit_once(reinterpret_cast<const void*>(kernels[which]), configured[which]) != cudaSuccess) return SPEAR_ERR_CUDA;
-  const int groups = p.n_tok * p.TN / 8;
-  const dim3 cgrid(groups, (h->kb + 8 * kConvertTiles - 1) / (8 * kConvertTiles));
-  const spear_status_t st = kv_launch(convert_kernel, cgrid, 256, 0, stream, c.x, c.ld_x, c.M, h->K, h->kb, p.TN / 16,
-                                      const_cast<uint8_t*>(p.x16));
+  const int groups = p.n_tok * p.TN / 8, per = kConvertThreads / 32;
+  const int64_t tasks = (int64_t)groups * ((h->kb + kConvertTiles - 1) / kConvertTiles);
+  const spear_status_t st = kv_launch(convert_kernel, dim3((unsigned)std::min<int64_t>((tasks + per - 1) / per, h->sm_count)),
+                                      kConvertThreads, 0, stream, c.x, c.ld_x, c.M, h->K, h->kb, p.TN / 16, groups, h->x16);
   if (st != SPEAR_OK) return st;
   return kv_launch(kernels[which], dim3(grid), kThreads, smem, stream, p);
 }
