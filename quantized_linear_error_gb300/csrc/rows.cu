@@ -11,7 +11,10 @@
 // once, and a row is read once and written once.
 //
 // Bound by memory: a row stays in registers (8 to 32 elements a thread) between
-// the loads and the stores.
+// the loads and the stores. Measured: 12289 rows of 8192, bf16 with a bf16
+// residual, 134 us, 6.0 TB/s or 90% of a plain copy's rate; with an fp32 residual
+// and 8 bits 199 us, 83%; 8-bit rows of 12289 x 8192 bf16 48 us, 94%, of 4096 x
+// 14336 fp32 47 us, 92%; read back 52 us, 86%. One row 2.4 us, a launch's latency.
 #include <cuda_fp16.h>
 
 #include <algorithm>

@@ -27,6 +27,14 @@
 // channels a stage and one thread for both copies, a stage took 530 cycles of
 // that thread, 350 of the dequantising warps and 325 of the issuing one.
 //
+// Measured: 4096 tokens through 2 x 28672 x 8192 (3.85 TFLOP) 1.95 ms in bursts, 1.97
+// PFLOP/s or 103% of a library product's burst rate, 2.03 ms sustained; 2048 tokens
+// x 14336 x 4096 133 us, 94%; tensor pipe active 90% of the time (profile of this
+// case). Small calls are bound by stages of 580 cycles, whatever TN up to 128 (the
+// eight MMAs of a stage then take some 64 cycles each), and by some 9 us of start,
+// tokens' preparation, epilogue and end: 320 tokens x 4096 x 6144 20 us, of which 10
+// in the MMAs' loop.
+//
 // Work is split in whole tiles as long as they fill all pairs; what does not come
 // out even is split along K. The pairs that share a tile add their parts, as 32-bit
 // integers, in memory: no order of the additions changes the sum, so that a
@@ -52,7 +60,6 @@ constexpr int kRawBytes = 2 * kW8Tile * kW8Block;  // 128 rows x 128 channels
 constexpr int kMaxTokens = 192;                    // of a tile: two accumulators and two A slots in 512 columns
 constexpr int kSmem = 225 * 1024;
 constexpr int kMaxStages = 8, kMaxSlots = 4;
-
 
 struct GemmParams {
   const uint8_t *w, *x16;
