@@ -646,9 +646,9 @@ struct Cut {
   int64_t cycles;
 };
 
-// The cut with the least estimated time. Measured, in cycles of an SM: a stage takes the MMAs' 4 TN and 40 more, 200 in
-// calls so long that the power limit lowers the clocks (2048 tokens, 4096 x 14336: 511 ns with TN 192, 447 with 160);
-// 580 at least
+// The cut with the least estimated time. Measured, in cycles of an SM: a stage takes the MMAs' 4 TN and 40 more; its 16
+// KB of codes and 128 TN bytes of tokens come from L2 at 50 bytes a cycle when all SMs ask (1088 tokens through 22016 x
+// 4096: a stage 423 ns with TN 192, 396 with 160, 410 with 128; the call 104, 110, 137 us); 580 at least
 // (8 MMAs of 64 cycles, whatever TN, and the hand-over); the last tile's epilogue 25 TN; adding up a
 // split tile 3000 and 110 TN, which whole tiles that follow it hide (61 tokens through 22016 x 4096, 86 tiles on 76
 // pairs: 23.9 us; with all of them split 25.0); 8000 then (2048 tokens through 4096 x 4096, 13 x 160: 52.1 us with
@@ -656,12 +656,11 @@ struct Cut {
 // us, 2 x 160 whole 21, 3 x 112 21, 4 x 80 27; 512 tokens, 8192 x 8192: 3 x 176 split 54, whole 62, 4 x 128 59 and 58.
 Cut cut(const spear_w8_s* h, int M, size_t room) {
   const int pairs = h->sm_count / 2, ks = h->kb / 2, rows = (h->strips / kW8Tile + 1) / 2;
-  const int beside = (int64_t)M * h->strips * h->kb > (64ll << 30) / (kW8Strip * kW8K) ? 200 : 40;  // 2^36 products
   Cut best = {};
   for (int n = (M + kMaxTokens - 1) / kMaxTokens, most = n + 4; n <= most; ++n) {
     Cut c = {((M + n - 1) / n + 15) / 16 * 16, n, rows * n, 0, pairs, 0};
     if (n < most - 4 + 1 || (size_t)c.TN * n <= room) {
-      const int64_t stage = std::max(4 * c.TN + beside, 580);
+      const int64_t stage = std::max({4 * c.TN + 40, (kRawBytes + 128 * c.TN) / 50, 580});
       c.cycles = (c.tiles + pairs - 1) / pairs * ks * stage + 25 * c.TN;
       if (best.TN == 0 || c.cycles < best.cycles) best = c;
       const int over = c.tiles % pairs;
