@@ -200,6 +200,26 @@ def test_norm_in_place_and_strided():
     _near(y, w8.rms_norm(_np(odd), _np(w), 1e-5)[1], BF16)
 
 
+def test_rows_far_apart():
+    """Offsets past 32 bits, for few rows and for many."""
+    for M, ld in ((5, 1 << 30), (1300, 1 << 22)):
+        K = 2056
+        big = torch.empty((M - 1) * ld + K, dtype=BF16, device="cuda")
+        x = big.as_strided((M, K), (ld, 1))
+        x.copy_(_rand(M, M, K))
+        q = torch.empty((M - 1) * ld + K, dtype=torch.int8, device="cuda").as_strided((M, K), (ld, 1))
+        s = torch.empty(M, device="cuda")
+        spear.quantize_rows(x, q, s)
+        qr, sr = w8.quantize_rows(_np(x))
+        assert np.array_equal(q.cpu().numpy(), qr) and np.array_equal(s.cpu().numpy(), sr)
+        y, w = torch.empty(M, K, dtype=BF16, device="cuda"), _rand(1, K, dtype=BF16)
+        spear.rms_norm(x, w, y=y)
+        assert torch.equal(spear.dequantize_rows(q, s, x), spear.dequantize_rows(q, s, torch.empty_like(y)))
+        near = spear.rms_norm(_rand(M, M, K).bfloat16(), w, y=torch.empty_like(y))
+        assert torch.equal(y, near)
+        del big, x, q
+
+
 def test_norm_rows_that_are_not_finite():
     x, w = _rand(1, 6, 2048, dtype=BF16), _rand(2, 2048, dtype=BF16) + 1
     x[1, 5], x[3, 2047], x[4, 0] = float("nan"), float("inf"), float("-inf")

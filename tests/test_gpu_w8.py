@@ -197,6 +197,67 @@ def test_repeated_and_captured_calls_give_the_same_bits():
     assert a.check() == spear.SPEAR_OK and b.check() == spear.SPEAR_OK
 
 
+def test_two_streams_at_once():
+    """Layers with workspaces of their own, on two streams without an order between them."""
+    K = 2048
+    w, u = [_codes(i, 1400, K) for i in range(2)], [_codes(10 + i, 1400, K) for i in range(2)]
+    layers = [_layer(w[0], max_tokens=300), _layer(w[1], u[1], max_tokens=300)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    calls = []
+    for n, M in enumerate((300, 40, 8, 170, 25, 260)):
+        for i, layer in enumerate(layers):
+            x = _codes(n, M, K)
+            q, s = _dev(x[0]), _dev(x[1])
+            want = torch.empty(M, 1400, dtype=BF16, device="cuda")
+            layer.forward(q, s, want)
+            calls.append((i, q, s, want, torch.empty_like(want)))
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for i, q, s, _, y in calls:
+            layers[i].forward(q, s, y, stream=streams[i])
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, want) for _, _, _, want, y in calls)
+    assert all(layer.check() == spear.SPEAR_OK for layer in layers)
+
+
+def test_many_tokens_of_a_narrow_layer():
+    w = _codes(1, 520, 144)
+    layer = _layer(w, max_tokens=20011)
+    x = _codes(2, 20011, 144)
+    _equal(_forward(layer, x), w8.linear(*x, *w))
+    layer.close()
+
+
+def test_offsets_past_32_bits():
+    """Rows so far apart that elements and bytes from the first one on do not fit 32 bits, and weights of 2.7 GB."""
+    N, K, ld = 72, 160, 1 << 27
+    w = _codes(1, N, K)
+    layer = _layer(w)
+    for M in (20, 40):
+        x = _codes(M, M, K)
+        q = torch.empty((M - 1) * ld + K, dtype=torch.int8, device="cuda").as_strided((M, K), (ld, 1))
+        q.copy_(_dev(x[0]))
+        y = torch.empty((M - 1) * (ld // 2) + N, dtype=BF16, device="cuda").as_strided((M, N), (ld // 2, 1))
+        layer.forward(q, _dev(x[1]), y)
+        _equal(y.contiguous(), w8.linear(*x, *w))
+        del q, y
+    N, K = 131072, 20480
+    g = torch.Generator(device="cuda").manual_seed(0)
+    wq = torch.randint(-127, 128, (N, K), generator=g, device="cuda", dtype=torch.int8)
+    sw = torch.rand(N, generator=g, device="cuda")
+    layer = spear.SpearW8Linear(wq, sw, max_tokens=64)
+    rows = [0, 1, 65535, 104857, 104858, 131070, 131071]  # 104858 * 20480 is past 2^31
+    for M in (3, 50):
+        x = _codes(M, M, K)
+        y = torch.empty(M, N, dtype=F32, device="cuda")
+        layer.forward(_dev(x[0]), _dev(x[1]), y)
+        p = _dev(x[0]).double() @ wq[rows].double().t()
+        assert float(p.abs().max()) < 2 ** 24
+        assert torch.equal(y[:, rows], p.float() * _dev(x[1])[:, None] * sw[rows])
+    assert layer.check() == spear.SPEAR_OK
+    layer.close()
+
+
 def test_layers_share_a_workspace():
     """Layers of several shapes and token counts on one workspace, in one graph, give what they give alone."""
     shapes = [(700, 1024, False, 200), (256, 4096, False, 16), (2000, 2048, True, 300), (300, 512, False, 40)]
