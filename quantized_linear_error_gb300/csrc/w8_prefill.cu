@@ -190,6 +190,12 @@ SPEAR_DEVINL void umma2_commit(uint32_t leader, uint64_t* bar) {
       : "memory");
 }
 
+SPEAR_DEVINL uint16_t lds16(uint32_t addr) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));
+  return v;
+}
+
 // 32 rows x 16 columns of an accumulator: v[8 h + 4 i + e] is row 16 h + lane / 4 + 8 (e / 2), column 8 i + 2 (lane % 4)
 // + e % 2, the fragment of 8 x 8 matrices, so that a store of transposed matrices gives rows of tokens, and both
 // projections of a gated output stand in one lane.
@@ -238,18 +244,23 @@ struct Epilogue {
     const __half2 h = __floats2half2_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&h);
   }
-  // Eight neighbouring outputs of token m.
-  SPEAR_DEVINL void store8(uint32_t from, int m, int n) const {
-    if (m >= p.M) return;
-    const uint4 w = lds128(from);
-    uint16_t* y = static_cast<uint16_t*>(p.y) + m * p.ld_y + n;
-    if (p.vec && n + 8 <= p.N) {
-      *reinterpret_cast<uint4*>(y) = w;
-    } else {
-      const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+  // kOuts neighbouring outputs of each of 16 tokens, `step` bytes apart in shared memory from `from` on.
+  template <int kOuts>
+  SPEAR_DEVINL void store(uint32_t from, uint32_t step, int m0) const {
+    uint16_t* const y = static_cast<uint16_t*>(p.y);
+    if (p.vec && n0 + kOuts <= p.N) {  // eight outputs a lane
+      constexpr int kLanes = kOuts / 8, kTurns = kLanes / 2;
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (n + i < p.N) y[i] = (uint16_t)(words[i / 2] >> (16 * (i & 1)));
+      for (int i = 0; i < kTurns; ++i) {
+        const int t = i * (32 / kLanes) + lane / kLanes, q = lane % kLanes;
+        if (m0 + t < p.M) *reinterpret_cast<uint4*>(y + (m0 + t) * p.ld_y + n0 + 8 * q) = lds128(from + t * step + 16 * q);
+      }
+    } else {  // rows of any alignment: an output a lane, side by side
+      constexpr int kAtOnce = 32 / kOuts;
+      const int q = lane % kOuts;
+#pragma unroll 4
+      for (int t = lane / kOuts; t < 16; t += kAtOnce)
+        if (m0 + t < p.M && n0 + q < p.N) y[(m0 + t) * p.ld_y + n0 + q] = lds16(from + t * step + 2 * q);
     }
   }
 
@@ -287,7 +298,7 @@ struct Epilogue {
         store_transposed(at + (8 * (lane >> 4) + (lane & 7)) * 48 + ((lane >> 3) & 1) * 16, pack(v[0], v[1]), pack(v[8], v[9]),
                          pack(v[4], v[5]), pack(v[12], v[13]));
         __syncwarp();
-        store8(at + (lane >> 1) * 48 + (lane & 1) * 16, m0 + (lane >> 1), n0 + (lane & 1) * 8);
+        store<16>(at, 48, m0);
       } else {                 // 64 bytes a token, 80 apart
 #pragma unroll
         for (int i = 0; i < 2; ++i)
@@ -295,9 +306,7 @@ struct Epilogue {
                            pack(v[4 * i + 2], v[4 * i + 3]), pack(v[8 + 4 * i], v[8 + 4 * i + 1]),
                            pack(v[8 + 4 * i + 2], v[8 + 4 * i + 3]));
         __syncwarp();
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          store8(at + (8 * i + (lane >> 2)) * 80 + (lane & 3) * 16, m0 + 8 * i + (lane >> 2), n0 + (lane & 3) * 8);
+        store<32>(at, 80, m0);
       }
     }
   }

@@ -301,3 +301,67 @@ def test_captured_on_another_stream():
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip((ro, q, s, v), want))
+
+
+def _guarded(M, K, lead, ld, dtype, seed=None):
+    """Rows that start `lead` elements behind an aligned address, `ld` apart, with the buffer that holds them."""
+    n = lead + M * ld + 64
+    buf = torch.full((n,), 77, dtype=dtype, device="cuda") if seed is None else _rand(seed, n, dtype=dtype)
+    return buf, buf[lead:].as_strided((M, K), (ld, 1))
+
+
+# Rows that no wide access fits, in number enough that warps and blocks go through several: odd widths, starts and
+# distances, each a different one for every array.
+@pytest.mark.parametrize("x,res", [(BF16, BF16), (BF16, F32), (F16, F16), (F16, F32), (F32, F32), (BF16, None), (F32, None)])
+@pytest.mark.parametrize("M,K", [(11000, 1), (11000, 127), (11000, 256), (5300, 257), (5300, 511), (3000, 517), (2600, 1023),
+                                 (1500, 1025), (1300, 4097), (700, 8191), (400, 12289), (200, 16383), (170, 20487)])
+def test_many_rows_of_any_width(M, K, x, res):
+    xb, X = _guarded(M, K, 3, K + 2, x, 11)
+    rb, R = (None, None) if res is None else _guarded(M, K, 5, K + 1, res, 12)
+    w = _rand(13, K, dtype=x) + 1
+    yb, y = _guarded(M, K, 7, K + 3, x)
+    ob, ro = (None, None) if res is None else _guarded(M, K, 1, K + 5, res)
+    qb, q = _guarded(M, K, 9, K + 7, torch.int8)
+    s = torch.empty(M, device="cuda")
+    spear.rms_norm(X, w, 1e-5, R, ro, y, q, s)
+    h = X.double() if R is None else (X.float() + R.float()).double()
+    v = h / (h.square().mean(1, keepdim=True) + 1e-5).sqrt() * w.double()
+    half, floor = torch.finfo(x).eps / 2, 2.0 ** -25 if x is F16 else 2.0 ** -140
+    assert bool(((y.double() - v).abs() <= v.abs() * (NORM_REL + half * (1 + NORM_REL)) + floor).all())
+    a, sd = v.abs().amax(1), s.double()
+    assert bool(((sd - a / 127).abs() <= a / 127 * (NORM_REL + 2.0 ** -23) + floor).all())
+    assert bool(((q.double() * sd[:, None] - v).abs() <= sd[:, None] * (0.5 + 127 * 4 * NORM_REL) + floor).all())
+    if R is not None:
+        assert torch.equal(ro, (X.float() + R.float()).to(res))
+    keep = [(yb, y), (qb, q)] + ([] if ob is None else [(ob, ro)])
+    for buf, rows in keep:  # nothing beside the rows
+        rows.fill_(77)
+        assert bool((buf == 77).all())
+    # quantised, and in place over x and the residual: the same bits
+    q2b, q2 = _guarded(M, K, 2, K + 1, torch.int8)
+    spear.quantize_rows(X, q2, s)
+    qr, sr = w8.quantize_rows(_np(X))
+    assert np.array_equal(q2.cpu().numpy(), qr) and np.array_equal(s.cpu().numpy(), sr)
+    q2.fill_(77)
+    assert bool((q2b == 77).all())
+    want_y, want_r = torch.empty(M, K, dtype=x, device="cuda"), None if R is None else torch.empty(M, K, dtype=res, device="cuda")
+    spear.rms_norm(X, w, 1e-5, R, want_r, want_y)
+    spear.rms_norm(X, w, 1e-5, R, R, X)
+    assert torch.equal(X, want_y) and (R is None or torch.equal(R, want_r))
+
+
+@pytest.mark.parametrize("out", [BF16, F16, F32])
+@pytest.mark.parametrize("M,K", [(1, 1), (5, 15), (1, 16), (3, 16), (7, 17), (33, 31), (2, 33), (700, 4097), (129, 12289), (4, 16383)])
+def test_read_back_of_any_width(M, K, out):
+    """Rows one after the other, in a buffer that goes on, and rows apart."""
+    codes = torch.randint(-127, 128, (M, K), generator=torch.Generator().manual_seed(K)).to(torch.int8).cuda()
+    s = _rand(M, M).abs() + 0.1
+    want = (codes.float() * s[:, None]).to(out)
+    for lead, ld in ((0, K), (16, K), (1, K), (0, K + 1), (3, K + 8)):
+        _, q = _guarded(M, K, lead, ld, torch.int8)
+        q.copy_(codes)
+        buf, got = _guarded(M, K, lead, ld, out)
+        spear.dequantize_rows(q, s, got)
+        assert torch.equal(got, want)
+        got.fill_(77)
+        assert bool((buf == 77).all())
