@@ -641,8 +641,13 @@ __global__ void __launch_bounds__(kConvertThreads) convert_kernel(const int8_t* 
       w8_unpack(v[i].z ^ kW8Bias, b.x, b.y), w8_unpack(v[i].w ^ kW8Bias, b.z, b.w);
       if (k0 + i < kb) {
         uint8_t* at = tile + (int64_t)i * half_groups * 1024;
-        *reinterpret_cast<uint4*>(at + ((2 * t) ^ r) * 16) = a;
-        *reinterpret_cast<uint4*>(at + ((2 * t + 1) ^ r) * 16) = b;
+        // the lane's two chunks are one sector, the other way round in odd rows (16 bytes a store, half sectors: 320
+        // tokens of 4096 x 6144 20.8 us instead of 19.7)
+        const bool swap = r & 1;
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at + (t ^ (r >> 1)) * 32),
+                     "r"(swap ? b.x : a.x), "r"(swap ? b.y : a.y), "r"(swap ? b.z : a.z), "r"(swap ? b.w : a.w),
+                     "r"(swap ? a.x : b.x), "r"(swap ? a.y : b.y), "r"(swap ? a.z : b.z), "r"(swap ? a.w : b.w)
+                     : "memory");
       }
       v[i] = next[i];
     }
