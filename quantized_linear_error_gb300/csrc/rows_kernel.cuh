@@ -14,7 +14,7 @@
 // the loads and the stores. Measured: 12289 rows of 8192, bf16 with a bf16
 // residual, 142 us, 5.7 TB/s or 85% of a plain copy's rate; with an fp32 residual
 // and 8 bits 170 us, 97%; 8-bit rows of 12289 x 8192 bf16 46 us, 98%, of 4096 x
-// 14336 fp32 48 us, 90%; read back 52 us, 86%. One row 2.4 us, a launch's latency.
+// 14336 fp32 48 us, 90%; One row 2.4 us, a launch's latency.
 // Rows that start at any byte are bound by the instructions that shift their words:
 // 12289 x 8191 in 8 bits 116 us (39%; element by element 24%), the norm of 4096 x
 // 4097 47 us (42%; 20%).
