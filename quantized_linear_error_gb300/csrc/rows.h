@@ -23,6 +23,7 @@ struct RowsParams {
   float eps;
   int res_f32, weight_f32;
   int vec_x, vec_res, vec_res_out, vec_w, vec_y, vec_q;  // rows may be moved in wide accesses
+  int ring;        // rows on their way (of kernels that go through several)
   int staging_at;  // where the warps' shared memory for other stores begins
 };
 

@@ -221,17 +221,17 @@ SPEAR_DEVINL void lds8_any(uint32_t from, uint32_t at, float (&x)[8]) {
 }
 
 // How rows are handed out: a warp (K <= 256 NV) or a block a row, or warps or blocks that go through rows of their own
-// with the next kRing rows on their way: a thread copies what it will work on to shared memory, so that it waits for
-// its own copies alone. Measured, one row after the other / with rows on their way, shares of a plain copy's rate:
+// with the next one or two rows on their way (p.ring): a warp copies what it will work on to shared memory, so that it
+// waits for its own copies alone. Measured, one row after the other / with rows on their way, shares of a plain copy's rate:
 // 12289 rows of 8192 with the residual, bf16, 61 / 94%; 8-bit rows of 12289 x 8192 77 / 97%.
 enum RowsBy { kWarpRow, kBlockRow, kWarpRows, kBlockRows };
-constexpr int kRing = 2, kPartBytes = 3 * 32 * 8;
+constexpr int kPartBytes = 3 * 32 * 8;
 
 // NV groups of eight elements a thread, `stride` groups apart.
 // R: the residual's type (kWarpRows and kBlockRows; the others ask each time).
 // kOdd: rows of any alignment and width (the kernels of one row take them as they come).
-template <class T, int NV, bool kNorm, int kBy, class R, bool kOdd>
-__global__ void __launch_bounds__(kBy == kBlockRow || kBy == kBlockRows ? 1024 : 256) rows_kernel(const __grid_constant__ RowsParams p) {
+template <class T, int NV, bool kNorm, int kBy, class R, bool kOdd, int kThreads>
+__global__ void __launch_bounds__(kThreads, kThreads == 512 && NV < 3 ? 2 : 1) rows_kernel(const __grid_constant__ RowsParams p) {
   constexpr bool kWarp = kBy == kWarpRow || kBy == kWarpRows, kAhead = kBy == kWarpRows || kBy == kBlockRows, kAny = !kAhead || kOdd;
   extern __shared__ __align__(16) uint8_t smem[];
   auto part = reinterpret_cast<float2(*)[32]>(smem);  // [3][32], not for kWarpRow
@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(kBy == kBlockRow || kBy == kBlockRows ? 1024 :
   constexpr int kX = 256 * sizeof(T) + (kOdd ? 32 : 0), kR = 256 * sizeof(R) + (kOdd ? 32 : 0);
   const int lane = threadIdx.x & 31, warps = blockDim.x / 32, warp = threadIdx.x / 32;
   const int group_bytes = (kX + (kNorm && p.res ? kR : 0)) * warps, weight_bytes = 256 * (p.weight_f32 ? 4 : (int)sizeof(T));
-  const uint32_t ring = smem_u32(smem) + kPartBytes, weight_at = ring + kRing * NV * group_bytes;
+  const uint32_t ring = smem_u32(smem) + kPartBytes, weight_at = ring + p.ring * NV * group_bytes;
   const uint32_t staging = smem_u32(smem) + p.staging_at + warp * kStageBytes;
   // the warp's elements from k0 on of `row`, `size` bytes each, to `to`
   auto copy_warp = [&](uint32_t to, const char* row, int k0, int size) {
@@ -295,7 +295,8 @@ __global__ void __launch_bounds__(kBy == kBlockRow || kBy == kBlockRows ? 1024 :
         copy_warp(weight_at + (i * warps + warp) * weight_bytes, static_cast<const char*>(p.weight), (at - lane + i * stride) * 8,
                   p.weight_f32 ? 4 : sizeof(T));
 #pragma unroll
-    for (int i = 0; i < kRing; ++i) copy(first + i * next, i);
+    for (int i = 0; i < 2; ++i)
+      if (i < p.ring) copy(first + i * next, i);
   }
 
   float h[NV][8];
@@ -358,47 +359,56 @@ __global__ void __launch_bounds__(kBy == kBlockRow || kBy == kBlockRows ? 1024 :
   int stage = 0, turn = 0;
   for (int64_t row = first; row < p.M; row += next) {
     if constexpr (kAhead) {
-      cp_async_wait<kRing - 1>();
+      if (p.ring == 2) cp_async_wait<1>();
+      else cp_async_wait<0>();
       __syncwarp();  // what the warp's other lanes have copied
     }
+    auto sum_out = [&](int k, float (&sum)[8]) {
+      if (kAhead ? sizeof(R) == 4 : p.res_f32) put8<kAny>(static_cast<float*>(p.res_out) + row * p.ld_res_out, k, p.K, p.vec_res_out, staging, sum);
+      else put8<kAny>(static_cast<T*>(p.res_out) + row * p.ld_res_out, k, p.K, p.vec_res_out, staging, sum);
+    };
+    if constexpr (kAhead) {  // group by group: all of the residual's beside h would not fit the registers
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int k = (at + i * stride) * 8;
-      if constexpr (kAhead) {
-        read8(ring + (stage * NV + i) * group_bytes + warp * kX, x0 + row * p.ld_x * (int)sizeof(T), sizeof(T), h[i]);
+      for (int i = 0; i < NV; ++i) {
+        const uint32_t from = ring + (stage * NV + i) * group_bytes;
+        read8(from + warp * kX, x0 + row * p.ld_x * (int)sizeof(T), sizeof(T), h[i]);
         inside(i, h[i]);
-      } else {
-        load8<true>(static_cast<const T*>(p.x) + row * p.ld_x + k, p.K - k, p.vec_x && k + 8 <= p.K, h[i]);
+        if (kNorm && p.res) {
+          float r[8];
+          read8(from + warps * kX + warp * kR, r0 + row * p.ld_res * (int)sizeof(R), sizeof(R), r);
+          inside(i, r);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) h[i][j] += r[j];
+          sum_out((at + i * stride) * 8, h[i]);
+        }
       }
-    }
-    if (kNorm && p.res) {
-      float r[NV][8];
+    } else {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int k = (at + i * stride) * 8;
-        if constexpr (kAhead) {
-          read8(ring + (stage * NV + i) * group_bytes + warps * kX + warp * kR, r0 + row * p.ld_res * (int)sizeof(R),
-                sizeof(R), r[i]);
-          inside(i, r[i]);
-        } else {
+        load8<true>(static_cast<const T*>(p.x) + row * p.ld_x + k, p.K - k, p.vec_x && k + 8 <= p.K, h[i]);
+      }
+      if (kNorm && p.res) {
+        float r[NV][8];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          const int k = (at + i * stride) * 8;
           const bool vec = p.vec_res && k + 8 <= p.K;
           if (p.res_f32) load8<true>(static_cast<const float*>(p.res) + row * p.ld_res + k, p.K - k, vec, r[i]);
           else load8<true>(static_cast<const T*>(p.res) + row * p.ld_res + k, p.K - k, vec, r[i]);
         }
-      }
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int k = (at + i * stride) * 8;
+        for (int i = 0; i < NV; ++i) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) h[i][j] += r[i][j];
-        if (kAhead ? sizeof(R) == 4 : p.res_f32) put8<kAny>(static_cast<float*>(p.res_out) + row * p.ld_res_out, k, p.K, p.vec_res_out, staging, h[i]);
-        else put8<kAny>(static_cast<T*>(p.res_out) + row * p.ld_res_out, k, p.K, p.vec_res_out, staging, h[i]);
+          for (int j = 0; j < 8; ++j) h[i][j] += r[i][j];
+          sum_out((at + i * stride) * 8, h[i]);
+        }
       }
     }
     if constexpr (kAhead) {
       __syncwarp();  // all lanes have read the stage
-      copy(row + kRing * next, stage);
-      if (++stage == kRing) stage = 0;
+      copy(row + p.ring * next, stage);
+      if (++stage == p.ring) stage = 0;
     }
     float ss, top, rstd = 1.f;
     statistics(ss, top, part[turn], true);  // a thread may still read what the row before left there: two in turn
@@ -472,22 +482,32 @@ spear_status_t launch_rows(RowsParams p, int sms, int threads, cudaStream_t stre
   const bool odd = !wide || p.K % 8 != 0, f32 = kNorm && p.res && p.res_f32 && sizeof(T) == 2;
   const size_t more = odd ? 32 : 0, stages = wide ? 0 : (size_t)threads / 32 * kStageBytes;
   const size_t group = 256 * sizeof(T) + more + (kNorm && p.res ? 256 * (p.res_f32 ? 4 : sizeof(T)) + more : 0);
-  const size_t ring = (kRing * group + (kNorm ? 256 * (p.weight_f32 ? 4 : sizeof(T)) : 0)) * NV * (threads / 32) + kPartBytes;
-  // More than one row for each of the blocks that the SMs hold.
-  const int blocks = std::min(1024 / threads, (int)(228 * 1024 / (ring + stages + 1024)));  // of an SM
-  if (blocks > 0 && p.M > (int64_t)blocks * sms * per && (!kNorm || p.vec_w)) {
-    using F = std::conditional_t<kNorm, float, T>;
-    constexpr void (*kernels[4])(RowsParams) = {
-        rows_kernel<T, NV, kNorm, kMany, T, false>, rows_kernel<T, NV, kNorm, kMany, F, false>,
-        rows_kernel<T, NV, kNorm, kMany, T, true>, rows_kernel<T, NV, kNorm, kMany, F, true>};
-    static std::atomic<uint64_t> configured[4];
-    const int which = 2 * odd + f32;
-    if (smem_limit_once(reinterpret_cast<const void*>(kernels[which]), configured[which]) != cudaSuccess) return SPEAR_ERR_CUDA;
-    p.staging_at = (int)ring;
-    return kv_launch(kernels[which], dim3(blocks * sms), threads, ring + stages, stream, p);
+  const size_t weight = kNorm ? 256 * (p.weight_f32 ? 4 : sizeof(T)) : 0, warps = threads / 32;
+  auto bytes = [&](int ring) { return (ring * group + weight) * NV * warps + kPartBytes + stages; };
+  // More than one row for each of the blocks that the SMs hold. (A block a row with NV = 1: M <= sms.)
+  if constexpr (kWarp || NV > 1) {
+    // Blocks of an SM: of three and more groups a thread one, whose registers then hold them (two blocks of 64 registers a
+    // thread: norm of 4096 x 14336, bf16, 125 us against 77, of 4096 x 11008 with codes 68 against 65).
+    const int most = !kWarp && NV >= 3 ? 1 : 1024 / threads, room = 227 * 1024;
+    p.ring = bytes(2) <= (size_t)room ? 2 : 1;
+    const int blocks = std::min(most, (int)((room + 1024) / (bytes(p.ring) + 1024)));
+    if (blocks > 0 && p.M > (int64_t)blocks * sms * per && (!kNorm || p.vec_w)) {
+      using F = std::conditional_t<kNorm, float, T>;
+      constexpr int kMost = kWarp ? 256 : 512, kMore = !kWarp && NV == 4 ? 1024 : kMost;  // threads; K > 16384
+      constexpr void (*kernels[8])(RowsParams) = {
+          rows_kernel<T, NV, kNorm, kMany, T, false, kMost>, rows_kernel<T, NV, kNorm, kMany, F, false, kMost>,
+          rows_kernel<T, NV, kNorm, kMany, T, true, kMost>,  rows_kernel<T, NV, kNorm, kMany, F, true, kMost>,
+          rows_kernel<T, NV, kNorm, kMany, T, false, kMore>, rows_kernel<T, NV, kNorm, kMany, F, false, kMore>,
+          rows_kernel<T, NV, kNorm, kMany, T, true, kMore>,  rows_kernel<T, NV, kNorm, kMany, F, true, kMore>};
+      static std::atomic<uint64_t> configured[8];
+      const int which = 2 * odd + f32 + (threads > kMost ? 4 : 0);
+      if (smem_limit_once(reinterpret_cast<const void*>(kernels[which]), configured[which]) != cudaSuccess) return SPEAR_ERR_CUDA;
+      p.staging_at = (int)(bytes(p.ring) - stages);
+      return kv_launch(kernels[which], dim3(blocks * sms), threads, bytes(p.ring), stream, p);
+    }
   }
   p.staging_at = kPartBytes;
-  return kv_launch(rows_kernel<T, NV, kNorm, kOne, T, true>, dim3((unsigned)(((int64_t)p.M + per - 1) / per)), threads,
+  return kv_launch(rows_kernel<T, NV, kNorm, kOne, T, true, kWarp ? 256 : 1024>, dim3((unsigned)(((int64_t)p.M + per - 1) / per)), threads,
                    kPartBytes + stages, stream, p);
 }
 
