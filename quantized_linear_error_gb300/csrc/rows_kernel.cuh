@@ -230,8 +230,8 @@ constexpr int kPartBytes = 3 * 32 * 8;
 // NV groups of eight elements a thread, `stride` groups apart.
 // R: the residual's type (kWarpRows and kBlockRows; the others ask each time).
 // kOdd: rows of any alignment and width (the kernels of one row take them as they come).
-template <class T, int NV, bool kNorm, int kBy, class R, bool kOdd, int kThreads>
-__global__ void __launch_bounds__(kThreads, kThreads == 512 && NV < 3 ? 2 : 1) rows_kernel(const __grid_constant__ RowsParams p) {
+template <class T, int NV, bool kNorm, int kBy, class R, bool kOdd>
+__global__ void __launch_bounds__(kBy == kBlockRow || kBy == kBlockRows ? 1024 : 256) rows_kernel(const __grid_constant__ RowsParams p) {
   constexpr bool kWarp = kBy == kWarpRow || kBy == kWarpRows, kAhead = kBy == kWarpRows || kBy == kBlockRows, kAny = !kAhead || kOdd;
   extern __shared__ __align__(16) uint8_t smem[];
   auto part = reinterpret_cast<float2(*)[32]>(smem);  // [3][32], not for kWarpRow
@@ -486,28 +486,23 @@ spear_status_t launch_rows(RowsParams p, int sms, int threads, cudaStream_t stre
   auto bytes = [&](int ring) { return (ring * group + weight) * NV * warps + kPartBytes + stages; };
   // More than one row for each of the blocks that the SMs hold. (A block a row with NV = 1: M <= sms.)
   if constexpr (kWarp || NV > 1) {
-    // Blocks of an SM: of three and more groups a thread one, whose registers then hold them (two blocks of 64 registers a
-    // thread: norm of 4096 x 14336, bf16, 125 us against 77, of 4096 x 11008 with codes 68 against 65).
-    const int most = !kWarp && NV >= 3 ? 1 : 1024 / threads, room = 227 * 1024;
+    const int most = 1024 / threads, room = 227 * 1024;  // blocks of an SM, whose registers 1024 threads fill
     p.ring = bytes(2) <= (size_t)room ? 2 : 1;
     const int blocks = std::min(most, (int)((room + 1024) / (bytes(p.ring) + 1024)));
     if (blocks > 0 && p.M > (int64_t)blocks * sms * per && (!kNorm || p.vec_w)) {
       using F = std::conditional_t<kNorm, float, T>;
-      constexpr int kMost = kWarp ? 256 : 512, kMore = !kWarp && NV == 4 ? 1024 : kMost;  // threads; K > 16384
-      constexpr void (*kernels[8])(RowsParams) = {
-          rows_kernel<T, NV, kNorm, kMany, T, false, kMost>, rows_kernel<T, NV, kNorm, kMany, F, false, kMost>,
-          rows_kernel<T, NV, kNorm, kMany, T, true, kMost>,  rows_kernel<T, NV, kNorm, kMany, F, true, kMost>,
-          rows_kernel<T, NV, kNorm, kMany, T, false, kMore>, rows_kernel<T, NV, kNorm, kMany, F, false, kMore>,
-          rows_kernel<T, NV, kNorm, kMany, T, true, kMore>,  rows_kernel<T, NV, kNorm, kMany, F, true, kMore>};
-      static std::atomic<uint64_t> configured[8];
-      const int which = 2 * odd + f32 + (threads > kMost ? 4 : 0);
+      constexpr void (*kernels[4])(RowsParams) = {
+          rows_kernel<T, NV, kNorm, kMany, T, false>, rows_kernel<T, NV, kNorm, kMany, F, false>,
+          rows_kernel<T, NV, kNorm, kMany, T, true>, rows_kernel<T, NV, kNorm, kMany, F, true>};
+      static std::atomic<uint64_t> configured[4];
+      const int which = 2 * odd + f32;
       if (smem_limit_once(reinterpret_cast<const void*>(kernels[which]), configured[which]) != cudaSuccess) return SPEAR_ERR_CUDA;
       p.staging_at = (int)(bytes(p.ring) - stages);
       return kv_launch(kernels[which], dim3(blocks * sms), threads, bytes(p.ring), stream, p);
     }
   }
   p.staging_at = kPartBytes;
-  return kv_launch(rows_kernel<T, NV, kNorm, kOne, T, true, kWarp ? 256 : 1024>, dim3((unsigned)(((int64_t)p.M + per - 1) / per)), threads,
+  return kv_launch(rows_kernel<T, NV, kNorm, kOne, T, true>, dim3((unsigned)(((int64_t)p.M + per - 1) / per)), threads,
                    kPartBytes + stages, stream, p);
 }
 
@@ -517,8 +512,10 @@ spear_status_t launch_rows(const RowsParams& p, int sms, cudaStream_t stream) {
   if (groups <= 32) return launch_rows<T, 1, kNorm, true>(p, sms, 256, stream);
   if (groups <= 64) return launch_rows<T, 2, kNorm, true>(p, sms, 256, stream);
   if (groups <= 128) return launch_rows<T, 4, kNorm, true>(p, sms, 256, stream);
-  // A block a row: as many threads as it takes where there are few rows, else at most 512, so that two blocks fit an SM.
-  const int nv = p.M <= sms ? (groups + 1023) / 1024 : std::min(4, std::max(2, (groups + 511) / 512));
+  // A block a row: as many threads as it takes; where there are many rows two groups a thread at least, so that two blocks
+  // fit an SM. (Three and four groups a thread spill: norm of 4096 x 11008 in 480 threads 65 us, in 704 59; of 4096 x
+  // 14336, bf16, 171 in two blocks of 448, 77 in one with more registers, 79 in one of 896.)
+  const int nv = p.M <= sms ? (groups + 1023) / 1024 : std::max(2, (groups + 1023) / 1024);
   const int threads = ((groups + nv - 1) / nv + 31) / 32 * 32;
   switch (nv) {
     case 1: return launch_rows<T, 1, kNorm, false>(p, sms, threads, stream);
