@@ -12,12 +12,12 @@
 //
 // Bound by memory: a row stays in registers (8 to 32 elements a thread) between
 // the loads and the stores. Measured: 12289 rows of 8192, bf16 with a bf16
-// residual, 142 us, 5.7 TB/s or 85% of a plain copy's rate; with an fp32 residual
-// and 8 bits 170 us, 97%; 8-bit rows of 12289 x 8192 bf16 46 us, 98%, of 4096 x
-// 14336 fp32 48 us, 90%; One row 2.4 us, a launch's latency.
-// Rows that start at any byte are bound by the instructions that shift their words:
-// 12289 x 8191 in 8 bits 116 us (39%; element by element 24%), the norm of 4096 x
-// 4097 47 us (42%; 20%).
+// residual, 143 us, 5.6 TB/s or 84% of a plain copy's rate; with an fp32 residual
+// and 8 bits 168 us, 98%; 4096 x 14336 bf16 79 us, 89%; 8-bit rows of 12289 x 8192
+// bf16 46 us, 98%, of 4096 x 14336 fp32 44 us, 99%. One row 2.5 us, a launch's
+// latency. Rows that start at any byte are bound by the instructions that shift
+// their words: 12289 x 8191 in 8 bits 117 us (39%; element by element 24%), the norm
+// of 4096 x 4097 47 us (43%; 20%).
 #pragma once
 #include <algorithm>
 
@@ -227,11 +227,17 @@ SPEAR_DEVINL void lds8_any(uint32_t from, uint32_t at, float (&x)[8]) {
 enum RowsBy { kWarpRow, kBlockRow, kWarpRows, kBlockRows };
 constexpr int kPartBytes = 3 * 32 * 8;
 
+// Blocks of eight warps that go through several rows, of an SM: four groups a lane of the norm need more registers (20000
+// x 517 with four blocks 70 us, with two 52).
+template <int NV, bool kNorm>
+constexpr int kWarpBlocks = kNorm && NV == 4 ? 2 : 4;
+
 // NV groups of eight elements a thread, `stride` groups apart.
 // R: the residual's type (kWarpRows and kBlockRows; the others ask each time).
 // kOdd: rows of any alignment and width (the kernels of one row take them as they come).
 template <class T, int NV, bool kNorm, int kBy, class R, bool kOdd>
-__global__ void __launch_bounds__(kBy == kBlockRow || kBy == kBlockRows ? 1024 : 256) rows_kernel(const __grid_constant__ RowsParams p) {
+__global__ void __launch_bounds__(kBy == kBlockRow || kBy == kBlockRows ? 1024 : 256, kBy == kWarpRows ? (kNorm ? 2 : 4) : kBy == kWarpRow ? 4 : 1)
+    rows_kernel(const __grid_constant__ RowsParams p) {
   constexpr bool kWarp = kBy == kWarpRow || kBy == kWarpRows, kAhead = kBy == kWarpRows || kBy == kBlockRows, kAny = !kAhead || kOdd;
   extern __shared__ __align__(16) uint8_t smem[];
   auto part = reinterpret_cast<float2(*)[32]>(smem);  // [3][32], not for kWarpRow
@@ -486,7 +492,7 @@ spear_status_t launch_rows(RowsParams p, int sms, int threads, cudaStream_t stre
   auto bytes = [&](int ring) { return (ring * group + weight) * NV * warps + kPartBytes + stages; };
   // More than one row for each of the blocks that the SMs hold. (A block a row with NV = 1: M <= sms.)
   if constexpr (kWarp || NV > 1) {
-    const int most = 1024 / threads, room = 227 * 1024;  // blocks of an SM, whose registers 1024 threads fill
+    const int most = kWarp ? kWarpBlocks<NV, kNorm> : 1024 / threads, room = 227 * 1024;  // blocks of an SM: registers
     p.ring = bytes(2) <= (size_t)room ? 2 : 1;
     const int blocks = std::min(most, (int)((room + 1024) / (bytes(p.ring) + 1024)));
     if (blocks > 0 && p.M > (int64_t)blocks * sms * per && (!kNorm || p.vec_w)) {
