@@ -330,7 +330,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads + 128, 1) g
   Shared& sh = *reinterpret_cast<Shared*>(smem + p.stages * p.stage_bytes);
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
   const int rank = (int)cluster_rank(), pair = blockIdx.x / 2, pairs = gridDim.x / 2;
-  grid_launch_dependents();
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.stages; ++s) {
@@ -352,6 +351,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads + 128, 1) g
   __syncthreads();
   cluster_sync();
   tc_fence_after_sync();
+  // Not before tensor memory is held: a kernel that follows may want it too, and would then hold it while it waits for this one.
+  grid_launch_dependents();
   const uint32_t tmem = sh.tmem;
   const uint32_t a_base = tmem + 2 * p.acc_stride;
   const int b_bytes = p.TN * 128;  // half the tokens x 128 channels
