@@ -497,6 +497,9 @@ class _Rows:
         import torch
         self.types = {torch.bfloat16: SPEAR_BF16, torch.float16: SPEAR_F16, torch.float32: SPEAR_F32}
         self.i8, self.f32, self.empty = torch.int8, torch.float32, torch.empty
+        self.device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+        # (device index) -> its current stream's handle
+        self.stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda dev: _stream(None))
         L = load()
         self.norm, self.quantize, self.dequantize = L.spear_rms_norm, L.spear_quantize_rows, L.spear_dequantize_rows
 
@@ -509,6 +512,16 @@ def _rows() -> _Rows:
     if _rows_ is None:
         _rows_ = _Rows()
     return _rows_
+
+
+def _not_here(what, device):
+    raise ValueError(f"{what}: the tensors have to be on one device, which is the current one (they start on cuda:{device})")
+
+
+def _int32(what, **sizes):
+    for name, n in sizes.items():
+        if not -(1 << 31) <= n < 1 << 31:
+            raise ValueError(f"{what}: {name} = {n} is past 32 bits")
 
 
 def _ld(what, name, x, M, K, *dtypes) -> int:
@@ -540,8 +553,9 @@ def rms_norm(x, weight, eps=1e-5, residual=None, residual_out=None, y=None, q=No
     M, K = shape
     # one expression for all of a kind: it is on every step's way
     ld_x, one = x.stride()
-    ok = (xt in types and (wt is xt or wt is f32) and x.is_cuda and weight.is_cuda and weight.shape == (K,) and
-          weight.is_contiguous())
+    dev = x.get_device()
+    ok = (xt in types and (wt is xt or wt is f32) and dev == weight.get_device() and weight.shape == (K,) and
+          weight.is_contiguous() and not (M | K) >> 31)
     t, rp, ro, ld_r, ld_ro, rt, yp, ld_y, qp, ld_q, sp = types.get(xt, 0), 0, 0, 0, 0, 0, 0, 0, 0, 0, 0
     if residual is not None:
         if residual_out is None:
@@ -549,27 +563,27 @@ def rms_norm(x, weight, eps=1e-5, residual=None, residual_out=None, y=None, q=No
         rd = residual.dtype
         (ld_r, one_r), (ld_ro, one_ro) = residual.stride(), residual_out.stride()
         ok = (ok and (rd is xt or rd is f32) and residual_out.dtype is rd and residual.shape == shape == residual_out.shape and
-              residual.is_cuda and residual_out.is_cuda and (one_r == 1 == one_ro or K == 1))
+              dev == residual.get_device() == residual_out.get_device() and (one_r == 1 == one_ro or K == 1))
         rt, rp, ro = types.get(rd, 0), residual.data_ptr(), residual_out.data_ptr()
     else:
         ok = ok and residual_out is None
     if y is not None:
         ld_y, one_y = y.stride()
-        ok = ok and y.dtype is xt and y.shape == shape and y.is_cuda and (one_y == 1 or K == 1)
+        ok = ok and y.dtype is xt and y.shape == shape and y.get_device() == dev and (one_y == 1 or K == 1)
         yp = y.data_ptr()
     if q is not None and scales is not None:
         ld_q, one_q = q.stride()
-        ok = (ok and q.dtype is r.i8 and q.shape == shape and q.is_cuda and (one_q == 1 or K == 1) and
-              scales.dtype is f32 and scales.shape == (M,) and scales.is_cuda and scales.is_contiguous())
+        ok = (ok and q.dtype is r.i8 and q.shape == shape and q.get_device() == dev and (one_q == 1 or K == 1) and
+              scales.dtype is f32 and scales.shape == (M,) and scales.get_device() == dev and scales.is_contiguous())
         qp, sp = q.data_ptr(), scales.data_ptr()
     else:
         ok = ok and q is None and scales is None and y is not None
-    if not ok or (one != 1 and K > 1):
+    if not ok or dev < 0 or (one != 1 and K > 1) or dev != r.device():
         _bad_norm(r, x, weight, residual, residual_out, y, q, scales)
     if M < 2:  # the stride of a single row means nothing
         ld_x = ld_r = ld_ro = ld_y = ld_q = K
     st = r.norm(x.data_ptr(), ld_x, t, rp, ld_r, ro, ld_ro, rt, weight.data_ptr(), types[wt], eps, M, K, yp, ld_y, qp, ld_q, sp,
-                _stream(stream))
+                r.stream(dev) if stream is None else _stream(stream))
     if st:
         raise SpearError(st, "spear_rms_norm")
     return y if q is None else (q, scales)
@@ -590,7 +604,10 @@ def _bad_norm(r, x, weight, residual, residual_out, y, q, scales):
     if q is not None and scales is not None:
         _ld("rms_norm", "q", q, M, K, r.i8)
         _vector("rms_norm", "scales", scales, M, r.f32)
-    raise ValueError("rms_norm: give y, or q and scales, or all three")
+    if (q is None) != (scales is None) or (q is None and y is None):
+        raise ValueError("rms_norm: give y, or q and scales, or all three")
+    _int32("rms_norm", M=M, K=K)
+    _not_here("rms_norm", x.get_device())
 
 
 def quantize_rows(x, q=None, scales=None, stream=None):
@@ -604,15 +621,19 @@ def quantize_rows(x, q=None, scales=None, stream=None):
     if scales is None:
         scales = r.empty((M,), dtype=r.f32, device=x.device)
     (ld_x, one), (ld_q, one_q) = x.stride(), q.stride()
-    if not (xt in r.types and x.is_cuda and q.dtype is r.i8 and q.shape == shape and q.is_cuda and
-            (one == 1 == one_q or K == 1) and scales.dtype is r.f32 and scales.shape == (M,) and scales.is_cuda and
-            scales.is_contiguous()):
+    dev = x.get_device()
+    if not (xt in r.types and q.dtype is r.i8 and q.shape == shape and dev == q.get_device() == scales.get_device() and
+            (one == 1 == one_q or K == 1) and scales.dtype is r.f32 and scales.shape == (M,) and
+            scales.is_contiguous() and not (M | K) >> 31 and dev >= 0 and dev == r.device()):
         _ld("quantize_rows", "x", x, M, K, *r.types)
         _ld("quantize_rows", "q", q, M, K, r.i8)
         _vector("quantize_rows", "scales", scales, M, r.f32)
+        _int32("quantize_rows", M=M, K=K)
+        _not_here("quantize_rows", dev)
     if M < 2:
         ld_x = ld_q = K
-    st = r.quantize(x.data_ptr(), ld_x, r.types[xt], M, K, q.data_ptr(), ld_q, scales.data_ptr(), _stream(stream))
+    st = r.quantize(x.data_ptr(), ld_x, r.types[xt], M, K, q.data_ptr(), ld_q, scales.data_ptr(),
+                    r.stream(dev) if stream is None else _stream(stream))
     if st:
         raise SpearError(st, "spear_quantize_rows")
     return q, scales
@@ -624,15 +645,19 @@ def dequantize_rows(q, scales, out, stream=None):
     shape, ot = q.shape, out.dtype
     M, K = shape
     (ld_q, one_q), (ld_o, one) = q.stride(), out.stride()
-    if not (ot in r.types and out.is_cuda and q.dtype is r.i8 and out.shape == shape and q.is_cuda and
-            (one == 1 == one_q or K == 1) and scales.dtype is r.f32 and scales.shape == (M,) and scales.is_cuda and
-            scales.is_contiguous()):
+    dev = q.get_device()
+    if not (ot in r.types and q.dtype is r.i8 and out.shape == shape and dev == out.get_device() == scales.get_device() and
+            (one == 1 == one_q or K == 1) and scales.dtype is r.f32 and scales.shape == (M,) and
+            scales.is_contiguous() and not (M | K) >> 31 and dev >= 0 and dev == r.device()):
         _ld("dequantize_rows", "q", q, M, K, r.i8)
         _ld("dequantize_rows", "out", out, M, K, *r.types)
         _vector("dequantize_rows", "scales", scales, M, r.f32)
+        _int32("dequantize_rows", M=M, K=K)
+        _not_here("dequantize_rows", dev)
     if M < 2:
         ld_q = ld_o = K
-    st = r.dequantize(q.data_ptr(), ld_q, scales.data_ptr(), M, K, out.data_ptr(), ld_o, r.types[ot], _stream(stream))
+    st = r.dequantize(q.data_ptr(), ld_q, scales.data_ptr(), M, K, out.data_ptr(), ld_o, r.types[ot],
+                      r.stream(dev) if stream is None else _stream(stream))
     if st:
         raise SpearError(st, "spear_dequantize_rows")
     return out
@@ -640,6 +665,7 @@ def dequantize_rows(q, scales, out, stream=None):
 
 def w8_workspace_bytes(N, K, max_tokens, gated=False) -> int:
     """Bytes of the workspace of a :class:`SpearW8Linear` with weights [N][K]; the largest of several layers serves all."""
+    _int32("w8_workspace_bytes", N=int(N), K=int(K), max_tokens=int(max_tokens))
     some = 4096  # any address: nothing is read
     up = some if gated else None
     d = spear_w8_desc_t(int(K), int(N), some, some, up, up, SPEAR_ACT_SILU, int(max_tokens), None, 0)
@@ -674,6 +700,10 @@ class SpearW8Linear:
                 if _ld("SpearW8Linear", name, w, N, K, r.i8) != K or not w.is_contiguous():
                     raise ValueError(f"SpearW8Linear: {name} must be contiguous")
                 _vector("SpearW8Linear", "the scales of " + name, s, N, r.f32)
+        _int32("SpearW8Linear", N=N, K=K, max_tokens=int(max_tokens))
+        dev = qweight.get_device()
+        if dev != r.device() or any(t is not None and t.get_device() != dev for t in (scales, up, up_scales, workspace)):
+            _not_here("SpearW8Linear", dev)
         d = spear_w8_desc_t(K, N, _ptr(qweight), _ptr(scales), _ptr(up), _ptr(up_scales), acts[activation], int(max_tokens),
                             None, 0)
         if workspace is not None:
@@ -685,21 +715,25 @@ class SpearW8Linear:
         _check(L.spear_w8_create(byref(d), _stream(stream), byref(h)), "spear_w8_create")
         self.h, self.K, self.N, self.gated, self.max_tokens = h, K, N, up is not None, int(max_tokens)
         self.workspace = workspace
-        self._forward, self._types, self._i8, self._f32 = L.spear_w8_forward, r.types, r.i8, r.f32
+        self._forward, self._types, self._i8, self._f32, self._device = L.spear_w8_forward, r.types, r.i8, r.f32, dev
+        self._stream = r.stream
 
     def forward(self, q, scales, y, stream=None):
         """y [M][N] (bf16, f16 or fp32) of the 8-bit rows ``q`` int8 [M][K] with ``scales`` fp32 [M]."""
         M, K, N, yt = q.shape[0], self.K, self.N, y.dtype
         (ld_q, one_q), (ld_y, one) = q.stride(), y.stride()
-        if not (q.dtype is self._i8 and q.shape == (M, K) and q.is_cuda and one_q == 1 and yt in self._types and
-                y.shape == (M, N) and y.is_cuda and (one == 1 or N == 1) and scales.dtype is self._f32 and
-                scales.shape == (M,) and scales.is_cuda and scales.is_contiguous()):
+        if not (q.dtype is self._i8 and q.shape == (M, K) and one_q == 1 and yt in self._types and y.shape == (M, N) and
+                self._device == q.get_device() == y.get_device() == scales.get_device() and (one == 1 or N == 1) and
+                scales.dtype is self._f32 and scales.shape == (M,) and scales.is_contiguous() and not M >> 31):
             _ld("SpearW8Linear", "q", q, M, K, self._i8)
             _ld("SpearW8Linear", "y", y, M, N, *self._types)
             _vector("SpearW8Linear", "scales", scales, M, self._f32)
+            _int32("SpearW8Linear", M=M)
+            raise ValueError(f"SpearW8Linear: q, scales and y have to be on the layer's device, cuda:{self._device}")
         if M < 2:
             ld_q, ld_y = K, N
-        st = self._forward(self.h, q.data_ptr(), ld_q, scales.data_ptr(), y.data_ptr(), ld_y, self._types[yt], M, _stream(stream))
+        st = self._forward(self.h, q.data_ptr(), ld_q, scales.data_ptr(), y.data_ptr(), ld_y, self._types[yt], M,
+                           self._stream(self._device) if stream is None else _stream(stream))
         if st:
             raise SpearError(st, "spear_w8_forward")
         return y

@@ -365,3 +365,30 @@ def test_read_back_of_any_width(M, K, out):
         assert torch.equal(got, want)
         got.fill_(77)
         assert bool((buf == 77).all())
+
+
+@pytest.mark.parametrize("M,K", [((1 << 32) + 3, 16), ((1 << 31) + 1, 16), (3, (1 << 32) + 16), (1, (1 << 31))])
+def test_sizes_past_32_bits_mean_what_they_say(M, K):
+    """They are refused, not cut to their lower half. (Views of few elements: nothing is read.)"""
+    def view(dtype, *shape):
+        return torch.empty(1, dtype=dtype, device="cuda").as_strided(shape, (0,) * (len(shape) - 1) + (1,)) if shape[-1] == 1 \
+            else torch.empty(64, dtype=dtype, device="cuda")[:1].expand(shape)
+    x, q, s, w = view(BF16, M, K), view(torch.int8, M, K), view(F32, M), view(BF16, K)
+    with pytest.raises(ValueError):
+        spear.rms_norm(x, w, 1e-5, q=q, scales=s)
+    with pytest.raises(ValueError):
+        spear.quantize_rows(x, q, s)
+    with pytest.raises(ValueError):
+        spear.dequantize_rows(q, s, x)
+
+
+def test_rows_and_results_on_one_device():
+    x, w = torch.zeros(4, 64, dtype=BF16, device="cuda"), torch.ones(64, dtype=BF16, device="cuda")
+    q, s = torch.zeros(4, 64, dtype=torch.int8, device="cuda"), torch.zeros(4, device="cuda")
+    for call in (lambda: spear.rms_norm(x, w.cpu(), y=x), lambda: spear.rms_norm(x.cpu(), w, y=x.cpu()),
+                 lambda: spear.rms_norm(x, w, residual=x.cpu(), y=x), lambda: spear.rms_norm(x, w, q=q, scales=s.cpu()),
+                 lambda: spear.rms_norm(x, w, y=x.cpu()), lambda: spear.quantize_rows(x, q.cpu(), s),
+                 lambda: spear.quantize_rows(x.cpu(), q.cpu(), s.cpu()), lambda: spear.dequantize_rows(q, s, x.cpu()),
+                 lambda: spear.dequantize_rows(q, s.cpu(), x)):
+        with pytest.raises(ValueError):
+            call()

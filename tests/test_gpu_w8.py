@@ -353,3 +353,27 @@ def test_rows_to_product_and_back():
     full = (torch.nn.functional.silu(hn @ W.double().t()) * (hn @ U.double().t())) @ D.double().t()
     assert (y.double() - full).norm() / full.norm() < 0.05
     pair.close(), down.close()
+
+
+def test_sizes_past_32_bits_and_other_devices_are_refused():
+    w = torch.zeros(32, 64, dtype=torch.int8, device="cuda")
+    s = torch.ones(32, device="cuda")
+    for n in ((1 << 32) + 8, 1 << 31):
+        with pytest.raises(ValueError):
+            spear.SpearW8Linear(w, s, max_tokens=n)
+        with pytest.raises(ValueError):
+            spear.w8_workspace_bytes(32, 64, n)
+        with pytest.raises(ValueError):
+            spear.w8_workspace_bytes(n, 64, 8)
+    with pytest.raises(ValueError):
+        spear.SpearW8Linear(w, s.cpu())
+    layer = spear.SpearW8Linear(w, s, max_tokens=8)
+    x, xs, y = torch.zeros(2, 64, dtype=torch.int8, device="cuda"), torch.ones(2, device="cuda"), torch.empty(2, 32, device="cuda")
+    for args in ((x.cpu(), xs, y), (x, xs.cpu(), y), (x, xs, y.cpu())):
+        with pytest.raises(ValueError):
+            layer.forward(*args)
+    M = (1 << 32) + 2  # views of few elements: nothing is read
+    with pytest.raises(ValueError):
+        layer.forward(x[:1].expand(M, 64), xs[:1].expand(M), y[:1].expand(M, 32))
+    layer.forward(x, xs, y)
+    assert not y.any()
