@@ -50,7 +50,7 @@ __global__ void __launch_bounds__(256) dequantize_kernel(const int8_t* __restric
                                                          const float* __restrict__ scales, int M, int K,
                                                          T* __restrict__ out, int64_t ld_out, int vec) {
   kv_follow();
-  const int groups = (K + 15) / 16;
+  const int groups = (K - 1) / 16 + 1;
   uint4 w[kTurns];
   float s[kTurns];
   int64_t row[kTurns];
@@ -65,12 +65,12 @@ __global__ void __launch_bounds__(256) dequantize_kernel(const int8_t* __restric
     if (row[i] >= M) continue;
     const int8_t* src = q + row[i] * ld_q + k[i];
     s[i] = scales[row[i]];
-    if (vec && k[i] + 16 <= K) {
+    if (vec && K - k[i] >= 16) {
       w[i] = __ldcs(reinterpret_cast<const uint4*>(src));
     } else {
       int8_t c[16];
 #pragma unroll
-      for (int j = 0; j < 16; ++j) c[j] = k[i] + j < K ? src[j] : (int8_t)0;
+      for (int j = 0; j < 16; ++j) c[j] = j < K - k[i] ? src[j] : (int8_t)0;
       memcpy(&w[i], c, 16);
     }
   }
@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(256) dequantize_kernel(const int8_t* __restric
     values8(w[i].x, w[i].y, v[0]), values8(w[i].z, w[i].w, v[1]);
 #pragma unroll
     for (int j = 0; j < 16; ++j) v[j >> 3][j & 7] *= s[i];
-    store16(out + row[i] * ld_out + k[i], K - k[i], k[i] + 16 <= K ? vec : 0, v[0], v[1]);
+    store16(out + row[i] * ld_out + k[i], K - k[i], K - k[i] >= 16 ? vec : 0, v[0], v[1]);
   }
 }
 
@@ -258,7 +258,7 @@ extern "C" spear_status_t spear_dequantize_rows(const int8_t* q, int64_t ld_q, c
   const bool wide = vec_ok(out, ld_out, M, s) && vec_ok(q, ld_q, M, 1);
   const bool flat = !wide && K >= 16 && (M == 1 || (ld_q == K && ld_out == K)) && aligned(q, 16) && aligned(out, 16);
   const int vec = !wide && !flat ? 0 : aligned(out, 32) && (flat || M == 1 || ld_out * s % 32 == 0) ? 2 : 1;
-  const int64_t groups = flat ? ((int64_t)M * K + 15) / 16 : (int64_t)M * ((K + 15) / 16);
+  const int64_t groups = flat ? ((int64_t)M * K + 15) / 16 : (int64_t)M * ((K - 1) / 16 + 1);
   const int64_t blocks = (groups + 256 * kTurns - 1) / (256 * kTurns);
   if (blocks > 0x7FFFFFFF) return SPEAR_ERR_UNSUPPORTED;
   const dim3 grid((unsigned)blocks);

@@ -500,8 +500,15 @@ class _Rows:
         self.device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
         # (device index) -> its current stream's handle
         self.stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda dev: _stream(None))
+        self.cuda = torch.cuda
         L = load()
         self.norm, self.quantize, self.dequantize = L.spear_rms_norm, L.spear_quantize_rows, L.spear_dequantize_rows
+
+    def on(self, stream):
+        """Context in which tensors are made on `stream` (the current one if None)."""
+        if stream is not None and not isinstance(stream, self.cuda.Stream):
+            stream = self.cuda.ExternalStream(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+        return self.cuda.stream(stream)
 
 
 _rows_ = None
@@ -616,10 +623,10 @@ def quantize_rows(x, q=None, scales=None, stream=None):
     r = _rows_ or _rows()
     shape, xt = x.shape, x.dtype
     M, K = shape
-    if q is None:
-        q = r.empty((M, K), dtype=r.i8, device=x.device)
-    if scales is None:
-        scales = r.empty((M,), dtype=r.f32, device=x.device)
+    if q is None or scales is None:
+        with r.on(stream):  # of the stream that writes them: memory that another stream has freed may still be in use there
+            q = r.empty((M, K), dtype=r.i8, device=x.device) if q is None else q
+            scales = r.empty((M,), dtype=r.f32, device=x.device) if scales is None else scales
     (ld_x, one), (ld_q, one_q) = x.stride(), q.stride()
     dev = x.get_device()
     if not (xt in r.types and q.dtype is r.i8 and q.shape == shape and dev == q.get_device() == scales.get_device() and

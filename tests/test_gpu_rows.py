@@ -392,3 +392,30 @@ def test_rows_and_results_on_one_device():
                  lambda: spear.dequantize_rows(q, s.cpu(), x)):
         with pytest.raises(ValueError):
             call()
+
+
+def test_read_back_of_the_widest_row():
+    K = (1 << 31) - 1
+    q = torch.zeros(K, dtype=torch.int8, device="cuda")
+    q[-40:] = torch.arange(40, dtype=torch.int8, device="cuda")
+    out = torch.full((K + 16,), 7, dtype=BF16, device="cuda")
+    s = torch.full((1,), 2.0, device="cuda")
+    spear.dequantize_rows(q.view(1, K), s, out[:K].view(1, K))
+    assert torch.equal(out[K - 40:K], 2 * torch.arange(40, device="cuda").to(BF16)) and not out[:K - 39].any()
+    assert bool((out[K:] == 7).all())
+
+
+def test_results_belong_to_the_stream_that_makes_them():
+    """Memory that the current stream freed and may still use is not given to rows quantised on another one."""
+    x = _rand(1, 2000, 4096, dtype=BF16)
+    want, ws = spear.quantize_rows(x)
+    other = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for stream in (other, other.cuda_stream):
+        used = torch.empty(2000, 4096, dtype=torch.int8, device="cuda")
+        for _ in range(50):
+            used.fill_(1)
+        del used  # its block goes to the next of this size on the current stream
+        q, s = spear.quantize_rows(x, stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(q, want) and torch.equal(s, ws)
