@@ -268,3 +268,20 @@ extern "C" spear_status_t spear_dequantize_rows(const int8_t* q, int64_t ld_q, c
     default: return launch_dequantize(flat, grid, stream, q, ld_q, scales, M, K, static_cast<float*>(out), ld_out, vec);
   }
 }
+
+extern "C" spear_status_t spear_rms_norm_args(const spear_rms_norm_args_t* a) {
+  if (!a) return SPEAR_ERR_INVALID_ARG;
+  return spear_rms_norm(a->x, a->ld_x, (spear_dtype_t)a->type, a->residual, a->ld_residual, a->residual_out,
+                        a->ld_residual_out, (spear_dtype_t)a->residual_type, a->weight, (spear_dtype_t)a->weight_type, a->eps,
+                        a->M, a->K, a->y, a->ld_y, a->q, a->ld_q, a->scales, a->stream);
+}
+
+extern "C" spear_status_t spear_quantize_rows_args(const spear_quantize_rows_args_t* a) {
+  if (!a) return SPEAR_ERR_INVALID_ARG;
+  return spear_quantize_rows(a->x, a->ld_x, (spear_dtype_t)a->type, a->M, a->K, a->q, a->ld_q, a->scales, a->stream);
+}
+
+extern "C" spear_status_t spear_dequantize_rows_args(const spear_dequantize_rows_args_t* a) {
+  if (!a) return SPEAR_ERR_INVALID_ARG;
+  return spear_dequantize_rows(a->q, a->ld_q, a->scales, a->M, a->K, a->out, a->ld_out, (spear_dtype_t)a->type, a->stream);
+}

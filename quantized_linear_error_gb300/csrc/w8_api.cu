@@ -173,6 +173,11 @@ extern "C" spear_status_t spear_w8_forward(spear_w8_t h, const int8_t* x, int64_
   return w8_many(h, M) ? w8_launch_prefill(h, c, stream) : w8_launch_decode(h, c, stream);
 }
 
+extern "C" spear_status_t spear_w8_forward_args(const spear_w8_forward_args_t* a) {
+  if (!a) return SPEAR_ERR_INVALID_ARG;
+  return spear_w8_forward(a->h, a->x, a->ld_x, a->x_scales, a->y, a->ld_y, (spear_dtype_t)a->type, a->M, a->stream);
+}
+
 extern "C" spear_status_t spear_w8_check(spear_w8_t h, cudaStream_t stream) {
   if (!h) return SPEAR_ERR_INVALID_ARG;
   unsigned status = 0;

@@ -12,6 +12,7 @@ import ctypes
 import re
 from ctypes import POINTER, byref, c_char_p, c_double, c_float, c_int, c_int32, c_int64, c_void_p
 from pathlib import Path
+from struct import Struct
 
 PKG = Path(__file__).resolve().parent
 LIB_PATH = PKG / "libspear_gb300.so"
@@ -117,6 +118,9 @@ def load(path: Path | None = None):
     L.spear_w8_workspace.argtypes = [POINTER(spear_w8_desc_t), POINTER(c_int64)]
     L.spear_w8_create.argtypes = [POINTER(spear_w8_desc_t), H, POINTER(c_void_p)]
     L.spear_w8_forward.argtypes = [H, H, c_int64, H, H, c_int64, c_int, c_int32, H]
+    for name in ("spear_rms_norm_args", "spear_quantize_rows_args", "spear_dequantize_rows_args", "spear_w8_forward_args"):
+        getattr(L, name).argtypes = [c_char_p]  # a packed struct
+        getattr(L, name).restype = c_int
     L.spear_w8_check.argtypes = [H, H]
     L.spear_w8_destroy.argtypes = [H]
     L.spear_status_string.argtypes = [c_int]
@@ -125,8 +129,8 @@ def load(path: Path | None = None):
                  "spear_linear_forward", "spear_linear_forward_host", "spear_linear_destroy",
                  "spear_linear_dequantize", "spear_linear_check", "spear_linear_debug_set",
                  "spear_kv_create", "spear_kv_append", "spear_kv_read", "spear_kv_attention", "spear_kv_check",
-                 "spear_kv_destroy", "spear_rms_norm", "spear_quantize_rows", "spear_dequantize_rows", "spear_w8_workspace", "spear_w8_create",
-                 "spear_w8_forward", "spear_w8_check", "spear_w8_destroy"):
+                 "spear_kv_destroy", "spear_rms_norm", "spear_quantize_rows", "spear_dequantize_rows",
+                 "spear_w8_workspace", "spear_w8_create", "spear_w8_forward", "spear_w8_check", "spear_w8_destroy"):
         getattr(L, name).restype = c_int
     _lib = L
     return L
@@ -502,7 +506,11 @@ class _Rows:
         self.stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda dev: _stream(None))
         self.cuda = torch.cuda
         L = load()
-        self.norm, self.quantize, self.dequantize = L.spear_rms_norm, L.spear_quantize_rows, L.spear_dequantize_rows
+        self.norm, self.quantize, self.dequantize, self.forward = (
+            L.spear_rms_norm_args, L.spear_quantize_rows_args, L.spear_dequantize_rows_args, L.spear_w8_forward_args)
+        # their structs: addresses and distances of 64 bits, then sizes and types of 32
+        self.norm_args, self.quantize_args = Struct("=QqQqQqQQqQqQQ5if").pack, Struct("=QqQqQQ3i").pack
+        self.dequantize_args, self.forward_args = Struct("=QqQQqQ3i").pack, Struct("=QQqQQqQ2i").pack
 
     def on(self, stream):
         """Context in which tensors are made on `stream` (the current one if None)."""
@@ -589,8 +597,8 @@ def rms_norm(x, weight, eps=1e-5, residual=None, residual_out=None, y=None, q=No
         _bad_norm(r, x, weight, residual, residual_out, y, q, scales)
     if M < 2:  # the stride of a single row means nothing
         ld_x = ld_r = ld_ro = ld_y = ld_q = K
-    st = r.norm(x.data_ptr(), ld_x, t, rp, ld_r, ro, ld_ro, rt, weight.data_ptr(), types[wt], eps, M, K, yp, ld_y, qp, ld_q, sp,
-                r.stream(dev) if stream is None else _stream(stream))
+    st = r.norm(r.norm_args(x.data_ptr(), ld_x, rp, ld_r, ro, ld_ro, weight.data_ptr(), yp, ld_y, qp, ld_q, sp,
+                            r.stream(dev) if stream is None else _stream(stream), t, rt, types[wt], M, K, eps))
     if st:
         raise SpearError(st, "spear_rms_norm")
     return y if q is None else (q, scales)
@@ -639,8 +647,8 @@ def quantize_rows(x, q=None, scales=None, stream=None):
         _not_here("quantize_rows", dev)
     if M < 2:
         ld_x = ld_q = K
-    st = r.quantize(x.data_ptr(), ld_x, r.types[xt], M, K, q.data_ptr(), ld_q, scales.data_ptr(),
-                    r.stream(dev) if stream is None else _stream(stream))
+    st = r.quantize(r.quantize_args(x.data_ptr(), ld_x, q.data_ptr(), ld_q, scales.data_ptr(),
+                                    r.stream(dev) if stream is None else _stream(stream), r.types[xt], M, K))
     if st:
         raise SpearError(st, "spear_quantize_rows")
     return q, scales
@@ -663,8 +671,8 @@ def dequantize_rows(q, scales, out, stream=None):
         _not_here("dequantize_rows", dev)
     if M < 2:
         ld_q = ld_o = K
-    st = r.dequantize(q.data_ptr(), ld_q, scales.data_ptr(), M, K, out.data_ptr(), ld_o, r.types[ot],
-                      r.stream(dev) if stream is None else _stream(stream))
+    st = r.dequantize(r.dequantize_args(q.data_ptr(), ld_q, scales.data_ptr(), out.data_ptr(), ld_o,
+                                        r.stream(dev) if stream is None else _stream(stream), r.types[ot], M, K))
     if st:
         raise SpearError(st, "spear_dequantize_rows")
     return out
@@ -722,8 +730,8 @@ class SpearW8Linear:
         _check(L.spear_w8_create(byref(d), _stream(stream), byref(h)), "spear_w8_create")
         self.h, self.K, self.N, self.gated, self.max_tokens = h, K, N, up is not None, int(max_tokens)
         self.workspace = workspace
-        self._forward, self._types, self._i8, self._f32, self._device = L.spear_w8_forward, r.types, r.i8, r.f32, dev
-        self._stream = r.stream
+        self._forward, self._types, self._i8, self._f32, self._device = r.forward, r.types, r.i8, r.f32, dev
+        self._args, self._stream = r.forward_args, r.stream
 
     def forward(self, q, scales, y, stream=None):
         """y [M][N] (bf16, f16 or fp32) of the 8-bit rows ``q`` int8 [M][K] with ``scales`` fp32 [M]."""
@@ -739,8 +747,8 @@ class SpearW8Linear:
             raise ValueError(f"SpearW8Linear: q, scales and y have to be on the layer's device, cuda:{self._device}")
         if M < 2:
             ld_q, ld_y = K, N
-        st = self._forward(self.h, q.data_ptr(), ld_q, scales.data_ptr(), y.data_ptr(), ld_y, self._types[yt], M,
-                           self._stream(self._device) if stream is None else _stream(stream))
+        st = self._forward(self._args(self.h.value or 0, q.data_ptr(), ld_q, scales.data_ptr(), y.data_ptr(), ld_y,
+                                      self._stream(self._device) if stream is None else _stream(stream), self._types[yt], M))
         if st:
             raise SpearError(st, "spear_w8_forward")
         return y

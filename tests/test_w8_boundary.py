@@ -105,3 +105,31 @@ def test_dequantize_rejects_bad_arguments(L, bad):
     a = dict(q=4 << 20, ld_q=K, scales=5 << 20, M=M, K=K, out=1 << 20, ld_out=K, type=0)
     a.update(bad)
     assert L.spear_dequantize_rows(*a.values(), None) == BAD
+
+
+def test_arguments_in_a_struct_mean_the_same(L):
+    """Each field is where the library looks for it: spoilt one by one, only the one that the call then refuses changes."""
+    r = spear._rows()
+    ok, unsupported = spear.SPEAR_OK, UNSUPPORTED
+    norm = dict(x=1 << 20, ld_x=K, res=6 << 20, ld_res=K, res_out=7 << 20, ld_res_out=K, weight=2 << 20, y=3 << 20, ld_y=K,
+                q=4 << 20, ld_q=K, scales=5 << 20, stream=0, type=0, res_type=0, weight_type=0, M=0, K=K, eps=1e-5)
+    call = lambda **kw: L.spear_rms_norm_args(r.norm_args(*{**norm, **kw}.values()))
+    assert call() == ok and call(K=32769) == unsupported
+    assert call(eps=-1.0) == BAD and call(type=3) == BAD and call(weight_type=1) == BAD and call(weight=0) == BAD
+    for bad in (dict(x=0), dict(ld_x=K - 1), dict(ld_res=K - 1), dict(res_out=0), dict(ld_res_out=0), dict(res=1 + (6 << 20)),
+                dict(ld_y=K - 1), dict(y=1 + (3 << 20)), dict(ld_q=K - 1), dict(scales=2 + (5 << 20)), dict(q=3 << 20),
+                dict(res_type=1)):
+        assert call(M=4, **bad) == BAD, bad
+    quant = dict(x=1 << 20, ld_x=K, q=4 << 20, ld_q=K, scales=5 << 20, stream=0, type=0, M=0, K=K)
+    call = lambda **kw: L.spear_quantize_rows_args(r.quantize_args(*{**quant, **kw}.values()))
+    assert call() == ok and call(K=32769) == unsupported and call(type=3) == BAD
+    for bad in (dict(x=0), dict(ld_x=K - 1), dict(q=0), dict(ld_q=K - 1), dict(scales=1 + (5 << 20))):
+        assert call(M=4, **bad) == BAD, bad
+    back = dict(q=4 << 20, ld_q=K, scales=5 << 20, out=1 << 20, ld_out=K, stream=0, type=0, M=0, K=K)
+    call = lambda **kw: L.spear_dequantize_rows_args(r.dequantize_args(*{**back, **kw}.values()))
+    assert call() == ok and call(K=0) == BAD and call(type=3) == BAD
+    for bad in (dict(q=0), dict(ld_q=K - 1), dict(scales=1 + (5 << 20)), dict(out=0), dict(ld_out=K - 1)):
+        assert call(M=4, **bad) == BAD, bad
+    assert L.spear_w8_forward_args(r.forward_args(0, 16, 64, 16, 16, 8, 0, 0, 1)) == BAD
+    for name in ("rms_norm", "quantize_rows", "dequantize_rows", "w8_forward"):
+        assert getattr(L, f"spear_{name}_args")(None) == BAD
