@@ -28,8 +28,8 @@
 // that thread, 350 of the dequantising warps and 325 of the issuing one.
 //
 // Measured: 4096 tokens through 2 x 28672 x 8192 (3.85 TFLOP) 1.95 ms in bursts, 1.97
-// PFLOP/s or 103% of a library product's burst rate, 2.03 ms sustained; 2048 tokens
-// x 14336 x 4096 133 us, 94%; tensor pipe active 90% of the time (profile of this
+// PFLOP/s or 103% of a library product's burst rate, 2.01 ms sustained; 2048 tokens
+// x 14336 x 4096 135 us, 93%; tensor pipe active 90% of the time (profile of this
 // case). Small calls are bound by stages of 580 cycles, whatever TN up to 128 (the
 // eight MMAs of a stage then take some 64 cycles each), and by some 9 us of start,
 // tokens' preparation, epilogue and end: 320 tokens x 4096 x 6144 20 us, of which 10
