@@ -68,7 +68,7 @@ struct GemmParams {
   int64_t ld_y;
   int* sums;              // [tile][rank][token][row] of shared tiles, zero between calls
   unsigned *counters, *status;
-  int type, vec;          // vec: 16-bit results may be stored eight at a time
+  int type, vec;          // vec: results may be stored 16 bytes at a time
   int M, N, ks, act, w_tiles;  // ks: stages of a tile
   int TN, n_tok;               // tokens of a tile, token tiles
   int tiles, sk_tiles, sk_pairs;  // tiles in all; those split along K, over that many pairs
@@ -190,11 +190,8 @@ SPEAR_DEVINL void umma2_commit(uint32_t leader, uint64_t* bar) {
       : "memory");
 }
 
-SPEAR_DEVINL uint16_t lds16(uint32_t addr) {
-  uint16_t v;
-  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));
-  return v;
-}
+SPEAR_DEVINL void lds(uint16_t& v, uint32_t addr) { asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr)); }
+SPEAR_DEVINL void lds(uint32_t& v, uint32_t addr) { asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr)); }
 
 // 32 rows x 16 columns of an accumulator: v[8 h + 4 i + e] is row 16 h + lane / 4 + 8 (e / 2), column 8 i + 2 (lane % 4)
 // + e % 2, the fragment of 8 x 8 matrices, so that a store of transposed matrices gives rows of tokens, and both
@@ -244,23 +241,27 @@ struct Epilogue {
     const __half2 h = __floats2half2_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&h);
   }
-  // kOuts neighbouring outputs of each of 16 tokens, `step` bytes apart in shared memory from `from` on.
-  template <int kOuts>
+  // kOuts neighbouring outputs of each of 16 tokens, `step` bytes apart in shared memory from `from` on. E: as wide.
+  template <int kOuts, class E>
   SPEAR_DEVINL void store(uint32_t from, uint32_t step, int m0) const {
-    uint16_t* const y = static_cast<uint16_t*>(p.y);
-    if (p.vec && n0 + kOuts <= p.N) {  // eight outputs a lane
-      constexpr int kLanes = kOuts / 8, kTurns = kLanes / 2;
+    E* const y = static_cast<E*>(p.y);
+    if (p.vec && n0 + kOuts <= p.N) {  // 16 bytes a lane
+      constexpr int kOf = 16 / sizeof(E), kLanes = kOuts / kOf, kTurns = kLanes / 2;
 #pragma unroll
       for (int i = 0; i < kTurns; ++i) {
         const int t = i * (32 / kLanes) + lane / kLanes, q = lane % kLanes;
-        if (m0 + t < p.M) *reinterpret_cast<uint4*>(y + (m0 + t) * p.ld_y + n0 + 8 * q) = lds128(from + t * step + 16 * q);
+        if (m0 + t < p.M) *reinterpret_cast<uint4*>(y + (m0 + t) * p.ld_y + n0 + kOf * q) = lds128(from + t * step + 16 * q);
       }
     } else {  // rows of any alignment: an output a lane, side by side
       constexpr int kAtOnce = 32 / kOuts;
       const int q = lane % kOuts;
 #pragma unroll 4
       for (int t = lane / kOuts; t < 16; t += kAtOnce)
-        if (m0 + t < p.M && n0 + q < p.N) y[(m0 + t) * p.ld_y + n0 + q] = lds16(from + t * step + 2 * q);
+        if (m0 + t < p.M && n0 + q < p.N) {
+          E e;
+          lds(e, from + t * step + sizeof(E) * q);
+          y[(m0 + t) * p.ld_y + n0 + q] = e;
+        }
     }
   }
 
@@ -283,22 +284,25 @@ struct Epilogue {
 #pragma unroll
         for (int e = 0; e < 2; ++e) v[4 * q + e] = w8_act<kF32>(v[4 * q + e], p.act) * v[4 * q + e + 2];
     }
-    if constexpr (kF32) {
+    const uint32_t at = smem_u32(sh.sums);
+    __syncwarp();
+    if constexpr (kF32) {  // 128 (64 gated) bytes a token, 16 more apart: no bank conflicts
+      constexpr int kStep = kGated ? 80 : 144;
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
         if (kGated && (j & 2)) continue;
-        const int m = m0 + 4 * (j & 4 ? 2 : 0) + 2 * (lane & 3) + (j & 1);
-        const int n = n0 + (kGated ? 8 * (j >> 3) : 16 * (j >> 3) + 8 * ((j >> 1) & 1)) + (lane >> 2);
-        if (m < p.M && n < p.N) static_cast<float*>(p.y)[m * p.ld_y + n] = v[j];
+        const int t = 2 * (j & 4) + 2 * (lane & 3) + (j & 1);
+        const int n = kGated ? 8 * (j >> 3) + (lane >> 2) : 16 * (j >> 3) + 8 * ((j >> 1) & 1) + (lane >> 2);
+        asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + t * kStep + 4 * n), "f"(v[j]) : "memory");
       }
-    } else {
-      const uint32_t at = smem_u32(sh.sums);
       __syncwarp();
+      store<kGated ? 16 : 32, uint32_t>(at, kStep, m0);
+    } else {
       if constexpr (kGated) {  // 32 bytes a token, 48 apart: no bank conflicts
         store_transposed(at + (8 * (lane >> 4) + (lane & 7)) * 48 + ((lane >> 3) & 1) * 16, pack(v[0], v[1]), pack(v[8], v[9]),
                          pack(v[4], v[5]), pack(v[12], v[13]));
         __syncwarp();
-        store<16>(at, 48, m0);
+        store<16, uint16_t>(at, 48, m0);
       } else {                 // 64 bytes a token, 80 apart
 #pragma unroll
         for (int i = 0; i < 2; ++i)
@@ -306,7 +310,7 @@ struct Epilogue {
                            pack(v[4 * i + 2], v[4 * i + 3]), pack(v[8 + 4 * i], v[8 + 4 * i + 1]),
                            pack(v[8 + 4 * i + 2], v[8 + 4 * i + 3]));
         __syncwarp();
-        store<32>(at, 80, m0);
+        store<32, uint16_t>(at, 80, m0);
       }
     }
   }
@@ -712,7 +716,7 @@ spear_status_t w8_launch_prefill(const spear_w8_s* h, const W8Call& c, cudaStrea
   p.w = h->w, p.x16 = h->x16, p.w_scales = h->w_scales, p.x_scales = c.x_scales;
   p.y = c.y, p.ld_y = c.ld_y, p.sums = h->sums, p.counters = h->gemm_counters, p.status = h->status;
   p.type = c.type, p.M = c.M, p.N = h->N, p.ks = h->kb / 2, p.act = h->act, p.w_tiles = h->strips / kW8Tile;
-  p.vec = (reinterpret_cast<uintptr_t>(c.y) & 15) == 0 && (c.ld_y % 8 == 0 || c.M == 1);
+  p.vec = (reinterpret_cast<uintptr_t>(c.y) & 15) == 0 && (c.ld_y % (c.type == SPEAR_F32 ? 4 : 8) == 0 || c.M == 1);
   const int pairs = h->sm_count / 2;
   const Cut k = cut(h, c.M, x16_tokens(h));
   p.TN = k.TN, p.n_tok = k.n_tok, p.tiles = k.tiles, p.sk_tiles = k.sk_tiles, p.sk_pairs = k.sk_pairs;
