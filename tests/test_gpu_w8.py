@@ -78,9 +78,9 @@ def test_gated(N, K, activation):
             # A relative error d of z is an error d |z| of exp(-z), and |z| < 88 where the result is not below 2^-120.
             # Half steps of fp32 (2^-24): SiLU's z = g carries 2 (two scales), 88 * 2 = 176; GELU's z carries 3 * 2
             # from g's cube and 4 of its own products and sum, 88 * 10 = 880. Beside them the second projection (2),
-            # exp (4), the sum, the quotient and the product: 10. So 186 < 2^8 and 890 < 2^10 half steps.
-            # 16-bit results take a faster exponential and quotient: 88 for the rounding of z log2(e), 8 of their own.
-            # 282 < 2^9 and 986 < 2^10.
+            # exp (4), the sum, the quotient (4) and the product: 13. So 189 < 2^8 and 893 < 2^10 half steps.
+            # 16-bit results take a faster exponential: 88 for the rounding of z log2(e), 8 of its own.
+            # 285 < 2^9 and 989 < 2^10.
             rel = 2.0 ** ((-16 if dtype is F32 else -15) if activation == "silu" else -14)
             tol = np.abs(want) * (rel + torch.finfo(dtype).eps / 2) + 2.0 ** -120
             assert np.all(np.abs(y - want) <= tol)
