@@ -377,3 +377,29 @@ def test_sizes_past_32_bits_and_other_devices_are_refused():
         layer.forward(x[:1].expand(M, 64), xs[:1].expand(M), y[:1].expand(M, 32))
     layer.forward(x, xs, y)
     assert not y.any()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("N", [1, 15, 17, 31, 48, 100, 257, 1026])
+def test_results_of_any_alignment(N, gated, dtype):
+    """Starts and distances of results that fit wide stores, and those that do not: the same bits, and nothing beside them."""
+    K = 208
+    w, u = _codes(N, N, K), _codes(N + 1, N, K)
+    layer = _layer(w, u if gated else None, max_tokens=300)
+    for M in (3, 20, 40, 209):
+        x = _codes(M, M, K)
+        xd = _dev(x[0]), _dev(x[1])
+        want = torch.empty(M, N, dtype=dtype, device="cuda")
+        layer.forward(*xd, want)
+        if not gated:
+            _equal(want, w8.linear(*x, *w))
+        for lead, more in ((0, 0), (1, 0), (0, 1), (8, 8 - N % 8), (4, 4 - N % 4), (2, 2 + N % 2)):
+            buf = torch.full((lead + M * (N + more) + 40,), 7.0, dtype=dtype, device="cuda")
+            y = buf[lead:].as_strided((M, N), (N + more, 1))
+            layer.forward(*xd, y)
+            assert torch.equal(y, want)
+            y.fill_(7.0)
+            assert bool((buf == 7.0).all())
+    assert layer.check() == spear.SPEAR_OK
+    layer.close()
