@@ -640,6 +640,14 @@ spear_status_t spear_w8_forward_args(const spear_w8_forward_args_t* args);
  * cleared and the workspace reset. */
 spear_status_t spear_w8_check(spear_w8_t h, cudaStream_t stream);
 
+/* Test surface for the bounded waits, as spear_linear_debug_set: wait_ns sets the device-side wait limit of this handle's
+ * calls (0 restores the default of 100 ms); skip_arrive != 0 leaves out an arrival, so that a wait must run out:
+ *  - up to 32 tokens: the first copy of weights (the call then gives up copying, writes wrong values and latches TIMEOUT);
+ *  - more: the dequantising warps' first one in one pair of CTAs (which then gives up: its tiles are not written, tiles
+ *    that it shares with others are not completed, and TIMEOUT is latched).
+ * Errors: INVALID_ARG (NULL, wait_ns < 0). */
+spear_status_t spear_w8_debug_set(spear_w8_t h, int64_t wait_ns, int32_t skip_arrive);
+
 /* Free the handle's device memory (waits for queued work). NULL is accepted. */
 spear_status_t spear_w8_destroy(spear_w8_t h);
 

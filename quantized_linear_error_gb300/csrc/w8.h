@@ -38,6 +38,8 @@ struct spear_w8_s {
   unsigned* counters;       // [strips], of the few-token kernel's shared rows; zero between calls
   unsigned* gemm_counters;  // of the tensor-core kernel's shared tiles; zero between calls
   size_t control_bytes;
+  uint64_t wait_ns;         // limit of the device-side waits
+  int skip_arrive;          // one of them runs out (see spear_w8_debug_set)
   // The workspace: the caller's, which several handles may use in turn, or the handle's own.
   void* ws;
   int ws_owned;
@@ -61,6 +63,8 @@ struct W8Call {
 // kernel's warp MMAs take as long as the weights' bytes from 17 tokens on; the other one's start costs 6 us more. 32
 // tokens through 17 / 34 / 59 / 67 / 235 MB: 9.1 / - / 21.5 / 24.0 / 66 us against 13.8 / - / 15.7 / 20.0 / 43.
 inline bool w8_many(const spear_w8_s* h, int M) { return M > 32 || (M > 16 && (int64_t)h->strips * h->kb > 36 * 1024); }
+
+constexpr uint64_t kW8WaitNs = 100000000ull;  // limit of a device-side wait, unless set otherwise
 
 constexpr int kRowsMaxWidth = 32768;       // 1024 threads x 32 elements in registers
 

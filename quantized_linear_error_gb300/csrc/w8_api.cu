@@ -107,6 +107,7 @@ extern "C" spear_status_t spear_w8_create(const spear_w8_desc_t* d, cudaStream_t
   const int64_t blocks = (int64_t)h->strips * h->kb;
   h->control_bytes = (32 + h->strips + w8_prefill_counters(h)) * 4;
   h->sums_bytes = w8_prefill_sums(h);
+  h->wait_ns = kW8WaitNs;
   cudaError_t e = cudaMalloc(&h->w, (size_t)blocks * kW8Block);
   if (e == cudaSuccess) e = cudaMalloc(&h->w_scales, (size_t)h->strips * 16 * 4);
   if (e == cudaSuccess) e = cudaMalloc(&h->control, h->control_bytes);
@@ -176,6 +177,13 @@ extern "C" spear_status_t spear_w8_forward(spear_w8_t h, const int8_t* x, int64_
 extern "C" spear_status_t spear_w8_forward_args(const spear_w8_forward_args_t* a) {
   if (!a) return SPEAR_ERR_INVALID_ARG;
   return spear_w8_forward(a->h, a->x, a->ld_x, a->x_scales, a->y, a->ld_y, (spear_dtype_t)a->type, a->M, a->stream);
+}
+
+extern "C" spear_status_t spear_w8_debug_set(spear_w8_t h, int64_t wait_ns, int32_t skip_arrive) {
+  if (!h || wait_ns < 0) return SPEAR_ERR_INVALID_ARG;
+  h->wait_ns = wait_ns ? (uint64_t)wait_ns : kW8WaitNs;
+  h->skip_arrive = skip_arrive != 0;
+  return SPEAR_OK;
 }
 
 extern "C" spear_status_t spear_w8_check(spear_w8_t h, cudaStream_t stream) {

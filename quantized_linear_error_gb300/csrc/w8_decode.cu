@@ -35,8 +35,10 @@ struct StreamParams {
   int64_t ld_y;
   float* part;
   unsigned *counters, *status;
+  uint64_t wait_ns;
   int type, M, K, N, kq, gated, act;  // kq: units of a row group
   int units, balanced, per;           // units in all; split evenly, or `per` whole row groups a CTA
+  int skip_arrive;                    // the first barrier of the first warp expects an arrival that never comes
 };
 
 SPEAR_DEVINL void mma_f16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -44,8 +46,6 @@ SPEAR_DEVINL void mma_f16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-
-constexpr uint64_t kWaitNs = 100000000ull;
 
 // First unit of CTA c.
 __host__ __device__ inline int range_start(int c, int grid, int units, int balanced, int per, int kq) {
@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(NW * 32, 1) stream_kernel(const __grid_constan
   };
   if (lane == 0) {
 #pragma unroll
-    for (int d = 0; d < D; ++d) mbar_init(bars + d, 1);
+    for (int d = 0; d < D; ++d) mbar_init(bars + d, d == 0 && warp == 0 && blockIdx.x == 0 && p.skip_arrive ? 2 : 1);
     fence_mbar_init();
   }
   __syncwarp();
@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(NW * 32, 1) stream_kernel(const __grid_constan
           w8_unpack(xr[q][j].w ^ kW8Bias, b[q][j][6], b[q][j][7]);
         }
       fetch_x(u + NW);
-      if (u < copied && !__all_sync(0xffffffffu, mbar_wait_bounded(bars + stage, phase, kWaitNs))) {
+      if (u < copied && !__all_sync(0xffffffffu, mbar_wait_bounded(bars + stage, phase, p.wait_ns))) {
         copied = min(copied, fu);  // no further copies; those in flight are still waited for
         if (lane == 0) atomicOr(p.status, kStatusTimeoutPipe);
       }
@@ -274,9 +274,9 @@ spear_status_t launch(const spear_w8_s* h, const W8Call& c, const Split& sp, cud
   static std::atomic<uint64_t> configured{0};
   if (smem_limit_once(reinterpret_cast<const void*>(&stream_kernel<MT, RS, KU, NW, D>), configured) != cudaSuccess)
     return SPEAR_ERR_CUDA;
-  StreamParams p = {h->w, h->w_scales, c.x, c.ld_x, c.x_scales, c.y, c.ld_y, h->part, h->counters, h->status};
+  StreamParams p = {h->w, h->w_scales, c.x, c.ld_x, c.x_scales, c.y, c.ld_y, h->part, h->counters, h->status, h->wait_ns};
   p.type = c.type, p.M = c.M, p.K = h->K, p.N = h->N, p.kq = sp.kq, p.gated = h->gated, p.act = h->act;
-  p.units = sp.groups * sp.kq, p.per = sp.per, p.balanced = sp.balanced;
+  p.units = sp.groups * sp.kq, p.per = sp.per, p.balanced = sp.balanced, p.skip_arrive = h->skip_arrive;
   return kv_launch(stream_kernel<MT, RS, KU, NW, D>, dim3(sp.grid), NW * 32, P::kSmem, stream, p);
 }
 

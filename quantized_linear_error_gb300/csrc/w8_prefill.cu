@@ -54,7 +54,6 @@
 namespace spear {
 namespace {
 
-constexpr uint64_t kWaitNs = 100000000ull;
 constexpr int kThreads = 15 * 32;
 constexpr int kRawBytes = 2 * kW8Tile * kW8Block;  // 128 rows x 128 channels
 constexpr int kMaxTokens = 192;                    // of a tile: two accumulators and two A slots in 512 columns
@@ -68,11 +67,13 @@ struct GemmParams {
   int64_t ld_y;
   int* sums;              // [tile][rank][token][row] of shared tiles, zero between calls
   unsigned *counters, *status;
+  uint64_t wait_ns;
   int type, vec;          // vec: results may be stored 16 bytes at a time
   int M, N, ks, act, w_tiles;  // ks: stages of a tile
   int TN, n_tok;               // tokens of a tile, token tiles
   int tiles, sk_tiles, sk_pairs;  // tiles in all; those split along K, over that many pairs
   int stages, slots, stage_bytes, acc_stride;
+  int skip_arrive;  // the first pair's first barrier of the dequantising warps expects an arrival that never comes
 };
 
 // Add `bytes` of 32-bit integers in shared memory to those at dst; waits for such copies by the thread that issued them.
@@ -147,9 +148,9 @@ SPEAR_DEVINL bool mbar_test(uint32_t bar, unsigned parity) {
   return ok != 0;
 }
 // Bounded wait of a whole warp; most phases are over when they are asked for, which a test shows sooner than a try.
-SPEAR_DEVINL bool wait_bar(uint64_t* bar, unsigned parity) {
+SPEAR_DEVINL bool wait_bar(uint64_t* bar, unsigned parity, uint64_t limit_ns) {
   if (__all_sync(0xffffffffu, mbar_test(smem_u32(bar), parity))) return true;
-  return warp_wait(bar, parity, kWaitNs, 0);
+  return warp_wait(bar, parity, limit_ns, 0);
 }
 // By the elected lane of a warp whose control flow is uniform.
 SPEAR_DEVINL void expect_and_copy(uint32_t leader, uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
@@ -338,7 +339,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads + 128, 1) g
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.stages; ++s) {
       mbar_init(&sh.raw[s], 2);
-      mbar_init(&sh.a[s], 8);
+      mbar_init(&sh.a[s], s == 0 && blockIdx.x == 0 && p.skip_arrive ? 9 : 8);
       mbar_init(&sh.empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -383,7 +384,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads + 128, 1) g
           grid_wait();
           follows = true;
         }
-        ok = wait_bar(&sh.empty[s], phase);
+        ok = wait_bar(&sh.empty[s], phase, p.wait_ns);
         if (!ok) break;
         if (tokens) {
           expect_and_copy(leader, dst + s * p.stage_bytes, src, b_bytes, smem_u32(&sh.raw[s]));
@@ -404,8 +405,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads + 128, 1) g
     const int left = min(issued, p.stages);
     if (issued < p.stages) s = 0, phase = 0;
     for (int i = 0; i < left; ++i) {
-      if (ok) ok = wait_bar(&sh.empty[s], phase);
-      else warp_wait(&sh.raw[s], phase, kWaitNs / 10, 0);
+      if (ok) ok = wait_bar(&sh.empty[s], phase, p.wait_ns);
+      else warp_wait(&sh.raw[s], phase, kW8WaitNs / 10, 0);
       if (++s == p.stages) s = 0, phase ^= 1;
     }
   } else if (warp == 1) {
@@ -416,12 +417,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads + 128, 1) g
       int s = 0, slot = 0, buf = 0;
       unsigned phase = 0, acc_phase = 1;
       while (ok && segs.get(p, sg)) {
-        ok = wait_bar(&sh.acc_empty[buf], acc_phase);
+        ok = wait_bar(&sh.acc_empty[buf], acc_phase, p.wait_ns);
         if (!ok) break;
         tc_fence_after_sync();
         const uint32_t d = tmem + buf * p.acc_stride;
         for (int k = sg.k0; k < sg.k1; ++k) {
-          ok = wait_bar(&sh.a[s], phase);
+          ok = wait_bar(&sh.a[s], phase, p.wait_ns);
           if (!ok) break;
           tc_fence_after_sync();
           const uint64_t desc = sw128_kmajor_desc(smem_u32(smem + s * p.stage_bytes));
@@ -460,7 +461,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads + 128, 1) g
     while (ok && segs.get(p, sg)) {
       int k = sg.k0 + skip;
       for (; k < sg.k1; k += 2) {
-        ok = wait_bar(&sh.raw[s], phase);
+        ok = wait_bar(&sh.raw[s], phase, p.wait_ns);
         if (!ok) break;
         const uint32_t from = s * p.stage_bytes;
         uint4 v[8];  // all loads ahead of the first conversion
@@ -477,7 +478,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads + 128, 1) g
         };
         convert(0);
         if (n >= p.slots) {
-          ok = wait_bar(&sh.empty[es], e_phase);
+          ok = wait_bar(&sh.empty[es], e_phase, p.wait_ns);
           if (!ok) break;
           tc_fence_after_sync();
         }
@@ -505,7 +506,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads + 128, 1) g
     while (segs.get(p, sg)) {
       const int row = sg.tile / p.n_tok, tok = sg.tile - row * p.n_tok;
       const Epilogue<kGated, kF32> out(p, mine, lane, (row * 2 + rank) * 128 + 32 * quarter, tok);
-      ok = wait_bar(&sh.acc_full[buf], phase);
+      ok = wait_bar(&sh.acc_full[buf], phase, p.wait_ns);
       if (!ok) break;
       tc_fence_after_sync();
       const uint32_t acc = tmem + buf * p.acc_stride + ((uint32_t)(32 * quarter) << 16);
@@ -717,6 +718,7 @@ spear_status_t w8_launch_prefill(const spear_w8_s* h, const W8Call& c, cudaStrea
   p.y = c.y, p.ld_y = c.ld_y, p.sums = h->sums, p.counters = h->gemm_counters, p.status = h->status;
   p.type = c.type, p.M = c.M, p.N = h->N, p.ks = h->kb / 2, p.act = h->act, p.w_tiles = h->strips / kW8Tile;
   p.vec = (reinterpret_cast<uintptr_t>(c.y) & 15) == 0 && (c.ld_y % (c.type == SPEAR_F32 ? 4 : 8) == 0 || c.M == 1);
+  p.wait_ns = h->wait_ns, p.skip_arrive = h->skip_arrive;
   const int pairs = h->sm_count / 2;
   const Cut k = cut(h, c.M, x16_tokens(h));
   p.TN = k.TN, p.n_tok = k.n_tok, p.tiles = k.tiles, p.sk_tiles = k.sk_tiles, p.sk_pairs = k.sk_pairs;

@@ -123,6 +123,7 @@ def load(path: Path | None = None):
         getattr(L, name).restype = c_int
     L.spear_w8_check.argtypes = [H, H]
     L.spear_w8_destroy.argtypes = [H]
+    L.spear_w8_debug_set.argtypes = [H, c_int64, c_int32]
     L.spear_status_string.argtypes = [c_int]
     L.spear_status_string.restype = c_char_p
     for name in ("spear_linear_create", "spear_linear_forward_decode", "spear_linear_forward_prefill",
@@ -130,7 +131,8 @@ def load(path: Path | None = None):
                  "spear_linear_dequantize", "spear_linear_check", "spear_linear_debug_set",
                  "spear_kv_create", "spear_kv_append", "spear_kv_read", "spear_kv_attention", "spear_kv_check",
                  "spear_kv_destroy", "spear_rms_norm", "spear_quantize_rows", "spear_dequantize_rows",
-                 "spear_w8_workspace", "spear_w8_create", "spear_w8_forward", "spear_w8_check", "spear_w8_destroy"):
+                 "spear_w8_workspace", "spear_w8_create", "spear_w8_forward", "spear_w8_check", "spear_w8_destroy",
+                 "spear_w8_debug_set"):
         getattr(L, name).restype = c_int
     _lib = L
     return L
@@ -755,6 +757,9 @@ class SpearW8Linear:
 
     def check(self, stream=None) -> int:
         return load().spear_w8_check(self.h, _stream(stream))
+
+    def debug_set(self, wait_ns: int = 0, skip_arrive: bool = False) -> None:
+        _check(load().spear_w8_debug_set(self.h, int(wait_ns), int(bool(skip_arrive))), "spear_w8_debug_set")
 
     def close(self) -> None:
         if getattr(self, "h", None) and self.h.value:

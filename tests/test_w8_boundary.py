@@ -133,3 +133,7 @@ def test_arguments_in_a_struct_mean_the_same(L):
     assert L.spear_w8_forward_args(r.forward_args(0, 16, 64, 16, 16, 8, 0, 0, 1)) == BAD
     for name in ("rms_norm", "quantize_rows", "dequantize_rows", "w8_forward"):
         assert getattr(L, f"spear_{name}_args")(None) == BAD
+
+
+def test_debug_set_needs_a_handle(L):
+    assert L.spear_w8_debug_set(None, 0, 0) == BAD
