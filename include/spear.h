@@ -637,7 +637,11 @@ spear_status_t spear_w8_forward_args(const spear_w8_forward_args_t* args);
 
 /* Synchronise `stream` and report the handle's device status: OK, or TIMEOUT if
  * a bounded device-side wait gave up since the last check; the status is then
- * cleared and the workspace reset. */
+ * cleared and the workspace reset. Handles that share the workspace: a call that
+ * gave up may leave it so that later ones of more than 32 tokens (17 through many
+ * weights) are wrong, until one of the handles that took part is checked; a handle
+ * that made such a call reports TIMEOUT too. So check all of them, with no call on
+ * the workspace running, before their results are used. */
 spear_status_t spear_w8_check(spear_w8_t h, cudaStream_t stream);
 
 /* Test surface for the bounded waits, as spear_linear_debug_set: wait_ns sets the device-side wait limit of this handle's

@@ -44,8 +44,9 @@ struct spear_w8_s {
   void* ws;
   int ws_owned;
   float* part;              // sums of the few-token kernel's shared rows
-  int* sums;                // of the tensor-core kernel's shared tiles; zero between calls
-  size_t sums_bytes;
+  unsigned* spoilt;         // set by a call that gave up and may have left sums that are not zero
+  int* sums;                // of the tensor-core kernel's shared tiles, behind it; zero between calls
+  size_t sums_bytes;        // of both
   uint8_t* x16;             // tokens in f16
 };
 
@@ -65,6 +66,8 @@ struct W8Call {
 inline bool w8_many(const spear_w8_s* h, int M) { return M > 32 || (M > 16 && (int64_t)h->strips * h->kb > 36 * 1024); }
 
 constexpr uint64_t kW8WaitNs = 100000000ull;  // limit of a device-side wait, unless set otherwise
+
+constexpr size_t kW8SumsAt = 128;               // bytes from `spoilt` to the sums
 
 constexpr int kRowsMaxWidth = 32768;       // 1024 threads x 32 elements in registers
 

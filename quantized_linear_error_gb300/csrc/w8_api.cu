@@ -122,11 +122,13 @@ extern "C" spear_status_t spear_w8_create(const spear_w8_desc_t* d, cudaStream_t
     h->gemm_counters = h->counters + h->strips;
     char* ws = static_cast<char*>(h->ws);
     h->part = reinterpret_cast<float*>(ws);
-    h->sums = reinterpret_cast<int*>(ws + w8_decode_workspace(h));
-    h->x16 = reinterpret_cast<uint8_t*>(h->sums) + h->sums_bytes;
+    ws += w8_decode_workspace(h);
+    h->spoilt = reinterpret_cast<unsigned*>(ws);
+    h->sums = reinterpret_cast<int*>(ws + kW8SumsAt);
+    h->x16 = reinterpret_cast<uint8_t*>(ws + h->sums_bytes);
     e = cudaMemsetAsync(h->control, 0, h->control_bytes, stream);
   }
-  if (e == cudaSuccess && h->sums_bytes) e = cudaMemsetAsync(h->sums, 0, h->sums_bytes, stream);
+  if (e == cudaSuccess && h->sums_bytes) e = cudaMemsetAsync(h->spoilt, 0, h->sums_bytes, stream);
   if (e == cudaSuccess) {
     const int64_t chunks = blocks * 64;
     layout_kernel<<<(unsigned)((chunks + 255) / 256), 256, 0, stream>>>(d->qweight, d->qweight_up, d->N, d->K, h->kb, chunks,
@@ -194,7 +196,7 @@ extern "C" spear_status_t spear_w8_check(spear_w8_t h, cudaStream_t stream) {
     return SPEAR_ERR_CUDA;
   if (status == 0) return SPEAR_OK;
   if (cudaMemsetAsync(h->control, 0, h->control_bytes, stream) != cudaSuccess ||
-      (h->sums_bytes && cudaMemsetAsync(h->sums, 0, h->sums_bytes, stream) != cudaSuccess) ||
+      (h->sums_bytes && cudaMemsetAsync(h->spoilt, 0, h->sums_bytes, stream) != cudaSuccess) ||
       cudaStreamSynchronize(stream) != cudaSuccess)
     return SPEAR_ERR_CUDA;
   return SPEAR_ERR_TIMEOUT;

@@ -66,7 +66,7 @@ struct GemmParams {
   void* y;
   int64_t ld_y;
   int* sums;              // [tile][rank][token][row] of shared tiles, zero between calls
-  unsigned *counters, *status;
+  unsigned *counters, *status, *spoilt;
   uint64_t wait_ns;
   int type, vec;          // vec: results may be stored 16 bytes at a time
   int M, N, ks, act, w_tiles;  // ks: stages of a tile
@@ -189,6 +189,12 @@ SPEAR_DEVINL void umma2_commit(uint32_t leader, uint64_t* bar) {
           smem_u32(bar)),
       "r"(leader)
       : "memory");
+}
+
+// A wait ran out. Parts that other pairs have added may stay in the sums, which other handles share.
+SPEAR_DEVINL void gave_up(const GemmParams& p) {
+  atomicOr(p.status, kStatusTimeoutPipe);
+  if (p.sk_tiles) atomicOr(p.spoilt, 1u);
 }
 
 SPEAR_DEVINL void lds(uint16_t& v, uint32_t addr) { asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr)); }
@@ -400,7 +406,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads + 128, 1) g
       }
     }
     if (!follows) grid_wait();
-    if (!ok && lane == 0) atomicOr(p.status, kStatusTimeoutPipe);
+    if (!ok && lane == 0) gave_up(p);
     // every stage's MMAs have run before the CTA may leave (or, given up, its copies have landed)
     const int left = min(issued, p.stages);
     if (issued < p.stages) s = 0, phase = 0;
@@ -436,7 +442,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads + 128, 1) g
         umma2_commit(leader, &sh.acc_full[buf]);
         if ((buf ^= 1) == 0) acc_phase ^= 1;
       }
-      if (!ok && lane == 0) atomicOr(p.status, kStatusTimeoutPipe);
+      if (!ok && lane == 0) gave_up(p);
+    } else if (blockIdx.x == 1 && lane == 0 && p.sk_tiles && __ldcg(p.spoilt)) {
+      atomicOr(p.status, kStatusTimeoutPipe);  // the sums of this call's shared tiles are wrong
     }
   } else if (warp < 10) {
     grid_wait();
@@ -494,7 +502,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads + 128, 1) g
       }
       skip = k - sg.k1;
     }
-    if (!ok && lane == 0) atomicOr(p.status, kStatusTimeoutPipe);
+    if (!ok && lane == 0) gave_up(p);
   } else {
     grid_wait();  // the tokens' scales, and what the kernel before this one may still read of y
     const int quarter = warp & 3;
@@ -601,7 +609,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads + 128, 1) g
       if (lane == 0) mbar_arrive_cluster(emptied + 8 * buf);
       if ((buf ^= 1) == 0) phase ^= 1;
     }
-    if (!ok && lane == 0) atomicOr(p.status, kStatusTimeoutPipe);
+    if (!ok && lane == 0) gave_up(p);
   }
   __syncwarp();
   tc_fence_before_sync();
@@ -703,9 +711,10 @@ size_t x16_tokens(const spear_w8_s* h) { return (size_t)h->max_tokens + h->max_t
 }  // namespace
 
 // Arrival counters (2 CTAs x 4 warps a shared tile, fewer than one tile a pair) and sums of shared tiles: zero between calls.
+// The sums follow a word that says that they may not be.
 size_t w8_prefill_counters(const spear_w8_s* h) { return w8_many(h, h->max_tokens) ? (size_t)h->sm_count * 4 : 0; }
 size_t w8_prefill_sums(const spear_w8_s* h) {
-  return w8_many(h, h->max_tokens) ? (size_t)h->sm_count * kMaxTokens * 128 * sizeof(int) : 0;
+  return w8_many(h, h->max_tokens) ? kW8SumsAt + (size_t)h->sm_count * kMaxTokens * 128 * sizeof(int) : 0;
 }
 // The tokens in f16.
 size_t w8_prefill_workspace(const spear_w8_s* h) {
@@ -715,7 +724,7 @@ size_t w8_prefill_workspace(const spear_w8_s* h) {
 spear_status_t w8_launch_prefill(const spear_w8_s* h, const W8Call& c, cudaStream_t stream) {
   GemmParams p = {};
   p.w = h->w, p.x16 = h->x16, p.w_scales = h->w_scales, p.x_scales = c.x_scales;
-  p.y = c.y, p.ld_y = c.ld_y, p.sums = h->sums, p.counters = h->gemm_counters, p.status = h->status;
+  p.y = c.y, p.ld_y = c.ld_y, p.sums = h->sums, p.counters = h->gemm_counters, p.status = h->status, p.spoilt = h->spoilt;
   p.type = c.type, p.M = c.M, p.N = h->N, p.ks = h->kb / 2, p.act = h->act, p.w_tiles = h->strips / kW8Tile;
   p.vec = (reinterpret_cast<uintptr_t>(c.y) & 15) == 0 && (c.ld_y % (c.type == SPEAR_F32 ? 4 : 8) == 0 || c.M == 1);
   p.wait_ns = h->wait_ns, p.skip_arrive = h->skip_arrive;
