@@ -53,7 +53,8 @@ class AttentionBlock:
         return self.o.forward(a.view(T, -1), y)
 
     def check(self) -> bool:
-        return all(x.check() == spear.SPEAR_OK for x in (self.qkv, self.cache, self.o))
+        # each of them: a check also makes its handle fit again
+        return all([x.check() == spear.SPEAR_OK for x in (self.qkv, self.cache, self.o)])
 
     def close(self):
         for x in (self.qkv, self.cache, self.o):

@@ -85,7 +85,8 @@ class Decoder:
         return y
 
     def check(self) -> bool:
-        return all(b.check() for b in self.blocks) and all(x.check() == spear.SPEAR_OK for f in self.ffs for x in (f.pair, f.down))
+        # each of them: a check also makes its handle fit again
+        return all([b.check() for b in self.blocks] + [x.check() == spear.SPEAR_OK for f in self.ffs for x in (f.pair, f.down)])
 
     def close(self):
         for b in self.blocks:
