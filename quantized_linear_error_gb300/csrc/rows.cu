@@ -189,6 +189,7 @@ extern "C" spear_status_t spear_rms_norm(const void* x, int64_t ld_x, spear_dtyp
   if (weight_type != type && weight_type != SPEAR_F32) return SPEAR_ERR_INVALID_ARG;
   const unsigned sx = size_of(type), sw = size_of(weight_type);
   if (!rows_ok(weight, K, K, sw)) return SPEAR_ERR_INVALID_ARG;
+  if (M == 1) ld_x = ld_residual = ld_residual_out = ld_y = ld_q = K;  // of no account
   if (M > 0) {
     if (q && scales &&
         (extents_meet(x, ld_x, sx, M, K, scales, 1, 4, M, 1) || extents_meet(weight, K, sw, 1, K, scales, 1, 4, M, 1) ||
@@ -233,6 +234,7 @@ extern "C" spear_status_t spear_rms_norm(const void* x, int64_t ld_x, spear_dtyp
 extern "C" spear_status_t spear_quantize_rows(const void* x, int64_t ld_x, spear_dtype_t type, int32_t M, int32_t K,
                                               int8_t* q, int64_t ld_q, float* scales, cudaStream_t stream) {
   if (!type_ok(type) || M < 0 || K < 1) return SPEAR_ERR_INVALID_ARG;
+  if (M == 1) ld_x = ld_q = K;  // of no account
   if (M > 0 && (!rows_ok(x, ld_x, K, size_of(type)) || !q || ld_q < K || !scales || !aligned(scales, 4) ||
                 rows_overlap(q, ld_q, 1, x, ld_x, size_of(type), M, K, false) ||
                 extents_meet(q, ld_q, 1, M, K, scales, 1, 4, M, 1) ||
@@ -250,6 +252,7 @@ extern "C" spear_status_t spear_dequantize_rows(const int8_t* q, int64_t ld_q, c
                                                 void* out, int64_t ld_out, spear_dtype_t type, cudaStream_t stream) {
   if (!type_ok(type) || M < 0 || K < 1) return SPEAR_ERR_INVALID_ARG;
   const unsigned s = size_of(type);
+  if (M == 1) ld_q = ld_out = K;  // of no account
   if (M > 0 && (!q || ld_q < K || !scales || !aligned(scales, 4) || !rows_ok(out, ld_out, K, s) ||
                 rows_overlap(out, ld_out, s, q, ld_q, 1, M, K, false) ||
                 extents_meet(out, ld_out, s, M, K, scales, 1, 4, M, 1)))

@@ -163,9 +163,10 @@ extern "C" spear_status_t spear_w8_forward(spear_w8_t h, const int8_t* x, int64_
   if (!h || M < 0 || M > h->max_tokens) return SPEAR_ERR_INVALID_ARG;
   if (type != SPEAR_BF16 && type != SPEAR_F16 && type != SPEAR_F32) return SPEAR_ERR_INVALID_ARG;
   if (M == 0) return SPEAR_OK;
+  if (M == 1) ld_x = h->K, ld_y = h->N;  // of no account
   const unsigned size = type == SPEAR_F32 ? 4 : 2;
   if (!x || !x_scales || !y || !aligned(x, 16) || !aligned(x_scales, 4) || !aligned(y, size)) return SPEAR_ERR_INVALID_ARG;
-  if (ld_x < h->K || (M > 1 && ld_x % 16 != 0) || ld_y < h->N) return SPEAR_ERR_INVALID_ARG;
+  if (ld_x < h->K || ld_x % 16 != 0 || ld_y < h->N) return SPEAR_ERR_INVALID_ARG;
   const uintptr_t x0 = reinterpret_cast<uintptr_t>(x), y0 = reinterpret_cast<uintptr_t>(y), s0 = reinterpret_cast<uintptr_t>(x_scales);
   const uintptr_t x1 = x0 + (uintptr_t)(M - 1) * ld_x + h->K, y1 = y0 + ((uintptr_t)(M - 1) * ld_y + h->N) * size;
   if ((x0 < y1 && y0 < x1) || (s0 < y1 && y0 < s0 + (uintptr_t)M * 4)) return SPEAR_ERR_INVALID_ARG;

@@ -1,0 +1,101 @@
+"""8-bit rows and linears at the C entry points and at edges that the other tests leave out."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import w8
+from quantized_linear_error_gb300 import spear
+
+from .test_gpu_rows import _codes_near, _near, _np, _rand
+from .test_gpu_w8 import _codes, _dev, _equal, _layer
+
+pytestmark = pytest.mark.gpu
+
+BF16, F16, F32 = torch.bfloat16, torch.float16, torch.float32
+
+
+@pytest.mark.parametrize("ld", [0, -7, 1 << 40])
+def test_a_single_row_of_any_distance(ld):
+    L, stream = spear.load(), torch.cuda.current_stream().cuda_stream
+    K, N = 208, 40
+    x, w, r = _rand(1, 1, K, dtype=BF16), _rand(2, K, dtype=BF16), _rand(3, 1, K, dtype=BF16)
+    ro, y = torch.empty_like(r), torch.empty_like(x)
+    q, s = torch.empty(1, K, dtype=torch.int8, device="cuda"), torch.empty(1, device="cuda")
+    p = lambda t: t.data_ptr()
+    assert L.spear_rms_norm(p(x), ld, 0, p(r), ld, p(ro), ld, 0, p(w), 0, 1e-5, 1, K, p(y), ld, p(q), ld, p(s), stream) == 0
+    want = torch.empty_like(x)
+    spear.rms_norm(x, w, 1e-5, r.clone(), y=want)
+    assert torch.equal(y, want) and torch.equal(ro, (x.float() + r.float()).bfloat16())
+    assert L.spear_quantize_rows(p(x), ld, 0, 1, K, p(q), ld, p(s), stream) == 0
+    assert all(torch.equal(a, b) for a, b in zip((q, s), spear.quantize_rows(x)))
+    assert L.spear_dequantize_rows(p(q), ld, p(s), 1, K, p(y), ld, 0, stream) == 0
+    assert torch.equal(y, spear.dequantize_rows(q, s, torch.empty_like(y)))
+    weights = _codes(1, N, K)
+    layer = _layer(weights)
+    out = torch.empty(1, N, dtype=F32, device="cuda")
+    assert L.spear_w8_forward(layer.h, p(q), ld, p(s), p(out), ld, spear.SPEAR_F32, 1, stream) == 0
+    _equal(out, w8.linear(q.cpu().numpy(), s.cpu().numpy(), *weights))
+    layer.close()
+
+
+def _gate_of(g):
+    """A gated layer whose results for a token of codes (1, 0, 0 ...) are act(g) times one."""
+    N = len(g)
+    w, one = np.zeros((N, 16), np.int8), np.zeros((N, 16), np.int8)
+    w[:, 0], one[:, 0] = 1, 1
+    return (w, g), (one, np.ones(N, np.float32))
+
+
+@pytest.mark.parametrize("activation", ["silu", "gelu"])
+@pytest.mark.parametrize("M", [1, 20, 40])
+def test_fp32_activation_is_off_by_its_roundings_alone(activation, M):
+    """g and the second projection are exact here, so that only the activation's own operations round. In half steps of
+    fp32 (2^-24 of a value), with t = exp(-|z|): expf 2 of t (one step), the divisor 1 + t carries t / (1 + t) of that and
+    rounds once, the quotient rounds once.
+      SiLU, g > 0: 2 t / (1 + t) + 1 + 1 <= 3. g < 0: g t rounds once more and t's own error stays in part, 2 / (1 + t), so
+      2 + 1 + 1 + 1 = 5.
+      GELU: z's constants, products and sum are 7 at most, which exp turns into 7 |z| of t, so 7 |z| t / (1 + t) <= 2
+      more for g > 0 and 7 |z| for g < 0.
+    Second orders are below 2^-10 of these."""
+    rng = np.random.default_rng(M)
+    top = 80 if activation == "silu" else 9
+    g = np.concatenate([rng.uniform(-top, top, 20000), rng.uniform(-3, 3, 40000), rng.normal(0, 1, 5000)]).astype(np.float32)
+    w, u = _gate_of(g)
+    layer = _layer(w, u, max_tokens=64, activation=activation)
+    x = np.zeros((M, 16), np.int8)
+    x[:, 0] = 1
+    y = torch.empty(M, len(g), dtype=F32, device="cuda")
+    layer.forward(_dev(x), _dev(np.ones(M, np.float32)), y)
+    y = y.cpu().numpy().astype(np.float64)
+    assert np.array_equal(y, np.broadcast_to(y[:1], y.shape))
+    want = w8.act(g, activation)
+    z = np.abs(g.astype(np.float64))
+    if activation == "gelu":
+        z = 2 * np.sqrt(2 / np.pi) * (z + 0.044715 * z ** 3)
+    steps = np.where(g > 0, 3.0, 5.0)
+    if activation == "gelu":
+        steps += np.where(g > 0, 2.0, 7 * z)
+    off = np.abs(y[0] - want) / np.abs(want) * 2.0 ** 24
+    print(activation, M, "half steps off: g > 0", off[g > 0].max(), "g < 0", off[g < 0].max(), "mean", off.mean())
+    assert np.all(off <= steps * (1 + 2.0 ** -10))
+    layer.close()
+
+
+@pytest.mark.parametrize("M", [1, 40])
+def test_fp32_activation_of_the_ends(M):
+    g = np.array([0.0, -0.0, np.inf, np.nan, 3e38, -3e38, 1e30, -1e30, 200.0, -200.0, 2.0 ** -140, -2.0 ** -140, 2.0 ** -149],
+                 np.float32)
+    w, u = _gate_of(g)
+    for activation in ("silu", "gelu"):
+        layer = _layer(w, u, max_tokens=64, activation=activation)
+        x = np.zeros((M, 16), np.int8)
+        x[:, 0] = 1
+        y = torch.empty(M, len(g), dtype=F32, device="cuda")
+        layer.forward(_dev(x), _dev(np.ones(M, np.float32)), y)
+        y = y.cpu().numpy()
+        for row in y:
+            assert row[0] == 0 and row[1] == 0 and row[2] == np.inf and np.isnan(row[3])
+            assert np.array_equal(row[[4, 6, 8]], g[[4, 6, 8]]) and not row[[5, 7, 9]].any()
+            # half of g, of the denormal numbers too
+            assert np.all(np.abs(row[10:].astype(np.float64) - g[10:].astype(np.float64) / 2) <= 2.0 ** -149)
+        layer.close()

@@ -137,3 +137,18 @@ def test_arguments_in_a_struct_mean_the_same(L):
 
 def test_debug_set_needs_a_handle(L):
     assert L.spear_w8_debug_set(None, 0, 0) == BAD
+
+
+@pytest.mark.parametrize("ld", [0, -5, 1])
+def test_the_distance_of_a_single_row_is_of_no_account(L, ld):
+    """Past the checks of the arguments comes that of the width, which stops these calls before the device."""
+    W = 32769
+    lds = dict(ld_x=ld, ld_res=ld, ld_res_out=ld, ld_y=ld, ld_q=ld)
+    assert _norm(L, **{**RES, **lds, "M": 1, "K": W}) == UNSUPPORTED
+    assert _norm(L, **{**RES, **lds, "M": 2, "K": W}) == BAD
+    quant = lambda M: L.spear_quantize_rows(1 << 20, ld, 0, M, W, 4 << 20, ld, 5 << 20, None)
+    assert quant(1) == UNSUPPORTED and quant(2) == BAD
+    # what overlaps is found whatever the distance says
+    assert _norm(L, M=1, ld_x=ld, ld_y=ld, ld_q=ld, y=(1 << 20) + 2) == BAD
+    assert L.spear_quantize_rows(1 << 20, ld, 0, 1, K, (1 << 20) + 2, ld, 5 << 20, None) == BAD
+    assert L.spear_dequantize_rows(4 << 20, ld, 5 << 20, 1, K, (4 << 20) + 16, ld, 0, None) == BAD
