@@ -99,3 +99,24 @@ def test_fp32_activation_of_the_ends(M):
             # half of g, of the denormal numbers too
             assert np.all(np.abs(row[10:].astype(np.float64) - g[10:].astype(np.float64) / 2) <= 2.0 ** -149)
         layer.close()
+
+
+@pytest.mark.parametrize("M", [1, 20, 40])
+def test_fp32_quotient_rounds_once(M):
+    """SiLU's bound of the test above, element by element, where exp's part fades: for g > 0 2 t / (1 + t) half steps come
+    of t, one of the divisor's rounding and one of the quotient's; for g < 0 2 / (1 + t), and one more of g t. A quotient
+    of two steps' error is beyond it."""
+    rng = np.random.default_rng(100 + M)
+    g = np.concatenate([rng.uniform(2, 12, 100000), -rng.uniform(0, 1, 20000)]).astype(np.float32)
+    w, u = _gate_of(g)
+    layer = _layer(w, u, max_tokens=64)
+    x = np.zeros((M, 16), np.int8)
+    x[:, 0] = 1
+    y = torch.empty(M, len(g), dtype=F32, device="cuda")
+    layer.forward(_dev(x), _dev(np.ones(M, np.float32)), y)
+    want, t = w8.act(g, "silu"), np.exp(-np.abs(g.astype(np.float64)))
+    bound = np.where(g > 0, 2 * t / (1 + t) + 2, 2 / (1 + t) + 3)
+    off = np.abs(y[0].cpu().numpy().astype(np.float64) - want) / np.abs(want) * 2.0 ** 24
+    print(M, "largest share of the bound", (off / bound)[g > 0].max(), (off / bound)[g < 0].max())
+    assert np.all(off <= bound * (1 + 2.0 ** -10))
+    layer.close()
