@@ -120,3 +120,47 @@ def test_fp32_quotient_rounds_once(M):
     print(M, "largest share of the bound", (off / bound)[g > 0].max(), (off / bound)[g < 0].max())
     assert np.all(off <= bound * (1 + 2.0 ** -10))
     layer.close()
+
+
+@pytest.mark.parametrize("activation", ["silu", "gelu"])
+@pytest.mark.parametrize("N,K", [(8, 64), (15, 96), (129, 272), (1000, 1040), (2048, 4096)])
+def test_gated_f16_results(N, K, activation):
+    """The bound of bf16 results (the fast exponential: 2^-15 of SiLU, 2^-14 of GELU), with f16's rounding and, below its
+    normal numbers, half its smallest step."""
+    w, u = _codes(N, N, K), _codes(N + 1, N, K)
+    layer = _layer(w, u, max_tokens=300, activation=activation)
+    rel, half = 2.0 ** (-15 if activation == "silu" else -14), 2.0 ** -11
+    for M in (1, 7, 16, 30, 33, 130, 260):
+        x = _codes(M, M, K)
+        want = w8.gated(*x, *w, *u, activation)
+        assert np.abs(want).max() < 60000
+        y = torch.full((M, N), 7.0, dtype=F16, device="cuda")
+        layer.forward(_dev(x[0]), _dev(x[1]), y)
+        y = y.cpu().numpy().astype(np.float64)
+        assert np.all(np.abs(y - want) <= np.abs(want) * (rel + half * (1 + rel)) + 2.0 ** -25)
+    assert layer.check() == spear.SPEAR_OK
+    layer.close()
+
+
+PAIRS = [(BF16, BF16, BF16), (BF16, F32, BF16), (F16, F16, F32), (F16, F32, F16), (F32, F32, F32), (BF16, BF16, F32)]
+ROWS = [1, 7, 250, 256, 257, 512, 517, 1000, 1016, 1024, 1032, 4096, 4100, 8200, 11008, 12296, 16384, 20488, 28671, 32768]
+
+
+@pytest.mark.parametrize("i,K", list(enumerate(ROWS)))
+@pytest.mark.parametrize("M", [4, 150])
+def test_norm_with_a_residual_in_all_outputs(i, K, M):
+    """Few rows: the kernels that take a row and end, on what the residual's addition leaves in fp32."""
+    for x, res, weight in (PAIRS[i % 6], PAIRS[(i + 3) % 6]):
+        X, W, R = _rand(K, M, K, dtype=x), _rand(K + 1, K, dtype=weight) + 1, _rand(K + 2, M, K, dtype=res, scale=3.0)
+        ro, y = torch.empty_like(R), torch.empty_like(X)
+        q, s = torch.empty(M, K, dtype=torch.int8, device="cuda"), torch.empty(M, device="cuda")
+        spear.rms_norm(X, W, 1e-5, R, ro, y, q, s)
+        h = X.float() + R.float()
+        assert torch.equal(ro, h.to(res))
+        v = w8.rms_norm(_np(h), _np(W), 1e-5)[1]
+        _near(y, v, x)
+        _codes_near(q, s, v)
+        y1, q1, s1 = torch.empty_like(y), torch.empty_like(q), torch.empty_like(s)
+        spear.rms_norm(X, W, 1e-5, R.clone(), y=y1)
+        spear.rms_norm(X, W, 1e-5, R, q=q1, scales=s1)  # in place
+        assert torch.equal(y1, y) and torch.equal(q1, q) and torch.equal(s1, s) and torch.equal(R, ro)
