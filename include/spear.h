@@ -486,7 +486,11 @@ spear_status_t spear_kv_destroy(spear_kv_t h);
  * Matrices are rows of K (or N) contiguous elements, ld elements from one row
  * to the next (ld >= K; of no account for a single row), aligned to their
  * elements. Rows whose base and ld are multiples of 16 bytes (8 for codes) are
- * moved in wide accesses. M == 0 is a no-op. Calls only enqueue on `stream`.
+ * moved in wide accesses. Where rows that the norm or the quantiser reads start
+ * or end elsewhere, it reads the whole aligned 16-byte words that hold them: up
+ * to 15 bytes before and behind a row, which are in the same words as the row's
+ * own and which nothing depends on. M == 0 is a no-op. Calls only enqueue on
+ * `stream`.
  * ---------------------------------------------------------------------- */
 typedef enum { SPEAR_BF16 = 0, SPEAR_F16 = 1, SPEAR_F32 = 2 } spear_dtype_t;
 
@@ -497,14 +501,18 @@ typedef enum { SPEAR_BF16 = 0, SPEAR_F16 = 1, SPEAR_F32 = 2 } spear_dtype_t;
  *   y = round(v) (x's type), and / or q, scales = v in 8 bits.
  * Statistics and sums are fp32, of the unrounded h. The codes are taken from
  * h * weight, whose row v is up to a positive factor, which goes into the scale
- * alone; where max |h * weight| is below 2^-110 the row counts as zeros.
+ * alone; where max |h * weight| is below 2^-110 the row counts as zeros. h * weight
+ * is formed in fp32, of rows with a sum of squares beyond 2^120 after h has been
+ * scaled by 2^-96: elements of the weight beyond 2^66 in size, or of such rows
+ * below 2^-60, may leave its range.
  *   x: device, `type`, [M][ld_x]; weight: device [K], `type` or fp32;
  *   residual, residual_out: device, `type` or fp32 (residual_type), both or
  *     neither; the same rows (residual_out == residual) or apart;
  *   y: or NULL; q: int8 [M][ld_q], with scales fp32 [M], or NULL; one of both.
  * y and residual_out may be x's own rows if the element types are the same;
  * else results share no element with each other or with what is read. K up to
- * 32768. eps >= 0, finite; with eps 0 a row of zeros gives NaN.
+ * 32768 (as for the quantiser: rows for wider linears are the caller's to
+ * quantise). eps >= 0, finite; with eps 0 a row of zeros gives NaN.
  * Rows with an element that is not finite give NaN (in residual_out only there).
  * Errors: INVALID_ARG, UNSUPPORTED (K), CUDA. */
 spear_status_t spear_rms_norm(const void* x, int64_t ld_x, spear_dtype_t type, const void* residual,
@@ -521,7 +529,8 @@ spear_status_t spear_quantize_rows(const void* x, int64_t ld_x, spear_dtype_t ty
                                    int64_t ld_q, float* scales, cudaStream_t stream);
 
 /* What rows in 8 bits stand for: out = round(code * scale) as `type`.
- * Errors: INVALID_ARG, UNSUPPORTED (more than 2^39 elements), CUDA. */
+ * Errors: INVALID_ARG, UNSUPPORTED (more than 2^40 groups of 16 elements, the
+ * last of a row with fewer), CUDA. */
 spear_status_t spear_dequantize_rows(const int8_t* q, int64_t ld_q, const float* scales, int32_t M, int32_t K, void* out,
                                      int64_t ld_out, spear_dtype_t type, cudaStream_t stream);
 
@@ -543,8 +552,9 @@ typedef struct {
   int32_t max_tokens;          /* largest M a forward on this handle will use (>= 1) */
   void* workspace;             /* device, 128-byte aligned, or NULL: the handle allocates its own. A workspace serves any
                                   number of handles whose calls follow one another (a model's layers), is the library's
-                                  alone while they live, and is larger than the weights of small layers: 16 MB and
-                                  2.25 K bytes a token */
+                                  alone while they live, and is larger than the weights of small layers: 1.2 MB, or where
+                                  calls may go to the tensor cores (more than 32 tokens, 17 through more than 36 MB of
+                                  weights) 16.2 MB + K (512 + 2.25 max_tokens) bytes, K rounded up to 128 */
   int64_t workspace_bytes;     /* at least what spear_w8_workspace says (ignored without a workspace) */
 } spear_w8_desc_t;
 

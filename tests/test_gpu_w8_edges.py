@@ -164,3 +164,16 @@ def test_norm_with_a_residual_in_all_outputs(i, K, M):
         spear.rms_norm(X, W, 1e-5, R.clone(), y=y1)
         spear.rms_norm(X, W, 1e-5, R, q=q1, scales=s1)  # in place
         assert torch.equal(y1, y) and torch.equal(q1, q) and torch.equal(s1, s) and torch.equal(R, ro)
+
+
+@pytest.mark.parametrize("N,K", [(8, 16), (4096, 4096), (8192, 28672), (64, 1 << 20)])
+@pytest.mark.parametrize("gated", [False, True])
+def test_the_workspace_is_what_the_header_says(N, K, gated):
+    """1.2 MB, or 16.2 MB + K (512 + 2.25 max_tokens) bytes: within 2% (the figures are rounded)."""
+    wide = (K + 127) // 128 * 128
+    weights = wide * ((N * (2 if gated else 1) + 127) // 128 * 128)
+    for tokens in (1, 16, 17, 32, 33, 64, 1000, 100000):
+        many = tokens > 32 or (tokens > 16 and weights > 36 << 20)
+        want = 16.2e6 + wide * (512 + 2.25 * tokens) if many else 1.2e6
+        got = spear.w8_workspace_bytes(N, K, tokens, gated)
+        assert abs(got - want) <= 0.02 * want + (wide * 2 if many else 0.04 * want), (tokens, got, want)
