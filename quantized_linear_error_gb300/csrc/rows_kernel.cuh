@@ -14,10 +14,13 @@
 // the loads and the stores. Measured: 12289 rows of 8192, bf16 with a bf16
 // residual, 143 us, 5.6 TB/s or 84% of a plain copy's rate; with an fp32 residual
 // and 8 bits 168 us, 98%; 4096 x 14336 bf16 79 us, 89%; 8-bit rows of 12289 x 8192
-// bf16 46 us, 98%, of 4096 x 14336 fp32 44 us, 99%. One row 2.5 us, a launch's
-// latency. Rows that start at any byte are bound by the instructions that shift
-// their words: 12289 x 8191 in 8 bits 117 us (39%; element by element 24%), the norm
-// of 4096 x 4097 47 us (43%; 20%).
+// bf16 46 us, 98%, of 4096 x 14336 fp32 44 us, 99%. One row of 4096 2.3 us in a graph
+// (1.9 without a residual), a launch's latency. Rows that start at any byte are bound
+// by the instructions that shift their words: 12289 x 8191 in 8 bits 117 us (39%;
+// element by element 24%), the norm of 4096 x 4097 47 us (43%; 20%). More than 16384
+// channels: the registers of 1024 threads, 2048 x 28672 109 us, 64%. Four groups a
+// thread with the norm spill: up to 296 bytes a thread in the kernels of one row, 84 in
+// those of several (wide rows of 16 bits: 24).
 #pragma once
 #include <algorithm>
 

@@ -60,9 +60,12 @@ struct W8Call {
   int M;
 };
 
-// Whether M tokens go to the tensor-core kernel: more than 32, or more than 16 through many weights. The streaming
-// kernel's warp MMAs take as long as the weights' bytes from 17 tokens on; the other one's start costs 6 us more. 32
-// tokens through 17 / 34 / 59 / 67 / 235 MB: 9.1 / - / 21.5 / 24.0 / 66 us against 13.8 / - / 15.7 / 20.0 / 43.
+// Whether M tokens go to the tensor-core kernel: more than 32, or more than 16 through many weights. From 17 tokens on
+// the streaming kernel is at some 2.7 TB/s at best; the other one starts later and is faster then, whatever the count up
+// to 32. 17 / 24 / 32 tokens, streaming against tensor cores, in us: 17 MB (4096 x 4096) 8.8 / 8.9 / 9.0 against
+// 13.6 / 13.8 / 13.9, 25 MB (6144 x 4096) 13.9 / 14.0 / 14.4 against 13.6 / 13.5 / 13.6, 34 MB (4096 x 8192) 13.1 / 13.1 /
+// 13.3 against 15.2 / 15.3 / 15.3, 45 MB (11008 x 4096) 20.4 / 20.5 / 21.4 against 17.2 / 16.9 / 17.0, 59 MB (14336 x 4096)
+// 21.6 / 21.8 / 22.2 against 16.2 / 16.2 / 16.3.
 inline bool w8_many(const spear_w8_s* h, int M) { return M > 32 || (M > 16 && (int64_t)h->strips * h->kb > 36 * 1024); }
 
 constexpr uint64_t kW8WaitNs = 100000000ull;  // limit of a device-side wait, unless set otherwise

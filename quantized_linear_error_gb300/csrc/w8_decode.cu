@@ -1,5 +1,5 @@
-// Few tokens (up to 32) through 8-bit integer weights: a kernel that streams
-// the weights once.
+// Few tokens (up to 32, or 16 where weights are many) through 8-bit integer
+// weights: a kernel that streams the weights once.
 //
 //   y[m][n] = round(s_x[m] s_w[n] sum_k q_x[m][k] q_w[n][k])
 //
@@ -16,8 +16,12 @@
 // same rows along K in turn, and their sums are added in shared memory in a
 // fixed order. Measured: 8 tokens x 28672 x 8192 (235 MB) 38 us, 6.1 TB/s or 91% of
 // a plain copy's rate; 16 tokens 41 us, 85%; a token through 4096 x 4096 5.2 us, of
-// which the bytes take 2.5 and a launch's latency the rest. From 17 tokens on the
-// warp MMAs take as long as the bytes (32 tokens: 63 us).
+// which the bytes take 2.5 and a launch's latency the rest. From 17 tokens on a unit
+// is 2 KB and its tokens' codes are as many as its weights', loaded and converted
+// for every two strips anew: 32 tokens through 4096 x 8192 (34 MB) 13.2 us, 38% of
+// HBM, with the tensor pipe active 32% of the cycles, the integer pipe 42% and an
+// issue slot used 49% by 16 warps, which wait for results of a few cycles and for
+// tokens most. (28672 x 8192 63 us; such layers take the other kernel.)
 #include <algorithm>
 
 #include "w8_device.cuh"

@@ -1,5 +1,5 @@
-// Many tokens (more than 32) through 8-bit integer weights on the tcgen05
-// tensor cores.
+// Many tokens (more than 32, or 16 where weights are many) through 8-bit integer
+// weights on the tcgen05 tensor cores.
 //
 //   y[m][n] = round(s_x[m] s_w[n] sum_k q_x[m][k] q_w[n][k])
 //
@@ -27,13 +27,19 @@
 // channels a stage and one thread for both copies, a stage took 530 cycles of
 // that thread, 350 of the dequantising warps and 325 of the issuing one.
 //
-// Measured: 4096 tokens through 2 x 28672 x 8192 (3.85 TFLOP) 1.95 ms in bursts, 1.97
-// PFLOP/s or 103% of a library product's burst rate, 2.01 ms sustained; 2048 tokens
+// Measured: 4096 tokens through 2 x 28672 x 8192 (3.85 TFLOP) 1.93 to 2.00 ms in bursts,
+// 100 to 104% of a library product's burst rate, 2.00 to 2.05 ms call after call, 98 to
+// 100% (112 to 115% of its sustained rate); 2048 tokens
 // x 14336 x 4096 135 us, 93%; tensor pipe active 90% of the time (profile of this
 // case). Small calls are bound by stages of 580 cycles, whatever TN up to 128 (the
 // eight MMAs of a stage then take some 64 cycles each), and by some 9 us of start,
 // tokens' preparation, epilogue and end: 320 tokens x 4096 x 6144 20 us, of which 10
-// in the MMAs' loop.
+// in the MMAs' loop. Far from their floors (bytes or operations at a plain copy's and
+// the library product's rates): few outputs, whose row tile is 256 all the same, while
+// the tokens' f16 tiles are written and read back (4096 x 28672 into 64 outputs 129 us,
+// floor 18; 5000 x 8192 into 16 60, 6), and few channels, where four epilogue warps take
+// longer than the MMAs (4096 tokens of 64, 256 and 512 channels into 8192 outputs 43, 46
+// and 50 us, floors 10, 10 and 18).
 //
 // Work is split in whole tiles as long as they fill all pairs; what does not come
 // out even is split along K. The pairs that share a tile add their parts, as 32-bit
@@ -674,7 +680,8 @@ struct Cut {
   int64_t cycles;
 };
 
-// The cut with the least estimated time. Measured, in cycles of an SM: a stage takes the MMAs' 4 TN and 40 more; its 16
+// The cut with the least estimated time, where the MMAs of the next tile hide every epilogue but the last: below some 700
+// channels they do not, the estimate is too low and its choice there was not measured. Measured, in cycles of an SM: a stage takes the MMAs' 4 TN and 40 more; its 16
 // KB of codes and 128 TN bytes of tokens come from L2 at 50 bytes a cycle when all SMs ask (1088 tokens through 22016 x
 // 4096: a stage 423 ns with TN 192, 396 with 160, 410 with 128; the call 104, 110, 137 us); 580 at least
 // (8 MMAs of 64 cycles, whatever TN, and the hand-over); the last tile's epilogue 25 TN; adding up a
