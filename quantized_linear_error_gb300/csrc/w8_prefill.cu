@@ -681,8 +681,8 @@ struct Cut {
 };
 
 // The cut with the least estimated time, where the MMAs of the next tile hide every epilogue but the last: below some 700
-// channels they do not, the estimate is too low and its choice there was not measured. Measured, in cycles of an SM: a stage takes the MMAs' 4 TN and 40 more; its 16
-// KB of codes and 128 TN bytes of tokens come from L2 at 50 bytes a cycle when all SMs ask (1088 tokens through 22016 x
+// channels they do not, the estimate is too low and its choice there was not measured.
+// Measured, in cycles of an SM: a stage takes the MMAs' 4 TN and 40 more; its 16 KB of codes and 128 TN bytes of tokens come from L2 at 50 bytes a cycle when all SMs ask (1088 tokens through 22016 x
 // 4096: a stage 423 ns with TN 192, 396 with 160, 410 with 128; the call 104, 110, 137 us); 580 at least
 // (8 MMAs of 64 cycles, whatever TN, and the hand-over); the last tile's epilogue 25 TN; adding up a
 // split tile 3000 and 110 TN, which whole tiles that follow it hide (61 tokens through 22016 x 4096, 86 tiles on 76
